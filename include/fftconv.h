@@ -301,6 +301,121 @@ fftconv_status_t fftconv_eqlinear_prepare(const void *W, int64_t T, int64_t C_ou
 fftconv_status_t fftconv_eqlinear_fwd(const void *x, const void *W_f, void *y, int64_t N, int64_t T,
                                       int64_t C_in, int64_t C_out, fftconv_dtype_t dtype, hipStream_t stream);
 
+/* ---- Decay attention -----------------------------------------------------
+ * Linear attention with a decay for each head: the mixer that hybrid models
+ * set beside the long convolution, and the one with a recurrent form for
+ * single tokens.  With d_h = exp(log_decay[h]) and, per sequence and head, an
+ * fp32 state S (Dk x Dv, row-major):
+ *
+ *     S_t = d S_{t-1} + k_t v_t^T,     out_t = scale * S_t^T q_t
+ *
+ * that is out_t = scale * sum_{j <= t} d^(t-j) (q_t . k_j) v_j, plus the carried
+ * state's scale * d^(t+1) S_0^T q_t.  log_decay is an fp32 device array of H
+ * values <= 0 (0: no decay, -inf: d = 0); it is a constant of the model, with no gradient.
+ *
+ * Heads: q and out have H heads, k and v have Hk, H a multiple of Hk; head h
+ * uses k/v head h / (H / Hk).  Widths: 1 <= Dk, Dv <= 256.
+ * Layouts: q (B, N, H, Dk), k (B, N, Hk, Dk), v (B, N, Hk, Dv), out (B, N, H, Dv).
+ * `strides` gives (batch, token, head) in elements for each tensor in the
+ * order of the arguments, NULL = dense; rows of Dk or Dv values are contiguous.
+ * Pointers need the alignment of their elements only; rows at 16-byte aligned
+ * addresses of whole 16-byte pieces are the fast case.
+ * Packed sequences: with cu_seqlens (device int32, B + 1 ascending values from
+ * 0 to the total) the tensors hold N tokens in all, (N, H, D), sequence b is
+ * tokens cu_seqlens[b] .. cu_seqlens[b+1] - 1, and batch strides are ignored.
+ * Bounds outside [0, N] are clamped; tokens of no sequence are not written.
+ * Precision: products of fp16 / bf16 storage run on the matrix cores with fp32
+ * accumulation; the products q k^T and the state are rounded to the storage
+ * type where they meet v and q, and the state itself is kept and returned to
+ * fp32 precision.  fp32 storage uses fp32 matrix instructions throughout.
+ * Range: nothing is clamped.  In fp16, scale * (q.k) and the state's elements
+ * must stay below 65504; a NaN or infinity in a token reaches every output of its
+ * sequence and head from its 64-token block on, never another sequence. */
+
+/* Device scratch bytes of fftconv_decay_fwd for T tokens in all (B * N, or N
+ * when packed); 0 where none is needed or an argument is unsupported. */
+size_t fftconv_decay_fwd_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t Dk, int64_t Dv,
+                                         fftconv_dtype_t dtype);
+
+/* Prompt form over whole sequences.
+ *   strides      int64[12] host array: q, k, v, out (or NULL)
+ *   state_in     initial states, fp32 (B, H, Dk, Dv), or NULL (zero)
+ *   state_out    receives the states after the last token, or NULL; may be state_in
+ *   state_slots  NULL, or device int32 (B): state_in and state_out are pools
+ *                (n_slots, H, Dk, Dv) and sequence b uses slot state_slots[b].
+ *                A slot outside [0, n_slots) means no state: zero, and none kept.
+ *                Slots of one call must differ.
+ * An empty sequence passes its state on.  Asynchronous on stream; out and the
+ * workspace must not overlap any argument. */
+fftconv_status_t fftconv_decay_fwd(const void *q, const void *k, const void *v, const float *log_decay, void *out,
+                                   const int64_t *strides, const float *state_in, float *state_out,
+                                   const int32_t *state_slots, int64_t n_slots, const int32_t *cu_seqlens, int64_t B,
+                                   int64_t N, int64_t H, int64_t Hk, int64_t Dk, int64_t Dv, float scale,
+                                   fftconv_dtype_t dtype, void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* One token of each of B sequences: q (B, H, Dk), k (B, Hk, Dk), v (B, Hk, Dv),
+ * out (B, H, Dv); the states are updated in place.  strides: int64[8] host
+ * array, (batch, head) of q, k, v, out, or NULL.  state and state_slots as
+ * above; a row whose slot is outside [0, n_slots) gets zeros.  No workspace. */
+fftconv_status_t fftconv_decay_step(const void *q, const void *k, const void *v, const float *log_decay, float *state,
+                                    void *out, const int64_t *strides, const int32_t *state_slots, int64_t n_slots,
+                                    int64_t B, int64_t H, int64_t Hk, int64_t Dk, int64_t Dv, float scale,
+                                    fftconv_dtype_t dtype, hipStream_t stream);
+
+size_t fftconv_decay_bwd_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t Hk, int64_t Dk, int64_t Dv,
+                                         fftconv_dtype_t dtype);
+
+/* Gradients of sum(dout * out) + sum(dstate_out * state_out) of the prompt form:
+ * with G_t = scale q_t dout_t^T + d G_{t+1} (dstate_out in place of d G behind the last token),
+ *   dq_t = scale S_t dout_t,   dk_t = G_t v_t,   dv_t = G_t^T k_t,   dstate_in = d G_0,
+ * dk and dv summed over the heads that share a key/value head.  dq, dk, dv and
+ * dstate_in may each be NULL (skipped); dstate_out NULL = zero.  States are
+ * fp32 (B, H, Dk, Dv).  strides: int64[21], dout, q, k, v, dq, dk, dv, or NULL. */
+fftconv_status_t fftconv_decay_bwd(const void *dout, const void *q, const void *k, const void *v,
+                                   const float *log_decay, void *dq, void *dk, void *dv, const int64_t *strides,
+                                   const float *state_in, const float *dstate_out, float *dstate_in,
+                                   const int32_t *cu_seqlens, int64_t B, int64_t N, int64_t H, int64_t Hk, int64_t Dk,
+                                   int64_t Dv, float scale, fftconv_dtype_t dtype, void *workspace,
+                                   size_t workspace_bytes, hipStream_t stream);
+
+/* ---- Linear product ---------------------------------------------------------
+ * The dense products around a mixer, with what follows them fused:
+ *     pre = x W^T + bias,     out = act(pre) + residual
+ * x (M, K), W (N, K), bias (N), residual, out, pre (M, N), one storage type,
+ * fp32 accumulation, everything after the product in fp32, one rounding.  Rows
+ * are contiguous; `strides` gives the row strides in elements (NULL = dense).
+ * Any sizes and element-aligned pointers; 16-byte aligned rows of whole 16-byte pieces are
+ * the fast case. */
+typedef enum {
+    FFTCONV_ACT_NONE = 0,
+    FFTCONV_ACT_RELU = 1,
+    FFTCONV_ACT_GELU = 2,      /* z/2 (1 + erf(z / sqrt 2))                                  */
+    FFTCONV_ACT_GELU_TANH = 3, /* z/2 (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3)))              */
+    FFTCONV_ACT_SILU = 4       /* z / (1 + exp(-z))                                          */
+} fftconv_activation_t;
+
+size_t fftconv_linear_fwd_workspace_bytes(int64_t M, int64_t N, int64_t K, fftconv_dtype_t dtype);
+
+/* bias, residual and pre may be NULL; pre receives x W^T + bias for the
+ * backward call.  out may be the residual itself (same pointer and stride), and
+ * overlaps nothing else.  strides: int64[5], x, W, residual, out, pre. */
+fftconv_status_t fftconv_linear_fwd(const void *x, const void *W, const void *bias, const void *residual, void *out,
+                                    void *pre, const int64_t *strides, int64_t M, int64_t N, int64_t K,
+                                    fftconv_activation_t activation, fftconv_dtype_t dtype, void *workspace,
+                                    size_t workspace_bytes, hipStream_t stream);
+
+size_t fftconv_linear_bwd_workspace_bytes(int64_t M, int64_t N, int64_t K, fftconv_dtype_t dtype);
+
+/* Gradients of sum(dout * out), with dz = dout * act'(pre):
+ *     dx = dz W,   dW = dz^T x,   dbias = sum over rows of dz      (the residual's is dout)
+ * each NULL = skipped.  pre may be NULL for FFTCONV_ACT_NONE; relu's slope at 0
+ * is 0.  dz is rounded to the storage type where it meets W and x; dbias sums it unrounded.
+ * strides: int64[6], dout, x, W, pre, dx, dW. */
+fftconv_status_t fftconv_linear_bwd(const void *dout, const void *x, const void *W, const void *pre, void *dx, void *dW,
+                                    void *dbias, const int64_t *strides, int64_t M, int64_t N, int64_t K,
+                                    fftconv_activation_t activation, fftconv_dtype_t dtype, void *workspace,
+                                    size_t workspace_bytes, hipStream_t stream);
+
 /* Static text for a status code. */
 const char *fftconv_status_string(fftconv_status_t status);
 

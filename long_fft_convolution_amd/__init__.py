@@ -90,6 +90,25 @@ def _load():
     lib.fftconv_eqlinear_prepare.restype = ctypes.c_int
     lib.fftconv_eqlinear_fwd.argtypes = [vp, vp, vp, i64, i64, i64, i64, ctypes.c_int, vp]
     lib.fftconv_eqlinear_fwd.restype = ctypes.c_int
+    ints = [i64] * 6
+    lib.fftconv_decay_fwd_workspace_bytes.argtypes = [i64] * 5 + [ctypes.c_int]
+    lib.fftconv_decay_fwd_workspace_bytes.restype = sz
+    lib.fftconv_decay_fwd.argtypes = [vp] * 9 + [i64, vp] + ints + [ctypes.c_float, ctypes.c_int, vp, sz, vp]
+    lib.fftconv_decay_fwd.restype = ctypes.c_int
+    lib.fftconv_decay_step.argtypes = [vp] * 8 + [i64] * 6 + [ctypes.c_float, ctypes.c_int, vp]
+    lib.fftconv_decay_step.restype = ctypes.c_int
+    lib.fftconv_decay_bwd_workspace_bytes.argtypes = ints + [ctypes.c_int]
+    lib.fftconv_decay_bwd_workspace_bytes.restype = sz
+    lib.fftconv_decay_bwd.argtypes = [vp] * 13 + ints + [ctypes.c_float, ctypes.c_int, vp, sz, vp]
+    lib.fftconv_decay_bwd.restype = ctypes.c_int
+    lib.fftconv_linear_fwd_workspace_bytes.argtypes = [i64] * 3 + [ctypes.c_int]
+    lib.fftconv_linear_fwd_workspace_bytes.restype = sz
+    lib.fftconv_linear_fwd.argtypes = [vp] * 7 + [i64] * 3 + [ctypes.c_int, ctypes.c_int, vp, sz, vp]
+    lib.fftconv_linear_fwd.restype = ctypes.c_int
+    lib.fftconv_linear_bwd_workspace_bytes.argtypes = [i64] * 3 + [ctypes.c_int]
+    lib.fftconv_linear_bwd_workspace_bytes.restype = sz
+    lib.fftconv_linear_bwd.argtypes = [vp] * 8 + [i64] * 3 + [ctypes.c_int, ctypes.c_int, vp, sz, vp]
+    lib.fftconv_linear_bwd.restype = ctypes.c_int
     _lib = lib
     return lib
 
@@ -350,6 +369,258 @@ def eqlinear(x, W, stream=None):
     y = torch.empty((x.shape[0], T, C_out), dtype=x.dtype, device=x.device)
     fftconv_eqlinear_fwd(x, W_f, y, stream)
     return y
+
+
+# ---------------------------------------------------------------- decay attention
+def _dtype_of(dtype) -> int:
+    return dtype if isinstance(dtype, int) else dtype_code(dtype)
+
+
+def _rows_tensor(t, name, like, dims):
+    """Checks a tensor argument whose rows must be contiguous (other strides are free)."""
+    if not t.is_cuda or t.device != like.device:
+        raise ValueError(f"{name} must be a tensor on {like.device}" if like.is_cuda else f"{name} must be a device tensor")
+    if t.dtype != like.dtype:
+        raise ValueError(f"{name} must have dtype {like.dtype}")
+    if t.dim() != dims:
+        raise ValueError(f"{name} must have {dims} dimensions")
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise ValueError(f"{name} must be contiguous along its last dimension")
+
+
+def _plain_tensor(t, name, dtype, shape, device):
+    if t is None:
+        return
+    if not t.is_cuda or t.device != device or t.dtype != dtype or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor on {device}")
+    if shape is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, not {tuple(t.shape)}")
+
+
+def _strides(tensors, packed):
+    """(batch, token, head) of each tensor; None (an absent gradient) counts as dense zeros."""
+    flat = []
+    for t in tensors:
+        if t is None:
+            flat += (0, 0, 0)
+        elif packed:
+            flat += (0, t.stride(0), t.stride(1))
+        else:
+            flat += t.stride()[:3]
+    return (ctypes.c_int64 * len(flat))(*flat)
+
+
+def _nbytes(t):
+    return 0 if t is None else t.numel() * t.element_size()
+
+
+def _decay_shapes(q, k, v, log_decay, cu_seqlens):
+    dims = 4 if cu_seqlens is None else 3
+    _rows_tensor(q, "q", q, dims)
+    _rows_tensor(k, "k", q, dims)
+    _rows_tensor(v, "v", q, dims)
+    lead = tuple(q.shape[:-2])
+    if tuple(k.shape[:-2]) != lead or tuple(v.shape[:-1]) != tuple(k.shape[:-1]) or k.shape[-1] != q.shape[-1]:
+        raise ValueError(f"shapes of q {tuple(q.shape)}, k {tuple(k.shape)}, v {tuple(v.shape)} do not match")
+    H, Hk, Dk, Dv = q.shape[-2], k.shape[-2], q.shape[-1], v.shape[-1]
+    _plain_tensor(log_decay, "log_decay", torch.float32, (H,), q.device)
+    if cu_seqlens is None:
+        return lead[0], lead[1], H, Hk, Dk, Dv
+    _plain_tensor(cu_seqlens, "cu_seqlens", torch.int32, None, q.device)
+    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+        raise ValueError("cu_seqlens must hold B + 1 values")
+    return cu_seqlens.numel() - 1, lead[0], H, Hk, Dk, Dv
+
+
+def fftconv_decay_fwd_workspace_bytes(B: int, T: int, H: int, Dk: int, Dv: int, dtype) -> int:
+    return int(_load().fftconv_decay_fwd_workspace_bytes(B, T, H, Dk, Dv, _dtype_of(dtype)))
+
+
+def fftconv_decay_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor, out: torch.Tensor,
+                      scale: float, state_in: torch.Tensor | None = None, state_out: torch.Tensor | None = None,
+                      state_slots: torch.Tensor | None = None, cu_seqlens: torch.Tensor | None = None,
+                      workspace: torch.Tensor | None = None, stream=None) -> None:
+    """out <- decay attention of q, k, v: (B, N, heads, width), or packed (T, heads, width) with cu_seqlens.
+
+    state_in / state_out: fp32 (B, H, Dk, Dv), or pools of such matrices with state_slots (B) int32.
+    """
+    B, N, H, Hk, Dk, Dv = _decay_shapes(q, k, v, log_decay, cu_seqlens)
+    _rows_tensor(out, "out", q, q.dim())
+    if tuple(out.shape) != (*q.shape[:-1], Dv):
+        raise ValueError(f"out must have shape {(*q.shape[:-1], Dv)}")
+    n_slots = 0
+    if state_slots is not None:
+        _plain_tensor(state_slots, "state_slots", torch.int32, (B,), q.device)
+        pool = state_in if state_in is not None else state_out
+        n_slots = pool.shape[0] if pool is not None else 0
+    for name, t in (("state_in", state_in), ("state_out", state_out)):
+        _plain_tensor(t, name, torch.float32, (B if state_slots is None else n_slots, H, Dk, Dv), q.device)
+    _dev_tensor(workspace, "workspace")
+    _check(_load().fftconv_decay_fwd(
+        _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(out), _strides((q, k, v, out), cu_seqlens is not None),
+        _ptr(state_in), _ptr(state_out), _ptr(state_slots), n_slots, _ptr(cu_seqlens), B, N, H, Hk, Dk, Dv, scale,
+        dtype_code(q.dtype), _ptr(workspace), _nbytes(workspace), _stream(stream, q.device)))
+
+
+def fftconv_decay_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor,
+                       state: torch.Tensor, out: torch.Tensor, scale: float, state_slots: torch.Tensor | None = None,
+                       stream=None) -> None:
+    """One token of each sequence: q (B, H, Dk), k (B, Hk, Dk), v (B, Hk, Dv) -> out (B, H, Dv), state in place."""
+    for name, t in (("q", q), ("k", k), ("v", v), ("out", out)):
+        _rows_tensor(t, name, q, 3)
+    (B, H, Dk), (Hk, Dv) = q.shape, v.shape[1:]
+    if tuple(k.shape) != (B, Hk, Dk) or v.shape[0] != B or tuple(out.shape) != (B, H, Dv):
+        raise ValueError(f"shapes of q {tuple(q.shape)}, k {tuple(k.shape)}, v {tuple(v.shape)}, "
+                         f"out {tuple(out.shape)} do not match")
+    _plain_tensor(log_decay, "log_decay", torch.float32, (H,), q.device)
+    n_slots = 0
+    if state_slots is not None:
+        _plain_tensor(state_slots, "state_slots", torch.int32, (B,), q.device)
+        n_slots = state.shape[0]
+    _plain_tensor(state, "state", torch.float32, (B if state_slots is None else n_slots, H, Dk, Dv), q.device)
+    strides = (ctypes.c_int64 * 8)(*q.stride()[:2], *k.stride()[:2], *v.stride()[:2], *out.stride()[:2])
+    _check(_load().fftconv_decay_step(
+        _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(state), _ptr(out), strides, _ptr(state_slots), n_slots,
+        B, H, Hk, Dk, Dv, scale, dtype_code(q.dtype), _stream(stream, q.device)))
+
+
+def fftconv_decay_bwd_workspace_bytes(B: int, T: int, H: int, Hk: int, Dk: int, Dv: int, dtype) -> int:
+    return int(_load().fftconv_decay_bwd_workspace_bytes(B, T, H, Hk, Dk, Dv, _dtype_of(dtype)))
+
+
+def fftconv_decay_bwd(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor,
+                      dq: torch.Tensor | None, dk: torch.Tensor | None, dv: torch.Tensor | None, scale: float,
+                      state_in: torch.Tensor | None = None, dstate_out: torch.Tensor | None = None,
+                      dstate_in: torch.Tensor | None = None, cu_seqlens: torch.Tensor | None = None,
+                      workspace: torch.Tensor | None = None, stream=None) -> None:
+    """Gradients of fftconv_decay_fwd into dq, dk, dv, dstate_in (None = skip)."""
+    B, N, H, Hk, Dk, Dv = _decay_shapes(q, k, v, log_decay, cu_seqlens)
+    for name, t, shape in (("dout", dout, (*q.shape[:-1], Dv)), ("dq", dq, q.shape), ("dk", dk, k.shape),
+                           ("dv", dv, v.shape)):
+        if t is None and name != "dout":
+            continue
+        _rows_tensor(t, name, q, q.dim())
+        if tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name} must have shape {tuple(shape)}")
+    for name, t in (("state_in", state_in), ("dstate_out", dstate_out), ("dstate_in", dstate_in)):
+        _plain_tensor(t, name, torch.float32, (B, H, Dk, Dv), q.device)
+    _dev_tensor(workspace, "workspace")
+    _check(_load().fftconv_decay_bwd(
+        _ptr(dout), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(dq), _ptr(dk), _ptr(dv),
+        _strides((dout, q, k, v, dq, dk, dv), cu_seqlens is not None), _ptr(state_in), _ptr(dstate_out),
+        _ptr(dstate_in), _ptr(cu_seqlens), B, N, H, Hk, Dk, Dv, scale, dtype_code(q.dtype), _ptr(workspace),
+        _nbytes(workspace), _stream(stream, q.device)))
+
+
+def _scratch(nbytes, device):
+    return None if nbytes == 0 else torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+def decay_attention(q, k, v, log_decay, scale=None, state_in=None, cu_seqlens=None, stream=None):
+    """Decay attention of whole sequences (allocations by torch); returns (out, final states).  scale: Dk^-0.5."""
+    B, N, H, Hk, Dk, Dv = _decay_shapes(q, k, v, log_decay, cu_seqlens)
+    T = N if cu_seqlens is not None else B * N
+    out = torch.empty((*q.shape[:-1], Dv), dtype=q.dtype, device=q.device)
+    state_out = torch.empty((B, H, Dk, Dv), dtype=torch.float32, device=q.device)
+    ws = _scratch(fftconv_decay_fwd_workspace_bytes(B, T, H, Dk, Dv, q.dtype), q.device)
+    fftconv_decay_fwd(q, k, v, log_decay, out, Dk ** -0.5 if scale is None else scale, state_in, state_out,
+                      cu_seqlens=cu_seqlens, workspace=ws, stream=stream)
+    return out, state_out
+
+
+def decay_attention_bwd(q, k, v, log_decay, dout, scale=None, state_in=None, dstate_out=None, cu_seqlens=None,
+                        stream=None):
+    """Gradients of decay_attention; returns (dq, dk, dv, dstate_in), the last None without state_in."""
+    B, N, H, Hk, Dk, Dv = _decay_shapes(q, k, v, log_decay, cu_seqlens)
+    T = N if cu_seqlens is not None else B * N
+    dq, dk, dv = (torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k, v))
+    dstate_in = None if state_in is None else torch.empty_like(state_in)
+    ws = _scratch(fftconv_decay_bwd_workspace_bytes(B, T, H, Hk, Dk, Dv, q.dtype), q.device)
+    fftconv_decay_bwd(dout, q, k, v, log_decay, dq, dk, dv, Dk ** -0.5 if scale is None else scale, state_in,
+                      dstate_out, dstate_in, cu_seqlens, ws, stream)
+    return dq, dk, dv, dstate_in
+
+
+# ---------------------------------------------------------------- linear product
+ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
+
+
+def _activation(name) -> int:
+    if name not in ACTIVATIONS:
+        raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}, not {name!r}")
+    return ACTIVATIONS[name]
+
+
+def _matrices(like, *named):
+    for name, t, shape in named:
+        if t is None:
+            continue
+        _rows_tensor(t, name, like, len(shape))
+        if tuple(t.shape) != shape:
+            raise ValueError(f"{name} must have shape {shape}, not {tuple(t.shape)}")
+
+
+def _row_strides(*tensors):
+    return (ctypes.c_int64 * len(tensors))(*(0 if t is None else t.stride(0) for t in tensors))
+
+
+def fftconv_linear_fwd_workspace_bytes(M: int, N: int, K: int, dtype) -> int:
+    return int(_load().fftconv_linear_fwd_workspace_bytes(M, N, K, _dtype_of(dtype)))
+
+
+def fftconv_linear_fwd(x: torch.Tensor, W: torch.Tensor, bias: torch.Tensor | None, residual: torch.Tensor | None,
+                       out: torch.Tensor, pre: torch.Tensor | None = None, activation: str = "none",
+                       workspace: torch.Tensor | None = None, stream=None) -> None:
+    """out <- act(x W^T + bias) + residual for x (M, K), W (N, K); pre (optional) <- x W^T + bias."""
+    _rows_tensor(x, "x", x, 2)
+    _rows_tensor(W, "W", x, 2)
+    (M, K), N = x.shape, W.shape[0]
+    _matrices(x, ("W", W, (N, K)), ("bias", bias, (N,)), ("residual", residual, (M, N)), ("out", out, (M, N)),
+              ("pre", pre, (M, N)))
+    _dev_tensor(workspace, "workspace")
+    _check(_load().fftconv_linear_fwd(
+        _ptr(x), _ptr(W), _ptr(bias), _ptr(residual), _ptr(out), _ptr(pre), _row_strides(x, W, residual, out, pre),
+        M, N, K, _activation(activation), dtype_code(x.dtype), _ptr(workspace), _nbytes(workspace),
+        _stream(stream, x.device)))
+
+
+def fftconv_linear_bwd_workspace_bytes(M: int, N: int, K: int, dtype) -> int:
+    return int(_load().fftconv_linear_bwd_workspace_bytes(M, N, K, _dtype_of(dtype)))
+
+
+def fftconv_linear_bwd(dout: torch.Tensor, x: torch.Tensor, W: torch.Tensor, pre: torch.Tensor | None,
+                       dx: torch.Tensor | None, dW: torch.Tensor | None, dbias: torch.Tensor | None,
+                       activation: str = "none", workspace: torch.Tensor | None = None, stream=None) -> None:
+    """Gradients of fftconv_linear_fwd into dx, dW, dbias (None = skip); the residual's is dout."""
+    _rows_tensor(x, "x", x, 2)
+    _rows_tensor(W, "W", x, 2)
+    (M, K), N = x.shape, W.shape[0]
+    _matrices(x, ("dout", dout, (M, N)), ("W", W, (N, K)), ("pre", pre, (M, N)), ("dx", dx, (M, K)),
+              ("dW", dW, (N, K)), ("dbias", dbias, (N,)))
+    _dev_tensor(workspace, "workspace")
+    _check(_load().fftconv_linear_bwd(
+        _ptr(dout), _ptr(x), _ptr(W), _ptr(pre), _ptr(dx), _ptr(dW), _ptr(dbias),
+        _row_strides(dout, x, W, pre, dx, dW), M, N, K, _activation(activation), dtype_code(x.dtype),
+        _ptr(workspace), _nbytes(workspace), _stream(stream, x.device)))
+
+
+def linear_act(x, W, bias=None, residual=None, activation="none", keep_pre=False, stream=None):
+    """act(x W^T + bias) + residual (allocations by torch); with keep_pre also x W^T + bias for linear_act_bwd."""
+    M, N = x.shape[0], W.shape[0]
+    out = torch.empty((M, N), dtype=x.dtype, device=x.device)
+    pre = torch.empty_like(out) if keep_pre else None
+    ws = _scratch(fftconv_linear_fwd_workspace_bytes(M, N, x.shape[1], x.dtype), x.device)
+    fftconv_linear_fwd(x, W, bias, residual, out, pre, activation, ws, stream)
+    return (out, pre) if keep_pre else out
+
+
+def linear_act_bwd(dout, x, W, pre=None, activation="none", bias=True, stream=None):
+    """Gradients of linear_act; returns (dx, dW, dbias), dbias None without a bias."""
+    dx, dW = (torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (x, W))
+    dbias = torch.empty(W.shape[0], dtype=x.dtype, device=x.device) if bias else None
+    ws = _scratch(fftconv_linear_bwd_workspace_bytes(x.shape[0], W.shape[0], x.shape[1], x.dtype), x.device)
+    fftconv_linear_bwd(dout, x, W, pre, dx, dW, dbias, activation, ws, stream)
+    return dx, dW, dbias
 
 
 def alloc_filter(H: int, N: int, dtype: torch.dtype, device="cuda") -> torch.Tensor:

@@ -17,7 +17,9 @@ CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "libfftconv.so")
 BUILD_DIR = os.path.join(HERE, "_build")
 
-SOURCES = ["api.cpp", "bwd.hip", "eqlinear.hip", "filter.hip", "fused.hip", "multipass.hip", "pair_mfma.hip", "pair16k.hip"]
+SOURCES = ["multipass.hip", "pair16k.hip", "pair_mfma.hip", "decay_f32.hip", "decay_bf16.hip", "decay_f16.hip",
+           "linear_bf16.hip", "linear_f16.hip", "linear_f32.hip", "fused.hip", "eqlinear.hip", "bwd.hip", "filter.hip",
+           "api.cpp", "sequence_ops.cpp"]   # the longest compilations first
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

@@ -101,6 +101,8 @@ hipError_t upload(const std::vector<float2> &v, const float2 **out) {
 
 namespace fftconv {
 
+void set_last_error(const char *text) { g_last_error = text; }
+
 namespace {
 std::mutex g_pair_mu;
 std::map<int, PairTables> g_pair_tables;

@@ -16,6 +16,9 @@ constexpr int kMinLog = 10;
 constexpr int kMaxLog = 22;
 constexpr int kMaskBlocks = 128;
 
+// The calling thread's error text (fftconv_last_error).
+void set_last_error(const char *text);
+
 enum StorageType : int { ST_F32 = 0, ST_F16 = 1, ST_BF16 = 2 };
 enum KfLayout : int { KF_NATURAL = 0, KF_ROWS = 1, KF_PAIR = 2, KF_PAIR3 = 3 };
 

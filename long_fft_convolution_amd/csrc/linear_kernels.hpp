@@ -1,0 +1,512 @@
+// linear_kernels.hpp -- out = act(x W^T + bias) + residual and its gradients
+// on the matrix cores.  Instantiated per storage type by linear_f16.hip,
+// linear_bf16.hip and linear_f32.hip.
+//
+// One tile kernel serves the three products of a linear layer,
+//     C[m][n] = sum_k A(m, k) B(n, k):
+//     out: A = x, B = W, both contiguous along k;
+//     dx:  A = dz, B(n, k) = W[k][n], contiguous along n;
+//     dW:  A(m, k) = dz[k][m], B(n, k) = x[k][n], both contiguous along the tile.
+// A workgroup computes a BM x BN tile over K steps of 128 bytes; tiles of both
+// operands stream from HBM straight into LDS (buffer loads with an LDS
+// destination, 16 bytes a lane, zero past the operand's edge by the buffer
+// unit's range check), two stages deep, so the step being multiplied hides
+// the next one's loads and no register holds them.  The destination of such a
+// load is linear in the lane, so the bank swizzle permutes the source: lane
+// l fetches the 16 bytes that belong at its place.
+//
+// An operand contiguous along k lies in LDS as rows of 128 bytes, its eight
+// 16-byte slots exchanged by s ^ (row & 7); one contiguous along the tile as k
+// rows of the tile's width, read with the transposing LDS read (16-bit types;
+// 32-byte granules exchanged by (k & 3) + 4 ((k >> 3) & 1)) or value by value
+// (fp32; 64-byte granules exchanged by (k >> 3) & 3).  The product is taken as
+// B A (rows n, columns m), so a lane holds four neighbouring n of one row.
+#pragma once
+
+#include "mma.hpp"
+#include "sequence_ops.hpp"
+
+namespace fftconv {
+
+__device__ __forceinline__ float act_value(float z, int act) {
+    switch (act) {
+    case ACT_RELU: return z > 0.0f ? z : (z != z ? z : 0.0f);
+    case ACT_GELU: return 0.5f * z * (1.0f + erff(z * 0.70710678118654752440f));
+    case ACT_GELU_TANH: return 0.5f * z * (1.0f + tanhf(0.79788456080286535588f * (z + 0.044715f * z * z * z)));
+    case ACT_SILU: return z / (1.0f + __expf(-z));
+    default: return z;
+    }
+}
+__device__ __forceinline__ float act_slope(float z, int act) {
+    switch (act) {
+    case ACT_RELU: return z > 0.0f ? 1.0f : 0.0f;
+    case ACT_GELU:
+        return 0.5f * (1.0f + erff(z * 0.70710678118654752440f)) + z * __expf(-0.5f * z * z) * 0.39894228040143267794f;
+    case ACT_GELU_TANH: {
+        const float t = tanhf(0.79788456080286535588f * (z + 0.044715f * z * z * z));
+        const float u = z * z;
+        // (1 - t^2) vanishes before the factor overflows
+        const float s = 1.0f - t * t;
+        return 0.5f * (1.0f + t) + (s == 0.0f ? 0.0f : 0.5f * z * s * 0.79788456080286535588f * (1.0f + 0.134145f * u));
+    }
+    case ACT_SILU: {
+        const float p = 1.0f / (1.0f + __expf(-z));
+        const float n = 1.0f - p;
+        return p * (1.0f + (n == 0.0f ? 0.0f : z * n));
+    }
+    default: return 1.0f;
+    }
+}
+
+template <typename T> struct Quad { T v[4]; };
+
+template <typename T> __device__ __forceinline__ void load_quad(const T *p, int n, int vec, float *f) {
+    if (vec && n >= 4) {
+        Quad<T> q;
+        __builtin_memcpy(&q, __builtin_assume_aligned(p, 4 * sizeof(T)), sizeof q);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = (float)q.v[i];
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = i < n ? (float)p[i] : 0.0f;
+    }
+}
+template <typename T> __device__ __forceinline__ void store_quad(T *p, int n, int vec, const float *f) {
+    if (vec && n >= 4) {
+        Quad<T> q;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) q.v[i] = (T)f[i];
+        __builtin_memcpy(__builtin_assume_aligned(p, 4 * sizeof(T)), &q, sizeof q);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < n) p[i] = (T)f[i];
+    }
+}
+
+// bias, kept pre-activation, activation, residual, store: values n .. n + 3 of row m
+template <typename T>
+__device__ __forceinline__ void linear_epilogue(const LinearGemm &a, int64_t m, int64_t n, float *f) {
+    const int left = a.N - n < 4 ? (int)(a.N - n) : 4;
+    float t[4];
+    if (a.bias) {
+        load_quad(static_cast<const T *>(a.bias) + n, left, a.vec_b, t);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] += t[i];
+    }
+    if (a.pre) store_quad(static_cast<T *>(a.pre) + m * a.ldp + n, left, a.vec_p, f);
+    if (a.act != ACT_NONE) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = act_value(f[i], a.act);
+    }
+    if (a.res) {
+        load_quad(static_cast<const T *>(a.res) + m * a.ldr + n, left, a.vec_r, t);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] += t[i];
+    }
+    store_quad(static_cast<T *>(a.C) + m * a.ldc + n, left, a.vec_c, f);
+}
+
+// One operand's tile: R rows (of m or n) by BK of k.  KC: contiguous along k.
+template <typename T, int R, int NW, bool KC> struct OperandTile {
+    static constexpr int E = 16 / (int)sizeof(T);
+    static constexpr int BK = 128 / (int)sizeof(T);
+    static constexpr int PR = KC ? BK / E : R / E;          // 16-byte pieces of an LDS row
+    static constexpr int PIECES = R * BK / E;
+    static constexpr int N = PIECES / (64 * NW);            // loads of a lane
+    static constexpr int ROWLEN = KC ? BK : R;              // values of an LDS row
+    static_assert(PIECES % (64 * NW) == 0, "whole loads");
+
+    // exchange of the 32-byte granules of a 16-bit tile's k rows: the eight rows k = 8 g + r (g < 2, r < 4)
+    // that one half of a transposing read meets lie in eight different granules of the banks' 256 bytes
+    // (tiles of 64 have rows of 128 bytes, two of which share a period)
+    static __device__ __forceinline__ int granule(int k) {
+        return R >= 128 ? (k & 3) | ((k >> 1) & 4) : ((k >> 1) & 1) | ((k >> 2) & 2);
+    }
+    // LDS piece p holds source piece (row, slot)
+    static __device__ __forceinline__ void source(int p, int &row, int &slot) {
+        row = p / PR;
+        const int s = p % PR;
+        if (KC) slot = s ^ (row & 7);
+        else if (sizeof(T) == 2) slot = (s & ~15) | ((((s >> 1) & 7) ^ granule(row)) << 1) | (s & 1);
+        else slot = (s & ~15) | ((((s >> 2) & 3) ^ ((row >> 3) & 3)) << 2) | (s & 3);
+    }
+
+    uint32_t off[N];    // byte offset of each load from the tile's origin at k = 0
+    // rows: how many of the tile's R rows exist (rounded up to pieces along the tile)
+    __device__ __forceinline__ void prepare(int64_t ld, int64_t rows) {
+        const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            int row, slot;
+            source((i * NW + wave) * 64 + lane, row, slot);
+            const bool in = KC ? row < rows : slot * E < rows;
+            off[i] = in ? (uint32_t)(row * ld * (int64_t)sizeof(T)) + slot * 16 : 0x80000000u;
+        }
+    }
+    // origin: the tile's first row at the step's first k; kleft: k values left in this step
+    // (pieces that begin past it read zero)
+    __device__ __forceinline__ void issue(const T *origin, T *tile, int kleft) const {
+        // the buffer view and the LDS place are scalar operands: the wave index as one
+        const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+        auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<T *>(origin), (short)0, 0x7fffffff, 0x00020000);
+        auto place = [&](int i) { return FFTCONV_LDS_CAST(void, tile + (i * NW + wave) * 64 * E); };
+        if (kleft >= BK) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, place(i), 16, off[i], 0, 0, 0);
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            int row, slot;
+            source((i * NW + wave) * 64 + lane, row, slot);
+            const uint32_t o = (KC ? slot * E : row) < kleft ? off[i] : 0x80000000u;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, place(i), 16, o, 0, 0, 0);
+        }
+    }
+    // the same tile without alignment or whole pieces: through registers, value by value at the edges
+    __device__ __forceinline__ void fetch(const T *origin, int64_t ld, int64_t rows, int64_t kleft, uint4 *r) const {
+        const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            int row, slot;
+            source((i * NW + wave) * 64 + lane, row, slot);
+            const int64_t most = KC ? kleft : rows;     // along the contiguous direction
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (row < (KC ? rows : kleft)) {
+                const T *p = origin + row * ld + slot * E;
+                if (slot * E + E <= most) {
+                    __builtin_memcpy(&v, p, 16);
+                } else {
+                    T e[E];
+#pragma unroll
+                    for (int j = 0; j < E; ++j) e[j] = slot * E + j < most ? p[j] : (T)0.0f;
+                    __builtin_memcpy(&v, e, 16);
+                }
+            }
+            r[i] = v;
+        }
+    }
+    static __device__ __forceinline__ void put(T *tile, const uint4 *r) {
+        const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+#pragma unroll
+        for (int i = 0; i < N; ++i) *reinterpret_cast<uint4 *>(tile + ((i * NW + wave) * 64 + lane) * E) = r[i];
+    }
+    // operand of rows r0 .. r0 + 15 at k slots kk * 32 + 8 g + j
+    static __device__ __forceinline__ typename Mma<T>::v8 frag(const T *tile, int r0, int kk) {
+        const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
+        if constexpr (KC) {
+            const int row = r0 + c;
+            if constexpr (sizeof(T) == 2) {
+                return lds_row8<T>(tile + row * BK + (((kk * 4 + g) ^ (row & 7)) * E));
+            } else {
+                const f32x4 a = *reinterpret_cast<const f32x4 *>(tile + row * BK + ((2 * g) ^ (row & 7)) * E);
+                const f32x4 b = *reinterpret_cast<const f32x4 *>(tile + row * BK + ((2 * g + 1) ^ (row & 7)) * E);
+                return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+            }
+        } else if constexpr (sizeof(T) == 2) {
+            const int k = kk * 32 + g * 8 + (c >> 2);             // and k + 4
+            const int col = r0 + (c & 3) * 4;                     // 16 columns: one 32-byte granule
+            const int h = granule(k);                             // the same for k + 4
+            const T *p = tile + k * R + ((col & ~127) | ((((col >> 4) & 7) ^ h) << 4) | (col & 15));
+            typedef typename Mma<T>::v4 v4;
+            const v4 a = __builtin_bit_cast(v4, __builtin_amdgcn_ds_read_tr16_b64_v4i16(FFTCONV_LDS_CAST(s16x4, p)));
+            const v4 b = __builtin_bit_cast(v4, __builtin_amdgcn_ds_read_tr16_b64_v4i16(FFTCONV_LDS_CAST(s16x4, p + 4 * R)));
+            return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+        } else {
+            typename Mma<T>::v8 v;
+            const int col = r0 + c;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int k = kk * 32 + g * 8 + j;
+                v[j] = tile[k * R + ((col & ~63) | ((((col >> 4) & 3) ^ (g & 3)) << 4) | (col & 15))];
+            }
+            return v;
+        }
+    }
+};
+
+// Tile of workgroup id: ids are dealt to the 8 XCDs in turn, so consecutive ids of one XCD take
+// neighbouring tiles (bands of 8 tile rows), whose operands its own L2 then holds.
+__device__ __forceinline__ void tile_of(int64_t id, int64_t tm, int64_t tn, int64_t &bm, int64_t &bn) {
+    const int64_t total = tm * tn, per = total / 8, rest = total % 8;
+    const int64_t xcd = id % 8, at = id / 8;
+    id = xcd * per + (xcd < rest ? xcd : rest) + at;
+    const int64_t band = 8 * tn, b = id / band;
+    const int64_t rows = tm - b * 8 < 8 ? tm - b * 8 : 8;
+    // scalar values: what they address is the same for the whole wave
+    bm = __builtin_amdgcn_readfirstlane((int)(b * 8 + id % band % rows));
+    bn = __builtin_amdgcn_readfirstlane((int)(id % band / rows));
+}
+
+// TM x TN 16x16 tiles per wave, WM x WN waves.  VEC: operands 16-byte aligned in rows of whole pieces.
+template <typename T, int LAYOUT, int TM, int TN, int WM, int WN, bool VEC>
+__global__ __launch_bounds__(64 * WM * WN, 2) void linear_gemm_kernel(const LinearGemm a) {
+#ifdef __HIP_DEVICE_COMPILE__   // the host pass, which cannot take the LDS-destination loads, needs the stub alone
+    constexpr int BM = TM * WM * 16, BN = TN * WN * 16, NW = WM * WN;
+    constexpr bool AK = LAYOUT != LAYOUT_TN, BKC = LAYOUT == LAYOUT_NT;
+    using TA = OperandTile<T, BM, NW, AK>;
+    using TB = OperandTile<T, BN, NW, BKC>;
+    constexpr int BK = TA::BK, KK = BK / 32;
+    // two stages as separate arrays: the loads into one are then known not to alias the reads of the other
+    __shared__ __attribute__((aligned(128))) T sa0[BM * BK], sb0[BN * BK];
+    __shared__ __attribute__((aligned(128))) T sa1[BM * BK], sb1[BN * BK];
+    const int64_t tm = (a.M + BM - 1) / BM, tn = (a.N + BN - 1) / BN;
+    int64_t bm, bn;
+    tile_of(blockIdx.x, tm, tn, bm, bn);
+    const int64_t m0 = bm * BM, n0 = bn * BN;
+    const int64_t k0 = blockIdx.y * a.kper, k1 = k0 + a.kper < a.K ? k0 + a.kper : a.K;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, c = lane & 15;
+    const int wm = (wave / WN) * TM * 16, wn = (wave % WN) * TN * 16;
+    const T *pa = static_cast<const T *>(a.A) + (AK ? m0 * a.lda + k0 : k0 * a.lda + m0);
+    const T *pb = static_cast<const T *>(a.B) + (BKC ? n0 * a.ldb + k0 : k0 * a.ldb + n0);
+    const int64_t sa_step = AK ? BK : BK * a.lda, sb_step = BKC ? BK : BK * a.ldb;
+
+    TA ta;
+    TB tb;
+    if (VEC) {
+        ta.prepare(a.lda, a.M - m0);
+        tb.prepare(a.ldb, a.N - n0);
+    }
+    f32x4 acc[TM][TN];
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+
+    uint4 ra[VEC ? 1 : TA::N], rb[VEC ? 1 : TB::N];
+    auto bring = [&](int64_t k, T *na, T *nb) __attribute__((always_inline)) {
+        const int64_t left = k1 - k;
+        const int kl = left < BK ? (int)left : BK;
+        if constexpr (VEC) {
+            ta.issue(pa, na, kl);
+            tb.issue(pb, nb, kl);
+        } else {
+            ta.fetch(pa, a.lda, a.M - m0, kl, ra);
+            tb.fetch(pb, a.ldb, a.N - n0, kl, rb);
+        }
+        pa += sa_step;
+        pb += sb_step;
+    };
+    // multiplies the step in (ca, cb) while the next one travels into (na, nb)
+    auto step = [&](int64_t k, T *ca, T *cb, T *na, T *nb) __attribute__((always_inline)) {
+        if constexpr (!VEC) {
+            TA::put(ca, ra);
+            TB::put(cb, rb);
+        }
+        __syncthreads();      // this step's tiles are in LDS; the other stage's readers are done
+        if (k + BK < k1) bring(k + BK, na, nb);
+#pragma unroll
+        for (int kk = 0; kk < KK; ++kk) {
+            typename Mma<T>::v8 fa[TM], fb[TN];
+#pragma unroll
+            for (int i = 0; i < TM; ++i) fa[i] = TA::frag(ca, wm + i * 16, kk);
+#pragma unroll
+            for (int j = 0; j < TN; ++j) fb[j] = TB::frag(cb, wn + j * 16, kk);
+#pragma unroll
+            for (int i = 0; i < TM; ++i)
+#pragma unroll
+                for (int j = 0; j < TN; ++j) acc[i][j] = Mma<T>::mma(fb[j], fa[i], acc[i][j]);
+        }
+    };
+    if (k0 < k1) bring(k0, sa0, sb0);
+    for (int64_t k = k0; k < k1; k += 2 * BK) {
+        step(k, sa0, sb0, sa1, sb1);
+        if (k + BK < k1) step(k + BK, sa1, sb1, sa0, sb0);
+    }
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+        const int64_t m = m0 + wm + i * 16 + c;
+        if (m >= a.M) continue;
+#pragma unroll
+        for (int j = 0; j < TN; ++j) {
+            const int64_t n = n0 + wn + j * 16 + g * 4;
+            if (n >= a.N) continue;
+            float f[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
+            if (a.part) {
+                float *p = a.part + ((int64_t)blockIdx.y * a.M + m) * a.N + n;
+                store_quad(p, a.N - n < 4 ? (int)(a.N - n) : 4, a.N % 4 == 0, f);
+            } else {
+                linear_epilogue<T>(a, m, n, f);
+            }
+        }
+    }
+#endif
+}
+
+// joins the splits of a product: sum of the partial sums in split order, then the epilogue
+template <typename T> __global__ __launch_bounds__(256) void linear_join_kernel(const LinearGemm a) {
+    const int64_t quads = (a.N + 3) / 4, total = a.M * quads;
+    for (int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+        const int64_t m = i / quads, n = i % quads * 4;
+        const int left = a.N - n < 4 ? (int)(a.N - n) : 4;
+        float f[4] = {0, 0, 0, 0};
+        for (int s = 0; s < a.splits; ++s) {
+            float t[4];
+            load_quad(a.part + ((int64_t)s * a.M + m) * a.N + n, left, a.N % 4 == 0, t);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) f[j] += t[j];
+        }
+        linear_epilogue<T>(a, m, n, f);
+    }
+}
+
+// Few rows (M <= 16 MT): bound by the bytes of W.  A wave multiplies 16 rows of W, read straight
+// from HBM in the operand layout, with the rows of x; the workgroup's waves share K and join in LDS.
+template <typename T, int MT, bool VEC>
+__global__ __launch_bounds__(256) void linear_rows_kernel(const LinearGemm a) {
+    constexpr int U = 4;
+    __shared__ f32x4 part[4][MT][64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, c = lane & 15;
+    const int64_t n0 = (int64_t)blockIdx.x * 16;
+    const int64_t per = ((a.K + 31) / 32 + 3) / 4 * 32;
+    const int64_t k0 = wave * per, k1 = k0 + per < a.K ? k0 + per : a.K;
+    const T *pw = static_cast<const T *>(a.B) + (n0 + c) * a.ldb;
+    const T *px = static_cast<const T *>(a.A) + c * a.lda;
+    const bool wn = n0 + c < a.N;
+    typedef typename Mma<T>::v8 v8;
+    auto load8 = [&](const T *p, int64_t k, bool in) {
+        v8 v;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = (T)0.0f;
+        if (VEC) {
+            if (in && k < k1) __builtin_memcpy(&v, __builtin_assume_aligned(p + k, 16), sizeof v);
+        } else if (in && k + 8 <= k1) {
+            __builtin_memcpy(&v, p + k, sizeof v);
+        } else if (in) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (k + j < k1) v[j] = p[k + j];
+        }
+        return v;
+    };
+    f32x4 acc[MT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) acc[i] = f32x4{0, 0, 0, 0};
+    for (int64_t k = k0; k < k1; k += 32 * U) {
+        v8 w[U], x[U][MT];
+#pragma unroll
+        for (int u = 0; u < U; ++u) w[u] = load8(pw, k + u * 32 + g * 8, wn);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int i = 0; i < MT; ++i) x[u][i] = load8(px + (int64_t)i * 16 * a.lda, k + u * 32 + g * 8, i * 16 + c < a.M);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int i = 0; i < MT; ++i) acc[i] = Mma<T>::mma(w[u], x[u][i], acc[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < MT; ++i) part[wave][i][lane] = acc[i];
+    __syncthreads();
+    for (int i = wave; i < MT; i += 4) {
+        const f32x4 s = part[0][i][lane] + part[1][i][lane] + part[2][i][lane] + part[3][i][lane];
+        const int64_t m = i * 16 + c, n = n0 + g * 4;
+        if (m < a.M && n < a.N) {
+            float f[4] = {s[0], s[1], s[2], s[3]};
+            linear_epilogue<T>(a, m, n, f);
+        }
+    }
+}
+
+// grid of the dz kernel: (columns / 256, slabs); thread: one column over the slab's rows.
+template <typename T> __global__ __launch_bounds__(256) void linear_dz_kernel(const LinearDz a) {
+    const int64_t n = blockIdx.x * (int64_t)256 + threadIdx.x;
+    const int64_t m0 = blockIdx.y * a.rows, m1 = m0 + a.rows < a.M ? m0 + a.rows : a.M;
+    const bool in = n < a.N;
+    if (n >= (a.dz ? a.ldz : a.N)) return;
+    const T *po = static_cast<const T *>(a.dout), *pp = static_cast<const T *>(a.pre);
+    T *pz = static_cast<T *>(a.dz);
+    float sum = 0.0f;
+    for (int64_t m = m0; m < m1; m += 8) {
+        float d[8], z[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const bool ok = in && m + u < m1;
+            d[u] = ok ? (float)po[(m + u) * a.ldo + n] : 0.0f;
+            z[u] = ok && a.act != ACT_NONE ? (float)pp[(m + u) * a.ldp + n] : 0.0f;
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            if (a.act != ACT_NONE) d[u] *= act_slope(z[u], a.act);
+            sum += d[u];
+            if (pz && m + u < m1) pz[(m + u) * a.ldz + n] = (T)d[u];
+        }
+    }
+    if (a.colsum && in) a.colsum[blockIdx.y * a.N + n] = sum;
+}
+template <typename T>
+__global__ __launch_bounds__(256) void linear_colsum_kernel(const float *colsum, int64_t slabs, int64_t N, T *dbias) {
+    const int64_t n = blockIdx.x * (int64_t)256 + threadIdx.x;
+    if (n >= N) return;
+    float s = 0.0f;
+    for (int64_t i = 0; i < slabs; ++i) s += colsum[i * N + n];
+    dbias[n] = (T)s;
+}
+
+// ---- host side of one storage type ----------------------------------------
+template <typename T, int LAYOUT>
+static hipError_t gemm_layout(const LinearGemm &a, int tile, bool vec, hipStream_t stream) {
+    auto blocks = [&](int bm, int bn) {
+        return dim3((unsigned)(((a.M + bm - 1) / bm) * ((a.N + bn - 1) / bn)), (unsigned)a.splits);
+    };
+    if (!vec) {
+        linear_gemm_kernel<T, LAYOUT, 4, 4, 2, 2, false><<<blocks(128, 128), 256, 0, stream>>>(a);
+    } else if (tile == 256) {
+        if constexpr (sizeof(T) == 2)
+            linear_gemm_kernel<T, LAYOUT, 8, 4, 2, 4, true><<<blocks(256, 256), 512, 0, stream>>>(a);
+    } else if (tile == 128) {
+        linear_gemm_kernel<T, LAYOUT, 4, 4, 2, 2, true><<<blocks(128, 128), 256, 0, stream>>>(a);
+    } else {
+        linear_gemm_kernel<T, LAYOUT, 2, 2, 2, 2, true><<<blocks(64, 64), 256, 0, stream>>>(a);
+    }
+    return hipGetLastError();
+}
+
+template <typename T>
+static hipError_t gemm_typed(const LinearGemm &a, int layout, int tile, bool vec, hipStream_t stream) {
+    hipError_t e = layout == LAYOUT_NT   ? gemm_layout<T, LAYOUT_NT>(a, tile, vec, stream)
+                   : layout == LAYOUT_NN ? gemm_layout<T, LAYOUT_NN>(a, tile, vec, stream)
+                                         : gemm_layout<T, LAYOUT_TN>(a, tile, vec, stream);
+    if (e != hipSuccess || !a.part) return e;
+    const int64_t n = (a.M * ((a.N + 3) / 4) + 255) / 256;
+    linear_join_kernel<T><<<(unsigned)(n < 4096 ? n : 4096), 256, 0, stream>>>(a);
+    return hipGetLastError();
+}
+
+template <typename T> static hipError_t rows_typed(const LinearGemm &a, bool vec, hipStream_t stream) {
+    const unsigned grid = (unsigned)((a.N + 15) / 16);
+#define FFTCONV_ROWS(MT)                                                                       \
+    do {                                                                                       \
+        if (vec) linear_rows_kernel<T, MT, true><<<grid, 256, 0, stream>>>(a);                 \
+        else linear_rows_kernel<T, MT, false><<<grid, 256, 0, stream>>>(a);                    \
+    } while (0)
+    if (a.M <= 16) FFTCONV_ROWS(1);
+    else if (a.M <= 32) FFTCONV_ROWS(2);
+    else FFTCONV_ROWS(4);
+#undef FFTCONV_ROWS
+    return hipGetLastError();
+}
+
+template <typename T>
+static hipError_t dz_typed(const LinearDz &a, int64_t slabs, void *dbias, hipStream_t stream) {
+    const int64_t cols = a.dz ? a.ldz : a.N;
+    linear_dz_kernel<T><<<dim3((unsigned)((cols + 255) / 256), (unsigned)slabs), 256, 0, stream>>>(a);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || !a.colsum) return e;
+    linear_colsum_kernel<T><<<(unsigned)((a.N + 255) / 256), 256, 0, stream>>>(a.colsum, slabs, a.N, static_cast<T *>(dbias));
+    return hipGetLastError();
+}
+
+#define FFTCONV_LINEAR_TYPE(NAME, T)                                                                            \
+    hipError_t launch_linear_gemm_##NAME(const LinearGemm &a, int layout, int tile, bool vec, hipStream_t s) {   \
+        return gemm_typed<T>(a, layout, tile, vec, s);                                                           \
+    }                                                                                                            \
+    hipError_t launch_linear_rows_##NAME(const LinearGemm &a, bool vec, hipStream_t s) {                         \
+        return rows_typed<T>(a, vec, s);                                                                         \
+    }                                                                                                            \
+    hipError_t launch_linear_dz_##NAME(const LinearDz &a, int64_t slabs, void *dbias, hipStream_t s) {           \
+        return dz_typed<T>(a, slabs, dbias, s);                                                                  \
+    }
+
+}  // namespace fftconv

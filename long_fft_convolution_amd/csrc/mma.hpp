@@ -1,0 +1,94 @@
+// mma.hpp -- real 16x16x32 tile products on the matrix cores for the three
+// storage types, shared by the decay-attention and linear-product kernels.
+//
+// mma(a, b, c): C (16x16, fp32) += A (16 x 32) B (32 x 16).  Lane l = 16 g + c
+// holds, of A, row c at the 8 K slots 8 g + j; of B, column c at the same
+// slots; of C, rows 4 g + i of column c.  fp16 / bf16: one
+// v_mfma_f32_16x16x32.  fp32: eight v_mfma_f32_16x16x4, the j-th taking slot
+// 8 g + j of every lane -- the contraction index may be met in any order as
+// long as A and B agree, so the fp32 operands keep the 16-bit operand layout.
+#pragma once
+#include <hip/hip_bf16.h>
+#include <hip/hip_fp16.h>
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "fftconv_internal.hpp"
+
+namespace fftconv {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+template <typename T> struct Mma;
+
+// fp16 and bf16: 4 values at column steps of a transposed LDS read
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+#define FFTCONV_LDS_CAST(type, p) \
+    ((__attribute__((address_space(3))) type *)(__attribute__((address_space(3))) void *)(p))
+
+template <> struct Mma<_Float16> {
+    typedef _Float16 v8 __attribute__((ext_vector_type(8)));
+    typedef _Float16 v4 __attribute__((ext_vector_type(4)));
+    static __device__ __forceinline__ f32x4 mma(v8 a, v8 b, f32x4 c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+    }
+    static constexpr int kSplit = 2;   // 2 x 11 bits hold an fp32 value to 2^-22,
+    static constexpr bool kNarrow = true;   // given a scale that keeps the second term out of the subnormals
+};
+template <> struct Mma<__bf16> {
+    typedef __bf16 v8 __attribute__((ext_vector_type(8)));
+    typedef __bf16 v4 __attribute__((ext_vector_type(4)));
+    static __device__ __forceinline__ f32x4 mma(v8 a, v8 b, f32x4 c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+    }
+    static constexpr int kSplit = 3;   // 3 x 8 bits hold an fp32 value to 2^-24
+    static constexpr bool kNarrow = false;
+};
+template <> struct Mma<float> {
+    typedef float v8 __attribute__((ext_vector_type(8)));
+    typedef float v4 __attribute__((ext_vector_type(4)));
+    static __device__ __forceinline__ f32x4 mma(const v8 &a, const v8 &b, f32x4 c) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[j], b[j], c, 0, 0, 0);
+        return c;
+    }
+    static constexpr int kSplit = 1;
+    static constexpr bool kNarrow = false;
+};
+
+// 8 consecutive values of one LDS row (16-byte aligned)
+template <typename T> __device__ __forceinline__ typename Mma<T>::v8 lds_row8(const T *p) {
+    return *reinterpret_cast<const typename Mma<T>::v8 *>(p);
+}
+template <> __device__ __forceinline__ Mma<float>::v8 lds_row8<float>(const float *p) {
+    const f32x4 a = *reinterpret_cast<const f32x4 *>(p), b = *reinterpret_cast<const f32x4 *>(p + 4);
+    return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
+// One column of 8 consecutive LDS rows (rows row0 .. row0 + 7 at stride ld),
+// for the column whose 4-wide group of 16 lanes starts at col4(l % 4): lane c
+// of the 16 receives column col4(c / 4) + c % 4.  16-bit types take two
+// transposing reads (ds_read_b64_tr_b16: the 16 lanes read four rows of four
+// 4-value groups and receive one column each); col is this lane's own group
+// address, col4(l % 4), and row its own row, row0 + (l % 16) / 4.  fp32 reads
+// its column value by value (mine = this lane's own column).
+template <typename T>
+__device__ __forceinline__ typename Mma<T>::v8 lds_col8(const T *tile, int ld, int row0, int group_col, int mine) {
+    if constexpr (sizeof(T) == 2) {
+        const int r = (threadIdx.x & 15) >> 2;
+        const T *p = tile + (row0 + r) * ld + group_col;
+        typedef typename Mma<T>::v4 v4;
+        const v4 a = __builtin_bit_cast(v4, __builtin_amdgcn_ds_read_tr16_b64_v4i16(FFTCONV_LDS_CAST(s16x4, p)));
+        const v4 b = __builtin_bit_cast(v4, __builtin_amdgcn_ds_read_tr16_b64_v4i16(FFTCONV_LDS_CAST(s16x4, p + 4 * ld)));
+        return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+    } else {
+        typename Mma<T>::v8 v;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = tile[(row0 + j) * ld + mine];
+        return v;
+    }
+}
+
+template <typename T> __device__ __forceinline__ float to_f(T x) { return (float)x; }
+
+}  // namespace fftconv

@@ -1,0 +1,645 @@
+// sequence_ops.cpp -- host side of the decay-attention and linear-product
+// entry points of include/fftconv.h: argument checks, the rules that choose a
+// kernel variant and split the work, workspace layout, launches.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdarg>
+#include <cstdio>
+
+#include "../../include/fftconv.h"
+#include "fftconv_internal.hpp"
+#include "sequence_ops.hpp"
+
+using namespace fftconv;
+
+namespace {
+
+fftconv_status_t fail(fftconv_status_t st, const char *fmt, ...) {
+    char buf[512];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(buf, sizeof buf, fmt, ap);
+    va_end(ap);
+    set_last_error(buf);
+    return st;
+}
+fftconv_status_t ok() {
+    set_last_error("");
+    return FFTCONV_OK;
+}
+fftconv_status_t hip_status(const char *what, hipError_t e) {
+    return e == hipSuccess ? ok() : fail(FFTCONV_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
+}
+
+bool dtype_ok(int dt) { return dt == FFTCONV_F32 || dt == FFTCONV_F16 || dt == FFTCONV_BF16; }
+int64_t elem_bytes(int dt) { return dt == FFTCONV_F32 ? 4 : 2; }
+bool aligned(const void *p, int64_t n) { return reinterpret_cast<uintptr_t>(p) % (uintptr_t)n == 0; }
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
+
+// A tensor argument: `dims` sizes and strides (elements) above a contiguous row of `row` values.
+struct View {
+    const char *name;
+    const void *p;
+    int dims;
+    int64_t size[3], stride[3], row;
+    int64_t bytes_per;
+
+    bool empty() const {
+        for (int i = 0; i < dims; ++i)
+            if (size[i] == 0) return true;
+        return row == 0;
+    }
+    // bytes from p to the end of the last row
+    int64_t span() const {
+        if (empty()) return 0;
+        int64_t last = row;
+        for (int i = 0; i < dims; ++i) last += (size[i] - 1) * stride[i];
+        return last * bytes_per;
+    }
+    bool overlaps(const View &o) const {
+        if (!p || !o.p || empty() || o.empty()) return false;
+        auto a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(o.p);
+        return a < b + (uintptr_t)o.span() && b < a + (uintptr_t)span();
+    }
+    // every element at a place of its own: each stride reaches past what the smaller ones span
+    bool distinct() const {
+        int order[3] = {0, 1, 2};
+        std::sort(order, order + dims, [&](int x, int y) { return stride[x] < stride[y]; });
+        int64_t reach = row;
+        for (int i = 0; i < dims; ++i) {
+            const int d = order[i];
+            if (size[d] <= 1) continue;
+            if (stride[d] < reach) return false;
+            reach += (size[d] - 1) * stride[d];
+        }
+        return true;
+    }
+    // rows may be met 16 bytes at a time
+    bool vec16() const {
+        const int64_t e = 16 / bytes_per;
+        if (!aligned(p, 16)) return false;
+        for (int i = 0; i < dims; ++i)
+            if (size[i] > 1 && stride[i] % e) return false;
+        return true;
+    }
+};
+
+// The checks that every tensor argument passes; outputs also hold each element once.
+fftconv_status_t check_view(const View &v, bool required, bool output) {
+    if (!v.p) {
+        if (!required || v.empty()) return FFTCONV_OK;
+        return fail(FFTCONV_ERR_INVALID_ARGUMENT, "%s must be non-null", v.name);
+    }
+    if (!aligned(v.p, v.bytes_per))
+        return fail(FFTCONV_ERR_INVALID_ARGUMENT, "%s must be aligned to its %d-byte elements", v.name, (int)v.bytes_per);
+    for (int i = 0; i < v.dims; ++i) {
+        if (v.size[i] <= 1) continue;
+        if (v.stride[i] < 0) return fail(FFTCONV_ERR_INVALID_ARGUMENT, "%s has a negative stride", v.name);
+        if (v.stride[i] > (int64_t(1) << 40) / v.size[i])
+            return fail(FFTCONV_ERR_INVALID_ARGUMENT, "%s has a stride of %lld elements", v.name, (long long)v.stride[i]);
+    }
+    if (output && !v.distinct())
+        return fail(FFTCONV_ERR_INVALID_ARGUMENT, "%s: strides let its elements share memory", v.name);
+    return FFTCONV_OK;
+}
+
+// ---- decay attention --------------------------------------------------------
+constexpr int64_t kMaxHeadDim = 256;
+constexpr int64_t kSegStep = 64;          // segments are whole chunks
+constexpr int64_t kMinSegment = 256;      // below this the second read of y, z costs more than it spreads
+constexpr int64_t kWalkSlots = 512;       // workgroups that walk at once: two on each of 256 CUs
+
+int64_t z_tiles(int64_t dz) { return ceil_div(dz, dz <= 64 ? 64 : 128); }
+
+// Tokens of a segment.  A walk is serial, so the chip fills only when (sequence, head, z tile)
+// triples number about kWalkSlots; fewer are cut into segments, at the price of reading y and z
+// twice (a pass of their own sums each segment first).
+int64_t segment_tokens(int64_t B, int64_t N, int64_t T, int64_t H, int64_t dz, bool packed) {
+    const int64_t per_token = H * z_tiles(dz);
+    if (!packed && B * per_token * 2 > kWalkSlots) return round_up(std::max<int64_t>(N, 1), kSegStep);
+    int64_t len = std::max(kMinSegment, ceil_div(T * per_token, kWalkSlots));
+    if (!packed && N > 0) len = ceil_div(N, ceil_div(N, len));    // equal segments
+    return round_up(len, kSegStep);
+}
+int64_t segment_count(int64_t B, int64_t N, int64_t T, int64_t seglen, bool packed) {
+    return packed ? T / seglen + B : B * std::max<int64_t>(1, ceil_div(N, seglen));
+}
+bool segmented(int64_t N, int64_t T, int64_t seglen, bool packed) { return (packed ? T : N) > seglen; }
+
+// Bytes of the segments' states of one walk over T tokens in B sequences.
+size_t walk_bytes(int64_t B, int64_t T, int64_t H, int64_t dx, int64_t dz) {
+    size_t most = 0;
+    for (bool packed : {false, true}) {
+        // equal sequences: T = B N; a packed call may hold any lengths
+        const int64_t N = packed ? T : ceil_div(T, std::max<int64_t>(B, 1));
+        const int64_t len = segment_tokens(B, N, T, H, dz, packed);
+        if (segmented(N, T, len, packed))
+            most = std::max(most, (size_t)segment_count(B, N, T, len, packed) * H * dx * dz * sizeof(float));
+    }
+    return align_up(most, 256);
+}
+
+hipError_t launch_walk(int dt, const DecayWalk &a, bool out_f32, hipStream_t s) {
+    return dt == FFTCONV_F32   ? launch_decay_walk_f32(a, out_f32, s)
+           : dt == FFTCONV_F16 ? launch_decay_walk_f16(a, out_f32, s)
+                               : launch_decay_walk_bf16(a, out_f32, s);
+}
+
+struct DecayShape {
+    int64_t B, N, H, Hk, Dk, Dv;
+    int dt;
+    bool packed;
+    int64_t T() const { return packed ? N : B * N; }
+};
+
+// heads: H or Hk; strides (batch, token, head) at st
+View heads_view(const char *name, const void *p, const DecayShape &s, int64_t heads, int64_t row, const int64_t *st) {
+    View v{name, p, 3, {s.packed ? 1 : s.B, s.N, heads}, {0, 0, 0}, row, elem_bytes(s.dt)};
+    if (st) {
+        for (int i = 0; i < 3; ++i) v.stride[i] = st[i];
+        if (s.packed) v.stride[0] = 0;
+    } else {
+        v.stride[0] = s.N * heads * row;
+        v.stride[1] = heads * row;
+        v.stride[2] = row;
+    }
+    return v;
+}
+
+fftconv_status_t check_shape(const DecayShape &s, float scale) {
+    if (!dtype_ok(s.dt)) return fail(FFTCONV_ERR_UNSUPPORTED, "dtype %d is not supported", s.dt);
+    if (s.B < 0 || s.N < 0 || s.H < 0 || s.Hk < 0)
+        return fail(FFTCONV_ERR_INVALID_ARGUMENT, "B=%lld, N=%lld, H=%lld and Hk=%lld must be >= 0", (long long)s.B,
+                    (long long)s.N, (long long)s.H, (long long)s.Hk);
+    if (s.Dk < 1 || s.Dk > kMaxHeadDim || s.Dv < 1 || s.Dv > kMaxHeadDim)
+        return fail(FFTCONV_ERR_UNSUPPORTED, "head widths Dk=%lld and Dv=%lld must be in [1, %lld]", (long long)s.Dk,
+                    (long long)s.Dv, (long long)kMaxHeadDim);
+    if (s.H > 0 && (s.Hk < 1 || s.H % s.Hk))
+        return fail(FFTCONV_ERR_INVALID_ARGUMENT, "H=%lld must be a multiple of Hk=%lld", (long long)s.H, (long long)s.Hk);
+    if (s.H > 65535) return fail(FFTCONV_ERR_UNSUPPORTED, "H=%lld is above 65535", (long long)s.H);
+    if (s.B >= (int64_t(1) << 31) || s.N >= (int64_t(1) << 31) || (s.B > 0 && s.N > (int64_t(1) << 40) / s.B) ||
+        (s.H > 0 && s.B > ((int64_t(1) << 31) - 1) / s.H))
+        return fail(FFTCONV_ERR_UNSUPPORTED, "B=%lld, N=%lld, H=%lld: too many sequences or tokens", (long long)s.B,
+                    (long long)s.N, (long long)s.H);
+    if (!std::isfinite(scale)) return fail(FFTCONV_ERR_INVALID_ARGUMENT, "scale must be finite");
+    return FFTCONV_OK;
+}
+
+fftconv_status_t check_workspace(const void *ws, size_t have, size_t need) {
+    if (need == 0) return FFTCONV_OK;
+    if (!ws || have < need) return fail(FFTCONV_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", ws ? have : (size_t)0, need);
+    if (!aligned(ws, 16)) return fail(FFTCONV_ERR_INVALID_ARGUMENT, "workspace must be 16-byte aligned");
+    return FFTCONV_OK;
+}
+
+View state_view(const char *name, const void *p, int64_t count, const DecayShape &s) {
+    return View{name, p, 1, {count, 1, 1}, {s.H * s.Dk * s.Dv, 0, 0}, s.H * s.Dk * s.Dv, 4};
+}
+View raw_view(const char *name, const void *p, int64_t bytes) { return View{name, p, 1, {1, 1, 1}, {0, 0, 0}, bytes, 1}; }
+
+fftconv_status_t check_apart(const View *outs, int nout, const View *ins, int nin) {
+    for (int i = 0; i < nout; ++i) {
+        for (int j = 0; j < nin; ++j)
+            if (outs[i].overlaps(ins[j]))
+                return fail(FFTCONV_ERR_INVALID_ARGUMENT, "%s overlaps %s", outs[i].name, ins[j].name);
+        for (int j = 0; j < i; ++j)
+            if (outs[i].overlaps(outs[j]))
+                return fail(FFTCONV_ERR_INVALID_ARGUMENT, "%s overlaps %s", outs[i].name, outs[j].name);
+    }
+    return FFTCONV_OK;
+}
+
+void set_x(DecayWalk &w, const View &v, int64_t H) {
+    w.x = v.p, w.xb = v.stride[0], w.xt = v.stride[1], w.xh = v.stride[2], w.gx = (int)(H / v.size[2]);
+    w.DX = (int)v.row;
+    w.vec_x = v.vec16() && v.row % (16 / v.bytes_per) == 0;
+}
+void set_y(DecayWalk &w, const View &v, int64_t H) {
+    w.y = v.p, w.yb = v.stride[0], w.yt = v.stride[1], w.yh = v.stride[2], w.gy = (int)(H / v.size[2]);
+    w.vec_y = v.vec16() && v.row % (16 / v.bytes_per) == 0;
+}
+void set_z(DecayWalk &w, const View &v, int64_t H) {
+    w.z = v.p, w.zb = v.stride[0], w.zt = v.stride[1], w.zh = v.stride[2], w.gz = (int)(H / v.size[2]);
+    w.DZ = (int)v.row;
+    w.vec_z = v.vec16() && v.row % (16 / v.bytes_per) == 0;
+}
+void set_out(DecayWalk &w, const View &v, int64_t H) {
+    w.out = const_cast<void *>(v.p), w.ob = v.stride[0], w.ot = v.stride[1], w.oh = v.stride[2];
+    w.go = (int)(H / v.size[2]);
+    w.vec_o = v.vec16();
+}
+void set_segments(DecayWalk &w, const DecayShape &s, float *seg) {
+    w.seglen = segment_tokens(s.B, s.N, s.T(), s.H, w.DZ, s.packed);
+    w.nblk = segment_count(s.B, s.N, s.T(), w.seglen, s.packed);
+    w.seg = segmented(s.N, s.T(), w.seglen, s.packed) ? seg : nullptr;
+}
+
+}  // namespace
+
+size_t fftconv_decay_fwd_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t Dk, int64_t Dv,
+                                         fftconv_dtype_t dtype) {
+    if (!dtype_ok(dtype) || B < 1 || T < 1 || H < 1 || Dk < 1 || Dv < 1 || Dk > kMaxHeadDim || Dv > kMaxHeadDim) return 0;
+    return walk_bytes(B, T, H, Dk, Dv);
+}
+
+fftconv_status_t fftconv_decay_fwd(const void *q, const void *k, const void *v, const float *log_decay, void *out,
+                                   const int64_t *strides, const float *state_in, float *state_out,
+                                   const int32_t *state_slots, int64_t n_slots, const int32_t *cu_seqlens, int64_t B,
+                                   int64_t N, int64_t H, int64_t Hk, int64_t Dk, int64_t Dv, float scale,
+                                   fftconv_dtype_t dtype, void *workspace, size_t workspace_bytes, hipStream_t stream) {
+    const DecayShape s{B, N, H, Hk, Dk, Dv, (int)dtype, cu_seqlens != nullptr};
+    fftconv_status_t st = check_shape(s, scale);
+    if (st != FFTCONV_OK) return st;
+    if (n_slots < 0) return fail(FFTCONV_ERR_INVALID_ARGUMENT, "n_slots=%lld must be >= 0", (long long)n_slots);
+    if (B == 0 || H == 0) return ok();
+    const View vq = heads_view("q", q, s, H, Dk, strides), vk = heads_view("k", k, s, Hk, Dk, strides ? strides + 3 : nullptr),
+               vv = heads_view("v", v, s, Hk, Dv, strides ? strides + 6 : nullptr),
+               vo = heads_view("out", out, s, H, Dv, strides ? strides + 9 : nullptr);
+    for (const View *x : {&vq, &vk, &vv})
+        if ((st = check_view(*x, true, false)) != FFTCONV_OK) return st;
+    if ((st = check_view(vo, true, true)) != FFTCONV_OK) return st;
+    if (!log_decay) return fail(FFTCONV_ERR_INVALID_ARGUMENT, "log_decay must be non-null");
+    const int64_t states = state_slots ? n_slots : B;
+    const View si = state_view("state_in", state_in, states, s), so = state_view("state_out", state_out, states, s);
+    for (const View *x : {&si, &so})
+        if ((st = check_view(*x, false, false)) != FFTCONV_OK) return st;
+    for (const void *p : {(const void *)log_decay, (const void *)state_slots, (const void *)cu_seqlens})
+        if (!aligned(p, 4)) return fail(FFTCONV_ERR_INVALID_ARGUMENT, "log_decay, state_slots and cu_seqlens must be 4-byte aligned");
+    const size_t need = fftconv_decay_fwd_workspace_bytes(B, s.T(), H, Dk, Dv, dtype);
+    if ((st = check_workspace(workspace, workspace_bytes, need)) != FFTCONV_OK) return st;
+    const View ws = raw_view("workspace", need ? workspace : nullptr, (int64_t)need);
+    const View ld = raw_view("log_decay", log_decay, H * 4), sl = raw_view("state_slots", state_slots, B * 4),
+               cu = raw_view("cu_seqlens", cu_seqlens, (B + 1) * 4);
+    // state_out may be state_in itself (the pool updated in place), nothing else
+    if (state_out && state_in && state_out != state_in && si.overlaps(so))
+        return fail(FFTCONV_ERR_INVALID_ARGUMENT, "state_out overlaps state_in without being it");
+    const View outs[] = {vo, so, ws}, ins[] = {vq, vk, vv, ld, sl, cu};
+    if ((st = check_apart(outs, 3, ins, 6)) != FFTCONV_OK) return st;
+    const View apart[] = {vo, ws};
+    if ((st = check_apart(apart, 2, &si, 1)) != FFTCONV_OK) return st;
+    if (s.T() == 0 && !state_out) return ok();
+
+    DecayWalk w{};
+    set_x(w, vq, H);
+    set_y(w, vk, H);
+    set_z(w, vv, H);
+    set_out(w, vo, H);
+    w.log_decay = log_decay;
+    w.state0 = state_in, w.state1 = state_out;
+    w.s0x = w.s1x = Dv, w.s0z = w.s1z = 1;
+    w.slots = state_slots, w.n_slots = n_slots;
+    w.cu = cu_seqlens;
+    w.B = B, w.N = N, w.H = (int)H;
+    w.p_scale = scale, w.u_scale = 1.0f, w.i_scale = scale;
+    w.off = 1;
+    set_segments(w, s, static_cast<float *>(workspace));
+    return hip_status("decay attention", launch_walk(dtype, w, false, stream));
+}
+
+fftconv_status_t fftconv_decay_step(const void *q, const void *k, const void *v, const float *log_decay, float *state,
+                                    void *out, const int64_t *strides, const int32_t *state_slots, int64_t n_slots,
+                                    int64_t B, int64_t H, int64_t Hk, int64_t Dk, int64_t Dv, float scale,
+                                    fftconv_dtype_t dtype, hipStream_t stream) {
+    const DecayShape s{B, 1, H, Hk, Dk, Dv, (int)dtype, false};
+    fftconv_status_t st = check_shape(s, scale);
+    if (st != FFTCONV_OK) return st;
+    if (n_slots < 0) return fail(FFTCONV_ERR_INVALID_ARGUMENT, "n_slots=%lld must be >= 0", (long long)n_slots);
+    if (B == 0 || H == 0) return ok();
+    int64_t full[12];
+    if (strides)
+        for (int i = 0; i < 4; ++i) full[3 * i] = strides[2 * i], full[3 * i + 1] = 0, full[3 * i + 2] = strides[2 * i + 1];
+    const int64_t *f = strides ? full : nullptr;
+    const View vq = heads_view("q", q, s, H, Dk, f), vk = heads_view("k", k, s, Hk, Dk, f ? f + 3 : nullptr),
+               vv = heads_view("v", v, s, Hk, Dv, f ? f + 6 : nullptr), vo = heads_view("out", out, s, H, Dv, f ? f + 9 : nullptr);
+    for (const View *x : {&vq, &vk, &vv})
+        if ((st = check_view(*x, true, false)) != FFTCONV_OK) return st;
+    if ((st = check_view(vo, true, true)) != FFTCONV_OK) return st;
+    if (!log_decay || !state) return fail(FFTCONV_ERR_INVALID_ARGUMENT, "log_decay and state must be non-null");
+    const View vs = state_view("state", state, state_slots ? n_slots : B, s);
+    if ((st = check_view(vs, false, false)) != FFTCONV_OK) return st;
+    for (const void *p : {(const void *)log_decay, (const void *)state_slots})
+        if (!aligned(p, 4)) return fail(FFTCONV_ERR_INVALID_ARGUMENT, "log_decay and state_slots must be 4-byte aligned");
+    const View outs[] = {vo, vs}, ins[] = {vq, vk, vv, raw_view("log_decay", log_decay, H * 4),
+                                           raw_view("state_slots", state_slots, B * 4)};
+    if ((st = check_apart(outs, 2, ins, 5)) != FFTCONV_OK) return st;
+
+    DecayStep a{};
+    a.q = q, a.k = k, a.v = v, a.out = out;
+    a.qb = vq.stride[0], a.qh = vq.stride[2], a.kb = vk.stride[0], a.kh = vk.stride[2];
+    a.vb = vv.stride[0], a.vh = vv.stride[2], a.ob = vo.stride[0], a.oh = vo.stride[2];
+    a.log_decay = log_decay, a.state = state, a.slots = state_slots, a.n_slots = n_slots;
+    a.B = B, a.H = (int)H, a.group = (int)(H / Hk), a.Dk = (int)Dk, a.Dv = (int)Dv, a.scale = scale;
+    const bool vec = Dv % 4 == 0 && aligned(state, 16);
+    const hipError_t e = dtype == FFTCONV_F32   ? launch_decay_step_f32(a, vec, stream)
+                         : dtype == FFTCONV_F16 ? launch_decay_step_f16(a, vec, stream)
+                                                : launch_decay_step_bf16(a, vec, stream);
+    return hip_status("decay step", e);
+}
+
+// workspace of the backward call: the walks' segment states, then fp32 gradients of the heads
+// that share a key/value head
+size_t fftconv_decay_bwd_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t Hk, int64_t Dk, int64_t Dv,
+                                         fftconv_dtype_t dtype) {
+    if (!dtype_ok(dtype) || B < 1 || T < 1 || H < 1 || Hk < 1 || Dk < 1 || Dv < 1 || Dk > kMaxHeadDim || Dv > kMaxHeadDim)
+        return 0;
+    const size_t walks = std::max(walk_bytes(B, T, H, Dv, Dk), walk_bytes(B, T, H, Dk, Dv));
+    return walks + (H == Hk ? 0 : align_up((size_t)T * H * std::max(Dk, Dv) * sizeof(float), 256));
+}
+
+fftconv_status_t fftconv_decay_bwd(const void *dout, const void *q, const void *k, const void *v,
+                                   const float *log_decay, void *dq, void *dk, void *dv, const int64_t *strides,
+                                   const float *state_in, const float *dstate_out, float *dstate_in,
+                                   const int32_t *cu_seqlens, int64_t B, int64_t N, int64_t H, int64_t Hk, int64_t Dk,
+                                   int64_t Dv, float scale, fftconv_dtype_t dtype, void *workspace,
+                                   size_t workspace_bytes, hipStream_t stream) {
+    const DecayShape s{B, N, H, Hk, Dk, Dv, (int)dtype, cu_seqlens != nullptr};
+    fftconv_status_t st = check_shape(s, scale);
+    if (st != FFTCONV_OK) return st;
+    if (B == 0 || H == 0) return ok();
+    auto at = [&](int i) { return strides ? strides + 3 * i : nullptr; };
+    const View vd = heads_view("dout", dout, s, H, Dv, at(0)), vq = heads_view("q", q, s, H, Dk, at(1)),
+               vk = heads_view("k", k, s, Hk, Dk, at(2)), vv = heads_view("v", v, s, Hk, Dv, at(3)),
+               gq = heads_view("dq", dq, s, H, Dk, at(4)), gk = heads_view("dk", dk, s, Hk, Dk, at(5)),
+               gv = heads_view("dv", dv, s, Hk, Dv, at(6));
+    for (const View *x : {&vd, &vq, &vk, &vv})
+        if ((st = check_view(*x, true, false)) != FFTCONV_OK) return st;
+    for (const View *x : {&gq, &gk, &gv})
+        if ((st = check_view(*x, false, true)) != FFTCONV_OK) return st;
+    if (!log_decay) return fail(FFTCONV_ERR_INVALID_ARGUMENT, "log_decay must be non-null");
+    const View si = state_view("state_in", state_in, B, s), dso = state_view("dstate_out", dstate_out, B, s),
+               dsi = state_view("dstate_in", dstate_in, B, s);
+    for (const View *x : {&si, &dso, &dsi})
+        if ((st = check_view(*x, false, false)) != FFTCONV_OK) return st;
+    for (const void *p : {(const void *)log_decay, (const void *)cu_seqlens})
+        if (!aligned(p, 4)) return fail(FFTCONV_ERR_INVALID_ARGUMENT, "log_decay and cu_seqlens must be 4-byte aligned");
+    const size_t need = fftconv_decay_bwd_workspace_bytes(B, s.T(), H, Hk, Dk, Dv, dtype);
+    if ((st = check_workspace(workspace, workspace_bytes, need)) != FFTCONV_OK) return st;
+    const View ws = raw_view("workspace", need ? workspace : nullptr, (int64_t)need);
+    const View outs[] = {gq, gk, gv, dsi, ws},
+               ins[] = {vd, vq, vk, vv, si, dso, raw_view("log_decay", log_decay, H * 4),
+                        raw_view("cu_seqlens", cu_seqlens, (B + 1) * 4)};
+    if ((st = check_apart(outs, 5, ins, 8)) != FFTCONV_OK) return st;
+
+    const size_t walks = std::max(walk_bytes(B, std::max<int64_t>(s.T(), 1), H, Dv, Dk),
+                                  walk_bytes(B, std::max<int64_t>(s.T(), 1), H, Dk, Dv));
+    float *seg = static_cast<float *>(workspace);
+    float *part = reinterpret_cast<float *>(static_cast<char *>(workspace) + walks);
+    DecayWalk w{};
+    w.log_decay = log_decay;
+    w.cu = cu_seqlens;
+    w.B = B, w.N = N, w.H = (int)H;
+    // dq: x, y, z = dout, v, k forwards, state S^T
+    if (dq && s.T() > 0) {
+        DecayWalk a = w;
+        set_x(a, vd, H);
+        set_y(a, vv, H);
+        set_z(a, vk, H);
+        set_out(a, gq, H);
+        a.state0 = state_in, a.s0x = 1, a.s0z = Dv;
+        a.p_scale = scale, a.u_scale = 1.0f, a.i_scale = scale;
+        a.off = 1;
+        set_segments(a, s, seg);
+        const hipError_t e = launch_walk(dtype, a, false, stream);
+        if (e != hipSuccess) return hip_status("dq", e);
+    }
+    // dk: x, y, z = v, dout, q and dv: x, y, z = k, q, dout, from each sequence's end
+    for (int which = 0; which < 2; ++which) {
+        const View &g = which ? gv : gk;
+        const bool want_state = which == 1 && dstate_in;
+        if (!(g.p && s.T() > 0) && !want_state) continue;
+        DecayWalk a = w;
+        set_x(a, which ? vk : vv, H);
+        set_y(a, which ? vq : vd, H);
+        set_z(a, which ? vd : vq, H);
+        View o = g;
+        if (H != Hk || !g.p) o = heads_view("", g.p ? part : nullptr, s, H, g.row, nullptr), o.bytes_per = 4;
+        set_out(a, o, H);
+        a.state0 = dstate_out, a.s0x = which ? Dv : 1, a.s0z = which ? 1 : Dv;
+        if (want_state) a.state1 = dstate_in, a.s1x = Dv, a.s1z = 1;
+        a.p_scale = scale, a.u_scale = scale, a.i_scale = 1.0f;
+        a.off = 0, a.reverse = 1;
+        set_segments(a, s, seg);
+        hipError_t e = launch_walk(dtype, a, H != Hk, stream);
+        if (e == hipSuccess && H != Hk && g.p && s.T() > 0) {
+            auto sum = dtype == FFTCONV_F32   ? launch_decay_group_sum_f32
+                       : dtype == FFTCONV_F16 ? launch_decay_group_sum_f16
+                                              : launch_decay_group_sum_bf16;
+            e = sum(part, const_cast<void *>(g.p), s.packed ? 1 : B, N, (int)Hk, (int)(H / Hk), (int)g.row, g.stride[0],
+                    g.stride[1], g.stride[2], stream);
+        }
+        if (e != hipSuccess) return hip_status(which ? "dv" : "dk", e);
+    }
+    return ok();
+}
+
+// ---- linear product -----------------------------------------------------------
+namespace {
+
+constexpr int64_t kRowsMost = 64;   // rows that the few-rows kernel takes
+
+struct GemmPlan {
+    int tile;
+    int splits;
+    int64_t kper;
+};
+
+// Tile and split of K for an M x N x K product.  A tile must leave enough workgroups for 256 CUs;
+// where even small tiles do not, K is split and the partial sums joined by a second kernel.
+GemmPlan plan_gemm(int64_t M, int64_t N, int64_t K, int dt, bool vec) {
+    const int64_t bk = 128 / elem_bytes(dt);
+    auto tiles = [&](int64_t t) { return ceil_div(M, t) * ceil_div(N, t); };
+    GemmPlan p{128, 1, round_up(std::max<int64_t>(K, 1), bk)};
+    if (vec && dt != FFTCONV_F32 && tiles(256) >= 200) p.tile = 256;
+    else if (vec && tiles(128) < 256) p.tile = 64;
+    const int64_t n = tiles(p.tile);
+    const int64_t steps = ceil_div(K, bk);
+    if (n < 256 && steps >= 16) {
+        const int64_t want = std::min(ceil_div(512, n), steps / 8);
+        if (want > 1) {
+            p.kper = ceil_div(steps, want) * bk;
+            p.splits = (int)ceil_div(K, p.kper);
+        }
+    }
+    return p;
+}
+size_t plan_bytes(const GemmPlan &p, int64_t M, int64_t N) {
+    return p.splits > 1 ? align_up((size_t)p.splits * M * N * sizeof(float), 256) : 0;
+}
+// the workspace covers a call with or without 16-byte access
+size_t gemm_bytes(int64_t M, int64_t N, int64_t K, int dt) {
+    return std::max(plan_bytes(plan_gemm(M, N, K, dt, true), M, N), plan_bytes(plan_gemm(M, N, K, dt, false), M, N));
+}
+
+hipError_t run_gemm(int dt, LinearGemm &g, int layout, bool vec, float *part, hipStream_t s) {
+    const GemmPlan p = plan_gemm(g.M, g.N, g.K, dt, vec);
+    g.splits = p.splits, g.kper = p.kper, g.part = p.splits > 1 ? part : nullptr;
+    return dt == FFTCONV_F32   ? launch_linear_gemm_f32(g, layout, p.tile, vec, s)
+           : dt == FFTCONV_F16 ? launch_linear_gemm_f16(g, layout, p.tile, vec, s)
+                               : launch_linear_gemm_bf16(g, layout, p.tile, vec, s);
+}
+
+fftconv_status_t check_linear(int64_t M, int64_t N, int64_t K, int act, int dt) {
+    if (!dtype_ok(dt)) return fail(FFTCONV_ERR_UNSUPPORTED, "dtype %d is not supported", dt);
+    if (act < 0 || act > 4) return fail(FFTCONV_ERR_UNSUPPORTED, "activation %d is not supported", act);
+    for (int64_t n : {M, N, K})
+        if (n < 0 || n >= (int64_t(1) << 31))
+            return fail(FFTCONV_ERR_INVALID_ARGUMENT, "M=%lld, N=%lld, K=%lld must be in [0, 2^31)", (long long)M,
+                        (long long)N, (long long)K);
+    return FFTCONV_OK;
+}
+View matrix(const char *name, const void *p, int64_t rows, int64_t cols, int64_t ld, int dt) {
+    return View{name, p, 1, {rows, 1, 1}, {ld, 0, 0}, cols, elem_bytes(dt)};
+}
+// four neighbouring values at a time
+bool quad(const View &v) {
+    return aligned(v.p, 4 * v.bytes_per) && (v.size[0] <= 1 || v.stride[0] % 4 == 0);
+}
+// whole 16-byte pieces along rows, and byte offsets of a tile of 256 rows within 31 bits
+bool pieces(const View &v) {
+    return v.vec16() && v.row % (16 / v.bytes_per) == 0 && v.stride[0] * v.bytes_per < (int64_t(1) << 22);
+}
+
+}  // namespace
+
+size_t fftconv_linear_fwd_workspace_bytes(int64_t M, int64_t N, int64_t K, fftconv_dtype_t dtype) {
+    if (!dtype_ok(dtype) || M < 1 || N < 1 || K < 1 || M <= kRowsMost) return 0;
+    return gemm_bytes(M, N, K, dtype);
+}
+
+fftconv_status_t fftconv_linear_fwd(const void *x, const void *W, const void *bias, const void *residual, void *out,
+                                    void *pre, const int64_t *strides, int64_t M, int64_t N, int64_t K,
+                                    fftconv_activation_t activation, fftconv_dtype_t dtype, void *workspace,
+                                    size_t workspace_bytes, hipStream_t stream) {
+    fftconv_status_t st = check_linear(M, N, K, activation, dtype);
+    if (st != FFTCONV_OK) return st;
+    if (M == 0 || N == 0) return ok();
+    auto ld = [&](int i, int64_t dense) { return strides ? strides[i] : dense; };
+    const View vx = matrix("x", x, M, K, ld(0, K), dtype), vw = matrix("W", W, N, K, ld(1, K), dtype),
+               vb = matrix("bias", bias, 1, N, N, dtype), vr = matrix("residual", residual, M, N, ld(2, N), dtype),
+               vo = matrix("out", out, M, N, ld(3, N), dtype), vp = matrix("pre", pre, M, N, ld(4, N), dtype);
+    for (const View *v : {&vx, &vw})
+        if ((st = check_view(*v, true, false)) != FFTCONV_OK) return st;
+    for (const View *v : {&vb, &vr})
+        if ((st = check_view(*v, false, false)) != FFTCONV_OK) return st;
+    if ((st = check_view(vo, true, true)) != FFTCONV_OK) return st;
+    if ((st = check_view(vp, false, true)) != FFTCONV_OK) return st;
+    const size_t need = fftconv_linear_fwd_workspace_bytes(M, N, K, dtype);
+    if ((st = check_workspace(workspace, workspace_bytes, need)) != FFTCONV_OK) return st;
+    const View ws = raw_view("workspace", need ? workspace : nullptr, (int64_t)need);
+    const View outs[] = {vo, vp, ws}, ins[] = {vx, vw, vb};
+    if ((st = check_apart(outs, 3, ins, 3)) != FFTCONV_OK) return st;
+    // out may be the residual itself: each value is read by the lane that then writes it
+    const bool in_place = residual && residual == out && vr.stride[0] == vo.stride[0];
+    const View touched[] = {vp, ws};
+    if ((st = check_apart(touched, 2, &vr, 1)) != FFTCONV_OK) return st;
+    if (!in_place && vo.overlaps(vr))
+        return fail(FFTCONV_ERR_INVALID_ARGUMENT, "out overlaps residual without being it");
+
+    LinearGemm g{};
+    g.A = x, g.lda = vx.stride[0], g.B = W, g.ldb = vw.stride[0];
+    g.M = M, g.N = N, g.K = K;
+    g.C = out, g.ldc = vo.stride[0], g.vec_c = quad(vo);
+    g.bias = bias, g.vec_b = quad(vb);
+    g.res = residual, g.ldr = vr.stride[0], g.vec_r = quad(vr);
+    g.pre = pre, g.ldp = vp.stride[0], g.vec_p = quad(vp);
+    g.act = activation;
+    const bool vec = pieces(vx) && pieces(vw);
+    if (M <= kRowsMost) {
+        const hipError_t e = dtype == FFTCONV_F32   ? launch_linear_rows_f32(g, vec, stream)
+                             : dtype == FFTCONV_F16 ? launch_linear_rows_f16(g, vec, stream)
+                                                    : launch_linear_rows_bf16(g, vec, stream);
+        return hip_status("linear product", e);
+    }
+    return hip_status("linear product", run_gemm(dtype, g, LAYOUT_NT, vec, static_cast<float *>(workspace), stream));
+}
+
+// workspace of the backward call: dz (rows of whole 16-byte pieces), column sums of slabs of
+// rows, then the partial sums of a split product
+namespace {
+struct LinearBwdLayout {
+    int64_t ldz, rows, slabs;
+    size_t dz, colsum, part, total;
+};
+LinearBwdLayout linear_bwd_layout(int64_t M, int64_t N, int64_t K, int dt) {
+    LinearBwdLayout l{};
+    l.ldz = round_up(N, 16 / elem_bytes(dt));
+    // enough slabs to fill the chip, few enough that their sums are cheap to join
+    l.slabs = std::max<int64_t>(1, std::min<int64_t>(ceil_div(M, 32), ceil_div(2048, ceil_div(N, 256) + 1)));
+    l.rows = std::max<int64_t>(1, ceil_div(M, l.slabs));
+    l.slabs = std::max<int64_t>(1, ceil_div(M, l.rows));
+    l.colsum = align_up((size_t)M * l.ldz * elem_bytes(dt), 256);
+    l.part = l.colsum + align_up((size_t)l.slabs * N * sizeof(float), 256);
+    l.total = l.part + std::max(gemm_bytes(M, K, N, dt), gemm_bytes(N, K, M, dt));
+    return l;
+}
+}  // namespace
+
+size_t fftconv_linear_bwd_workspace_bytes(int64_t M, int64_t N, int64_t K, fftconv_dtype_t dtype) {
+    if (!dtype_ok(dtype) || M < 0 || N < 0 || K < 0) return 0;
+    return linear_bwd_layout(M, N, K, dtype).total;
+}
+
+fftconv_status_t fftconv_linear_bwd(const void *dout, const void *x, const void *W, const void *pre, void *dx, void *dW,
+                                    void *dbias, const int64_t *strides, int64_t M, int64_t N, int64_t K,
+                                    fftconv_activation_t activation, fftconv_dtype_t dtype, void *workspace,
+                                    size_t workspace_bytes, hipStream_t stream) {
+    fftconv_status_t st = check_linear(M, N, K, activation, dtype);
+    if (st != FFTCONV_OK) return st;
+    auto ld = [&](int i, int64_t dense) { return strides ? strides[i] : dense; };
+    const View vd = matrix("dout", dout, M, N, ld(0, N), dtype), vx = matrix("x", x, M, K, ld(1, K), dtype),
+               vw = matrix("W", W, N, K, ld(2, K), dtype), vp = matrix("pre", pre, M, N, ld(3, N), dtype),
+               gx = matrix("dx", dx, M, K, ld(4, K), dtype), gw = matrix("dW", dW, N, K, ld(5, K), dtype),
+               gb = matrix("dbias", dbias, 1, N, N, dtype);
+    const bool need_pre = activation != FFTCONV_ACT_NONE;
+    if ((st = check_view(vd, true, false)) != FFTCONV_OK) return st;
+    if ((st = check_view(vx, dW != nullptr, false)) != FFTCONV_OK) return st;
+    if ((st = check_view(vw, dx != nullptr, false)) != FFTCONV_OK) return st;
+    if ((st = check_view(vp, need_pre, false)) != FFTCONV_OK) return st;
+    for (const View *v : {&gx, &gw, &gb})
+        if ((st = check_view(*v, false, true)) != FFTCONV_OK) return st;
+    const LinearBwdLayout l = linear_bwd_layout(M, N, K, dtype);
+    if ((st = check_workspace(workspace, workspace_bytes, l.total)) != FFTCONV_OK) return st;
+    const View ws = raw_view("workspace", workspace, (int64_t)l.total);
+    const View outs[] = {gx, gw, gb, ws}, ins[] = {vd, vx, vw, vp};
+    if ((st = check_apart(outs, 4, ins, 4)) != FFTCONV_OK) return st;
+
+    char *base = static_cast<char *>(workspace);
+    // without an activation dout itself is dz, unless its rows are not whole 16-byte pieces
+    const bool own_dz = (dx || dW) && (need_pre || !pieces(vd));
+    LinearDz z{};
+    z.dout = dout, z.pre = pre, z.ldo = vd.stride[0], z.ldp = vp.stride[0], z.M = M, z.N = N, z.act = activation;
+    z.dz = own_dz ? base : nullptr, z.ldz = l.ldz;
+    z.colsum = dbias ? reinterpret_cast<float *>(base + l.colsum) : nullptr;
+    z.rows = l.rows;
+    hipError_t e = hipSuccess;
+    if ((own_dz && M > 0 && N > 0) || (dbias && N > 0)) {
+        e = dtype == FFTCONV_F32   ? launch_linear_dz_f32(z, l.slabs, dbias, stream)
+            : dtype == FFTCONV_F16 ? launch_linear_dz_f16(z, l.slabs, dbias, stream)
+                                   : launch_linear_dz_bf16(z, l.slabs, dbias, stream);
+        if (e != hipSuccess) return hip_status("dz", e);
+    }
+    const void *dz = own_dz ? base : dout;
+    const int64_t ldz = own_dz ? l.ldz : vd.stride[0];
+    const bool small_ldz = ldz * elem_bytes(dtype) < (int64_t(1) << 22);
+    float *part = reinterpret_cast<float *>(base + l.part);
+    if (dx && M > 0 && K > 0) {
+        LinearGemm g{};
+        g.A = dz, g.lda = ldz, g.B = W, g.ldb = vw.stride[0];
+        g.M = M, g.N = K, g.K = N;
+        g.C = dx, g.ldc = gx.stride[0], g.vec_c = quad(gx);
+        e = run_gemm(dtype, g, LAYOUT_NN, small_ldz && pieces(vw), part, stream);
+        if (e != hipSuccess) return hip_status("dx", e);
+    }
+    if (dW && N > 0 && K > 0) {
+        LinearGemm g{};
+        g.A = dz, g.lda = ldz, g.B = x, g.ldb = vx.stride[0];
+        g.M = N, g.N = K, g.K = M;
+        g.C = dW, g.ldc = gw.stride[0], g.vec_c = quad(gw);
+        e = run_gemm(dtype, g, LAYOUT_TN, small_ldz && pieces(vx), part, stream);
+        if (e != hipSuccess) return hip_status("dW", e);
+    }
+    return ok();
+}

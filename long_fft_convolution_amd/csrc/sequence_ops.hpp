@@ -1,0 +1,101 @@
+// sequence_ops.hpp -- what the host side of the decay-attention and
+// linear-product operators (sequence_ops.cpp) passes to their kernels
+// (decay_kernels.hpp, linear_kernels.hpp), and the launchers per storage type.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace fftconv {
+
+// One walk over sequences: the prompt form, or one gradient (decay_kernels.hpp).
+struct DecayWalk {
+    const void *x, *y, *z;
+    void *out;
+    int64_t xb, xt, xh, yb, yt, yh, zb, zt, zh, ob, ot, oh;   // strides (batch, token, head), elements
+    int gx, gy, gz, go;              // heads that share one x / y / z / out head
+    const float *log_decay;          // (H)
+    const float *state0;             // initial state or null; (slots or B, H) matrices of DX * DZ
+    float *state1;                   // final state or null
+    int64_t s0x, s0z, s1x, s1z;      // element strides of a state along DX and DZ
+    const int32_t *slots;            // state slot of each sequence or null
+    int64_t n_slots;
+    const int32_t *cu;               // packed sequences' bounds (B + 1) or null
+    int64_t B, N;                    // N: tokens of each sequence, or of all when packed
+    int H, DX, DZ;
+    int64_t seglen;                  // tokens per segment, a multiple of the chunk
+    int64_t nblk;                    // segments launched (an upper bound when packed)
+    float *seg;                      // state before each segment (nblk, H, DX, DZ), null when one segment each
+    float p_scale, u_scale, i_scale;
+    int off, reverse;
+    int vec_x, vec_y, vec_z, vec_o;  // 16-byte access allowed
+};
+
+// One single-token step (decay_kernels.hpp).
+struct DecayStep {
+    const void *q, *k, *v;
+    void *out;
+    int64_t qb, qh, kb, kh, vb, vh, ob, oh;
+    const float *log_decay;
+    float *state;
+    const int32_t *slots;
+    int64_t n_slots, B;
+    int H, group, Dk, Dv;
+    float scale;
+};
+
+enum LinearAct : int { ACT_NONE = 0, ACT_RELU = 1, ACT_GELU = 2, ACT_GELU_TANH = 3, ACT_SILU = 4 };
+enum LinearLayout : int { LAYOUT_NT = 0, LAYOUT_NN = 1, LAYOUT_TN = 2 };
+
+// One product C[m][n] = sum_k A(m, k) B(n, k) with its epilogue (linear_kernels.hpp).
+struct LinearGemm {
+    const void *A, *B;
+    int64_t lda, ldb;
+    int64_t M, N, K;
+    void *C;
+    int64_t ldc;
+    const void *bias, *res;   // null: none
+    int64_t ldr;
+    void *pre;                // null: not kept
+    int64_t ldp;
+    int act;
+    int vec_c, vec_r, vec_p, vec_b;   // 4-value access allowed
+    int64_t kper;             // K of one split, a multiple of the K step
+    float *part;              // splits x M x N partial sums, null when not split
+    int splits;
+};
+
+// dz = dout * act'(pre) into rows of ldz (zeros behind N), and column sums of slabs of rows.
+struct LinearDz {
+    const void *dout, *pre;
+    int64_t ldo, ldp, M, N;
+    int act;
+    void *dz;          // null: not written (act none, dout itself is used)
+    int64_t ldz;
+    float *colsum;     // slabs x N, null: no bias gradient
+    int64_t rows;      // rows of a slab
+};
+
+hipError_t launch_decay_walk_f16(const DecayWalk &a, bool out_f32, hipStream_t stream);
+hipError_t launch_decay_step_f16(const DecayStep &a, bool vec, hipStream_t stream);
+hipError_t launch_decay_group_sum_f16(const float *src, void *dst, int64_t B, int64_t N, int Hk, int group, int D,
+                                      int64_t db, int64_t dt, int64_t dh, hipStream_t stream);
+hipError_t launch_linear_gemm_f16(const LinearGemm &a, int layout, int tile, bool vec, hipStream_t stream);
+hipError_t launch_linear_rows_f16(const LinearGemm &a, bool vec, hipStream_t stream);
+hipError_t launch_linear_dz_f16(const LinearDz &a, int64_t slabs, void *dbias, hipStream_t stream);
+hipError_t launch_decay_walk_bf16(const DecayWalk &a, bool out_f32, hipStream_t stream);
+hipError_t launch_decay_step_bf16(const DecayStep &a, bool vec, hipStream_t stream);
+hipError_t launch_decay_group_sum_bf16(const float *src, void *dst, int64_t B, int64_t N, int Hk, int group, int D,
+                                      int64_t db, int64_t dt, int64_t dh, hipStream_t stream);
+hipError_t launch_linear_gemm_bf16(const LinearGemm &a, int layout, int tile, bool vec, hipStream_t stream);
+hipError_t launch_linear_rows_bf16(const LinearGemm &a, bool vec, hipStream_t stream);
+hipError_t launch_linear_dz_bf16(const LinearDz &a, int64_t slabs, void *dbias, hipStream_t stream);
+hipError_t launch_decay_walk_f32(const DecayWalk &a, bool out_f32, hipStream_t stream);
+hipError_t launch_decay_step_f32(const DecayStep &a, bool vec, hipStream_t stream);
+hipError_t launch_decay_group_sum_f32(const float *src, void *dst, int64_t B, int64_t N, int Hk, int group, int D,
+                                      int64_t db, int64_t dt, int64_t dh, hipStream_t stream);
+hipError_t launch_linear_gemm_f32(const LinearGemm &a, int layout, int tile, bool vec, hipStream_t stream);
+hipError_t launch_linear_rows_f32(const LinearGemm &a, bool vec, hipStream_t stream);
+hipError_t launch_linear_dz_f32(const LinearDz &a, int64_t slabs, void *dbias, hipStream_t stream);
+
+}  // namespace fftconv
