@@ -16,7 +16,7 @@
 // both from the sequence's end with off = 0 (the state's gradient is read
 // before it is decayed; the walk keeps d G).
 //
-// A sequence is walked in chunks of C tokens: within a chunk the masked
+// A sequence is walked in chunks of C = 32 tokens: within a chunk the masked
 // product P = (X Y^T) o decay and O = P Z; across chunks O += diag(d^i) X E and
 // E <- d^C E + Y^T (d^(C-1-s) Z).  All four products run on the matrix cores.
 // One workgroup of four waves walks one (segment, head, tile of <= 128 z
@@ -25,7 +25,7 @@
 // leaves the registers.  The waves share only the chunk's X, Y, Z in LDS:
 // every wave recomputes P, whose accumulator layout is the operand layout of
 // P Z (rows of Y permuted so that a lane's 8 values are consecutive tokens),
-// which costs a third more matrix instructions than sharing P but saves its
+// which costs a fifth more matrix instructions than sharing P but saves its
 // LDS round trip and a barrier.
 //
 // Rounding (16-bit types): P and the state are rounded to the storage type
@@ -134,84 +134,187 @@ __device__ __forceinline__ float decay_power(float log2d, int64_t n) {
 
 constexpr float kLog2e = 1.44269504088896340736f;
 
-// Rows of a chunk from HBM into registers (16 bytes each), zeros outside; then into LDS.
-template <typename T, int C, int DP> struct ChunkLoad {
-    static constexpr int E = 16 / (int)sizeof(T);        // values of a piece
-    static constexpr int PR = DP / E;                    // pieces of a row
-    static constexpr int N = C * PR / 256;               // pieces of a thread
-    static constexpr int LD = DP + E;                    // LDS row stride: 16 bytes off the banks' period
-    static_assert(C * PR % 256 == 0, "whole pieces");
-    uint4 r[N];
+// A 64-bit value that is the same in every lane, as a scalar.
+__device__ __forceinline__ int64_t scalar(int64_t v) {
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v), hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
+    return (int64_t)((uint64_t)hi << 32 | lo);
+}
 
-    // tokens t0 .. t0 + C - 1 of a sequence of len tokens whose first token row is p
-    __device__ __forceinline__ void load(const T *p, int64_t stride, int64_t t0, int64_t end, int64_t len, int reverse,
-                                         int cols, int col0, int vec) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int idx = i * 256 + threadIdx.x, row = idx / PR, col = col0 + (idx % PR) * E;
-            const int64_t t = t0 + row;
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (t < end && col < cols) {
-                const T *src = p + (reverse ? len - 1 - t : t) * stride + col;
-                if (vec) {
-                    v = *reinterpret_cast<const uint4 *>(src);
-                } else {
-                    T e[E];
-#pragma unroll
-                    for (int j = 0; j < E; ++j) e[j] = col + j < cols ? src[j] : (T)0.0f;
-                    __builtin_memcpy(&v, e, 16);
-                }
-            }
-            r[i] = v;
+// Tokens of a chunk.  32 is one contraction step of the 16-bit matrix instruction: with it the
+// chunk's own products cost least (a 64-token chunk has half its P blocks to spare) and three
+// stages of tiles fit two workgroups on a CU.
+constexpr int kChunk = 32;
+
+// A chunk's tile of one operand in LDS: kChunk rows of DP values in 16-byte slots, slot s of row r
+// lying at s ^ f(r).  f spreads over the banks what one read instruction meets: 16 neighbouring
+// rows (X), or the permuted rows 8 (c / 4) + c % 4 and the columns of four rows (Y, Z).
+template <typename T, int DP, bool PERMUTED> struct ChunkTile {
+    static constexpr int E = 16 / (int)sizeof(T);            // values of a slot
+    static constexpr int PR = DP / E;                        // slots of a row
+    static constexpr int N = kChunk * PR / 256;              // 16-byte loads of a thread
+    static constexpr int VALUES = kChunk * DP;
+    static_assert(kChunk * PR % 256 == 0, "whole loads");
+    static __device__ __forceinline__ int f(int row) {
+        if (PR == 8) return PERMUTED ? ((row >> 1) & 1) << 2 | ((row >> 3) & 3) : (row >> 1) & 7;
+        return PERMUTED ? (row & 3) << 2 | ((row >> 3) & 3) : row & 15;
+    }
+    static __device__ __forceinline__ void source(int i, int &row, int &slot) {
+        const int idx = i * 256 + (threadIdx.x & 255);
+        row = idx / PR;
+        slot = idx % PR ^ f(row);
+    }
+    static __device__ __forceinline__ const T *at(const T *tile, int row, int slot) {
+        return tile + (row * PR + (slot ^ f(row))) * E;
+    }
+    // 8 values of a row at column col (a multiple of 8)
+    static __device__ __forceinline__ typename Mma<T>::v8 row8(const T *tile, int row, int col) {
+        if constexpr (sizeof(T) == 2) {
+            return *reinterpret_cast<const typename Mma<T>::v8 *>(at(tile, row, col / 8));
+        } else {
+            const f32x4 a = *reinterpret_cast<const f32x4 *>(at(tile, row, col / 4));
+            const f32x4 b = *reinterpret_cast<const f32x4 *>(at(tile, row, col / 4 + 1));
+            return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
         }
     }
-    __device__ __forceinline__ void store(T *tile) const {
+    // Rows 8 g + j of this lane's own column, mine.  16-bit types: two transposing reads, in which 16
+    // lanes read four rows of four 4-column groups and lane c receives column c % 4 of group c / 4;
+    // group is the start of the group that lanes of this c % 4 read.  fp32: value by value.
+    static __device__ __forceinline__ typename Mma<T>::v8 col8(const T *tile, int group, int mine) {
+        const int lane = threadIdx.x & 63, g = lane >> 4;
+        if constexpr (sizeof(T) == 2) {
+            const int row = g * 8 + ((lane & 15) >> 2);
+            const T *p = at(tile, row, group / 8) + group % 8;     // f(row + 4) = f(row)
+            typedef typename Mma<T>::v4 v4;
+            const v4 a = __builtin_bit_cast(v4, __builtin_amdgcn_ds_read_tr16_b64_v4i16(FFTCONV_LDS_CAST(s16x4, p)));
+            const v4 b = __builtin_bit_cast(v4, __builtin_amdgcn_ds_read_tr16_b64_v4i16(FFTCONV_LDS_CAST(s16x4, p + 4 * DP)));
+            return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+        } else {
+            typename Mma<T>::v8 v;
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int idx = i * 256 + threadIdx.x;
-            *reinterpret_cast<uint4 *>(tile + (idx / PR) * LD + (idx % PR) * E) = r[i];
+            for (int j = 0; j < 8; ++j) v[j] = at(tile, g * 8 + j, mine / 4)[mine % 4];
+            return v;
         }
     }
 };
 
-template <typename T> constexpr int decay_chunk() { return sizeof(T) == 2 ? 64 : 32; }
+// Brings a tensor's chunks into LDS.  VEC: loads with an LDS destination (rows of whole, aligned
+// 16-byte pieces; a piece outside the chunk or the columns reads zero by the buffer unit's range
+// check); else value by value through registers.
+template <typename T, int DP, bool PERMUTED, bool VEC> struct ChunkSource {
+    using Tile = ChunkTile<T, DP, PERMUTED>;
+    const T *p;            // the sequence's first row
+    int64_t stride, len;
+    int cols, col0, reverse;
+    uint32_t off[VEC ? Tile::N : 1];
+
+    __device__ __forceinline__ void init(const void *base, int64_t batch, int64_t sb, int64_t row0, int64_t st, int64_t head,
+                                         int64_t sh, int64_t len_, int cols_, int col0_, int reverse_) {
+        p = static_cast<const T *>(base) + batch * sb + row0 * st + head * sh;
+        stride = st;
+        len = len_;
+        cols = cols_, col0 = col0_, reverse = reverse_;
+        if constexpr (VEC) {
+#pragma unroll
+            for (int i = 0; i < Tile::N; ++i) {
+                int row, slot;
+                Tile::source(i, row, slot);
+                const int col = col0 + slot * Tile::E;
+                off[i] = col < cols ? (uint32_t)(((reverse ? kChunk - 1 - row : row) * stride + col) * (int64_t)sizeof(T))
+                                    : 0x80000000u;
+            }
+        }
+    }
+    // tokens t0 .. t0 + n - 1 (n <= kChunk) into the tile; the rest becomes zero
+    __device__ __forceinline__ void bring(int64_t t0, int n, T *tile) const {
+        if constexpr (VEC) {
+            const int wave = __builtin_amdgcn_readfirstlane((threadIdx.x & 255) >> 6);
+            const T *first = p + (reverse ? len - t0 - kChunk : t0) * stride;
+            auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<T *>(first), (short)0, 0x7fffffff, 0x00020000);
+#pragma unroll
+            for (int i = 0; i < Tile::N; ++i) {
+                uint32_t o = off[i];
+                if (n < kChunk) {
+                    int row, slot;
+                    Tile::source(i, row, slot);
+                    if (row >= n) o = 0x80000000u;
+                }
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                    rsrc, FFTCONV_LDS_CAST(void, tile + (i * 256 + wave * 64) * Tile::E), 16, o, 0, 0, 0);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < Tile::N; ++i) {
+                int row, slot;
+                Tile::source(i, row, slot);
+                const int col = col0 + slot * Tile::E;
+                const T *src = p + (reverse ? len - 1 - (t0 + row) : t0 + row) * stride + col;
+                T e[Tile::E];
+#pragma unroll
+                for (int j = 0; j < Tile::E; ++j) e[j] = row < n && col + j < cols ? src[j] : (T)0.0f;
+                __builtin_memcpy(tile + (i * 256 + (threadIdx.x & 255)) * Tile::E, e, 16);
+            }
+        }
+    }
+};
+
+// Stages of tiles in LDS: the chunk in use and those on their way.  Three where two workgroups of
+// them fit a CU's 160 KB, else two; without LDS-destination loads one.
+constexpr int walk_stages(int bytes, bool vec) { return !vec ? 1 : (3 * bytes <= 78 * 1024 ? 3 : (2 * bytes <= 150 * 1024 ? 2 : 1)); }
 
 // grid: (nblk, H, z tiles); OUT = false: the segment's own sum only (y, z read), for every
 // segment that another follows.  DXP: DX padded; NT: 16-column tiles of E per wave.
-template <typename T, typename TO, int DXP, int NT, bool OUT>
+template <typename T, typename TO, int DXP, int NT, bool OUT, bool VEC>
 __global__ __launch_bounds__(256, DXP <= 128 ? 2 : 1) void decay_walk_kernel(const DecayWalk a) {
-    constexpr int C = decay_chunk<T>();
+#ifdef __HIP_DEVICE_COMPILE__   // the host pass, which cannot take the LDS-destination loads, needs the stub alone
     constexpr int KX = DXP / 32;          // 32-wide contraction steps over DX
-    constexpr int KC = C / 32;            // and over a chunk's tokens
-    constexpr int RT = C / 16;            // 16-token row tiles of a chunk
     constexpr int DZT = NT * 64;          // z columns of a workgroup
     constexpr int kSplit = Mma<T>::kSplit;
-    using LX = ChunkLoad<T, C, DXP>;
-    using LZ = ChunkLoad<T, C, DZT>;
+    using TX = ChunkTile<T, DXP, false>;
+    using TY = ChunkTile<T, DXP, true>;
+    using TZ = ChunkTile<T, DZT, true>;
     using v8 = typename Mma<T>::v8;
-    __shared__ __attribute__((aligned(16))) T sx[OUT ? C * LX::LD : 8];
-    __shared__ __attribute__((aligned(16))) T sy[C * LX::LD];
-    __shared__ __attribute__((aligned(16))) T sz[C * LZ::LD];
-    __shared__ float upd[2 * C];          // u_scale d^(C - off - s): weight of token s in the next state
-    __shared__ float row_w[C];            // i_scale d^(i + off): weight of the chunk's first state in row i
+    constexpr int kBytes = ((OUT ? 2 : 1) * TY::VALUES + TZ::VALUES) * (int)sizeof(T);
+    constexpr int S = walk_stages(kBytes, VEC);
+    constexpr int kLoads = (OUT ? 2 : 1) * TY::N + TZ::N;
+    // stages as separate arrays: loads into one are then known not to alias reads of another
+    __shared__ __attribute__((aligned(128))) T x0[OUT ? TX::VALUES : 8], y0[TY::VALUES], z0[TZ::VALUES];
+    __shared__ __attribute__((aligned(128))) T x1[OUT && S > 1 ? TX::VALUES : 8], y1[S > 1 ? TY::VALUES : 8], z1[S > 1 ? TZ::VALUES : 8];
+    __shared__ __attribute__((aligned(128))) T x2[OUT && S > 2 ? TX::VALUES : 8], y2[S > 2 ? TY::VALUES : 8], z2[S > 2 ? TZ::VALUES : 8];
+    __shared__ __attribute__((aligned(16))) float upd[2 * kChunk];   // u_scale d^(C - off - s): weight of token s in the next state
+    __shared__ float row_w[kChunk];       // i_scale d^(i + off): weight of the chunk's first state in row i
 
     SegInfo si;
     if (!find_segment(a, blockIdx.x, false, si)) return;
+    si.seq = scalar(si.seq), si.index = scalar(si.index), si.count = scalar(si.count);
+    si.start = scalar(si.start), si.len = scalar(si.len);
     if (!OUT && si.index + 1 >= si.count) return;
-    const int h = blockIdx.y, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int h = blockIdx.y, tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int g = lane >> 4, c = lane & 15;
-    const int z0 = blockIdx.z * DZT;                     // first z column of the workgroup
+    const int col0 = blockIdx.z * DZT;                   // first z column of the workgroup
     const int zw = wave * NT * 16;                       // this wave's columns within it
     const int64_t t_begin = si.index * a.seglen;
     const int64_t t_end = t_begin + a.seglen < si.len && si.index + 1 < si.count ? t_begin + a.seglen : si.len;
     const int64_t row0 = a.cu ? si.start : 0, batch = a.cu ? 0 : si.seq;
-    const T *px = static_cast<const T *>(a.x) + batch * a.xb + row0 * a.xt + (h / a.gx) * a.xh;
-    const T *py = static_cast<const T *>(a.y) + batch * a.yb + row0 * a.yt + (h / a.gy) * a.yh;
-    const T *pz = static_cast<const T *>(a.z) + batch * a.zb + row0 * a.zt + (h / a.gz) * a.zh;
     const float log2d = a.log_decay[h] * kLog2e;
 
-    for (int i = tid; i < 2 * C; i += 256) upd[i] = i < C ? a.u_scale * decay_power(log2d, C - a.off - i) : 0.0f;
-    for (int i = tid; i < C; i += 256) row_w[i] = a.i_scale * decay_power(log2d, i + a.off);
+    for (int i = tid; i < 2 * kChunk; i += 256) upd[i] = i < kChunk ? a.u_scale * decay_power(log2d, kChunk - a.off - i) : 0.0f;
+    for (int i = tid; i < kChunk; i += 256) row_w[i] = a.i_scale * decay_power(log2d, i + a.off);
+
+    ChunkSource<T, DXP, false, VEC> src_x;
+    ChunkSource<T, DXP, true, VEC> src_y;
+    ChunkSource<T, DZT, true, VEC> src_z;
+    if (OUT) src_x.init(a.x, batch, a.xb, row0, a.xt, h / a.gx, a.xh, si.len, a.DX, 0, a.reverse);
+    src_y.init(a.y, batch, a.yb, row0, a.yt, h / a.gy, a.yh, si.len, a.DX, 0, a.reverse);
+    src_z.init(a.z, batch, a.zb, row0, a.zt, h / a.gz, a.zh, si.len, a.DZ, col0, a.reverse);
+    auto bring = [&](int64_t t, T *x, T *y, T *z) __attribute__((always_inline)) {
+        const int n = t_end - t < kChunk ? (int)(t_end - t) : kChunk;
+        if (OUT) src_x.bring(t, n, x);
+        src_y.bring(t, n, y);
+        src_z.bring(t, n, z);
+    };
+    if (S > 1 && t_begin < t_end) bring(t_begin, x0, y0, z0);
+    if (S > 2 && t_begin + kChunk < t_end) bring(t_begin + kChunk, x1, y1, z1);
 
     // z column of accumulator column m of tile t (NT = 2: a lane's two tiles hold 8 neighbours)
     auto zcol = [&](int m, int t) { return zw + (NT == 2 ? (m >> 2) * 8 + t * 4 + (m & 3) : m); };
@@ -237,119 +340,114 @@ __global__ __launch_bounds__(256, DXP <= 128 ? 2 : 1) void decay_walk_kernel(con
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const int dx = kk * 32 + g * 8 + r * 4 + i, dz = z0 + zcol(c, t);
+                        const int dx = kk * 32 + g * 8 + r * 4 + i, dz = col0 + zcol(c, t);
                         E[kk][r][t][i] = s0 && dx < a.DX && dz < a.DZ ? s0[dx * sx_ + dz * sz_] : 0.0f;
                     }
     }
-    // decay of P: tile pair at row offset 16 o from its 32 tokens, value (r, i): d^(16 o + c - 8 g - 4 r - i)
-    float fac[2 * KC][2][4];
+    // decay of P in row tile rt, accumulator (r, i): d^(16 rt + c - 8 g - 4 r - i), 0 above the diagonal
+    float fac[2][2][4];
     if (OUT) {
 #pragma unroll
-        for (int o = 0; o < 2 * KC; ++o)
+        for (int rt = 0; rt < 2; ++rt)
 #pragma unroll
             for (int r = 0; r < 2; ++r)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int n = 16 * o + c - 8 * g - 4 * r - i;
-                    fac[o][r][i] = n < 0 ? 0.0f : a.p_scale * decay_power(log2d, n);
+                    const int n = 16 * rt + c - 8 * g - 4 * r - i;
+                    fac[rt][r][i] = n < 0 ? 0.0f : a.p_scale * decay_power(log2d, n);
                 }
     }
-
-    LX lx, ly;
-    LZ lz;
-    if (OUT) lx.load(px, a.xt, t_begin, t_end, si.len, a.reverse, a.DX, 0, a.vec_x);
-    ly.load(py, a.yt, t_begin, t_end, si.len, a.reverse, a.DX, 0, a.vec_y);
-    lz.load(pz, a.zt, t_begin, t_end, si.len, a.reverse, a.DZ, z0, a.vec_z);
+    const float dfull = decay_power(log2d, kChunk);
+    TO *out = OUT ? static_cast<TO *>(a.out) + batch * a.ob + row0 * a.ot + (h / a.go) * a.oh + col0 + zw + (NT == 2 ? g * 8 : g * 4)
+                  : nullptr;
+    const int out_cols = a.DZ - (col0 + zw + (NT == 2 ? g * 8 : g * 4));    // columns left for this lane
     int ex = 0;            // the accumulators hold E * 2^ex (fp16 only, else 0)
-    for (int64_t t0 = t_begin; t0 < t_end; t0 += C) {
-        __syncthreads();
-        if (OUT) lx.store(sx);
-        ly.store(sy);
-        lz.store(sz);
-        __syncthreads();
-        if (t0 + C < t_end) {
-            if (OUT) lx.load(px, a.xt, t0 + C, t_end, si.len, a.reverse, a.DX, 0, a.vec_x);
-            ly.load(py, a.yt, t0 + C, t_end, si.len, a.reverse, a.DX, 0, a.vec_y);
-            lz.load(pz, a.zt, t0 + C, t_end, si.len, a.reverse, a.DZ, z0, a.vec_z);
+
+    // one chunk at token t in (x, y, z); (nx, ny, nz) is free for the chunk S - 1 ahead
+    auto chunk = [&](int64_t t, const T *x, const T *y, const T *z, T *nx, T *ny, T *nz) __attribute__((always_inline)) {
+        if constexpr (S == 1) {
+            __syncthreads();
+            bring(t, nx, ny, nz);
+            __syncthreads();
+        } else {
+            // this chunk's loads are the oldest; with three stages the next chunk's, if there is one,
+            // may still travel (vmcnt retires in order).  The wait on LDS reads keeps every wave's
+            // reads of the freed stage before the loads into it.
+            asm volatile("" ::: "memory");
+            if (S == 3 && t + kChunk < t_end) __builtin_amdgcn_s_waitcnt((kLoads & 15) | 0x70 | (kLoads >> 4) << 14);
+            else __builtin_amdgcn_s_waitcnt(0x70);
+            __builtin_amdgcn_s_barrier();
+            asm volatile("" ::: "memory");
+            if (t + (S - 1) * kChunk < t_end) bring(t + (S - 1) * kChunk, nx, ny, nz);
         }
-        const int n = t_end - t0 < C ? (int)(t_end - t0) : C;
-        // this wave's columns of Z, tokens 8 g .. 8 g + 7 of each 32
-        v8 zf[KC][NT];
+        const int n = t_end - t < kChunk ? (int)(t_end - t) : kChunk;
+        // this wave's columns of Z, tokens 8 g .. 8 g + 7
+        v8 zf[NT];
 #pragma unroll
-        for (int kc = 0; kc < KC; ++kc)
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-                zf[kc][t] = lds_col8<T>(sz, LZ::LD, kc * 32 + g * 8,
-                                        zw + (NT == 2 ? (lane & 3) * 8 + t * 4 : (lane & 3) * 4), zcol(c, t));
+        for (int q = 0; q < NT; ++q)
+            zf[q] = TZ::col8(z, zw + (NT == 2 ? (lane & 3) * 8 + q * 4 : (lane & 3) * 4), zcol(c, q));
         if (OUT) {
             const float unscale = Mma<T>::kNarrow ? ldexpf(1.0f, -ex) : 1.0f;
-            v8 ef[KX][NT];     // the state as an operand: row zcol(c, t), slots 8 g + j
+            v8 ef[KX][NT];     // the state as an operand: row zcol(c, q), slots 8 g + j
 #pragma unroll
             for (int kk = 0; kk < KX; ++kk)
 #pragma unroll
-                for (int t = 0; t < NT; ++t)
+                for (int q = 0; q < NT; ++q)
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) ef[kk][t][j] = (T)(Mma<T>::kNarrow ? E[kk][j >> 2][t][j & 3] * unscale : E[kk][j >> 2][t][j & 3]);
-#pragma unroll
-            for (int rt = 0; rt < RT; ++rt) {
-                v8 xf[KX];
-#pragma unroll
-                for (int kk = 0; kk < KX; ++kk) xf[kk] = lds_row8<T>(sx + (rt * 16 + c) * LX::LD + kk * 32 + g * 8);
-                f32x4 o[NT];
-#pragma unroll
-                for (int t = 0; t < NT; ++t) o[t] = f32x4{0, 0, 0, 0};
-#pragma unroll
-                for (int kk = 0; kk < KX; ++kk)
-#pragma unroll
-                    for (int t = 0; t < NT; ++t) o[t] = Mma<T>::mma(ef[kk][t], xf[kk], o[t]);
-                const float rw = row_w[rt * 16 + c];
-#pragma unroll
-                for (int t = 0; t < NT; ++t) o[t] *= rw;
-#pragma unroll
-                for (int kc = 0; kc <= rt / 2; ++kc) {
-                    v8 pf;
-#pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        // rows of Y permuted: accumulator row m is token kc * 32 + 8 (m / 4) + 4 r + m % 4
-                        f32x4 p = {0, 0, 0, 0};
-                        const T *yr = sy + (kc * 32 + (c >> 2) * 8 + r * 4 + (c & 3)) * LX::LD + g * 8;
-#pragma unroll
-                        for (int kk = 0; kk < KX; ++kk) p = Mma<T>::mma(lds_row8<T>(yr + kk * 32), xf[kk], p);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) pf[r * 4 + i] = (T)(p[i] * fac[rt - 2 * kc][r][i]);
+                    for (int j = 0; j < 8; ++j) {
+                        const float e = E[kk][j >> 2][q][j & 3];
+                        ef[kk][q][j] = (T)(Mma<T>::kNarrow ? e * unscale : e);
                     }
 #pragma unroll
-                    for (int t = 0; t < NT; ++t) o[t] = Mma<T>::mma(zf[kc][t], pf, o[t]);
+            for (int rt = 0; rt < 2; ++rt) {
+                f32x4 o[NT], p[2];
+#pragma unroll
+                for (int q = 0; q < NT; ++q) o[q] = f32x4{0, 0, 0, 0};
+                p[0] = p[1] = f32x4{0, 0, 0, 0};
+#pragma unroll
+                for (int kk = 0; kk < KX; ++kk) {
+                    const v8 xf = TX::row8(x, rt * 16 + c, kk * 32 + g * 8);
+#pragma unroll
+                    for (int q = 0; q < NT; ++q) o[q] = Mma<T>::mma(ef[kk][q], xf, o[q]);
+                    // rows of Y permuted: accumulator row m is token 8 (m / 4) + 4 r + m % 4
+#pragma unroll
+                    for (int r = 0; r < 2; ++r)
+                        p[r] = Mma<T>::mma(TY::row8(y, (c >> 2) * 8 + r * 4 + (c & 3), kk * 32 + g * 8), xf, p[r]);
+                }
+                const float rw = row_w[rt * 16 + c];
+                v8 pf;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) pf[j] = (T)(p[j >> 2][j & 3] * fac[rt][j >> 2][j & 3]);
+#pragma unroll
+                for (int q = 0; q < NT; ++q) {
+                    o[q] *= rw;
+                    o[q] = Mma<T>::mma(zf[q], pf, o[q]);
                 }
                 const int row = rt * 16 + c;
                 if (row < n && a.out) {
-                    const int64_t tok = a.reverse ? si.len - 1 - (t0 + row) : t0 + row;
-                    TO *po = static_cast<TO *>(a.out) + batch * a.ob + (row0 + tok) * a.ot + (h / a.go) * a.oh;
-                    const int dz = z0 + zw + (NT == 2 ? g * 8 : g * 4);
-                    if (a.vec_o && dz + NT * 4 <= a.DZ) {
+                    TO *po = out + (a.reverse ? si.len - 1 - (t + row) : t + row) * a.ot;
+                    if ((VEC || a.vec_o) && NT * 4 <= out_cols) {
                         TO w[NT * 4];
 #pragma unroll
                         for (int j = 0; j < NT * 4; ++j) w[j] = (TO)o[j >> 2][j & 3];
-                        __builtin_memcpy(__builtin_assume_aligned(po + dz, sizeof(TO) * NT * 4 < 16 ? sizeof(TO) * NT * 4 : 16), w,
-                                         sizeof w);
+                        __builtin_memcpy(__builtin_assume_aligned(po, sizeof(TO) * NT * 4 < 16 ? sizeof(TO) * NT * 4 : 16), w, sizeof w);
                     } else {
 #pragma unroll
                         for (int j = 0; j < NT * 4; ++j)
-                            if (dz + j < a.DZ) po[dz + j] = (TO)o[j >> 2][j & 3];
+                            if (j < out_cols) po[j] = (TO)o[j >> 2][j & 3];
                     }
                 }
             }
         }
         // E <- d^n E + Y^T (weights Z)
-        float dn = decay_power(log2d, n), lift = 1.0f;
+        float dn = n == kChunk ? dfull : decay_power(log2d, n), lift = 1.0f;
         if (Mma<T>::kNarrow) {
             float most = 0.0f;
 #pragma unroll
-            for (int kc = 0; kc < KC; ++kc)
+            for (int q = 0; q < NT; ++q)
 #pragma unroll
-                for (int t = 0; t < NT; ++t)
+                for (int j = 0; j < 8; ++j) most = fmaxf(most, fabsf((float)zf[q][j]));
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) most = fmaxf(most, fabsf((float)zf[kc][t][j]));
             for (int s = 1; s < 64; s <<= 1) most = fmaxf(most, __shfl_xor(most, s));
             most *= fabsf(a.u_scale);
             // the largest term near 2^14; the weights are at most u_scale
@@ -365,40 +463,49 @@ __global__ __launch_bounds__(256, DXP <= 128 ? 2 : 1) void decay_walk_kernel(con
 #pragma unroll
             for (int r = 0; r < 2; ++r)
 #pragma unroll
-                for (int t = 0; t < NT; ++t) E[kk][r][t] *= dn;
+                for (int q = 0; q < NT; ++q) E[kk][r][q] *= dn;
+        v8 zs[NT][kSplit];
+        float w[8];
 #pragma unroll
-        for (int kc = 0; kc < KC; ++kc) {
-            v8 zw_[NT][kSplit];
-            float w[8];
+        for (int j = 0; j < 8; ++j) w[j] = upd[kChunk - n + g * 8 + j];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) w[j] = upd[C - n + kc * 32 + g * 8 + j] * lift;
+        for (int q = 0; q < NT; ++q)
 #pragma unroll
-            for (int t = 0; t < NT; ++t)
+            for (int j = 0; j < 8; ++j) {
+                float rest = (float)zf[q][j] * (Mma<T>::kNarrow ? w[j] * lift : w[j]);
+                // one value for every use: left to itself the compiler rounds the product to fp16 once
+                // through fp32 and once fused, and the two first terms then differ at ties
+                if (kSplit > 1) asm("" : "+v"(rest));
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    float rest = (float)zf[kc][t][j] * w[j];
-                    // one value for every use: left to itself the compiler rounds the product to fp16 once
-                    // through fp32 and once fused, and the two first terms then differ at ties
-                    if (kSplit > 1) asm("" : "+v"(rest));
-#pragma unroll
-                    for (int s = 0; s < kSplit; ++s) {
-                        const T part = (T)rest;
-                        zw_[t][s][j] = part;
-                        rest -= (float)part;
-                    }
+                for (int s = 0; s < kSplit; ++s) {
+                    const T part = (T)rest;
+                    zs[q][s][j] = part;
+                    rest -= (float)part;
                 }
+            }
 #pragma unroll
-            for (int kk = 0; kk < KX; ++kk)
+        for (int kk = 0; kk < KX; ++kk)
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    // rows of the state permuted like zcol: row m is kk * 32 + 8 (m / 4) + 4 r + m % 4
-                    const v8 yf = lds_col8<T>(sy, LX::LD, kc * 32 + g * 8, kk * 32 + (lane & 3) * 8 + r * 4,
-                                              kk * 32 + (c >> 2) * 8 + r * 4 + (c & 3));
+            for (int r = 0; r < 2; ++r) {
+                // rows of the state permuted like zcol: row m is kk * 32 + 8 (m / 4) + 4 r + m % 4
+                const v8 yf = TY::col8(y, kk * 32 + (lane & 3) * 8 + r * 4, kk * 32 + (c >> 2) * 8 + r * 4 + (c & 3));
 #pragma unroll
-                    for (int t = 0; t < NT; ++t)
+                for (int q = 0; q < NT; ++q)
 #pragma unroll
-                        for (int s = 0; s < kSplit; ++s) E[kk][r][t] = Mma<T>::mma(yf, zw_[t][s], E[kk][r][t]);
-                }
+                    for (int s = 0; s < kSplit; ++s) E[kk][r][q] = Mma<T>::mma(yf, zs[q][s], E[kk][r][q]);
+            }
+    };
+    __syncthreads();       // the tables above
+    for (int64_t t = t_begin; t < t_end; t += S * kChunk) {
+        if constexpr (S == 1) {
+            chunk(t, x0, y0, z0, x0, y0, z0);
+        } else if constexpr (S == 2) {
+            chunk(t, x0, y0, z0, x1, y1, z1);
+            if (t + kChunk < t_end) chunk(t + kChunk, x1, y1, z1, x0, y0, z0);
+        } else {
+            chunk(t, x0, y0, z0, x2, y2, z2);
+            if (t + kChunk < t_end) chunk(t + kChunk, x1, y1, z1, x0, y0, z0);
+            if (t + 2 * kChunk < t_end) chunk(t + 2 * kChunk, x2, y2, z2, x1, y1, z1);
         }
     }
 
@@ -422,9 +529,10 @@ __global__ __launch_bounds__(256, DXP <= 128 ? 2 : 1) void decay_walk_kernel(con
             for (int t = 0; t < NT; ++t)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int dx = kk * 32 + g * 8 + r * 4 + i, dz = z0 + zcol(c, t);
+                    const int dx = kk * 32 + g * 8 + r * 4 + i, dz = col0 + zcol(c, t);
                     if (dx < a.DX && dz < a.DZ) s1[dx * sx_ + dz * sz_] = E[kk][r][t][i] * unscale;
                 }
+#endif
 }
 
 // The single-token form: E <- d E + k v^T, out = scale E^T q, one workgroup per (sequence,
@@ -538,24 +646,25 @@ static __global__ __launch_bounds__(256) void decay_chain_kernel(const DecayWalk
 }
 
 // ---- host side of one storage type ----------------------------------------
-template <typename T, typename TO> static hipError_t walk_dispatch(const DecayWalk &a, bool out, hipStream_t stream) {
+template <typename T, typename TO, bool OUT, bool VEC> static hipError_t walk_launch(const DecayWalk &a, hipStream_t stream) {
     const bool narrow = a.DZ <= 64;
     const dim3 grid((unsigned)a.nblk, (unsigned)a.H, (unsigned)((a.DZ + (narrow ? 63 : 127)) / (narrow ? 64 : 128)));
-#define FFTCONV_WALK(DXP)                                                                                       \
-    do {                                                                                                        \
-        if (out) {                                                                                              \
-            if (narrow) decay_walk_kernel<T, TO, DXP, 1, true><<<grid, 256, 0, stream>>>(a);                    \
-            else decay_walk_kernel<T, TO, DXP, 2, true><<<grid, 256, 0, stream>>>(a);                           \
-        } else {                                                                                                \
-            if (narrow) decay_walk_kernel<T, T, DXP, 1, false><<<grid, 256, 0, stream>>>(a);                    \
-            else decay_walk_kernel<T, T, DXP, 2, false><<<grid, 256, 0, stream>>>(a);                           \
-        }                                                                                                       \
+#define FFTCONV_WALK(DXP)                                                                       \
+    do {                                                                                        \
+        if (narrow) decay_walk_kernel<T, TO, DXP, 1, OUT, VEC><<<grid, 256, 0, stream>>>(a);     \
+        else decay_walk_kernel<T, TO, DXP, 2, OUT, VEC><<<grid, 256, 0, stream>>>(a);            \
     } while (0)
     if (a.DX <= 64) FFTCONV_WALK(64);
     else if (a.DX <= 128) FFTCONV_WALK(128);
     else FFTCONV_WALK(256);
 #undef FFTCONV_WALK
     return hipGetLastError();
+}
+
+template <typename T, typename TO> static hipError_t walk_dispatch(const DecayWalk &a, bool out, hipStream_t stream) {
+    if (!out) return a.vec_y && a.vec_z ? walk_launch<T, T, false, true>(a, stream) : walk_launch<T, T, false, false>(a, stream);
+    return a.vec_x && a.vec_y && a.vec_z && a.vec_o ? walk_launch<T, TO, true, true>(a, stream)
+                                                    : walk_launch<T, TO, true, false>(a, stream);
 }
 
 template <typename T> static hipError_t walk_typed(const DecayWalk &a, bool out_f32, hipStream_t stream) {

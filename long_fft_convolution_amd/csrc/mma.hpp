@@ -65,30 +65,4 @@ template <> __device__ __forceinline__ Mma<float>::v8 lds_row8<float>(const floa
     return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
-// One column of 8 consecutive LDS rows (rows row0 .. row0 + 7 at stride ld),
-// for the column whose 4-wide group of 16 lanes starts at col4(l % 4): lane c
-// of the 16 receives column col4(c / 4) + c % 4.  16-bit types take two
-// transposing reads (ds_read_b64_tr_b16: the 16 lanes read four rows of four
-// 4-value groups and receive one column each); col is this lane's own group
-// address, col4(l % 4), and row its own row, row0 + (l % 16) / 4.  fp32 reads
-// its column value by value (mine = this lane's own column).
-template <typename T>
-__device__ __forceinline__ typename Mma<T>::v8 lds_col8(const T *tile, int ld, int row0, int group_col, int mine) {
-    if constexpr (sizeof(T) == 2) {
-        const int r = (threadIdx.x & 15) >> 2;
-        const T *p = tile + (row0 + r) * ld + group_col;
-        typedef typename Mma<T>::v4 v4;
-        const v4 a = __builtin_bit_cast(v4, __builtin_amdgcn_ds_read_tr16_b64_v4i16(FFTCONV_LDS_CAST(s16x4, p)));
-        const v4 b = __builtin_bit_cast(v4, __builtin_amdgcn_ds_read_tr16_b64_v4i16(FFTCONV_LDS_CAST(s16x4, p + 4 * ld)));
-        return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
-    } else {
-        typename Mma<T>::v8 v;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = tile[(row0 + j) * ld + mine];
-        return v;
-    }
-}
-
-template <typename T> __device__ __forceinline__ float to_f(T x) { return (float)x; }
-
 }  // namespace fftconv

@@ -212,19 +212,23 @@ fftconv_status_t check_apart(const View *outs, int nout, const View *ins, int ni
     return FFTCONV_OK;
 }
 
+// whole 16-byte pieces along rows, and a chunk's rows within 31 bits of byte offset
+bool chunk_vec(const View &v) {
+    return v.vec16() && v.row % (16 / v.bytes_per) == 0 && (v.size[1] <= 1 || v.stride[1] * v.bytes_per < (int64_t(1) << 25));
+}
 void set_x(DecayWalk &w, const View &v, int64_t H) {
     w.x = v.p, w.xb = v.stride[0], w.xt = v.stride[1], w.xh = v.stride[2], w.gx = (int)(H / v.size[2]);
     w.DX = (int)v.row;
-    w.vec_x = v.vec16() && v.row % (16 / v.bytes_per) == 0;
+    w.vec_x = chunk_vec(v);
 }
 void set_y(DecayWalk &w, const View &v, int64_t H) {
     w.y = v.p, w.yb = v.stride[0], w.yt = v.stride[1], w.yh = v.stride[2], w.gy = (int)(H / v.size[2]);
-    w.vec_y = v.vec16() && v.row % (16 / v.bytes_per) == 0;
+    w.vec_y = chunk_vec(v);
 }
 void set_z(DecayWalk &w, const View &v, int64_t H) {
     w.z = v.p, w.zb = v.stride[0], w.zt = v.stride[1], w.zh = v.stride[2], w.gz = (int)(H / v.size[2]);
     w.DZ = (int)v.row;
-    w.vec_z = v.vec16() && v.row % (16 / v.bytes_per) == 0;
+    w.vec_z = chunk_vec(v);
 }
 void set_out(DecayWalk &w, const View &v, int64_t H) {
     w.out = const_cast<void *>(v.p), w.ob = v.stride[0], w.ot = v.stride[1], w.oh = v.stride[2];
