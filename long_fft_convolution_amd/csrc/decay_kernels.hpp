@@ -31,9 +31,15 @@
 // Rounding (16-bit types): P and the state are rounded to the storage type
 // as operands of O (an error like the output's own rounding).  The state is
 // an fp32 result, so its update must not lose: d^(C-1-s) Z is split into
-// 2 (fp16) or 3 (bf16) storage-type terms that hold it to fp32 precision; in
-// fp16, whose second term would fall among the subnormals for |Z| << 1, the
-// accumulators hold E times a power of two that follows each chunk's largest |Z|.
+// 2 (fp16) or 3 (bf16) storage-type terms that hold it to fp32 precision (2 in
+// bf16 where only outputs see the state).
+//
+// The accumulators hold E times a gain that grows by d^-C a chunk, so that
+// decaying the state costs one factor in the chunk's weights instead of a
+// multiplication of every accumulator; they are brought back when the gain
+// has grown by 2^16 (few bits of its exponent, so exp2 of it is exact to a
+// few 2^-24), in fp16 also when the terms leave the range that keeps the
+// second one out of the subnormals.
 //
 // A call with few (sequence, head) pairs splits sequences into segments: a
 // first pass over y, z gives each segment's own sum, a small kernel chains
@@ -263,12 +269,11 @@ constexpr int walk_stages(int bytes, bool vec) { return !vec ? 1 : (3 * bytes <=
 
 // grid: (nblk, H, z tiles); OUT = false: the segment's own sum only (y, z read), for every
 // segment that another follows.  DXP: DX padded; NT: 16-column tiles of E per wave.
-template <typename T, typename TO, int DXP, int NT, bool OUT, bool VEC>
+template <typename T, typename TO, int DXP, int NT, bool OUT, bool VEC, int TERMS>
 __global__ __launch_bounds__(256, DXP <= 128 ? 2 : 1) void decay_walk_kernel(const DecayWalk a) {
 #ifdef __HIP_DEVICE_COMPILE__   // the host pass, which cannot take the LDS-destination loads, needs the stub alone
     constexpr int KX = DXP / 32;          // 32-wide contraction steps over DX
     constexpr int DZT = NT * 64;          // z columns of a workgroup
-    constexpr int kSplit = Mma<T>::kSplit;
     using TX = ChunkTile<T, DXP, false>;
     using TY = ChunkTile<T, DXP, true>;
     using TZ = ChunkTile<T, DZT, true>;
@@ -287,7 +292,8 @@ __global__ __launch_bounds__(256, DXP <= 128 ? 2 : 1) void decay_walk_kernel(con
     if (!find_segment(a, blockIdx.x, false, si)) return;
     si.seq = scalar(si.seq), si.index = scalar(si.index), si.count = scalar(si.count);
     si.start = scalar(si.start), si.len = scalar(si.len);
-    if (!OUT && si.index + 1 >= si.count) return;
+    // the last segment's sum is wanted only for the final state
+    if (!OUT && si.index + 1 >= si.count && !a.state1) return;
     const int h = blockIdx.y, tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int g = lane >> 4, c = lane & 15;
@@ -357,11 +363,12 @@ __global__ __launch_bounds__(256, DXP <= 128 ? 2 : 1) void decay_walk_kernel(con
                     fac[rt][r][i] = n < 0 ? 0.0f : a.p_scale * decay_power(log2d, n);
                 }
     }
-    const float dfull = decay_power(log2d, kChunk);
+    const float wn = -log2d * kChunk;   // growth of the gain's exponent over a full chunk
     TO *out = OUT ? static_cast<TO *>(a.out) + batch * a.ob + row0 * a.ot + (h / a.go) * a.oh + col0 + zw + (NT == 2 ? g * 8 : g * 4)
                   : nullptr;
     const int out_cols = a.DZ - (col0 + zw + (NT == 2 ? g * 8 : g * 4));    // columns left for this lane
-    int ex = 0;            // the accumulators hold E * 2^ex (fp16 only, else 0)
+    float grown = 0.0f;    // the accumulators hold E * 2^(grown + ex)
+    int ex = 0;            // (ex: fp16 only, else 0)
 
     // one chunk at token t in (x, y, z); (nx, ny, nz) is free for the chunk S - 1 ahead
     auto chunk = [&](int64_t t, const T *x, const T *y, const T *z, T *nx, T *ny, T *nz) __attribute__((always_inline)) {
@@ -387,7 +394,7 @@ __global__ __launch_bounds__(256, DXP <= 128 ? 2 : 1) void decay_walk_kernel(con
         for (int q = 0; q < NT; ++q)
             zf[q] = TZ::col8(z, zw + (NT == 2 ? (lane & 3) * 8 + q * 4 : (lane & 3) * 4), zcol(c, q));
         if (OUT) {
-            const float unscale = Mma<T>::kNarrow ? ldexpf(1.0f, -ex) : 1.0f;
+            const float unscale = Mma<T>::kNarrow ? ldexpf(exp2f(-grown), -ex) : exp2f(-grown);
             v8 ef[KX][NT];     // the state as an operand: row zcol(c, q), slots 8 g + j
 #pragma unroll
             for (int kk = 0; kk < KX; ++kk)
@@ -414,7 +421,7 @@ __global__ __launch_bounds__(256, DXP <= 128 ? 2 : 1) void decay_walk_kernel(con
                     for (int r = 0; r < 2; ++r)
                         p[r] = Mma<T>::mma(TY::row8(y, (c >> 2) * 8 + r * 4 + (c & 3), kk * 32 + g * 8), xf, p[r]);
                 }
-                const float rw = row_w[rt * 16 + c];
+                const float rw = Mma<T>::kNarrow ? row_w[rt * 16 + c] : row_w[rt * 16 + c] * unscale;
                 v8 pf;
 #pragma unroll
                 for (int j = 0; j < 8; ++j) pf[j] = (T)(p[j >> 2][j & 3] * fac[rt][j >> 2][j & 3]);
@@ -425,13 +432,13 @@ __global__ __launch_bounds__(256, DXP <= 128 ? 2 : 1) void decay_walk_kernel(con
                 }
                 const int row = rt * 16 + c;
                 if (row < n && a.out) {
-                    TO *po = out + (a.reverse ? si.len - 1 - (t + row) : t + row) * a.ot;
+                    TO *po = out + ((a.reverse ? si.len - 1 - t : t) * a.ot + (int64_t)(a.reverse ? -row : row) * a.ot);
                     if ((VEC || a.vec_o) && NT * 4 <= out_cols) {
                         TO w[NT * 4];
 #pragma unroll
                         for (int j = 0; j < NT * 4; ++j) w[j] = (TO)o[j >> 2][j & 3];
                         __builtin_memcpy(__builtin_assume_aligned(po, sizeof(TO) * NT * 4 < 16 ? sizeof(TO) * NT * 4 : 16), w, sizeof w);
-                    } else {
+                    } else if (!VEC || sizeof(T) == 4) {     // (whole pieces of 8 columns need no such edge)
 #pragma unroll
                         for (int j = 0; j < NT * 4; ++j)
                             if (j < out_cols) po[j] = (TO)o[j >> 2][j & 3];
@@ -439,45 +446,52 @@ __global__ __launch_bounds__(256, DXP <= 128 ? 2 : 1) void decay_walk_kernel(con
                 }
             }
         }
-        // E <- d^n E + Y^T (weights Z)
-        float dn = n == kChunk ? dfull : decay_power(log2d, n), lift = 1.0f;
+        // E <- d^n E + Y^T (weights Z), in units of the gain
+        float next = n == kChunk ? grown + wn : (float)n * -log2d + grown, most = 0.0f;
+        bool back = !(fabsf(next) <= 16.0f);
         if (Mma<T>::kNarrow) {
-            float most = 0.0f;
 #pragma unroll
             for (int q = 0; q < NT; ++q)
 #pragma unroll
                 for (int j = 0; j < 8; ++j) most = fmaxf(most, fabsf((float)zf[q][j]));
 #pragma unroll
             for (int s = 1; s < 64; s <<= 1) most = fmaxf(most, __shfl_xor(most, s));
-            most *= fabsf(a.u_scale);
-            // the largest term near 2^14; the weights are at most u_scale
-            int next = ex;
-            if (most > 0.0f) next = 13 - ilogbf(most);
-            next = next < -60 ? -60 : (next > 60 ? 60 : next);
-            dn = ldexpf(dn, next - ex);
-            lift = ldexpf(1.0f, next);
-            ex = next;
+            most *= fabsf(a.u_scale);      // the weights are at most u_scale
+            const float top = ldexpf(most * exp2f(next), ex);
+            back = back || top > 32768.0f || (top < 16.0f && most > 0.0f);
         }
+        if (__builtin_amdgcn_readfirstlane(back)) {
+            int e1 = 0;
+            if (Mma<T>::kNarrow) {
+                e1 = most > 0.0f ? 13 - ilogbf(most) : ex;     // the largest term near 2^14
+                e1 = e1 < -60 ? -60 : (e1 > 60 ? 60 : e1);
+            }
+            const float r = ldexpf(exp2f(-next), e1 - ex);
 #pragma unroll
-        for (int kk = 0; kk < KX; ++kk)
+            for (int kk = 0; kk < KX; ++kk)
 #pragma unroll
-            for (int r = 0; r < 2; ++r)
+                for (int r2 = 0; r2 < 2; ++r2)
 #pragma unroll
-                for (int q = 0; q < NT; ++q) E[kk][r][q] *= dn;
-        v8 zs[NT][kSplit];
+                    for (int q = 0; q < NT; ++q) E[kk][r2][q] *= r;
+            ex = e1;
+            next = 0.0f;
+        }
+        grown = next;
+        const float gain = Mma<T>::kNarrow ? ldexpf(exp2f(grown), ex) : exp2f(grown);
+        v8 zs[NT][TERMS];
         float w[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) w[j] = upd[kChunk - n + g * 8 + j];
+        for (int j = 0; j < 8; ++j) w[j] = upd[kChunk - n + g * 8 + j] * gain;
 #pragma unroll
         for (int q = 0; q < NT; ++q)
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                float rest = (float)zf[q][j] * (Mma<T>::kNarrow ? w[j] * lift : w[j]);
+                float rest = (float)zf[q][j] * w[j];
                 // one value for every use: left to itself the compiler rounds the product to fp16 once
                 // through fp32 and once fused, and the two first terms then differ at ties
-                if (kSplit > 1) asm("" : "+v"(rest));
+                if (TERMS > 1) asm("" : "+v"(rest));
 #pragma unroll
-                for (int s = 0; s < kSplit; ++s) {
+                for (int s = 0; s < TERMS; ++s) {
                     const T part = (T)rest;
                     zs[q][s][j] = part;
                     rest -= (float)part;
@@ -492,7 +506,7 @@ __global__ __launch_bounds__(256, DXP <= 128 ? 2 : 1) void decay_walk_kernel(con
 #pragma unroll
                 for (int q = 0; q < NT; ++q)
 #pragma unroll
-                    for (int s = 0; s < kSplit; ++s) E[kk][r][q] = Mma<T>::mma(yf, zs[q][s], E[kk][r][q]);
+                    for (int s = 0; s < TERMS; ++s) E[kk][r][q] = Mma<T>::mma(yf, zs[q][s], E[kk][r][q]);
             }
     };
     __syncthreads();       // the tables above
@@ -509,14 +523,14 @@ __global__ __launch_bounds__(256, DXP <= 128 ? 2 : 1) void decay_walk_kernel(con
         }
     }
 
-    const float unscale = Mma<T>::kNarrow ? ldexpf(1.0f, -ex) : 1.0f;
+    const float unscale = ldexpf(exp2f(-grown), -ex);
     float *s1 = nullptr;
     int64_t sx_ = a.s1x, sz_ = a.s1z;
     if (!OUT) {
         s1 = a.seg + ((int64_t)blockIdx.x * a.H + h) * a.DX * a.DZ;
         sx_ = a.DZ;
         sz_ = 1;
-    } else if (a.state1 && si.index + 1 == si.count) {
+    } else if (a.state1 && !a.seg) {      // segmented: the chain kernel has it
         const int64_t slot = state_slot(a.slots, a.n_slots, si.seq);
         if (slot >= 0) s1 = a.state1 + (slot * a.H + h) * (int64_t)a.DX * a.DZ;
     }
@@ -612,47 +626,55 @@ __global__ __launch_bounds__(256) void decay_group_sum_kernel(const float *src, 
     }
 }
 
-// State before each segment from the segments' own sums, in place: grid (B, H, pieces of 1024).
-static __global__ __launch_bounds__(256) void decay_chain_kernel(const DecayWalk a) {
+// State before each segment from the segments' own sums, in place, and the final state:
+// grid (B, H, pieces of 256 V values).  V = 4: Dx * Dz a multiple of 4.
+template <int V> static __global__ __launch_bounds__(256) void decay_chain_kernel(const DecayWalk a) {
+    typedef float vec __attribute__((ext_vector_type(V)));
     SegInfo si;
     if (!find_segment(a, blockIdx.x, true, si)) return;
     const int h = blockIdx.y;
-    const int64_t nst = (int64_t)a.DX * a.DZ;
-    const float dn = decay_power(a.log_decay[h] * kLog2e, a.seglen);
-    const int64_t slot = a.state0 ? state_slot(a.slots, a.n_slots, si.seq) : -1;
+    const int64_t nst = (int64_t)a.DX * a.DZ, e = (blockIdx.z * (int64_t)256 + threadIdx.x) * V;
+    if (e >= nst) return;
+    const float log2d = a.log_decay[h] * kLog2e;
+    const float dn = decay_power(log2d, a.seglen), dlast = decay_power(log2d, si.len - (si.count - 1) * a.seglen);
+    const int64_t slot = state_slot(a.slots, a.n_slots, si.seq);
+    vec run = 0.0f;
+    if (slot >= 0 && a.state0) {
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-        const int64_t e = blockIdx.z * (int64_t)1024 + u * 256 + threadIdx.x;
-        if (e >= nst) continue;
-        float run = 0.0f;
-        if (slot >= 0) {
-            const int64_t x = e / a.DZ, z = e % a.DZ;
-            run = a.state0[(slot * a.H + h) * nst + x * a.s0x + z * a.s0z];
-        }
-        float *p = a.seg + (si.first * a.H + h) * nst + e;
-        const int64_t step = a.H * nst;
-        for (int64_t s = 0; s < si.count; s += 8) {
-            float own[8];
+        for (int i = 0; i < V; ++i)
+            run[i] = a.state0[(slot * a.H + h) * nst + (e + i) / a.DZ * a.s0x + (e + i) % a.DZ * a.s0z];
+    }
+    float *p = a.seg + (si.first * a.H + h) * nst + e;
+    const int64_t step = a.H * nst;
+    constexpr int U = 8;
+    for (int64_t s = 0; s < si.count; s += U) {
+        vec own[U];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) own[j] = s + j + 1 < si.count ? p[(s + j) * step] : 0.0f;
+        for (int j = 0; j < U; ++j)
+            own[j] = s + j < si.count && (a.state1 || s + j + 1 < si.count) ? *reinterpret_cast<const vec *>(p + (s + j) * step) : (vec)0.0f;
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (s + j < si.count) {
-                    p[(s + j) * step] = run;
-                    run = dn * run + own[j];
-                }
-        }
+        for (int j = 0; j < U; ++j)
+            if (s + j < si.count) {
+                *reinterpret_cast<vec *>(p + (s + j) * step) = run;
+                run = (s + j + 1 < si.count ? dn : dlast) * run + own[j];
+            }
+    }
+    if (slot >= 0 && a.state1) {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            a.state1[(slot * a.H + h) * nst + (e + i) / a.DZ * a.s1x + (e + i) % a.DZ * a.s1z] = run[i];
     }
 }
 
 // ---- host side of one storage type ----------------------------------------
-template <typename T, typename TO, bool OUT, bool VEC> static hipError_t walk_launch(const DecayWalk &a, hipStream_t stream) {
+template <typename T, typename TO, bool OUT, bool VEC, int TERMS>
+static hipError_t walk_launch(const DecayWalk &a, hipStream_t stream) {
     const bool narrow = a.DZ <= 64;
     const dim3 grid((unsigned)a.nblk, (unsigned)a.H, (unsigned)((a.DZ + (narrow ? 63 : 127)) / (narrow ? 64 : 128)));
-#define FFTCONV_WALK(DXP)                                                                       \
-    do {                                                                                        \
-        if (narrow) decay_walk_kernel<T, TO, DXP, 1, OUT, VEC><<<grid, 256, 0, stream>>>(a);     \
-        else decay_walk_kernel<T, TO, DXP, 2, OUT, VEC><<<grid, 256, 0, stream>>>(a);            \
+#define FFTCONV_WALK(DXP)                                                                             \
+    do {                                                                                              \
+        if (narrow) decay_walk_kernel<T, TO, DXP, 1, OUT, VEC, TERMS><<<grid, 256, 0, stream>>>(a);    \
+        else decay_walk_kernel<T, TO, DXP, 2, OUT, VEC, TERMS><<<grid, 256, 0, stream>>>(a);           \
     } while (0)
     if (a.DX <= 64) FFTCONV_WALK(64);
     else if (a.DX <= 128) FFTCONV_WALK(128);
@@ -661,22 +683,30 @@ template <typename T, typename TO, bool OUT, bool VEC> static hipError_t walk_la
     return hipGetLastError();
 }
 
-template <typename T, typename TO> static hipError_t walk_dispatch(const DecayWalk &a, bool out, hipStream_t stream) {
-    if (!out) return a.vec_y && a.vec_z ? walk_launch<T, T, false, true>(a, stream) : walk_launch<T, T, false, false>(a, stream);
-    return a.vec_x && a.vec_y && a.vec_z && a.vec_o ? walk_launch<T, TO, true, true>(a, stream)
-                                                    : walk_launch<T, TO, true, false>(a, stream);
+template <typename T, typename TO> static hipError_t walk_out(const DecayWalk &a, hipStream_t stream) {
+    // Only a walk from a sequence's beginning may return its state.  The choice does not look at what was
+    // asked for, so an output's bits do not depend on the other outputs.
+    constexpr int kExact = Mma<T>::kExactTerms, kTerms = Mma<T>::kTerms;
+    if (!(a.vec_x && a.vec_y && a.vec_z && a.vec_o)) return walk_launch<T, TO, true, false, kExact>(a, stream);
+    if (!a.seg) return walk_launch<T, TO, true, true, kExact>(a, stream);
+    return walk_launch<T, TO, true, true, kTerms>(a, stream);
 }
 
 template <typename T> static hipError_t walk_typed(const DecayWalk &a, bool out_f32, hipStream_t stream) {
+    constexpr int kExact = Mma<T>::kExactTerms;
     if (a.seg) {
-        hipError_t e = walk_dispatch<T, T>(a, false, stream);
+        hipError_t e = a.vec_y && a.vec_z ? walk_launch<T, T, false, true, kExact>(a, stream)
+                                          : walk_launch<T, T, false, false, kExact>(a, stream);
         if (e != hipSuccess) return e;
         const int64_t nst = (int64_t)a.DX * a.DZ;
-        decay_chain_kernel<<<dim3((unsigned)a.B, (unsigned)a.H, (unsigned)((nst + 1023) / 1024)), 256, 0, stream>>>(a);
+        const bool quads = nst % 4 == 0;
+        const dim3 grid((unsigned)a.B, (unsigned)a.H, (unsigned)((nst + (quads ? 1023 : 255)) / (quads ? 1024 : 256)));
+        if (quads) decay_chain_kernel<4><<<grid, 256, 0, stream>>>(a);
+        else decay_chain_kernel<1><<<grid, 256, 0, stream>>>(a);
         e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    return out_f32 ? walk_dispatch<T, float>(a, true, stream) : walk_dispatch<T, T>(a, true, stream);
+    return out_f32 ? walk_out<T, float>(a, stream) : walk_out<T, T>(a, stream);
 }
 
 template <typename T> static hipError_t step_typed(const DecayStep &a, bool vec, hipStream_t stream) {

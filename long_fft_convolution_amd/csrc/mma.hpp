@@ -32,8 +32,10 @@ template <> struct Mma<_Float16> {
     static __device__ __forceinline__ f32x4 mma(v8 a, v8 b, f32x4 c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
     }
-    static constexpr int kSplit = 2;   // 2 x 11 bits hold an fp32 value to 2^-22,
-    static constexpr bool kNarrow = true;   // given a scale that keeps the second term out of the subnormals
+    // terms of the storage type that hold an fp32 value to fp32 precision (2 x 11 bits, given a scale
+    // that keeps the second term out of the subnormals), and to well below one storage rounding
+    static constexpr int kExactTerms = 2, kTerms = 2;
+    static constexpr bool kNarrow = true;   // the type's range needs that scale
 };
 template <> struct Mma<__bf16> {
     typedef __bf16 v8 __attribute__((ext_vector_type(8)));
@@ -41,7 +43,7 @@ template <> struct Mma<__bf16> {
     static __device__ __forceinline__ f32x4 mma(v8 a, v8 b, f32x4 c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
     }
-    static constexpr int kSplit = 3;   // 3 x 8 bits hold an fp32 value to 2^-24
+    static constexpr int kExactTerms = 3, kTerms = 2;   // 3 x 8 bits; 2 x 8 bits
     static constexpr bool kNarrow = false;
 };
 template <> struct Mma<float> {
@@ -52,7 +54,7 @@ template <> struct Mma<float> {
         for (int j = 0; j < 8; ++j) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[j], b[j], c, 0, 0, 0);
         return c;
     }
-    static constexpr int kSplit = 1;
+    static constexpr int kExactTerms = 1, kTerms = 1;
     static constexpr bool kNarrow = false;
 };
 

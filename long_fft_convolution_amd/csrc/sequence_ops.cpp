@@ -119,10 +119,10 @@ int64_t z_tiles(int64_t dz) { return ceil_div(dz, dz <= 64 ? 64 : 128); }
 // twice (a pass of their own sums each segment first).
 int64_t segment_tokens(int64_t B, int64_t N, int64_t T, int64_t H, int64_t dz, bool packed) {
     const int64_t per_token = H * z_tiles(dz);
-    if (!packed && B * per_token * 2 > kWalkSlots) return round_up(std::max<int64_t>(N, 1), kSegStep);
-    int64_t len = std::max(kMinSegment, ceil_div(T * per_token, kWalkSlots));
-    if (!packed && N > 0) len = ceil_div(N, ceil_div(N, len));    // equal segments
-    return round_up(len, kSegStep);
+    if (packed) return round_up(std::max(kMinSegment, ceil_div(T * per_token, kWalkSlots)), kSegStep);
+    // equal sequences: as many equal segments as all walk at once
+    const int64_t most = std::max<int64_t>(1, kWalkSlots / std::max<int64_t>(1, B * per_token));
+    return round_up(std::max(N <= kMinSegment ? std::max<int64_t>(N, 1) : kMinSegment, ceil_div(N, most)), kSegStep);
 }
 int64_t segment_count(int64_t B, int64_t N, int64_t T, int64_t seglen, bool packed) {
     return packed ? T / seglen + B : B * std::max<int64_t>(1, ceil_div(N, seglen));
