@@ -226,7 +226,7 @@ template <typename T, int DP, bool PERMUTED, bool VEC> struct ChunkSource {
                 Tile::source(i, row, slot);
                 const int col = col0 + slot * Tile::E;
                 off[i] = col < cols ? (uint32_t)(((reverse ? kChunk - 1 - row : row) * stride + col) * (int64_t)sizeof(T))
-                                    : 0x80000000u;
+                                    : kSkip;
             }
         }
     }
@@ -235,42 +235,72 @@ template <typename T, int DP, bool PERMUTED, bool VEC> struct ChunkSource {
         if constexpr (VEC) {
             const int wave = __builtin_amdgcn_readfirstlane((threadIdx.x & 255) >> 6);
             const T *first = p + (reverse ? len - t0 - kChunk : t0) * stride;
-            auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<T *>(first), (short)0, 0x7fffffff, 0x00020000);
+            const auto view = wide_view(first);
 #pragma unroll
             for (int i = 0; i < Tile::N; ++i) {
                 uint32_t o = off[i];
                 if (n < kChunk) {
                     int row, slot;
                     Tile::source(i, row, slot);
-                    if (row >= n) o = 0x80000000u;
+                    if (row >= n) o = kSkip;
                 }
                 __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                    rsrc, FFTCONV_LDS_CAST(void, tile + (i * 256 + wave * 64) * Tile::E), 16, o, 0, 0, 0);
+                    view, FFTCONV_LDS_CAST(void, tile + (i * 256 + wave * 64) * Tile::E), 16, o, 0, 0, 0);
             }
         } else {
+            const auto view = wide_view(p + (reverse ? len - t0 - kChunk : t0) * stride);
 #pragma unroll
             for (int i = 0; i < Tile::N; ++i) {
                 int row, slot;
                 Tile::source(i, row, slot);
                 const int col = col0 + slot * Tile::E;
-                const T *src = p + (reverse ? len - 1 - (t0 + row) : t0 + row) * stride + col;
+                const uint32_t at = (uint32_t)(((reverse ? kChunk - 1 - row : row) * stride + col) * (int64_t)sizeof(T));
                 T e[Tile::E];
 #pragma unroll
-                for (int j = 0; j < Tile::E; ++j) e[j] = row < n && col + j < cols ? src[j] : (T)0.0f;
+                for (int j = 0; j < Tile::E; ++j)
+                    e[j] = view_load<T>(view, row < n && col + j < cols ? at + j * (uint32_t)sizeof(T) : kSkip);
                 __builtin_memcpy(tile + (i * 256 + (threadIdx.x & 255)) * Tile::E, e, 16);
             }
         }
     }
 };
 
+// NT * 4 neighbouring outputs of a lane at byte offset off (or kSkip).  WHOLE: aligned, and all there
+// or none; else `left` of them are, written one by one unless vec and all are there.
+template <typename TO, int NT, bool WHOLE>
+__device__ __forceinline__ void put_row(__amdgpu_buffer_rsrc_t view, uint32_t off, const f32x4 *o, int vec, int left) {
+    struct Row { TO w[NT * 4]; } row;
+#pragma unroll
+    for (int j = 0; j < NT * 4; ++j) row.w[j] = (TO)o[j >> 2][j & 3];
+    const bool whole = WHOLE || (vec && NT * 4 <= left);
+    view_store(view, whole ? off : kSkip, row);
+    if (!WHOLE) {
+#pragma unroll
+        for (int j = 0; j < NT * 4; ++j)
+            view_store(view, !whole && j < left && off != kSkip ? off + j * (uint32_t)sizeof(TO) : kSkip, row.w[j]);
+    }
+}
+
+// Work item of workgroup id: ids go to the 8 XCDs in turn, so runs of set.share items are dealt to
+// one XCD, whose L2 then holds what they have in common.
+__device__ __forceinline__ void work_of(const DecaySet &set, uint32_t id, int &kind, int &zt, int &h, int64_t &blk) {
+    const uint32_t run = set.share, round = id / (8 * run), in = id % (8 * run);
+    uint32_t w = (round * 8 + in % 8) * run + in / 8;
+    kind = w % set.kinds, w /= set.kinds;
+    zt = w % set.ztiles, w /= set.ztiles;
+    h = w % set.w[0].H;
+    blk = w / set.w[0].H;
+}
+
 // Stages of tiles in LDS: the chunk in use and those on their way.  Three where two workgroups of
 // them fit a CU's 160 KB, else two; without LDS-destination loads one.
 constexpr int walk_stages(int bytes, bool vec) { return !vec ? 1 : (3 * bytes <= 78 * 1024 ? 3 : (2 * bytes <= 150 * 1024 ? 2 : 1)); }
 
-// grid: (nblk, H, z tiles); OUT = false: the segment's own sum only (y, z read), for every
+// OUT = false: the segment's own sum only (y, z read), for every
 // segment that another follows.  DXP: DX padded; NT: 16-column tiles of E per wave.
-template <typename T, typename TO, int DXP, int NT, bool OUT, bool VEC, int TERMS>
-__global__ __launch_bounds__(256, DXP <= 128 ? 2 : 1) void decay_walk_kernel(const DecayWalk a) {
+// grid: work items (see work_of)
+template <typename T, int DXP, int NT, bool OUT, bool VEC, int TERMS>
+__global__ __launch_bounds__(256, DXP <= 128 ? 2 : 1) void decay_walk_kernel(const DecaySet set) {
 #ifdef __HIP_DEVICE_COMPILE__   // the host pass, which cannot take the LDS-destination loads, needs the stub alone
     constexpr int KX = DXP / 32;          // 32-wide contraction steps over DX
     constexpr int DZT = NT * 64;          // z columns of a workgroup
@@ -288,16 +318,20 @@ __global__ __launch_bounds__(256, DXP <= 128 ? 2 : 1) void decay_walk_kernel(con
     __shared__ __attribute__((aligned(16))) float upd[2 * kChunk];   // u_scale d^(C - off - s): weight of token s in the next state
     __shared__ float row_w[kChunk];       // i_scale d^(i + off): weight of the chunk's first state in row i
 
+    int kind, h, zt;
+    int64_t blk;
+    work_of(set, blockIdx.x, kind, zt, h, blk);
+    const DecayWalk &a = set.w[kind];
     SegInfo si;
-    if (!find_segment(a, blockIdx.x, false, si)) return;
+    if (blk >= a.nblk || zt * DZT >= a.DZ || !find_segment(a, blk, false, si)) return;
     si.seq = scalar(si.seq), si.index = scalar(si.index), si.count = scalar(si.count);
     si.start = scalar(si.start), si.len = scalar(si.len);
     // the last segment's sum is wanted only for the final state
     if (!OUT && si.index + 1 >= si.count && !a.state1) return;
-    const int h = blockIdx.y, tid = threadIdx.x, lane = tid & 63;
+    const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int g = lane >> 4, c = lane & 15;
-    const int col0 = blockIdx.z * DZT;                   // first z column of the workgroup
+    const int col0 = zt * DZT;                   // first z column of the workgroup
     const int zw = wave * NT * 16;                       // this wave's columns within it
     const int64_t t_begin = si.index * a.seglen;
     const int64_t t_end = t_begin + a.seglen < si.len && si.index + 1 < si.count ? t_begin + a.seglen : si.len;
@@ -329,15 +363,16 @@ __global__ __launch_bounds__(256, DXP <= 128 ? 2 : 1) void decay_walk_kernel(con
     f32x4 E[KX][2][NT];
     {
         const float *s0 = nullptr;
-        int64_t sx_ = a.s0x, sz_ = a.s0z;
+        uint32_t sx_ = (uint32_t)a.s0x, sz_ = (uint32_t)a.s0z;
         if (a.seg && OUT) {
-            s0 = a.seg + ((int64_t)blockIdx.x * a.H + h) * a.DX * a.DZ;
-            sx_ = a.DZ;
-            sz_ = 1;
+            s0 = a.seg + (blk * a.H + h) * (int64_t)a.DX * a.DZ;
+            sx_ = (uint32_t)a.segx;
+            sz_ = (uint32_t)a.segz;
         } else if (OUT && a.state0) {
             const int64_t slot = state_slot(a.slots, a.n_slots, si.seq);
             if (slot >= 0) s0 = a.state0 + (slot * a.H + h) * (int64_t)a.DX * a.DZ;
         }
+        const auto view = wide_view(s0);
 #pragma unroll
         for (int kk = 0; kk < KX; ++kk)
 #pragma unroll
@@ -347,7 +382,7 @@ __global__ __launch_bounds__(256, DXP <= 128 ? 2 : 1) void decay_walk_kernel(con
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int dx = kk * 32 + g * 8 + r * 4 + i, dz = col0 + zcol(c, t);
-                        E[kk][r][t][i] = s0 && dx < a.DX && dz < a.DZ ? s0[dx * sx_ + dz * sz_] : 0.0f;
+                        E[kk][r][t][i] = view_load<float>(view, s0 && dx < a.DX && dz < a.DZ ? (uint32_t)(dx * sx_ + dz * sz_) * 4u : kSkip);
                     }
     }
     // decay of P in row tile rt, accumulator (r, i): d^(16 rt + c - 8 g - 4 r - i), 0 above the diagonal
@@ -364,9 +399,16 @@ __global__ __launch_bounds__(256, DXP <= 128 ? 2 : 1) void decay_walk_kernel(con
                 }
     }
     const float wn = -log2d * kChunk;   // growth of the gain's exponent over a full chunk
-    TO *out = OUT ? static_cast<TO *>(a.out) + batch * a.ob + row0 * a.ot + (h / a.go) * a.oh + col0 + zw + (NT == 2 ? g * 8 : g * 4)
-                  : nullptr;
-    const int out_cols = a.DZ - (col0 + zw + (NT == 2 ? g * 8 : g * 4));    // columns left for this lane
+    const int zl = col0 + zw + (NT == 2 ? g * 8 : g * 4);      // this lane's first column of the output
+    const int out_cols = a.DZ - zl;                             // and how many are left
+    const uint32_t out_e = a.out_f32 ? 4u : (uint32_t)sizeof(T);
+    char *out0 = static_cast<char *>(a.out) + (OUT ? (batch * a.ob + row0 * a.ot + (h / a.go) * a.oh) * out_e : 0);
+    uint32_t out_off[2];        // this lane's places in a chunk's rows
+#pragma unroll
+    for (int rt = 0; rt < 2; ++rt) {
+        const int row = rt * 16 + c;
+        out_off[rt] = out_cols > 0 ? (uint32_t)((a.reverse ? kChunk - 1 - row : row) * a.ot + zl) * out_e : kSkip;
+    }
     float grown = 0.0f;    // the accumulators hold E * 2^(grown + ex)
     int ex = 0;            // (ex: fp16 only, else 0)
 
@@ -430,19 +472,11 @@ __global__ __launch_bounds__(256, DXP <= 128 ? 2 : 1) void decay_walk_kernel(con
                     o[q] *= rw;
                     o[q] = Mma<T>::mma(zf[q], pf, o[q]);
                 }
-                const int row = rt * 16 + c;
-                if (row < n && a.out) {
-                    TO *po = out + ((a.reverse ? si.len - 1 - t : t) * a.ot + (int64_t)(a.reverse ? -row : row) * a.ot);
-                    if ((VEC || a.vec_o) && NT * 4 <= out_cols) {
-                        TO w[NT * 4];
-#pragma unroll
-                        for (int j = 0; j < NT * 4; ++j) w[j] = (TO)o[j >> 2][j & 3];
-                        __builtin_memcpy(__builtin_assume_aligned(po, sizeof(TO) * NT * 4 < 16 ? sizeof(TO) * NT * 4 : 16), w, sizeof w);
-                    } else if (!VEC || sizeof(T) == 4) {     // (whole pieces of 8 columns need no such edge)
-#pragma unroll
-                        for (int j = 0; j < NT * 4; ++j)
-                            if (j < out_cols) po[j] = (TO)o[j >> 2][j & 3];
-                    }
+                if (a.out) {
+                    const auto view = wide_view(out0 + (a.reverse ? si.len - t - kChunk : t) * a.ot * out_e);
+                    const uint32_t off = rt * 16 + c < n ? out_off[rt] : kSkip;
+                    if (a.out_f32) put_row<float, NT, VEC && sizeof(T) == 2>(view, off, o, a.vec_o, out_cols);
+                    else put_row<T, NT, VEC && sizeof(T) == 2>(view, off, o, a.vec_o, out_cols);
                 }
             }
         }
@@ -525,16 +559,17 @@ __global__ __launch_bounds__(256, DXP <= 128 ? 2 : 1) void decay_walk_kernel(con
 
     const float unscale = ldexpf(exp2f(-grown), -ex);
     float *s1 = nullptr;
-    int64_t sx_ = a.s1x, sz_ = a.s1z;
+    uint32_t sx_ = (uint32_t)a.s1x, sz_ = (uint32_t)a.s1z;
     if (!OUT) {
-        s1 = a.seg + ((int64_t)blockIdx.x * a.H + h) * a.DX * a.DZ;
-        sx_ = a.DZ;
-        sz_ = 1;
+        s1 = a.seg + (blk * a.H + h) * (int64_t)a.DX * a.DZ;
+        sx_ = (uint32_t)a.segx;
+        sz_ = (uint32_t)a.segz;
     } else if (a.state1 && !a.seg) {      // segmented: the chain kernel has it
         const int64_t slot = state_slot(a.slots, a.n_slots, si.seq);
         if (slot >= 0) s1 = a.state1 + (slot * a.H + h) * (int64_t)a.DX * a.DZ;
     }
     if (!s1) return;
+    const auto view = wide_view(s1);
 #pragma unroll
     for (int kk = 0; kk < KX; ++kk)
 #pragma unroll
@@ -544,7 +579,7 @@ __global__ __launch_bounds__(256, DXP <= 128 ? 2 : 1) void decay_walk_kernel(con
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int dx = kk * 32 + g * 8 + r * 4 + i, dz = col0 + zcol(c, t);
-                    if (dx < a.DX && dz < a.DZ) s1[dx * sx_ + dz * sz_] = E[kk][r][t][i] * unscale;
+                    view_store(view, dx < a.DX && dz < a.DZ ? (uint32_t)(dx * sx_ + dz * sz_) * 4u : kSkip, E[kk][r][t][i] * unscale);
                 }
 #endif
 }
@@ -612,28 +647,36 @@ __global__ __launch_bounds__(256) void decay_step_kernel(const DecayStep a) {
     }
 }
 
-// Gradients of shared heads: dst (tokens, Hk, D) <- sum over the group of src (tokens, H, D), fp32.
-template <typename T>
-__global__ __launch_bounds__(256) void decay_group_sum_kernel(const float *src, T *dst, int64_t B, int64_t N, int Hk,
-                                                              int group, int D, int64_t db, int64_t dt, int64_t dh) {
-    const int64_t n = B * N * Hk * D;
+// grid (blocks, tensors): a thread sums the group's values of V neighbouring columns.
+template <typename T, int V> __global__ __launch_bounds__(256) void decay_group_sum_kernel(const DecayGroupSum a) {
+    const int k = blockIdx.y;
+    if (!a.dst[k] || (V == 4) != (a.vec[k] != 0)) return;
+    typedef float vec __attribute__((ext_vector_type(V)));
+    const int D = a.D[k], Q = D / V;
+    const int64_t n = a.B * a.N * a.Hk * Q;
     for (int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
-        const int64_t d = i % D, hk = i / D % Hk, t = i / D / Hk;
-        const float *p = src + (t * Hk + hk) * group * D + d;
-        float s = 0.0f;
-        for (int j = 0; j < group; ++j) s += p[(int64_t)j * D];
-        dst[(t / N) * db + (t % N) * dt + hk * dh + d] = (T)s;
+        const int d = (int)(i % Q) * V;
+        const int64_t head = i / Q, hk = head % a.Hk, t = head / a.Hk;
+        const float *p = a.src[k] + head * a.group * D + d;
+        vec s = 0.0f;
+        for (int j = 0; j < a.group; ++j) s += *reinterpret_cast<const vec *>(p + (int64_t)j * D);
+        T *q = static_cast<T *>(a.dst[k]) + t / a.N * a.db[k] + t % a.N * a.dt[k] + hk * a.dh[k] + d;
+        T w[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) w[j] = (T)s[j];
+        __builtin_memcpy(__builtin_assume_aligned(q, V * sizeof(T)), w, sizeof w);
     }
 }
 
 // State before each segment from the segments' own sums, in place, and the final state:
-// grid (B, H, pieces of 256 V values).  V = 4: Dx * Dz a multiple of 4.
-template <int V> static __global__ __launch_bounds__(256) void decay_chain_kernel(const DecayWalk a) {
+// grid (B, H, kinds x pieces of 256 V values).  V = 4: Dx * Dz a multiple of 4.
+template <int V> static __global__ __launch_bounds__(256) void decay_chain_kernel(const DecaySet set) {
+    const DecayWalk &a = set.w[blockIdx.z % set.kinds];
     typedef float vec __attribute__((ext_vector_type(V)));
     SegInfo si;
     if (!find_segment(a, blockIdx.x, true, si)) return;
     const int h = blockIdx.y;
-    const int64_t nst = (int64_t)a.DX * a.DZ, e = (blockIdx.z * (int64_t)256 + threadIdx.x) * V;
+    const int64_t nst = (int64_t)a.DX * a.DZ, e = (blockIdx.z / set.kinds * (int64_t)256 + threadIdx.x) * V;
     if (e >= nst) return;
     const float log2d = a.log_decay[h] * kLog2e;
     const float dn = decay_power(log2d, a.seglen), dlast = decay_power(log2d, si.len - (si.count - 1) * a.seglen);
@@ -667,46 +710,53 @@ template <int V> static __global__ __launch_bounds__(256) void decay_chain_kerne
 }
 
 // ---- host side of one storage type ----------------------------------------
-template <typename T, typename TO, bool OUT, bool VEC, int TERMS>
-static hipError_t walk_launch(const DecayWalk &a, hipStream_t stream) {
-    const bool narrow = a.DZ <= 64;
-    const dim3 grid((unsigned)a.nblk, (unsigned)a.H, (unsigned)((a.DZ + (narrow ? 63 : 127)) / (narrow ? 64 : 128)));
-#define FFTCONV_WALK(DXP)                                                                             \
-    do {                                                                                              \
-        if (narrow) decay_walk_kernel<T, TO, DXP, 1, OUT, VEC, TERMS><<<grid, 256, 0, stream>>>(a);    \
-        else decay_walk_kernel<T, TO, DXP, 2, OUT, VEC, TERMS><<<grid, 256, 0, stream>>>(a);           \
-    } while (0)
-    if (a.DX <= 64) FFTCONV_WALK(64);
-    else if (a.DX <= 128) FFTCONV_WALK(128);
-    else FFTCONV_WALK(256);
-#undef FFTCONV_WALK
+template <typename T, bool OUT, bool VEC, int TERMS> static hipError_t walk_launch(const DecaySet &set, hipStream_t stream) {
+    bool narrow = true;
+    int dx = 0;
+    for (int i = 0; i < set.kinds; ++i) {
+        narrow = narrow && set.w[i].ztile == 64;
+        dx = set.w[i].DX > dx ? set.w[i].DX : dx;
+    }
+    const int64_t items = set.w[0].nblk * set.w[0].H * set.ztiles * set.kinds, round = 8 * (int64_t)set.share;
+    const unsigned grid = (unsigned)((items + round - 1) / round * round);
+    // (rows wider than 128 leave registers for 64 z columns only: decay_z_tile)
+    if (dx > 128) {
+        if (!narrow) return hipErrorInvalidValue;
+        decay_walk_kernel<T, 256, 1, OUT, VEC, TERMS><<<grid, 256, 0, stream>>>(set);
+    } else if (dx > 64) {
+        if (narrow) decay_walk_kernel<T, 128, 1, OUT, VEC, TERMS><<<grid, 256, 0, stream>>>(set);
+        else decay_walk_kernel<T, 128, 2, OUT, VEC, TERMS><<<grid, 256, 0, stream>>>(set);
+    } else {
+        if (narrow) decay_walk_kernel<T, 64, 1, OUT, VEC, TERMS><<<grid, 256, 0, stream>>>(set);
+        else decay_walk_kernel<T, 64, 2, OUT, VEC, TERMS><<<grid, 256, 0, stream>>>(set);
+    }
     return hipGetLastError();
 }
 
-template <typename T, typename TO> static hipError_t walk_out(const DecayWalk &a, hipStream_t stream) {
+template <typename T> static hipError_t walks_typed(const DecaySet &set, hipStream_t stream) {
     // Only a walk from a sequence's beginning may return its state.  The choice does not look at what was
     // asked for, so an output's bits do not depend on the other outputs.
     constexpr int kExact = Mma<T>::kExactTerms, kTerms = Mma<T>::kTerms;
-    if (!(a.vec_x && a.vec_y && a.vec_z && a.vec_o)) return walk_launch<T, TO, true, false, kExact>(a, stream);
-    if (!a.seg) return walk_launch<T, TO, true, true, kExact>(a, stream);
-    return walk_launch<T, TO, true, true, kTerms>(a, stream);
+    bool vec = true;
+    for (int i = 0; i < set.kinds; ++i) vec = vec && set.w[i].vec_x && set.w[i].vec_y && set.w[i].vec_z && set.w[i].vec_o;
+    if (!vec) return walk_launch<T, true, false, kExact>(set, stream);
+    return set.w[0].seg ? walk_launch<T, true, true, kTerms>(set, stream) : walk_launch<T, true, true, kExact>(set, stream);
 }
 
-template <typename T> static hipError_t walk_typed(const DecayWalk &a, bool out_f32, hipStream_t stream) {
+template <typename T> static hipError_t sums_typed(const DecaySet &set, hipStream_t stream) {
+    if (!set.w[0].seg) return hipSuccess;
     constexpr int kExact = Mma<T>::kExactTerms;
-    if (a.seg) {
-        hipError_t e = a.vec_y && a.vec_z ? walk_launch<T, T, false, true, kExact>(a, stream)
-                                          : walk_launch<T, T, false, false, kExact>(a, stream);
-        if (e != hipSuccess) return e;
-        const int64_t nst = (int64_t)a.DX * a.DZ;
-        const bool quads = nst % 4 == 0;
-        const dim3 grid((unsigned)a.B, (unsigned)a.H, (unsigned)((nst + (quads ? 1023 : 255)) / (quads ? 1024 : 256)));
-        if (quads) decay_chain_kernel<4><<<grid, 256, 0, stream>>>(a);
-        else decay_chain_kernel<1><<<grid, 256, 0, stream>>>(a);
-        e = hipGetLastError();
-        if (e != hipSuccess) return e;
-    }
-    return out_f32 ? walk_out<T, float>(a, stream) : walk_out<T, T>(a, stream);
+    bool vec = true;
+    for (int i = 0; i < set.kinds; ++i) vec = vec && set.w[i].vec_y && set.w[i].vec_z;
+    const hipError_t e = vec ? walk_launch<T, false, true, kExact>(set, stream) : walk_launch<T, false, false, kExact>(set, stream);
+    if (e != hipSuccess) return e;
+    const int64_t nst = (int64_t)set.w[0].DX * set.w[0].DZ;
+    const bool quads = nst % 4 == 0;
+    const unsigned pieces = (unsigned)((nst + (quads ? 1023 : 255)) / (quads ? 1024 : 256));
+    const dim3 grid((unsigned)set.w[0].B, (unsigned)set.w[0].H, pieces * set.kinds);
+    if (quads) decay_chain_kernel<4><<<grid, 256, 0, stream>>>(set);
+    else decay_chain_kernel<1><<<grid, 256, 0, stream>>>(set);
+    return hipGetLastError();
 }
 
 template <typename T> static hipError_t step_typed(const DecayStep &a, bool vec, hipStream_t stream) {
@@ -721,26 +771,23 @@ template <typename T> static hipError_t step_typed(const DecayStep &a, bool vec,
     return hipGetLastError();
 }
 
-template <typename T>
-static hipError_t group_sum_typed(const float *src, void *dst, int64_t B, int64_t N, int Hk, int group, int D,
-                                  int64_t db, int64_t dt, int64_t dh, hipStream_t stream) {
-    const int64_t n = B * N * Hk * D;
-    const int64_t blocks = (n + 255) / 256;
-    decay_group_sum_kernel<T><<<(unsigned)(blocks < 8192 ? blocks : 8192), 256, 0, stream>>>(
-        src, static_cast<T *>(dst), B, N, Hk, group, D, db, dt, dh);
+template <typename T> static hipError_t group_sum_typed(const DecayGroupSum &a, hipStream_t stream) {
+    int64_t most[2] = {0, 0};     // threads of the tensors met value by value, and four at a time
+    for (int k = 0; k < 2; ++k)
+        if (a.dst[k]) {
+            const int64_t n = a.B * a.N * a.Hk * a.D[k] / (a.vec[k] ? 4 : 1);
+            most[a.vec[k] != 0] = n > most[a.vec[k] != 0] ? n : most[a.vec[k] != 0];
+        }
+    auto grid = [](int64_t n) { return dim3((unsigned)(n / 256 < 4096 ? n / 256 + 1 : 4096), 2); };
+    if (most[1]) decay_group_sum_kernel<T, 4><<<grid(most[1]), 256, 0, stream>>>(a);
+    if (most[0]) decay_group_sum_kernel<T, 1><<<grid(most[0]), 256, 0, stream>>>(a);
     return hipGetLastError();
 }
 
-#define FFTCONV_DECAY_TYPE(NAME, T)                                                                            \
-    hipError_t launch_decay_walk_##NAME(const DecayWalk &a, bool out_f32, hipStream_t s) {                      \
-        return walk_typed<T>(a, out_f32, s);                                                                    \
-    }                                                                                                           \
-    hipError_t launch_decay_step_##NAME(const DecayStep &a, bool vec, hipStream_t s) {                          \
-        return step_typed<T>(a, vec, s);                                                                        \
-    }                                                                                                           \
-    hipError_t launch_decay_group_sum_##NAME(const float *src, void *dst, int64_t B, int64_t N, int Hk, int gr, \
-                                             int D, int64_t db, int64_t dt, int64_t dh, hipStream_t s) {        \
-        return group_sum_typed<T>(src, dst, B, N, Hk, gr, D, db, dt, dh, s);                                    \
-    }
+#define FFTCONV_DECAY_TYPE(NAME, T)                                                                                      \
+    hipError_t launch_decay_sums_##NAME(const DecaySet &set, hipStream_t s) { return sums_typed<T>(set, s); }             \
+    hipError_t launch_decay_walks_##NAME(const DecaySet &set, hipStream_t s) { return walks_typed<T>(set, s); }           \
+    hipError_t launch_decay_step_##NAME(const DecayStep &a, bool vec, hipStream_t s) { return step_typed<T>(a, vec, s); } \
+    hipError_t launch_decay_group_sum_##NAME(const DecayGroupSum &a, hipStream_t s) { return group_sum_typed<T>(a, s); }
 
 }  // namespace fftconv

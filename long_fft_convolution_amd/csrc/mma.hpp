@@ -67,4 +67,33 @@ template <> __device__ __forceinline__ Mma<float>::v8 lds_row8<float>(const floa
     return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
+// A raw buffer view at a wave-uniform p whose offsets up to 2^31 - 2 are in range; kSkip is out of
+// range, so a load there reads zero and a store there writes nothing.  Lanes that have nothing to do
+// take that offset instead of a branch: the accumulators then never live across a region that runs with
+// part of the lanes (where moving one to another register would lose the others' values).
+constexpr uint32_t kSkip = 0x80000000u;
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t wide_view(const void *p) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), (short)0, 0x7fffffff, 0x00020000);
+}
+// one value, and `bytes` bytes, at a byte offset of a view
+template <typename T> __device__ __forceinline__ T view_load(__amdgpu_buffer_rsrc_t v, uint32_t off) {
+    if constexpr (sizeof(T) == 4) return __builtin_bit_cast(T, __builtin_amdgcn_raw_buffer_load_b32(v, off, 0, 0));
+    else return __builtin_bit_cast(T, __builtin_amdgcn_raw_buffer_load_b16(v, off, 0, 0));
+}
+template <typename V> __device__ __forceinline__ void view_store(__amdgpu_buffer_rsrc_t v, uint32_t off, const V &x) {
+    if constexpr (sizeof(V) == 2) __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(unsigned short, x), v, off, 0, 0);
+    else if constexpr (sizeof(V) == 4) __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, x), v, off, 0, 0);
+    else if constexpr (sizeof(V) == 8) __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, x), v, off, 0, 0);
+    else if constexpr (sizeof(V) == 16) __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, x), v, off, 0, 0);
+    else {
+        struct Half { unsigned char b[sizeof(V) / 2]; };
+        struct Two { Half h[2]; };
+        const Two t = __builtin_bit_cast(Two, x);
+        view_store(v, off, t.h[0]);
+        view_store(v, off + (uint32_t)(sizeof(V) / 2), t.h[1]);     // kSkip + 16 is out of range, too
+    }
+}
+
 }  // namespace fftconv

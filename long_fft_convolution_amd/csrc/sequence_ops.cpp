@@ -7,6 +7,7 @@
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
+#include <initializer_list>
 
 #include "../../include/fftconv.h"
 #include "fftconv_internal.hpp"
@@ -112,16 +113,15 @@ constexpr int64_t kSegStep = 64;          // segments are whole chunks
 constexpr int64_t kMinSegment = 256;      // below this the second read of y, z costs more than it spreads
 constexpr int64_t kWalkSlots = 512;       // workgroups that walk at once: two on each of 256 CUs
 
-int64_t z_tiles(int64_t dz) { return ceil_div(dz, dz <= 64 ? 64 : 128); }
+int64_t z_tiles(int64_t dx, int64_t dz) { return ceil_div(dz, decay_z_tile(dx, dz)); }
 
-// Tokens of a segment.  A walk is serial, so the chip fills only when (sequence, head, z tile)
-// triples number about kWalkSlots; fewer are cut into segments, at the price of reading y and z
-// twice (a pass of their own sums each segment first).
-int64_t segment_tokens(int64_t B, int64_t N, int64_t T, int64_t H, int64_t dz, bool packed) {
-    const int64_t per_token = H * z_tiles(dz);
-    if (packed) return round_up(std::max(kMinSegment, ceil_div(T * per_token, kWalkSlots)), kSegStep);
+// Tokens of a segment.  A walk is serial, so the chip fills only when the walks (kinds of walk x
+// sequences x heads x z tiles) number about kWalkSlots; fewer are cut into segments, at the price of
+// reading y and z twice (a pass of their own sums each segment first).
+int64_t segment_tokens(int64_t B, int64_t N, int64_t T, int64_t walks_per_sequence, bool packed) {
+    if (packed) return round_up(std::max(kMinSegment, ceil_div(T * walks_per_sequence, kWalkSlots)), kSegStep);
     // equal sequences: as many equal segments as all walk at once
-    const int64_t most = std::max<int64_t>(1, kWalkSlots / std::max<int64_t>(1, B * per_token));
+    const int64_t most = std::max<int64_t>(1, kWalkSlots / std::max<int64_t>(1, B * walks_per_sequence));
     return round_up(std::max(N <= kMinSegment ? std::max<int64_t>(N, 1) : kMinSegment, ceil_div(N, most)), kSegStep);
 }
 int64_t segment_count(int64_t B, int64_t N, int64_t T, int64_t seglen, bool packed) {
@@ -129,23 +129,31 @@ int64_t segment_count(int64_t B, int64_t N, int64_t T, int64_t seglen, bool pack
 }
 bool segmented(int64_t N, int64_t T, int64_t seglen, bool packed) { return (packed ? T : N) > seglen; }
 
-// Bytes of the segments' states of one walk over T tokens in B sequences.
-size_t walk_bytes(int64_t B, int64_t T, int64_t H, int64_t dx, int64_t dz) {
+// Bytes of the segments' states of one set of H x dx x dz sums over T tokens in B sequences.
+size_t seg_bytes(int64_t B, int64_t T, int64_t walks_per_sequence, int64_t H, int64_t dx, int64_t dz) {
     size_t most = 0;
     for (bool packed : {false, true}) {
         // equal sequences: T = B N; a packed call may hold any lengths
         const int64_t N = packed ? T : ceil_div(T, std::max<int64_t>(B, 1));
-        const int64_t len = segment_tokens(B, N, T, H, dz, packed);
+        const int64_t len = segment_tokens(B, N, T, walks_per_sequence, packed);
         if (segmented(N, T, len, packed))
             most = std::max(most, (size_t)segment_count(B, N, T, len, packed) * H * dx * dz * sizeof(float));
     }
     return align_up(most, 256);
 }
+int64_t fwd_walks(int64_t H, int64_t Dk, int64_t Dv) { return H * z_tiles(Dk, Dv); }
+// dq, dk (Dv x Dk) and dv (Dk x Dv)
+int64_t bwd_walks(int64_t H, int64_t Dk, int64_t Dv) { return H * (2 * z_tiles(Dv, Dk) + z_tiles(Dk, Dv)); }
 
-hipError_t launch_walk(int dt, const DecayWalk &a, bool out_f32, hipStream_t s) {
-    return dt == FFTCONV_F32   ? launch_decay_walk_f32(a, out_f32, s)
-           : dt == FFTCONV_F16 ? launch_decay_walk_f16(a, out_f32, s)
-                               : launch_decay_walk_bf16(a, out_f32, s);
+hipError_t launch_sums(int dt, const DecaySet &a, hipStream_t s) {
+    return dt == FFTCONV_F32   ? launch_decay_sums_f32(a, s)
+           : dt == FFTCONV_F16 ? launch_decay_sums_f16(a, s)
+                               : launch_decay_sums_bf16(a, s);
+}
+hipError_t launch_walks(int dt, const DecaySet &a, hipStream_t s) {
+    return dt == FFTCONV_F32   ? launch_decay_walks_f32(a, s)
+           : dt == FFTCONV_F16 ? launch_decay_walks_f16(a, s)
+                               : launch_decay_walks_bf16(a, s);
 }
 
 struct DecayShape {
@@ -212,9 +220,13 @@ fftconv_status_t check_apart(const View *outs, int nout, const View *ins, int ni
     return FFTCONV_OK;
 }
 
-// whole 16-byte pieces along rows, and a chunk's rows within 31 bits of byte offset
-bool chunk_vec(const View &v) {
-    return v.vec16() && v.row % (16 / v.bytes_per) == 0 && (v.size[1] <= 1 || v.stride[1] * v.bytes_per < (int64_t(1) << 25));
+// whole 16-byte pieces along rows
+bool chunk_vec(const View &v) { return v.vec16() && v.row % (16 / v.bytes_per) == 0; }
+// The walks reach a chunk's rows by 31-bit offsets.
+fftconv_status_t check_reach(const View &v) {
+    if (v.size[1] > 1 && v.stride[1] * v.bytes_per >= (int64_t(1) << 25))
+        return fail(FFTCONV_ERR_UNSUPPORTED, "%s has a token stride of %lld elements, above 32 MiB", v.name, (long long)v.stride[1]);
+    return FFTCONV_OK;
 }
 void set_x(DecayWalk &w, const View &v, int64_t H) {
     w.x = v.p, w.xb = v.stride[0], w.xt = v.stride[1], w.xh = v.stride[2], w.gx = (int)(H / v.size[2]);
@@ -235,10 +247,31 @@ void set_out(DecayWalk &w, const View &v, int64_t H) {
     w.go = (int)(H / v.size[2]);
     w.vec_o = v.vec16();
 }
-void set_segments(DecayWalk &w, const DecayShape &s, float *seg) {
-    w.seglen = segment_tokens(s.B, s.N, s.T(), s.H, w.DZ, s.packed);
+void set_segments(DecayWalk &w, const DecayShape &s, int64_t walks_per_sequence, float *seg) {
+    w.seglen = segment_tokens(s.B, s.N, s.T(), walks_per_sequence, s.packed);
     w.nblk = segment_count(s.B, s.N, s.T(), w.seglen, s.packed);
     w.seg = segmented(s.N, s.T(), w.seglen, s.packed) ? seg : nullptr;
+}
+DecaySet make_set(std::initializer_list<const DecayWalk *> walks, int64_t group) {
+    DecaySet set{};
+    for (const DecayWalk *w : walks)
+        if (w) {
+            set.w[set.kinds++] = *w;
+            set.w[set.kinds - 1].ztile = decay_z_tile(w->DX, w->DZ);
+            set.ztiles = std::max(set.ztiles, (int)z_tiles(w->DX, w->DZ));
+        }
+    // neighbours share tensors: the walks of a head, its z tiles, and the heads of a group
+    set.share = (int)std::min<int64_t>(16, set.kinds * set.ztiles * group);
+    return set;
+}
+// the padded widths that a launch's walks must have in common
+bool same_class(const DecayWalk &a, const DecayWalk &b) {
+    auto width = [](int dx) { return dx <= 64 ? 64 : dx <= 128 ? 128 : 256; };
+    return width(a.DX) == width(b.DX) && decay_z_tile(a.DX, a.DZ) == decay_z_tile(b.DX, b.DZ);
+}
+// items of a launch, as a check that they fit a grid
+bool too_many(const DecaySet &s) {
+    return (double)s.w[0].nblk * s.w[0].H * s.ztiles * s.kinds + 8 * 16 > 2147483647.0;
 }
 
 }  // namespace
@@ -246,7 +279,7 @@ void set_segments(DecayWalk &w, const DecayShape &s, float *seg) {
 size_t fftconv_decay_fwd_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t Dk, int64_t Dv,
                                          fftconv_dtype_t dtype) {
     if (!dtype_ok(dtype) || B < 1 || T < 1 || H < 1 || Dk < 1 || Dv < 1 || Dk > kMaxHeadDim || Dv > kMaxHeadDim) return 0;
-    return walk_bytes(B, T, H, Dk, Dv);
+    return seg_bytes(B, T, fwd_walks(H, Dk, Dv), H, Dk, Dv);
 }
 
 fftconv_status_t fftconv_decay_fwd(const void *q, const void *k, const void *v, const float *log_decay, void *out,
@@ -265,6 +298,8 @@ fftconv_status_t fftconv_decay_fwd(const void *q, const void *k, const void *v, 
     for (const View *x : {&vq, &vk, &vv})
         if ((st = check_view(*x, true, false)) != FFTCONV_OK) return st;
     if ((st = check_view(vo, true, true)) != FFTCONV_OK) return st;
+    for (const View *x : {&vq, &vk, &vv, &vo})
+        if ((st = check_reach(*x)) != FFTCONV_OK) return st;
     if (!log_decay) return fail(FFTCONV_ERR_INVALID_ARGUMENT, "log_decay must be non-null");
     const int64_t states = state_slots ? n_slots : B;
     const View si = state_view("state_in", state_in, states, s), so = state_view("state_out", state_out, states, s);
@@ -299,8 +334,13 @@ fftconv_status_t fftconv_decay_fwd(const void *q, const void *k, const void *v, 
     w.B = B, w.N = N, w.H = (int)H;
     w.p_scale = scale, w.u_scale = 1.0f, w.i_scale = scale;
     w.off = 1;
-    set_segments(w, s, static_cast<float *>(workspace));
-    return hip_status("decay attention", launch_walk(dtype, w, false, stream));
+    set_segments(w, s, fwd_walks(H, Dk, Dv), static_cast<float *>(workspace));
+    w.segx = Dv, w.segz = 1;
+    const DecaySet set = make_set({&w}, H / Hk);
+    if (too_many(set)) return fail(FFTCONV_ERR_UNSUPPORTED, "B=%lld, N=%lld, H=%lld: too many sequences or tokens", (long long)B, (long long)N, (long long)H);
+    hipError_t e = launch_sums(dtype, set, stream);
+    if (e == hipSuccess) e = launch_walks(dtype, set, stream);
+    return hip_status("decay attention", e);
 }
 
 fftconv_status_t fftconv_decay_step(const void *q, const void *k, const void *v, const float *log_decay, float *state,
@@ -343,14 +383,27 @@ fftconv_status_t fftconv_decay_step(const void *q, const void *k, const void *v,
     return hip_status("decay step", e);
 }
 
-// workspace of the backward call: the walks' segment states, then fp32 gradients of the heads
-// that share a key/value head
+// workspace of the backward call: the states and the states' gradients before each segment, then fp32
+// gradients of the heads that share a key/value head
+namespace {
+struct DecayBwdLayout {
+    size_t grads, dk, dv, total;
+};
+DecayBwdLayout decay_bwd_layout(int64_t B, int64_t T, int64_t H, int64_t Hk, int64_t Dk, int64_t Dv) {
+    DecayBwdLayout l{};
+    l.grads = seg_bytes(B, T, bwd_walks(H, Dk, Dv), H, Dk, Dv);
+    l.dk = 2 * l.grads;
+    l.dv = l.dk + (H == Hk ? 0 : align_up((size_t)T * H * Dk * sizeof(float), 256));
+    l.total = l.dv + (H == Hk ? 0 : align_up((size_t)T * H * Dv * sizeof(float), 256));
+    return l;
+}
+}  // namespace
+
 size_t fftconv_decay_bwd_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t Hk, int64_t Dk, int64_t Dv,
                                          fftconv_dtype_t dtype) {
     if (!dtype_ok(dtype) || B < 1 || T < 1 || H < 1 || Hk < 1 || Dk < 1 || Dv < 1 || Dk > kMaxHeadDim || Dv > kMaxHeadDim)
         return 0;
-    const size_t walks = std::max(walk_bytes(B, T, H, Dv, Dk), walk_bytes(B, T, H, Dk, Dv));
-    return walks + (H == Hk ? 0 : align_up((size_t)T * H * std::max(Dk, Dv) * sizeof(float), 256));
+    return decay_bwd_layout(B, T, H, Hk, Dk, Dv).total;
 }
 
 fftconv_status_t fftconv_decay_bwd(const void *dout, const void *q, const void *k, const void *v,
@@ -372,6 +425,8 @@ fftconv_status_t fftconv_decay_bwd(const void *dout, const void *q, const void *
         if ((st = check_view(*x, true, false)) != FFTCONV_OK) return st;
     for (const View *x : {&gq, &gk, &gv})
         if ((st = check_view(*x, false, true)) != FFTCONV_OK) return st;
+    for (const View *x : {&vd, &vq, &vk, &vv, &gq, &gk, &gv})
+        if (x->p && (st = check_reach(*x)) != FFTCONV_OK) return st;
     if (!log_decay) return fail(FFTCONV_ERR_INVALID_ARGUMENT, "log_decay must be non-null");
     const View si = state_view("state_in", state_in, B, s), dso = state_view("dstate_out", dstate_out, B, s),
                dsi = state_view("dstate_in", dstate_in, B, s);
@@ -387,56 +442,85 @@ fftconv_status_t fftconv_decay_bwd(const void *dout, const void *q, const void *
                         raw_view("cu_seqlens", cu_seqlens, (B + 1) * 4)};
     if ((st = check_apart(outs, 5, ins, 8)) != FFTCONV_OK) return st;
 
-    const size_t walks = std::max(walk_bytes(B, std::max<int64_t>(s.T(), 1), H, Dv, Dk),
-                                  walk_bytes(B, std::max<int64_t>(s.T(), 1), H, Dk, Dv));
-    float *seg = static_cast<float *>(workspace);
-    float *part = reinterpret_cast<float *>(static_cast<char *>(workspace) + walks);
+    const DecayBwdLayout lay = decay_bwd_layout(B, s.T(), H, Hk, Dk, Dv);
+    char *base = static_cast<char *>(workspace);
+    const bool shared = H != Hk, tokens = s.T() > 0;
     DecayWalk w{};
     w.log_decay = log_decay;
     w.cu = cu_seqlens;
     w.B = B, w.N = N, w.H = (int)H;
-    // dq: x, y, z = dout, v, k forwards, state S^T
-    if (dq && s.T() > 0) {
-        DecayWalk a = w;
-        set_x(a, vd, H);
-        set_y(a, vv, H);
-        set_z(a, vk, H);
-        set_out(a, gq, H);
-        a.state0 = state_in, a.s0x = 1, a.s0z = Dv;
-        a.p_scale = scale, a.u_scale = 1.0f, a.i_scale = scale;
-        a.off = 1;
-        set_segments(a, s, seg);
-        const hipError_t e = launch_walk(dtype, a, false, stream);
-        if (e != hipSuccess) return hip_status("dq", e);
-    }
-    // dk: x, y, z = v, dout, q and dv: x, y, z = k, q, dout, from each sequence's end
-    for (int which = 0; which < 2; ++which) {
-        const View &g = which ? gv : gk;
-        const bool want_state = which == 1 && dstate_in;
-        if (!(g.p && s.T() > 0) && !want_state) continue;
-        DecayWalk a = w;
-        set_x(a, which ? vk : vv, H);
-        set_y(a, which ? vq : vd, H);
-        set_z(a, which ? vd : vq, H);
-        View o = g;
-        if (H != Hk || !g.p) o = heads_view("", g.p ? part : nullptr, s, H, g.row, nullptr), o.bytes_per = 4;
-        set_out(a, o, H);
-        a.state0 = dstate_out, a.s0x = which ? Dv : 1, a.s0z = which ? 1 : Dv;
-        if (want_state) a.state1 = dstate_in, a.s1x = Dv, a.s1z = 1;
-        a.p_scale = scale, a.u_scale = scale, a.i_scale = 1.0f;
-        a.off = 0, a.reverse = 1;
-        set_segments(a, s, seg);
-        hipError_t e = launch_walk(dtype, a, H != Hk, stream);
-        if (e == hipSuccess && H != Hk && g.p && s.T() > 0) {
-            auto sum = dtype == FFTCONV_F32   ? launch_decay_group_sum_f32
-                       : dtype == FFTCONV_F16 ? launch_decay_group_sum_f16
-                                              : launch_decay_group_sum_bf16;
-            e = sum(part, const_cast<void *>(g.p), s.packed ? 1 : B, N, (int)Hk, (int)(H / Hk), (int)g.row, g.stride[0],
-                    g.stride[1], g.stride[2], stream);
+    set_segments(w, s, bwd_walks(H, Dk, Dv), nullptr);
+    const bool cut = segmented(s.N, s.T(), w.seglen, s.packed);
+    // dq: x, y, z = dout, v, k forwards, state S^T (Dv x Dk)
+    DecayWalk q_ = w;
+    set_x(q_, vd, H);
+    set_y(q_, vv, H);
+    set_z(q_, vk, H);
+    set_out(q_, gq, H);
+    q_.state0 = state_in, q_.s0x = 1, q_.s0z = Dv;
+    q_.p_scale = scale, q_.u_scale = 1.0f, q_.i_scale = scale;
+    q_.off = 1;
+    q_.seg = cut ? reinterpret_cast<float *>(base) : nullptr, q_.segx = Dk, q_.segz = 1;
+    // dk: x, y, z = v, dout, q from each sequence's end, state G^T (Dv x Dk)
+    auto set_grad = [&](DecayWalk &g, const View &grad, size_t part) {
+        View o = grad;
+        if (shared) o = heads_view("", grad.p ? base + part : nullptr, s, H, grad.row, nullptr), o.bytes_per = 4;
+        set_out(g, o, H);
+        g.out_f32 = shared;
+        g.p_scale = scale, g.u_scale = scale, g.i_scale = 1.0f;
+        g.reverse = 1;
+        g.state0 = dstate_out;
+        g.seg = cut ? reinterpret_cast<float *>(base + lay.grads) : nullptr;
+    };
+    DecayWalk k_ = w;
+    set_x(k_, vv, H);
+    set_y(k_, vd, H);
+    set_z(k_, vq, H);
+    set_grad(k_, gk, lay.dk);
+    k_.s0x = 1, k_.s0z = Dv;
+    k_.state1 = dstate_in, k_.s1x = 1, k_.s1z = Dv;
+    k_.segx = Dk, k_.segz = 1;
+    // dv: x, y, z = k, q, dout, state G (Dk x Dv): the same sums read the other way round
+    DecayWalk v_ = w;
+    set_x(v_, vk, H);
+    set_y(v_, vq, H);
+    set_z(v_, vd, H);
+    set_grad(v_, gv, lay.dv);
+    v_.s0x = Dv, v_.s0z = 1;
+    v_.segx = 1, v_.segz = Dk;
+
+    const bool run_q = dq && tokens, run_v = dv && tokens, sum_g = (dk && tokens) || run_v || dstate_in;
+    // the state's own gradient comes from the chain of sums, or from dk's walk when there are none
+    const bool run_k = (dk && tokens) || (dstate_in && !cut);
+    const DecaySet sums = make_set({run_q ? &q_ : nullptr, sum_g ? &k_ : nullptr}, H / Hk);
+    if (too_many(make_set({&q_, &k_, &v_}, H / Hk)))
+        return fail(FFTCONV_ERR_UNSUPPORTED, "B=%lld, N=%lld, H=%lld: too many sequences or tokens", (long long)B,
+                    (long long)N, (long long)H);
+    hipError_t e = hipSuccess;
+    if (sums.kinds) e = launch_sums(dtype, sums, stream);
+    const bool together = same_class(k_, v_);
+    const DecaySet first = make_set({run_k ? &k_ : nullptr, run_v && together ? &v_ : nullptr, run_q ? &q_ : nullptr}, H / Hk);
+    if (e == hipSuccess && first.kinds) e = launch_walks(dtype, first, stream);
+    if (e == hipSuccess && run_v && !together) e = launch_walks(dtype, make_set({&v_}, H / Hk), stream);
+    if (e == hipSuccess && shared && tokens && (dk || dv)) {
+        DecayGroupSum g{};
+        const View *grads[] = {&gk, &gv};
+        const size_t parts[] = {lay.dk, lay.dv};
+        for (int i = 0; i < 2; ++i) {
+            const View &o = *grads[i];
+            g.src[i] = reinterpret_cast<const float *>(base + parts[i]);
+            g.dst[i] = const_cast<void *>(o.p);
+            g.D[i] = (int)o.row;
+            g.db[i] = o.stride[0], g.dt[i] = o.stride[1], g.dh[i] = o.stride[2];
+            g.vec[i] = o.row % 4 == 0 && aligned(o.p, 4 * o.bytes_per) && o.stride[0] % 4 == 0 && o.stride[1] % 4 == 0 &&
+                       o.stride[2] % 4 == 0;
         }
-        if (e != hipSuccess) return hip_status(which ? "dv" : "dk", e);
+        g.B = s.packed ? 1 : B, g.N = N, g.Hk = (int)Hk, g.group = (int)(H / Hk);
+        e = dtype == FFTCONV_F32   ? launch_decay_group_sum_f32(g, stream)
+            : dtype == FFTCONV_F16 ? launch_decay_group_sum_f16(g, stream)
+                                   : launch_decay_group_sum_bf16(g, stream);
     }
-    return ok();
+    return hip_status("decay attention gradients", e);
 }
 
 // ---- linear product -----------------------------------------------------------

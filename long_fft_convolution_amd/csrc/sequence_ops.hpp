@@ -8,6 +8,10 @@
 
 namespace fftconv {
 
+// z columns of a workgroup's state: 128 (two 16-column tiles for each of four waves), 64 where no more are
+// needed or the state's rows leave no registers for more.
+inline int decay_z_tile(int64_t dx, int64_t dz) { return dz <= 64 || dx > 128 ? 64 : 128; }
+
 // One walk over sequences: the prompt form, or one gradient (decay_kernels.hpp).
 struct DecayWalk {
     const void *x, *y, *z;
@@ -23,12 +27,25 @@ struct DecayWalk {
     const int32_t *cu;               // packed sequences' bounds (B + 1) or null
     int64_t B, N;                    // N: tokens of each sequence, or of all when packed
     int H, DX, DZ;
+    int ztile;                       // z columns of a workgroup
     int64_t seglen;                  // tokens per segment, a multiple of the chunk
     int64_t nblk;                    // segments launched (an upper bound when packed)
-    float *seg;                      // state before each segment (nblk, H, DX, DZ), null when one segment each
+    float *seg;                      // state before each segment (nblk, H) matrices, null when one segment each
+    int64_t segx, segz;              // their strides along DX and DZ
     float p_scale, u_scale, i_scale;
     int off, reverse;
     int vec_x, vec_y, vec_z, vec_o;  // 16-byte access allowed
+    int out_f32;                     // out is fp32 (a part of a sum over heads), else the storage type
+};
+
+// Walks that one launch runs side by side: they have the same sequences, segments and H, and the same
+// padded widths.  Work is dealt to the chip in runs of `share` neighbours (walk fastest, then z tile,
+// head, segment), which read the same tensors and land on one XCD.
+struct DecaySet {
+    DecayWalk w[3];
+    int kinds;       // walks in use
+    int ztiles;      // z tiles of a walk (of the widest)
+    int share;
 };
 
 // One single-token step (decay_kernels.hpp).
@@ -42,6 +59,16 @@ struct DecayStep {
     int64_t n_slots, B;
     int H, group, Dk, Dv;
     float scale;
+};
+
+// Gradients of shared heads: dst (tokens, Hk, D) <- sum over each group of src (tokens, H, D), fp32.
+struct DecayGroupSum {
+    const float *src[2];
+    void *dst[2];                    // up to two tensors; null: none
+    int D[2], vec[2];                // vec: four values at a time
+    int64_t db[2], dt[2], dh[2];     // strides of dst
+    int64_t B, N;
+    int Hk, group;
 };
 
 enum LinearAct : int { ACT_NONE = 0, ACT_RELU = 1, ACT_GELU = 2, ACT_GELU_TANH = 3, ACT_SILU = 4 };
@@ -76,24 +103,27 @@ struct LinearDz {
     int64_t rows;      // rows of a slab
 };
 
-hipError_t launch_decay_walk_f16(const DecayWalk &a, bool out_f32, hipStream_t stream);
+// sums of segments and their chain (nothing when the walks are not segmented), then the walks
+hipError_t launch_decay_sums_f16(const DecaySet &s, hipStream_t stream);
+hipError_t launch_decay_walks_f16(const DecaySet &s, hipStream_t stream);
 hipError_t launch_decay_step_f16(const DecayStep &a, bool vec, hipStream_t stream);
-hipError_t launch_decay_group_sum_f16(const float *src, void *dst, int64_t B, int64_t N, int Hk, int group, int D,
-                                      int64_t db, int64_t dt, int64_t dh, hipStream_t stream);
+hipError_t launch_decay_group_sum_f16(const DecayGroupSum &a, hipStream_t stream);
 hipError_t launch_linear_gemm_f16(const LinearGemm &a, int layout, int tile, bool vec, hipStream_t stream);
 hipError_t launch_linear_rows_f16(const LinearGemm &a, bool vec, hipStream_t stream);
 hipError_t launch_linear_dz_f16(const LinearDz &a, int64_t slabs, void *dbias, hipStream_t stream);
-hipError_t launch_decay_walk_bf16(const DecayWalk &a, bool out_f32, hipStream_t stream);
+// sums of segments and their chain (nothing when the walks are not segmented), then the walks
+hipError_t launch_decay_sums_bf16(const DecaySet &s, hipStream_t stream);
+hipError_t launch_decay_walks_bf16(const DecaySet &s, hipStream_t stream);
 hipError_t launch_decay_step_bf16(const DecayStep &a, bool vec, hipStream_t stream);
-hipError_t launch_decay_group_sum_bf16(const float *src, void *dst, int64_t B, int64_t N, int Hk, int group, int D,
-                                      int64_t db, int64_t dt, int64_t dh, hipStream_t stream);
+hipError_t launch_decay_group_sum_bf16(const DecayGroupSum &a, hipStream_t stream);
 hipError_t launch_linear_gemm_bf16(const LinearGemm &a, int layout, int tile, bool vec, hipStream_t stream);
 hipError_t launch_linear_rows_bf16(const LinearGemm &a, bool vec, hipStream_t stream);
 hipError_t launch_linear_dz_bf16(const LinearDz &a, int64_t slabs, void *dbias, hipStream_t stream);
-hipError_t launch_decay_walk_f32(const DecayWalk &a, bool out_f32, hipStream_t stream);
+// sums of segments and their chain (nothing when the walks are not segmented), then the walks
+hipError_t launch_decay_sums_f32(const DecaySet &s, hipStream_t stream);
+hipError_t launch_decay_walks_f32(const DecaySet &s, hipStream_t stream);
 hipError_t launch_decay_step_f32(const DecayStep &a, bool vec, hipStream_t stream);
-hipError_t launch_decay_group_sum_f32(const float *src, void *dst, int64_t B, int64_t N, int Hk, int group, int D,
-                                      int64_t db, int64_t dt, int64_t dh, hipStream_t stream);
+hipError_t launch_decay_group_sum_f32(const DecayGroupSum &a, hipStream_t stream);
 hipError_t launch_linear_gemm_f32(const LinearGemm &a, int layout, int tile, bool vec, hipStream_t stream);
 hipError_t launch_linear_rows_f32(const LinearGemm &a, bool vec, hipStream_t stream);
 hipError_t launch_linear_dz_f32(const LinearDz &a, int64_t slabs, void *dbias, hipStream_t stream);
