@@ -28,31 +28,45 @@
 
 namespace fftconv {
 
+// exp and reciprocal of the hardware (each within an ulp or two of fp32, against results rounded to
+// 16 bits, or to 24 after sums of K terms)
+__device__ __forceinline__ float fast_exp(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504088896340736f); }
+__device__ __forceinline__ float fast_rcp(float x) { return __builtin_amdgcn_rcpf(x); }
+// 1 / (1 + exp(-x)); 0 and 1 at the far ends
+__device__ __forceinline__ float logistic(float x) { return fast_rcp(1.0f + fast_exp(-x)); }
+// Phi(z), the normal distribution's integral, from e = exp(-z^2 / 2): erfc by Abramowitz and Stegun,
+// Handbook of Mathematical Functions, 7.1.26, |error| <= 1.5e-7.
+__device__ __forceinline__ float normal_cdf(float z, float e) {
+    const float t = fast_rcp(fmaf(0.3275911f * 0.70710678118654752440f, fabsf(z), 1.0f));
+    const float p = t * fmaf(t, fmaf(t, fmaf(t, fmaf(t, 1.061405429f, -1.453152027f), 1.421413741f), -0.284496736f), 0.254829592f);
+    const float tail = 0.5f * p * e;                // Phi(-|z|)
+    return z < 0.0f ? tail : 1.0f - tail;
+}
+// z (1 + tanh u) / 2 = z logistic(2 u), u = sqrt(2 / pi) (z + 0.044715 z^3)
+constexpr float kTanh2 = 2.0f * 0.79788456080286535588f;
 __device__ __forceinline__ float act_value(float z, int act) {
     switch (act) {
     case ACT_RELU: return z > 0.0f ? z : (z != z ? z : 0.0f);
-    case ACT_GELU: return 0.5f * z * (1.0f + erff(z * 0.70710678118654752440f));
-    case ACT_GELU_TANH: return 0.5f * z * (1.0f + tanhf(0.79788456080286535588f * (z + 0.044715f * z * z * z)));
-    case ACT_SILU: return z / (1.0f + __expf(-z));
+    case ACT_GELU: return z * normal_cdf(z, fast_exp(-0.5f * z * z));
+    case ACT_GELU_TANH: return z * logistic(kTanh2 * z * fmaf(0.044715f * z, z, 1.0f));
+    case ACT_SILU: return z * logistic(z);
     default: return z;
     }
 }
 __device__ __forceinline__ float act_slope(float z, int act) {
     switch (act) {
     case ACT_RELU: return z > 0.0f ? 1.0f : 0.0f;
-    case ACT_GELU:
-        return 0.5f * (1.0f + erff(z * 0.70710678118654752440f)) + z * __expf(-0.5f * z * z) * 0.39894228040143267794f;
+    case ACT_GELU: {
+        const float e = fast_exp(-0.5f * z * z);
+        return normal_cdf(z, e) + (e == 0.0f ? 0.0f : z * e * 0.39894228040143267794f);
+    }
     case ACT_GELU_TANH: {
-        const float t = tanhf(0.79788456080286535588f * (z + 0.044715f * z * z * z));
-        const float u = z * z;
-        // (1 - t^2) vanishes before the factor overflows
-        const float s = 1.0f - t * t;
-        return 0.5f * (1.0f + t) + (s == 0.0f ? 0.0f : 0.5f * z * s * 0.79788456080286535588f * (1.0f + 0.134145f * u));
+        const float u = z * z, p = logistic(kTanh2 * z * fmaf(0.044715f, u, 1.0f)), n = p * (1.0f - p);
+        return p + (n == 0.0f ? 0.0f : z * n * kTanh2 * fmaf(0.134145f, u, 1.0f));   // n vanishes first
     }
     case ACT_SILU: {
-        const float p = 1.0f / (1.0f + __expf(-z));
-        const float n = 1.0f - p;
-        return p * (1.0f + (n == 0.0f ? 0.0f : z * n));
+        const float p = logistic(z), n = p * (1.0f - p);
+        return p + (n == 0.0f ? 0.0f : z * n);
     }
     default: return 1.0f;
     }
@@ -409,39 +423,78 @@ __global__ __launch_bounds__(256) void linear_rows_kernel(const LinearGemm a) {
     }
 }
 
-// grid of the dz kernel: (columns / 256, slabs); thread: one column over the slab's rows.
-template <typename T> __global__ __launch_bounds__(256) void linear_dz_kernel(const LinearDz a) {
-    const int64_t n = blockIdx.x * (int64_t)256 + threadIdx.x;
+// dz and the column sums of slabs of rows.  grid: (columns / (32 V), slabs); thread: V neighbouring
+// columns of every eighth row of the slab; the eight rows' sums are joined in LDS.
+template <typename T, int V> __global__ __launch_bounds__(256) void linear_dz_kernel(const LinearDz a) {
+    constexpr int U = 4;
+    __shared__ float part[8][32 * V];
+    const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
+    const int64_t n = (blockIdx.x * (int64_t)32 + tx) * V;
     const int64_t m0 = blockIdx.y * a.rows, m1 = m0 + a.rows < a.M ? m0 + a.rows : a.M;
-    const bool in = n < a.N;
-    if (n >= (a.dz ? a.ldz : a.N)) return;
-    const T *po = static_cast<const T *>(a.dout), *pp = static_cast<const T *>(a.pre);
-    T *pz = static_cast<T *>(a.dz);
-    float sum = 0.0f;
-    for (int64_t m = m0; m < m1; m += 8) {
-        float d[8], z[8];
+    const T *po = static_cast<const T *>(a.dout) + n, *pp = static_cast<const T *>(a.pre) + n;
+    T *pz = static_cast<T *>(a.dz) + n;
+    struct Row { T v[V]; };
+    float sum[V];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-            const bool ok = in && m + u < m1;
-            d[u] = ok ? (float)po[(m + u) * a.ldo + n] : 0.0f;
-            z[u] = ok && a.act != ACT_NONE ? (float)pp[(m + u) * a.ldp + n] : 0.0f;
-        }
+    for (int j = 0; j < V; ++j) sum[j] = 0.0f;
+    const bool in = n < a.N, pad = a.dz && n < a.ldz;      // (V > 1: N is a multiple of V)
+    if (in || pad)
+        for (int64_t m = m0 + ty; m < m1; m += 8 * U) {
+            Row d[U], z[U];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-            if (a.act != ACT_NONE) d[u] *= act_slope(z[u], a.act);
-            sum += d[u];
-            if (pz && m + u < m1) pz[(m + u) * a.ldz + n] = (T)d[u];
+            for (int u = 0; u < U; ++u)
+                if (in && m + u * 8 < m1) {
+                    __builtin_memcpy(&d[u], __builtin_assume_aligned(po + (m + u * 8) * a.ldo, V * sizeof(T)), sizeof(Row));
+                    if (a.act != ACT_NONE)
+                        __builtin_memcpy(&z[u], __builtin_assume_aligned(pp + (m + u * 8) * a.ldp, V * sizeof(T)), sizeof(Row));
+                } else {
+#pragma unroll
+                    for (int j = 0; j < V; ++j) d[u].v[j] = z[u].v[j] = (T)0.0f;
+                }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (m + u * 8 >= m1) continue;
+                Row w;
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    const float f = (float)d[u].v[j] * (a.act != ACT_NONE ? act_slope((float)z[u].v[j], a.act) : 1.0f);
+                    sum[j] += f;
+                    w.v[j] = (T)f;
+                }
+                if (a.dz) __builtin_memcpy(__builtin_assume_aligned(pz + (m + u * 8) * a.ldz, V * sizeof(T)), &w, sizeof(Row));
+            }
         }
+    if (!a.colsum) return;
+#pragma unroll
+    for (int j = 0; j < V; ++j) part[ty][tx * V + j] = sum[j];
+    __syncthreads();
+    for (int i = threadIdx.x; i < 32 * V; i += 256) {
+        const int64_t col = blockIdx.x * (int64_t)(32 * V) + i;
+        float s = 0.0f;
+#pragma unroll
+        for (int r = 0; r < 8; ++r) s += part[r][i];
+        if (col < a.N) a.colsum[blockIdx.y * a.N + col] = s;
     }
-    if (a.colsum && in) a.colsum[blockIdx.y * a.N + n] = sum;
 }
+// sums of the slabs' sums: 16 columns x 16 shares of the slabs a workgroup
 template <typename T>
 __global__ __launch_bounds__(256) void linear_colsum_kernel(const float *colsum, int64_t slabs, int64_t N, T *dbias) {
-    const int64_t n = blockIdx.x * (int64_t)256 + threadIdx.x;
-    if (n >= N) return;
+    __shared__ float part[16][17];
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    const int64_t n = blockIdx.x * (int64_t)16 + tx;
     float s = 0.0f;
-    for (int64_t i = 0; i < slabs; ++i) s += colsum[i * N + n];
-    dbias[n] = (T)s;
+    if (n < N) {
+#pragma unroll 8
+        for (int64_t i = ty; i < slabs; i += 16) s += colsum[i * N + n];
+    }
+    part[ty][tx] = s;
+    __syncthreads();
+    if (ty == 0 && n < N) {
+        float t = 0.0f;
+#pragma unroll
+        for (int r = 0; r < 16; ++r) t += part[r][tx];
+        dbias[n] = (T)t;
+    }
 }
 
 // ---- host side of one storage type ----------------------------------------
@@ -490,11 +543,13 @@ template <typename T> static hipError_t rows_typed(const LinearGemm &a, bool vec
 
 template <typename T>
 static hipError_t dz_typed(const LinearDz &a, int64_t slabs, void *dbias, hipStream_t stream) {
+    constexpr int V = 16 / (int)sizeof(T);
     const int64_t cols = a.dz ? a.ldz : a.N;
-    linear_dz_kernel<T><<<dim3((unsigned)((cols + 255) / 256), (unsigned)slabs), 256, 0, stream>>>(a);
+    if (a.vec) linear_dz_kernel<T, V><<<dim3((unsigned)((cols + 32 * V - 1) / (32 * V)), (unsigned)slabs), 256, 0, stream>>>(a);
+    else linear_dz_kernel<T, 1><<<dim3((unsigned)((cols + 31) / 32), (unsigned)slabs), 256, 0, stream>>>(a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || !a.colsum) return e;
-    linear_colsum_kernel<T><<<(unsigned)((a.N + 255) / 256), 256, 0, stream>>>(a.colsum, slabs, a.N, static_cast<T *>(dbias));
+    linear_colsum_kernel<T><<<(unsigned)((a.N + 15) / 16), 256, 0, stream>>>(a.colsum, slabs, a.N, static_cast<T *>(dbias));
     return hipGetLastError();
 }
 

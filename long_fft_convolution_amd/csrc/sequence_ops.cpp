@@ -654,9 +654,10 @@ struct LinearBwdLayout {
 LinearBwdLayout linear_bwd_layout(int64_t M, int64_t N, int64_t K, int dt) {
     LinearBwdLayout l{};
     l.ldz = round_up(N, 16 / elem_bytes(dt));
-    // enough slabs to fill the chip, few enough that their sums are cheap to join
+    // slabs of rows: enough workgroups (of 256 columns) to fill the chip eight times over, few enough
+    // that their sums are cheap to join
     l.slabs = std::max<int64_t>(1, std::min<int64_t>(ceil_div(M, 32), ceil_div(2048, ceil_div(N, 256) + 1)));
-    l.rows = std::max<int64_t>(1, ceil_div(M, l.slabs));
+    l.rows = round_up(std::max<int64_t>(1, ceil_div(M, l.slabs)), 8);
     l.slabs = std::max<int64_t>(1, ceil_div(M, l.rows));
     l.colsum = align_up((size_t)M * l.ldz * elem_bytes(dt), 256);
     l.part = l.colsum + align_up((size_t)l.slabs * N * sizeof(float), 256);
@@ -702,6 +703,7 @@ fftconv_status_t fftconv_linear_bwd(const void *dout, const void *x, const void 
     z.dz = own_dz ? base : nullptr, z.ldz = l.ldz;
     z.colsum = dbias ? reinterpret_cast<float *>(base + l.colsum) : nullptr;
     z.rows = l.rows;
+    z.vec = pieces(vd) && (!need_pre || pieces(vp));
     hipError_t e = hipSuccess;
     if ((own_dz && M > 0 && N > 0) || (dbias && N > 0)) {
         e = dtype == FFTCONV_F32   ? launch_linear_dz_f32(z, l.slabs, dbias, stream)

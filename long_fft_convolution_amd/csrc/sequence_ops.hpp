@@ -101,6 +101,7 @@ struct LinearDz {
     int64_t ldz;
     float *colsum;     // slabs x N, null: no bias gradient
     int64_t rows;      // rows of a slab
+    int vec;           // rows of whole 16-byte pieces
 };
 
 // sums of segments and their chain (nothing when the walks are not segmented), then the walks
