@@ -235,7 +235,6 @@ template <typename T, int DP, bool PERMUTED, bool VEC> struct ChunkSource {
         if constexpr (VEC) {
             const int wave = __builtin_amdgcn_readfirstlane((threadIdx.x & 255) >> 6);
             const T *first = p + (reverse ? len - t0 - kChunk : t0) * stride;
-            const auto view = wide_view(first);
 #pragma unroll
             for (int i = 0; i < Tile::N; ++i) {
                 uint32_t o = off[i];
@@ -244,8 +243,7 @@ template <typename T, int DP, bool PERMUTED, bool VEC> struct ChunkSource {
                     Tile::source(i, row, slot);
                     if (row >= n) o = kSkip;
                 }
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                    view, FFTCONV_LDS_CAST(void, tile + (i * 256 + wave * 64) * Tile::E), 16, o, 0, 0, 0);
+                lds_load16(first, tile + (i * 256 + wave * 64) * Tile::E, o);
             }
         } else {
             const auto view = wide_view(p + (reverse ? len - t0 - kChunk : t0) * stride);
@@ -301,7 +299,7 @@ constexpr int walk_stages(int bytes, bool vec) { return !vec ? 1 : (3 * bytes <=
 // grid: work items (see work_of)
 template <typename T, int DXP, int NT, bool OUT, bool VEC, int TERMS>
 __global__ __launch_bounds__(256, DXP <= 128 ? 2 : 1) void decay_walk_kernel(const DecaySet set) {
-#ifdef __HIP_DEVICE_COMPILE__   // the host pass, which cannot take the LDS-destination loads, needs the stub alone
+#ifdef __HIP_DEVICE_COMPILE__   // the host pass, which cannot take the scalar operands, needs the stub alone
     constexpr int KX = DXP / 32;          // 32-wide contraction steps over DX
     constexpr int DZT = NT * 64;          // z columns of a workgroup
     using TX = ChunkTile<T, DXP, false>;
@@ -311,7 +309,6 @@ __global__ __launch_bounds__(256, DXP <= 128 ? 2 : 1) void decay_walk_kernel(con
     constexpr int kBytes = ((OUT ? 2 : 1) * TY::VALUES + TZ::VALUES) * (int)sizeof(T);
     constexpr int S = walk_stages(kBytes, VEC);
     constexpr int kLoads = (OUT ? 2 : 1) * TY::N + TZ::N;
-    // stages as separate arrays: loads into one are then known not to alias reads of another
     __shared__ __attribute__((aligned(128))) T x0[OUT ? TX::VALUES : 8], y0[TY::VALUES], z0[TZ::VALUES];
     __shared__ __attribute__((aligned(128))) T x1[OUT && S > 1 ? TX::VALUES : 8], y1[S > 1 ? TY::VALUES : 8], z1[S > 1 ? TZ::VALUES : 8];
     __shared__ __attribute__((aligned(128))) T x2[OUT && S > 2 ? TX::VALUES : 8], y2[S > 2 ? TY::VALUES : 8], z2[S > 2 ? TZ::VALUES : 8];
@@ -422,11 +419,8 @@ __global__ __launch_bounds__(256, DXP <= 128 ? 2 : 1) void decay_walk_kernel(con
             // this chunk's loads are the oldest; with three stages the next chunk's, if there is one,
             // may still travel (vmcnt retires in order).  The wait on LDS reads keeps every wave's
             // reads of the freed stage before the loads into it.
-            asm volatile("" ::: "memory");
-            if (S == 3 && t + kChunk < t_end) __builtin_amdgcn_s_waitcnt((kLoads & 15) | 0x70 | (kLoads >> 4) << 14);
-            else __builtin_amdgcn_s_waitcnt(0x70);
-            __builtin_amdgcn_s_barrier();
-            asm volatile("" ::: "memory");
+            if (S == 3 && t + kChunk < t_end) wait_loads_and_barrier<kLoads>();
+            else wait_loads_and_barrier<0>();
             if (t + (S - 1) * kChunk < t_end) bring(t + (S - 1) * kChunk, nx, ny, nz);
         }
         const int n = t_end - t < kChunk ? (int)(t_end - t) : kChunk;

@@ -7,19 +7,22 @@
 //     out: A = x, B = W, both contiguous along k;
 //     dx:  A = dz, B(n, k) = W[k][n], contiguous along n;
 //     dW:  A(m, k) = dz[k][m], B(n, k) = x[k][n], both contiguous along the tile.
-// A workgroup computes a BM x BN tile over K steps of 128 bytes; tiles of both
+// A workgroup computes a BM x BN tile over K steps of 32.  Tiles of both
 // operands stream from HBM straight into LDS (buffer loads with an LDS
 // destination, 16 bytes a lane, zero past the operand's edge by the buffer
-// unit's range check), two stages deep, so the step being multiplied hides
-// the next one's loads and no register holds them.  The destination of such a
-// load is linear in the lane, so the bank swizzle permutes the source: lane
-// l fetches the 16 bytes that belong at its place.
+// unit's range check) through a ring of S stages, so S - 1 steps of loads are
+// on their way and no register holds them.  Fragments are read from LDS half
+// a step ahead of the products that take them: the second half of a wave's
+// rows under the products of the first, the next step's columns and first half
+// under those of the second.  The destination of an LDS load is linear in the
+// lane, so the bank swizzle permutes the source: lane l fetches the 16 bytes
+// that belong at its place.
 //
-// An operand contiguous along k lies in LDS as rows of 128 bytes, its eight
-// 16-byte slots exchanged by s ^ (row & 7); one contiguous along the tile as k
-// rows of the tile's width, read with the transposing LDS read (16-bit types;
-// 32-byte granules exchanged by (k & 3) + 4 ((k >> 3) & 1)) or value by value
-// (fp32; 64-byte granules exchanged by (k >> 3) & 3).  The product is taken as
+// An operand contiguous along k lies in LDS as rows of 32 values, its 16-byte
+// slots exchanged so that one slot of 16 neighbouring rows covers all banks;
+// one contiguous along the tile as k rows of the tile's width, read with the
+// transposing LDS read (16-bit types; 32-byte granules exchanged by k) or value
+// by value (fp32; 64-byte granules exchanged by k / 8).  The product is taken as
 // B A (rows n, columns m), so a lane holds four neighbouring n of one row.
 #pragma once
 
@@ -121,16 +124,17 @@ __device__ __forceinline__ void linear_epilogue(const LinearGemm &a, int64_t m, 
     store_quad(static_cast<T *>(a.C) + m * a.ldc + n, left, a.vec_c, f);
 }
 
-// One operand's tile: R rows (of m or n) by BK of k.  KC: contiguous along k.
+// One operand's tile: R rows (of m or n) by 32 of k.  KC: contiguous along k.
+constexpr int kStepK = 32;
 template <typename T, int R, int NW, bool KC> struct OperandTile {
     static constexpr int E = 16 / (int)sizeof(T);
-    static constexpr int BK = 128 / (int)sizeof(T);
-    static constexpr int PR = KC ? BK / E : R / E;          // 16-byte pieces of an LDS row
-    static constexpr int PIECES = R * BK / E;
-    static constexpr int N = PIECES / (64 * NW);            // loads of a lane
-    static constexpr int ROWLEN = KC ? BK : R;              // values of an LDS row
-    static_assert(PIECES % (64 * NW) == 0, "whole loads");
+    static constexpr int PR = KC ? kStepK / E : R / E;      // 16-byte pieces of an LDS row
+    static constexpr int VALUES = R * kStepK;
+    static constexpr int N = VALUES / E / (64 * NW);        // loads of a lane
+    static_assert(VALUES / E % (64 * NW) == 0, "whole loads");
 
+    // exchange of the slots of a row of k values: 4 (16-bit) or 8 (fp32) slots, 4 or 2 rows to the banks' 256 bytes
+    static __device__ __forceinline__ int turn(int row) { return PR == 4 ? (row >> 2) & 3 : row & 7; }
     // exchange of the 32-byte granules of a 16-bit tile's k rows: the eight rows k = 8 g + r (g < 2, r < 4)
     // that one half of a transposing read meets lie in eight different granules of the banks' 256 bytes
     // (tiles of 64 have rows of 128 bytes, two of which share a period)
@@ -138,10 +142,11 @@ template <typename T, int R, int NW, bool KC> struct OperandTile {
         return R >= 128 ? (k & 3) | ((k >> 1) & 4) : ((k >> 1) & 1) | ((k >> 2) & 2);
     }
     // LDS piece p holds source piece (row, slot)
-    static __device__ __forceinline__ void source(int p, int &row, int &slot) {
+    static __device__ __forceinline__ void source(int i, int &row, int &slot) {
+        const int p = i * 64 * NW + (int)threadIdx.x;
         row = p / PR;
         const int s = p % PR;
-        if (KC) slot = s ^ (row & 7);
+        if (KC) slot = s ^ turn(row);
         else if (sizeof(T) == 2) slot = (s & ~15) | ((((s >> 1) & 7) ^ granule(row)) << 1) | (s & 1);
         else slot = (s & ~15) | ((((s >> 2) & 3) ^ ((row >> 3) & 3)) << 2) | (s & 3);
     }
@@ -149,42 +154,39 @@ template <typename T, int R, int NW, bool KC> struct OperandTile {
     uint32_t off[N];    // byte offset of each load from the tile's origin at k = 0
     // rows: how many of the tile's R rows exist (rounded up to pieces along the tile)
     __device__ __forceinline__ void prepare(int64_t ld, int64_t rows) {
-        const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             int row, slot;
-            source((i * NW + wave) * 64 + lane, row, slot);
+            source(i, row, slot);
             const bool in = KC ? row < rows : slot * E < rows;
-            off[i] = in ? (uint32_t)(row * ld * (int64_t)sizeof(T)) + slot * 16 : 0x80000000u;
+            off[i] = in ? (uint32_t)(row * ld * (int64_t)sizeof(T)) + slot * 16 : kSkip;
         }
     }
     // origin: the tile's first row at the step's first k; kleft: k values left in this step
     // (pieces that begin past it read zero)
     __device__ __forceinline__ void issue(const T *origin, T *tile, int kleft) const {
         // the buffer view and the LDS place are scalar operands: the wave index as one
-        const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-        auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<T *>(origin), (short)0, 0x7fffffff, 0x00020000);
-        auto place = [&](int i) { return FFTCONV_LDS_CAST(void, tile + (i * NW + wave) * 64 * E); };
-        if (kleft >= BK) {
+        const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        auto place = [&](int i) { return tile + (i * NW + wave) * 64 * E; };
+        if (kleft >= kStepK) {
 #pragma unroll
-            for (int i = 0; i < N; ++i) __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, place(i), 16, off[i], 0, 0, 0);
+            for (int i = 0; i < N; ++i) lds_load16(origin, place(i), off[i]);
             return;
         }
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             int row, slot;
-            source((i * NW + wave) * 64 + lane, row, slot);
-            const uint32_t o = (KC ? slot * E : row) < kleft ? off[i] : 0x80000000u;
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, place(i), 16, o, 0, 0, 0);
+            source(i, row, slot);
+            const uint32_t o = (KC ? slot * E : row) < kleft ? off[i] : kSkip;
+            lds_load16(origin, place(i), o);
         }
     }
     // the same tile without alignment or whole pieces: through registers, value by value at the edges
     __device__ __forceinline__ void fetch(const T *origin, int64_t ld, int64_t rows, int64_t kleft, uint4 *r) const {
-        const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             int row, slot;
-            source((i * NW + wave) * 64 + lane, row, slot);
+            source(i, row, slot);
             const int64_t most = KC ? kleft : rows;     // along the contiguous direction
             uint4 v = make_uint4(0, 0, 0, 0);
             if (row < (KC ? rows : kleft)) {
@@ -202,24 +204,23 @@ template <typename T, int R, int NW, bool KC> struct OperandTile {
         }
     }
     static __device__ __forceinline__ void put(T *tile, const uint4 *r) {
-        const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
 #pragma unroll
-        for (int i = 0; i < N; ++i) *reinterpret_cast<uint4 *>(tile + ((i * NW + wave) * 64 + lane) * E) = r[i];
+        for (int i = 0; i < N; ++i) *reinterpret_cast<uint4 *>(tile + (i * 64 * NW + (int)threadIdx.x) * E) = r[i];
     }
-    // operand of rows r0 .. r0 + 15 at k slots kk * 32 + 8 g + j
-    static __device__ __forceinline__ typename Mma<T>::v8 frag(const T *tile, int r0, int kk) {
+    // operand of rows r0 .. r0 + 15 at k slots 8 g + j
+    static __device__ __forceinline__ typename Mma<T>::v8 frag(const T *tile, int r0) {
         const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
         if constexpr (KC) {
             const int row = r0 + c;
             if constexpr (sizeof(T) == 2) {
-                return lds_row8<T>(tile + row * BK + (((kk * 4 + g) ^ (row & 7)) * E));
+                return *reinterpret_cast<const typename Mma<T>::v8 *>(tile + row * kStepK + (g ^ turn(row)) * E);
             } else {
-                const f32x4 a = *reinterpret_cast<const f32x4 *>(tile + row * BK + ((2 * g) ^ (row & 7)) * E);
-                const f32x4 b = *reinterpret_cast<const f32x4 *>(tile + row * BK + ((2 * g + 1) ^ (row & 7)) * E);
+                const f32x4 a = *reinterpret_cast<const f32x4 *>(tile + row * kStepK + ((2 * g) ^ turn(row)) * E);
+                const f32x4 b = *reinterpret_cast<const f32x4 *>(tile + row * kStepK + ((2 * g + 1) ^ turn(row)) * E);
                 return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
             }
         } else if constexpr (sizeof(T) == 2) {
-            const int k = kk * 32 + g * 8 + (c >> 2);             // and k + 4
+            const int k = g * 8 + (c >> 2);                       // and k + 4
             const int col = r0 + (c & 3) * 4;                     // 16 columns: one 32-byte granule
             const int h = granule(k);                             // the same for k + 4
             const T *p = tile + k * R + ((col & ~127) | ((((col >> 4) & 7) ^ h) << 4) | (col & 15));
@@ -232,7 +233,7 @@ template <typename T, int R, int NW, bool KC> struct OperandTile {
             const int col = r0 + c;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const int k = kk * 32 + g * 8 + j;
+                const int k = g * 8 + j;
                 v[j] = tile[k * R + ((col & ~63) | ((((col >> 4) & 3) ^ (g & 3)) << 4) | (col & 15))];
             }
             return v;
@@ -253,80 +254,204 @@ __device__ __forceinline__ void tile_of(int64_t id, int64_t tm, int64_t tn, int6
     bn = __builtin_amdgcn_readfirstlane((int)(id % band / rows));
 }
 
-// TM x TN 16x16 tiles per wave, WM x WN waves.  VEC: operands 16-byte aligned in rows of whole pieces.
-template <typename T, int LAYOUT, int TM, int TN, int WM, int WN, bool VEC>
+// TM x TN 16x16 tiles per wave, WM x WN waves, S stages (even).  VEC: operands 16-byte aligned in rows of
+// whole pieces.
+template <typename T, int LAYOUT, int TM, int TN, int WM, int WN, int S, bool VEC>
 __global__ __launch_bounds__(64 * WM * WN, 2) void linear_gemm_kernel(const LinearGemm a) {
-#ifdef __HIP_DEVICE_COMPILE__   // the host pass, which cannot take the LDS-destination loads, needs the stub alone
-    constexpr int BM = TM * WM * 16, BN = TN * WN * 16, NW = WM * WN;
+#ifdef __HIP_DEVICE_COMPILE__   // the host pass, which cannot take the scalar operands, needs the stub alone
+    constexpr int BM = TM * WM * 16, BN = TN * WN * 16, NW = WM * WN, BK = kStepK;
     constexpr bool AK = LAYOUT != LAYOUT_TN, BKC = LAYOUT == LAYOUT_NT;
     using TA = OperandTile<T, BM, NW, AK>;
     using TB = OperandTile<T, BN, NW, BKC>;
-    constexpr int BK = TA::BK, KK = BK / 32;
-    // two stages as separate arrays: the loads into one are then known not to alias the reads of the other
-    __shared__ __attribute__((aligned(128))) T sa0[BM * BK], sb0[BN * BK];
-    __shared__ __attribute__((aligned(128))) T sa1[BM * BK], sb1[BN * BK];
+    using v8 = typename Mma<T>::v8;
+    static_assert(S == 2 || S == 4, "the loop is unrolled over the stages and the two fragment sets");
+    __shared__ __attribute__((aligned(128))) T sa0[TA::VALUES], sb0[TB::VALUES], sa1[TA::VALUES], sb1[TB::VALUES];
+    __shared__ __attribute__((aligned(128))) T sa2[S > 2 ? TA::VALUES : 8], sb2[S > 2 ? TB::VALUES : 8];
+    __shared__ __attribute__((aligned(128))) T sa3[S > 2 ? TA::VALUES : 8], sb3[S > 2 ? TB::VALUES : 8];
     const int64_t tm = (a.M + BM - 1) / BM, tn = (a.N + BN - 1) / BN;
     int64_t bm, bn;
     tile_of(blockIdx.x, tm, tn, bm, bn);
     const int64_t m0 = bm * BM, n0 = bn * BN;
     const int64_t k0 = blockIdx.y * a.kper, k1 = k0 + a.kper < a.K ? k0 + a.kper : a.K;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, c = lane & 15;
+    const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = (wave / WN) * TM * 16, wn = (wave % WN) * TN * 16;
     const T *pa = static_cast<const T *>(a.A) + (AK ? m0 * a.lda + k0 : k0 * a.lda + m0);
     const T *pb = static_cast<const T *>(a.B) + (BKC ? n0 * a.ldb + k0 : k0 * a.ldb + n0);
     const int64_t sa_step = AK ? BK : BK * a.lda, sb_step = BKC ? BK : BK * a.ldb;
 
-    TA ta;
-    TB tb;
-    if (VEC) {
-        ta.prepare(a.lda, a.M - m0);
-        tb.prepare(a.ldb, a.N - n0);
-    }
     f32x4 acc[TM][TN];
 #pragma unroll
     for (int i = 0; i < TM; ++i)
 #pragma unroll
         for (int j = 0; j < TN; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
-
-    uint4 ra[VEC ? 1 : TA::N], rb[VEC ? 1 : TB::N];
-    auto bring = [&](int64_t k, T *na, T *nb) __attribute__((always_inline)) {
-        const int64_t left = k1 - k;
-        const int kl = left < BK ? (int)left : BK;
-        if constexpr (VEC) {
+    constexpr int H = TM / 2;       // row tiles of a half
+    auto read_b = [&](const T *t, v8 *f) __attribute__((always_inline)) {
+#pragma unroll
+        for (int j = 0; j < TN; ++j) f[j] = TB::frag(t, wn + j * 16);
+    };
+    auto read_a = [&](const T *t, v8 *f, int half) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < H; ++i) f[i] = TA::frag(t, wm + (half * H + i) * 16);
+    };
+    auto multiply = [&](const v8 *fa, const v8 *fb, int half) __attribute__((always_inline)) {
+#pragma unroll
+        for (int p = 0; p < Mma<T>::kParts; ++p)
+#pragma unroll
+            for (int i = 0; i < H; ++i)
+#pragma unroll
+                for (int j = 0; j < TN; ++j) acc[half * H + i][j] = Mma<T>::mma(fb[j], fa[i], acc[half * H + i][j], p);
+    };
+    TA ta;
+    TB tb;
+    if constexpr (VEC) {
+        constexpr int kLoads = TA::N + TB::N, kLeft = (S - 2) * kLoads;
+        ta.prepare(a.lda, a.M - m0);
+        tb.prepare(a.ldb, a.N - n0);
+        const int steps = (int)((k1 - k0 + BK - 1) / BK), full = (int)((k1 - k0) / BK);
+        int next = 0;              // the next step to bring
+        auto bring = [&](T *na, T *nb, bool whole) __attribute__((always_inline)) {
+            const int kl = whole || next < full ? BK : (int)(k1 - k0) - next * BK;
             ta.issue(pa, na, kl);
             tb.issue(pb, nb, kl);
-        } else {
+            pa += sa_step;
+            pb += sb_step;
+            ++next;
+        };
+        // waits until the oldest stage of this wave's loads is there (with `deep`, S - 2 stages behind it may
+        // still travel) and its LDS reads are done, then for the other waves
+        auto arrive = [&](bool deep) __attribute__((always_inline)) {
+            if (deep) wait_loads_and_barrier<kLeft>();
+            else wait_loads_and_barrier<0>();
+        };
+        v8 lo[H], hi[H], b0[TN], b1[TN];
+        if (steps > 0) bring(sa0, sb0, false);
+        if (steps > 1) bring(sa1, sb1, false);
+        if (S > 2 && steps > 2) bring(sa2, sb2, false);
+        if (S > 2 && steps > 3) bring(sa3, sb3, false);
+        if (steps > 0) {
+            arrive(false);
+            read_b(sb0, b0);
+            read_a(sa0, lo, 0);
+        }
+        // one step in stage (ca, cb); the fragments of the next come from (na, nb).  At the barrier every
+        // wave has all it needs of (ca, cb), which then takes the step S ahead.
+        auto step = [&](T *ca, T *cb, const T *na, const T *nb, const v8 *fb, v8 *gb) __attribute__((always_inline)) {
+            read_a(ca, hi, 1);
+            __builtin_amdgcn_sched_barrier(0);      // reads first: products of the half before hide them
+            multiply(lo, fb, 0);
+            arrive(true);
+            read_b(nb, gb);
+            read_a(na, lo, 0);
+            bring(ca, cb, true);
+            __builtin_amdgcn_sched_barrier(0);
+            multiply(hi, fb, 1);
+        };
+        // the same near the end, where there may be no next step and nothing left to bring
+        auto last = [&](int k, T *ca, T *cb, const T *na, const T *nb, const v8 *fb, v8 *gb) __attribute__((always_inline)) {
+            read_a(ca, hi, 1);
+            multiply(lo, fb, 0);
+            if (k + 1 < steps) {
+                arrive(k + S - 1 < steps);
+                if (k + S < steps) bring(ca, cb, false);
+                read_b(nb, gb);
+                read_a(na, lo, 0);
+            }
+            multiply(hi, fb, 1);
+        };
+        int k = 0;
+        for (; k + 2 * S <= full; k += S) {
+            step(sa0, sb0, sa1, sb1, b0, b1);
+            if constexpr (S == 2) {
+                step(sa1, sb1, sa0, sb0, b1, b0);
+            } else {
+                step(sa1, sb1, sa2, sb2, b1, b0);
+                step(sa2, sb2, sa3, sb3, b0, b1);
+                step(sa3, sb3, sa0, sb0, b1, b0);
+            }
+        }
+        for (; k < steps; k += S) {
+            last(k, sa0, sb0, sa1, sb1, b0, b1);
+            if constexpr (S == 2) {
+                if (k + 1 < steps) last(k + 1, sa1, sb1, sa0, sb0, b1, b0);
+            } else {
+                if (k + 1 < steps) last(k + 1, sa1, sb1, sa2, sb2, b1, b0);
+                if (k + 2 < steps) last(k + 2, sa2, sb2, sa3, sb3, b0, b1);
+                if (k + 3 < steps) last(k + 3, sa3, sb3, sa0, sb0, b1, b0);
+            }
+        }
+    } else {
+        uint4 ra[TA::N], rb[TB::N];
+        auto fetch = [&](int64_t k) __attribute__((always_inline)) {
+            const int kl = k1 - k < BK ? (int)(k1 - k) : BK;
             ta.fetch(pa, a.lda, a.M - m0, kl, ra);
             tb.fetch(pb, a.ldb, a.N - n0, kl, rb);
-        }
-        pa += sa_step;
-        pb += sb_step;
-    };
-    // multiplies the step in (ca, cb) while the next one travels into (na, nb)
-    auto step = [&](int64_t k, T *ca, T *cb, T *na, T *nb) __attribute__((always_inline)) {
-        if constexpr (!VEC) {
+            pa += sa_step;
+            pb += sb_step;
+        };
+        auto step = [&](int64_t k, T *ca, T *cb) __attribute__((always_inline)) {
+            v8 fa[H], fb[TN];
             TA::put(ca, ra);
             TB::put(cb, rb);
+            __syncthreads();
+            if (k + BK < k1) fetch(k + BK);
+            read_b(cb, fb);
+            read_a(ca, fa, 0);
+            multiply(fa, fb, 0);
+            read_a(ca, fa, 1);
+            multiply(fa, fb, 1);
+        };
+        if (k0 < k1) fetch(k0);
+        for (int64_t k = k0; k < k1; k += 2 * BK) {
+            step(k, sa0, sb0);
+            if (k + BK < k1) step(k + BK, sa1, sb1);
         }
-        __syncthreads();      // this step's tiles are in LDS; the other stage's readers are done
-        if (k + BK < k1) bring(k + BK, na, nb);
+    }
+    if (a.quads && !a.part) {
+        // every row of every tensor in whole, aligned quads: 32-bit places in views of the tile, no branches
+        struct Q { T v[4]; };
+        const int64_t at = m0 + wm, col = n0 + wn;
+        const auto vc = wide_view(static_cast<T *>(a.C) + at * a.ldc + col), vr = wide_view(static_cast<const T *>(a.res) + at * a.ldr + col),
+                   vp = wide_view(static_cast<T *>(a.pre) + at * a.ldp + col), vb = wide_view(static_cast<const T *>(a.bias) + col);
+        const int rows = a.M - at < TM * 16 ? (int)(a.M - at) : TM * 16, cols = a.N - col < TN * 16 ? (int)(a.N - col) : TN * 16;
+        float bias[TN][4];
 #pragma unroll
-        for (int kk = 0; kk < KK; ++kk) {
-            typename Mma<T>::v8 fa[TM], fb[TN];
+        for (int j = 0; j < TN; ++j) {
+            const Q q = view_load_wide<Q>(vb, a.bias && j * 16 + g * 4 < cols ? (j * 16 + g * 4) * (uint32_t)sizeof(T) : kSkip);
 #pragma unroll
-            for (int i = 0; i < TM; ++i) fa[i] = TA::frag(ca, wm + i * 16, kk);
-#pragma unroll
-            for (int j = 0; j < TN; ++j) fb[j] = TB::frag(cb, wn + j * 16, kk);
-#pragma unroll
-            for (int i = 0; i < TM; ++i)
-#pragma unroll
-                for (int j = 0; j < TN; ++j) acc[i][j] = Mma<T>::mma(fb[j], fa[i], acc[i][j]);
+            for (int e = 0; e < 4; ++e) bias[j][e] = (float)q.v[e];
         }
-    };
-    if (k0 < k1) bring(k0, sa0, sb0);
-    for (int64_t k = k0; k < k1; k += 2 * BK) {
-        step(k, sa0, sb0, sa1, sb1);
-        if (k + BK < k1) step(k + BK, sa1, sb1, sa0, sb0);
+#pragma unroll
+        for (int i = 0; i < TM; ++i) {
+            const int row = i * 16 + c;
+#pragma unroll
+            for (int j = 0; j < TN; ++j) {
+                const bool in = row < rows && j * 16 + g * 4 < cols;
+                const uint32_t x = (uint32_t)(j * 16 + g * 4) * (uint32_t)sizeof(T);
+                float f[4];
+                Q q;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) f[e] = acc[i][j][e] + bias[j][e];
+                if (a.pre) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) q.v[e] = (T)f[e];
+                    view_store(vp, in ? (uint32_t)(row * (uint32_t)a.ldp) * (uint32_t)sizeof(T) + x : kSkip, q);
+                }
+                if (a.act != ACT_NONE) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) f[e] = act_value(f[e], a.act);
+                }
+                if (a.res) {
+                    q = view_load_wide<Q>(vr, in ? (uint32_t)(row * (uint32_t)a.ldr) * (uint32_t)sizeof(T) + x : kSkip);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) f[e] += (float)q.v[e];
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) q.v[e] = (T)f[e];
+                view_store(vc, in ? (uint32_t)(row * (uint32_t)a.ldc) * (uint32_t)sizeof(T) + x : kSkip, q);
+            }
+        }
+        return;
     }
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
@@ -503,15 +628,16 @@ static hipError_t gemm_layout(const LinearGemm &a, int tile, bool vec, hipStream
     auto blocks = [&](int bm, int bn) {
         return dim3((unsigned)(((a.M + bm - 1) / bm) * ((a.N + bn - 1) / bn)), (unsigned)a.splits);
     };
+    constexpr int S = sizeof(T) == 2 ? 4 : 2;      // stages of the 128 tile: 64 KB
     if (!vec) {
-        linear_gemm_kernel<T, LAYOUT, 4, 4, 2, 2, false><<<blocks(128, 128), 256, 0, stream>>>(a);
+        linear_gemm_kernel<T, LAYOUT, 4, 4, 2, 2, 2, false><<<blocks(128, 128), 256, 0, stream>>>(a);
     } else if (tile == 256) {
         if constexpr (sizeof(T) == 2)
-            linear_gemm_kernel<T, LAYOUT, 8, 4, 2, 4, true><<<blocks(256, 256), 512, 0, stream>>>(a);
+            linear_gemm_kernel<T, LAYOUT, 8, 4, 2, 4, 4, true><<<blocks(256, 256), 512, 0, stream>>>(a);
     } else if (tile == 128) {
-        linear_gemm_kernel<T, LAYOUT, 4, 4, 2, 2, true><<<blocks(128, 128), 256, 0, stream>>>(a);
+        linear_gemm_kernel<T, LAYOUT, 4, 4, 2, 2, S, true><<<blocks(128, 128), 256, 0, stream>>>(a);
     } else {
-        linear_gemm_kernel<T, LAYOUT, 2, 2, 2, 2, true><<<blocks(64, 64), 256, 0, stream>>>(a);
+        linear_gemm_kernel<T, LAYOUT, 2, 2, 2, 2, S, true><<<blocks(64, 64), 256, 0, stream>>>(a);
     }
     return hipGetLastError();
 }

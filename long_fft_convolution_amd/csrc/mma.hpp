@@ -29,7 +29,8 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 template <> struct Mma<_Float16> {
     typedef _Float16 v8 __attribute__((ext_vector_type(8)));
     typedef _Float16 v4 __attribute__((ext_vector_type(4)));
-    static __device__ __forceinline__ f32x4 mma(v8 a, v8 b, f32x4 c) {
+    static constexpr int kParts = 1;
+    static __device__ __forceinline__ f32x4 mma(v8 a, v8 b, f32x4 c, int part = 0) {
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
     }
     // terms of the storage type that hold an fp32 value to fp32 precision (2 x 11 bits, given a scale
@@ -40,7 +41,8 @@ template <> struct Mma<_Float16> {
 template <> struct Mma<__bf16> {
     typedef __bf16 v8 __attribute__((ext_vector_type(8)));
     typedef __bf16 v4 __attribute__((ext_vector_type(4)));
-    static __device__ __forceinline__ f32x4 mma(v8 a, v8 b, f32x4 c) {
+    static constexpr int kParts = 1;
+    static __device__ __forceinline__ f32x4 mma(v8 a, v8 b, f32x4 c, int part = 0) {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
     }
     static constexpr int kExactTerms = 3, kTerms = 2;   // 3 x 8 bits; 2 x 8 bits
@@ -49,6 +51,10 @@ template <> struct Mma<__bf16> {
 template <> struct Mma<float> {
     typedef float v8 __attribute__((ext_vector_type(8)));
     typedef float v4 __attribute__((ext_vector_type(4)));
+    static constexpr int kParts = 8;      // instructions of one product, for callers that interleave several
+    static __device__ __forceinline__ f32x4 mma(const v8 &a, const v8 &b, f32x4 c, int part) {
+        return __builtin_amdgcn_mfma_f32_16x16x4f32(a[part], b[part], c, 0, 0, 0);
+    }
     static __device__ __forceinline__ f32x4 mma(const v8 &a, const v8 &b, f32x4 c) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[j], b[j], c, 0, 0, 0);
@@ -57,15 +63,6 @@ template <> struct Mma<float> {
     static constexpr int kExactTerms = 1, kTerms = 1;
     static constexpr bool kNarrow = false;
 };
-
-// 8 consecutive values of one LDS row (16-byte aligned)
-template <typename T> __device__ __forceinline__ typename Mma<T>::v8 lds_row8(const T *p) {
-    return *reinterpret_cast<const typename Mma<T>::v8 *>(p);
-}
-template <> __device__ __forceinline__ Mma<float>::v8 lds_row8<float>(const float *p) {
-    const f32x4 a = *reinterpret_cast<const f32x4 *>(p), b = *reinterpret_cast<const f32x4 *>(p + 4);
-    return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
-}
 
 // A raw buffer view at a wave-uniform p whose offsets up to 2^31 - 2 are in range; kSkip is out of
 // range, so a load there reads zero and a store there writes nothing.  Lanes that have nothing to do
@@ -82,6 +79,10 @@ template <typename T> __device__ __forceinline__ T view_load(__amdgpu_buffer_rsr
     if constexpr (sizeof(T) == 4) return __builtin_bit_cast(T, __builtin_amdgcn_raw_buffer_load_b32(v, off, 0, 0));
     else return __builtin_bit_cast(T, __builtin_amdgcn_raw_buffer_load_b16(v, off, 0, 0));
 }
+template <typename V> __device__ __forceinline__ V view_load_wide(__amdgpu_buffer_rsrc_t v, uint32_t off) {
+    if constexpr (sizeof(V) == 8) return __builtin_bit_cast(V, (u32x2)__builtin_amdgcn_raw_buffer_load_b64(v, off, 0, 0));
+    else return __builtin_bit_cast(V, (u32x4)__builtin_amdgcn_raw_buffer_load_b128(v, off, 0, 0));
+}
 template <typename V> __device__ __forceinline__ void view_store(__amdgpu_buffer_rsrc_t v, uint32_t off, const V &x) {
     if constexpr (sizeof(V) == 2) __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(unsigned short, x), v, off, 0, 0);
     else if constexpr (sizeof(V) == 4) __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, x), v, off, 0, 0);
@@ -94,6 +95,27 @@ template <typename V> __device__ __forceinline__ void view_store(__amdgpu_buffer
         view_store(v, off, t.h[0]);
         view_store(v, off + (uint32_t)(sizeof(V) / 2), t.h[1]);     // kSkip + 16 is out of range, too
     }
+}
+
+// The 64 lanes' 16 bytes at byte offsets off from the wave-uniform p, straight into LDS at dst + 16 lane
+// (dst wave-uniform); zeros for offsets out of range, like wide_view.  Written out because the compiler
+// follows only a few of such loads apart and makes every LDS read wait for the rest: here the kernel says
+// itself (wait_loads) what has to have arrived.  The instruction has no destination register, and waits
+// that the compiler adds for its own loads only grow stricter by loads it does not know.
+__device__ __forceinline__ void lds_load16(const void *p, void *dst, uint32_t off) {
+    const uint64_t base = reinterpret_cast<uint64_t>(p);
+    const u32x4 view = {(uint32_t)base, (uint32_t)(base >> 32) & 0xffffu, 0x7fffffffu, 0x00020000u};
+    const uint32_t at = (uint32_t)(uintptr_t)FFTCONV_LDS_CAST(void, dst);
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(at), "v"(off), "s"(view) : "memory");
+}
+// Waits until at most LEFT of this wave's vector loads and stores, and none of its LDS reads, are on their
+// way, then for the other waves of the workgroup.
+template <int LEFT> __device__ __forceinline__ void wait_loads_and_barrier() {
+    static_assert(LEFT < 64, "six bits");
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt((LEFT & 15) | 0x70 | (LEFT >> 4) << 14);
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
 }
 
 }  // namespace fftconv

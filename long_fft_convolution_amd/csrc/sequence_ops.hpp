@@ -87,6 +87,7 @@ struct LinearGemm {
     int64_t ldp;
     int act;
     int vec_c, vec_r, vec_p, vec_b;   // 4-value access allowed
+    int quads;                // N a multiple of 4, 4-value access everywhere, a tile's rows within 31 bits
     int64_t kper;             // K of one split, a multiple of the K step
     float *part;              // splits x M x N partial sums, null when not split
     int splits;
