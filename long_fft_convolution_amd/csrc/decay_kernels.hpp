@@ -152,8 +152,9 @@ __device__ __forceinline__ int64_t scalar(int64_t v) {
 constexpr int kChunk = 32;
 
 // A chunk's tile of one operand in LDS: kChunk rows of DP values in 16-byte slots, slot s of row r
-// lying at s ^ f(r).  f spreads over the banks what one read instruction meets: 16 neighbouring
-// rows (X), or the permuted rows 8 (c / 4) + c % 4 and the columns of four rows (Y, Z).
+// lying at s ^ f(r).  f spreads over the 128 bytes of an LDS cycle what the cycle's lanes read: eight
+// neighbouring rows (X), or the permuted rows 8 (c / 4) + c % 4 of eight c (Y), and four groups of four
+// columns of four rows (Y, Z: two cycles, the 8-byte groups being of one half of their slots).
 template <typename T, int DP, bool PERMUTED> struct ChunkTile {
     static constexpr int E = 16 / (int)sizeof(T);            // values of a slot
     static constexpr int PR = DP / E;                        // slots of a row
@@ -161,8 +162,8 @@ template <typename T, int DP, bool PERMUTED> struct ChunkTile {
     static constexpr int VALUES = kChunk * DP;
     static_assert(kChunk * PR % 256 == 0, "whole loads");
     static __device__ __forceinline__ int f(int row) {
-        if (PR == 8) return PERMUTED ? ((row >> 1) & 1) << 2 | ((row >> 3) & 3) : (row >> 1) & 7;
-        return PERMUTED ? (row & 3) << 2 | ((row >> 3) & 3) : row & 15;
+        if (PERMUTED) return (row & 1) << 2 | (row & 2) | ((row >> 3) & 1);
+        return row & 7;
     }
     static __device__ __forceinline__ void source(int i, int &row, int &slot) {
         const int idx = i * 256 + (threadIdx.x & 255);

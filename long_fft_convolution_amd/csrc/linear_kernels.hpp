@@ -133,14 +133,12 @@ template <typename T, int R, int NW, bool KC> struct OperandTile {
     static constexpr int N = VALUES / E / (64 * NW);        // loads of a lane
     static_assert(VALUES / E % (64 * NW) == 0, "whole loads");
 
-    // exchange of the slots of a row of k values: 4 (16-bit) or 8 (fp32) slots, 4 or 2 rows to the banks' 256 bytes
-    static __device__ __forceinline__ int turn(int row) { return PR == 4 ? (row >> 2) & 3 : row & 7; }
-    // exchange of the 32-byte granules of a 16-bit tile's k rows: the eight rows k = 8 g + r (g < 2, r < 4)
-    // that one half of a transposing read meets lie in eight different granules of the banks' 256 bytes
-    // (tiles of 64 have rows of 128 bytes, two of which share a period)
-    static __device__ __forceinline__ int granule(int k) {
-        return R >= 128 ? (k & 3) | ((k >> 1) & 4) : ((k >> 1) & 1) | ((k >> 2) & 2);
-    }
+    // An LDS cycle serves 128 bytes: eight lanes of a 16-byte read, sixteen of a transposing one.
+    // Exchange of the slots of a row of k values (4 in 16-bit types, 8 in fp32): one slot of eight
+    // neighbouring rows covers 128 bytes.
+    static __device__ __forceinline__ int turn(int row) { return PR == 4 ? (row >> 1) & 3 : row & 7; }
+    // Exchange of the 32-byte granules of a 16-bit tile's k rows: one granule of four neighbouring rows does.
+    static __device__ __forceinline__ int granule(int k) { return R >= 128 ? (k & 3) | ((k >> 1) & 4) : k & 3; }
     // LDS piece p holds source piece (row, slot)
     static __device__ __forceinline__ void source(int i, int &row, int &slot) {
         const int p = i * 64 * NW + (int)threadIdx.x;
