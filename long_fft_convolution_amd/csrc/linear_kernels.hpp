@@ -7,23 +7,29 @@
 //     out: A = x, B = W, both contiguous along k;
 //     dx:  A = dz, B(n, k) = W[k][n], contiguous along n;
 //     dW:  A(m, k) = dz[k][m], B(n, k) = x[k][n], both contiguous along the tile.
-// A workgroup computes a BM x BN tile over K steps of 32.  Tiles of both
-// operands stream from HBM straight into LDS (buffer loads with an LDS
-// destination, 16 bytes a lane, zero past the operand's edge by the buffer
-// unit's range check) through a ring of S stages, so S - 1 steps of loads are
-// on their way and no register holds them.  Fragments are read from LDS half
-// a step ahead of the products that take them: the second half of a wave's
-// rows under the products of the first, the next step's columns and first half
-// under those of the second.  The destination of an LDS load is linear in the
-// lane, so the bank swizzle permutes the source: lane l fetches the 16 bytes
-// that belong at its place.
+// A workgroup computes a tile over K stages of 128 bytes (64 or 32 values).
+// Tiles of both operands stream from HBM straight into LDS (buffer loads with
+// an LDS destination, 16 bytes a lane, whole 128-byte lines, zero past the
+// operand's edge by the buffer unit's range check), so no register holds them.
+// The destination of such a load is linear in the lane, so the bank swizzle
+// permutes the source: lane l fetches the 16 bytes that belong at its place.
 //
-// An operand contiguous along k lies in LDS as rows of 32 values, its 16-byte
-// slots exchanged so that one slot of 16 neighbouring rows covers all banks;
-// one contiguous along the tile as k rows of the tile's width, read with the
-// transposing LDS read (16-bit types; 32-byte granules exchanged by k) or value
-// by value (fp32; 64-byte granules exchanged by k / 8).  The product is taken as
-// B A (rows n, columns m), so a lane holds four neighbouring n of one row.
+// LDS holds two stages, but each operand's tile is two halves (A0, A1, B0, B1)
+// and a wave reads each of them into registers once, ahead of its products:
+//     A0 B0, A0 B1   while B1 and A1 of this stage are read,
+//     A1 B0, A1 B1   while A0 and B0 of the next stage are read,
+// with a barrier before each line.  A half's place is thus free for the stage
+// after next long before its products are done, and its loads have a stage and
+// a half (three of those lines) to arrive; LDS reads pass under products.
+// At 256 x 256 x 64 a line is 32 matrix instructions a wave (1024 cycles of a
+// SIMD's two waves) against 12 LDS reads (768 cycles of the CU's LDS).
+//
+// An operand contiguous along k lies in LDS as rows of 128 bytes, its eight
+// 16-byte slots exchanged by the row; one contiguous along the tile as k rows of
+// the tile's width, read with the transposing LDS read (16-bit types; 32-byte
+// granules exchanged by k) or value by value (fp32; 64-byte granules exchanged by
+// k / 8).  The product is taken as B A (rows n, columns m), so a lane holds four
+// neighbouring n of one row.
 #pragma once
 
 #include "mma.hpp"
@@ -124,29 +130,27 @@ __device__ __forceinline__ void linear_epilogue(const LinearGemm &a, int64_t m, 
     store_quad(static_cast<T *>(a.C) + m * a.ldc + n, left, a.vec_c, f);
 }
 
-// One operand's tile: R rows (of m or n) by 32 of k.  KC: contiguous along k.
-constexpr int kStepK = 32;
+// Half an operand's tile: R rows (of m or n) by BK of k.  KC: contiguous along k.
 template <typename T, int R, int NW, bool KC> struct OperandTile {
     static constexpr int E = 16 / (int)sizeof(T);
-    static constexpr int PR = KC ? kStepK / E : R / E;      // 16-byte pieces of an LDS row
-    static constexpr int VALUES = R * kStepK;
+    static constexpr int BK = 128 / (int)sizeof(T);
+    static constexpr int PR = KC ? BK / E : R / E;          // 16-byte pieces of an LDS row
+    static constexpr int VALUES = R * BK;
     static constexpr int N = VALUES / E / (64 * NW);        // loads of a lane
     static_assert(VALUES / E % (64 * NW) == 0, "whole loads");
 
-    // An LDS cycle serves 128 bytes: eight lanes of a 16-byte read, sixteen of a transposing one.
-    // Exchange of the slots of a row of k values (4 in 16-bit types, 8 in fp32): one slot of eight
-    // neighbouring rows covers 128 bytes.
-    static __device__ __forceinline__ int turn(int row) { return PR == 4 ? (row >> 1) & 3 : row & 7; }
-    // Exchange of the 32-byte granules of a 16-bit tile's k rows: one granule of four neighbouring rows does.
-    static __device__ __forceinline__ int granule(int k) { return R >= 128 ? (k & 3) | ((k >> 1) & 4) : k & 3; }
+    // An LDS cycle serves 128 bytes: eight lanes of a 16-byte read (one slot of eight neighbouring rows),
+    // sixteen of a transposing one (one 32-byte granule of four neighbouring k rows), 32 of a 4-byte one.
+    static __device__ __forceinline__ int granule(int k) { return R >= 64 ? k & 3 : (k >> 1) & 1; }
+    static __device__ __forceinline__ int granule32(int k) { return (k >> 3) & (R >= 64 ? 3 : 1); }
     // LDS piece p holds source piece (row, slot)
     static __device__ __forceinline__ void source(int i, int &row, int &slot) {
         const int p = i * 64 * NW + (int)threadIdx.x;
         row = p / PR;
         const int s = p % PR;
-        if (KC) slot = s ^ turn(row);
-        else if (sizeof(T) == 2) slot = (s & ~15) | ((((s >> 1) & 7) ^ granule(row)) << 1) | (s & 1);
-        else slot = (s & ~15) | ((((s >> 2) & 3) ^ ((row >> 3) & 3)) << 2) | (s & 3);
+        if (KC) slot = s ^ (row & 7);
+        else if (sizeof(T) == 2) slot = (((s >> 1) ^ granule(row)) << 1) | (s & 1);
+        else slot = (((s >> 2) ^ granule32(row)) << 2) | (s & 3);
     }
 
     uint32_t off[N];    // byte offset of each load from the tile's origin at k = 0
@@ -166,7 +170,7 @@ template <typename T, int R, int NW, bool KC> struct OperandTile {
         // the buffer view and the LDS place are scalar operands: the wave index as one
         const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
         auto place = [&](int i) { return tile + (i * NW + wave) * 64 * E; };
-        if (kleft >= kStepK) {
+        if (kleft >= BK) {
 #pragma unroll
             for (int i = 0; i < N; ++i) lds_load16(origin, place(i), off[i]);
             return;
@@ -205,23 +209,22 @@ template <typename T, int R, int NW, bool KC> struct OperandTile {
 #pragma unroll
         for (int i = 0; i < N; ++i) *reinterpret_cast<uint4 *>(tile + (i * 64 * NW + (int)threadIdx.x) * E) = r[i];
     }
-    // operand of rows r0 .. r0 + 15 at k slots 8 g + j
-    static __device__ __forceinline__ typename Mma<T>::v8 frag(const T *tile, int r0) {
+    // operand of rows r0 .. r0 + 15 at k slots kk * 32 + 8 g + j
+    static __device__ __forceinline__ typename Mma<T>::v8 frag(const T *tile, int r0, int kk) {
         const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
         if constexpr (KC) {
             const int row = r0 + c;
             if constexpr (sizeof(T) == 2) {
-                return *reinterpret_cast<const typename Mma<T>::v8 *>(tile + row * kStepK + (g ^ turn(row)) * E);
+                return *reinterpret_cast<const typename Mma<T>::v8 *>(tile + row * BK + ((kk * 4 + g) ^ (row & 7)) * E);
             } else {
-                const f32x4 a = *reinterpret_cast<const f32x4 *>(tile + row * kStepK + ((2 * g) ^ turn(row)) * E);
-                const f32x4 b = *reinterpret_cast<const f32x4 *>(tile + row * kStepK + ((2 * g + 1) ^ turn(row)) * E);
+                const f32x4 a = *reinterpret_cast<const f32x4 *>(tile + row * BK + ((2 * g) ^ (row & 7)) * E);
+                const f32x4 b = *reinterpret_cast<const f32x4 *>(tile + row * BK + ((2 * g + 1) ^ (row & 7)) * E);
                 return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
             }
         } else if constexpr (sizeof(T) == 2) {
-            const int k = g * 8 + (c >> 2);                       // and k + 4
+            const int k = kk * 32 + g * 8 + (c >> 2);             // and k + 4
             const int col = r0 + (c & 3) * 4;                     // 16 columns: one 32-byte granule
-            const int h = granule(k);                             // the same for k + 4
-            const T *p = tile + k * R + ((col & ~127) | ((((col >> 4) & 7) ^ h) << 4) | (col & 15));
+            const T *p = tile + k * R + ((((col >> 4) ^ granule(k)) << 4) | (col & 15));   // the same exchange for k + 4
             typedef typename Mma<T>::v4 v4;
             const v4 a = __builtin_bit_cast(v4, __builtin_amdgcn_ds_read_tr16_b64_v4i16(FFTCONV_LDS_CAST(s16x4, p)));
             const v4 b = __builtin_bit_cast(v4, __builtin_amdgcn_ds_read_tr16_b64_v4i16(FFTCONV_LDS_CAST(s16x4, p + 4 * R)));
@@ -231,8 +234,8 @@ template <typename T, int R, int NW, bool KC> struct OperandTile {
             const int col = r0 + c;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const int k = g * 8 + j;
-                v[j] = tile[k * R + ((col & ~63) | ((((col >> 4) & 3) ^ (g & 3)) << 4) | (col & 15))];
+                const int k = kk * 32 + g * 8 + j;
+                v[j] = tile[k * R + ((((col >> 4) ^ granule32(k)) << 4) | (col & 15))];
             }
             return v;
         }
@@ -252,222 +255,215 @@ __device__ __forceinline__ void tile_of(int64_t id, int64_t tm, int64_t tn, int6
     bn = __builtin_amdgcn_readfirstlane((int)(id % band / rows));
 }
 
-// TM x TN 16x16 tiles per wave, WM x WN waves, S stages (even).  VEC: operands 16-byte aligned in rows of
-// whole pieces.
-template <typename T, int LAYOUT, int TM, int TN, int WM, int WN, int S, bool VEC>
+// TM x TN 16x16 tiles per wave in each quadrant (A half x B half), WM x WN waves.  VEC: operands 16-byte
+// aligned in rows of whole pieces.
+template <typename T, int LAYOUT, int TM, int TN, int WM, int WN, bool VEC>
 __global__ __launch_bounds__(64 * WM * WN, 2) void linear_gemm_kernel(const LinearGemm a) {
 #ifdef __HIP_DEVICE_COMPILE__   // the host pass, which cannot take the scalar operands, needs the stub alone
-    constexpr int BM = TM * WM * 16, BN = TN * WN * 16, NW = WM * WN, BK = kStepK;
+    constexpr int HM = TM * WM * 16, HN = TN * WN * 16, NW = WM * WN;     // rows and columns of a half
     constexpr bool AK = LAYOUT != LAYOUT_TN, BKC = LAYOUT == LAYOUT_NT;
-    using TA = OperandTile<T, BM, NW, AK>;
-    using TB = OperandTile<T, BN, NW, BKC>;
+    using TA = OperandTile<T, HM, NW, AK>;
+    using TB = OperandTile<T, HN, NW, BKC>;
     using v8 = typename Mma<T>::v8;
-    static_assert(S == 2 || S == 4, "the loop is unrolled over the stages and the two fragment sets");
-    __shared__ __attribute__((aligned(128))) T sa0[TA::VALUES], sb0[TB::VALUES], sa1[TA::VALUES], sb1[TB::VALUES];
-    __shared__ __attribute__((aligned(128))) T sa2[S > 2 ? TA::VALUES : 8], sb2[S > 2 ? TB::VALUES : 8];
-    __shared__ __attribute__((aligned(128))) T sa3[S > 2 ? TA::VALUES : 8], sb3[S > 2 ? TB::VALUES : 8];
-    const int64_t tm = (a.M + BM - 1) / BM, tn = (a.N + BN - 1) / BN;
+    constexpr int BK = TA::BK, KK = BK / 32;
+    __shared__ __attribute__((aligned(128))) T sa[VEC ? 2 : 1][2][TA::VALUES];    // [stage][half]
+    __shared__ __attribute__((aligned(128))) T sb[VEC ? 2 : 1][2][TB::VALUES];
+    const int64_t tm = (a.M + 2 * HM - 1) / (2 * HM), tn = (a.N + 2 * HN - 1) / (2 * HN);
     int64_t bm, bn;
     tile_of(blockIdx.x, tm, tn, bm, bn);
-    const int64_t m0 = bm * BM, n0 = bn * BN;
+    const int64_t m0 = bm * 2 * HM, n0 = bn * 2 * HN;
     const int64_t k0 = blockIdx.y * a.kper, k1 = k0 + a.kper < a.K ? k0 + a.kper : a.K;
     const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int wm = (wave / WN) * TM * 16, wn = (wave % WN) * TN * 16;
+    const int wm = (wave / WN) * TM * 16, wn = (wave % WN) * TN * 16;      // the wave's part of a half
+    // first rows of the halves at the first k; steps of a stage
     const T *pa = static_cast<const T *>(a.A) + (AK ? m0 * a.lda + k0 : k0 * a.lda + m0);
     const T *pb = static_cast<const T *>(a.B) + (BKC ? n0 * a.ldb + k0 : k0 * a.ldb + n0);
-    const int64_t sa_step = AK ? BK : BK * a.lda, sb_step = BKC ? BK : BK * a.ldb;
+    const int64_t a_half = AK ? HM * a.lda : HM, b_half = BKC ? HN * a.ldb : HN;
+    const int64_t a_step = AK ? BK : BK * a.lda, b_step = BKC ? BK : BK * a.ldb;
 
-    f32x4 acc[TM][TN];
+    f32x4 acc[2][2][TM][TN];
 #pragma unroll
-    for (int i = 0; i < TM; ++i)
+    for (int i = 0; i < 4 * TM * TN; ++i) (&acc[0][0][0][0])[i] = f32x4{0, 0, 0, 0};
+    auto read_a = [&](const T *t, v8 (&f)[KK][TM]) __attribute__((always_inline)) {
 #pragma unroll
-        for (int j = 0; j < TN; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
-    constexpr int H = TM / 2;       // row tiles of a half
-    auto read_b = [&](const T *t, v8 *f) __attribute__((always_inline)) {
+        for (int kk = 0; kk < KK; ++kk)
 #pragma unroll
-        for (int j = 0; j < TN; ++j) f[j] = TB::frag(t, wn + j * 16);
+            for (int i = 0; i < TM; ++i) f[kk][i] = TA::frag(t, wm + i * 16, kk);
     };
-    auto read_a = [&](const T *t, v8 *f, int half) __attribute__((always_inline)) {
+    auto read_b = [&](const T *t, v8 (&f)[KK][TN]) __attribute__((always_inline)) {
 #pragma unroll
-        for (int i = 0; i < H; ++i) f[i] = TA::frag(t, wm + (half * H + i) * 16);
+        for (int kk = 0; kk < KK; ++kk)
+#pragma unroll
+            for (int j = 0; j < TN; ++j) f[kk][j] = TB::frag(t, wn + j * 16, kk);
     };
-    auto multiply = [&](const v8 *fa, const v8 *fb, int half) __attribute__((always_inline)) {
+    auto multiply = [&](const v8 (&fa)[KK][TM], const v8 (&fb)[KK][TN], f32x4 (&o)[TM][TN]) __attribute__((always_inline)) {
 #pragma unroll
-        for (int p = 0; p < Mma<T>::kParts; ++p)
+        for (int kk = 0; kk < KK; ++kk)
 #pragma unroll
-            for (int i = 0; i < H; ++i)
+            for (int p = 0; p < Mma<T>::kParts; ++p)
 #pragma unroll
-                for (int j = 0; j < TN; ++j) acc[half * H + i][j] = Mma<T>::mma(fb[j], fa[i], acc[half * H + i][j], p);
+                for (int i = 0; i < TM; ++i)
+#pragma unroll
+                    for (int j = 0; j < TN; ++j) o[i][j] = Mma<T>::mma(fb[kk][j], fa[kk][i], o[i][j], p);
     };
-    TA ta;
-    TB tb;
+    v8 a0[KK][TM], a1[KK][TM], b0[KK][TN], b1[KK][TN];
+    const int stages = (int)((k1 - k0 + BK - 1) / BK);
+    TA ta[2];
+    TB tb[2];
     if constexpr (VEC) {
-        constexpr int kLoads = TA::N + TB::N, kLeft = (S - 2) * kLoads;
-        ta.prepare(a.lda, a.M - m0);
-        tb.prepare(a.ldb, a.N - n0);
-        const int steps = (int)((k1 - k0 + BK - 1) / BK), full = (int)((k1 - k0) / BK);
-        int next = 0;              // the next step to bring
-        auto bring = [&](T *na, T *nb, bool whole) __attribute__((always_inline)) {
-            const int kl = whole || next < full ? BK : (int)(k1 - k0) - next * BK;
-            ta.issue(pa, na, kl);
-            tb.issue(pb, nb, kl);
-            pa += sa_step;
-            pb += sb_step;
-            ++next;
+        constexpr int L = TA::N + TB::N;      // loads of one half of each operand
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            ta[h].prepare(a.lda, a.M - m0 - h * HM);
+            tb[h].prepare(a.ldb, a.N - n0 - h * HN);
+        }
+        auto bring = [&](int s, int h, bool whole) __attribute__((always_inline)) {
+            const int64_t left = k1 - k0 - (int64_t)s * BK;
+            const int kl = whole || left >= BK ? BK : (int)left;
+            ta[h].issue(pa + s * a_step + h * a_half, sa[s & 1][h], kl);
+            tb[h].issue(pb + s * b_step + h * b_half, sb[s & 1][h], kl);
         };
-        // waits until the oldest stage of this wave's loads is there (with `deep`, S - 2 stages behind it may
-        // still travel) and its LDS reads are done, then for the other waves
-        auto arrive = [&](bool deep) __attribute__((always_inline)) {
-            if (deep) wait_loads_and_barrier<kLeft>();
+        // one stage; more1, more2, more3: that many stages follow
+        auto stage = [&](int s, bool more1, bool more2, bool more3) __attribute__((always_inline)) {
+            const int at = s & 1;
+            if (more1) wait_loads_and_barrier<2 * L>();     // A1, B1 of this stage have arrived
             else wait_loads_and_barrier<0>();
-        };
-        v8 lo[H], hi[H], b0[TN], b1[TN];
-        if (steps > 0) bring(sa0, sb0, false);
-        if (steps > 1) bring(sa1, sb1, false);
-        if (S > 2 && steps > 2) bring(sa2, sb2, false);
-        if (S > 2 && steps > 3) bring(sa3, sb3, false);
-        if (steps > 0) {
-            arrive(false);
-            read_b(sb0, b0);
-            read_a(sa0, lo, 0);
-        }
-        // one step in stage (ca, cb); the fragments of the next come from (na, nb).  At the barrier every
-        // wave has all it needs of (ca, cb), which then takes the step S ahead.
-        auto step = [&](T *ca, T *cb, const T *na, const T *nb, const v8 *fb, v8 *gb) __attribute__((always_inline)) {
-            read_a(ca, hi, 1);
-            __builtin_amdgcn_sched_barrier(0);      // reads first: products of the half before hide them
-            multiply(lo, fb, 0);
-            arrive(true);
-            read_b(nb, gb);
-            read_a(na, lo, 0);
-            bring(ca, cb, true);
+            if (more2) bring(s + 2, 0, more3);
+            read_b(sb[at][1], b1);
+            read_a(sa[at][1], a1);
+            __builtin_amdgcn_sched_barrier(0);              // reads first: the products hide them
+            multiply(a0, b0, acc[0][0]);
+            multiply(a0, b1, acc[0][1]);
+            if (more2) wait_loads_and_barrier<2 * L>();     // A0, B0 of the next
+            else if (more1) wait_loads_and_barrier<L>();
+            if (more2) bring(s + 2, 1, more3);
+            if (more1) read_a(sa[at ^ 1][0], a0);
             __builtin_amdgcn_sched_barrier(0);
-            multiply(hi, fb, 1);
+            multiply(a1, b0, acc[1][0]);
+            if (more1) read_b(sb[at ^ 1][0], b0);
+            __builtin_amdgcn_sched_barrier(0);
+            multiply(a1, b1, acc[1][1]);
         };
-        // the same near the end, where there may be no next step and nothing left to bring
-        auto last = [&](int k, T *ca, T *cb, const T *na, const T *nb, const v8 *fb, v8 *gb) __attribute__((always_inline)) {
-            read_a(ca, hi, 1);
-            multiply(lo, fb, 0);
-            if (k + 1 < steps) {
-                arrive(k + S - 1 < steps);
-                if (k + S < steps) bring(ca, cb, false);
-                read_b(nb, gb);
-                read_a(na, lo, 0);
-            }
-            multiply(hi, fb, 1);
-        };
-        int k = 0;
-        for (; k + 2 * S <= full; k += S) {
-            step(sa0, sb0, sa1, sb1, b0, b1);
-            if constexpr (S == 2) {
-                step(sa1, sb1, sa0, sb0, b1, b0);
+        if (stages > 0) {
+            bring(0, 0, false);
+            bring(0, 1, false);
+            if (stages > 1) {
+                bring(1, 0, false);
+                bring(1, 1, false);
+                wait_loads_and_barrier<3 * L>();
             } else {
-                step(sa1, sb1, sa2, sb2, b1, b0);
-                step(sa2, sb2, sa3, sb3, b0, b1);
-                step(sa3, sb3, sa0, sb0, b1, b0);
+                wait_loads_and_barrier<L>();
             }
-        }
-        for (; k < steps; k += S) {
-            last(k, sa0, sb0, sa1, sb1, b0, b1);
-            if constexpr (S == 2) {
-                if (k + 1 < steps) last(k + 1, sa1, sb1, sa0, sb0, b1, b0);
-            } else {
-                if (k + 1 < steps) last(k + 1, sa1, sb1, sa2, sb2, b1, b0);
-                if (k + 2 < steps) last(k + 2, sa2, sb2, sa3, sb3, b0, b1);
-                if (k + 3 < steps) last(k + 3, sa3, sb3, sa0, sb0, b1, b0);
-            }
+            read_a(sa[0][0], a0);
+            read_b(sb[0][0], b0);
+            int s = 0;
+            for (; s + 3 < stages; ++s) stage(s, true, true, true);
+            if (s + 2 < stages) stage(s++, true, true, false);
+            if (s + 1 < stages) stage(s++, true, false, false);
+            stage(s, false, false, false);
         }
     } else {
-        uint4 ra[TA::N], rb[TB::N];
-        auto fetch = [&](int64_t k) __attribute__((always_inline)) {
-            const int kl = k1 - k < BK ? (int)(k1 - k) : BK;
-            ta.fetch(pa, a.lda, a.M - m0, kl, ra);
-            tb.fetch(pb, a.ldb, a.N - n0, kl, rb);
-            pa += sa_step;
-            pb += sb_step;
+        uint4 ra[2][TA::N], rb[2][TB::N];
+        auto fetch = [&](int s) __attribute__((always_inline)) {
+            const int64_t left = k1 - k0 - (int64_t)s * BK;
+            const int kl = left < BK ? (int)left : BK;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                ta[h].fetch(pa + s * a_step + h * a_half, a.lda, a.M - m0 - h * HM, kl, ra[h]);
+                tb[h].fetch(pb + s * b_step + h * b_half, a.ldb, a.N - n0 - h * HN, kl, rb[h]);
+            }
         };
-        auto step = [&](int64_t k, T *ca, T *cb) __attribute__((always_inline)) {
-            v8 fa[H], fb[TN];
-            TA::put(ca, ra);
-            TB::put(cb, rb);
+        if (stages > 0) fetch(0);
+        for (int s = 0; s < stages; ++s) {
             __syncthreads();
-            if (k + BK < k1) fetch(k + BK);
-            read_b(cb, fb);
-            read_a(ca, fa, 0);
-            multiply(fa, fb, 0);
-            read_a(ca, fa, 1);
-            multiply(fa, fb, 1);
-        };
-        if (k0 < k1) fetch(k0);
-        for (int64_t k = k0; k < k1; k += 2 * BK) {
-            step(k, sa0, sb0);
-            if (k + BK < k1) step(k + BK, sa1, sb1);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                TA::put(sa[0][h], ra[h]);
+                TB::put(sb[0][h], rb[h]);
+            }
+            __syncthreads();
+            if (s + 1 < stages) fetch(s + 1);
+            read_a(sa[0][0], a0);
+            read_b(sb[0][0], b0);
+            multiply(a0, b0, acc[0][0]);
+            read_b(sb[0][1], b1);
+            multiply(a0, b1, acc[0][1]);
+            read_a(sa[0][1], a1);
+            multiply(a1, b1, acc[1][1]);
+            multiply(a1, b0, acc[1][0]);
         }
     }
     if (a.quads && !a.part) {
         // every row of every tensor in whole, aligned quads: 32-bit places in views of the tile, no branches
         struct Q { T v[4]; };
-        const int64_t at = m0 + wm, col = n0 + wn;
-        const auto vc = wide_view(static_cast<T *>(a.C) + at * a.ldc + col), vr = wide_view(static_cast<const T *>(a.res) + at * a.ldr + col),
-                   vp = wide_view(static_cast<T *>(a.pre) + at * a.ldp + col), vb = wide_view(static_cast<const T *>(a.bias) + col);
-        const int rows = a.M - at < TM * 16 ? (int)(a.M - at) : TM * 16, cols = a.N - col < TN * 16 ? (int)(a.N - col) : TN * 16;
-        float bias[TN][4];
+        const auto vc = wide_view(static_cast<T *>(a.C) + m0 * a.ldc + n0), vr = wide_view(static_cast<const T *>(a.res) + m0 * a.ldr + n0),
+                   vp = wide_view(static_cast<T *>(a.pre) + m0 * a.ldp + n0), vb = wide_view(static_cast<const T *>(a.bias) + n0);
+        const int rows = a.M - m0 < 2 * HM ? (int)(a.M - m0) : 2 * HM, cols = a.N - n0 < 2 * HN ? (int)(a.N - n0) : 2 * HN;
 #pragma unroll
-        for (int j = 0; j < TN; ++j) {
-            const Q q = view_load_wide<Q>(vb, a.bias && j * 16 + g * 4 < cols ? (j * 16 + g * 4) * (uint32_t)sizeof(T) : kSkip);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) bias[j][e] = (float)q.v[e];
-        }
-#pragma unroll
-        for (int i = 0; i < TM; ++i) {
-            const int row = i * 16 + c;
+        for (int hb = 0; hb < 2; ++hb)
 #pragma unroll
             for (int j = 0; j < TN; ++j) {
-                const bool in = row < rows && j * 16 + g * 4 < cols;
-                const uint32_t x = (uint32_t)(j * 16 + g * 4) * (uint32_t)sizeof(T);
-                float f[4];
-                Q q;
+                const int col = hb * HN + wn + j * 16 + g * 4;
+                const uint32_t x = (uint32_t)col * (uint32_t)sizeof(T);
+                const Q qb = view_load_wide<Q>(vb, a.bias && col < cols ? x : kSkip);
+                float bias[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) f[e] = acc[i][j][e] + bias[j][e];
-                if (a.pre) {
+                for (int e = 0; e < 4; ++e) bias[e] = (float)qb.v[e];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) q.v[e] = (T)f[e];
-                    view_store(vp, in ? (uint32_t)(row * (uint32_t)a.ldp) * (uint32_t)sizeof(T) + x : kSkip, q);
-                }
-                if (a.act != ACT_NONE) {
+                for (int ha = 0; ha < 2; ++ha)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) f[e] = act_value(f[e], a.act);
-                }
-                if (a.res) {
-                    q = view_load_wide<Q>(vr, in ? (uint32_t)(row * (uint32_t)a.ldr) * (uint32_t)sizeof(T) + x : kSkip);
+                    for (int i = 0; i < TM; ++i) {
+                        const int row = ha * HM + wm + i * 16 + c;
+                        const bool in = row < rows && col < cols;
+                        float f[4];
+                        Q q;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) f[e] += (float)q.v[e];
-                }
+                        for (int e = 0; e < 4; ++e) f[e] = acc[ha][hb][i][j][e] + bias[e];
+                        if (a.pre) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) q.v[e] = (T)f[e];
-                view_store(vc, in ? (uint32_t)(row * (uint32_t)a.ldc) * (uint32_t)sizeof(T) + x : kSkip, q);
+                            for (int e = 0; e < 4; ++e) q.v[e] = (T)f[e];
+                            view_store(vp, in ? (uint32_t)(row * (uint32_t)a.ldp) * (uint32_t)sizeof(T) + x : kSkip, q);
+                        }
+                        if (a.act != ACT_NONE) {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) f[e] = act_value(f[e], a.act);
+                        }
+                        if (a.res) {
+                            q = view_load_wide<Q>(vr, in ? (uint32_t)(row * (uint32_t)a.ldr) * (uint32_t)sizeof(T) + x : kSkip);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) f[e] += (float)q.v[e];
+                        }
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) q.v[e] = (T)f[e];
+                        view_store(vc, in ? (uint32_t)(row * (uint32_t)a.ldc) * (uint32_t)sizeof(T) + x : kSkip, q);
+                    }
             }
-        }
         return;
     }
 #pragma unroll
-    for (int i = 0; i < TM; ++i) {
-        const int64_t m = m0 + wm + i * 16 + c;
-        if (m >= a.M) continue;
+    for (int ha = 0; ha < 2; ++ha)
 #pragma unroll
-        for (int j = 0; j < TN; ++j) {
-            const int64_t n = n0 + wn + j * 16 + g * 4;
-            if (n >= a.N) continue;
-            float f[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
-            if (a.part) {
-                float *p = a.part + ((int64_t)blockIdx.y * a.M + m) * a.N + n;
-                store_quad(p, a.N - n < 4 ? (int)(a.N - n) : 4, a.N % 4 == 0, f);
-            } else {
-                linear_epilogue<T>(a, m, n, f);
-            }
+        for (int i = 0; i < TM; ++i) {
+            const int64_t m = m0 + ha * HM + wm + i * 16 + c;
+            if (m >= a.M) continue;
+#pragma unroll
+            for (int hb = 0; hb < 2; ++hb)
+#pragma unroll
+                for (int j = 0; j < TN; ++j) {
+                    const int64_t n = n0 + hb * HN + wn + j * 16 + g * 4;
+                    if (n >= a.N) continue;
+                    float f[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) f[e] = acc[ha][hb][i][j][e];
+                    if (a.part) {
+                        float *p = a.part + ((int64_t)blockIdx.y * a.M + m) * a.N + n;
+                        store_quad(p, a.N - n < 4 ? (int)(a.N - n) : 4, a.N % 4 == 0, f);
+                    } else {
+                        linear_epilogue<T>(a, m, n, f);
+                    }
+                }
         }
-    }
 #endif
 }
 
@@ -626,16 +622,14 @@ static hipError_t gemm_layout(const LinearGemm &a, int tile, bool vec, hipStream
     auto blocks = [&](int bm, int bn) {
         return dim3((unsigned)(((a.M + bm - 1) / bm) * ((a.N + bn - 1) / bn)), (unsigned)a.splits);
     };
-    constexpr int S = sizeof(T) == 2 ? 4 : 2;      // stages of the 128 tile: 64 KB
     if (!vec) {
-        linear_gemm_kernel<T, LAYOUT, 4, 4, 2, 2, 2, false><<<blocks(128, 128), 256, 0, stream>>>(a);
+        linear_gemm_kernel<T, LAYOUT, 2, 2, 2, 2, false><<<blocks(128, 128), 256, 0, stream>>>(a);
     } else if (tile == 256) {
-        if constexpr (sizeof(T) == 2)
-            linear_gemm_kernel<T, LAYOUT, 8, 4, 2, 4, 4, true><<<blocks(256, 256), 512, 0, stream>>>(a);
+        if constexpr (sizeof(T) == 2) linear_gemm_kernel<T, LAYOUT, 4, 2, 2, 4, true><<<blocks(256, 256), 512, 0, stream>>>(a);
     } else if (tile == 128) {
-        linear_gemm_kernel<T, LAYOUT, 4, 4, 2, 2, S, true><<<blocks(128, 128), 256, 0, stream>>>(a);
+        linear_gemm_kernel<T, LAYOUT, 2, 2, 2, 2, true><<<blocks(128, 128), 256, 0, stream>>>(a);
     } else {
-        linear_gemm_kernel<T, LAYOUT, 2, 2, 2, 2, S, true><<<blocks(64, 64), 256, 0, stream>>>(a);
+        linear_gemm_kernel<T, LAYOUT, 1, 1, 2, 2, true><<<blocks(64, 64), 256, 0, stream>>>(a);
     }
     return hipGetLastError();
 }

@@ -112,10 +112,13 @@ __device__ __forceinline__ void lds_load16(const void *p, void *dst, uint32_t of
 // way, then for the other waves of the workgroup.
 template <int LEFT> __device__ __forceinline__ void wait_loads_and_barrier() {
     static_assert(LEFT < 64, "six bits");
+    // products before the wait are issued before it: they are what it hides behind
+    __builtin_amdgcn_sched_barrier(0);
     asm volatile("" ::: "memory");
     __builtin_amdgcn_s_waitcnt((LEFT & 15) | 0x70 | (LEFT >> 4) << 14);
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
 }
 
 }  // namespace fftconv

@@ -537,15 +537,15 @@ struct GemmPlan {
 // Tile and split of K for an M x N x K product.  A tile must leave enough workgroups for 256 CUs;
 // where even small tiles do not, K is split and the partial sums joined by a second kernel.
 GemmPlan plan_gemm(int64_t M, int64_t N, int64_t K, int dt, bool vec) {
-    const int64_t bk = 32;     // K of a step
+    const int64_t bk = 128 / elem_bytes(dt);     // K of a stage
     auto tiles = [&](int64_t t) { return ceil_div(M, t) * ceil_div(N, t); };
     GemmPlan p{128, 1, round_up(std::max<int64_t>(K, 1), bk)};
     if (vec && dt != FFTCONV_F32 && tiles(256) >= 200) p.tile = 256;
     else if (vec && tiles(128) < 256) p.tile = 64;
     const int64_t n = tiles(p.tile);
     const int64_t steps = ceil_div(K, bk);
-    if (n < 256 && steps >= 32) {
-        const int64_t want = std::min(ceil_div(512, n), steps / 16);
+    if (n < 256 && steps >= 16) {
+        const int64_t want = std::min(ceil_div(512, n), steps / 8);
         if (want > 1) {
             p.kper = ceil_div(steps, want) * bk;
             p.splits = (int)ceil_div(K, p.kper);
