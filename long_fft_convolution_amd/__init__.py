@@ -133,6 +133,16 @@ def _stream(stream, device):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _raw_stream(stream, device):
+    """The stream's handle as an integer, without making a Stream object for the current one."""
+    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
+
+
+def _at(t):
+    """A tensor's address for a pointer argument."""
+    return None if t is None else t.data_ptr()
+
+
 def _dev_tensor(t, name):
     if t is None:
         return
@@ -376,14 +386,20 @@ def _dtype_of(dtype) -> int:
     return dtype if isinstance(dtype, int) else dtype_code(dtype)
 
 
-def _rows_tensor(t, name, like, dims):
+def _rows_tensor(t, name, like, shape):
     """Checks a tensor argument whose rows must be contiguous (other strides are free)."""
-    if not t.is_cuda or t.device != like.device:
-        raise ValueError(f"{name} must be a tensor on {like.device}" if like.is_cuda else f"{name} must be a device tensor")
+    # the common case in few steps: this is on the path of a single token
+    if t.dtype is like.dtype and t.shape == shape and t.device == like.device and t.is_cuda and \
+            (t.is_contiguous() or t.stride(-1) == 1):
+        return
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if t.device != like.device:
+        raise ValueError(f"{name} must be on {like.device}")
     if t.dtype != like.dtype:
         raise ValueError(f"{name} must have dtype {like.dtype}")
-    if t.dim() != dims:
-        raise ValueError(f"{name} must have {dims} dimensions")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
     if t.stride(-1) != 1 and t.shape[-1] > 1:
         raise ValueError(f"{name} must be contiguous along its last dimension")
 
@@ -391,14 +407,19 @@ def _rows_tensor(t, name, like, dims):
 def _plain_tensor(t, name, dtype, shape, device):
     if t is None:
         return
-    if not t.is_cuda or t.device != device or t.dtype != dtype or not t.is_contiguous():
+    if t.dtype is not dtype or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor on {device}")
-    if shape is not None and tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {shape}, not {tuple(t.shape)}")
 
 
+_strides_of = {n: ctypes.c_int64 * n for n in (5, 6, 8, 12, 21)}
+
+
 def _strides(tensors, packed):
-    """(batch, token, head) of each tensor; None (an absent gradient) counts as dense zeros."""
+    """(batch, token, head) of each tensor, None where all are dense (an absent gradient counts as dense)."""
+    if all(t is None or t.is_contiguous() for t in tensors):
+        return None
     flat = []
     for t in tensors:
         if t is None:
@@ -407,7 +428,7 @@ def _strides(tensors, packed):
             flat += (0, t.stride(0), t.stride(1))
         else:
             flat += t.stride()[:3]
-    return (ctypes.c_int64 * len(flat))(*flat)
+    return _strides_of[len(flat)](*flat)
 
 
 def _nbytes(t):
@@ -415,21 +436,21 @@ def _nbytes(t):
 
 
 def _decay_shapes(q, k, v, log_decay, cu_seqlens):
+    qs, ks, vs = q.shape, k.shape, v.shape
     dims = 4 if cu_seqlens is None else 3
-    _rows_tensor(q, "q", q, dims)
-    _rows_tensor(k, "k", q, dims)
-    _rows_tensor(v, "v", q, dims)
-    lead = tuple(q.shape[:-2])
-    if tuple(k.shape[:-2]) != lead or tuple(v.shape[:-1]) != tuple(k.shape[:-1]) or k.shape[-1] != q.shape[-1]:
-        raise ValueError(f"shapes of q {tuple(q.shape)}, k {tuple(k.shape)}, v {tuple(v.shape)} do not match")
-    H, Hk, Dk, Dv = q.shape[-2], k.shape[-2], q.shape[-1], v.shape[-1]
+    if len(qs) != dims or len(ks) != dims or len(vs) != dims:
+        raise ValueError(f"q, k and v must have {dims} dimensions, not {len(qs)}, {len(ks)} and {len(vs)}")
+    H, Hk, Dk, Dv = qs[-2], ks[-2], qs[-1], vs[-1]
+    _rows_tensor(q, "q", q, qs)
+    _rows_tensor(k, "k", q, (*qs[:-2], Hk, Dk))
+    _rows_tensor(v, "v", q, (*qs[:-2], Hk, Dv))
     _plain_tensor(log_decay, "log_decay", torch.float32, (H,), q.device)
     if cu_seqlens is None:
-        return lead[0], lead[1], H, Hk, Dk, Dv
-    _plain_tensor(cu_seqlens, "cu_seqlens", torch.int32, None, q.device)
+        return qs[0], qs[1], H, Hk, Dk, Dv
     if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
         raise ValueError("cu_seqlens must hold B + 1 values")
-    return cu_seqlens.numel() - 1, lead[0], H, Hk, Dk, Dv
+    _plain_tensor(cu_seqlens, "cu_seqlens", torch.int32, cu_seqlens.shape, q.device)
+    return cu_seqlens.numel() - 1, qs[0], H, Hk, Dk, Dv
 
 
 def fftconv_decay_fwd_workspace_bytes(B: int, T: int, H: int, Dk: int, Dv: int, dtype) -> int:
@@ -445,43 +466,46 @@ def fftconv_decay_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_dec
     state_in / state_out: fp32 (B, H, Dk, Dv), or pools of such matrices with state_slots (B) int32.
     """
     B, N, H, Hk, Dk, Dv = _decay_shapes(q, k, v, log_decay, cu_seqlens)
-    _rows_tensor(out, "out", q, q.dim())
-    if tuple(out.shape) != (*q.shape[:-1], Dv):
-        raise ValueError(f"out must have shape {(*q.shape[:-1], Dv)}")
-    n_slots = 0
+    _rows_tensor(out, "out", q, (*q.shape[:-1], Dv))
+    n_slots, device = 0, q.device
     if state_slots is not None:
-        _plain_tensor(state_slots, "state_slots", torch.int32, (B,), q.device)
+        _plain_tensor(state_slots, "state_slots", torch.int32, (B,), device)
         pool = state_in if state_in is not None else state_out
         n_slots = pool.shape[0] if pool is not None else 0
-    for name, t in (("state_in", state_in), ("state_out", state_out)):
-        _plain_tensor(t, name, torch.float32, (B if state_slots is None else n_slots, H, Dk, Dv), q.device)
+    states = (B if state_slots is None else n_slots, H, Dk, Dv)
+    _plain_tensor(state_in, "state_in", torch.float32, states, device)
+    _plain_tensor(state_out, "state_out", torch.float32, states, device)
     _dev_tensor(workspace, "workspace")
-    _check(_load().fftconv_decay_fwd(
-        _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(out), _strides((q, k, v, out), cu_seqlens is not None),
-        _ptr(state_in), _ptr(state_out), _ptr(state_slots), n_slots, _ptr(cu_seqlens), B, N, H, Hk, Dk, Dv, scale,
-        dtype_code(q.dtype), _ptr(workspace), _nbytes(workspace), _stream(stream, q.device)))
+    _check((_lib or _load()).fftconv_decay_fwd(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), out.data_ptr(),
+        _strides((q, k, v, out), cu_seqlens is not None), _at(state_in), _at(state_out), _at(state_slots), n_slots,
+        _at(cu_seqlens), B, N, H, Hk, Dk, Dv, scale, _DTYPE_CODE[q.dtype], _at(workspace), _nbytes(workspace),
+        _raw_stream(stream, device)))
 
 
 def fftconv_decay_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor,
                        state: torch.Tensor, out: torch.Tensor, scale: float, state_slots: torch.Tensor | None = None,
                        stream=None) -> None:
     """One token of each sequence: q (B, H, Dk), k (B, Hk, Dk), v (B, Hk, Dv) -> out (B, H, Dv), state in place."""
-    for name, t in (("q", q), ("k", k), ("v", v), ("out", out)):
-        _rows_tensor(t, name, q, 3)
-    (B, H, Dk), (Hk, Dv) = q.shape, v.shape[1:]
-    if tuple(k.shape) != (B, Hk, Dk) or v.shape[0] != B or tuple(out.shape) != (B, H, Dv):
-        raise ValueError(f"shapes of q {tuple(q.shape)}, k {tuple(k.shape)}, v {tuple(v.shape)}, "
-                         f"out {tuple(out.shape)} do not match")
-    _plain_tensor(log_decay, "log_decay", torch.float32, (H,), q.device)
+    if q.dim() != 3 or v.dim() != 3:
+        raise ValueError("q and v must have 3 dimensions")
+    (B, H, Dk), (_, Hk, Dv), device = q.shape, v.shape, q.device
+    _rows_tensor(q, "q", q, (B, H, Dk))
+    _rows_tensor(k, "k", q, (B, Hk, Dk))
+    _rows_tensor(v, "v", q, (B, Hk, Dv))
+    _rows_tensor(out, "out", q, (B, H, Dv))
+    _plain_tensor(log_decay, "log_decay", torch.float32, (H,), device)
     n_slots = 0
     if state_slots is not None:
-        _plain_tensor(state_slots, "state_slots", torch.int32, (B,), q.device)
+        _plain_tensor(state_slots, "state_slots", torch.int32, (B,), device)
         n_slots = state.shape[0]
-    _plain_tensor(state, "state", torch.float32, (B if state_slots is None else n_slots, H, Dk, Dv), q.device)
-    strides = (ctypes.c_int64 * 8)(*q.stride()[:2], *k.stride()[:2], *v.stride()[:2], *out.stride()[:2])
-    _check(_load().fftconv_decay_step(
-        _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(state), _ptr(out), strides, _ptr(state_slots), n_slots,
-        B, H, Hk, Dk, Dv, scale, dtype_code(q.dtype), _stream(stream, q.device)))
+    _plain_tensor(state, "state", torch.float32, (B if state_slots is None else n_slots, H, Dk, Dv), device)
+    strides = None
+    if not (q.is_contiguous() and k.is_contiguous() and v.is_contiguous() and out.is_contiguous()):
+        strides = _strides_of[8](*q.stride()[:2], *k.stride()[:2], *v.stride()[:2], *out.stride()[:2])
+    _check((_lib or _load()).fftconv_decay_step(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), state.data_ptr(), out.data_ptr(), strides,
+        _at(state_slots), n_slots, B, H, Hk, Dk, Dv, scale, _DTYPE_CODE[q.dtype], _raw_stream(stream, device)))
 
 
 def fftconv_decay_bwd_workspace_bytes(B: int, T: int, H: int, Hk: int, Dk: int, Dv: int, dtype) -> int:
@@ -495,21 +519,18 @@ def fftconv_decay_bwd(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: t
                       workspace: torch.Tensor | None = None, stream=None) -> None:
     """Gradients of fftconv_decay_fwd into dq, dk, dv, dstate_in (None = skip)."""
     B, N, H, Hk, Dk, Dv = _decay_shapes(q, k, v, log_decay, cu_seqlens)
-    for name, t, shape in (("dout", dout, (*q.shape[:-1], Dv)), ("dq", dq, q.shape), ("dk", dk, k.shape),
-                           ("dv", dv, v.shape)):
-        if t is None and name != "dout":
-            continue
-        _rows_tensor(t, name, q, q.dim())
-        if tuple(t.shape) != tuple(shape):
-            raise ValueError(f"{name} must have shape {tuple(shape)}")
+    _rows_tensor(dout, "dout", q, (*q.shape[:-1], Dv))
+    for name, t, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
+        if t is not None:
+            _rows_tensor(t, name, q, like.shape)
     for name, t in (("state_in", state_in), ("dstate_out", dstate_out), ("dstate_in", dstate_in)):
         _plain_tensor(t, name, torch.float32, (B, H, Dk, Dv), q.device)
     _dev_tensor(workspace, "workspace")
-    _check(_load().fftconv_decay_bwd(
-        _ptr(dout), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(dq), _ptr(dk), _ptr(dv),
-        _strides((dout, q, k, v, dq, dk, dv), cu_seqlens is not None), _ptr(state_in), _ptr(dstate_out),
-        _ptr(dstate_in), _ptr(cu_seqlens), B, N, H, Hk, Dk, Dv, scale, dtype_code(q.dtype), _ptr(workspace),
-        _nbytes(workspace), _stream(stream, q.device)))
+    _check((_lib or _load()).fftconv_decay_bwd(
+        dout.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), _at(dq), _at(dk), _at(dv),
+        _strides((dout, q, k, v, dq, dk, dv), cu_seqlens is not None), _at(state_in), _at(dstate_out),
+        _at(dstate_in), _at(cu_seqlens), B, N, H, Hk, Dk, Dv, scale, _DTYPE_CODE[q.dtype], _at(workspace),
+        _nbytes(workspace), _raw_stream(stream, q.device)))
 
 
 def _scratch(nbytes, device):
@@ -551,17 +572,20 @@ def _activation(name) -> int:
     return ACTIVATIONS[name]
 
 
-def _matrices(like, *named):
-    for name, t, shape in named:
-        if t is None:
-            continue
-        _rows_tensor(t, name, like, len(shape))
-        if tuple(t.shape) != shape:
-            raise ValueError(f"{name} must have shape {shape}, not {tuple(t.shape)}")
-
-
 def _row_strides(*tensors):
-    return (ctypes.c_int64 * len(tensors))(*(0 if t is None else t.stride(0) for t in tensors))
+    """Row strides of the matrices, None where all are dense."""
+    if all(t is None or t.is_contiguous() for t in tensors):
+        return None
+    return _strides_of[len(tensors)](*(0 if t is None else t.stride(0) for t in tensors))
+
+
+def _linear_shapes(x, W):
+    if x.dim() != 2 or W.dim() != 2:
+        raise ValueError("x and W must have 2 dimensions")
+    (M, K), N = x.shape, W.shape[0]
+    _rows_tensor(x, "x", x, (M, K))
+    _rows_tensor(W, "W", x, (N, K))
+    return M, N, K
 
 
 def fftconv_linear_fwd_workspace_bytes(M: int, N: int, K: int, dtype) -> int:
@@ -572,16 +596,19 @@ def fftconv_linear_fwd(x: torch.Tensor, W: torch.Tensor, bias: torch.Tensor | No
                        out: torch.Tensor, pre: torch.Tensor | None = None, activation: str = "none",
                        workspace: torch.Tensor | None = None, stream=None) -> None:
     """out <- act(x W^T + bias) + residual for x (M, K), W (N, K); pre (optional) <- x W^T + bias."""
-    _rows_tensor(x, "x", x, 2)
-    _rows_tensor(W, "W", x, 2)
-    (M, K), N = x.shape, W.shape[0]
-    _matrices(x, ("W", W, (N, K)), ("bias", bias, (N,)), ("residual", residual, (M, N)), ("out", out, (M, N)),
-              ("pre", pre, (M, N)))
+    M, N, K = _linear_shapes(x, W)
+    _rows_tensor(out, "out", x, (M, N))
+    if bias is not None:
+        _rows_tensor(bias, "bias", x, (N,))
+    if residual is not None:
+        _rows_tensor(residual, "residual", x, (M, N))
+    if pre is not None:
+        _rows_tensor(pre, "pre", x, (M, N))
     _dev_tensor(workspace, "workspace")
-    _check(_load().fftconv_linear_fwd(
-        _ptr(x), _ptr(W), _ptr(bias), _ptr(residual), _ptr(out), _ptr(pre), _row_strides(x, W, residual, out, pre),
-        M, N, K, _activation(activation), dtype_code(x.dtype), _ptr(workspace), _nbytes(workspace),
-        _stream(stream, x.device)))
+    _check((_lib or _load()).fftconv_linear_fwd(
+        x.data_ptr(), W.data_ptr(), _at(bias), _at(residual), out.data_ptr(), _at(pre),
+        _row_strides(x, W, residual, out, pre), M, N, K, _activation(activation), _DTYPE_CODE[x.dtype],
+        _at(workspace), _nbytes(workspace), _raw_stream(stream, x.device)))
 
 
 def fftconv_linear_bwd_workspace_bytes(M: int, N: int, K: int, dtype) -> int:
@@ -592,16 +619,16 @@ def fftconv_linear_bwd(dout: torch.Tensor, x: torch.Tensor, W: torch.Tensor, pre
                        dx: torch.Tensor | None, dW: torch.Tensor | None, dbias: torch.Tensor | None,
                        activation: str = "none", workspace: torch.Tensor | None = None, stream=None) -> None:
     """Gradients of fftconv_linear_fwd into dx, dW, dbias (None = skip); the residual's is dout."""
-    _rows_tensor(x, "x", x, 2)
-    _rows_tensor(W, "W", x, 2)
-    (M, K), N = x.shape, W.shape[0]
-    _matrices(x, ("dout", dout, (M, N)), ("W", W, (N, K)), ("pre", pre, (M, N)), ("dx", dx, (M, K)),
-              ("dW", dW, (N, K)), ("dbias", dbias, (N,)))
+    M, N, K = _linear_shapes(x, W)
+    for name, t, shape in (("dout", dout, (M, N)), ("pre", pre, (M, N)), ("dx", dx, (M, K)), ("dW", dW, (N, K)),
+                           ("dbias", dbias, (N,))):
+        if t is not None:
+            _rows_tensor(t, name, x, shape)
     _dev_tensor(workspace, "workspace")
-    _check(_load().fftconv_linear_bwd(
-        _ptr(dout), _ptr(x), _ptr(W), _ptr(pre), _ptr(dx), _ptr(dW), _ptr(dbias),
-        _row_strides(dout, x, W, pre, dx, dW), M, N, K, _activation(activation), dtype_code(x.dtype),
-        _ptr(workspace), _nbytes(workspace), _stream(stream, x.device)))
+    _check((_lib or _load()).fftconv_linear_bwd(
+        _at(dout), x.data_ptr(), W.data_ptr(), _at(pre), _at(dx), _at(dW), _at(dbias),
+        _row_strides(dout, x, W, pre, dx, dW), M, N, K, _activation(activation), _DTYPE_CODE[x.dtype],
+        _at(workspace), _nbytes(workspace), _raw_stream(stream, x.device)))
 
 
 def linear_act(x, W, bias=None, residual=None, activation="none", keep_pre=False, stream=None):

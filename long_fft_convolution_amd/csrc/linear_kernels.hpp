@@ -269,10 +269,12 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void linear_gemm_kernel(const Line
     __shared__ __attribute__((aligned(128))) T sa[VEC ? 2 : 1][2][TA::VALUES];    // [stage][half]
     __shared__ __attribute__((aligned(128))) T sb[VEC ? 2 : 1][2][TB::VALUES];
     const int64_t tm = (a.M + 2 * HM - 1) / (2 * HM), tn = (a.N + 2 * HN - 1) / (2 * HN);
+    const bool whole = blockIdx.x < a.full;
+    const int64_t piece = blockIdx.x - a.full;         // of the split tiles
     int64_t bm, bn;
-    tile_of(blockIdx.x, tm, tn, bm, bn);
+    tile_of(whole ? blockIdx.x : a.full + piece / a.splits, tm, tn, bm, bn);
     const int64_t m0 = bm * 2 * HM, n0 = bn * 2 * HN;
-    const int64_t k0 = blockIdx.y * a.kper, k1 = k0 + a.kper < a.K ? k0 + a.kper : a.K;
+    const int64_t k0 = whole ? 0 : piece % a.splits * a.kper, k1 = !whole && k0 + a.kper < a.K ? k0 + a.kper : a.K;
     const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = (wave / WN) * TM * 16, wn = (wave % WN) * TN * 16;      // the wave's part of a half
@@ -329,16 +331,16 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void linear_gemm_kernel(const Line
             const int at = s & 1;
             if (more1) wait_loads_and_barrier<2 * L>();     // A1, B1 of this stage have arrived
             else wait_loads_and_barrier<0>();
-            if (more2) bring(s + 2, 0, more3);
             read_b(sb[at][1], b1);
             read_a(sa[at][1], a1);
+            if (more2) bring(s + 2, 0, more3);
             __builtin_amdgcn_sched_barrier(0);              // reads first: the products hide them
             multiply(a0, b0, acc[0][0]);
             multiply(a0, b1, acc[0][1]);
             if (more2) wait_loads_and_barrier<2 * L>();     // A0, B0 of the next
             else if (more1) wait_loads_and_barrier<L>();
-            if (more2) bring(s + 2, 1, more3);
             if (more1) read_a(sa[at ^ 1][0], a0);
+            if (more2) bring(s + 2, 1, more3);
             __builtin_amdgcn_sched_barrier(0);
             multiply(a1, b0, acc[1][0]);
             if (more1) read_b(sb[at ^ 1][0], b0);
@@ -394,7 +396,16 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void linear_gemm_kernel(const Line
             multiply(a1, b0, acc[1][0]);
         }
     }
-    if (a.quads && !a.part) {
+    if (!whole) {
+        float *part = a.part + piece * (4 * HM * HN);
+#pragma unroll
+        for (int i = 0; i < 4 * TM * TN; ++i) {
+            const int ha = i / (2 * TM * TN), hb = i / (TM * TN) % 2, r = i / TN % TM, j = i % TN;
+            *reinterpret_cast<f32x4 *>(part + (ha * HM + wm + r * 16 + c) * (2 * HN) + hb * HN + wn + j * 16 + g * 4) = acc[ha][hb][r][j];
+        }
+        return;
+    }
+    if (a.quads) {
         // every row of every tensor in whole, aligned quads: 32-bit places in views of the tile, no branches
         struct Q { T v[4]; };
         const auto vc = wide_view(static_cast<T *>(a.C) + m0 * a.ldc + n0), vr = wide_view(static_cast<const T *>(a.res) + m0 * a.ldr + n0),
@@ -456,89 +467,97 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void linear_gemm_kernel(const Line
                     float f[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) f[e] = acc[ha][hb][i][j][e];
-                    if (a.part) {
-                        float *p = a.part + ((int64_t)blockIdx.y * a.M + m) * a.N + n;
-                        store_quad(p, a.N - n < 4 ? (int)(a.N - n) : 4, a.N % 4 == 0, f);
-                    } else {
-                        linear_epilogue<T>(a, m, n, f);
-                    }
+                    linear_epilogue<T>(a, m, n, f);
                 }
         }
 #endif
 }
 
-// joins the splits of a product: sum of the partial sums in split order, then the epilogue
-template <typename T> __global__ __launch_bounds__(256) void linear_join_kernel(const LinearGemm a) {
-    const int64_t quads = (a.N + 3) / 4, total = a.M * quads;
-    for (int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-        const int64_t m = i / quads, n = i % quads * 4;
-        const int left = a.N - n < 4 ? (int)(a.N - n) : 4;
-        float f[4] = {0, 0, 0, 0};
-        for (int s = 0; s < a.splits; ++s) {
-            float t[4];
-            load_quad(a.part + ((int64_t)s * a.M + m) * a.N + n, left, a.N % 4 == 0, t);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) f[j] += t[j];
-        }
-        linear_epilogue<T>(a, m, n, f);
-    }
+// Joins the split tiles: sum of a tile's parts in their order, then the epilogue.  grid: (tile rows /
+// rows a workgroup takes, split tiles).
+template <typename T, int TILE> __global__ __launch_bounds__(256) void linear_join_kernel(const LinearGemm a) {
+    constexpr int kQuads = TILE / 4, kRows = 256 / kQuads;
+    const int64_t tm = (a.M + TILE - 1) / TILE, tn = (a.N + TILE - 1) / TILE;
+    int64_t bm, bn;
+    tile_of(a.full + blockIdx.y, tm, tn, bm, bn);
+    const int row = blockIdx.x * kRows + threadIdx.x / kQuads, col = threadIdx.x % kQuads * 4;
+    const int64_t m = bm * TILE + row, n = bn * TILE + col;
+    if (m >= a.M || n >= a.N) return;
+    const float *p = a.part + (int64_t)blockIdx.y * a.splits * (TILE * TILE) + row * TILE + col;
+    f32x4 sum = {0, 0, 0, 0};
+#pragma unroll 4
+    for (int s = 0; s < a.splits; ++s) sum += *reinterpret_cast<const f32x4 *>(p + (int64_t)s * (TILE * TILE));
+    float f[4] = {sum[0], sum[1], sum[2], sum[3]};
+    linear_epilogue<T>(a, m, n, f);
 }
 
-// Few rows (M <= 16 MT): bound by the bytes of W.  A wave multiplies 16 rows of W, read straight
-// from HBM in the operand layout, with the rows of x; the workgroup's waves share K and join in LDS.
-template <typename T, int MT, bool VEC>
-__global__ __launch_bounds__(256) void linear_rows_kernel(const LinearGemm a) {
-    constexpr int U = 4;
-    __shared__ f32x4 part[4][MT][64];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, c = lane & 15;
-    const int64_t n0 = (int64_t)blockIdx.x * 16;
-    const int64_t per = ((a.K + 31) / 32 + 3) / 4 * 32;
-    const int64_t k0 = wave * per, k1 = k0 + per < a.K ? k0 + per : a.K;
-    const T *pw = static_cast<const T *>(a.B) + (n0 + c) * a.ldb;
-    const T *px = static_cast<const T *>(a.A) + c * a.lda;
-    const bool wn = n0 + c < a.N;
-    typedef typename Mma<T>::v8 v8;
-    auto load8 = [&](const T *p, int64_t k, bool in) {
-        v8 v;
+// One to four rows: bound by the bytes of W; more rows take the tile kernel, whose 64 x 64 tiles stream W as
+// fast (26 us at 65 x 2560 -> 10240, where lanes that read 16 rows of W each in the matrix cores' operand
+// layout, 64 bytes a row, took 43 us at 64 rows).  A wave streams four rows of W, 16 bytes a lane, 1 KB of a row at a time, multiplies them with the rows of x
+// in fp32 and joins its lanes at the end.
+template <typename T, int M, bool VEC>
+__global__ __launch_bounds__(256) void linear_vector_kernel(const LinearGemm a) {
+    constexpr int E = 16 / (int)sizeof(T), R = 4, U = M == 1 ? 4 : 2;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t n0 = ((int64_t)blockIdx.x * 4 + wave) * R;
+    if (n0 >= a.N) return;
+    // VEC: value j of a lane's piece u is k0 + (u * 64 + lane) * E + j; else k0 + (u * E + j) * 64 + lane, value
+    // by value.  Loads past K take an offset out of range instead of a branch, so all of a batch are on
+    // their way together.
+    struct Piece { T v[E]; };
+    auto load = [&](const T *row, int64_t k0, int u) {
+        const auto view = wide_view(row + k0);
+        Piece q;
+        if constexpr (VEC) {
+            const int at = (u * 64 + lane) * E;
+            q = view_load_wide<Piece>(view, k0 + at < a.K ? (uint32_t)at * (uint32_t)sizeof(T) : kSkip);
+        } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = (T)0.0f;
-        if (VEC) {
-            if (in && k < k1) __builtin_memcpy(&v, __builtin_assume_aligned(p + k, 16), sizeof v);
-        } else if (in && k + 8 <= k1) {
-            __builtin_memcpy(&v, p + k, sizeof v);
-        } else if (in) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (k + j < k1) v[j] = p[k + j];
+            for (int j = 0; j < E; ++j) {
+                const int at = (u * E + j) * 64 + lane;
+                q.v[j] = view_load<T>(view, k0 + at < a.K ? (uint32_t)at * (uint32_t)sizeof(T) : kSkip);
+            }
         }
-        return v;
+        return q;
     };
-    f32x4 acc[MT];
+    const T *pw[R], *px[M];
 #pragma unroll
-    for (int i = 0; i < MT; ++i) acc[i] = f32x4{0, 0, 0, 0};
-    for (int64_t k = k0; k < k1; k += 32 * U) {
-        v8 w[U], x[U][MT];
+    for (int r = 0; r < R; ++r) pw[r] = static_cast<const T *>(a.B) + (n0 + r < a.N ? n0 + r : n0) * a.ldb;
 #pragma unroll
-        for (int u = 0; u < U; ++u) w[u] = load8(pw, k + u * 32 + g * 8, wn);
+    for (int m = 0; m < M; ++m) px[m] = static_cast<const T *>(a.A) + (m < a.M ? m : 0) * a.lda;
+    float sum[R][M];
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int m = 0; m < M; ++m) sum[r][m] = 0.0f;
+    for (int64_t k0 = 0; k0 < a.K; k0 += 64 * E * U) {
+        Piece w[U][R], x[U][M];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+#pragma unroll
+            for (int r = 0; r < R; ++r) w[u][r] = load(pw[r], k0, u);
+#pragma unroll
+            for (int m = 0; m < M; ++m) x[u][m] = load(px[m], k0, u);
+        }
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int i = 0; i < MT; ++i) x[u][i] = load8(px + (int64_t)i * 16 * a.lda, k + u * 32 + g * 8, i * 16 + c < a.M);
+            for (int j = 0; j < E; ++j)
 #pragma unroll
-        for (int u = 0; u < U; ++u)
+                for (int m = 0; m < M; ++m)
 #pragma unroll
-            for (int i = 0; i < MT; ++i) acc[i] = Mma<T>::mma(w[u], x[u][i], acc[i]);
+                    for (int r = 0; r < R; ++r) sum[r][m] = fmaf((float)w[u][r].v[j], (float)x[u][m].v[j], sum[r][m]);
     }
 #pragma unroll
-    for (int i = 0; i < MT; ++i) part[wave][i][lane] = acc[i];
-    __syncthreads();
-    for (int i = wave; i < MT; i += 4) {
-        const f32x4 s = part[0][i][lane] + part[1][i][lane] + part[2][i][lane] + part[3][i][lane];
-        const int64_t m = i * 16 + c, n = n0 + g * 4;
-        if (m < a.M && n < a.N) {
-            float f[4] = {s[0], s[1], s[2], s[3]};
-            linear_epilogue<T>(a, m, n, f);
+    for (int m = 0; m < M; ++m) {
+        float f[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            f[r] = sum[r][m];
+#pragma unroll
+            for (int s = 1; s < 64; s <<= 1) f[r] += __shfl_xor(f[r], s);
         }
+        if (lane == 0 && m < a.M) linear_epilogue<T>(a, m, n0, f);
     }
 }
 
@@ -619,17 +638,15 @@ __global__ __launch_bounds__(256) void linear_colsum_kernel(const float *colsum,
 // ---- host side of one storage type ----------------------------------------
 template <typename T, int LAYOUT>
 static hipError_t gemm_layout(const LinearGemm &a, int tile, bool vec, hipStream_t stream) {
-    auto blocks = [&](int bm, int bn) {
-        return dim3((unsigned)(((a.M + bm - 1) / bm) * ((a.N + bn - 1) / bn)), (unsigned)a.splits);
-    };
+    const unsigned grid = (unsigned)(a.full + (a.tiles - a.full) * a.splits);
     if (!vec) {
-        linear_gemm_kernel<T, LAYOUT, 2, 2, 2, 2, false><<<blocks(128, 128), 256, 0, stream>>>(a);
+        linear_gemm_kernel<T, LAYOUT, 2, 2, 2, 2, false><<<grid, 256, 0, stream>>>(a);
     } else if (tile == 256) {
-        if constexpr (sizeof(T) == 2) linear_gemm_kernel<T, LAYOUT, 4, 2, 2, 4, true><<<blocks(256, 256), 512, 0, stream>>>(a);
+        if constexpr (sizeof(T) == 2) linear_gemm_kernel<T, LAYOUT, 4, 2, 2, 4, true><<<grid, 512, 0, stream>>>(a);
     } else if (tile == 128) {
-        linear_gemm_kernel<T, LAYOUT, 2, 2, 2, 2, true><<<blocks(128, 128), 256, 0, stream>>>(a);
+        linear_gemm_kernel<T, LAYOUT, 2, 2, 2, 2, true><<<grid, 256, 0, stream>>>(a);
     } else {
-        linear_gemm_kernel<T, LAYOUT, 1, 1, 2, 2, true><<<blocks(64, 64), 256, 0, stream>>>(a);
+        linear_gemm_kernel<T, LAYOUT, 1, 1, 2, 2, true><<<grid, 256, 0, stream>>>(a);
     }
     return hipGetLastError();
 }
@@ -639,23 +656,20 @@ static hipError_t gemm_typed(const LinearGemm &a, int layout, int tile, bool vec
     hipError_t e = layout == LAYOUT_NT   ? gemm_layout<T, LAYOUT_NT>(a, tile, vec, stream)
                    : layout == LAYOUT_NN ? gemm_layout<T, LAYOUT_NN>(a, tile, vec, stream)
                                          : gemm_layout<T, LAYOUT_TN>(a, tile, vec, stream);
-    if (e != hipSuccess || !a.part) return e;
-    const int64_t n = (a.M * ((a.N + 3) / 4) + 255) / 256;
-    linear_join_kernel<T><<<(unsigned)(n < 4096 ? n : 4096), 256, 0, stream>>>(a);
+    const unsigned split = (unsigned)(a.tiles - a.full);
+    if (e != hipSuccess || split == 0) return e;
+    const dim3 grid((unsigned)(tile * tile / 1024), split);
+    if (tile == 256) linear_join_kernel<T, 256><<<grid, 256, 0, stream>>>(a);
+    else if (tile == 128) linear_join_kernel<T, 128><<<grid, 256, 0, stream>>>(a);
+    else linear_join_kernel<T, 64><<<grid, 256, 0, stream>>>(a);
     return hipGetLastError();
 }
 
-template <typename T> static hipError_t rows_typed(const LinearGemm &a, bool vec, hipStream_t stream) {
+template <typename T, bool VEC> static hipError_t vector_typed(const LinearGemm &a, hipStream_t stream) {
     const unsigned grid = (unsigned)((a.N + 15) / 16);
-#define FFTCONV_ROWS(MT)                                                                       \
-    do {                                                                                       \
-        if (vec) linear_rows_kernel<T, MT, true><<<grid, 256, 0, stream>>>(a);                 \
-        else linear_rows_kernel<T, MT, false><<<grid, 256, 0, stream>>>(a);                    \
-    } while (0)
-    if (a.M <= 16) FFTCONV_ROWS(1);
-    else if (a.M <= 32) FFTCONV_ROWS(2);
-    else FFTCONV_ROWS(4);
-#undef FFTCONV_ROWS
+    if (a.M == 1) linear_vector_kernel<T, 1, VEC><<<grid, 256, 0, stream>>>(a);
+    else if (a.M == 2) linear_vector_kernel<T, 2, VEC><<<grid, 256, 0, stream>>>(a);
+    else linear_vector_kernel<T, 4, VEC><<<grid, 256, 0, stream>>>(a);
     return hipGetLastError();
 }
 
@@ -675,8 +689,8 @@ static hipError_t dz_typed(const LinearDz &a, int64_t slabs, void *dbias, hipStr
     hipError_t launch_linear_gemm_##NAME(const LinearGemm &a, int layout, int tile, bool vec, hipStream_t s) {   \
         return gemm_typed<T>(a, layout, tile, vec, s);                                                           \
     }                                                                                                            \
-    hipError_t launch_linear_rows_##NAME(const LinearGemm &a, bool vec, hipStream_t s) {                         \
-        return rows_typed<T>(a, vec, s);                                                                         \
+    hipError_t launch_linear_vector_##NAME(const LinearGemm &a, bool vec, hipStream_t s) {                       \
+        return vec ? vector_typed<T, true>(a, s) : vector_typed<T, false>(a, s);                                 \
     }                                                                                                            \
     hipError_t launch_linear_dz_##NAME(const LinearDz &a, int64_t slabs, void *dbias, hipStream_t s) {           \
         return dz_typed<T>(a, slabs, dbias, s);                                                                  \

@@ -526,39 +526,56 @@ fftconv_status_t fftconv_decay_bwd(const void *dout, const void *q, const void *
 // ---- linear product -----------------------------------------------------------
 namespace {
 
-constexpr int64_t kRowsMost = 64;   // rows that the few-rows kernel takes
+constexpr int64_t kVectorRows = 4;   // rows that the kernel for single tokens takes
 
 struct GemmPlan {
-    int tile;
-    int splits;
-    int64_t kper;
+    int tile, splits;
+    int64_t tiles, full, kper;
 };
 
-// Tile and split of K for an M x N x K product.  A tile must leave enough workgroups for 256 CUs;
-// where even small tiles do not, K is split and the partial sums joined by a second kernel.
+// Tile and split of K for an M x N x K product: the least of a model's times.  A stage (128 bytes of K)
+// of one tile takes a CU `alone` microseconds, and `each` where several tiles share the CU (measured
+// with bf16 and fp32 at M = 300 .. 8192, N = 768 .. 10240, K = 768 .. 10240; the 256 tile fills a CU).
+// The fullest of 256 CUs decides.  Tiles beyond a multiple of 256 may be split along K: their parts
+// then pass through memory and a second kernel.
 GemmPlan plan_gemm(int64_t M, int64_t N, int64_t K, int dt, bool vec) {
-    const int64_t bk = 128 / elem_bytes(dt);     // K of a stage
-    auto tiles = [&](int64_t t) { return ceil_div(M, t) * ceil_div(N, t); };
-    GemmPlan p{128, 1, round_up(std::max<int64_t>(K, 1), bk)};
-    if (vec && dt != FFTCONV_F32 && tiles(256) >= 200) p.tile = 256;
-    else if (vec && tiles(128) < 256) p.tile = 64;
-    const int64_t n = tiles(p.tile);
-    const int64_t steps = ceil_div(K, bk);
-    if (n < 256 && steps >= 16) {
-        const int64_t want = std::min(ceil_div(512, n), steps / 8);
-        if (want > 1) {
-            p.kper = ceil_div(steps, want) * bk;
-            p.splits = (int)ceil_div(K, p.kper);
+    struct Kind {
+        int tile;
+        double alone16, each16, alone32, each32;
+    };
+    static const Kind kinds[] = {{256, 1.45, 1.45, 0.0, 0.0}, {128, 0.60, 0.47, 2.2, 2.05}, {64, 0.28, 0.22, 0.60, 0.52}};
+    constexpr double kStart = 4.0, kJoin = 2.0, kBytesPerUs = 6.0e6;
+    constexpr int64_t kCus = 256;
+    const int64_t bk = 128 / elem_bytes(dt), stages = std::max<int64_t>(1, ceil_div(K, bk));
+    GemmPlan best{};
+    double least = 1e300;
+    for (const Kind &k : kinds) {
+        if (vec ? (dt == FFTCONV_F32 && k.tile == 256) : k.tile != 128) continue;
+        const int64_t tiles = ceil_div(M, k.tile) * ceil_div(N, k.tile);
+        const double alone = dt == FFTCONV_F32 ? k.alone32 : k.alone16, each = dt == FFTCONV_F32 ? k.each32 : k.each16;
+        for (int splits = 1; splits <= 16; ++splits) {
+            if (splits > 1 && stages < 4 * splits) break;
+            const int64_t per = ceil_div(stages, splits);
+            if (ceil_div(stages, per) != splits) continue;
+            const int64_t full = splits == 1 ? tiles : tiles / kCus * kCus, parts = (tiles - full) * splits;
+            if (splits > 1 && parts == 0) break;
+            const int64_t whole = ceil_div(full, kCus), part = ceil_div(parts, kCus);
+            double us = kStart + (double)(whole * stages + part * per) * (whole + part <= 1 ? alone : each);
+            if (splits > 1) us += kJoin + 2.0 * parts * k.tile * k.tile * 4 / kBytesPerUs;
+            if (us < least) {
+                least = us;
+                best = GemmPlan{k.tile, splits, tiles, full, per * bk};
+            }
         }
     }
-    return p;
+    return best;
 }
-size_t plan_bytes(const GemmPlan &p, int64_t M, int64_t N) {
-    return p.splits > 1 ? align_up((size_t)p.splits * M * N * sizeof(float), 256) : 0;
+size_t plan_bytes(const GemmPlan &p) {
+    return align_up((size_t)(p.tiles - p.full) * p.splits * p.tile * p.tile * sizeof(float), 256);
 }
 // the workspace covers a call with or without 16-byte access
 size_t gemm_bytes(int64_t M, int64_t N, int64_t K, int dt) {
-    return std::max(plan_bytes(plan_gemm(M, N, K, dt, true), M, N), plan_bytes(plan_gemm(M, N, K, dt, false), M, N));
+    return std::max(plan_bytes(plan_gemm(M, N, K, dt, true)), plan_bytes(plan_gemm(M, N, K, dt, false)));
 }
 
 hipError_t run_gemm(int dt, LinearGemm &g, int layout, bool vec, float *part, hipStream_t s) {
@@ -566,7 +583,8 @@ hipError_t run_gemm(int dt, LinearGemm &g, int layout, bool vec, float *part, hi
     const int64_t reach = (int64_t(1) << 22) / elem_bytes(dt);
     g.quads = g.N % 4 == 0 && g.vec_c && g.ldc < reach && (!g.bias || g.vec_b) && (!g.res || (g.vec_r && g.ldr < reach)) &&
               (!g.pre || (g.vec_p && g.ldp < reach));
-    g.splits = p.splits, g.kper = p.kper, g.part = p.splits > 1 ? part : nullptr;
+    if (p.full + (p.tiles - p.full) * p.splits > 0x7fffffff) return hipErrorInvalidValue;
+    g.tiles = p.tiles, g.full = p.full, g.splits = p.splits, g.kper = p.kper, g.part = part;
     return dt == FFTCONV_F32   ? launch_linear_gemm_f32(g, layout, p.tile, vec, s)
            : dt == FFTCONV_F16 ? launch_linear_gemm_f16(g, layout, p.tile, vec, s)
                                : launch_linear_gemm_bf16(g, layout, p.tile, vec, s);
@@ -596,7 +614,7 @@ bool pieces(const View &v) {
 }  // namespace
 
 size_t fftconv_linear_fwd_workspace_bytes(int64_t M, int64_t N, int64_t K, fftconv_dtype_t dtype) {
-    if (!dtype_ok(dtype) || M < 1 || N < 1 || K < 1 || M <= kRowsMost) return 0;
+    if (!dtype_ok(dtype) || M < 1 || N < 1 || K < 1 || M <= kVectorRows) return 0;
     return gemm_bytes(M, N, K, dtype);
 }
 
@@ -638,10 +656,10 @@ fftconv_status_t fftconv_linear_fwd(const void *x, const void *W, const void *bi
     g.pre = pre, g.ldp = vp.stride[0], g.vec_p = quad(vp);
     g.act = activation;
     const bool vec = pieces(vx) && pieces(vw);
-    if (M <= kRowsMost) {
-        const hipError_t e = dtype == FFTCONV_F32   ? launch_linear_rows_f32(g, vec, stream)
-                             : dtype == FFTCONV_F16 ? launch_linear_rows_f16(g, vec, stream)
-                                                    : launch_linear_rows_bf16(g, vec, stream);
+    if (M <= kVectorRows) {
+        const hipError_t e = dtype == FFTCONV_F32   ? launch_linear_vector_f32(g, vec, stream)
+                             : dtype == FFTCONV_F16 ? launch_linear_vector_f16(g, vec, stream)
+                                                    : launch_linear_vector_bf16(g, vec, stream);
         return hip_status("linear product", e);
     }
     return hip_status("linear product", run_gemm(dtype, g, LAYOUT_NT, vec, static_cast<float *>(workspace), stream));

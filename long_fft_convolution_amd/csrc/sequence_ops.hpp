@@ -88,9 +88,12 @@ struct LinearGemm {
     int act;
     int vec_c, vec_r, vec_p, vec_b;   // 4-value access allowed
     int quads;                // N a multiple of 4, 4-value access everywhere, a tile's rows within 31 bits
-    int64_t kper;             // K of one split, a multiple of the K step
-    float *part;              // splits x M x N partial sums, null when not split
+    // Tiles below `full` are computed whole; each of the others in `splits` parts of kper of K (whole
+    // stages), whose sums go to part (tile-sized matrices, fp32) and are joined by a second kernel.
+    int64_t tiles, full;
     int splits;
+    int64_t kper;
+    float *part;
 };
 
 // dz = dout * act'(pre) into rows of ldz (zeros behind N), and column sums of slabs of rows.
@@ -111,7 +114,7 @@ hipError_t launch_decay_walks_f16(const DecaySet &s, hipStream_t stream);
 hipError_t launch_decay_step_f16(const DecayStep &a, bool vec, hipStream_t stream);
 hipError_t launch_decay_group_sum_f16(const DecayGroupSum &a, hipStream_t stream);
 hipError_t launch_linear_gemm_f16(const LinearGemm &a, int layout, int tile, bool vec, hipStream_t stream);
-hipError_t launch_linear_rows_f16(const LinearGemm &a, bool vec, hipStream_t stream);
+hipError_t launch_linear_vector_f16(const LinearGemm &a, bool vec, hipStream_t stream);
 hipError_t launch_linear_dz_f16(const LinearDz &a, int64_t slabs, void *dbias, hipStream_t stream);
 // sums of segments and their chain (nothing when the walks are not segmented), then the walks
 hipError_t launch_decay_sums_bf16(const DecaySet &s, hipStream_t stream);
@@ -119,7 +122,7 @@ hipError_t launch_decay_walks_bf16(const DecaySet &s, hipStream_t stream);
 hipError_t launch_decay_step_bf16(const DecayStep &a, bool vec, hipStream_t stream);
 hipError_t launch_decay_group_sum_bf16(const DecayGroupSum &a, hipStream_t stream);
 hipError_t launch_linear_gemm_bf16(const LinearGemm &a, int layout, int tile, bool vec, hipStream_t stream);
-hipError_t launch_linear_rows_bf16(const LinearGemm &a, bool vec, hipStream_t stream);
+hipError_t launch_linear_vector_bf16(const LinearGemm &a, bool vec, hipStream_t stream);
 hipError_t launch_linear_dz_bf16(const LinearDz &a, int64_t slabs, void *dbias, hipStream_t stream);
 // sums of segments and their chain (nothing when the walks are not segmented), then the walks
 hipError_t launch_decay_sums_f32(const DecaySet &s, hipStream_t stream);
@@ -127,7 +130,7 @@ hipError_t launch_decay_walks_f32(const DecaySet &s, hipStream_t stream);
 hipError_t launch_decay_step_f32(const DecayStep &a, bool vec, hipStream_t stream);
 hipError_t launch_decay_group_sum_f32(const DecayGroupSum &a, hipStream_t stream);
 hipError_t launch_linear_gemm_f32(const LinearGemm &a, int layout, int tile, bool vec, hipStream_t stream);
-hipError_t launch_linear_rows_f32(const LinearGemm &a, bool vec, hipStream_t stream);
+hipError_t launch_linear_vector_f32(const LinearGemm &a, bool vec, hipStream_t stream);
 hipError_t launch_linear_dz_f32(const LinearDz &a, int64_t slabs, void *dbias, hipStream_t stream);
 
 }  // namespace fftconv
