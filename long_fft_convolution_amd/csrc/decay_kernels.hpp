@@ -37,9 +37,10 @@
 // The accumulators hold E times a gain that grows by d^-C a chunk, so that
 // decaying the state costs one factor in the chunk's weights instead of a
 // multiplication of every accumulator; they are brought back when the gain
-// has grown by 2^16 (few bits of its exponent, so exp2 of it is exact to a
-// few 2^-24), in fp16 also when the terms leave the range that keeps the
-// second one out of the subnormals.
+// would pass 2^16 (few bits of its exponent, so exp2 of it is exact to a few
+// 2^-24), in fp16 also when the terms leave the range that keeps the second
+// one out of the subnormals.  Heads that forget more than 2^8 a chunk have
+// their accumulators multiplied each time.
 //
 // A call with few (sequence, head) pairs splits sequences into segments: a
 // first pass over y, z gives each segment's own sum, a small kernel chains
@@ -55,7 +56,7 @@ struct SegInfo {
     int64_t start, len;   // the sequence's first token and length
     int64_t seq, index;   // sequence, segment within it
     int64_t count;        // segments of the sequence
-    int64_t first;        // block index of the sequence's first segment
+    int64_t slot;         // place of the sequence's first state among the segments' states
 };
 
 __device__ __forceinline__ void packed_bounds(const DecayWalk &a, int64_t b, int64_t &start, int64_t &len) {
@@ -77,11 +78,11 @@ __device__ inline bool find_segment(const DecayWalk &a, int64_t blk, bool by_seq
         info.seq = by_seq ? blk : blk / per;
         info.index = by_seq ? 0 : blk % per;
         info.start = 0;
-        info.first = info.seq * per;
+        info.slot = info.seq * ((a.N + a.sublen - 1) / a.sublen);
         return info.seq < a.B;
     }
     __shared__ int64_t wave_sum[4];
-    __shared__ int64_t hit[6];
+    __shared__ int64_t hit[5];
     if (threadIdx.x == 0) hit[0] = -1;
     int64_t before = 0;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -112,7 +113,6 @@ __device__ inline bool find_segment(const DecayWalk &a, int64_t blk, bool by_seq
             hit[2] = n;
             hit[3] = start;
             hit[4] = len;
-            hit[5] = first;
         }
         __syncthreads();
         if (hit[0] >= 0) break;
@@ -123,8 +123,14 @@ __device__ inline bool find_segment(const DecayWalk &a, int64_t blk, bool by_seq
     info.count = hit[2];
     info.start = hit[3];
     info.len = hit[4];
-    info.first = hit[5];
+    // no two sequences meet: start / sublen + ceil(len / sublen) <= (start + len) / sublen + 1
+    info.slot = info.start / a.sublen + info.seq;
     return info.seq >= 0;
+}
+
+// Of a sequence's `count` parts, those that precede its last segment.
+__device__ __forceinline__ int64_t parts_before_last(const DecayWalk &a, int64_t count) {
+    return count > 0 ? (count - 1) / a.parts * a.parts : 0;
 }
 
 // Slot of sequence seq in the state pool, or -1 (no state kept).
@@ -295,12 +301,14 @@ __device__ __forceinline__ void work_of(const DecaySet &set, uint32_t id, int &k
 // them fit a CU's 160 KB, else two; without LDS-destination loads one.
 constexpr int walk_stages(int bytes, bool vec) { return !vec ? 1 : (3 * bytes <= 78 * 1024 ? 3 : (2 * bytes <= 150 * 1024 ? 2 : 1)); }
 
-// OUT = false: the segment's own sum only (y, z read), for every
-// segment that another follows.  DXP: DX padded; NT: 16-column tiles of E per wave.
+// MODE kSums: the segment's own sum only (y, z read), for every
+// segment that another follows; kOut: outputs in the storage type; kOutAny: in it or fp32, by the walk.  DXP: DX padded; NT: 16-column tiles of E per wave.
+enum WalkMode : int { kSums = 0, kOut = 1, kOutAny = 2 };
 // grid: work items (see work_of)
-template <typename T, int DXP, int NT, bool OUT, bool VEC, int TERMS>
+template <typename T, int DXP, int NT, int MODE, bool VEC, int TERMS>
 __global__ __launch_bounds__(256, DXP <= 128 ? 2 : 1) void decay_walk_kernel(const DecaySet set) {
 #ifdef __HIP_DEVICE_COMPILE__   // the host pass, which cannot take the scalar operands, needs the stub alone
+    constexpr bool OUT = MODE != kSums;
     constexpr int KX = DXP / 32;          // 32-wide contraction steps over DX
     constexpr int DZT = NT * 64;          // z columns of a workgroup
     using TX = ChunkTile<T, DXP, false>;
@@ -323,9 +331,9 @@ __global__ __launch_bounds__(256, DXP <= 128 ? 2 : 1) void decay_walk_kernel(con
     SegInfo si;
     if (blk >= a.nblk || zt * DZT >= a.DZ || !find_segment(a, blk, false, si)) return;
     si.seq = scalar(si.seq), si.index = scalar(si.index), si.count = scalar(si.count);
-    si.start = scalar(si.start), si.len = scalar(si.len);
-    // the last segment's sum is wanted only for the final state
-    if (!OUT && si.index + 1 >= si.count && !a.state1) return;
+    si.start = scalar(si.start), si.len = scalar(si.len), si.slot = scalar(si.slot);
+    // only the final state wants the sums of the last segment's parts
+    if (!OUT && !a.state1 && si.index >= parts_before_last(a, si.count)) return;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int g = lane >> 4, c = lane & 15;
@@ -363,7 +371,7 @@ __global__ __launch_bounds__(256, DXP <= 128 ? 2 : 1) void decay_walk_kernel(con
         const float *s0 = nullptr;
         uint32_t sx_ = (uint32_t)a.s0x, sz_ = (uint32_t)a.s0z;
         if (a.seg && OUT) {
-            s0 = a.seg + (blk * a.H + h) * (int64_t)a.DX * a.DZ;
+            s0 = a.seg + ((si.slot + si.index * (a.seglen / a.sublen)) * a.H + h) * (int64_t)a.DX * a.DZ;
             sx_ = (uint32_t)a.segx;
             sz_ = (uint32_t)a.segz;
         } else if (OUT && a.state0) {
@@ -396,18 +404,19 @@ __global__ __launch_bounds__(256, DXP <= 128 ? 2 : 1) void decay_walk_kernel(con
                     fac[rt][r][i] = n < 0 ? 0.0f : a.p_scale * decay_power(log2d, n);
                 }
     }
-    const float wn = -log2d * kChunk;   // growth of the gain's exponent over a full chunk
+    const bool slow = __builtin_amdgcn_readfirstlane(fabsf(log2d) * kChunk <= 8.0f);   // the gain carries the decay
     const int zl = col0 + zw + (NT == 2 ? g * 8 : g * 4);      // this lane's first column of the output
     const int out_cols = a.DZ - zl;                             // and how many are left
-    const uint32_t out_e = a.out_f32 ? 4u : (uint32_t)sizeof(T);
+    const uint32_t out_e = MODE == kOutAny && a.out_f32 ? 4u : (uint32_t)sizeof(T);
     char *out0 = static_cast<char *>(a.out) + (OUT ? (batch * a.ob + row0 * a.ot + (h / a.go) * a.oh) * out_e : 0);
     uint32_t out_off[2];        // this lane's places in a chunk's rows
 #pragma unroll
     for (int rt = 0; rt < 2; ++rt) {
         const int row = rt * 16 + c;
-        out_off[rt] = out_cols > 0 ? (uint32_t)((a.reverse ? kChunk - 1 - row : row) * a.ot + zl) * out_e : kSkip;
+        out_off[rt] = out_cols > 0 && a.out ? (uint32_t)((a.reverse ? kChunk - 1 - row : row) * a.ot + zl) * out_e : kSkip;
     }
-    float grown = 0.0f;    // the accumulators hold E * 2^(grown + ex)
+    float grown = 0.0f;    // the accumulators hold E * 2^(grown + ex); grown = -log2 d * held
+    int held = 0;
     int ex = 0;            // (ex: fp16 only, else 0)
 
     // one chunk at token t in (x, y, z); (nx, ny, nz) is free for the chunk S - 1 ahead
@@ -430,6 +439,39 @@ __global__ __launch_bounds__(256, DXP <= 128 ? 2 : 1) void decay_walk_kernel(con
 #pragma unroll
         for (int q = 0; q < NT; ++q)
             zf[q] = TZ::col8(z, zw + (NT == 2 ? (lane & 3) * 8 + q * 4 : (lane & 3) * 4), zcol(c, q));
+        // the gain after this chunk; brought back first where that leaves its range
+        const float growth = slow ? (float)n * -log2d : 0.0f;
+        held = slow ? held + n : 0;
+        float next = slow ? (float)held * -log2d : 0.0f, most = 0.0f;
+        bool back = fabsf(next) > 16.0f;
+        if (Mma<T>::kNarrow) {
+#pragma unroll
+            for (int q = 0; q < NT; ++q)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) most = fmaxf(most, fabsf((float)zf[q][j]));
+            most = wave_max(most) * fabsf(a.u_scale);      // the weights are at most u_scale
+            const float top = ldexpf(most * exp2f(next), ex);
+            back = back || top > 32768.0f || (top < 16.0f && most > 0.0f);
+        }
+        if (__builtin_amdgcn_readfirstlane(back)) {
+            int e1 = 0;
+            if (Mma<T>::kNarrow) {
+                e1 = most > 0.0f ? 13 - ilogbf(most) - (int)ceilf(growth) : ex;     // the largest term near 2^14
+                e1 = e1 < -60 ? -60 : (e1 > 60 ? 60 : e1);
+            }
+            const float r = ldexpf(exp2f(-grown), e1 - ex);
+#pragma unroll
+            for (int kk = 0; kk < KX; ++kk)
+#pragma unroll
+                for (int r2 = 0; r2 < 2; ++r2)
+#pragma unroll
+                    for (int q = 0; q < NT; ++q) E[kk][r2][q] *= r;
+            ex = e1;
+            grown = 0.0f;
+            held = slow ? n : 0;
+            next = growth;
+        }
+        const float gain = Mma<T>::kNarrow ? ldexpf(exp2f(next), ex) : exp2f(next);
         if (OUT) {
             const float unscale = Mma<T>::kNarrow ? ldexpf(exp2f(-grown), -ex) : exp2f(-grown);
             v8 ef[KX][NT];     // the state as an operand: row zcol(c, q), slots 8 g + j
@@ -467,46 +509,25 @@ __global__ __launch_bounds__(256, DXP <= 128 ? 2 : 1) void decay_walk_kernel(con
                     o[q] *= rw;
                     o[q] = Mma<T>::mma(zf[q], pf, o[q]);
                 }
-                if (a.out) {
+                {
                     const auto view = wide_view(out0 + (a.reverse ? si.len - t - kChunk : t) * a.ot * out_e);
                     const uint32_t off = rt * 16 + c < n ? out_off[rt] : kSkip;
-                    if (a.out_f32) put_row<float, NT, VEC && sizeof(T) == 2>(view, off, o, a.vec_o, out_cols);
+                    if (MODE == kOutAny && a.out_f32) put_row<float, NT, VEC && sizeof(T) == 2>(view, off, o, a.vec_o, out_cols);
                     else put_row<T, NT, VEC && sizeof(T) == 2>(view, off, o, a.vec_o, out_cols);
                 }
             }
         }
         // E <- d^n E + Y^T (weights Z), in units of the gain
-        float next = n == kChunk ? grown + wn : (float)n * -log2d + grown, most = 0.0f;
-        bool back = !(fabsf(next) <= 16.0f);
-        if (Mma<T>::kNarrow) {
-#pragma unroll
-            for (int q = 0; q < NT; ++q)
-#pragma unroll
-                for (int j = 0; j < 8; ++j) most = fmaxf(most, fabsf((float)zf[q][j]));
-#pragma unroll
-            for (int s = 1; s < 64; s <<= 1) most = fmaxf(most, __shfl_xor(most, s));
-            most *= fabsf(a.u_scale);      // the weights are at most u_scale
-            const float top = ldexpf(most * exp2f(next), ex);
-            back = back || top > 32768.0f || (top < 16.0f && most > 0.0f);
-        }
-        if (__builtin_amdgcn_readfirstlane(back)) {
-            int e1 = 0;
-            if (Mma<T>::kNarrow) {
-                e1 = most > 0.0f ? 13 - ilogbf(most) : ex;     // the largest term near 2^14
-                e1 = e1 < -60 ? -60 : (e1 > 60 ? 60 : e1);
-            }
-            const float r = ldexpf(exp2f(-next), e1 - ex);
+        if (!slow) {
+            const float dn = decay_power(log2d, n);
 #pragma unroll
             for (int kk = 0; kk < KX; ++kk)
 #pragma unroll
-                for (int r2 = 0; r2 < 2; ++r2)
+                for (int r = 0; r < 2; ++r)
 #pragma unroll
-                    for (int q = 0; q < NT; ++q) E[kk][r2][q] *= r;
-            ex = e1;
-            next = 0.0f;
+                    for (int q = 0; q < NT; ++q) E[kk][r][q] *= dn;
         }
         grown = next;
-        const float gain = Mma<T>::kNarrow ? ldexpf(exp2f(grown), ex) : exp2f(grown);
         v8 zs[NT][TERMS];
         float w[8];
 #pragma unroll
@@ -556,7 +577,7 @@ __global__ __launch_bounds__(256, DXP <= 128 ? 2 : 1) void decay_walk_kernel(con
     float *s1 = nullptr;
     uint32_t sx_ = (uint32_t)a.s1x, sz_ = (uint32_t)a.s1z;
     if (!OUT) {
-        s1 = a.seg + (blk * a.H + h) * (int64_t)a.DX * a.DZ;
+        s1 = a.seg + ((si.slot + si.index) * a.H + h) * (int64_t)a.DX * a.DZ;
         sx_ = (uint32_t)a.segx;
         sz_ = (uint32_t)a.segz;
     } else if (a.state1 && !a.seg) {      // segmented: the chain kernel has it
@@ -682,18 +703,22 @@ template <int V> static __global__ __launch_bounds__(256) void decay_chain_kerne
         for (int i = 0; i < V; ++i)
             run[i] = a.state0[(slot * a.H + h) * nst + (e + i) / a.DZ * a.s0x + (e + i) % a.DZ * a.s0z];
     }
-    float *p = a.seg + (si.first * a.H + h) * nst + e;
+    float *p = a.seg + (si.slot * a.H + h) * nst + e;
     const int64_t step = a.H * nst;
+    // sums to add, and states to write (the walks start at the first part of a segment)
+    const int64_t sums = a.state1 ? si.count : parts_before_last(a, si.count), states = parts_before_last(a, si.count) + 1;
     constexpr int U = 8;
-    for (int64_t s = 0; s < si.count; s += U) {
+    int to_state = 0;       // parts until the next segment starts
+    for (int64_t s = 0; s < sums || s < states; s += U) {
         vec own[U];
 #pragma unroll
         for (int j = 0; j < U; ++j)
-            own[j] = s + j < si.count && (a.state1 || s + j + 1 < si.count) ? *reinterpret_cast<const vec *>(p + (s + j) * step) : (vec)0.0f;
+            own[j] = s + j < sums ? *reinterpret_cast<const vec *>(p + (s + j) * step) : (vec)0.0f;
 #pragma unroll
         for (int j = 0; j < U; ++j)
-            if (s + j < si.count) {
-                *reinterpret_cast<vec *>(p + (s + j) * step) = run;
+            if (s + j < sums || s + j < states) {
+                if (to_state == 0 && s + j < states) *reinterpret_cast<vec *>(p + (s + j) * step) = run;
+                to_state = to_state == 0 ? a.parts - 1 : to_state - 1;
                 run = (s + j + 1 < si.count ? dn : dlast) * run + own[j];
             }
     }
@@ -705,7 +730,7 @@ template <int V> static __global__ __launch_bounds__(256) void decay_chain_kerne
 }
 
 // ---- host side of one storage type ----------------------------------------
-template <typename T, bool OUT, bool VEC, int TERMS> static hipError_t walk_launch(const DecaySet &set, hipStream_t stream) {
+template <typename T, int MODE, bool VEC, int TERMS> static hipError_t walk_launch(const DecaySet &set, hipStream_t stream) {
     bool narrow = true;
     int dx = 0;
     for (int i = 0; i < set.kinds; ++i) {
@@ -717,13 +742,13 @@ template <typename T, bool OUT, bool VEC, int TERMS> static hipError_t walk_laun
     // (rows wider than 128 leave registers for 64 z columns only: decay_z_tile)
     if (dx > 128) {
         if (!narrow) return hipErrorInvalidValue;
-        decay_walk_kernel<T, 256, 1, OUT, VEC, TERMS><<<grid, 256, 0, stream>>>(set);
+        decay_walk_kernel<T, 256, 1, MODE, VEC, TERMS><<<grid, 256, 0, stream>>>(set);
     } else if (dx > 64) {
-        if (narrow) decay_walk_kernel<T, 128, 1, OUT, VEC, TERMS><<<grid, 256, 0, stream>>>(set);
-        else decay_walk_kernel<T, 128, 2, OUT, VEC, TERMS><<<grid, 256, 0, stream>>>(set);
+        if (narrow) decay_walk_kernel<T, 128, 1, MODE, VEC, TERMS><<<grid, 256, 0, stream>>>(set);
+        else decay_walk_kernel<T, 128, 2, MODE, VEC, TERMS><<<grid, 256, 0, stream>>>(set);
     } else {
-        if (narrow) decay_walk_kernel<T, 64, 1, OUT, VEC, TERMS><<<grid, 256, 0, stream>>>(set);
-        else decay_walk_kernel<T, 64, 2, OUT, VEC, TERMS><<<grid, 256, 0, stream>>>(set);
+        if (narrow) decay_walk_kernel<T, 64, 1, MODE, VEC, TERMS><<<grid, 256, 0, stream>>>(set);
+        else decay_walk_kernel<T, 64, 2, MODE, VEC, TERMS><<<grid, 256, 0, stream>>>(set);
     }
     return hipGetLastError();
 }
@@ -734,8 +759,11 @@ template <typename T> static hipError_t walks_typed(const DecaySet &set, hipStre
     constexpr int kExact = Mma<T>::kExactTerms, kTerms = Mma<T>::kTerms;
     bool vec = true;
     for (int i = 0; i < set.kinds; ++i) vec = vec && set.w[i].vec_x && set.w[i].vec_y && set.w[i].vec_z && set.w[i].vec_o;
-    if (!vec) return walk_launch<T, true, false, kExact>(set, stream);
-    return set.w[0].seg ? walk_launch<T, true, true, kTerms>(set, stream) : walk_launch<T, true, true, kExact>(set, stream);
+    bool any = false;
+    for (int i = 0; i < set.kinds; ++i) any = any || set.w[i].out_f32;
+    if (!vec) return walk_launch<T, kOutAny, false, kExact>(set, stream);
+    if (any) return set.w[0].seg ? walk_launch<T, kOutAny, true, kTerms>(set, stream) : walk_launch<T, kOutAny, true, kExact>(set, stream);
+    return set.w[0].seg ? walk_launch<T, kOut, true, kTerms>(set, stream) : walk_launch<T, kOut, true, kExact>(set, stream);
 }
 
 template <typename T> static hipError_t sums_typed(const DecaySet &set, hipStream_t stream) {
@@ -743,7 +771,7 @@ template <typename T> static hipError_t sums_typed(const DecaySet &set, hipStrea
     constexpr int kExact = Mma<T>::kExactTerms;
     bool vec = true;
     for (int i = 0; i < set.kinds; ++i) vec = vec && set.w[i].vec_y && set.w[i].vec_z;
-    const hipError_t e = vec ? walk_launch<T, false, true, kExact>(set, stream) : walk_launch<T, false, false, kExact>(set, stream);
+    const hipError_t e = vec ? walk_launch<T, kSums, true, kExact>(set, stream) : walk_launch<T, kSums, false, kExact>(set, stream);
     if (e != hipSuccess) return e;
     const int64_t nst = (int64_t)set.w[0].DX * set.w[0].DZ;
     const bool quads = nst % 4 == 0;

@@ -332,17 +332,20 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void linear_gemm_kernel(const Line
             if (more1) wait_loads_and_barrier<2 * L>();     // A1, B1 of this stage have arrived
             else wait_loads_and_barrier<0>();
             read_b(sb[at][1], b1);
-            read_a(sa[at][1], a1);
             if (more2) bring(s + 2, 0, more3);
             __builtin_amdgcn_sched_barrier(0);              // reads first: the products hide them
             multiply(a0, b0, acc[0][0]);
+            __builtin_amdgcn_sched_barrier(0);
+            read_a(sa[at][1], a1);
+            __builtin_amdgcn_sched_barrier(0);
             multiply(a0, b1, acc[0][1]);
             if (more2) wait_loads_and_barrier<2 * L>();     // A0, B0 of the next
             else if (more1) wait_loads_and_barrier<L>();
-            if (more1) read_a(sa[at ^ 1][0], a0);
             if (more2) bring(s + 2, 1, more3);
             __builtin_amdgcn_sched_barrier(0);
             multiply(a1, b0, acc[1][0]);
+            __builtin_amdgcn_sched_barrier(0);
+            if (more1) read_a(sa[at ^ 1][0], a0);
             if (more1) read_b(sb[at ^ 1][0], b0);
             __builtin_amdgcn_sched_barrier(0);
             multiply(a1, b1, acc[1][1]);

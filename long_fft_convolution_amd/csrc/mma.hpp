@@ -121,4 +121,20 @@ template <int LEFT> __device__ __forceinline__ void wait_loads_and_barrier() {
     __builtin_amdgcn_sched_barrier(0);
 }
 
+// Largest of the wave's 64 values (not negative), in every lane: four steps within rows of 16 lanes, two
+// that exchange rows.
+__device__ __forceinline__ float wave_max(float x) {
+#define FFTCONV_DPP(CTRL) \
+    x = fmaxf(x, __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, x), CTRL, 0xf, 0xf, true)))
+    FFTCONV_DPP(0xb1);      // lanes 1 0 3 2 of each four
+    FFTCONV_DPP(0x4e);      // lanes 2 3 0 1
+    FFTCONV_DPP(0x141);     // halves of a row mirrored
+    FFTCONV_DPP(0x140);     // rows mirrored
+#undef FFTCONV_DPP
+    const auto a = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(uint32_t, x), __builtin_bit_cast(uint32_t, x), false, false);
+    x = fmaxf(__builtin_bit_cast(float, a[0]), __builtin_bit_cast(float, a[1]));
+    const auto b = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, x), __builtin_bit_cast(uint32_t, x), false, false);
+    return fmaxf(__builtin_bit_cast(float, b[0]), __builtin_bit_cast(float, b[1]));
+}
+
 }  // namespace fftconv

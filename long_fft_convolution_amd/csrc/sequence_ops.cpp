@@ -109,41 +109,70 @@ fftconv_status_t check_view(const View &v, bool required, bool output) {
 
 // ---- decay attention --------------------------------------------------------
 constexpr int64_t kMaxHeadDim = 256;
-constexpr int64_t kSegStep = 64;          // segments are whole chunks
+constexpr int64_t kSegStep = 64;          // parts of a segment are whole chunks
 constexpr int64_t kMinSegment = 256;      // below this the second read of y, z costs more than it spreads
-constexpr int64_t kWalkSlots = 512;       // workgroups that walk at once: two on each of 256 CUs
+constexpr int64_t kCus = 256;
 
 int64_t z_tiles(int64_t dx, int64_t dz) { return ceil_div(dz, decay_z_tile(dx, dz)); }
 
-// Tokens of a segment.  A walk is serial, so the chip fills only when the walks (kinds of walk x
-// sequences x heads x z tiles) number about kWalkSlots; fewer are cut into segments, at the price of
-// reading y and z twice (a pass of their own sums each segment first).
-int64_t segment_tokens(int64_t B, int64_t N, int64_t T, int64_t walks_per_sequence, bool packed) {
-    if (packed) return round_up(std::max(kMinSegment, ceil_div(T * walks_per_sequence, kWalkSlots)), kSegStep);
-    // equal sequences: as many equal segments as all walk at once
-    const int64_t most = std::max<int64_t>(1, kWalkSlots / std::max<int64_t>(1, B * walks_per_sequence));
-    return round_up(std::max(N <= kMinSegment ? std::max<int64_t>(N, 1) : kMinSegment, ceil_div(N, most)), kSegStep);
-}
-int64_t segment_count(int64_t B, int64_t N, int64_t T, int64_t seglen, bool packed) {
-    return packed ? T / seglen + B : B * std::max<int64_t>(1, ceil_div(N, seglen));
-}
-bool segmented(int64_t N, int64_t T, int64_t seglen, bool packed) { return (packed ? T : N) > seglen; }
+struct DecayShape {
+    int64_t B, N, H, Hk, Dk, Dv;
+    int dt;
+    bool packed;
+    int64_t T() const { return packed ? N : B * N; }
+};
 
-// Bytes of the segments' states of one set of H x dx x dz sums over T tokens in B sequences.
-size_t seg_bytes(int64_t B, int64_t T, int64_t walks_per_sequence, int64_t H, int64_t dx, int64_t dz) {
-    size_t most = 0;
-    for (bool packed : {false, true}) {
-        // equal sequences: T = B N; a packed call may hold any lengths
-        const int64_t N = packed ? T : ceil_div(T, std::max<int64_t>(B, 1));
-        const int64_t len = segment_tokens(B, N, T, walks_per_sequence, packed);
-        if (segmented(N, T, len, packed))
-            most = std::max(most, (size_t)segment_count(B, N, T, len, packed) * H * dx * dz * sizeof(float));
+// How sequences are cut.  A walk is serial, so the chip fills only when the walks (kinds of walk x
+// sequences x heads x z tiles) number about two or three a CU; fewer are cut into segments, at the price
+// of reading y and z twice (a pass of its own sums each segment first).  That pass reads half as much
+// per token and is cut finer where segments are few: a segment is `seglen / sublen` parts.
+struct DecayCut {
+    int64_t seglen, sublen, segments, parts;   // tokens; how many there are at most
+    bool cut;                                  // more than one segment a sequence
+};
+DecayCut decay_cut(const DecayShape &s, int64_t walks_per_token, int64_t sums_per_token, bool wide) {
+    const int64_t slots = kCus * (wide ? 2 : 3), T = s.T();
+    DecayCut c{};
+    int64_t len;
+    if (s.packed) {
+        len = std::max(kMinSegment, ceil_div(T * walks_per_token, slots));
+    } else {
+        // equal sequences: as many equal segments as all walk at once
+        const int64_t most = std::max<int64_t>(1, slots / std::max<int64_t>(1, s.B * walks_per_token));
+        len = std::max(std::min(kMinSegment, std::max<int64_t>(s.N, 1)), ceil_div(s.N, most));
     }
-    return align_up(most, 256);
+    len = round_up(len, kSegStep);
+    c.cut = (s.packed ? T : s.N) > len;
+    // parts: two sums a CU, of at least four chunks
+    const int64_t segs = std::max<int64_t>(1, s.packed ? T / len : s.B * (ceil_div(s.N, len) - 1));
+    int64_t parts = !c.cut ? 1 : std::max<int64_t>(1, 2 * kCus / std::max<int64_t>(1, segs * sums_per_token));
+    parts = std::min(parts, std::max<int64_t>(1, len / 128));
+    c.sublen = round_up(ceil_div(len, parts), kSegStep);
+    c.seglen = c.sublen * parts;
+    auto count = [&](int64_t l) { return s.packed ? T / l + s.B : s.B * std::max<int64_t>(1, ceil_div(s.N, l)); };
+    c.segments = count(c.seglen), c.parts = count(c.sublen);
+    c.cut = (s.packed ? T : s.N) > c.seglen;
+    return c;
 }
-int64_t fwd_walks(int64_t H, int64_t Dk, int64_t Dv) { return H * z_tiles(Dk, Dv); }
-// dq, dk (Dv x Dk) and dv (Dk x Dv)
-int64_t bwd_walks(int64_t H, int64_t Dk, int64_t Dv) { return H * (2 * z_tiles(Dv, Dk) + z_tiles(Dk, Dv)); }
+bool wide_walks(int64_t Dk, int64_t Dv) { return Dk > 64 || Dv > 64; }
+DecayCut fwd_cut(const DecayShape &s) {
+    const int64_t walks = s.H * z_tiles(s.Dk, s.Dv);
+    return decay_cut(s, walks, walks, wide_walks(s.Dk, s.Dv));
+}
+// dq, dk (Dv x Dk) and dv (Dk x Dv); sums of both states as Dv x Dk
+DecayCut bwd_cut(const DecayShape &s) {
+    const int64_t sums = 2 * s.H * z_tiles(s.Dv, s.Dk);
+    return decay_cut(s, sums + s.H * z_tiles(s.Dk, s.Dv), sums, wide_walks(s.Dk, s.Dv));
+}
+size_t cut_bytes(const DecayShape &s, const DecayCut &c) {
+    return c.cut ? align_up((size_t)c.parts * s.H * s.Dk * s.Dv * sizeof(float), 256) : 0;
+}
+// Workspace sizes are asked for by the number of tokens: the most of B equal sequences and of a packed
+// call, whose sequences may have any lengths.
+size_t most_bytes(DecayCut (*cut)(const DecayShape &), int64_t B, int64_t T, int64_t H, int64_t Dk, int64_t Dv) {
+    const DecayShape equal{B, ceil_div(T, std::max<int64_t>(B, 1)), H, H, Dk, Dv, 0, false}, packed{B, T, H, H, Dk, Dv, 0, true};
+    return std::max(cut_bytes(equal, cut(equal)), cut_bytes(packed, cut(packed)));
+}
 
 hipError_t launch_sums(int dt, const DecaySet &a, hipStream_t s) {
     return dt == FFTCONV_F32   ? launch_decay_sums_f32(a, s)
@@ -155,13 +184,6 @@ hipError_t launch_walks(int dt, const DecaySet &a, hipStream_t s) {
            : dt == FFTCONV_F16 ? launch_decay_walks_f16(a, s)
                                : launch_decay_walks_bf16(a, s);
 }
-
-struct DecayShape {
-    int64_t B, N, H, Hk, Dk, Dv;
-    int dt;
-    bool packed;
-    int64_t T() const { return packed ? N : B * N; }
-};
 
 // heads: H or Hk; strides (batch, token, head) at st
 View heads_view(const char *name, const void *p, const DecayShape &s, int64_t heads, int64_t row, const int64_t *st) {
@@ -247,10 +269,13 @@ void set_out(DecayWalk &w, const View &v, int64_t H) {
     w.go = (int)(H / v.size[2]);
     w.vec_o = v.vec16();
 }
-void set_segments(DecayWalk &w, const DecayShape &s, int64_t walks_per_sequence, float *seg) {
-    w.seglen = segment_tokens(s.B, s.N, s.T(), walks_per_sequence, s.packed);
-    w.nblk = segment_count(s.B, s.N, s.T(), w.seglen, s.packed);
-    w.seg = segmented(s.N, s.T(), w.seglen, s.packed) ? seg : nullptr;
+void set_cut(DecayWalk &w, const DecayCut &c) {
+    w.seglen = c.seglen, w.sublen = c.sublen, w.parts = (int)(c.seglen / c.sublen), w.nblk = c.segments;
+}
+// the same walks over the parts that have sums of their own
+DecaySet parts_of(DecaySet set, const DecayCut &c) {
+    for (int i = 0; i < set.kinds; ++i) set.w[i].seglen = c.sublen, set.w[i].nblk = c.parts;
+    return set;
 }
 DecaySet make_set(std::initializer_list<const DecayWalk *> walks, int64_t group) {
     DecaySet set{};
@@ -279,7 +304,7 @@ bool too_many(const DecaySet &s) {
 size_t fftconv_decay_fwd_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t Dk, int64_t Dv,
                                          fftconv_dtype_t dtype) {
     if (!dtype_ok(dtype) || B < 1 || T < 1 || H < 1 || Dk < 1 || Dv < 1 || Dk > kMaxHeadDim || Dv > kMaxHeadDim) return 0;
-    return seg_bytes(B, T, fwd_walks(H, Dk, Dv), H, Dk, Dv);
+    return most_bytes(fwd_cut, B, T, H, Dk, Dv);
 }
 
 fftconv_status_t fftconv_decay_fwd(const void *q, const void *k, const void *v, const float *log_decay, void *out,
@@ -334,11 +359,15 @@ fftconv_status_t fftconv_decay_fwd(const void *q, const void *k, const void *v, 
     w.B = B, w.N = N, w.H = (int)H;
     w.p_scale = scale, w.u_scale = 1.0f, w.i_scale = scale;
     w.off = 1;
-    set_segments(w, s, fwd_walks(H, Dk, Dv), static_cast<float *>(workspace));
+    const DecayCut cut = fwd_cut(s);
+    set_cut(w, cut);
+    w.seg = cut.cut ? static_cast<float *>(workspace) : nullptr;
     w.segx = Dv, w.segz = 1;
-    const DecaySet set = make_set({&w}, H / Hk);
-    if (too_many(set)) return fail(FFTCONV_ERR_UNSUPPORTED, "B=%lld, N=%lld, H=%lld: too many sequences or tokens", (long long)B, (long long)N, (long long)H);
-    hipError_t e = launch_sums(dtype, set, stream);
+    const DecaySet set = make_set({&w}, H / Hk), sums = parts_of(set, cut);
+    if (too_many(set) || too_many(sums))
+        return fail(FFTCONV_ERR_UNSUPPORTED, "B=%lld, N=%lld, H=%lld: too many sequences or tokens", (long long)B,
+                    (long long)N, (long long)H);
+    hipError_t e = launch_sums(dtype, sums, stream);
     if (e == hipSuccess) e = launch_walks(dtype, set, stream);
     return hip_status("decay attention", e);
 }
@@ -391,7 +420,7 @@ struct DecayBwdLayout {
 };
 DecayBwdLayout decay_bwd_layout(int64_t B, int64_t T, int64_t H, int64_t Hk, int64_t Dk, int64_t Dv) {
     DecayBwdLayout l{};
-    l.grads = seg_bytes(B, T, bwd_walks(H, Dk, Dv), H, Dk, Dv);
+    l.grads = most_bytes(bwd_cut, B, T, H, Dk, Dv);
     l.dk = 2 * l.grads;
     l.dv = l.dk + (H == Hk ? 0 : align_up((size_t)T * H * Dk * sizeof(float), 256));
     l.total = l.dv + (H == Hk ? 0 : align_up((size_t)T * H * Dv * sizeof(float), 256));
@@ -449,8 +478,9 @@ fftconv_status_t fftconv_decay_bwd(const void *dout, const void *q, const void *
     w.log_decay = log_decay;
     w.cu = cu_seqlens;
     w.B = B, w.N = N, w.H = (int)H;
-    set_segments(w, s, bwd_walks(H, Dk, Dv), nullptr);
-    const bool cut = segmented(s.N, s.T(), w.seglen, s.packed);
+    const DecayCut c = bwd_cut(s);
+    const bool cut = c.cut;
+    set_cut(w, c);
     // dq: x, y, z = dout, v, k forwards, state S^T (Dv x Dk)
     DecayWalk q_ = w;
     set_x(q_, vd, H);
@@ -493,11 +523,12 @@ fftconv_status_t fftconv_decay_bwd(const void *dout, const void *q, const void *
     // the state's own gradient comes from the chain of sums, or from dk's walk when there are none
     const bool run_k = (dk && tokens) || (dstate_in && !cut);
     const DecaySet sums = make_set({run_q ? &q_ : nullptr, sum_g ? &k_ : nullptr}, H / Hk);
-    if (too_many(make_set({&q_, &k_, &v_}, H / Hk)))
+    const DecaySet all = make_set({&q_, &k_, &v_}, H / Hk);
+    if (too_many(all) || too_many(parts_of(all, c)))
         return fail(FFTCONV_ERR_UNSUPPORTED, "B=%lld, N=%lld, H=%lld: too many sequences or tokens", (long long)B,
                     (long long)N, (long long)H);
     hipError_t e = hipSuccess;
-    if (sums.kinds) e = launch_sums(dtype, sums, stream);
+    if (sums.kinds) e = launch_sums(dtype, parts_of(sums, c), stream);
     const bool together = same_class(k_, v_);
     const DecaySet first = make_set({run_k ? &k_ : nullptr, run_v && together ? &v_ : nullptr, run_q ? &q_ : nullptr}, H / Hk);
     if (e == hipSuccess && first.kinds) e = launch_walks(dtype, first, stream);

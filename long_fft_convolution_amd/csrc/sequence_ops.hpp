@@ -28,9 +28,11 @@ struct DecayWalk {
     int64_t B, N;                    // N: tokens of each sequence, or of all when packed
     int H, DX, DZ;
     int ztile;                       // z columns of a workgroup
-    int64_t seglen;                  // tokens per segment, a multiple of the chunk
+    int64_t seglen;                  // tokens per segment, a multiple of sublen
+    int64_t sublen;                  // tokens per part that has a sum of its own, a multiple of the chunk
+    int parts;                       // seglen / sublen of the walks
     int64_t nblk;                    // segments launched (an upper bound when packed)
-    float *seg;                      // state before each segment (nblk, H) matrices, null when one segment each
+    float *seg;                      // state before each part, (parts, H) matrices, null when one segment each
     int64_t segx, segz;              // their strides along DX and DZ
     float p_scale, u_scale, i_scale;
     int off, reverse;
