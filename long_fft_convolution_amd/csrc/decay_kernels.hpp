@@ -533,31 +533,28 @@ __global__ __launch_bounds__(256, DXP <= 128 ? 2 : 1) void decay_walk_kernel(con
 #pragma unroll
         for (int j = 0; j < 8; ++j) w[j] = upd[kChunk - n + g * 8 + j] * gain;
 #pragma unroll
-        for (int q = 0; q < NT; ++q)
+        for (int q = 0; q < NT; ++q) {
+            float weighted[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                float rest = (float)zf[q][j] * w[j];
-                // one value for every use: left to itself the compiler rounds the product to fp16 once
-                // through fp32 and once fused, and the two first terms then differ at ties
-                if (TERMS > 1) asm("" : "+v"(rest));
+            for (int j = 0; j < 8; ++j) weighted[j] = (float)zf[q][j] * w[j];
+            split8<T, TERMS>(weighted, zs[q]);
+        }
+        // terms outermost: an accumulator's next product comes 2 NT instructions later, past their latency
 #pragma unroll
-                for (int s = 0; s < TERMS; ++s) {
-                    const T part = (T)rest;
-                    zs[q][s][j] = part;
-                    rest -= (float)part;
-                }
-            }
+        for (int kk = 0; kk < KX; ++kk) {
+            // rows of the state permuted like zcol: row m is kk * 32 + 8 (m / 4) + 4 r + m % 4
+            v8 yf[2];
 #pragma unroll
-        for (int kk = 0; kk < KX; ++kk)
+            for (int r = 0; r < 2; ++r)
+                yf[r] = TY::col8(y, kk * 32 + (lane & 3) * 8 + r * 4, kk * 32 + (c >> 2) * 8 + r * 4 + (c & 3));
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                // rows of the state permuted like zcol: row m is kk * 32 + 8 (m / 4) + 4 r + m % 4
-                const v8 yf = TY::col8(y, kk * 32 + (lane & 3) * 8 + r * 4, kk * 32 + (c >> 2) * 8 + r * 4 + (c & 3));
+            for (int p = 0; p < TERMS * Mma<T>::kParts; ++p)
 #pragma unroll
-                for (int q = 0; q < NT; ++q)
+                for (int r = 0; r < 2; ++r)
 #pragma unroll
-                    for (int s = 0; s < TERMS; ++s) E[kk][r][q] = Mma<T>::mma(yf, zs[q][s], E[kk][r][q]);
-            }
+                    for (int q = 0; q < NT; ++q)
+                        E[kk][r][q] = Mma<T>::mma(yf[r], zs[q][p / Mma<T>::kParts], E[kk][r][q], p % Mma<T>::kParts);
+        }
     };
     __syncthreads();       // the tables above
     for (int64_t t = t_begin; t < t_end; t += S * kChunk) {
@@ -692,8 +689,13 @@ template <int V> static __global__ __launch_bounds__(256) void decay_chain_kerne
     SegInfo si;
     if (!find_segment(a, blockIdx.x, true, si)) return;
     const int h = blockIdx.y;
-    const int64_t nst = (int64_t)a.DX * a.DZ, e = (blockIdx.z / set.kinds * (int64_t)256 + threadIdx.x) * V;
+    const uint32_t nst = (uint32_t)(a.DX * a.DZ), e = (blockIdx.z / set.kinds * 256 + threadIdx.x) * V;
     if (e >= nst) return;
+    // place of element e + i in a state whose element (x, z) is at x sx + z sz
+    auto place = [&](int i, uint32_t sx, uint32_t sz) {
+        const uint32_t x = (e + i) / (uint32_t)a.DZ;
+        return x * sx + (e + i - x * (uint32_t)a.DZ) * sz;
+    };
     const float log2d = a.log_decay[h] * kLog2e;
     const float dn = decay_power(log2d, a.seglen), dlast = decay_power(log2d, si.len - (si.count - 1) * a.seglen);
     const int64_t slot = state_slot(a.slots, a.n_slots, si.seq);
@@ -701,10 +703,10 @@ template <int V> static __global__ __launch_bounds__(256) void decay_chain_kerne
     if (slot >= 0 && a.state0) {
 #pragma unroll
         for (int i = 0; i < V; ++i)
-            run[i] = a.state0[(slot * a.H + h) * nst + (e + i) / a.DZ * a.s0x + (e + i) % a.DZ * a.s0z];
+            run[i] = a.state0[(slot * a.H + h) * nst + place(i, (uint32_t)a.s0x, (uint32_t)a.s0z)];
     }
     float *p = a.seg + (si.slot * a.H + h) * nst + e;
-    const int64_t step = a.H * nst;
+    const int64_t step = (int64_t)a.H * nst;
     // sums to add, and states to write (the walks start at the first part of a segment)
     const int64_t sums = a.state1 ? si.count : parts_before_last(a, si.count), states = parts_before_last(a, si.count) + 1;
     constexpr int U = 8;
@@ -725,7 +727,7 @@ template <int V> static __global__ __launch_bounds__(256) void decay_chain_kerne
     if (slot >= 0 && a.state1) {
 #pragma unroll
         for (int i = 0; i < V; ++i)
-            a.state1[(slot * a.H + h) * nst + (e + i) / a.DZ * a.s1x + (e + i) % a.DZ * a.s1z] = run[i];
+            a.state1[(slot * a.H + h) * nst + place(i, (uint32_t)a.s1x, (uint32_t)a.s1z)] = run[i];
     }
 }
 

@@ -64,6 +64,51 @@ template <> struct Mma<float> {
     static constexpr bool kNarrow = false;
 };
 
+// Splits eight fp32 values into TERMS operands of the storage type whose sum holds them: the products
+// of all terms with another operand add up to the product with the value.
+template <typename T, int TERMS> __device__ __forceinline__ void split8(const float (&x)[8], typename Mma<T>::v8 (&out)[TERMS]) {
+    if constexpr (sizeof(T) == 2 && TERMS > 1 && !Mma<T>::kNarrow) {
+        // bf16 is the upper half of fp32: cutting it off leaves an exact rest, so three terms of 8 bits hold
+        // all 24 and each costs one bit operation and one subtraction
+        float rest[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) rest[j] = x[j];
+#pragma unroll
+        for (int s = 0; s < TERMS; ++s) {
+            if (s == TERMS - 1 && TERMS < 3) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) out[s][j] = (T)rest[j];      // the last of two, rounded
+                continue;
+            }
+            uint32_t u[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)     // upper halves of two values: bytes 2, 3 of each
+                u[j] = __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, rest[2 * j + 1]), __builtin_bit_cast(uint32_t, rest[2 * j]),
+                                             0x07060302u);
+            __builtin_memcpy(&out[s], u, 16);
+            if (s + 1 < TERMS) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    rest[j] -= __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, rest[j]) & 0xffff0000u);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            float rest = x[j];
+            // one value for every use: left to itself the compiler rounds a product to fp16 once through
+            // fp32 and once fused, and the two first terms then differ at ties
+            if (TERMS > 1) asm("" : "+v"(rest));
+#pragma unroll
+            for (int s = 0; s < TERMS; ++s) {
+                const T part = (T)rest;
+                out[s][j] = part;
+                rest -= (float)part;
+            }
+        }
+    }
+}
+
 // A raw buffer view at a wave-uniform p whose offsets up to 2^31 - 2 are in range; kSkip is out of
 // range, so a load there reads zero and a store there writes nothing.  Lanes that have nothing to do
 // take that offset instead of a branch: the accumulators then never live across a region that runs with
