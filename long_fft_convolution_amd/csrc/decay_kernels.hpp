@@ -32,7 +32,7 @@
 // as operands of O (an error like the output's own rounding).  The state is
 // an fp32 result, so its update must not lose: d^(C-1-s) Z is split into
 // 2 (fp16) or 3 (bf16) storage-type terms that hold it to fp32 precision (2 in
-// bf16 where only outputs see the state).
+// bf16 in segments that another follows, whose state only outputs see).
 //
 // The accumulators hold E times a gain that grows by d^-C a chunk, so that
 // decaying the state costs one factor in the chunk's weights instead of a
@@ -46,6 +46,8 @@
 // first pass over y, z gives each segment's own sum, a small kernel chains
 // them into the state before each segment, and the walk starts from there.
 #pragma once
+
+#include <type_traits>
 
 #include "mma.hpp"
 #include "sequence_ops.hpp"
@@ -301,11 +303,11 @@ __device__ __forceinline__ void work_of(const DecaySet &set, uint32_t id, int &k
 // them fit a CU's 160 KB, else two; without LDS-destination loads one.
 constexpr int walk_stages(int bytes, bool vec) { return !vec ? 1 : (3 * bytes <= 78 * 1024 ? 3 : (2 * bytes <= 150 * 1024 ? 2 : 1)); }
 
-// MODE kSums: the segment's own sum only (y, z read), for every
-// segment that another follows; kOut: outputs in the storage type; kOutAny: in it or fp32, by the walk.  DXP: DX padded; NT: 16-column tiles of E per wave.
+// MODE kSums: the part's own sum only (y, z read), for every part
+// that another segment follows; kOut: outputs in the storage type; kOutAny: in it or fp32, by the walk.  DXP: DX padded; NT: 16-column tiles of E per wave.
 enum WalkMode : int { kSums = 0, kOut = 1, kOutAny = 2 };
 // grid: work items (see work_of)
-template <typename T, int DXP, int NT, int MODE, bool VEC, int TERMS>
+template <typename T, int DXP, int NT, int MODE, bool VEC>
 __global__ __launch_bounds__(256, DXP <= 128 ? 2 : 1) void decay_walk_kernel(const DecaySet set) {
 #ifdef __HIP_DEVICE_COMPILE__   // the host pass, which cannot take the scalar operands, needs the stub alone
     constexpr bool OUT = MODE != kSums;
@@ -332,8 +334,10 @@ __global__ __launch_bounds__(256, DXP <= 128 ? 2 : 1) void decay_walk_kernel(con
     if (blk >= a.nblk || zt * DZT >= a.DZ || !find_segment(a, blk, false, si)) return;
     si.seq = scalar(si.seq), si.index = scalar(si.index), si.count = scalar(si.count);
     si.start = scalar(si.start), si.len = scalar(si.len), si.slot = scalar(si.slot);
-    // only the final state wants the sums of the last segment's parts
-    if (!OUT && !a.state1 && si.index >= parts_before_last(a, si.count)) return;
+    if (!OUT && si.index >= parts_before_last(a, si.count)) return;
+    // The final state comes from the last segment, of the walks that may be asked for one: whether it is
+    // asked for changes no output's bits.
+    const bool exact = !OUT || (a.keeps && si.index + 1 == si.count);
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int g = lane >> 4, c = lane & 15;
@@ -528,33 +532,39 @@ __global__ __launch_bounds__(256, DXP <= 128 ? 2 : 1) void decay_walk_kernel(con
                     for (int q = 0; q < NT; ++q) E[kk][r][q] *= dn;
         }
         grown = next;
-        v8 zs[NT][TERMS];
         float w[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) w[j] = upd[kChunk - n + g * 8 + j] * gain;
+        auto update = [&](auto terms) __attribute__((always_inline)) {
+            constexpr int TERMS = decltype(terms)::value;
+            v8 zs[NT][TERMS];
 #pragma unroll
-        for (int q = 0; q < NT; ++q) {
-            float weighted[8];
+            for (int q = 0; q < NT; ++q) {
+                float weighted[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) weighted[j] = (float)zf[q][j] * w[j];
-            split8<T, TERMS>(weighted, zs[q]);
-        }
-        // terms outermost: an accumulator's next product comes 2 NT instructions later, past their latency
+                for (int j = 0; j < 8; ++j) weighted[j] = (float)zf[q][j] * w[j];
+                split8<T, TERMS>(weighted, zs[q]);
+            }
+            // terms outermost: an accumulator's next product comes 2 NT instructions later, past their latency
 #pragma unroll
-        for (int kk = 0; kk < KX; ++kk) {
-            // rows of the state permuted like zcol: row m is kk * 32 + 8 (m / 4) + 4 r + m % 4
-            v8 yf[2];
-#pragma unroll
-            for (int r = 0; r < 2; ++r)
-                yf[r] = TY::col8(y, kk * 32 + (lane & 3) * 8 + r * 4, kk * 32 + (c >> 2) * 8 + r * 4 + (c & 3));
-#pragma unroll
-            for (int p = 0; p < TERMS * Mma<T>::kParts; ++p)
+            for (int kk = 0; kk < KX; ++kk) {
+                // rows of the state permuted like zcol: row m is kk * 32 + 8 (m / 4) + 4 r + m % 4
+                v8 yf[2];
 #pragma unroll
                 for (int r = 0; r < 2; ++r)
+                    yf[r] = TY::col8(y, kk * 32 + (lane & 3) * 8 + r * 4, kk * 32 + (c >> 2) * 8 + r * 4 + (c & 3));
 #pragma unroll
-                    for (int q = 0; q < NT; ++q)
-                        E[kk][r][q] = Mma<T>::mma(yf[r], zs[q][p / Mma<T>::kParts], E[kk][r][q], p % Mma<T>::kParts);
-        }
+                for (int p = 0; p < TERMS * Mma<T>::kParts; ++p)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r)
+#pragma unroll
+                        for (int q = 0; q < NT; ++q)
+                            E[kk][r][q] = Mma<T>::mma(yf[r], zs[q][p / Mma<T>::kParts], E[kk][r][q], p % Mma<T>::kParts);
+            }
+        };
+        constexpr int kExact = Mma<T>::kExactTerms, kTerms = Mma<T>::kTerms;
+        if (!OUT || kExact == kTerms || exact) update(std::integral_constant<int, kExact>{});
+        else update(std::integral_constant<int, kTerms>{});
     };
     __syncthreads();       // the tables above
     for (int64_t t = t_begin; t < t_end; t += S * kChunk) {
@@ -577,7 +587,7 @@ __global__ __launch_bounds__(256, DXP <= 128 ? 2 : 1) void decay_walk_kernel(con
         s1 = a.seg + ((si.slot + si.index) * a.H + h) * (int64_t)a.DX * a.DZ;
         sx_ = (uint32_t)a.segx;
         sz_ = (uint32_t)a.segz;
-    } else if (a.state1 && !a.seg) {      // segmented: the chain kernel has it
+    } else if (a.state1 && si.index + 1 == si.count) {
         const int64_t slot = state_slot(a.slots, a.n_slots, si.seq);
         if (slot >= 0) s1 = a.state1 + (slot * a.H + h) * (int64_t)a.DX * a.DZ;
     }
@@ -681,7 +691,7 @@ template <typename T, int V> __global__ __launch_bounds__(256) void decay_group_
     }
 }
 
-// State before each segment from the segments' own sums, in place, and the final state:
+// State before each segment from the parts' own sums, in place:
 // grid (B, H, kinds x pieces of 256 V values).  V = 4: Dx * Dz a multiple of 4.
 template <int V> static __global__ __launch_bounds__(256) void decay_chain_kernel(const DecaySet set) {
     const DecayWalk &a = set.w[blockIdx.z % set.kinds];
@@ -697,7 +707,7 @@ template <int V> static __global__ __launch_bounds__(256) void decay_chain_kerne
         return x * sx + (e + i - x * (uint32_t)a.DZ) * sz;
     };
     const float log2d = a.log_decay[h] * kLog2e;
-    const float dn = decay_power(log2d, a.seglen), dlast = decay_power(log2d, si.len - (si.count - 1) * a.seglen);
+    const float dn = decay_power(log2d, a.seglen);
     const int64_t slot = state_slot(a.slots, a.n_slots, si.seq);
     vec run = 0.0f;
     if (slot >= 0 && a.state0) {
@@ -707,32 +717,25 @@ template <int V> static __global__ __launch_bounds__(256) void decay_chain_kerne
     }
     float *p = a.seg + (si.slot * a.H + h) * nst + e;
     const int64_t step = (int64_t)a.H * nst;
-    // sums to add, and states to write (the walks start at the first part of a segment)
-    const int64_t sums = a.state1 ? si.count : parts_before_last(a, si.count), states = parts_before_last(a, si.count) + 1;
+    const int64_t sums = parts_before_last(a, si.count);     // the state behind them is the last segment's
     constexpr int U = 8;
     int to_state = 0;       // parts until the next segment starts
-    for (int64_t s = 0; s < sums || s < states; s += U) {
+    for (int64_t s = 0; s <= sums; s += U) {
         vec own[U];
 #pragma unroll
-        for (int j = 0; j < U; ++j)
-            own[j] = s + j < sums ? *reinterpret_cast<const vec *>(p + (s + j) * step) : (vec)0.0f;
+        for (int j = 0; j < U; ++j) own[j] = s + j < sums ? *reinterpret_cast<const vec *>(p + (s + j) * step) : (vec)0.0f;
 #pragma unroll
         for (int j = 0; j < U; ++j)
-            if (s + j < sums || s + j < states) {
-                if (to_state == 0 && s + j < states) *reinterpret_cast<vec *>(p + (s + j) * step) = run;
+            if (s + j <= sums) {
+                if (to_state == 0) *reinterpret_cast<vec *>(p + (s + j) * step) = run;
                 to_state = to_state == 0 ? a.parts - 1 : to_state - 1;
-                run = (s + j + 1 < si.count ? dn : dlast) * run + own[j];
+                run = dn * run + own[j];
             }
-    }
-    if (slot >= 0 && a.state1) {
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-            a.state1[(slot * a.H + h) * nst + place(i, (uint32_t)a.s1x, (uint32_t)a.s1z)] = run[i];
     }
 }
 
 // ---- host side of one storage type ----------------------------------------
-template <typename T, int MODE, bool VEC, int TERMS> static hipError_t walk_launch(const DecaySet &set, hipStream_t stream) {
+template <typename T, int MODE, bool VEC> static hipError_t walk_launch(const DecaySet &set, hipStream_t stream) {
     bool narrow = true;
     int dx = 0;
     for (int i = 0; i < set.kinds; ++i) {
@@ -744,36 +747,32 @@ template <typename T, int MODE, bool VEC, int TERMS> static hipError_t walk_laun
     // (rows wider than 128 leave registers for 64 z columns only: decay_z_tile)
     if (dx > 128) {
         if (!narrow) return hipErrorInvalidValue;
-        decay_walk_kernel<T, 256, 1, MODE, VEC, TERMS><<<grid, 256, 0, stream>>>(set);
+        decay_walk_kernel<T, 256, 1, MODE, VEC><<<grid, 256, 0, stream>>>(set);
     } else if (dx > 64) {
-        if (narrow) decay_walk_kernel<T, 128, 1, MODE, VEC, TERMS><<<grid, 256, 0, stream>>>(set);
-        else decay_walk_kernel<T, 128, 2, MODE, VEC, TERMS><<<grid, 256, 0, stream>>>(set);
+        if (narrow) decay_walk_kernel<T, 128, 1, MODE, VEC><<<grid, 256, 0, stream>>>(set);
+        else decay_walk_kernel<T, 128, 2, MODE, VEC><<<grid, 256, 0, stream>>>(set);
     } else {
-        if (narrow) decay_walk_kernel<T, 64, 1, MODE, VEC, TERMS><<<grid, 256, 0, stream>>>(set);
-        else decay_walk_kernel<T, 64, 2, MODE, VEC, TERMS><<<grid, 256, 0, stream>>>(set);
+        if (narrow) decay_walk_kernel<T, 64, 1, MODE, VEC><<<grid, 256, 0, stream>>>(set);
+        else decay_walk_kernel<T, 64, 2, MODE, VEC><<<grid, 256, 0, stream>>>(set);
     }
     return hipGetLastError();
 }
 
 template <typename T> static hipError_t walks_typed(const DecaySet &set, hipStream_t stream) {
-    // Only a walk from a sequence's beginning may return its state.  The choice does not look at what was
-    // asked for, so an output's bits do not depend on the other outputs.
-    constexpr int kExact = Mma<T>::kExactTerms, kTerms = Mma<T>::kTerms;
-    bool vec = true;
-    for (int i = 0; i < set.kinds; ++i) vec = vec && set.w[i].vec_x && set.w[i].vec_y && set.w[i].vec_z && set.w[i].vec_o;
-    bool any = false;
-    for (int i = 0; i < set.kinds; ++i) any = any || set.w[i].out_f32;
-    if (!vec) return walk_launch<T, kOutAny, false, kExact>(set, stream);
-    if (any) return set.w[0].seg ? walk_launch<T, kOutAny, true, kTerms>(set, stream) : walk_launch<T, kOutAny, true, kExact>(set, stream);
-    return set.w[0].seg ? walk_launch<T, kOut, true, kTerms>(set, stream) : walk_launch<T, kOut, true, kExact>(set, stream);
+    bool vec = true, any = false;
+    for (int i = 0; i < set.kinds; ++i) {
+        vec = vec && set.w[i].vec_x && set.w[i].vec_y && set.w[i].vec_z && set.w[i].vec_o;
+        any = any || set.w[i].out_f32;
+    }
+    if (!vec) return walk_launch<T, kOutAny, false>(set, stream);
+    return any ? walk_launch<T, kOutAny, true>(set, stream) : walk_launch<T, kOut, true>(set, stream);
 }
 
 template <typename T> static hipError_t sums_typed(const DecaySet &set, hipStream_t stream) {
     if (!set.w[0].seg) return hipSuccess;
-    constexpr int kExact = Mma<T>::kExactTerms;
     bool vec = true;
     for (int i = 0; i < set.kinds; ++i) vec = vec && set.w[i].vec_y && set.w[i].vec_z;
-    const hipError_t e = vec ? walk_launch<T, kSums, true, kExact>(set, stream) : walk_launch<T, kSums, false, kExact>(set, stream);
+    const hipError_t e = vec ? walk_launch<T, kSums, true>(set, stream) : walk_launch<T, kSums, false>(set, stream);
     if (e != hipSuccess) return e;
     const int64_t nst = (int64_t)set.w[0].DX * set.w[0].DZ;
     const bool quads = nst % 4 == 0;

@@ -352,7 +352,7 @@ fftconv_status_t fftconv_decay_fwd(const void *q, const void *k, const void *v, 
     set_z(w, vv, H);
     set_out(w, vo, H);
     w.log_decay = log_decay;
-    w.state0 = state_in, w.state1 = state_out;
+    w.state0 = state_in, w.state1 = state_out, w.keeps = 1;
     w.s0x = w.s1x = Dv, w.s0z = w.s1z = 1;
     w.slots = state_slots, w.n_slots = n_slots;
     w.cu = cu_seqlens;
@@ -508,7 +508,7 @@ fftconv_status_t fftconv_decay_bwd(const void *dout, const void *q, const void *
     set_z(k_, vq, H);
     set_grad(k_, gk, lay.dk);
     k_.s0x = 1, k_.s0z = Dv;
-    k_.state1 = dstate_in, k_.s1x = 1, k_.s1z = Dv;
+    k_.state1 = dstate_in, k_.s1x = 1, k_.s1z = Dv, k_.keeps = 1;
     k_.segx = Dk, k_.segz = 1;
     // dv: x, y, z = k, q, dout, state G (Dk x Dv): the same sums read the other way round
     DecayWalk v_ = w;
@@ -519,9 +519,8 @@ fftconv_status_t fftconv_decay_bwd(const void *dout, const void *q, const void *
     v_.s0x = Dv, v_.s0z = 1;
     v_.segx = 1, v_.segz = Dk;
 
-    const bool run_q = dq && tokens, run_v = dv && tokens, sum_g = (dk && tokens) || run_v || dstate_in;
-    // the state's own gradient comes from the chain of sums, or from dk's walk when there are none
-    const bool run_k = (dk && tokens) || (dstate_in && !cut);
+    // the gradient of the carried state comes out of dk's walk
+    const bool run_q = dq && tokens, run_k = (dk && tokens) || dstate_in, run_v = dv && tokens, sum_g = run_k || run_v;
     const DecaySet sums = make_set({run_q ? &q_ : nullptr, sum_g ? &k_ : nullptr}, H / Hk);
     const DecaySet all = make_set({&q_, &k_, &v_}, H / Hk);
     if (too_many(all) || too_many(parts_of(all, c)))

@@ -36,6 +36,7 @@ struct DecayWalk {
     int64_t segx, segz;              // their strides along DX and DZ
     float p_scale, u_scale, i_scale;
     int off, reverse;
+    int keeps;                       // this kind of walk can return its final state
     int vec_x, vec_y, vec_z, vec_o;  // 16-byte access allowed
     int out_f32;                     // out is fp32 (a part of a sum over heads), else the storage type
 };
