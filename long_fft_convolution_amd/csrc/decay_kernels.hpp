@@ -265,7 +265,7 @@ template <typename T, int DP, bool PERMUTED, bool VEC> struct ChunkSource {
                 T e[Tile::E];
 #pragma unroll
                 for (int j = 0; j < Tile::E; ++j)
-                    e[j] = view_load<T>(view, row < n && col + j < cols ? at + j * (uint32_t)sizeof(T) : kSkip);
+                    e[j] = view_load<T>(view, (row < n) & (col + j < cols) ? at + j * (uint32_t)sizeof(T) : kSkip);
                 __builtin_memcpy(tile + (i * 256 + (threadIdx.x & 255)) * Tile::E, e, 16);
             }
         }
@@ -279,12 +279,12 @@ __device__ __forceinline__ void put_row(__amdgpu_buffer_rsrc_t view, uint32_t of
     struct Row { TO w[NT * 4]; } row;
 #pragma unroll
     for (int j = 0; j < NT * 4; ++j) row.w[j] = (TO)o[j >> 2][j & 3];
-    const bool whole = WHOLE || (vec && NT * 4 <= left);
+    const bool whole = WHOLE | ((vec != 0) & (NT * 4 <= left));
     view_store(view, whole ? off : kSkip, row);
     if (!WHOLE) {
 #pragma unroll
         for (int j = 0; j < NT * 4; ++j)
-            view_store(view, !whole && j < left && off != kSkip ? off + j * (uint32_t)sizeof(TO) : kSkip, row.w[j]);
+            view_store(view, (!whole) & (j < left) & (off != kSkip) ? off + j * (uint32_t)sizeof(TO) : kSkip, row.w[j]);
     }
 }
 
@@ -383,17 +383,30 @@ __global__ __launch_bounds__(256, DXP <= 128 ? 2 : 1) void decay_walk_kernel(con
             if (slot >= 0) s0 = a.state0 + (slot * a.H + h) * (int64_t)a.DX * a.DZ;
         }
         const auto view = wide_view(s0);
+        if (OUT && a.seg && a.segx == 1 && a.DX % 4 == 0) {      // the segments' states: four rows of a column together
 #pragma unroll
-        for (int kk = 0; kk < KX; ++kk)
+            for (int kk = 0; kk < KX; ++kk)
 #pragma unroll
-            for (int r = 0; r < 2; ++r)
+                for (int r = 0; r < 2; ++r)
 #pragma unroll
-                for (int t = 0; t < NT; ++t)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int dx = kk * 32 + g * 8 + r * 4 + i, dz = col0 + zcol(c, t);
-                        E[kk][r][t][i] = view_load<float>(view, s0 && dx < a.DX && dz < a.DZ ? (uint32_t)(dx * sx_ + dz * sz_) * 4u : kSkip);
+                    for (int t = 0; t < NT; ++t) {
+                        const int dx = kk * 32 + g * 8 + r * 4, dz = col0 + zcol(c, t);
+                        E[kk][r][t] = view_load_wide<f32x4>(view, (dx < a.DX) & (dz < a.DZ) ? (uint32_t)(dx + dz * sz_) * 4u : kSkip);
                     }
+        } else {
+#pragma unroll
+            for (int kk = 0; kk < KX; ++kk)
+#pragma unroll
+                for (int r = 0; r < 2; ++r)
+#pragma unroll
+                    for (int t = 0; t < NT; ++t)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int dx = kk * 32 + g * 8 + r * 4 + i, dz = col0 + zcol(c, t);
+                            const uint32_t at = (uint32_t)(dx * sx_ + dz * sz_) * 4u;
+                            E[kk][r][t][i] = view_load<float>(view, (s0 != nullptr) & (dx < a.DX) & (dz < a.DZ) ? at : kSkip);
+                        }
+        }
     }
     // decay of P in row tile rt, accumulator (r, i): d^(16 rt + c - 8 g - 4 r - i), 0 above the diagonal
     float fac[2][2][4];
@@ -417,7 +430,7 @@ __global__ __launch_bounds__(256, DXP <= 128 ? 2 : 1) void decay_walk_kernel(con
 #pragma unroll
     for (int rt = 0; rt < 2; ++rt) {
         const int row = rt * 16 + c;
-        out_off[rt] = out_cols > 0 && a.out ? (uint32_t)((a.reverse ? kChunk - 1 - row : row) * a.ot + zl) * out_e : kSkip;
+        out_off[rt] = (out_cols > 0) & (a.out != nullptr) ? (uint32_t)((a.reverse ? kChunk - 1 - row : row) * a.ot + zl) * out_e : kSkip;
     }
     float grown = 0.0f;    // the accumulators hold E * 2^(grown + ex); grown = -log2 d * held
     int held = 0;
@@ -593,6 +606,19 @@ __global__ __launch_bounds__(256, DXP <= 128 ? 2 : 1) void decay_walk_kernel(con
     }
     if (!s1) return;
     const auto view = wide_view(s1);
+    if (!OUT && sx_ == 1 && a.DX % 4 == 0) {
+#pragma unroll
+        for (int kk = 0; kk < KX; ++kk)
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    const int dx = kk * 32 + g * 8 + r * 4, dz = col0 + zcol(c, t);
+                    const f32x4 e = E[kk][r][t] * unscale;
+                    view_store(view, (dx < a.DX) & (dz < a.DZ) ? (uint32_t)(dx + dz * sz_) * 4u : kSkip, e);
+                }
+        return;
+    }
 #pragma unroll
     for (int kk = 0; kk < KX; ++kk)
 #pragma unroll
@@ -602,7 +628,9 @@ __global__ __launch_bounds__(256, DXP <= 128 ? 2 : 1) void decay_walk_kernel(con
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int dx = kk * 32 + g * 8 + r * 4 + i, dz = col0 + zcol(c, t);
-                    view_store(view, dx < a.DX && dz < a.DZ ? (uint32_t)(dx * sx_ + dz * sz_) * 4u : kSkip, E[kk][r][t][i] * unscale);
+                    const uint32_t at = (uint32_t)(dx * sx_ + dz * sz_) * 4u;
+                    const float e = E[kk][r][t][i] * unscale;
+                    view_store(view, (dx < a.DX) & (dz < a.DZ) ? at : kSkip, e);
                 }
 #endif
 }
@@ -701,10 +729,10 @@ template <int V> static __global__ __launch_bounds__(256) void decay_chain_kerne
     const int h = blockIdx.y;
     const uint32_t nst = (uint32_t)(a.DX * a.DZ), e = (blockIdx.z / set.kinds * 256 + threadIdx.x) * V;
     if (e >= nst) return;
-    // place of element e + i in a state whose element (x, z) is at x sx + z sz
+    // place in a state whose element (x, z) is at x sx + z sz of what lies at e + i in a segment's
     auto place = [&](int i, uint32_t sx, uint32_t sz) {
-        const uint32_t x = (e + i) / (uint32_t)a.DZ;
-        return x * sx + (e + i - x * (uint32_t)a.DZ) * sz;
+        const uint32_t row = (uint32_t)(a.segx == 1 ? a.DX : a.DZ), hi = (e + i) / row, lo = e + i - hi * row;
+        return a.segx == 1 ? lo * sx + hi * sz : hi * sx + lo * sz;
     };
     const float log2d = a.log_decay[h] * kLog2e;
     const float dn = decay_power(log2d, a.seglen);

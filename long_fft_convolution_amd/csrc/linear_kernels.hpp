@@ -420,7 +420,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void linear_gemm_kernel(const Line
             for (int j = 0; j < TN; ++j) {
                 const int col = hb * HN + wn + j * 16 + g * 4;
                 const uint32_t x = (uint32_t)col * (uint32_t)sizeof(T);
-                const Q qb = view_load_wide<Q>(vb, a.bias && col < cols ? x : kSkip);
+                const Q qb = view_load_wide<Q>(vb, (a.bias != nullptr) & (col < cols) ? x : kSkip);
                 float bias[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) bias[e] = (float)qb.v[e];
@@ -429,7 +429,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void linear_gemm_kernel(const Line
 #pragma unroll
                     for (int i = 0; i < TM; ++i) {
                         const int row = ha * HM + wm + i * 16 + c;
-                        const bool in = row < rows && col < cols;
+                        const bool in = (row < rows) & (col < cols);
                         float f[4];
                         Q q;
 #pragma unroll

@@ -362,7 +362,7 @@ fftconv_status_t fftconv_decay_fwd(const void *q, const void *k, const void *v, 
     const DecayCut cut = fwd_cut(s);
     set_cut(w, cut);
     w.seg = cut.cut ? static_cast<float *>(workspace) : nullptr;
-    w.segx = Dv, w.segz = 1;
+    w.segx = 1, w.segz = Dk;
     const DecaySet set = make_set({&w}, H / Hk), sums = parts_of(set, cut);
     if (too_many(set) || too_many(sums))
         return fail(FFTCONV_ERR_UNSUPPORTED, "B=%lld, N=%lld, H=%lld: too many sequences or tokens", (long long)B,
@@ -490,7 +490,7 @@ fftconv_status_t fftconv_decay_bwd(const void *dout, const void *q, const void *
     q_.state0 = state_in, q_.s0x = 1, q_.s0z = Dv;
     q_.p_scale = scale, q_.u_scale = 1.0f, q_.i_scale = scale;
     q_.off = 1;
-    q_.seg = cut ? reinterpret_cast<float *>(base) : nullptr, q_.segx = Dk, q_.segz = 1;
+    q_.seg = cut ? reinterpret_cast<float *>(base) : nullptr, q_.segx = 1, q_.segz = Dv;
     // dk: x, y, z = v, dout, q from each sequence's end, state G^T (Dv x Dk)
     auto set_grad = [&](DecayWalk &g, const View &grad, size_t part) {
         View o = grad;
@@ -509,7 +509,7 @@ fftconv_status_t fftconv_decay_bwd(const void *dout, const void *q, const void *
     set_grad(k_, gk, lay.dk);
     k_.s0x = 1, k_.s0z = Dv;
     k_.state1 = dstate_in, k_.s1x = 1, k_.s1z = Dv, k_.keeps = 1;
-    k_.segx = Dk, k_.segz = 1;
+    k_.segx = 1, k_.segz = Dv;
     // dv: x, y, z = k, q, dout, state G (Dk x Dv): the same sums read the other way round
     DecayWalk v_ = w;
     set_x(v_, vk, H);
@@ -517,7 +517,7 @@ fftconv_status_t fftconv_decay_bwd(const void *dout, const void *q, const void *
     set_z(v_, vd, H);
     set_grad(v_, gv, lay.dv);
     v_.s0x = Dv, v_.s0z = 1;
-    v_.segx = 1, v_.segz = Dk;
+    v_.segx = Dv, v_.segz = 1;
 
     // the gradient of the carried state comes out of dk's walk
     const bool run_q = dq && tokens, run_k = (dk && tokens) || dstate_in, run_v = dv && tokens, sum_g = run_k || run_v;
