@@ -151,7 +151,7 @@ __device__ __forceinline__ void lds_load16(const void *p, void *dst, uint32_t of
     const uint64_t base = reinterpret_cast<uint64_t>(p);
     const u32x4 view = {(uint32_t)base, (uint32_t)(base >> 32) & 0xffffu, 0x7fffffffu, 0x00020000u};
     const uint32_t at = (uint32_t)(uintptr_t)FFTCONV_LDS_CAST(void, dst);
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(at), "v"(off), "s"(view) : "memory");
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(at), "v"(off), "s"(view) : "memory", "m0");
 }
 // Waits until at most LEFT of this wave's vector loads and stores, and none of its LDS reads, are on their
 // way, then for the other waves of the workgroup.

@@ -112,6 +112,7 @@ constexpr int64_t kMaxHeadDim = 256;
 constexpr int64_t kSegStep = 64;          // parts of a segment are whole chunks
 constexpr int64_t kMinSegment = 256;      // below this the second read of y, z costs more than it spreads
 constexpr int64_t kCus = 256;
+constexpr int64_t kMaxGroups = (int64_t(1) << 24) - 1;   // workgroups of 256 threads: a launch has fewer than 2^32 threads
 
 int64_t z_tiles(int64_t dx, int64_t dz) { return ceil_div(dz, decay_z_tile(dx, dz)); }
 
@@ -211,7 +212,7 @@ fftconv_status_t check_shape(const DecayShape &s, float scale) {
         return fail(FFTCONV_ERR_INVALID_ARGUMENT, "H=%lld must be a multiple of Hk=%lld", (long long)s.H, (long long)s.Hk);
     if (s.H > 65535) return fail(FFTCONV_ERR_UNSUPPORTED, "H=%lld is above 65535", (long long)s.H);
     if (s.B >= (int64_t(1) << 31) || s.N >= (int64_t(1) << 31) || (s.B > 0 && s.N > (int64_t(1) << 40) / s.B) ||
-        (s.H > 0 && s.B > ((int64_t(1) << 31) - 1) / s.H))
+        (s.H > 0 && s.B > kMaxGroups / s.H))
         return fail(FFTCONV_ERR_UNSUPPORTED, "B=%lld, N=%lld, H=%lld: too many sequences or tokens", (long long)s.B,
                     (long long)s.N, (long long)s.H);
     if (!std::isfinite(scale)) return fail(FFTCONV_ERR_INVALID_ARGUMENT, "scale must be finite");
@@ -296,7 +297,7 @@ bool same_class(const DecayWalk &a, const DecayWalk &b) {
 }
 // items of a launch, as a check that they fit a grid
 bool too_many(const DecaySet &s) {
-    return (double)s.w[0].nblk * s.w[0].H * s.ztiles * s.kinds + 8 * 16 > 2147483647.0;
+    return (double)s.w[0].nblk * s.w[0].H * s.ztiles * s.kinds + 8 * 16 > (double)kMaxGroups;
 }
 
 }  // namespace
@@ -613,11 +614,22 @@ hipError_t run_gemm(int dt, LinearGemm &g, int layout, bool vec, float *part, hi
     const int64_t reach = (int64_t(1) << 22) / elem_bytes(dt);
     g.quads = g.N % 4 == 0 && g.vec_c && g.ldc < reach && (!g.bias || g.vec_b) && (!g.res || (g.vec_r && g.ldr < reach)) &&
               (!g.pre || (g.vec_p && g.ldp < reach));
-    if (p.full + (p.tiles - p.full) * p.splits > 0x7fffffff) return hipErrorInvalidValue;
     g.tiles = p.tiles, g.full = p.full, g.splits = p.splits, g.kper = p.kper, g.part = part;
     return dt == FFTCONV_F32   ? launch_linear_gemm_f32(g, layout, p.tile, vec, s)
            : dt == FFTCONV_F16 ? launch_linear_gemm_f16(g, layout, p.tile, vec, s)
                                : launch_linear_gemm_bf16(g, layout, p.tile, vec, s);
+}
+
+// a launch has fewer than 2^32 threads: 512 a tile; 16 a column or more in the kernels that go over rows
+bool too_large(int64_t M, int64_t N, int64_t K, int dt) {
+    for (bool vec : {true, false}) {
+        const GemmPlan p = plan_gemm(M, N, K, dt, vec);
+        if (p.full + (p.tiles - p.full) * p.splits >= int64_t(1) << 23) return true;
+    }
+    return N >= int64_t(1) << 28;
+}
+fftconv_status_t too_large_status(int64_t M, int64_t N, int64_t K) {
+    return fail(FFTCONV_ERR_UNSUPPORTED, "M=%lld, N=%lld, K=%lld: too large a product", (long long)M, (long long)N, (long long)K);
 }
 
 fftconv_status_t check_linear(int64_t M, int64_t N, int64_t K, int act, int dt) {
@@ -655,6 +667,7 @@ fftconv_status_t fftconv_linear_fwd(const void *x, const void *W, const void *bi
     fftconv_status_t st = check_linear(M, N, K, activation, dtype);
     if (st != FFTCONV_OK) return st;
     if (M == 0 || N == 0) return ok();
+    if (too_large(M, N, K, dtype)) return too_large_status(M, N, K);
     auto ld = [&](int i, int64_t dense) { return strides ? strides[i] : dense; };
     const View vx = matrix("x", x, M, K, ld(0, K), dtype), vw = matrix("W", W, N, K, ld(1, K), dtype),
                vb = matrix("bias", bias, 1, N, N, dtype), vr = matrix("residual", residual, M, N, ld(2, N), dtype),
@@ -733,6 +746,7 @@ fftconv_status_t fftconv_linear_bwd(const void *dout, const void *x, const void 
                vw = matrix("W", W, N, K, ld(2, K), dtype), vp = matrix("pre", pre, M, N, ld(3, N), dtype),
                gx = matrix("dx", dx, M, K, ld(4, K), dtype), gw = matrix("dW", dW, N, K, ld(5, K), dtype),
                gb = matrix("dbias", dbias, 1, N, N, dtype);
+    if (too_large(M, K, N, dtype) || too_large(N, K, M, dtype) || N >= int64_t(1) << 28) return too_large_status(M, N, K);
     const bool need_pre = activation != FFTCONV_ACT_NONE;
     if ((st = check_view(vd, true, false)) != FFTCONV_OK) return st;
     if ((st = check_view(vx, dW != nullptr, false)) != FFTCONV_OK) return st;

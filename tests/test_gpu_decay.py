@@ -284,3 +284,94 @@ def test_another_stream_and_graph_replay():
         torch.cuda.synchronize()
         want, want_S = fc.decay_attention(qg, kg, vg, ag, scale=0.2)
         assert torch.equal(out, want) and torch.equal(S, want_S)
+
+
+@pytest.mark.parametrize("H,Hk,Dk,Dv", [(1, 1, 128, 128), (2, 1, 72, 40), (1, 1, 200, 136)])
+@pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
+def test_packed_in_segments_of_several_parts(H, Hk, Dk, Dv, dtype):
+    lens = (1500, 0, 1000, 64)
+    _say(f"packed in segments {dtype} H={H}/{Hk} Dk={Dk} Dv={Dv}")
+    B, T = len(lens), sum(lens)
+    q, k, v, a = _inputs((T,), H, Hk, Dk, Dv, dtype, 11)
+    a[0] = -0.003
+    dout = _rand((T, H, Dv), DT[dtype], 9)
+    S0, dS = (_rand((B, H, Dk, Dv), torch.float32, s) for s in (5, 6))
+    cu = torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int32).cuda()
+    qg, kg, vg, ag, dg, S0g, dSg = _gpu(q, k, v, a, dout, S0, dS)
+    out, S = fc.decay_attention(qg, kg, vg, ag, scale=0.2, state_in=S0g, cu_seqlens=cu)
+    grads = fc.decay_attention_bwd(qg, kg, vg, ag, dg, scale=0.2, state_in=S0g, dstate_out=dSg, cu_seqlens=cu)
+    want, want_S = np.zeros(out.shape), np.zeros(S.shape)
+    want_g = [np.zeros(g.shape) for g in grads]
+    for b, (i, j) in enumerate(_sequences(lens)):
+        part = [_f64(t[i:j]) for t in (q, k, v)]
+        want[i:j], want_S[b] = seq.decay_fwd(*part, _f64(a), 0.2, _f64(S0[b]))
+        g = seq.decay_bwd(_f64(dout[i:j]), *part, _f64(a), 0.2, _f64(S0[b]), _f64(dS[b]))
+        for n in range(3):
+            want_g[n][i:j] = g[n]
+        want_g[3][b] = g[3]
+    _close(out, want, TOL[dtype], "out")
+    _close(S, want_S, STATE_TOL, "state")
+    for name, x, y in zip(("dq", "dk", "dv"), grads, want_g):
+        _close(x, y, TOL[dtype], name)
+    _close(grads[3], want_g[3], STATE_TOL, "dstate_in")
+
+
+def test_tokens_and_states_past_four_gibibytes():
+    # rows 16 MiB apart and the last states of a pool of 4.3 GiB
+    N, H, D, ld = 300, 1, 128, 1 << 23
+    slots, n_slots = (65800, 3), 65801
+    _say(f"tokens {ld} elements apart, pool of {n_slots} states")
+    q, k, v, a = _inputs((N,), H, H, D, D, "bf16", 21)
+    a[0] = -0.01
+    views = [torch.empty((N, ld), dtype=torch.bfloat16, device="cuda")[:, :D].unsqueeze(1) for i in range(4)]
+    for view, t in zip(views, (q, k, v)):
+        view.copy_(t)
+    pool = torch.empty((n_slots, H, D, D), device="cuda")
+    S0 = _rand((2, H, D, D), torch.float32, 5)
+    for i, slot in enumerate(slots):
+        pool[slot] = S0[i].cuda()
+    cu = torch.tensor([0, 200, N], dtype=torch.int32).cuda()
+    at = torch.tensor(slots, dtype=torch.int32).cuda()
+    ws = torch.empty(max(1, fc.fftconv_decay_fwd_workspace_bytes(2, N, H, D, D, torch.bfloat16)), dtype=torch.uint8,
+                     device="cuda")
+    fc.fftconv_decay_fwd(*views[:3], a.cuda(), views[3], 0.2, pool, pool, at, cu, ws)
+    states = []
+    for b, (i, j) in enumerate(((0, 200), (200, N))):
+        want, S = seq.decay_fwd(_f64(q[i:j]), _f64(k[i:j]), _f64(v[i:j]), _f64(a), 0.2, _f64(S0[b]))
+        _close(views[3][i:j], want, TOL["bf16"], f"out[{b}]")
+        _close(pool[slots[b]], S, STATE_TOL, f"state[{b}]")
+        states.append(S)
+    tok = [t[:2].contiguous() for t in (q, k, v)]
+    out = torch.empty((2, H, D), dtype=torch.bfloat16, device="cuda")
+    fc.fftconv_decay_step(*_gpu(*tok), a.cuda(), pool, out, 0.2, at)
+    for b in range(2):
+        want, S = seq.decay_fwd(*(_f64(t[b:b + 1]) for t in tok), _f64(a), 0.2, states[b])
+        _close(out[b:b + 1], want, TOL["bf16"], f"token[{b}]")
+        _close(pool[slots[b]], S, STATE_TOL, f"state after the token[{b}]")
+
+
+def test_graph_replays_of_gradients_and_tokens():
+    B, N, H, Hk, D = 2, 700, 4, 2, 64
+    q, k, v, a = _inputs((B, N), H, Hk, D, D, "bf16", 1)
+    qg, kg, vg, ag, dg = _gpu(q, k, v, a, _rand((B, N, H, D), torch.bfloat16, 2))
+    grads = fc.decay_attention_bwd(qg, kg, vg, ag, dg, 0.2)[:3]
+    ws = torch.empty(fc.fftconv_decay_bwd_workspace_bytes(B, B * N, H, Hk, D, D, torch.bfloat16), dtype=torch.uint8,
+                     device="cuda")
+    S = torch.zeros((B, H, D, D), device="cuda")
+    out = torch.empty((B, H, D), dtype=torch.bfloat16, device="cuda")
+    tok = [t[:, 0].contiguous() for t in (qg, kg, vg)]
+    fc.fftconv_decay_step(*tok, ag, S, out, 0.2)
+    S.zero_()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        fc.fftconv_decay_bwd(dg, qg, kg, vg, ag, *grads, 0.2, workspace=ws)
+        fc.fftconv_decay_step(*tok, ag, S, out, 0.2)
+    eager_S, eager_out = torch.zeros_like(S), torch.empty_like(out)
+    for seed in (5, 6, 7):
+        dg.copy_(_rand((B, N, H, D), torch.bfloat16, seed))
+        graph.replay()
+        torch.cuda.synchronize()
+        for got, want in zip(grads, fc.decay_attention_bwd(qg, kg, vg, ag, dg, 0.2)):
+            assert torch.equal(got, want)
+        fc.fftconv_decay_step(*tok, ag, eager_S, eager_out, 0.2)
+        assert torch.equal(S, eager_S) and torch.equal(out, eager_out)

@@ -166,3 +166,54 @@ def test_repeatable_and_on_another_stream():
         b = fc.linear_act(x, W)
     s.synchronize()
     assert torch.equal(a, b)
+
+
+WHOLE_AND_SPLIT = [
+    # more tiles than compute units with a rest that is split along K, of each tile width; rows of the few-rows kernel
+    (1000, 2304, 768), (4100, 4400, 640), (1030, 9000, 260), (2, 333, 4095), (4, 50, 31), (4, 1030, 768),
+]
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("M,N,K", WHOLE_AND_SPLIT)
+def test_whole_and_split_tiles(M, N, K, dtype):
+    test_forward(M, N, K, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("M,apart", [(80, 1 << 26), (4200, 1 << 20)])      # bytes
+def test_rows_past_four_gibibytes(M, apart, dtype):
+    N, K, ld = 72, 96, apart // (2 if dtype == "bf16" else 4)
+    _say(f"linear {dtype}, {M} rows {ld} elements apart")
+    x, W, d = _rand((M, K), DT[dtype], 1), _rand((N, K), DT[dtype], 2, 0.1), _rand((M, N), DT[dtype], 3)
+    xv, dv, ov = (torch.empty((M, ld), dtype=DT[dtype], device="cuda")[:, :n] for n in (K, N, N))
+    xv.copy_(x), dv.copy_(d)
+    fc.fftconv_linear_fwd(xv, W.cuda(), None, None, ov, None, "none",
+                          torch.empty(max(1, fc.fftconv_linear_fwd_workspace_bytes(M, N, K, DT[dtype])), dtype=torch.uint8,
+                                      device="cuda"))
+    _close(ov, seq.linear_fwd(_f64(x), _f64(W), None, None, "none")[0], TOL[dtype], "out")
+    dx, dW, db = fc.linear_act_bwd(dv, xv, W.cuda())
+    for name, got, want in zip(("dx", "dW", "dbias"), (dx, dW, db), seq.linear_bwd(_f64(d), _f64(x), _f64(W), None, "none")):
+        _close(got, want, TOL[dtype], name)
+
+
+def test_graph_replays_equal_eager_calls():
+    M, N, K = 200, 300, 2048
+    x, W, b = (_rand(s, torch.bfloat16, i, 0.1).cuda() for i, s in enumerate(((M, K), (N, K), (N,))))
+    d = _rand((M, N), torch.bfloat16, 9).cuda()
+    out, pre = fc.linear_act(x, W, b, None, "gelu", keep_pre=True)      # loads the kernels
+    grads = fc.linear_act_bwd(d, x, W, pre, "gelu")
+    size = max(fc.fftconv_linear_fwd_workspace_bytes(M, N, K, x.dtype), fc.fftconv_linear_bwd_workspace_bytes(M, N, K, x.dtype))
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        fc.fftconv_linear_fwd(x, W, b, None, out, pre, "gelu", ws)
+        fc.fftconv_linear_bwd(d, x, W, pre, *grads, "gelu", ws)
+    for seed in (20, 21, 22):
+        x.copy_(_rand((M, K), torch.bfloat16, seed, 0.1))
+        graph.replay()
+        torch.cuda.synchronize()
+        want, want_pre = fc.linear_act(x, W, b, None, "gelu", keep_pre=True)
+        assert torch.equal(out, want) and torch.equal(pre, want_pre)
+        for got, w in zip(grads, fc.linear_act_bwd(d, x, W, want_pre, "gelu")):
+            assert torch.equal(got, w)

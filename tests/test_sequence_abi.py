@@ -152,3 +152,17 @@ def test_binding_refuses_host_tensors_and_wrong_shapes():
         fc.decay_attention(t, t, t, torch.zeros(2))
     with pytest.raises(ValueError, match="device"):
         fc.linear_act(torch.zeros(2, 3), torch.zeros(4, 3))
+
+
+def test_refuses_launches_past_the_grid():
+    # a launch holds fewer than 2^32 threads
+    assert _fwd(B=1 << 22, N=1, H=4, Hk=4, Dk=1, Dv=1) == UNSUPPORTED and "too many" in fc.fftconv_last_error()
+    assert _lin(M=1, N=1 << 28, K=1) == UNSUPPORTED and "too large" in fc.fftconv_last_error()
+    assert _lin(M=1 << 30, N=1 << 20, K=8, ws=None) == UNSUPPORTED and "too large" in fc.fftconv_last_error()
+    assert _linb(M=8, N=1 << 28, K=8) == UNSUPPORTED and "too large" in fc.fftconv_last_error()
+
+
+def test_refuses_token_strides_past_a_chunk_offset():
+    wide = 1 << 24      # elements of 2 bytes: 32 MiB
+    st = _ints(0, wide, 64, 12800, 128, 64, 12800, 128, 64, 25600, 256, 64)
+    assert _fwd(st=st) == UNSUPPORTED and "q has a token stride" in fc.fftconv_last_error()
