@@ -143,6 +143,7 @@ DecayCut decay_cut(const DecayShape &s, int64_t walks_per_token, int64_t sums_pe
         len = std::max(std::min(kMinSegment, std::max<int64_t>(s.N, 1)), ceil_div(s.N, most));
     }
     len = round_up(len, kSegStep);
+    if (!s.packed && ceil_div(s.N, len) < 3) len = round_up(std::max<int64_t>(s.N, 1), kSegStep);
     c.cut = (s.packed ? T : s.N) > len;
     // parts: two sums a CU, of at least four chunks
     const int64_t segs = std::max<int64_t>(1, s.packed ? T / len : s.B * (ceil_div(s.N, len) - 1));
