@@ -329,8 +329,11 @@ fftconv_status_t fftconv_eqlinear_fwd(const void *x, const void *W_f, void *y, i
  * type where they meet v and q, and the state itself is kept and returned to
  * fp32 precision.  fp32 storage uses fp32 matrix instructions throughout.
  * Range: nothing is clamped.  In fp16, scale * (q.k) and the state's elements
- * must stay below 65504; a NaN or infinity in a token reaches every output of its
- * sequence and head from its 64-token block on, never another sequence. */
+ * must stay below 65504; a NaN or infinity in a token may reach every output of its
+ * sequence and head from its block of 32 tokens on (blocks are counted from the
+ * sequence's start, in dk and dv from its end), never another sequence.
+ * Refused with FFTCONV_ERR_UNSUPPORTED: token strides of 32 MiB or more, and
+ * calls whose (sequence or segment, head) pairs pass 2^24. */
 
 /* Device scratch bytes of fftconv_decay_fwd for T tokens in all (B * N, or N
  * when packed); 0 where none is needed or an argument is unsupported. */
@@ -362,6 +365,7 @@ fftconv_status_t fftconv_decay_step(const void *q, const void *k, const void *v,
                                     int64_t B, int64_t H, int64_t Hk, int64_t Dk, int64_t Dv, float scale,
                                     fftconv_dtype_t dtype, hipStream_t stream);
 
+/* As above, for fftconv_decay_bwd. */
 size_t fftconv_decay_bwd_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t Hk, int64_t Dk, int64_t Dv,
                                          fftconv_dtype_t dtype);
 
@@ -385,7 +389,8 @@ fftconv_status_t fftconv_decay_bwd(const void *dout, const void *q, const void *
  * fp32 accumulation, everything after the product in fp32, one rounding.  Rows
  * are contiguous; `strides` gives the row strides in elements (NULL = dense).
  * Any sizes and element-aligned pointers; 16-byte aligned rows of whole 16-byte pieces are
- * the fast case. */
+ * the fast case.  Results repeat bit by bit.  Sizes are below 2^31, N below 2^28; products of
+ * more than 2^23 tiles (64 to 256 wide) are refused with FFTCONV_ERR_UNSUPPORTED. */
 typedef enum {
     FFTCONV_ACT_NONE = 0,
     FFTCONV_ACT_RELU = 1,
@@ -394,6 +399,7 @@ typedef enum {
     FFTCONV_ACT_SILU = 4       /* z / (1 + exp(-z))                                          */
 } fftconv_activation_t;
 
+/* Device scratch bytes of fftconv_linear_fwd; 0 where none is needed or an argument is unsupported. */
 size_t fftconv_linear_fwd_workspace_bytes(int64_t M, int64_t N, int64_t K, fftconv_dtype_t dtype);
 
 /* bias, residual and pre may be NULL; pre receives x W^T + bias for the
@@ -404,6 +410,7 @@ fftconv_status_t fftconv_linear_fwd(const void *x, const void *W, const void *bi
                                     fftconv_activation_t activation, fftconv_dtype_t dtype, void *workspace,
                                     size_t workspace_bytes, hipStream_t stream);
 
+/* As above, for fftconv_linear_bwd. */
 size_t fftconv_linear_bwd_workspace_bytes(int64_t M, int64_t N, int64_t K, fftconv_dtype_t dtype);
 
 /* Gradients of sum(dout * out), with dz = dout * act'(pre):

@@ -303,10 +303,17 @@ __device__ __forceinline__ void work_of(const DecaySet &set, uint32_t id, int &k
 // them fit a CU's 160 KB, else two; without LDS-destination loads one.
 constexpr int walk_stages(int bytes, bool vec) { return !vec ? 1 : (3 * bytes <= 78 * 1024 ? 3 : (2 * bytes <= 150 * 1024 ? 2 : 1)); }
 
-// MODE kSums: the part's own sum only (y, z read), for every part
-// that another segment follows; kOut: outputs in the storage type; kOutAny: in it or fp32, by the walk.  DXP: DX padded; NT: 16-column tiles of E per wave.
+// The walk.  MODE kSums: the part's own sum only (y, z read), for every part that another segment
+// follows; kOut: outputs in the storage type; kOutAny: in it or fp32, by the walk (the choice costs
+// registers, so the plain prompt has a kernel without it).  DXP: DX padded; NT: 16-column tiles of E per
+// wave.  grid: work items (see work_of).
+//
+// What bounds it: 20 heads of 128 x 128 in bf16, 131072 tokens: 625 us for 2.69 GB read and written, 4.3 TB/s, so
+// near the memory; the sums before it 340 us for 1.34 GB.  With few tokens a walk the serial chunk does:
+// about 1.0 us a chunk at 128 x 128, two thirds of it matrix products and the conversions that feed them (P
+// is computed by each of the four waves; sharing it through LDS would put a barrier and a round trip between
+// a chunk's products).  Two workgroups a CU overlap one's barriers and LDS reads with the other's products.
 enum WalkMode : int { kSums = 0, kOut = 1, kOutAny = 2 };
-// grid: work items (see work_of)
 template <typename T, int DXP, int NT, int MODE, bool VEC>
 __global__ __launch_bounds__(256, DXP <= 128 ? 2 : 1) void decay_walk_kernel(const DecaySet set) {
 #ifdef __HIP_DEVICE_COMPILE__   // the host pass, which cannot take the scalar operands, needs the stub alone
@@ -637,7 +644,9 @@ __global__ __launch_bounds__(256, DXP <= 128 ? 2 : 1) void decay_walk_kernel(con
 
 // The single-token form: E <- d E + k v^T, out = scale E^T q, one workgroup per (sequence,
 // head, tile of LANES * VEC value columns); LANES lanes along a row of the state, the other
-// 256 / LANES row groups share its rows, joined through LDS.
+// 256 / LANES row groups share its rows, joined through LDS.  Bound by the state, which is read and
+// written once: U rows of it are on their way in each lane.  256 sequences x 20 heads of 128 x 128 (676 MB):
+// 137 us, 4.9 TB/s, what a copy of 2 GiB reaches; 12 heads of one sequence: 3.3 us, a launch.
 template <typename T, int VEC, int LANES>
 __global__ __launch_bounds__(256) void decay_step_kernel(const DecayStep a) {
     constexpr int RG = 256 / LANES, U = 8;
@@ -698,7 +707,9 @@ __global__ __launch_bounds__(256) void decay_step_kernel(const DecayStep a) {
     }
 }
 
-// grid (blocks, tensors): a thread sums the group's values of V neighbouring columns.
+// grid (blocks, tensors): a thread sums the group's values of V neighbouring columns, in the heads' order (no
+// atomics).  Bound by the fp32 parts it reads: 8 x 1000 tokens, 12 heads of 64 in groups of 3, both tensors (57 MB
+// in and out): 10 us.
 template <typename T, int V> __global__ __launch_bounds__(256) void decay_group_sum_kernel(const DecayGroupSum a) {
     const int k = blockIdx.y;
     if (!a.dst[k] || (V == 4) != (a.vec[k] != 0)) return;
@@ -720,7 +731,9 @@ template <typename T, int V> __global__ __launch_bounds__(256) void decay_group_
 }
 
 // State before each segment from the parts' own sums, in place:
-// grid (B, H, kinds x pieces of 256 V values).  V = 4: Dx * Dz a multiple of 4.
+// grid (B, H, kinds x pieces of 256 V values).  V = 4: Dx * Dz a multiple of 4.  A thread follows its values
+// through all parts of a sequence, eight parts' loads ahead.  Latency bound: 15 us at 131072 tokens x 20
+// heads of 128 x 128.
 template <int V> static __global__ __launch_bounds__(256) void decay_chain_kernel(const DecaySet set) {
     const DecayWalk &a = set.w[blockIdx.z % set.kinds];
     typedef float vec __attribute__((ext_vector_type(V)));
@@ -815,7 +828,10 @@ template <typename T> static hipError_t step_typed(const DecayStep &a, bool vec,
     const unsigned bh = (unsigned)(a.B * a.H);
     if (!vec) {
         decay_step_kernel<T, 1, 32><<<dim3(bh, (a.Dv + 31) / 32), 256, 0, stream>>>(a);
-    } else if (bh < 512) {   // few rows: narrow tiles spread the state over more compute units
+    } else if (bh * ((a.Dv + 127) / 128) < 352) {
+        // few states: tiles of 32 columns spread them over more compute units.  128 x 128 states, back to
+        // back, narrow against wide: 3.3 against 4.1 us for 12, 6.3 / 6.9 for 256, 7.1 / 7.7 for 320, 10.8 / 10.2
+        // for 384, 11.1 / 10.0 for 512; 256 x 256: 15.0 / 15.6 for 160, 17.8 / 17.5 for 192.
         decay_step_kernel<T, 4, 8><<<dim3(bh, (a.Dv + 31) / 32), 256, 0, stream>>>(a);
     } else {
         decay_step_kernel<T, 4, 32><<<dim3(bh, (a.Dv + 127) / 128), 256, 0, stream>>>(a);

@@ -124,9 +124,18 @@ struct DecayShape {
 };
 
 // How sequences are cut.  A walk is serial, so the chip fills only when the walks (kinds of walk x
-// sequences x heads x z tiles) number about two or three a CU; fewer are cut into segments, at the price
-// of reading y and z twice (a pass of its own sums each segment first).  That pass reads half as much
-// per token and is cut finer where segments are few: a segment is `seglen / sublen` parts.
+// sequences x heads x z tiles) number two (rows wider than 64) or three a CU; fewer are cut into segments, at
+// the price of reading y and z twice (a pass of its own sums each segment first).  That pass reads half as
+// much per token and is cut finer where segments are few: a segment is `seglen / sublen` parts.
+// Measured in bf16, B x N tokens x heads of D x D:
+//     walks a CU 1, 2, 4:        4 x 4096 x 20 of 128: 136, 126, 151 us; 1 x 32768 x 12 of 64 at 1, 3, 4: 90, 73, 79 us
+//     shortest segment 128, 256, 512:  1 x 2048 x 20 of 128: 48, 47, 56 us; 1 x 8192: 80, 81, 93 us
+//     two segments against none:  12 x 4096 x 20 of 128: 332 against 245 us; its gradients at 4 x 4096: 259 against
+//         234 us; three or more against none: gradients of 5 x 2048 x 12 of 64: 58 against 72 us
+//     parts against whole segments in the sums:  1 x 512 x 20 of 128: 38 against 42 us; gradients of
+//         4 x 4096 cut in two: 259 against 287 us
+// Packed sequences have lengths that only the device knows: they are cut by the mean load (two walks a CU
+// against one: 148 against 168 us for 12 sequences of 0 to 6001 tokens, 136 against 107 for 12 of 1386).
 struct DecayCut {
     int64_t seglen, sublen, segments, parts;   // tokens; how many there are at most
     bool cut;                                  // more than one segment a sequence
@@ -143,6 +152,7 @@ DecayCut decay_cut(const DecayShape &s, int64_t walks_per_token, int64_t sums_pe
         len = std::max(std::min(kMinSegment, std::max<int64_t>(s.N, 1)), ceil_div(s.N, most));
     }
     len = round_up(len, kSegStep);
+    // two segments: the sums cost more than they spread
     if (!s.packed && ceil_div(s.N, len) < 3) len = round_up(std::max<int64_t>(s.N, 1), kSegStep);
     c.cut = (s.packed ? T : s.N) > len;
     // parts: two sums a CU, of at least four chunks
@@ -558,7 +568,10 @@ fftconv_status_t fftconv_decay_bwd(const void *dout, const void *q, const void *
 // ---- linear product -----------------------------------------------------------
 namespace {
 
-constexpr int64_t kVectorRows = 4;   // rows that the kernel for single tokens takes
+// Rows that the kernel for single tokens takes.  It against the tile kernel, bf16, 2560 -> 10240: 11.0 against
+// 14.8 us for one row, 11.5 / 14.8 for two, 13.4 / 15.0 for four, where its sums and rows of x fill the registers;
+// 768 -> 768: 8.8 / 12 us.
+constexpr int64_t kVectorRows = 4;
 
 struct GemmPlan {
     int tile, splits;
@@ -569,7 +582,10 @@ struct GemmPlan {
 // of one tile takes a CU `alone` microseconds, and `each` where several tiles share the CU (measured
 // with bf16 and fp32 at M = 300 .. 8192, N = 768 .. 10240, K = 768 .. 10240; the 256 tile fills a CU).
 // The fullest of 256 CUs decides.  Tiles beyond a multiple of 256 may be split along K: their parts
-// then pass through memory and a second kernel.
+// then pass through memory and a second kernel.  Measured, us by tile (bf16; M x N x K), the plan's choice
+// first: 16384 x 10240 x 2560: 256 692, 128 837, 64 1242; 512 x 10240 x 2560: 128 37, 64 44, 256 46;
+// 1000 x 2304 x 768 fp32: 64 37, 128 50; without splits the first three take 708, 40 and 42, and 300 x 768 x 10240
+// 46 where the split takes 18.
 GemmPlan plan_gemm(int64_t M, int64_t N, int64_t K, int dt, bool vec) {
     struct Kind {
         int tile;
