@@ -308,11 +308,12 @@ constexpr int walk_stages(int bytes, bool vec) { return !vec ? 1 : (3 * bytes <=
 // registers, so the plain prompt has a kernel without it).  DXP: DX padded; NT: 16-column tiles of E per
 // wave.  grid: work items (see work_of).
 //
-// What bounds it: 20 heads of 128 x 128 in bf16, 131072 tokens: 625 us for 2.69 GB read and written, 4.3 TB/s, so
-// near the memory; the sums before it 340 us for 1.34 GB.  With few tokens a walk the serial chunk does:
-// about 1.0 us a chunk at 128 x 128, two thirds of it matrix products and the conversions that feed them (P
-// is computed by each of the four waves; sharing it through LDS would put a barrier and a round trip between
-// a chunk's products).  Two workgroups a CU overlap one's barriers and LDS reads with the other's products.
+// What bounds it: 20 heads of 128 x 128 in bf16, 131072 tokens: 622 us for 2.69 GB read and written, 4.3 TB/s, so
+// near the memory; the sums before it 335 us for 1.34 GB.  With few tokens a walk the serial chunk does: 1.8 us
+// at 128 x 128 with one walk a CU (the gradients of 4 x 4096 tokens: 230 us for 128 chunks, the matrix units a
+// quarter of the time busy).  P is computed by each of the four waves: sharing it through LDS would put a
+// barrier and a round trip between a chunk's products.  Two workgroups a CU overlap one's barriers and
+// LDS reads with the other's products.
 enum WalkMode : int { kSums = 0, kOut = 1, kOutAny = 2 };
 template <typename T, int DXP, int NT, int MODE, bool VEC>
 __global__ __launch_bounds__(256, DXP <= 128 ? 2 : 1) void decay_walk_kernel(const DecaySet set) {
