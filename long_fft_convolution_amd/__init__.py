@@ -539,26 +539,32 @@ def _scratch(nbytes, device):
 
 def decay_attention(q, k, v, log_decay, scale=None, state_in=None, cu_seqlens=None, stream=None):
     """Decay attention of whole sequences (allocations by torch); returns (out, final states).  scale: Dk^-0.5."""
+    if stream is not None:
+        with torch.cuda.stream(stream):      # the scratch memory and the results are that stream's, too
+            return decay_attention(q, k, v, log_decay, scale, state_in, cu_seqlens)
     B, N, H, Hk, Dk, Dv = _decay_shapes(q, k, v, log_decay, cu_seqlens)
     T = N if cu_seqlens is not None else B * N
     out = torch.empty((*q.shape[:-1], Dv), dtype=q.dtype, device=q.device)
     state_out = torch.empty((B, H, Dk, Dv), dtype=torch.float32, device=q.device)
     ws = _scratch(fftconv_decay_fwd_workspace_bytes(B, T, H, Dk, Dv, q.dtype), q.device)
     fftconv_decay_fwd(q, k, v, log_decay, out, Dk ** -0.5 if scale is None else scale, state_in, state_out,
-                      cu_seqlens=cu_seqlens, workspace=ws, stream=stream)
+                      cu_seqlens=cu_seqlens, workspace=ws)
     return out, state_out
 
 
 def decay_attention_bwd(q, k, v, log_decay, dout, scale=None, state_in=None, dstate_out=None, cu_seqlens=None,
                         stream=None):
     """Gradients of decay_attention; returns (dq, dk, dv, dstate_in), the last None without state_in."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return decay_attention_bwd(q, k, v, log_decay, dout, scale, state_in, dstate_out, cu_seqlens)
     B, N, H, Hk, Dk, Dv = _decay_shapes(q, k, v, log_decay, cu_seqlens)
     T = N if cu_seqlens is not None else B * N
     dq, dk, dv = (torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k, v))
     dstate_in = None if state_in is None else torch.empty_like(state_in)
     ws = _scratch(fftconv_decay_bwd_workspace_bytes(B, T, H, Hk, Dk, Dv, q.dtype), q.device)
     fftconv_decay_bwd(dout, q, k, v, log_decay, dq, dk, dv, Dk ** -0.5 if scale is None else scale, state_in,
-                      dstate_out, dstate_in, cu_seqlens, ws, stream)
+                      dstate_out, dstate_in, cu_seqlens, ws)
     return dq, dk, dv, dstate_in
 
 
@@ -633,20 +639,26 @@ def fftconv_linear_bwd(dout: torch.Tensor, x: torch.Tensor, W: torch.Tensor, pre
 
 def linear_act(x, W, bias=None, residual=None, activation="none", keep_pre=False, stream=None):
     """act(x W^T + bias) + residual (allocations by torch); with keep_pre also x W^T + bias for linear_act_bwd."""
+    if stream is not None:
+        with torch.cuda.stream(stream):      # the scratch memory and the results are that stream's, too
+            return linear_act(x, W, bias, residual, activation, keep_pre)
     M, N = x.shape[0], W.shape[0]
     out = torch.empty((M, N), dtype=x.dtype, device=x.device)
     pre = torch.empty_like(out) if keep_pre else None
     ws = _scratch(fftconv_linear_fwd_workspace_bytes(M, N, x.shape[1], x.dtype), x.device)
-    fftconv_linear_fwd(x, W, bias, residual, out, pre, activation, ws, stream)
+    fftconv_linear_fwd(x, W, bias, residual, out, pre, activation, ws)
     return (out, pre) if keep_pre else out
 
 
 def linear_act_bwd(dout, x, W, pre=None, activation="none", bias=True, stream=None):
     """Gradients of linear_act; returns (dx, dW, dbias), dbias None without a bias."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return linear_act_bwd(dout, x, W, pre, activation, bias)
     dx, dW = (torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (x, W))
     dbias = torch.empty(W.shape[0], dtype=x.dtype, device=x.device) if bias else None
     ws = _scratch(fftconv_linear_bwd_workspace_bytes(x.shape[0], W.shape[0], x.shape[1], x.dtype), x.device)
-    fftconv_linear_bwd(dout, x, W, pre, dx, dW, dbias, activation, ws, stream)
+    fftconv_linear_bwd(dout, x, W, pre, dx, dW, dbias, activation, ws)
     return dx, dW, dbias
 
 

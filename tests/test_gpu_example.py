@@ -7,6 +7,7 @@ import numpy as np
 import pytest
 import torch
 
+import long_fft_convolution_amd as fc
 from oracle import sequence as seq
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
@@ -59,3 +60,31 @@ def test_block_against_the_oracle():
         size = np.linalg.norm(grads[name].double().cpu().numpy()) * np.linalg.norm(step)
         # fp32 gradients against a central difference: 1e-5 of the two vectors' sizes
         assert abs(got - want) < 1e-5 * size, (name, got, want)
+
+
+def test_scratch_memory_belongs_to_the_stream_given():
+    # behind work on that stream the calls run late; the current stream meanwhile takes and fills memory of its own
+    dev = "cuda"
+    g = torch.Generator(device=dev).manual_seed(3)
+    q, k, v, d = (torch.randn((1, 3000, 2, 64), generator=g, device=dev).to(torch.bfloat16) for _ in range(4))
+    a = -torch.rand(2, generator=g, device=dev) * 0.01
+    x, W = (torch.randn((n, 4096), generator=g, device=dev).to(torch.bfloat16) for n in (200, 100))
+    y = torch.randn((200, 100), generator=g, device=dev).to(torch.bfloat16)
+    work = torch.randn((4096, 4096), generator=g, device=dev)
+
+    def calls(stream):
+        return (*fc.decay_attention(q, k, v, a, stream=stream), *fc.decay_attention_bwd(q, k, v, a, d, stream=stream)[:3],
+                fc.linear_act(x, W, stream=stream), *fc.linear_act_bwd(y, x, W, stream=stream))
+
+    want = calls(None)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        for _ in range(4):
+            work = torch.nn.functional.normalize(work @ work)
+    got = calls(s)
+    taken = [torch.full((n,), 255, dtype=torch.uint8, device=dev) for n in (1 << 18, 1 << 20, 1 << 22, 1 << 24) for _ in range(4)]
+    torch.cuda.synchronize()
+    assert len(taken) == 16
+    for i, (w, t) in enumerate(zip(want, got)):
+        assert torch.equal(w, t), i
