@@ -538,7 +538,10 @@ def _scratch(nbytes, device):
 
 
 def decay_attention(q, k, v, log_decay, scale=None, state_in=None, cu_seqlens=None, stream=None):
-    """Decay attention of whole sequences (allocations by torch); returns (out, final states).  scale: Dk^-0.5."""
+    """Decay attention of whole sequences (allocations by torch); returns (out, final states).  scale: Dk^-0.5.
+
+    Packed tokens of no sequence (before cu_seqlens[0], from its last value on) have no result: their rows are not set.
+    """
     if stream is not None:
         with torch.cuda.stream(stream):      # the scratch memory and the results are that stream's, too
             return decay_attention(q, k, v, log_decay, scale, state_in, cu_seqlens)
@@ -554,7 +557,10 @@ def decay_attention(q, k, v, log_decay, scale=None, state_in=None, cu_seqlens=No
 
 def decay_attention_bwd(q, k, v, log_decay, dout, scale=None, state_in=None, dstate_out=None, cu_seqlens=None,
                         stream=None):
-    """Gradients of decay_attention; returns (dq, dk, dv, dstate_in), the last None without state_in."""
+    """Gradients of decay_attention; returns (dq, dk, dv, dstate_in), the last None without state_in.
+
+    Rows of packed tokens that belong to no sequence are not set.
+    """
     if stream is not None:
         with torch.cuda.stream(stream):
             return decay_attention_bwd(q, k, v, log_decay, dout, scale, state_in, dstate_out, cu_seqlens)

@@ -716,10 +716,17 @@ template <typename T, int V> __global__ __launch_bounds__(256) void decay_group_
     if (!a.dst[k] || (V == 4) != (a.vec[k] != 0)) return;
     typedef float vec __attribute__((ext_vector_type(V)));
     const int D = a.D[k], Q = D / V;
-    const int64_t n = a.B * a.N * a.Hk * Q;
+    // sequences lie one behind another: the tokens between the first bound and the last, clamped like the walks'
+    int64_t first = 0, end = a.B * a.N;
+    if (a.cu) {
+        const int64_t s = a.cu[0], e = a.cu[a.seqs];
+        first = s < 0 ? 0 : (s > a.N ? a.N : s);
+        end = e < first ? first : (e > a.N ? a.N : e);
+    }
+    const int64_t n = (end - first) * a.Hk * Q;
     for (int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
         const int d = (int)(i % Q) * V;
-        const int64_t head = i / Q, hk = head % a.Hk, t = head / a.Hk;
+        const int64_t head = i / Q + first * a.Hk, hk = head % a.Hk, t = head / a.Hk;
         const float *p = a.src[k] + head * a.group * D + d;
         vec s = 0.0f;
         for (int j = 0; j < a.group; ++j) s += *reinterpret_cast<const vec *>(p + (int64_t)j * D);

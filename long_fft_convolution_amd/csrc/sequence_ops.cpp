@@ -557,7 +557,7 @@ fftconv_status_t fftconv_decay_bwd(const void *dout, const void *q, const void *
             g.vec[i] = o.row % 4 == 0 && aligned(o.p, 4 * o.bytes_per) && o.stride[0] % 4 == 0 && o.stride[1] % 4 == 0 &&
                        o.stride[2] % 4 == 0;
         }
-        g.B = s.packed ? 1 : B, g.N = N, g.Hk = (int)Hk, g.group = (int)(H / Hk);
+        g.B = s.packed ? 1 : B, g.N = N, g.cu = cu_seqlens, g.seqs = B, g.Hk = (int)Hk, g.group = (int)(H / Hk);
         e = dtype == FFTCONV_F32   ? launch_decay_group_sum_f32(g, stream)
             : dtype == FFTCONV_F16 ? launch_decay_group_sum_f16(g, stream)
                                    : launch_decay_group_sum_bf16(g, stream);

@@ -64,13 +64,16 @@ struct DecayStep {
     float scale;
 };
 
-// Gradients of shared heads: dst (tokens, Hk, D) <- sum over each group of src (tokens, H, D), fp32.
+// Gradients of shared heads: dst (tokens, Hk, D) <- sum over each group of src (tokens, H, D), fp32.  When packed,
+// of the tokens that belong to a sequence: src holds nothing for the others, and dst keeps what it has there.
 struct DecayGroupSum {
     const float *src[2];
     void *dst[2];                    // up to two tensors; null: none
     int D[2], vec[2];                // vec: four values at a time
     int64_t db[2], dt[2], dh[2];     // strides of dst
     int64_t B, N;
+    const int32_t *cu;               // packed sequences' bounds (seqs + 1) or null
+    int64_t seqs;
     int Hk, group;
 };
 
