@@ -48,6 +48,13 @@ struct View {
     int64_t size[3], stride[3], row;
     int64_t bytes_per;
 
+    // A dimension of one element has no use for its stride, whatever the caller's view carries there: kernels and
+    // checks see 0 (the walks from a sequence's end start at a row some strides before its first).
+    View &settle() {
+        for (int i = 0; i < dims; ++i)
+            if (size[i] <= 1) stride[i] = 0;
+        return *this;
+    }
     bool empty() const {
         for (int i = 0; i < dims; ++i)
             if (size[i] == 0) return true;
@@ -208,7 +215,7 @@ View heads_view(const char *name, const void *p, const DecayShape &s, int64_t he
         v.stride[1] = heads * row;
         v.stride[2] = row;
     }
-    return v;
+    return v.settle();
 }
 
 fftconv_status_t check_shape(const DecayShape &s, float scale) {
@@ -659,7 +666,7 @@ fftconv_status_t check_linear(int64_t M, int64_t N, int64_t K, int act, int dt) 
     return FFTCONV_OK;
 }
 View matrix(const char *name, const void *p, int64_t rows, int64_t cols, int64_t ld, int dt) {
-    return View{name, p, 1, {rows, 1, 1}, {ld, 0, 0}, cols, elem_bytes(dt)};
+    return View{name, p, 1, {rows, 1, 1}, {ld, 0, 0}, cols, elem_bytes(dt)}.settle();
 }
 // four neighbouring values at a time
 bool quad(const View &v) {
