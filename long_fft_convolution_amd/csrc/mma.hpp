@@ -176,10 +176,13 @@ __device__ __forceinline__ float wave_max(float x) {
     FFTCONV_DPP(0x141);     // halves of a row mirrored
     FFTCONV_DPP(0x140);     // rows mirrored
 #undef FFTCONV_DPP
+    // (the halves of a result as values first: a bit cast of a vector's element reads the vector's first)
     const auto a = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(uint32_t, x), __builtin_bit_cast(uint32_t, x), false, false);
-    x = fmaxf(__builtin_bit_cast(float, a[0]), __builtin_bit_cast(float, a[1]));
+    const uint32_t a0 = a[0], a1 = a[1];
+    x = fmaxf(__builtin_bit_cast(float, a0), __builtin_bit_cast(float, a1));
     const auto b = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, x), __builtin_bit_cast(uint32_t, x), false, false);
-    return fmaxf(__builtin_bit_cast(float, b[0]), __builtin_bit_cast(float, b[1]));
+    const uint32_t b0 = b[0], b1 = b[1];
+    return fmaxf(__builtin_bit_cast(float, b0), __builtin_bit_cast(float, b1));
 }
 
 }  // namespace fftconv
