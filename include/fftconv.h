@@ -328,10 +328,12 @@ fftconv_status_t fftconv_eqlinear_fwd(const void *x, const void *W_f, void *y, i
  * accumulation; the products q k^T and the state are rounded to the storage
  * type where they meet v and q, and the state itself is kept and returned to
  * fp32 precision.  fp32 storage uses fp32 matrix instructions throughout.
- * Range: nothing is clamped.  In fp16, scale * (q.k) and the state's elements
- * must stay below 65504; a NaN or infinity in a token may reach every output of its
- * sequence and head from its block of 32 tokens on (blocks are counted from the
- * sequence's start, in dk and dv from its end), never another sequence.
+ * Range: nothing is clamped; results beyond the storage type become infinite.  q k^T and the
+ * states may be of any size that fp32 holds, in fp16 too: they are scaled by powers of two
+ * where they are rounded (elements below 2^-12 of a state's largest may keep fewer bits there).
+ * A NaN or infinity in a token may reach every output of its sequence and head from its
+ * block of 32 tokens on (blocks are counted from the sequence's start, in dk and dv from
+ * its end), never another sequence.
  * Refused with FFTCONV_ERR_UNSUPPORTED: token strides of 32 MiB or more, and
  * calls whose (sequence or segment, head) pairs pass 2^24. */
 

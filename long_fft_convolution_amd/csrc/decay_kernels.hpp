@@ -29,7 +29,9 @@
 // LDS round trip and a barrier.
 //
 // Rounding (16-bit types): P and the state are rounded to the storage type
-// as operands of O (an error like the output's own rounding).  The state is
+// as operands of O (an error like the output's own rounding), in fp16 after a
+// power of two where they are small or large for its range: the state by its
+// largest element in a wave's columns, P row by row.  The state is
 // an fp32 result, so its update must not lose: d^(C-1-s) Z is split into
 // 2 (fp16) or 3 (bf16) storage-type terms that hold it to fp32 precision (2 in
 // bf16 in segments that another follows, whose state only outputs see).
@@ -464,41 +466,28 @@ __global__ __launch_bounds__(256, DXP <= 128 ? 2 : 1) void decay_walk_kernel(con
 #pragma unroll
         for (int q = 0; q < NT; ++q)
             zf[q] = TZ::col8(z, zw + (NT == 2 ? (lane & 3) * 8 + q * 4 : (lane & 3) * 4), zcol(c, q));
-        // the gain after this chunk; brought back first where that leaves its range
-        const float growth = slow ? (float)n * -log2d : 0.0f;
-        held = slow ? held + n : 0;
-        float next = slow ? (float)held * -log2d : 0.0f, most = 0.0f;
-        bool back = fabsf(next) > 16.0f;
-        if (Mma<T>::kNarrow) {
-#pragma unroll
-            for (int q = 0; q < NT; ++q)
-#pragma unroll
-                for (int j = 0; j < 8; ++j) most = fmaxf(most, fabsf((float)zf[q][j]));
-            most = wave_max(most) * fabsf(a.u_scale);      // the weights are at most u_scale
-            const float top = ldexpf(most * exp2f(next), ex);
-            back = back || top > 32768.0f || (top < 16.0f && most > 0.0f);
-        }
-        if (__builtin_amdgcn_readfirstlane(back)) {
-            int e1 = 0;
-            if (Mma<T>::kNarrow) {
-                e1 = most > 0.0f ? 13 - ilogbf(most) - (int)ceilf(growth) : ex;     // the largest term near 2^14
-                e1 = e1 < -60 ? -60 : (e1 > 60 ? 60 : e1);
-            }
-            const float r = ldexpf(exp2f(-grown), e1 - ex);
-#pragma unroll
-            for (int kk = 0; kk < KX; ++kk)
-#pragma unroll
-                for (int r2 = 0; r2 < 2; ++r2)
-#pragma unroll
-                    for (int q = 0; q < NT; ++q) E[kk][r2][q] *= r;
-            ex = e1;
-            grown = 0.0f;
-            held = slow ? n : 0;
-            next = growth;
-        }
-        const float gain = Mma<T>::kNarrow ? ldexpf(exp2f(next), ex) : exp2f(next);
         if (OUT) {
-            const float unscale = Mma<T>::kNarrow ? ldexpf(exp2f(-grown), -ex) : exp2f(-grown);
+            // fp16: the state is an operand as it is where the largest element in this wave's columns has room in the
+            // type's range, else with that element at its upper end; outputs are brought back in fp32
+            float unscale = Mma<T>::kNarrow ? ldexpf(__builtin_amdgcn_exp2f(-grown), -ex) : __builtin_amdgcn_exp2f(-grown), to = 1.0f;
+            if (Mma<T>::kNarrow) {
+                float top = 0.0f;
+#pragma unroll
+                for (int kk = 0; kk < KX; ++kk)
+#pragma unroll
+                    for (int q = 0; q < NT; ++q)
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(E[kk][j >> 2][q][j & 3]));
+                const float size = top * unscale;
+                const bool low = __ballot(size >= kFp16LowAll) == 0, high = __ballot(!(size <= kFp16High)) != 0;
+                to = unscale;
+                unscale = 1.0f;
+                if (__builtin_expect(low | high, 0)) {
+                    const int shift = fp16_shift(wave_max(size));
+                    to = ldexpf(to, shift);
+                    unscale = ldexpf(1.0f, -shift);
+                }
+            }
             v8 ef[KX][NT];     // the state as an operand: row zcol(c, q), slots 8 g + j
 #pragma unroll
             for (int kk = 0; kk < KX; ++kk)
@@ -507,7 +496,7 @@ __global__ __launch_bounds__(256, DXP <= 128 ? 2 : 1) void decay_walk_kernel(con
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
                         const float e = E[kk][j >> 2][q][j & 3];
-                        ef[kk][q][j] = (T)(Mma<T>::kNarrow ? e * unscale : e);
+                        ef[kk][q][j] = (T)(Mma<T>::kNarrow ? e * to : e);
                     }
 #pragma unroll
             for (int rt = 0; rt < 2; ++rt) {
@@ -525,14 +514,38 @@ __global__ __launch_bounds__(256, DXP <= 128 ? 2 : 1) void decay_walk_kernel(con
                     for (int r = 0; r < 2; ++r)
                         p[r] = Mma<T>::mma(TY::row8(y, (c >> 2) * 8 + r * 4 + (c & 3), kk * 32 + g * 8), xf, p[r]);
                 }
-                const float rw = Mma<T>::kNarrow ? row_w[rt * 16 + c] : row_w[rt * 16 + c] * unscale;
+                const float rw = row_w[rt * 16 + c] * unscale;
+                float pw[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) pw[j] = p[j >> 2][j & 3] * fac[rt][j >> 2][j & 3];
                 v8 pf;
+                bool room = true;
+                float top = 0.0f;
+                if (Mma<T>::kNarrow) {      // P likewise, each row (one of the output's, the lanes of one c) by itself
 #pragma unroll
-                for (int j = 0; j < 8; ++j) pf[j] = (T)(p[j >> 2][j & 3] * fac[rt][j >> 2][j & 3]);
+                    for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(pw[j]));
+                    // (no short-circuit: one branch)
+                    room = ((~rows_vote(top >= kFp16Low) & 0xffff) | (__ballot(!(top <= kFp16High)) != 0)) == 0;
+                }
+                if (__builtin_expect(room, 1)) {
 #pragma unroll
-                for (int q = 0; q < NT; ++q) {
-                    o[q] *= rw;
-                    o[q] = Mma<T>::mma(zf[q], pf, o[q]);
+                    for (int j = 0; j < 8; ++j) pf[j] = (T)pw[j];
+#pragma unroll
+                    for (int q = 0; q < NT; ++q) {
+                        o[q] *= rw;
+                        o[q] = Mma<T>::mma(zf[q], pf, o[q]);
+                    }
+                } else {
+                    const int shift = fp16_shift(rows_max(top));
+                    const float rw_p = ldexpf(rw, shift), from = ldexpf(1.0f, -shift);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) pf[j] = (T)ldexpf(pw[j], shift);
+#pragma unroll
+                    for (int q = 0; q < NT; ++q) {
+                        o[q] *= rw_p;
+                        o[q] = Mma<T>::mma(zf[q], pf, o[q]);
+                        o[q] *= from;
+                    }
                 }
                 {
                     const auto view = wide_view(out0 + (a.reverse ? si.len - t - kChunk : t) * a.ot * out_e);
@@ -542,6 +555,40 @@ __global__ __launch_bounds__(256, DXP <= 128 ? 2 : 1) void decay_walk_kernel(con
                 }
             }
         }
+        // The gain after this chunk; brought back first where that leaves its range.  (Behind the outputs, which do not
+        // wait for Z's largest value then: fp16, 4 x 4096 tokens of 20 x 128: gradients 285 against 294 us.)
+        const float growth = slow ? (float)n * -log2d : 0.0f;
+        held = slow ? held + n : 0;
+        float next = slow ? (float)held * -log2d : 0.0f, most = 0.0f;
+        bool back = fabsf(next) > 16.0f;
+        if (Mma<T>::kNarrow) {
+#pragma unroll
+            for (int q = 0; q < NT; ++q)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) most = fmaxf(most, fabsf((float)zf[q][j]));
+            most = wave_max(most) * fabsf(a.u_scale);      // the weights are at most u_scale
+            const float top = ldexpf(most * __builtin_amdgcn_exp2f(next), ex);
+            back = back || top > 32768.0f || (top < 16.0f && most > 0.0f);
+        }
+        if (__builtin_amdgcn_readfirstlane(back)) {
+            int e1 = 0;
+            if (Mma<T>::kNarrow) {
+                e1 = most > 0.0f ? 13 - ilogbf(most) - (int)ceilf(growth) : ex;     // the largest term near 2^14
+                e1 = e1 < -60 ? -60 : (e1 > 60 ? 60 : e1);
+            }
+            const float r = ldexpf(__builtin_amdgcn_exp2f(-grown), e1 - ex);
+#pragma unroll
+            for (int kk = 0; kk < KX; ++kk)
+#pragma unroll
+                for (int r2 = 0; r2 < 2; ++r2)
+#pragma unroll
+                    for (int q = 0; q < NT; ++q) E[kk][r2][q] *= r;
+            ex = e1;
+            grown = 0.0f;
+            held = slow ? n : 0;
+            next = growth;
+        }
+        const float gain = Mma<T>::kNarrow ? ldexpf(__builtin_amdgcn_exp2f(next), ex) : __builtin_amdgcn_exp2f(next);
         // E <- d^n E + Y^T (weights Z), in units of the gain
         if (!slow) {
             const float dn = decay_power(log2d, n);

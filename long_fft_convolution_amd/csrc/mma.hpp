@@ -166,23 +166,46 @@ template <int LEFT> __device__ __forceinline__ void wait_loads_and_barrier() {
     __builtin_amdgcn_sched_barrier(0);
 }
 
-// Largest of the wave's 64 values (not negative), in every lane: four steps within rows of 16 lanes, two
-// that exchange rows.
+// Largest of the four lanes 16 g + c of each c, in all of them: two steps that exchange rows of 16.  For values that
+// are not negative, whose bits have their order (a NaN counts as the largest).
+__device__ __forceinline__ uint32_t rows_max_bits(uint32_t x) {
+    const auto a = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+    x = a[0] > a[1] ? a[0] : a[1];
+    const auto b = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+    return b[0] > b[1] ? b[0] : b[1];
+}
+__device__ __forceinline__ float rows_max(float x) {
+    const uint32_t most = rows_max_bits(__builtin_bit_cast(uint32_t, x));
+    return __builtin_bit_cast(float, most);
+}
+// The same of the wave's 64 values: four steps within rows of 16 lanes, then the rows.
 __device__ __forceinline__ float wave_max(float x) {
+    uint32_t u = __builtin_bit_cast(uint32_t, x);
 #define FFTCONV_DPP(CTRL) \
-    x = fmaxf(x, __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, x), CTRL, 0xf, 0xf, true)))
+    { const uint32_t other = (uint32_t)__builtin_amdgcn_mov_dpp((int)u, CTRL, 0xf, 0xf, true); u = u > other ? u : other; }
     FFTCONV_DPP(0xb1);      // lanes 1 0 3 2 of each four
     FFTCONV_DPP(0x4e);      // lanes 2 3 0 1
     FFTCONV_DPP(0x141);     // halves of a row mirrored
     FFTCONV_DPP(0x140);     // rows mirrored
 #undef FFTCONV_DPP
-    // (the halves of a result as values first: a bit cast of a vector's element reads the vector's first)
-    const auto a = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(uint32_t, x), __builtin_bit_cast(uint32_t, x), false, false);
-    const uint32_t a0 = a[0], a1 = a[1];
-    x = fmaxf(__builtin_bit_cast(float, a0), __builtin_bit_cast(float, a1));
-    const auto b = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, x), __builtin_bit_cast(uint32_t, x), false, false);
-    const uint32_t b0 = b[0], b1 = b[1];
-    return fmaxf(__builtin_bit_cast(float, b0), __builtin_bit_cast(float, b1));
+    u = rows_max_bits(u);
+    return __builtin_bit_cast(float, u);
+}
+// 32 bits whose lower half has bit c set where any of the lanes 16 g + c votes
+__device__ __forceinline__ uint32_t rows_vote(bool yes) {
+    const uint64_t lanes = __ballot(yes);
+    const uint32_t two = (uint32_t)lanes | (uint32_t)(lanes >> 32);
+    return two | two >> 16;
+}
+// fp16 operands need no scale while their largest value is below kFp16High and not below kFp16Low (one row) or
+// kFp16LowAll (several columns, some of which may be smaller): values above 2^-14 are normal numbers, smaller ones
+// are off by 2^-25, which is 2^-15 of a largest value of 2^-10.
+constexpr float kFp16Low = 0x1p-10f, kFp16LowAll = 0x1p-2f, kFp16High = 0x1p15f;
+// Power of two that brings a largest value of `top` to 2^14 .. 2^15 (2^100 at most: what is smaller still needs no
+// bits); infinity, NaN and zero as they come.
+__device__ __forceinline__ int fp16_shift(float top) {
+    const int s = 15 - __builtin_amdgcn_frexp_expf(top);
+    return s < 100 ? s : 100;
 }
 
 }  // namespace fftconv
