@@ -561,12 +561,19 @@ __global__ __launch_bounds__(256, DXP <= 128 ? 2 : 1) void decay_walk_kernel(con
         held = slow ? held + n : 0;
         float next = slow ? (float)held * -log2d : 0.0f, most = 0.0f;
         bool back = fabsf(next) > 16.0f;
+        float w[8], terms[NT][8];       // (terms: fp16)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[j] = upd[kChunk - n + g * 8 + j];
         if (Mma<T>::kNarrow) {
+            // the largest of the terms themselves: a head that forgets fast may weigh all that a chunk holds by very little
 #pragma unroll
             for (int q = 0; q < NT; ++q)
 #pragma unroll
-                for (int j = 0; j < 8; ++j) most = fmaxf(most, fabsf((float)zf[q][j]));
-            most = wave_max(most) * fabsf(a.u_scale);      // the weights are at most u_scale
+                for (int j = 0; j < 8; ++j) {
+                    terms[q][j] = (float)zf[q][j] * w[j];
+                    most = fmaxf(most, fabsf(terms[q][j]));
+                }
+            most = wave_max(most);
             const float top = ldexpf(most * __builtin_amdgcn_exp2f(next), ex);
             back = back || top > 32768.0f || (top < 16.0f && most > 0.0f);
         }
@@ -600,17 +607,18 @@ __global__ __launch_bounds__(256, DXP <= 128 ? 2 : 1) void decay_walk_kernel(con
                     for (int q = 0; q < NT; ++q) E[kk][r][q] *= dn;
         }
         grown = next;
-        float w[8];
+        if (!Mma<T>::kNarrow) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) w[j] = upd[kChunk - n + g * 8 + j] * gain;
-        auto update = [&](auto terms) __attribute__((always_inline)) {
-            constexpr int TERMS = decltype(terms)::value;
+            for (int j = 0; j < 8; ++j) w[j] *= gain;
+        }
+        auto update = [&](auto count) __attribute__((always_inline)) {
+            constexpr int TERMS = decltype(count)::value;
             v8 zs[NT][TERMS];
 #pragma unroll
             for (int q = 0; q < NT; ++q) {
                 float weighted[8];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) weighted[j] = (float)zf[q][j] * w[j];
+                for (int j = 0; j < 8; ++j) weighted[j] = Mma<T>::kNarrow ? terms[q][j] * gain : (float)zf[q][j] * w[j];
                 split8<T, TERMS>(weighted, zs[q]);
             }
             // terms outermost: an accumulator's next product comes 2 NT instructions later, past their latency

@@ -96,3 +96,18 @@ def test_columns_of_different_size(size, dtype):
     want, _ = seq.decay_fwd(_f64(q[0]), _f64(k[0]), _f64(v[0]), _f64(a), 1.0)
     for i in range(D):
         _close(out[0, :, 0, i], want[:, 0, i], TOL[dtype], f"column {i}")
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("N", [32, 25, 96])
+def test_state_of_tokens_long_decayed(N, dtype):
+    # only a chunk's first token adds to the state, which has forgotten 24 or 31 times exp(-0.75) when it is returned;
+    # 5e-6: exp of a product of up to 24, which is rounded in fp32 (2.5 2^-24 of it)
+    q, k, v = (_rand((1, N, 1, 64), 1.0, dtype, s) for s in (1, 2, 3))
+    first = N - (N % 32 or 32)
+    v[:, :first], v[:, first + 1:] = 0, 0
+    a = torch.tensor([-0.75])
+    _, S = fc.decay_attention(q.cuda(), k.cuda(), v.cuda(), a.cuda(), scale=1.0)
+    _, ws = seq.decay_fwd(_f64(q[0]), _f64(k[0]), _f64(v[0]), _f64(a), 1.0)
+    S = _f64(S[0])
+    assert np.linalg.norm(ws) > 0 and np.linalg.norm(S - ws) <= STATE_TOL * np.linalg.norm(ws)
