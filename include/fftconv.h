@@ -388,7 +388,10 @@ fftconv_status_t fftconv_decay_bwd(const void *dout, const void *q, const void *
  * The dense products around a mixer, with what follows them fused:
  *     pre = x W^T + bias,     out = act(pre) + residual
  * x (M, K), W (N, K), bias (N), residual, out, pre (M, N), one storage type,
- * fp32 accumulation, everything after the product in fp32, one rounding.  Rows
+ * fp32 accumulation, everything after the product in fp32, one rounding.
+ * Activations and their slopes (each of the slope's two summands) have relative errors of at
+ * most 2^-20 with fp32 storage (the tanh form: and 2^-22 for each unit of the exponential's
+ * argument) and 2^-15 before the rounding with 16-bit storage.  Rows
  * are contiguous; `strides` gives the row strides in elements (NULL = dense).
  * Any sizes and element-aligned pointers; 16-byte aligned rows of whole 16-byte pieces are
  * the fast case.  Results repeat bit by bit.  Sizes are below 2^31, N below 2^28; products of

@@ -42,44 +42,88 @@
 
 namespace fftconv {
 
-// exp and reciprocal of the hardware (each within an ulp or two of fp32, against results rounded to
-// 16 bits, or to 24 after sums of K terms)
-__device__ __forceinline__ float fast_exp(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504088896340736f); }
-__device__ __forceinline__ float fast_rcp(float x) { return __builtin_amdgcn_rcpf(x); }
-// 1 / (1 + exp(-x)); 0 and 1 at the far ends
-__device__ __forceinline__ float logistic(float x) { return fast_rcp(1.0f + fast_exp(-x)); }
-// Phi(z), the normal distribution's integral, from e = exp(-z^2 / 2): erfc by Abramowitz and Stegun,
-// Handbook of Mathematical Functions, 7.1.26, |error| <= 1.5e-7.
-__device__ __forceinline__ float normal_cdf(float z, float e) {
-    const float t = fast_rcp(fmaf(0.3275911f * 0.70710678118654752440f, fabsf(z), 1.0f));
-    const float p = t * fmaf(t, fmaf(t, fmaf(t, fmaf(t, 1.061405429f, -1.453152027f), 1.421413741f), -0.284496736f), 0.254829592f);
-    const float tail = 0.5f * p * e;                // Phi(-|z|)
+// Activations.  FULL: for results in fp32, relative errors of 2^-20 (the tanh form: and 2^-22 for each unit of the
+// logistic function's argument, which is rounded); else for results rounded to 16 bits, 2^-15 before that
+// rounding.  Slopes: of the size of their two summands.  exp and reciprocal are the hardware's, an ulp or two.
+//
+// exp(-(a + rest)) to fp32, a >= 0 and rest a correction to it: a log2 e, rounded, is off by 2^-24 of itself, which
+// is an absolute error of the exponent, so what the rounding left out is carried along.
+constexpr float kLog2eHi = 1.44269504f, kLog2eLo = 1.92596303e-8f;
+__device__ __forceinline__ float exp_minus(float a, float rest) {
+    constexpr float kLn2 = 0.69314718f;
+    a = a > 200.0f ? 200.0f : a;       // exp(-200) is 0; a NaN stays
+    const float t = -a * kLog2eHi, left = fmaf(-a, kLog2eHi, -t) - fmaf(a, kLog2eLo, rest * kLog2eHi);
+    return __builtin_amdgcn_exp2f(t) * fmaf(left, kLn2, 1.0f);
+}
+// p = 1 / (1 + exp(-x)) and p (1 - p); 0 and 1 at the far ends
+template <bool FULL> __device__ __forceinline__ float logistic(float x, float &n) {
+    if (FULL) {
+        const float e = exp_minus(fabsf(x), 0.0f), r = __builtin_amdgcn_rcpf(1.0f + e);
+        n = e * r * r;
+        return x >= 0.0f ? r : e * r;
+    }
+    const float p = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x * -kLog2eHi));
+    n = p * (1.0f - p);
+    return p;
+}
+// Phi(z), the normal distribution's integral, and e = exp(-z^2 / 2).  Phi(-|z|) / e = t P(t) with t = 1 / (1 + c |z|):
+// polynomials fitted here to the least relative error over |z| <= 14 (behind it e is 0), 3e-8 and 5e-6; with the
+// roundings of their evaluation 3e-7 and 5e-6.
+template <bool FULL> __device__ __forceinline__ float normal_cdf(float z, float &e) {
+    const float m = fabsf(z);
+    if (FULL) {
+        const float b = m > 20.0f ? 20.0f : m, s = b * b;
+        e = exp_minus(0.5f * s, 0.5f * fmaf(b, b, -s));
+    } else {
+        e = __builtin_amdgcn_exp2f(z * (z * (-0.5f * kLog2eHi)));
+    }
+    const float t = __builtin_amdgcn_rcpf(fmaf(FULL ? 0.35f : 0.31f, m, 1.0f));
+    float p;
+    if (FULL) {
+        p = fmaf(t, -2.914590947e-02f, 1.439716071e-01f);
+        p = fmaf(t, p, -2.557140887e-01f);
+        p = fmaf(t, p, 1.591739953e-01f);
+        p = fmaf(t, p, -2.310973220e-02f);
+        p = fmaf(t, p, 1.055079624e-01f);
+        p = fmaf(t, p, 1.198328733e-01f);
+        p = fmaf(t, p, 1.398618668e-01f);
+        p = fmaf(t, p, 1.396214068e-01f);
+    } else {
+        p = fmaf(t, -7.392912358e-02f, 1.804502904e-01f);
+        p = fmaf(t, p, 1.574476436e-02f);
+        p = fmaf(t, p, 1.334297657e-01f);
+        p = fmaf(t, p, 1.204412803e-01f);
+        p = fmaf(t, p, 1.238607019e-01f);
+    }
+    const float tail = t * p * e;                // Phi(-|z|)
     return z < 0.0f ? tail : 1.0f - tail;
 }
 // z (1 + tanh u) / 2 = z logistic(2 u), u = sqrt(2 / pi) (z + 0.044715 z^3)
 constexpr float kTanh2 = 2.0f * 0.79788456080286535588f;
-__device__ __forceinline__ float act_value(float z, int act) {
+template <bool FULL> __device__ __forceinline__ float act_value(float z, int act) {
+    float unused;
     switch (act) {
     case ACT_RELU: return z > 0.0f ? z : (z != z ? z : 0.0f);
-    case ACT_GELU: return z * normal_cdf(z, fast_exp(-0.5f * z * z));
-    case ACT_GELU_TANH: return z * logistic(kTanh2 * z * fmaf(0.044715f * z, z, 1.0f));
-    case ACT_SILU: return z * logistic(z);
+    case ACT_GELU: return z * normal_cdf<FULL>(z, unused);
+    case ACT_GELU_TANH: return z * logistic<FULL>(kTanh2 * z * fmaf(0.044715f * z, z, 1.0f), unused);
+    case ACT_SILU: return z * logistic<FULL>(z, unused);
     default: return z;
     }
 }
-__device__ __forceinline__ float act_slope(float z, int act) {
+template <bool FULL> __device__ __forceinline__ float act_slope(float z, int act) {
+    float n;
     switch (act) {
     case ACT_RELU: return z > 0.0f ? 1.0f : 0.0f;
     case ACT_GELU: {
-        const float e = fast_exp(-0.5f * z * z);
-        return normal_cdf(z, e) + (e == 0.0f ? 0.0f : z * e * 0.39894228040143267794f);
+        const float p = normal_cdf<FULL>(z, n);
+        return p + (n == 0.0f ? 0.0f : z * n * 0.39894228040143267794f);
     }
     case ACT_GELU_TANH: {
-        const float u = z * z, p = logistic(kTanh2 * z * fmaf(0.044715f, u, 1.0f)), n = p * (1.0f - p);
+        const float u = z * z, p = logistic<FULL>(kTanh2 * z * fmaf(0.044715f * z, z, 1.0f), n);
         return p + (n == 0.0f ? 0.0f : z * n * kTanh2 * fmaf(0.134145f, u, 1.0f));   // n vanishes first
     }
     case ACT_SILU: {
-        const float p = logistic(z), n = p * (1.0f - p);
+        const float p = logistic<FULL>(z, n);
         return p + (n == 0.0f ? 0.0f : z * n);
     }
     default: return 1.0f;
@@ -125,7 +169,7 @@ __device__ __forceinline__ void linear_epilogue(const LinearGemm &a, int64_t m, 
     if (a.pre) store_quad(static_cast<T *>(a.pre) + m * a.ldp + n, left, a.vec_p, f);
     if (a.act != ACT_NONE) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) f[i] = act_value(f[i], a.act);
+        for (int i = 0; i < 4; ++i) f[i] = act_value<sizeof(T) == 4>(f[i], a.act);
     }
     if (a.res) {
         load_quad(static_cast<const T *>(a.res) + m * a.ldr + n, left, a.vec_r, t);
@@ -446,7 +490,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void linear_gemm_kernel(const Line
                         }
                         if (a.act != ACT_NONE) {
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) f[e] = act_value(f[e], a.act);
+                            for (int e = 0; e < 4; ++e) f[e] = act_value<sizeof(T) == 4>(f[e], a.act);
                         }
                         if (a.res) {
                             q = view_load_wide<Q>(vr, in ? (uint32_t)(row * (uint32_t)a.ldr) * (uint32_t)sizeof(T) + x : kSkip);
@@ -606,7 +650,7 @@ template <typename T, int V> __global__ __launch_bounds__(256) void linear_dz_ke
                 Row w;
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
-                    const float f = (float)d[u].v[j] * (a.act != ACT_NONE ? act_slope((float)z[u].v[j], a.act) : 1.0f);
+                    const float f = (float)d[u].v[j] * (a.act != ACT_NONE ? act_slope<sizeof(T) == 4>((float)z[u].v[j], a.act) : 1.0f);
                     sum[j] += f;
                     w.v[j] = (T)f;
                 }
