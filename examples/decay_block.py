@@ -70,9 +70,11 @@ class DecayBlock:
         dh, dw_in, db_in = fc.linear_act_bwd(da, h, self.w_in, pre, "gelu")
         dh += dout                                              # the MLP's residual
         dmixed, dw_out, _ = fc.linear_act_bwd(dh, mixed, self.w_out, bias=False)
-        dq, dk, dv, _ = fc.decay_attention_bwd(q, k, v, self.log_decay, dmixed.unflatten(1, (self.H, self.D)),
-                                               cu_seqlens=cu_seqlens)
-        dqkv = torch.cat([t.flatten(1) for t in (dq, dk, dv)], dim=1)
+        dqkv = torch.empty_like(qkv)                            # dq, dk and dv into one buffer, as the projection takes it
+        scratch = torch.empty(fc.fftconv_decay_bwd_workspace_bytes(
+            cu_seqlens.numel() - 1, x.shape[0], self.H, self.Hk, self.D, self.D, x.dtype), dtype=torch.uint8, device=x.device)
+        fc.fftconv_decay_bwd(dmixed.unflatten(1, (self.H, self.D)), q, k, v, self.log_decay, *self._split(dqkv), self.D ** -0.5,
+                             cu_seqlens=cu_seqlens, workspace=scratch)
         dx, dw_qkv, db_qkv = fc.linear_act_bwd(dqkv, x, self.w_qkv)
         return dict(x=dx + dh, w_qkv=dw_qkv, b_qkv=db_qkv, w_out=dw_out, w_in=dw_in, b_in=db_in, w_mlp=dw_mlp)
 

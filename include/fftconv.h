@@ -318,6 +318,8 @@ fftconv_status_t fftconv_eqlinear_fwd(const void *x, const void *W_f, void *y, i
  * Layouts: q (B, N, H, Dk), k (B, N, Hk, Dk), v (B, N, Hk, Dv), out (B, N, H, Dv).
  * `strides` gives (batch, token, head) in elements for each tensor in the
  * order of the arguments, NULL = dense; rows of Dk or Dv values are contiguous.
+ * Results share no element with each other or an input; blocks of one buffer that repeat by a
+ * common stride (dq, dk, dv as heads of a fused buffer) are told apart, others by their spans.
  * Pointers need the alignment of their elements only; rows at 16-byte aligned
  * addresses of whole 16-byte pieces are the fast case.
  * Packed sequences: with cu_seqlens (device int32, B + 1 ascending values from

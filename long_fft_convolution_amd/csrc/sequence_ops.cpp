@@ -67,10 +67,30 @@ struct View {
         for (int i = 0; i < dims; ++i) last += (size[i] - 1) * stride[i];
         return last * bytes_per;
     }
+    // bytes from p that the view's elements stay within modulo a period: dimensions that step by whole periods
+    // add nothing
+    int64_t extent(int64_t period) const {
+        int64_t last = row;
+        for (int i = 0; i < dims; ++i)
+            if (stride[i] * bytes_per % period) last += (size[i] - 1) * stride[i];
+        return last * bytes_per;
+    }
+    // Whether the views may share memory.  Spans that meet belong to tensors of one buffer (column blocks of a matrix,
+    // heads side by side): those are apart where for some stride as a period their extents are arcs of its
+    // circle that do not touch.  What no stride tells apart counts as shared.
     bool overlaps(const View &o) const {
         if (!p || !o.p || empty() || o.empty()) return false;
-        auto a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(o.p);
-        return a < b + (uintptr_t)o.span() && b < a + (uintptr_t)span();
+        const auto a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(o.p);
+        if (a >= b + (uintptr_t)o.span() || b >= a + (uintptr_t)span()) return false;
+        for (const View *v : {this, &o})
+            for (int i = 0; i < v->dims; ++i) {
+                const int64_t period = v->stride[i] * v->bytes_per;
+                if (period <= 0) continue;
+                const int64_t mine = extent(period), its = o.extent(period), way = (int64_t)(b - a) % period;
+                const int64_t ahead = way < 0 ? way + period : way;      // from this view's start round to o's
+                if (mine <= ahead && ahead + its <= period) return false;
+            }
+        return true;
     }
     // every element at a place of its own: each stride reaches past what the smaller ones span
     bool distinct() const {
