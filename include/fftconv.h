@@ -396,7 +396,7 @@ fftconv_status_t fftconv_decay_bwd(const void *dout, const void *q, const void *
  * argument) and 2^-15 before the rounding with 16-bit storage.  Rows
  * are contiguous; `strides` gives the row strides in elements (NULL = dense).
  * Any sizes and element-aligned pointers; 16-byte aligned rows of whole 16-byte pieces are
- * the fast case.  Results repeat bit by bit.  Sizes are below 2^31, N below 2^28; products of
+ * the fast case.  Results repeat bit by bit.  Sizes are below 2^31, N at most 2^28 - 16; products of
  * more than 2^23 tiles (64 to 256 wide) are refused with FFTCONV_ERR_UNSUPPORTED. */
 typedef enum {
     FFTCONV_ACT_NONE = 0,

@@ -664,13 +664,14 @@ hipError_t run_gemm(int dt, LinearGemm &g, int layout, bool vec, float *part, hi
                                : launch_linear_gemm_bf16(g, layout, p.tile, vec, s);
 }
 
-// a launch has fewer than 2^32 threads: 512 a tile; 16 a column or more in the kernels that go over rows
+// a launch has fewer than 2^32 threads: 512 a tile; 256 for each 16 columns in the kernels that go over rows
+constexpr int64_t kMaxColumns = (int64_t(1) << 28) - 16;
 bool too_large(int64_t M, int64_t N, int64_t K, int dt) {
     for (bool vec : {true, false}) {
         const GemmPlan p = plan_gemm(M, N, K, dt, vec);
         if (p.full + (p.tiles - p.full) * p.splits >= int64_t(1) << 23) return true;
     }
-    return N >= int64_t(1) << 28;
+    return N > kMaxColumns;
 }
 fftconv_status_t too_large_status(int64_t M, int64_t N, int64_t K) {
     return fail(FFTCONV_ERR_UNSUPPORTED, "M=%lld, N=%lld, K=%lld: too large a product", (long long)M, (long long)N, (long long)K);
@@ -790,7 +791,7 @@ fftconv_status_t fftconv_linear_bwd(const void *dout, const void *x, const void 
                vw = matrix("W", W, N, K, ld(2, K), dtype), vp = matrix("pre", pre, M, N, ld(3, N), dtype),
                gx = matrix("dx", dx, M, K, ld(4, K), dtype), gw = matrix("dW", dW, N, K, ld(5, K), dtype),
                gb = matrix("dbias", dbias, 1, N, N, dtype);
-    if (too_large(M, K, N, dtype) || too_large(N, K, M, dtype) || N >= int64_t(1) << 28) return too_large_status(M, N, K);
+    if (too_large(M, K, N, dtype) || too_large(N, K, M, dtype) || N > kMaxColumns) return too_large_status(M, N, K);
     const bool need_pre = activation != FFTCONV_ACT_NONE;
     if ((st = check_view(vd, true, false)) != FFTCONV_OK) return st;
     if ((st = check_view(vx, dW != nullptr, false)) != FFTCONV_OK) return st;
