@@ -648,10 +648,10 @@ def linear_act(x, W, bias=None, residual=None, activation="none", keep_pre=False
     if stream is not None:
         with torch.cuda.stream(stream):      # the scratch memory and the results are that stream's, too
             return linear_act(x, W, bias, residual, activation, keep_pre)
-    M, N = x.shape[0], W.shape[0]
+    M, N, K = _linear_shapes(x, W)
     out = torch.empty((M, N), dtype=x.dtype, device=x.device)
     pre = torch.empty_like(out) if keep_pre else None
-    ws = _scratch(fftconv_linear_fwd_workspace_bytes(M, N, x.shape[1], x.dtype), x.device)
+    ws = _scratch(fftconv_linear_fwd_workspace_bytes(M, N, K, x.dtype), x.device)
     fftconv_linear_fwd(x, W, bias, residual, out, pre, activation, ws)
     return (out, pre) if keep_pre else out
 
@@ -661,9 +661,10 @@ def linear_act_bwd(dout, x, W, pre=None, activation="none", bias=True, stream=No
     if stream is not None:
         with torch.cuda.stream(stream):
             return linear_act_bwd(dout, x, W, pre, activation, bias)
+    M, N, K = _linear_shapes(x, W)
     dx, dW = (torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (x, W))
-    dbias = torch.empty(W.shape[0], dtype=x.dtype, device=x.device) if bias else None
-    ws = _scratch(fftconv_linear_bwd_workspace_bytes(x.shape[0], W.shape[0], x.shape[1], x.dtype), x.device)
+    dbias = torch.empty(N, dtype=x.dtype, device=x.device) if bias else None
+    ws = _scratch(fftconv_linear_bwd_workspace_bytes(M, N, K, x.dtype), x.device)
     fftconv_linear_bwd(dout, x, W, pre, dx, dW, dbias, activation, ws)
     return dx, dW, dbias
 
