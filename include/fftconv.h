@@ -423,7 +423,8 @@ size_t fftconv_linear_bwd_workspace_bytes(int64_t M, int64_t N, int64_t K, fftco
 /* Gradients of sum(dout * out), with dz = dout * act'(pre):
  *     dx = dz W,   dW = dz^T x,   dbias = sum over rows of dz      (the residual's is dout)
  * each NULL = skipped.  pre may be NULL for FFTCONV_ACT_NONE; relu's slope at 0
- * is 0.  dz is rounded to the storage type where it meets W and x; dbias sums it unrounded.
+ * is 0.  dz is rounded to the storage type where it meets W and x (in fp16, gradients below 2^-14
+ * keep fewer bits there: scale the loss); dbias sums it unrounded.
  * strides: int64[6], dout, x, W, pre, dx, dW. */
 fftconv_status_t fftconv_linear_bwd(const void *dout, const void *x, const void *W, const void *pre, void *dx, void *dW,
                                     void *dbias, const int64_t *strides, int64_t M, int64_t N, int64_t K,

@@ -310,12 +310,16 @@ constexpr int walk_stages(int bytes, bool vec) { return !vec ? 1 : (3 * bytes <=
 // registers, so the plain prompt has a kernel without it).  DXP: DX padded; NT: 16-column tiles of E per
 // wave.  grid: work items (see work_of).
 //
-// What bounds it: 20 heads of 128 x 128 in bf16, 131072 tokens: 622 us for 2.69 GB read and written, 4.3 TB/s, so
-// near the memory; the sums before it 335 us for 1.34 GB.  With few tokens a walk the serial chunk does: 1.8 us
-// at 128 x 128 with one walk a CU (the gradients of 4 x 4096 tokens: 230 us for 128 chunks, the matrix units a
-// quarter of the time busy).  P is computed by each of the four waves: sharing it through LDS would put a
-// barrier and a round trip between a chunk's products.  Two workgroups a CU overlap one's barriers and
-// LDS reads with the other's products.
+// What bounds it: 20 heads of 128 x 128 in bf16, 131072 tokens: 632 us for 2.69 GB read and written, 4.3 TB/s, so
+// near the memory; the sums before it 335 to 362 us for 1.34 GB.  With few tokens a walk the serial chunk does:
+// 1.8 us at 128 x 128 with one walk a CU (the gradients of 4 x 4096 tokens: 230 us for 128 chunks, the matrix
+// units a quarter of the time busy).  Two workgroups a CU overlap little where heads share k and v and memory
+// is no bound: packed prompts take 84 us for 22 chunks.  P is computed by each of the four waves: sharing it
+// through LDS would put a barrier and a round trip between a chunk's products (not tried).
+//
+// fp16's look at the sizes of the state and of P costs instructions where two workgroups compete for a SIMD:
+// gradients of 8 x 1000 tokens, 12 heads of 64: 67 us without, 70 with it; elsewhere it is hidden (prompts of
+// 4 x 4096 and 131072 tokens, gradients of 4 x 4096: within 1 %).
 enum WalkMode : int { kSums = 0, kOut = 1, kOutAny = 2 };
 template <typename T, int DXP, int NT, int MODE, bool VEC>
 __global__ __launch_bounds__(256, DXP <= 128 ? 2 : 1) void decay_walk_kernel(const DecaySet set) {
@@ -454,7 +458,8 @@ __global__ __launch_bounds__(256, DXP <= 128 ? 2 : 1) void decay_walk_kernel(con
             __syncthreads();
         } else {
             // this chunk's loads are the oldest; with three stages the next chunk's, if there is one,
-            // may still travel (vmcnt retires in order).  The wait on LDS reads keeps every wave's
+            // may still travel (vmcnt retires in order; it counts the stores of the chunk before as well, so
+            // as many of those loads have arrived, too).  The wait on LDS reads keeps every wave's
             // reads of the freed stage before the loads into it.
             if (S == 3 && t + kChunk < t_end) wait_loads_and_barrier<kLoads>();
             else wait_loads_and_barrier<0>();

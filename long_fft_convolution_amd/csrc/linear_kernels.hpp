@@ -24,10 +24,11 @@
 // At 256 x 256 x 64 a line is 32 matrix instructions a wave (1024 cycles of a
 // SIMD's two waves) against 12 LDS reads (768 cycles of the CU's LDS).
 //
-// Measured in bf16: 8192^3 774 us, 1420 TF/s; 16384 x 2560 -> 10240 696 us, 1234 TF/s, and
-// 775 us with bias, GELU and residual (the epilogue's 0.7 GB and its arithmetic do
-// not pass under products: a tile ends with them).  Two stages of 128 bytes against
-// four of 64: 785 against 857 us, the shorter ones leaving half the loads a line apart.
+// Measured in bf16: 8192^3 820 us, 1340 TF/s; 16384 x 2560 -> 10240 715 us, 1200 TF/s, 770 us with bias
+// and GELU, 920 to 980 with a residual as well, 905 to 930 with the pre-activation kept (the epilogue's
+// 0.3 to 0.7 GB and its arithmetic do not pass under products: a tile ends with them).  The library's
+// products in the same runs: 690 and 583 us.  Two stages of 128 bytes against four of 64: 785 against
+// 857 us, the shorter ones leaving half the loads a line apart.
 //
 // An operand contiguous along k lies in LDS as rows of 128 bytes, its eight
 // 16-byte slots exchanged by the row; one contiguous along the tile as k rows of
