@@ -431,6 +431,36 @@ fftconv_status_t fftconv_linear_bwd(const void *dout, const void *x, const void 
                                     fftconv_activation_t activation, fftconv_dtype_t dtype, void *workspace,
                                     size_t workspace_bytes, hipStream_t stream);
 
+/* ---- Root-mean-square norm ----------------------------------------------------
+ * The norm before a mixer or MLP with the residual stream's addition, over rows of any width (also the
+ * heads' own: queries and keys of the delta rule):
+ *     t = x + residual,    y = t / sqrt(mean(t^2) + eps) * weight
+ * x, residual, sum (M, G, D) rows of D values in (M, G) groups, weight (D) or NULL (ones), one storage
+ * type, 1 <= D <= 2^20, M * G < 2^31.  Everything is fp32 (squares beyond fp32's range make the row 0);
+ * `sum` receives t rounded once, out receives y, of the unrounded t.
+ *   scales  NULL: out (M, G, D) holds y in the storage type.  Else fp32 (M, G): out holds 8 bits (e4m3,
+ *           largest value 448) with y ~ scale * out, scale = max|y| / 448 of the row, at least 2^-126;
+ *           a row with a NaN has the scale NaN.
+ *   strides int64[8], (row, group) in elements of x, residual, out, sum, or NULL = dense; rows are contiguous.
+ * residual and sum may be NULL; sum may be the residual or x itself (same pointer and strides), else no
+ * result overlaps anything.  No workspace.  Asynchronous on stream. */
+fftconv_status_t fftconv_norm_fwd(const void *x, const void *residual, const void *weight, void *out, void *sum,
+                                  float *scales, const int64_t *strides, int64_t M, int64_t G, int64_t D, float eps,
+                                  fftconv_dtype_t dtype, hipStream_t stream);
+
+/* Device scratch bytes of fftconv_norm_bwd for `rows` = M * G; 0 where none is needed or an argument is unsupported. */
+size_t fftconv_norm_bwd_workspace_bytes(int64_t rows, int64_t D);
+
+/* Gradients of sum(dout * out) + sum(dsum * sum) with x the sum that the forward call normed (its x without a
+ * residual): r = 1 / sqrt(mean(x^2) + eps), u = weight dout,
+ *     dx = r (u - x r^2 mean(u x)) + dsum,    dweight = sum over rows of dout x r
+ * dx is the gradient of x and of the residual alike.  weight, dsum, dx and dweight may be NULL; dx may be dsum
+ * itself.  dweight is summed in fp32 in one order (results repeat bit by bit) and is zero without rows.
+ * strides: int64[8], dout, x, dsum, dx, or NULL. */
+fftconv_status_t fftconv_norm_bwd(const void *dout, const void *x, const void *weight, const void *dsum, void *dx,
+                                  void *dweight, const int64_t *strides, int64_t M, int64_t G, int64_t D, float eps,
+                                  fftconv_dtype_t dtype, void *workspace, size_t workspace_bytes, hipStream_t stream);
+
 /* Static text for a status code. */
 const char *fftconv_status_string(fftconv_status_t status);
 

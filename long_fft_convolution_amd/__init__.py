@@ -13,7 +13,9 @@ frequency-sparse filters.)
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import math
 import os
 
 import numpy as np
@@ -109,6 +111,12 @@ def _load():
     lib.fftconv_linear_bwd_workspace_bytes.restype = sz
     lib.fftconv_linear_bwd.argtypes = [vp] * 8 + [i64] * 3 + [ctypes.c_int, ctypes.c_int, vp, sz, vp]
     lib.fftconv_linear_bwd.restype = ctypes.c_int
+    lib.fftconv_norm_fwd.argtypes = [vp] * 7 + [i64] * 3 + [ctypes.c_float, ctypes.c_int, vp]
+    lib.fftconv_norm_fwd.restype = ctypes.c_int
+    lib.fftconv_norm_bwd_workspace_bytes.argtypes = [i64, i64]
+    lib.fftconv_norm_bwd_workspace_bytes.restype = sz
+    lib.fftconv_norm_bwd.argtypes = [vp] * 7 + [i64] * 3 + [ctypes.c_float, ctypes.c_int, vp, sz, vp]
+    lib.fftconv_norm_bwd.restype = ctypes.c_int
     _lib = lib
     return lib
 
@@ -667,6 +675,134 @@ def linear_act_bwd(dout, x, W, pre=None, activation="none", bias=True, stream=No
     ws = _scratch(fftconv_linear_bwd_workspace_bytes(M, N, K, x.dtype), x.device)
     fftconv_linear_bwd(dout, x, W, pre, dx, dW, dbias, activation, ws)
     return dx, dW, dbias
+
+
+# ---------------------------------------------------------------- root-mean-square norm
+def _on(device):
+    """The tensors' device as the current one for the call (the library launches on the current device)."""
+    return torch.cuda.device(device) if device.index != torch.cuda.current_device() else _here
+
+
+_here = contextlib.nullcontext()
+
+
+def _row_groups(shape, tensors):
+    """M, G, D of rows (..., D) and the (row, group) strides of each tensor, None where all are dense.
+
+    Leading dimensions beyond two are folded where every tensor's strides allow it.
+    """
+    D, lead = shape[-1], tuple(shape[:-1])
+    M = math.prod(lead)
+    if all(t is None or t.is_contiguous() for t in tensors):
+        return M, 1, D, None
+    if M == 0:
+        return M, 1, D, None
+    dims = [i for i, n in enumerate(lead) if n != 1]
+    # an outer run of dimensions and an inner one, each of which steps evenly in every tensor
+    def runs(t):
+        return {j for j in range(1, len(dims)) if t.stride(dims[j - 1]) != t.stride(dims[j]) * lead[dims[j]]}
+
+    cuts = set().union(*(runs(t) for t in tensors if t is not None))
+    if len(cuts) > 1:
+        raise ValueError("leading dimensions must fold into two evenly strided ones")
+    cut = cuts.pop() if cuts else 0
+    outer, inner = dims[:cut], dims[cut:]
+    G = math.prod(lead[i] for i in inner)
+    flat = []
+    for t in tensors:
+        if t is None:
+            flat += (0, 0)
+        else:
+            flat += (t.stride(outer[-1]) if outer else 0, t.stride(inner[-1]) if inner else 0)
+    return M // max(G, 1), G, D, _strides_of[8](*flat)
+
+
+def _weight_tensor(t, name, x):
+    if t is not None:
+        _plain_tensor(t, name, x.dtype, (x.shape[-1],), x.device)
+
+
+def fftconv_norm_fwd(x: torch.Tensor, weight: torch.Tensor | None, out: torch.Tensor, eps: float,
+                     residual: torch.Tensor | None = None, sum: torch.Tensor | None = None,
+                     scales: torch.Tensor | None = None, stream=None) -> None:
+    """out <- (x + residual) / rms * weight over the last dimension; sum (optional) <- x + residual.
+
+    With scales (fp32, one a row) out is torch.float8_e4m3fn and holds y / scale.
+    """
+    _rows_tensor(x, "x", x, x.shape)
+    if x.dim() == 0:
+        raise ValueError("x must have a dimension")
+    _weight_tensor(weight, "weight", x)
+    for name, t in (("residual", residual), ("sum", sum)):
+        if t is not None:
+            _rows_tensor(t, name, x, x.shape)
+    if scales is None:
+        _rows_tensor(out, "out", x, x.shape)
+    else:
+        _plain_tensor(scales, "scales", torch.float32, x.shape[:-1], x.device)
+        if out.dtype is not torch.float8_e4m3fn:
+            raise ValueError(f"out must have dtype {torch.float8_e4m3fn} with scales")
+        if out.device != x.device or out.shape != x.shape or (out.stride(-1) != 1 and out.shape[-1] > 1):
+            raise ValueError(f"out must be on {x.device}, of shape {tuple(x.shape)}, contiguous along its last dimension")
+    M, G, D, strides = _row_groups(x.shape, (x, residual, out, sum))
+    with _on(x.device):
+        _check((_lib or _load()).fftconv_norm_fwd(
+            x.data_ptr(), _at(residual), _at(weight), out.data_ptr(), _at(sum), _at(scales), strides, M, G, D, eps,
+            _DTYPE_CODE[x.dtype], _raw_stream(stream, x.device)))
+
+
+def fftconv_norm_bwd_workspace_bytes(rows: int, D: int) -> int:
+    return int(_load().fftconv_norm_bwd_workspace_bytes(rows, D))
+
+
+def fftconv_norm_bwd(dout: torch.Tensor, x: torch.Tensor, weight: torch.Tensor | None, dx: torch.Tensor | None,
+                     dweight: torch.Tensor | None, eps: float, dsum: torch.Tensor | None = None,
+                     workspace: torch.Tensor | None = None, stream=None) -> None:
+    """Gradients of fftconv_norm_fwd into dx and dweight (None = skip); x is the sum that was normed, dsum its own gradient."""
+    _rows_tensor(x, "x", x, x.shape)
+    if x.dim() == 0:
+        raise ValueError("x must have a dimension")
+    _weight_tensor(weight, "weight", x)
+    _weight_tensor(dweight, "dweight", x)
+    for name, t in (("dout", dout), ("dx", dx), ("dsum", dsum)):
+        if t is not None:
+            _rows_tensor(t, name, x, x.shape)
+    _dev_tensor(workspace, "workspace")
+    M, G, D, strides = _row_groups(x.shape, (dout, x, dsum, dx))
+    with _on(x.device):
+        _check((_lib or _load()).fftconv_norm_bwd(
+            dout.data_ptr(), x.data_ptr(), _at(weight), _at(dsum), _at(dx), _at(dweight), strides, M, G, D, eps,
+            _DTYPE_CODE[x.dtype], _at(workspace), _nbytes(workspace), _raw_stream(stream, x.device)))
+
+
+def rms_norm(x, weight=None, eps=1e-6, residual=None, eight_bits=False, stream=None):
+    """(x + residual) / rms * weight over the last dimension (allocations by torch).
+
+    Returns out, with eight_bits out (float8_e4m3fn) and its scales, and with a residual x + residual behind them.
+    """
+    if stream is not None:
+        with torch.cuda.stream(stream):      # the results are that stream's, too
+            return rms_norm(x, weight, eps, residual, eight_bits)
+    _rows_tensor(x, "x", x, x.shape)
+    out = torch.empty(x.shape, dtype=torch.float8_e4m3fn if eight_bits else x.dtype, device=x.device)
+    scales = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device) if eight_bits else None
+    total = torch.empty(x.shape, dtype=x.dtype, device=x.device) if residual is not None else None
+    fftconv_norm_fwd(x, weight, out, eps, residual, total, scales)
+    got = [t for t in (out, scales, total) if t is not None]
+    return got[0] if len(got) == 1 else tuple(got)
+
+
+def rms_norm_bwd(dout, x, weight=None, eps=1e-6, dsum=None, stream=None):
+    """Gradients of rms_norm, x being the sum that it normed; returns (dx, dweight), dweight None without a weight."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return rms_norm_bwd(dout, x, weight, eps, dsum)
+    _rows_tensor(x, "x", x, x.shape)
+    dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    dweight = None if weight is None else torch.empty_like(weight)
+    ws = _scratch(fftconv_norm_bwd_workspace_bytes(x.numel() // max(1, x.shape[-1]), x.shape[-1]), x.device)
+    fftconv_norm_bwd(dout, x, weight, dx, dweight, eps, dsum, ws)
+    return dx, dweight
 
 
 def alloc_filter(H: int, N: int, dtype: torch.dtype, device="cuda") -> torch.Tensor:

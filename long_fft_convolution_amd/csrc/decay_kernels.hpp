@@ -51,7 +51,7 @@
 
 #include <type_traits>
 
-#include "mma.hpp"
+#include "sequence_device.hpp"
 #include "sequence_ops.hpp"
 
 namespace fftconv {
@@ -137,23 +137,8 @@ __device__ __forceinline__ int64_t parts_before_last(const DecayWalk &a, int64_t
     return count > 0 ? (count - 1) / a.parts * a.parts : 0;
 }
 
-// Slot of sequence seq in the state pool, or -1 (no state kept).
-__device__ __forceinline__ int64_t state_slot(const int32_t *slots, int64_t n_slots, int64_t seq) {
-    if (!slots) return seq;
-    const int64_t s = slots[seq];
-    return s >= 0 && s < n_slots ? s : -1;
-}
-
 __device__ __forceinline__ float decay_power(float log2d, int64_t n) {
     return n <= 0 ? 1.0f : exp2f(log2d * (float)n);
-}
-
-constexpr float kLog2e = 1.44269504088896340736f;
-
-// A 64-bit value that is the same in every lane, as a scalar.
-__device__ __forceinline__ int64_t scalar(int64_t v) {
-    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v), hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
-    return (int64_t)((uint64_t)hi << 32 | lo);
 }
 
 // Tokens of a chunk.  32 is one contraction step of the 16-bit matrix instruction: with it the
@@ -273,22 +258,6 @@ template <typename T, int DP, bool PERMUTED, bool VEC> struct ChunkSource {
         }
     }
 };
-
-// NT * 4 neighbouring outputs of a lane at byte offset off (or kSkip).  WHOLE: aligned, and all there
-// or none; else `left` of them are, written one by one unless vec and all are there.
-template <typename TO, int NT, bool WHOLE>
-__device__ __forceinline__ void put_row(__amdgpu_buffer_rsrc_t view, uint32_t off, const f32x4 *o, int vec, int left) {
-    struct Row { TO w[NT * 4]; } row;
-#pragma unroll
-    for (int j = 0; j < NT * 4; ++j) row.w[j] = (TO)o[j >> 2][j & 3];
-    const bool whole = WHOLE | ((vec != 0) & (NT * 4 <= left));
-    view_store(view, whole ? off : kSkip, row);
-    if (!WHOLE) {
-#pragma unroll
-        for (int j = 0; j < NT * 4; ++j)
-            view_store(view, (!whole) & (j < left) & (off != kSkip) ? off + j * (uint32_t)sizeof(TO) : kSkip, row.w[j]);
-    }
-}
 
 // Work item of workgroup id: ids go to the 8 XCDs in turn, so runs of set.share items are dealt to
 // one XCD, whose L2 then holds what they have in common.
