@@ -386,6 +386,48 @@ fftconv_status_t fftconv_decay_bwd(const void *dout, const void *q, const void *
                                    int64_t Dv, float scale, fftconv_dtype_t dtype, void *workspace,
                                    size_t workspace_bytes, hipStream_t stream);
 
+/* ---- Gated delta rule --------------------------------------------------------
+ * Linear attention whose state forgets by a factor of each token and is corrected by what it got wrong,
+ * beside decay attention.  With a_t = exp(log_decay_t), beta_t, and per sequence and head an fp32 state
+ * S (Dk x Dv, row-major):
+ *
+ *     u_t = beta_t (v_t - a_t S_{t-1}^T k_t),    S_t = a_t S_{t-1} + k_t u_t^T,    out_t = scale * S_t^T q_t
+ *
+ * log_decay and beta are fp32 (B, N, H), dense: logarithms <= 0 (-inf: the state is cleared before the token),
+ * and any weight.  The rule is stable while beta |k|^2 <= 2: keys are meant to be normed (fftconv_norm_fwd over
+ * the heads' rows, weight 1 / sqrt(Dk)).
+ * Heads: v, out, log_decay, beta and the states have H heads, q and k Hk, H a multiple of Hk; head h uses q/k
+ * head h / (H / Hk).  Widths 1 <= Dk, Dv <= 256.
+ * Layouts: q, k (B, N, Hk, Dk), v, out (B, N, H, Dv); `strides` (batch, token, head), alignment, separation of
+ * results, packed sequences (cu_seqlens) and state pools (state_slots) as for decay attention.
+ * Precision: operands are exact sums of bf16 terms and products are accumulated in fp32; the states, and
+ * everything a state depends on, keep fp32 precision.  Outputs in 16 bits see the state to 2^-16 and the products
+ * q k^T to one rounding (bf16) or 2^-16 (fp16).
+ * A NaN or infinity in a token may reach every output of its sequence and head from its block of 64 tokens on,
+ * never another sequence.
+ * Refused with FFTCONV_ERR_UNSUPPORTED: token strides of 16 MiB or more, and calls whose (64 tokens, head) pairs
+ * pass 2^24 or whose (sequence, head) pairs pass 2^20. */
+
+/* Device scratch bytes of fftconv_delta_fwd for T tokens in all (B * N, or N when packed); 0 where none is needed or
+ * an argument is unsupported. */
+size_t fftconv_delta_fwd_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t Hk, int64_t Dk, int64_t Dv,
+                                         fftconv_dtype_t dtype);
+
+/* Prompt form over whole sequences; arguments as fftconv_decay_fwd, with beta.  strides: int64[12], q, k, v, out. */
+fftconv_status_t fftconv_delta_fwd(const void *q, const void *k, const void *v, const float *log_decay, const float *beta,
+                                   void *out, const int64_t *strides, const float *state_in, float *state_out,
+                                   const int32_t *state_slots, int64_t n_slots, const int32_t *cu_seqlens, int64_t B,
+                                   int64_t N, int64_t H, int64_t Hk, int64_t Dk, int64_t Dv, float scale,
+                                   fftconv_dtype_t dtype, void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* One token of each of B sequences: q, k (B, Hk, Dk), v, out (B, H, Dv), log_decay, beta (B, H); the states are
+ * updated in place.  strides: int64[8] host array, (batch, head) of q, k, v, out, or NULL.  state and state_slots as
+ * for fftconv_decay_step.  No workspace. */
+fftconv_status_t fftconv_delta_step(const void *q, const void *k, const void *v, const float *log_decay,
+                                    const float *beta, float *state, void *out, const int64_t *strides,
+                                    const int32_t *state_slots, int64_t n_slots, int64_t B, int64_t H, int64_t Hk,
+                                    int64_t Dk, int64_t Dv, float scale, fftconv_dtype_t dtype, hipStream_t stream);
+
 /* ---- Linear product ---------------------------------------------------------
  * The dense products around a mixer, with what follows them fused:
  *     pre = x W^T + bias,     out = act(pre) + residual

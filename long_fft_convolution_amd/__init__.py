@@ -111,6 +111,12 @@ def _load():
     lib.fftconv_linear_bwd_workspace_bytes.restype = sz
     lib.fftconv_linear_bwd.argtypes = [vp] * 8 + [i64] * 3 + [ctypes.c_int, ctypes.c_int, vp, sz, vp]
     lib.fftconv_linear_bwd.restype = ctypes.c_int
+    lib.fftconv_delta_fwd_workspace_bytes.argtypes = ints + [ctypes.c_int]
+    lib.fftconv_delta_fwd_workspace_bytes.restype = sz
+    lib.fftconv_delta_fwd.argtypes = [vp] * 10 + [i64, vp] + ints + [ctypes.c_float, ctypes.c_int, vp, sz, vp]
+    lib.fftconv_delta_fwd.restype = ctypes.c_int
+    lib.fftconv_delta_step.argtypes = [vp] * 9 + [i64] * 6 + [ctypes.c_float, ctypes.c_int, vp]
+    lib.fftconv_delta_step.restype = ctypes.c_int
     lib.fftconv_norm_fwd.argtypes = [vp] * 7 + [i64] * 3 + [ctypes.c_float, ctypes.c_int, vp]
     lib.fftconv_norm_fwd.restype = ctypes.c_int
     lib.fftconv_norm_bwd_workspace_bytes.argtypes = [i64, i64]
@@ -675,6 +681,104 @@ def linear_act_bwd(dout, x, W, pre=None, activation="none", bias=True, stream=No
     ws = _scratch(fftconv_linear_bwd_workspace_bytes(M, N, K, x.dtype), x.device)
     fftconv_linear_bwd(dout, x, W, pre, dx, dW, dbias, activation, ws)
     return dx, dW, dbias
+
+
+# ---------------------------------------------------------------- gated delta rule
+def _delta_shapes(q, k, v, log_decay, beta, cu_seqlens):
+    qs, ks, vs = q.shape, k.shape, v.shape
+    dims = 4 if cu_seqlens is None else 3
+    if len(qs) != dims or len(ks) != dims or len(vs) != dims:
+        raise ValueError(f"q, k and v must have {dims} dimensions, not {len(qs)}, {len(ks)} and {len(vs)}")
+    H, Hk, Dk, Dv = vs[-2], qs[-2], qs[-1], vs[-1]
+    _rows_tensor(q, "q", q, qs)
+    _rows_tensor(k, "k", q, qs)
+    _rows_tensor(v, "v", q, (*qs[:-2], H, Dv))
+    _plain_tensor(log_decay, "log_decay", torch.float32, (*qs[:-2], H), q.device)
+    _plain_tensor(beta, "beta", torch.float32, (*qs[:-2], H), q.device)
+    if cu_seqlens is None:
+        return qs[0], qs[1], H, Hk, Dk, Dv
+    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+        raise ValueError("cu_seqlens must hold B + 1 values")
+    _plain_tensor(cu_seqlens, "cu_seqlens", torch.int32, cu_seqlens.shape, q.device)
+    return cu_seqlens.numel() - 1, qs[0], H, Hk, Dk, Dv
+
+
+def fftconv_delta_fwd_workspace_bytes(B: int, T: int, H: int, Hk: int, Dk: int, Dv: int, dtype) -> int:
+    return int(_load().fftconv_delta_fwd_workspace_bytes(B, T, H, Hk, Dk, Dv, _dtype_of(dtype)))
+
+
+def fftconv_delta_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor, beta: torch.Tensor,
+                      out: torch.Tensor, scale: float, state_in: torch.Tensor | None = None,
+                      state_out: torch.Tensor | None = None, state_slots: torch.Tensor | None = None,
+                      cu_seqlens: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None) -> None:
+    """out <- gated delta rule over q, k (B, N, Hk, Dk), v (B, N, H, Dv), or packed (T, heads, width) with cu_seqlens.
+
+    log_decay, beta: fp32 (B, N, H).  state_in / state_out: fp32 (B, H, Dk, Dv), or pools of such matrices with
+    state_slots (B) int32.
+    """
+    B, N, H, Hk, Dk, Dv = _delta_shapes(q, k, v, log_decay, beta, cu_seqlens)
+    _rows_tensor(out, "out", q, v.shape)
+    n_slots, device = 0, q.device
+    if state_slots is not None:
+        _plain_tensor(state_slots, "state_slots", torch.int32, (B,), device)
+        pool = state_in if state_in is not None else state_out
+        n_slots = pool.shape[0] if pool is not None else 0
+    states = (B if state_slots is None else n_slots, H, Dk, Dv)
+    _plain_tensor(state_in, "state_in", torch.float32, states, device)
+    _plain_tensor(state_out, "state_out", torch.float32, states, device)
+    _dev_tensor(workspace, "workspace")
+    with _on(device):
+        _check((_lib or _load()).fftconv_delta_fwd(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), beta.data_ptr(), out.data_ptr(),
+            _strides((q, k, v, out), cu_seqlens is not None), _at(state_in), _at(state_out), _at(state_slots), n_slots,
+            _at(cu_seqlens), B, N, H, Hk, Dk, Dv, scale, _DTYPE_CODE[q.dtype], _at(workspace), _nbytes(workspace),
+            _raw_stream(stream, device)))
+
+
+def fftconv_delta_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor, beta: torch.Tensor,
+                       state: torch.Tensor, out: torch.Tensor, scale: float, state_slots: torch.Tensor | None = None,
+                       stream=None) -> None:
+    """One token of each sequence: q, k (B, Hk, Dk), v (B, H, Dv), log_decay, beta (B, H) -> out, state in place."""
+    if q.dim() != 3 or v.dim() != 3:
+        raise ValueError("q and v must have 3 dimensions")
+    (B, Hk, Dk), (_, H, Dv), device = q.shape, v.shape, q.device
+    _rows_tensor(q, "q", q, (B, Hk, Dk))
+    _rows_tensor(k, "k", q, (B, Hk, Dk))
+    _rows_tensor(v, "v", q, (B, H, Dv))
+    _rows_tensor(out, "out", q, (B, H, Dv))
+    _plain_tensor(log_decay, "log_decay", torch.float32, (B, H), device)
+    _plain_tensor(beta, "beta", torch.float32, (B, H), device)
+    n_slots = 0
+    if state_slots is not None:
+        _plain_tensor(state_slots, "state_slots", torch.int32, (B,), device)
+        n_slots = state.shape[0]
+    _plain_tensor(state, "state", torch.float32, (B if state_slots is None else n_slots, H, Dk, Dv), device)
+    strides = None
+    if not (q.is_contiguous() and k.is_contiguous() and v.is_contiguous() and out.is_contiguous()):
+        strides = _strides_of[8](*q.stride()[:2], *k.stride()[:2], *v.stride()[:2], *out.stride()[:2])
+    with _on(device):
+        _check((_lib or _load()).fftconv_delta_step(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), beta.data_ptr(), state.data_ptr(),
+            out.data_ptr(), strides, _at(state_slots), n_slots, B, H, Hk, Dk, Dv, scale, _DTYPE_CODE[q.dtype],
+            _raw_stream(stream, device)))
+
+
+def delta_attention(q, k, v, log_decay, beta, scale=None, state_in=None, cu_seqlens=None, stream=None):
+    """Gated delta rule over whole sequences (allocations by torch); returns (out, final states).  scale: Dk^-0.5.
+
+    Packed tokens of no sequence (before cu_seqlens[0], from its last value on) have no result: their rows are not set.
+    """
+    if stream is not None:
+        with torch.cuda.stream(stream):      # the scratch memory and the results are that stream's, too
+            return delta_attention(q, k, v, log_decay, beta, scale, state_in, cu_seqlens)
+    B, N, H, Hk, Dk, Dv = _delta_shapes(q, k, v, log_decay, beta, cu_seqlens)
+    T = N if cu_seqlens is not None else B * N
+    out = torch.empty(v.shape, dtype=q.dtype, device=q.device)
+    state_out = torch.empty((B, H, Dk, Dv), dtype=torch.float32, device=q.device)
+    ws = _scratch(fftconv_delta_fwd_workspace_bytes(B, T, H, Hk, Dk, Dv, q.dtype), q.device)
+    fftconv_delta_fwd(q, k, v, log_decay, beta, out, Dk ** -0.5 if scale is None else scale, state_in, state_out,
+                      cu_seqlens=cu_seqlens, workspace=ws)
+    return out, state_out
 
 
 # ---------------------------------------------------------------- root-mean-square norm

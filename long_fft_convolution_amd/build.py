@@ -17,9 +17,9 @@ CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "libfftconv.so")
 BUILD_DIR = os.path.join(HERE, "_build")
 
-SOURCES = ["multipass.hip", "pair16k.hip", "pair_mfma.hip", "decay_f32.hip", "decay_bf16.hip", "decay_f16.hip",
+SOURCES = ["delta_f32.hip", "delta_bf16.hip", "delta_f16.hip", "multipass.hip", "pair16k.hip", "pair_mfma.hip", "decay_f32.hip", "decay_bf16.hip", "decay_f16.hip",
            "linear_bf16.hip", "linear_f16.hip", "linear_f32.hip", "fused.hip", "eqlinear.hip", "bwd.hip", "filter.hip",
-           "norm.hip", "api.cpp", "sequence_ops.cpp", "norm_ops.cpp"]   # the longest compilations first
+           "norm.hip", "api.cpp", "sequence_ops.cpp", "norm_ops.cpp", "delta_ops.cpp"]   # the longest compilations first
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

@@ -1,0 +1,6 @@
+// delta_f16.hip -- the delta-attention kernels (delta_kernels.hpp) for f16 storage.
+#include "delta_kernels.hpp"
+
+namespace fftconv {
+FFTCONV_DELTA_TYPE(f16, _Float16)
+}  // namespace fftconv

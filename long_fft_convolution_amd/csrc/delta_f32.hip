@@ -1,0 +1,6 @@
+// delta_f32.hip -- the delta-attention kernels (delta_kernels.hpp) for f32 storage.
+#include "delta_kernels.hpp"
+
+namespace fftconv {
+FFTCONV_DELTA_TYPE(f32, float)
+}  // namespace fftconv

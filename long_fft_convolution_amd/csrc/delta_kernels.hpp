@@ -1,0 +1,913 @@
+// delta_kernels.hpp -- the gated delta rule: prompts, gradients and single
+// tokens.  Instantiated per storage type by delta_f16.hip, delta_bf16.hip and
+// delta_f32.hip.
+//
+// Mathematics.  Per sequence and head, with a_t = exp(log_decay_t) and an
+// fp32 state S (Dk x Dv),
+//
+//     w_t = v_t - a_t S_{t-1}^T k_t,  u_t = beta_t w_t,  S_t = a_t S_{t-1} + k_t u_t^T,  out_t = scale S_t^T q_t.
+//
+// Over a chunk of C = 64 tokens that starts from S, with G_i the sum of the
+// logarithms up to token i of the chunk, C_ij = exp(G_i - G_j) k_i . k_j for
+// j < i and P_ij = scale exp(G_i - G_j) q_i . k_j for j <= i,
+//
+//     r_i = v_i - exp(G_i) S^T k_i,   (I + C diag(beta)) w = r,   u = beta w,
+//     out_i = scale exp(G_i) S^T q_i + sum_j P_ij u_j,
+//     S <- exp(G_last) S + sum_j k_j (exp(G_last - G_j) u_j)^T.
+//
+// The inverse of I + C diag(beta) and P need no state: a first kernel computes
+// them for all chunks at once (delta_prepare_kernel).  What is left is serial
+// over the chunks and independent over the state's columns: one workgroup of
+// four waves walks one (sequence or segment, head, 64 or 128 columns), each
+// wave with its columns of S in its accumulators for the whole walk.  r, w and
+// u never leave the registers: the accumulators of a product over tokens are
+// the next product's operand when its contraction index is met in the order
+// token(slot 8 g + j) = 32 s + 16 (j / 4) + 4 g + j % 4, which is the order the
+// inverse and P are stored in.  Only k, q, v come through LDS.
+//
+// A call with few (sequence, head) pairs cuts sequences into segments.  A
+// segment is an affine map of the state before it, so a first walk finds its
+// own sum (from a zero state) and its map (from the unit matrix, without
+// values: Dk more columns), a small kernel chains them into the state before
+// each segment, and the walk with outputs starts from there.
+//
+// Rounding.  The state is an fp32 result over the whole sequence, so nothing
+// on its way may lose: all operands are exact sums of bf16 terms (an fp32
+// value: three, fp16: two, bf16: itself) and the products of terms i + j < 3
+// are taken, which drops 2^-24 of a product.  bf16 terms have fp32's range, so
+// nothing is scaled, fp16 included, and bf16 products are the fastest there
+// are.  Outputs in 16 bits see the state and u in two terms (2^-16) and P in
+// one (bf16: 2^-9, half an output rounding) or two (fp16).  The sums G are
+// 64 bits: behind a token that clears the state (a logarithm below -104, exp
+// = 0) the differences of the tokens that follow keep all their bits.
+#pragma once
+
+#include "delta_ops.hpp"
+#include "sequence_device.hpp"
+
+namespace fftconv {
+
+constexpr int kC = kDeltaChunk;
+typedef Mma<__bf16>::v8 bf8;
+
+// ---- sequences, chunks, segments -------------------------------------------
+struct Tokens {
+    int64_t seq, start, len;     // sequence, its first token, its length
+    int64_t unit;                // chunk or segment of it
+    int64_t row0, batch;         // tensors start at (batch, row0)
+};
+__device__ __forceinline__ void sequence_bounds(const DeltaArgs &a, int64_t b, int64_t &start, int64_t &len) {
+    if (!a.cu) {
+        start = 0, len = a.N;
+        return;
+    }
+    // bounds come from device memory: clamped to the tokens there are
+    int64_t s = a.cu[b], e = a.cu[b + 1];
+    s = s < 0 ? 0 : (s > a.N ? a.N : s);
+    e = e < s ? s : (e > a.N ? a.N : e);
+    start = s, len = e - s;
+}
+// Place of sequence b's first unit of `length` tokens.  Packed sequences: no two meet, since
+// start / length + ceil(len / length) <= (start + len) / length + 1; an empty one has a place of its own too.
+__device__ __forceinline__ int64_t first_place(const DeltaArgs &a, int64_t b, int64_t length) {
+    if (!a.cu) return b * (a.N > 0 ? (a.N + length - 1) / length : 1);
+    int64_t start, len;
+    sequence_bounds(a, b, start, len);
+    return start / length + b;
+}
+// The sequence and unit at a place; false when there is none.  An empty sequence has unit 0.
+__device__ __forceinline__ bool unit_at(const DeltaArgs &a, int64_t place, int64_t length, Tokens &t) {
+    int64_t lo = 0, hi = a.B - 1;
+    if (!a.cu) {
+        const int64_t per = a.N > 0 ? (a.N + length - 1) / length : 1;
+        lo = place / per;
+        if (lo >= a.B) return false;
+    } else {
+        while (lo < hi) {
+            const int64_t mid = (lo + hi + 1) / 2;
+            if (first_place(a, mid, length) <= place) lo = mid;
+            else hi = mid - 1;
+        }
+    }
+    t.seq = lo;
+    sequence_bounds(a, lo, t.start, t.len);
+    t.unit = place - first_place(a, lo, length);
+    t.row0 = a.cu ? t.start : 0;
+    t.batch = a.cu ? 0 : t.seq;
+    return t.unit >= 0 && (t.unit == 0 || t.unit * length < t.len);
+}
+__device__ __forceinline__ void make_scalar(Tokens &t) {
+    t.seq = scalar(t.seq), t.start = scalar(t.start), t.len = scalar(t.len), t.unit = scalar(t.unit);
+    t.row0 = scalar(t.row0), t.batch = scalar(t.batch);
+}
+
+// ---- operands ---------------------------------------------------------------
+// exact bf16 terms of a storage value, and of the masked products
+template <typename T> struct Terms;
+template <> struct Terms<__bf16> { static constexpr int kIn = 1, kOut = 2, kP = delta_terms(2, false); };
+template <> struct Terms<_Float16> { static constexpr int kIn = 2, kOut = 2, kP = delta_terms(2, true); };
+template <> struct Terms<float> { static constexpr int kIn = 3, kOut = 3, kP = delta_terms(4, false); };
+
+template <typename T> struct Raw8 { T v[8]; };
+template <typename T> __device__ __forceinline__ void in_terms(const Raw8<T> &x, bf8 (&out)[Terms<T>::kIn]) {
+    if constexpr (sizeof(T) == 2 && Terms<T>::kIn == 1) {
+        out[0] = __builtin_bit_cast(bf8, x);
+    } else {
+        float f[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = (float)x.v[j];
+        split8<__bf16, Terms<T>::kIn>(f, out);
+    }
+}
+// two accumulators of rows 16 (2 s) and 16 (2 s + 1) as the operand over their 32 rows
+template <int N> __device__ __forceinline__ void rows_terms(const f32x4 &a, const f32x4 &b, bf8 (&out)[N]) {
+    float f[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+    if constexpr (N == 1) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) out[0][j] = (__bf16)f[j];
+    } else {
+        split8<__bf16, N>(f, out);
+    }
+}
+// acc += sum of the products of terms i + j < MOST
+template <int MOST, int NA, int NB> __device__ __forceinline__ f32x4 mma_terms(const bf8 (&a)[NA], const bf8 (&b)[NB], f32x4 acc) {
+#pragma unroll
+    for (int i = 0; i < NA; ++i)
+#pragma unroll
+        for (int j = 0; j < NB; ++j)
+            if (i + j < MOST) acc = Mma<__bf16>::mma(a[i], b[j], acc);
+    return acc;
+}
+
+// exp of a 64-bit difference to fp32 precision: the part that fp32 does not hold as a factor 1 + lo
+__device__ __forceinline__ float exp_of(double d) {
+    const float hi = (float)d, lo = (float)(d - (double)hi);
+    const float e = expf(hi);
+    return __builtin_fmaf(e, lo, e);
+}
+
+// 8 values of a row at byte offset `at` (or kSkip), of which `left` exist
+template <typename T, bool VEC> __device__ __forceinline__ Raw8<T> load_row8(__amdgpu_buffer_rsrc_t view, uint32_t at, int left) {
+    Raw8<T> r;
+    if constexpr (VEC) {
+        const uint32_t o = left > 0 ? at : kSkip;
+        if constexpr (sizeof(T) == 2) {
+            r = __builtin_bit_cast(Raw8<T>, view_load_wide<u32x4>(view, o));
+        } else {
+            const u32x4 a = view_load_wide<u32x4>(view, o), b = view_load_wide<u32x4>(view, left > 4 && o != kSkip ? o + 16 : kSkip);
+            __builtin_memcpy(&r, &a, 16);
+            __builtin_memcpy(reinterpret_cast<char *>(&r) + 16, &b, 16);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) r.v[j] = view_load<T>(view, ((j < left) & (at != kSkip)) ? at + j * (uint32_t)sizeof(T) : kSkip);
+    }
+    return r;
+}
+
+// Ends a wave's LDS writes before its reads of them by other lanes.
+__device__ __forceinline__ void wave_sync() {
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_wave_barrier();
+}
+
+// ---- the part without state ---------------------------------------------------
+constexpr int kLd = kC + 4;      // row stride of a 64 x 64 matrix in LDS: 16-byte rows, columns on all banks
+
+// M (strictly lower, 64 x 64 in LDS) <- (I + M)^-1, lower blocks of 16; the blocks above the diagonal are left.
+// Diagonal blocks by forward substitution, a column a lane; the others, row of blocks by row, as
+// -T_ii sum_k M_ik T_kj on the fp32 matrix cores.
+__device__ __forceinline__ void invert_unit_lower(float *M) {
+    const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
+    {
+        const float *block = M + g * 16 * kLd + g * 16;
+        float t[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            float s = i == c ? 1.0f : 0.0f;
+#pragma unroll
+            for (int j4 = 0; j4 < i; j4 += 4) {
+                const f32x4 m = *reinterpret_cast<const f32x4 *>(block + i * kLd + j4);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (j4 + j < i) s -= m[j] * t[j4 + j];
+            }
+            t[i] = s;
+        }
+        wave_sync();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) M[(g * 16 + i) * kLd + g * 16 + c] = t[i];
+        wave_sync();
+    }
+    auto row4 = [&](int i, int k) { return *reinterpret_cast<const f32x4 *>(M + (16 * i + c) * kLd + 16 * k + 4 * g); };
+#pragma unroll
+    for (int i = 1; i < 4; ++i) {
+        f32x4 x[3];
+#pragma unroll
+        for (int j = 0; j < i; ++j) {
+            x[j] = f32x4{0, 0, 0, 0};
+#pragma unroll
+            for (int k = j; k < i; ++k) {
+                const f32x4 m = row4(i, k);
+#pragma unroll
+                for (int s = 0; s < 4; ++s)
+                    x[j] = __builtin_amdgcn_mfma_f32_16x16x4f32(m[s], M[(16 * k + 4 * g + s) * kLd + 16 * j + c], x[j], 0, 0, 0);
+            }
+        }
+        const f32x4 d = row4(i, i);
+        wave_sync();
+#pragma unroll
+        for (int j = 0; j < i; ++j) {
+            f32x4 t = f32x4{0, 0, 0, 0};
+#pragma unroll
+            for (int s = 0; s < 4; ++s) t = __builtin_amdgcn_mfma_f32_16x16x4f32(d[s], x[j][s], t, 0, 0, 0);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) M[(16 * i + 4 * g + r) * kLd + 16 * j + c] = -t[r];
+        }
+        wave_sync();
+    }
+}
+
+// One wave a (chunk, head): record of the chunk.  grid: chunks * H / 4.  Bound by latency: products, the inverse's
+// 16 serial steps and LDS round trips; eight waves a CU overlap them.
+template <typename T, int DXP, bool VEC> __global__ __launch_bounds__(256) void delta_prepare_kernel(const DeltaArgs a) {
+    constexpr int KX = DXP / 32, NP = Terms<T>::kP;
+    __shared__ __attribute__((aligned(16))) float matrix[4][kC * kLd];
+    __shared__ double sums[4][kC];
+    __shared__ float betas[4][kC];
+    const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t item = blockIdx.x * (int64_t)4 + wave;
+    if (item >= a.chunks * a.H) return;
+    const int64_t place = item / a.H;
+    const int h = (int)(item % a.H);
+    Tokens t;
+    if (!unit_at(a, place, kC, t)) return;
+    make_scalar(t);
+    const int64_t t0 = t.unit * kC;
+    const int n = t.len - t0 < kC ? (int)(t.len - t0) : kC;
+    if (n <= 0) return;
+    float *M = matrix[wave];
+    double *G = sums[wave];
+    float *beta = betas[wave];
+
+    // a token a lane: sums of the logarithms, weights
+    const int64_t gate = (t.batch * a.N + t.row0 + t0 + lane) * a.H + h;
+    float own = lane < n ? a.log_decay[gate] : 0.0f;
+    own = own < -128.0f ? -128.0f : own;       // exp of either is 0 in fp32, and the sums stay finite
+    const float b = lane < n ? a.beta[gate] : 0.0f;
+    double sum = own;
+#pragma unroll
+    for (int s = 1; s < 64; s <<= 1) {
+        const double up = __shfl_up(sum, s);
+        if (lane >= s) sum += up;
+    }
+    const double last = __shfl(sum, 63);
+    G[lane] = sum;
+    beta[lane] = b;
+    char *rec = a.rec + item * (int64_t)(delta_pieces(NP) * 1024);
+    {
+        float *vec = reinterpret_cast<float *>(rec + kDeltaInverse * 1024);
+        const float first = exp_of(sum);
+        vec[lane] = first;
+        vec[64 + lane] = exp_of(last - sum);
+        vec[128 + lane] = b;
+        vec[192 + lane] = a.scale * first;
+    }
+    wave_sync();
+
+    // products of keys (rows i, columns j <= i) and of keys with queries (rows j, columns i)
+    f32x4 kk[10], qk[10];
+#pragma unroll
+    for (int i = 0; i < 10; ++i) kk[i] = qk[i] = f32x4{0, 0, 0, 0};
+    {
+        const T *k0 = static_cast<const T *>(a.k) + t.batch * a.kb + (t.row0 + t0) * a.kt + (h / a.group) * a.kh;
+        const T *q0 = static_cast<const T *>(a.q) + t.batch * a.qb + (t.row0 + t0) * a.qt + (h / a.group) * a.qh;
+        const auto kv = wide_view(k0), qv = wide_view(q0);
+#pragma unroll 1
+        for (int s = 0; s < KX; ++s) {
+            const int col = s * 32 + g * 8, left = a.Dk - col;
+            bf8 kf[4][Terms<T>::kIn], qf[4][Terms<T>::kIn];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int row = 16 * r + c;
+                in_terms(load_row8<T, VEC>(kv, row < n ? (uint32_t)((row * a.kt + col) * (int64_t)sizeof(T)) : kSkip, row < n ? left : 0), kf[r]);
+                in_terms(load_row8<T, VEC>(qv, row < n ? (uint32_t)((row * a.qt + col) * (int64_t)sizeof(T)) : kSkip, row < n ? left : 0), qf[r]);
+            }
+#pragma unroll
+            for (int i = 0, at = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j <= i; ++j, ++at) {
+                    kk[at] = mma_terms<3>(kf[i], kf[j], kk[at]);
+                    qk[at] = mma_terms<3>(kf[j], qf[i], qk[at]);
+                }
+        }
+    }
+    // C diag(beta) into LDS
+#pragma unroll
+    for (int i = 0, at = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j <= i; ++j, ++at)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int row = 16 * i + 4 * g + r, col = 16 * j + c;
+                M[row * kLd + col] = col < row ? kk[at][r] * exp_of(G[row] - G[col]) * beta[col] : 0.0f;
+            }
+    wave_sync();
+    invert_unit_lower(M);
+    f32x4 *out = reinterpret_cast<f32x4 *>(rec);
+    bf8 *outp = reinterpret_cast<bf8 *>(rec + (kDeltaInverse + kDeltaVectors) * 1024);
+#pragma unroll
+    for (int i = 0, e = 0; i < 4; ++i)
+#pragma unroll
+        for (int s = 0; s <= i / 2; ++s, ++e) {
+            float p[8];
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const int j = 2 * s + half;      // block of columns
+                out[(e * 2 + half) * 64 + lane] =
+                    j <= i ? *reinterpret_cast<const f32x4 *>(M + (16 * i + c) * kLd + 16 * j + 4 * g) : f32x4{0, 0, 0, 0};
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int row = 16 * i + c, col = 16 * j + 4 * g + r;
+                    const f32x4 x = qk[j <= i ? i * (i + 1) / 2 + j : 0];
+                    p[half * 4 + r] = ((j <= i) & (col <= row)) ? x[r] * a.scale * exp_of(G[row] - G[col <= row ? col : row]) : 0.0f;
+                }
+            }
+            bf8 terms[NP];
+            rows_terms<NP>(f32x4{p[0], p[1], p[2], p[3]}, f32x4{p[4], p[5], p[6], p[7]}, terms);
+#pragma unroll
+            for (int u = 0; u < NP; ++u) outp[(e * NP + u) * 64 + lane] = terms[u];
+        }
+}
+
+// ---- tiles in LDS ------------------------------------------------------------
+// 64 rows of DP values in 16-byte slots, slot s of row r lying at s ^ f(r): eight neighbouring rows of a slot, and
+// four rows of four neighbouring slots, then lie on different banks.
+template <typename T, int DP> struct RowTile {
+    static constexpr int E = 16 / (int)sizeof(T), PR = DP / E, N = kC * PR / 256, BYTES = kC * DP * (int)sizeof(T);
+    static_assert(kC * PR % 256 == 0 && PR % 8 == 0, "whole loads");
+    static __device__ __forceinline__ int f(int row) { return (row & 1) << 2 | (row & 2) | ((row >> 2) & 1); }
+    static __device__ __forceinline__ const T *at(const T *tile, int row, int slot) { return tile + (row * PR + (slot ^ f(row))) * E; }
+    // 8 values of a row at column col (a multiple of 8)
+    static __device__ __forceinline__ Raw8<T> row8(const T *tile, int row, int col) {
+        Raw8<T> r;
+        if constexpr (sizeof(T) == 2) {
+            r = *reinterpret_cast<const Raw8<T> *>(__builtin_assume_aligned(at(tile, row, col / 8), 16));
+        } else {
+            const f32x4 a = *reinterpret_cast<const f32x4 *>(at(tile, row, col / 4)), b = *reinterpret_cast<const f32x4 *>(at(tile, row, col / 4 + 1));
+            __builtin_memcpy(&r, &a, 16);
+            __builtin_memcpy(reinterpret_cast<char *>(&r) + 16, &b, 16);
+        }
+        return r;
+    }
+    // Rows row0 .. row0 + 3 of this lane's own column, mine; row0 may differ between the wave's four groups of 16
+    // lanes.  16 bits: a transposing read, in which 16 lanes read four rows of four 4-column groups and lane c
+    // receives column c % 4 of group c / 4; group is the first column of the one that lanes of this c % 4 read.
+    static __device__ __forceinline__ void col4(const T *tile, int row0, int group, int mine, T *out) {
+        if constexpr (sizeof(T) == 2) {
+            const T *p = at(tile, row0 + ((threadIdx.x & 15) >> 2), group / 8) + group % 8;
+            const s16x4 v = __builtin_bit_cast(s16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16(FFTCONV_LDS_CAST(s16x4, p)));
+            __builtin_memcpy(out, &v, 8);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) out[j] = at(tile, row0 + j, mine / 4)[mine % 4];
+        }
+    }
+    // rows of the operand over tokens 32 s .. 32 s + 31
+    static __device__ __forceinline__ Raw8<T> col8(const T *tile, int s, int group, int mine) {
+        const int g = (threadIdx.x & 63) >> 4;
+        Raw8<T> r;
+        col4(tile, 32 * s + 4 * g, group, mine, r.v);
+        col4(tile, 32 * s + 16 + 4 * g, group, mine, r.v + 4);
+        return r;
+    }
+};
+// Brings a tensor's rows into a tile: VEC by LDS-destination loads (what lies outside the chunk or the columns reads
+// zero by the buffer unit's range check), else value by value.
+template <typename T, int DP, bool VEC> struct RowSource {
+    using Tile = RowTile<T, DP>;
+    const T *p;            // the sequence's first row
+    int64_t stride;
+    int cols, col0;
+    __device__ __forceinline__ void init(const void *base, int64_t off, int64_t st, int cols_, int col0_) {
+        p = static_cast<const T *>(base) + off;
+        stride = st, cols = cols_, col0 = col0_;
+    }
+    // n of the rows from token t on; the rest of the tile becomes zero
+    __device__ __forceinline__ void bring(int64_t t, int n, T *tile) const {
+        const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        const T *first = p + t * stride;
+#pragma unroll
+        for (int i = 0; i < Tile::N; ++i) {
+            const int idx = i * 256 + threadIdx.x, row = idx / Tile::PR, slot = idx % Tile::PR ^ Tile::f(row);
+            const int col = col0 + slot * Tile::E;
+            const uint32_t at = (uint32_t)((row * stride + col) * (int64_t)sizeof(T));
+            if constexpr (VEC) {
+                lds_load16(first, tile + (i * 256 + wave * 64) * Tile::E, ((row < n) & (col < cols)) ? at : kSkip);
+            } else {
+                const auto view = wide_view(first);
+                T e[Tile::E];
+#pragma unroll
+                for (int j = 0; j < Tile::E; ++j)
+                    e[j] = view_load<T>(view, ((row < n) & (col + j < cols)) ? at + j * (uint32_t)sizeof(T) : kSkip);
+                __builtin_memcpy(tile + idx * Tile::E, e, 16);
+            }
+        }
+    }
+};
+// `pieces` KB of a record (a multiple of four) as they are
+template <bool VEC> __device__ __forceinline__ void bring_record(const char *rec, int pieces, char *dst) {
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    for (int i = wave; i < pieces; i += 4) {
+        if constexpr (VEC) lds_load16(rec, dst + i * 1024, (uint32_t)(i * 1024 + lane * 16));
+        else *reinterpret_cast<f32x4 *>(dst + i * 1024 + lane * 16) = *reinterpret_cast<const f32x4 *>(rec + i * 1024 + lane * 16);
+    }
+}
+
+// ---- the state in a wave's accumulators ------------------------------------------
+// S[kk][r][t]: rows kk * 32 + g * 8 + r * 4 + i, column column(c, t) of the wave: as an operand over rows, lane
+// (g, c) holds the slots 8 g + j of its column.
+template <int KX, int NT> struct State {
+    f32x4 v[KX][2][NT];
+    template <typename F> __device__ __forceinline__ void each(F &&f) {
+#pragma unroll
+        for (int kk = 0; kk < KX; ++kk)
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        v[kk][r][t][i] = f(kk * 32 + (int)((threadIdx.x & 63) >> 4) * 8 + r * 4 + i, t, v[kk][r][t][i]);
+    }
+    // of a row-major matrix of rows x cols (null: zeros)
+    template <typename C> __device__ __forceinline__ void load(const float *p, int rows, int cols, C &&column) {
+        const auto view = wide_view(p);
+        each([&](int row, int t, float) __attribute__((always_inline)) {
+            const int col = column(t);
+            return view_load<float>(view, ((p != nullptr) & (row < rows) & (col < cols)) ? (uint32_t)(row * cols + col) * 4u : kSkip);
+        });
+    }
+    template <typename C> __device__ __forceinline__ void store(float *p, int rows, int cols, C &&column) {
+        const auto view = wide_view(p);
+        each([&](int row, int t, float x) __attribute__((always_inline)) {
+            const int col = column(t);
+            view_store(view, ((row < rows) & (col < cols)) ? (uint32_t)(row * cols + col) * 4u : kSkip, x);
+            return x;
+        });
+    }
+    __device__ __forceinline__ void terms(int kk, int t, bf8 (&out)[3]) const {
+        float f[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = v[kk][j >> 2][t][j & 3];
+        split8<__bf16, 3>(f, out);
+    }
+};
+
+// Work item of workgroup id: ids go to the 8 XCDs in turn, so runs of `run` items are dealt to one XCD, whose L2
+// then holds what they have in common.
+__device__ __forceinline__ uint32_t dealt(uint32_t id, uint32_t run) {
+    const uint32_t round = id / (8 * run), in = id % (8 * run);
+    return (round * 8 + in % 8) * run + in / 8;
+}
+inline __host__ __device__ int delta_run(int tiles, int group) {
+    const int n = tiles * group;
+    return n < 16 ? n : 16;
+}
+
+// MODE kDeltaSums: a segment's own sum and map, of those that another follows; kDeltaOut: outputs.
+enum DeltaMode : int { kDeltaSums = 0, kDeltaOut = 1 };
+
+template <typename T, int DXP, int NT, int MODE, bool VEC> struct WalkShape {
+    static constexpr bool OUT = MODE == kDeltaOut;
+    static constexpr int DZT = NT * 64;
+    using TX = RowTile<T, DXP>;
+    using TZ = RowTile<T, DZT>;
+    static constexpr int kQ = TX::BYTES, kV = (OUT ? 2 : 1) * TX::BYTES, kRec = kV + TZ::BYTES;
+    // the masked products stay in memory where LDS has no room for them (fp32 rows wider than 128)
+    static constexpr bool kProducts = OUT && kRec + delta_pieces(Terms<T>::kP) * 1024 <= 160 * 1024;
+    static constexpr int kPieces = kProducts ? delta_pieces(Terms<T>::kP) : 16, kBytes = kRec + kPieces * 1024;
+    static constexpr int kStages = VEC && 2 * kBytes <= 156 * 1024 ? 2 : 1;
+    static_assert(kBytes <= 160 * 1024, "LDS");
+};
+
+template <typename T, int DXP, int NT, int MODE, bool VEC>
+__global__ __launch_bounds__(256, 1) void delta_walk_kernel(const DeltaArgs a, int ztiles, int tiles) {
+#ifdef __HIP_DEVICE_COMPILE__   // the host pass, which cannot take the scalar operands, needs the stub alone
+    using W = WalkShape<T, DXP, NT, MODE, VEC>;
+    constexpr bool OUT = W::OUT;
+    constexpr int KX = DXP / 32, DZT = W::DZT, NIN = Terms<T>::kIn, NOUT = Terms<T>::kOut, NP = Terms<T>::kP;
+    using TX = typename W::TX;
+    using TZ = typename W::TZ;
+    __shared__ __attribute__((aligned(1024))) char lds[W::kStages * W::kBytes];
+
+    uint32_t w = dealt(blockIdx.x, delta_run(tiles, a.group));
+    const int tile = w % tiles;
+    w /= tiles;
+    const int h = w % a.H;
+    const int64_t place = w / a.H;
+    if (place >= a.segs) return;
+    Tokens tk;
+    if (!unit_at(a, place, a.seg_chunks * kC, tk)) return;
+    make_scalar(tk);
+    const int64_t chunks = (tk.len + kC - 1) / kC, first = tk.unit * a.seg_chunks;
+    const int64_t end = first + a.seg_chunks < chunks ? first + a.seg_chunks : chunks;
+    const bool last = end >= chunks;
+    if (!OUT && last) return;
+    const bool map = !OUT && tile >= ztiles;           // this workgroup's columns are the map's
+    const int cols = map ? a.Dk : a.Dv, col0 = (map ? tile - ztiles : tile) * DZT;
+    const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), zw = wave * NT * 16;
+    // column of accumulator column m of tile t (NT = 2: a lane's two tiles of outputs hold 8 neighbours)
+    auto zcol = [&](int m, int t) { return zw + (NT == 2 ? (m >> 2) * 8 + t * 4 + (m & 3) : m); };
+    auto zgroup = [&](int t) { return zw + (lane & 3) * (NT * 4) + t * 4; };
+    auto column = [&](int t) { return col0 + zcol(c, t); };
+
+    RowSource<T, DXP, VEC> src_k, src_q;
+    RowSource<T, DZT, VEC> src_v;
+    const int hk = h / a.group;
+    src_k.init(a.k, tk.batch * a.kb + tk.row0 * a.kt + hk * a.kh, a.kt, a.Dk, 0);
+    if (OUT) src_q.init(a.q, tk.batch * a.qb + tk.row0 * a.qt + hk * a.qh, a.qt, a.Dk, 0);
+    src_v.init(a.v, tk.batch * a.vb + tk.row0 * a.vt + h * a.vh, a.vt, map ? 0 : a.Dv, col0);
+    const char *rec0 = a.rec + (first_place(a, tk.seq, kC) * a.H + h) * (int64_t)(delta_pieces(NP) * 1024);
+    const int64_t rec_step = (int64_t)a.H * delta_pieces(NP) * 1024;
+    auto bring = [&](int64_t ch, char *stage) __attribute__((always_inline)) {
+        const int64_t t = ch * kC;
+        const int n = tk.len - t < kC ? (int)(tk.len - t) : kC;
+        src_k.bring(t, n, reinterpret_cast<T *>(stage));
+        if (OUT) src_q.bring(t, n, reinterpret_cast<T *>(stage + W::kQ));
+        src_v.bring(t, n, reinterpret_cast<T *>(stage + W::kV));
+        bring_record<VEC>(rec0 + ch * rec_step, W::kPieces, stage + W::kRec);
+    };
+    if (W::kStages == 2 && first < end) bring(first, lds);
+
+    State<KX, NT> S;
+    const int64_t nst = (int64_t)a.Dk * a.Dv;
+    {
+        const float *p = nullptr;
+        if (OUT && a.seg_state && tk.unit > 0) {
+            p = a.seg_state + (place * a.H + h) * nst;
+        } else if (OUT && a.state0) {
+            const int64_t slot = state_slot(a.slots, a.n_slots, tk.seq);
+            if (slot >= 0) p = a.state0 + (slot * a.H + h) * nst;
+        }
+        S.load(p, a.Dk, cols, column);
+        if (map) S.each([&](int row, int t, float) __attribute__((always_inline)) { return row == column(t) ? 1.0f : 0.0f; });
+    }
+    const int out_cols = a.Dv - (col0 + zw + g * NT * 4);       // of this lane's first column of the output on
+    T *out0 = OUT ? static_cast<T *>(a.out) + tk.batch * a.ob + tk.row0 * a.ot + h * a.oh : nullptr;
+
+    for (int64_t ch = first; ch < end; ++ch) {
+        char *stage = lds;
+        if constexpr (W::kStages == 2) {
+            stage += ((ch - first) & 1) * W::kBytes;
+            // This chunk's loads were issued a chunk ago; four stores followed them (16-bit outputs).  The wait on LDS
+            // reads keeps every wave's reads of the other stage before the loads into it.
+            if (OUT && sizeof(T) == 2 && ch > first) wait_loads_and_barrier<4>();
+            else wait_loads_and_barrier<0>();
+            if (ch + 1 < end) bring(ch + 1, lds + ((ch + 1 - first) & 1) * W::kBytes);
+        } else {
+            __syncthreads();
+            bring(ch, stage);
+            wait_loads_and_barrier<0>();
+        }
+        const T *tk_ = reinterpret_cast<const T *>(stage), *tq = reinterpret_cast<const T *>(stage + W::kQ),
+                *tv = reinterpret_cast<const T *>(stage + W::kV);
+        const f32x4 *inv = reinterpret_cast<const f32x4 *>(stage + W::kRec);
+        const float *vec = reinterpret_cast<const float *>(stage + W::kRec + kDeltaInverse * 1024);
+        const bf8 *prod = reinterpret_cast<const bf8 *>((W::kProducts ? stage + W::kRec : rec0 + ch * rec_step) + (kDeltaInverse + kDeltaVectors) * 1024);
+
+        // k S, and the state's part of the outputs
+        f32x4 x[4][NT], o[4][NT];
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+            for (int t = 0; t < NT; ++t) x[r][t] = o[r][t] = f32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int kk = 0; kk < KX; ++kk) {
+            bf8 st[NT][3];
+#pragma unroll
+            for (int t = 0; t < NT; ++t) S.terms(kk, t, st[t]);
+            bf8 kf[4][NIN];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) in_terms(TX::row8(tk_, 16 * r + c, kk * 32 + g * 8), kf[r]);
+#pragma unroll
+            for (int i = 0; i < NIN; ++i)
+#pragma unroll
+                for (int j = 0; j < 3; ++j)
+                    if (i + j < 3)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+#pragma unroll
+                            for (int t = 0; t < NT; ++t) x[r][t] = Mma<__bf16>::mma(kf[r][i], st[t][j], x[r][t]);
+            if (OUT) {
+                bf8 qf[4][NIN];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) in_terms(TX::row8(tq, 16 * r + c, kk * 32 + g * 8), qf[r]);
+#pragma unroll
+                for (int i = 0; i < NIN; ++i)
+#pragma unroll
+                    for (int j = 0; j < NOUT; ++j)
+                        if (i + j < NOUT)
+#pragma unroll
+                            for (int r = 0; r < 4; ++r)
+#pragma unroll
+                                for (int t = 0; t < NT; ++t) o[r][t] = Mma<__bf16>::mma(st[t][j], qf[r][i], o[r][t]);
+            }
+        }
+        // r = v - exp(G) k S as operands over tokens
+        bf8 rs[2][NT][3];
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                f32x4 res[2];
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const int row = 32 * s + 16 * half + 4 * g;
+                    T v[4];
+                    TZ::col4(tv, row, zgroup(t), zcol(c, t), v);
+                    const f32x4 f = *reinterpret_cast<const f32x4 *>(vec + row);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) res[half][i] = (float)v[i] - f[i] * x[2 * s + half][t][i];
+                }
+                rows_terms<3>(res[0], res[1], rs[s][t]);
+            }
+        // w = inverse r, u = beta w
+        f32x4 u[4][NT];
+#pragma unroll
+        for (int r = 0, e = 0; r < 4; ++r) {
+#pragma unroll
+            for (int t = 0; t < NT; ++t) u[r][t] = f32x4{0, 0, 0, 0};
+#pragma unroll
+            for (int s = 0; s <= r / 2; ++s, ++e) {
+                bf8 tf[3];
+                rows_terms<3>(inv[e * 128 + lane], inv[e * 128 + 64 + lane], tf);
+#pragma unroll
+                for (int t = 0; t < NT; ++t) u[r][t] = mma_terms<3>(tf, rs[s][t], u[r][t]);
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const f32x4 b = *reinterpret_cast<const f32x4 *>(vec + 128 + 16 * r + 4 * g);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) u[r][t] *= b;
+        }
+        if (OUT) {
+            const int64_t t0 = ch * kC;
+            const int n = tk.len - t0 < kC ? (int)(tk.len - t0) : kC;
+            bf8 us[2][NT][NOUT];
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+#pragma unroll
+                for (int t = 0; t < NT; ++t) rows_terms<NOUT>(u[2 * s][t], u[2 * s + 1][t], us[s][t]);
+            const auto view = wide_view(out0 + t0 * a.ot);
+#pragma unroll
+            for (int r = 0, e = 0; r < 4; ++r) {
+                const float f = vec[192 + 16 * r + c];
+#pragma unroll
+                for (int t = 0; t < NT; ++t) o[r][t] *= f;
+#pragma unroll
+                for (int s = 0; s <= r / 2; ++s, ++e) {
+                    bf8 pf[NP];
+#pragma unroll
+                    for (int p = 0; p < NP; ++p) pf[p] = prod[(e * NP + p) * 64 + lane];
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) o[r][t] = mma_terms<NOUT>(us[s][t], pf, o[r][t]);
+                }
+                const int row = 16 * r + c;
+                const uint32_t at = ((row < n) & (out_cols > 0)) ? (uint32_t)((row * a.ot + col0 + zw + g * NT * 4) * (int64_t)sizeof(T)) : kSkip;
+                put_row<T, NT, VEC && sizeof(T) == 2>(view, at, o[r], VEC, out_cols);
+            }
+        }
+        // S <- exp(G_last) S + k^T (exp(G_last - G) u)
+        const float keep = vec[63];
+        bf8 es[2][NT][3];
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            const f32x4 f0 = *reinterpret_cast<const f32x4 *>(vec + 64 + 32 * s + 4 * g),
+                        f1 = *reinterpret_cast<const f32x4 *>(vec + 64 + 32 * s + 16 + 4 * g);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) rows_terms<3>(u[2 * s][t] * f0, u[2 * s + 1][t] * f1, es[s][t]);
+        }
+#pragma unroll
+        for (int kk = 0; kk < KX; ++kk) {
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+#pragma unroll
+                for (int t = 0; t < NT; ++t) S.v[kk][r][t] *= keep;
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                // rows of the state permuted like its operand: row m is kk * 32 + 8 (m / 4) + 4 r + m % 4
+                bf8 kf[2][NIN];
+#pragma unroll
+                for (int r = 0; r < 2; ++r)
+                    in_terms(TX::col8(tk_, s, kk * 32 + (lane & 3) * 8 + r * 4, kk * 32 + (c >> 2) * 8 + r * 4 + (c & 3)), kf[r]);
+#pragma unroll
+                for (int i = 0; i < NIN; ++i)
+#pragma unroll
+                    for (int j = 0; j < 3; ++j)
+                        if (i + j < 3)
+#pragma unroll
+                            for (int r = 0; r < 2; ++r)
+#pragma unroll
+                                for (int t = 0; t < NT; ++t) S.v[kk][r][t] = Mma<__bf16>::mma(kf[r][i], es[s][t][j], S.v[kk][r][t]);
+            }
+        }
+    }
+
+    if (!OUT) {
+        float *p = map ? a.seg_map + (place * a.H + h) * (int64_t)a.Dk * a.Dk : a.seg_state + (place * a.H + h) * nst;
+        S.store(p, a.Dk, cols, column);
+    } else if (a.state1 && last) {
+        const int64_t slot = state_slot(a.slots, a.n_slots, tk.seq);
+        if (slot >= 0) S.store(a.state1 + (slot * a.H + h) * nst, a.Dk, a.Dv, column);
+    }
+#endif
+}
+
+// State before each segment from the segments' own sums and maps, in place of the sums: S <- map S + sum, one
+// workgroup a (sequence, head, 64 columns).  grid (B, H, tiles).
+template <int DXP> static __global__ __launch_bounds__(256, 1) void delta_chain_kernel(const DeltaArgs a) {
+    constexpr int KX = DXP / 32;
+    const int h = blockIdx.y, col0 = blockIdx.z * 64;
+    const int64_t seq = blockIdx.x;
+    int64_t start, len;
+    sequence_bounds(a, seq, start, len);
+    const int64_t length = a.seg_chunks * kC, count = (len + length - 1) / length;
+    if (count < 2) return;
+    const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15, wave = threadIdx.x >> 6;
+    auto column = [&](int) { return col0 + wave * 16 + c; };
+    const int64_t nst = (int64_t)a.Dk * a.Dv, nmap = (int64_t)a.Dk * a.Dk, place0 = first_place(a, seq, length);
+    State<KX, 1> S, sum;
+    {
+        const float *p = nullptr;
+        if (a.state0) {
+            const int64_t slot = state_slot(a.slots, a.n_slots, seq);
+            if (slot >= 0) p = a.state0 + (slot * a.H + h) * nst;
+        }
+        S.load(p, a.Dk, a.Dv, column);
+    }
+    for (int64_t i = 0; i + 1 < count; ++i) {
+        float *own = a.seg_state + ((place0 + i) * a.H + h) * nst;
+        const float *map = a.seg_map + ((place0 + i) * a.H + h) * nmap;
+        sum.load(own, a.Dk, a.Dv, column);
+        const auto view = wide_view(map);
+        bf8 st[KX][3];
+#pragma unroll
+        for (int kk = 0; kk < KX; ++kk) S.terms(kk, 0, st[kk]);
+#pragma unroll
+        for (int kk = 0; kk < KX; ++kk)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const int row = kk * 32 + (c >> 2) * 8 + r * 4 + (c & 3);
+                f32x4 acc = sum.v[kk][r][0];
+#pragma unroll
+                for (int x = 0; x < KX; ++x) {
+                    const int col = x * 32 + g * 8, left = row < a.Dk ? a.Dk - col : 0;
+                    bf8 mf[3];
+                    in_terms(load_row8<float, false>(view, left > 0 ? (uint32_t)(row * a.Dk + col) * 4u : kSkip, left), mf);
+                    acc = mma_terms<3>(mf, st[x], acc);
+                }
+                sum.v[kk][r][0] = acc;
+            }
+        if (i > 0) S.store(own, a.Dk, a.Dv, column);
+        S = sum;
+    }
+    S.store(a.seg_state + ((place0 + count - 1) * a.H + h) * nst, a.Dk, a.Dv, column);
+}
+
+// The single-token form.  One workgroup a (sequence, head, LANES * VEC columns), LANES lanes along a row of the state,
+// 256 / LANES groups of rows; the rows stay in registers between the products with k and q (which are taken of the
+// state before the token: out = scale (a S^T q + (q . k) u)) and the update.  Bound by the state, which is read and
+// written once.
+template <typename T, int VEC, int LANES, int ROWS>
+__global__ __launch_bounds__(256) void delta_step_kernel(const DeltaStep a) {
+    constexpr int RG = 256 / LANES, W = LANES * VEC;
+    static_assert(ROWS * RG <= 256 && W <= 256, "a row and a column a thread");
+    __shared__ float sq[256], sk[256];
+    __shared__ float part[2][RG][W];
+    __shared__ float both[4];
+    __shared__ float u[W];
+    const int tid = threadIdx.x, lc = tid % LANES, rg = tid / LANES;
+    const int64_t b = blockIdx.x / a.H;
+    const int h = blockIdx.x % a.H, hk = h / a.group;
+    const int dv0 = (blockIdx.y * LANES + lc) * VEC;
+    const T *q = static_cast<const T *>(a.q) + b * a.qb + hk * a.qh;
+    const T *k = static_cast<const T *>(a.k) + b * a.kb + hk * a.kh;
+    const T *v = static_cast<const T *>(a.v) + b * a.vb + h * a.vh;
+    const int64_t slot = state_slot(a.slots, a.n_slots, b);
+    typedef float vec __attribute__((ext_vector_type(VEC)));
+    const bool live = dv0 < a.Dv && slot >= 0;   // VEC divides Dv
+    float *s = live ? a.state + (slot * a.H + h) * (int64_t)a.Dk * a.Dv + dv0 : nullptr;
+    vec e[ROWS];
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+        const int r = i * RG + rg;
+        e[i] = (vec)0.0f;
+        if (live && r < a.Dk) e[i] = *reinterpret_cast<const vec *>(s + (int64_t)r * a.Dv);
+    }
+    const float d = expf(a.log_decay[b * a.H + h]), beta = a.beta[b * a.H + h];
+    {
+        const float qi = tid < a.Dk ? (float)q[tid] : 0.0f, ki = tid < a.Dk ? (float)k[tid] : 0.0f;
+        sq[tid] = qi;
+        sk[tid] = ki;
+        float x = qi * ki;
+#pragma unroll
+        for (int i = 1; i < 64; i <<= 1) x += __shfl_xor(x, i);
+        if ((tid & 63) == 0) both[tid >> 6] = x;
+    }
+    __syncthreads();
+    vec ak = (vec)0.0f, aq = (vec)0.0f;
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+        const int r = i * RG + rg;
+        ak += e[i] * sk[r];
+        aq += e[i] * sq[r];
+    }
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) part[0][rg][lc * VEC + i] = ak[i], part[1][rg][lc * VEC + i] = aq[i];
+    __syncthreads();
+    if (tid < W) {
+        const int dv = blockIdx.y * W + tid;
+        float k0 = 0.0f, q0 = 0.0f;
+        for (int r = 0; r < RG; ++r) k0 += part[0][r][tid], q0 += part[1][r][tid];
+        const float vv = dv < a.Dv ? (float)v[dv] : 0.0f;
+        const float w = beta * (vv - d * k0);
+        u[tid] = w;
+        const float qk = (both[0] + both[1]) + (both[2] + both[3]);
+        if (dv < a.Dv) static_cast<T *>(a.out)[b * a.ob + h * a.oh + dv] = (T)(slot >= 0 ? a.scale * (d * q0 + qk * w) : 0.0f);
+    }
+    __syncthreads();
+    if (!live) return;
+    vec mine;
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) mine[i] = u[lc * VEC + i];
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+        const int r = i * RG + rg;
+        if (r < a.Dk) *reinterpret_cast<vec *>(s + (int64_t)r * a.Dv) = d * e[i] + sk[r] * mine;
+    }
+}
+
+// ---- host side of one storage type ----------------------------------------
+template <typename T> static hipError_t delta_prepare_typed(const DeltaArgs &a, hipStream_t s) {
+    const unsigned grid = (unsigned)((a.chunks * a.H + 3) / 4);
+    if (grid == 0) return hipSuccess;
+    if (a.vec) {
+        if (a.Dk <= 64) delta_prepare_kernel<T, 64, true><<<grid, 256, 0, s>>>(a);
+        else if (a.Dk <= 128) delta_prepare_kernel<T, 128, true><<<grid, 256, 0, s>>>(a);
+        else delta_prepare_kernel<T, 256, true><<<grid, 256, 0, s>>>(a);
+    } else {
+        if (a.Dk <= 64) delta_prepare_kernel<T, 64, false><<<grid, 256, 0, s>>>(a);
+        else if (a.Dk <= 128) delta_prepare_kernel<T, 128, false><<<grid, 256, 0, s>>>(a);
+        else delta_prepare_kernel<T, 256, false><<<grid, 256, 0, s>>>(a);
+    }
+    return hipGetLastError();
+}
+template <typename T, int DXP, int NT, int MODE, bool VEC> static hipError_t delta_walk_launch(const DeltaArgs &a, hipStream_t s) {
+    const int ztiles = (a.Dv + NT * 64 - 1) / (NT * 64), tiles = ztiles + (MODE == kDeltaSums ? (a.Dk + NT * 64 - 1) / (NT * 64) : 0);
+    const int64_t items = a.segs * a.H * tiles, round = 8 * (int64_t)delta_run(tiles, a.group);
+    delta_walk_kernel<T, DXP, NT, MODE, VEC><<<(unsigned)((items + round - 1) / round * round), 256, 0, s>>>(a, ztiles, tiles);
+    return hipGetLastError();
+}
+template <typename T, int MODE, bool VEC> static hipError_t delta_walks(const DeltaArgs &a, hipStream_t s) {
+    // (rows wider than 128 leave registers and LDS for 64 columns only)
+    if (a.Dk > 128) return delta_walk_launch<T, 256, 1, MODE, VEC>(a, s);
+    if (a.Dk > 64) return a.wide ? delta_walk_launch<T, 128, 2, MODE, VEC>(a, s) : delta_walk_launch<T, 128, 1, MODE, VEC>(a, s);
+    return a.wide ? delta_walk_launch<T, 64, 2, MODE, VEC>(a, s) : delta_walk_launch<T, 64, 1, MODE, VEC>(a, s);
+}
+template <typename T> static hipError_t delta_fwd_typed(const DeltaArgs &a, hipStream_t s) {
+    if (a.seg_state) {
+        const hipError_t e = a.vec ? delta_walks<T, kDeltaSums, true>(a, s) : delta_walks<T, kDeltaSums, false>(a, s);
+        if (e != hipSuccess) return e;
+        const dim3 grid((unsigned)a.B, (unsigned)a.H, (unsigned)((a.Dv + 63) / 64));
+        if (a.Dk <= 64) delta_chain_kernel<64><<<grid, 256, 0, s>>>(a);
+        else if (a.Dk <= 128) delta_chain_kernel<128><<<grid, 256, 0, s>>>(a);
+        else delta_chain_kernel<256><<<grid, 256, 0, s>>>(a);
+        const hipError_t e2 = hipGetLastError();
+        if (e2 != hipSuccess) return e2;
+    }
+    return a.vec ? delta_walks<T, kDeltaOut, true>(a, s) : delta_walks<T, kDeltaOut, false>(a, s);
+}
+template <typename T, int VEC, int LANES> static hipError_t delta_step_rows(const DeltaStep &a, hipStream_t s) {
+    constexpr int RG = 256 / LANES;
+    const dim3 grid((unsigned)(a.B * a.H), (unsigned)((a.Dv + LANES * VEC - 1) / (LANES * VEC)));
+    if (a.Dk <= 64) delta_step_kernel<T, VEC, LANES, 64 / RG><<<grid, 256, 0, s>>>(a);
+    else if (a.Dk <= 128) delta_step_kernel<T, VEC, LANES, 128 / RG><<<grid, 256, 0, s>>>(a);
+    else delta_step_kernel<T, VEC, LANES, 256 / RG><<<grid, 256, 0, s>>>(a);
+    return hipGetLastError();
+}
+template <typename T> static hipError_t delta_step_typed(const DeltaStep &a, bool vec, hipStream_t s) {
+    if (!vec) return delta_step_rows<T, 1, 32>(a, s);
+    if (a.B * a.H * ((a.Dv + 127) / 128) < 352) return delta_step_rows<T, 4, 8>(a, s);
+    return delta_step_rows<T, 4, 32>(a, s);
+}
+
+#define FFTCONV_DELTA_TYPE(NAME, T)                                                                                  \
+    hipError_t launch_delta_prepare_##NAME(const DeltaArgs &a, hipStream_t s) { return delta_prepare_typed<T>(a, s); } \
+    hipError_t launch_delta_fwd_##NAME(const DeltaArgs &a, hipStream_t s) { return delta_fwd_typed<T>(a, s); }         \
+    hipError_t launch_delta_step_##NAME(const DeltaStep &a, bool vec, hipStream_t s) { return delta_step_typed<T>(a, vec, s); }
+
+}  // namespace fftconv

@@ -1,0 +1,237 @@
+// delta_ops.cpp -- host side of the gated delta rule's entry points of
+// include/fftconv.h: argument checks, how sequences are cut, workspace
+// layout, launches.
+#include <cmath>
+#include <initializer_list>
+
+#include "arguments.hpp"
+#include "delta_ops.hpp"
+
+using namespace fftconv;
+
+namespace {
+
+struct DeltaShape {
+    int64_t B, N, H, Hk, Dk, Dv;
+    int dt;
+    bool packed;
+    int64_t T() const { return packed ? N : B * N; }
+    // places of units of `length` tokens (see first_place of the kernels)
+    int64_t places(int64_t length) const { return packed ? N / length + B : B * std::max<int64_t>(1, ceil_div(N, length)); }
+};
+
+int terms_of(int dt) { return delta_terms(dt == FFTCONV_F32 ? 4 : 2, dt == FFTCONV_F16); }
+size_t record_bytes(const DeltaShape &s) { return (size_t)delta_pieces(terms_of(s.dt)) * 1024; }
+
+// How sequences are cut.  A walk is serial: 64 tokens take microseconds, whatever else the chip does.  With
+// segments the walks' work is three times that of the walk alone (sums and maps, outputs) and the chain adds to it,
+// so sequences are cut where at least four segments of each walk at once.
+struct DeltaCut {
+    int64_t seg_chunks, segs;
+    bool cut, wide;
+};
+DeltaCut fwd_cut(const DeltaShape &s) {
+    DeltaCut c{};
+    const int64_t chunks = std::max<int64_t>(1, ceil_div(s.packed ? ceil_div(s.N, s.B) : s.N, kDeltaChunk));
+    const int64_t wide = s.B * s.H * ceil_div(s.Dv, 128), narrow = s.B * s.H * ceil_div(s.Dv, 64);
+    c.wide = s.Dk <= 128 && s.Dv > 64 && narrow > kCus;
+    const int64_t most = kCus / std::max<int64_t>(1, s.Dv > 64 && s.Dk <= 128 ? wide : narrow);
+    const int64_t segments = std::min<int64_t>(most, chunks / 8);
+    if (segments >= 4) {
+        c.seg_chunks = ceil_div(chunks, segments);
+        c.cut = true;
+        c.wide = s.Dk <= 128 && s.Dv > 64;
+    } else {
+        c.seg_chunks = (int64_t(1) << 31) / kDeltaChunk;      // one segment, whatever the length
+    }
+    c.segs = s.places(c.seg_chunks * kDeltaChunk);
+    return c;
+}
+
+struct DeltaFwdLayout {
+    size_t states, maps, total;
+};
+DeltaFwdLayout fwd_layout(const DeltaShape &s, const DeltaCut &c) {
+    DeltaFwdLayout l{};
+    l.states = align_up((size_t)s.places(kDeltaChunk) * s.H * record_bytes(s), 256);
+    l.maps = l.states + (c.cut ? align_up((size_t)c.segs * s.H * s.Dk * s.Dv * 4, 256) : 0);
+    l.total = l.maps + (c.cut ? (size_t)c.segs * s.H * s.Dk * s.Dk * 4 : 0);
+    return l;
+}
+
+fftconv_status_t check_shape(const DeltaShape &s, float scale) {
+    if (!dtype_ok(s.dt)) return fail(FFTCONV_ERR_UNSUPPORTED, "dtype %d is not supported", s.dt);
+    if (s.B < 0 || s.N < 0 || s.H < 0 || s.Hk < 0)
+        return fail(FFTCONV_ERR_INVALID_ARGUMENT, "B=%lld, N=%lld, H=%lld and Hk=%lld must be >= 0", (long long)s.B,
+                    (long long)s.N, (long long)s.H, (long long)s.Hk);
+    if (s.Dk < 1 || s.Dk > kMaxHeadDim || s.Dv < 1 || s.Dv > kMaxHeadDim)
+        return fail(FFTCONV_ERR_UNSUPPORTED, "head widths Dk=%lld and Dv=%lld must be in [1, %lld]", (long long)s.Dk,
+                    (long long)s.Dv, (long long)kMaxHeadDim);
+    if (s.H > 0 && (s.Hk < 1 || s.H % s.Hk))
+        return fail(FFTCONV_ERR_INVALID_ARGUMENT, "H=%lld must be a multiple of Hk=%lld", (long long)s.H, (long long)s.Hk);
+    if (s.H > 65535) return fail(FFTCONV_ERR_UNSUPPORTED, "H=%lld is above 65535", (long long)s.H);
+    // a launch has a workgroup for four (chunk, head) pairs and one for each walk and 64 of at most 512 columns
+    if (s.B >= (int64_t(1) << 31) || s.N >= (int64_t(1) << 31) || (s.B > 0 && s.N > (int64_t(1) << 40) / s.B) ||
+        (s.H > 0 && (s.B > kMaxGroups / 16 / s.H || s.places(kDeltaChunk) > kMaxGroups / s.H)))
+        return fail(FFTCONV_ERR_UNSUPPORTED, "B=%lld, N=%lld, H=%lld: too many sequences or tokens", (long long)s.B,
+                    (long long)s.N, (long long)s.H);
+    if (!std::isfinite(scale)) return fail(FFTCONV_ERR_INVALID_ARGUMENT, "scale must be finite");
+    return FFTCONV_OK;
+}
+
+// heads: H or Hk; strides (batch, token, head) at st
+View heads_view(const char *name, const void *p, const DeltaShape &s, int64_t heads, int64_t row, const int64_t *st) {
+    View v{name, p, 3, {s.packed ? 1 : s.B, s.N, heads}, {0, 0, 0}, row, elem_bytes(s.dt)};
+    if (st) {
+        for (int i = 0; i < 3; ++i) v.stride[i] = st[i];
+        if (s.packed) v.stride[0] = 0;
+    } else {
+        v.stride[0] = s.N * heads * row;
+        v.stride[1] = heads * row;
+        v.stride[2] = row;
+    }
+    return v.settle();
+}
+View gate_view(const char *name, const void *p, const DeltaShape &s) {
+    return View{name, p, 1, {s.T(), 1, 1}, {s.H, 0, 0}, s.H, 4}.settle();
+}
+View state_view(const char *name, const void *p, int64_t count, const DeltaShape &s) {
+    return View{name, p, 1, {count, 1, 1}, {s.H * s.Dk * s.Dv, 0, 0}, s.H * s.Dk * s.Dv, 4}.settle();
+}
+// The walks reach a chunk's rows by 31-bit offsets.
+fftconv_status_t check_reach(const View &v) {
+    if (v.size[1] > 1 && v.stride[1] * v.bytes_per >= (int64_t(1) << 24))
+        return fail(FFTCONV_ERR_UNSUPPORTED, "%s has a token stride of %lld elements, 16 MiB or more", v.name, (long long)v.stride[1]);
+    return FFTCONV_OK;
+}
+fftconv_status_t check_ints(std::initializer_list<const void *> ps) {
+    for (const void *p : ps)
+        if (!aligned(p, 4)) return fail(FFTCONV_ERR_INVALID_ARGUMENT, "state_slots and cu_seqlens must be 4-byte aligned");
+    return FFTCONV_OK;
+}
+
+hipError_t launch_prepare(int dt, const DeltaArgs &a, hipStream_t s) {
+    return dt == FFTCONV_F32   ? launch_delta_prepare_f32(a, s)
+           : dt == FFTCONV_F16 ? launch_delta_prepare_f16(a, s)
+                               : launch_delta_prepare_bf16(a, s);
+}
+hipError_t launch_fwd(int dt, const DeltaArgs &a, hipStream_t s) {
+    return dt == FFTCONV_F32   ? launch_delta_fwd_f32(a, s)
+           : dt == FFTCONV_F16 ? launch_delta_fwd_f16(a, s)
+                               : launch_delta_fwd_bf16(a, s);
+}
+
+// what every call over whole sequences hands to the kernels
+DeltaArgs common_args(const DeltaShape &s, const View &q, const View &k, const View &v, const float *log_decay, const float *beta,
+                      float scale, const int32_t *cu) {
+    DeltaArgs a{};
+    a.q = q.p, a.qb = q.stride[0], a.qt = q.stride[1], a.qh = q.stride[2];
+    a.k = k.p, a.kb = k.stride[0], a.kt = k.stride[1], a.kh = k.stride[2];
+    a.v = v.p, a.vb = v.stride[0], a.vt = v.stride[1], a.vh = v.stride[2];
+    a.log_decay = log_decay, a.beta = beta, a.scale = scale, a.cu = cu;
+    a.B = s.B, a.N = s.N, a.H = (int)s.H, a.group = (int)(s.H / s.Hk), a.Dk = (int)s.Dk, a.Dv = (int)s.Dv;
+    a.chunks = s.places(kDeltaChunk);
+    if (s.T() == 0) a.chunks = 0;
+    return a;
+}
+
+}  // namespace
+
+size_t fftconv_delta_fwd_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t Hk, int64_t Dk, int64_t Dv,
+                                         fftconv_dtype_t dtype) {
+    if (!dtype_ok(dtype) || B < 1 || T < 1 || H < 1 || Hk < 1 || Dk < 1 || Dv < 1 || Dk > kMaxHeadDim || Dv > kMaxHeadDim) return 0;
+    // by the number of tokens: the most of B equal sequences and of a packed call
+    const DeltaShape equal{B, ceil_div(T, B), H, Hk, Dk, Dv, dtype, false}, packed{B, T, H, Hk, Dk, Dv, dtype, true};
+    return std::max(fwd_layout(equal, fwd_cut(equal)).total, fwd_layout(packed, fwd_cut(packed)).total);
+}
+
+fftconv_status_t fftconv_delta_fwd(const void *q, const void *k, const void *v, const float *log_decay, const float *beta,
+                                   void *out, const int64_t *strides, const float *state_in, float *state_out,
+                                   const int32_t *state_slots, int64_t n_slots, const int32_t *cu_seqlens, int64_t B,
+                                   int64_t N, int64_t H, int64_t Hk, int64_t Dk, int64_t Dv, float scale,
+                                   fftconv_dtype_t dtype, void *workspace, size_t workspace_bytes, hipStream_t stream) {
+    const DeltaShape s{B, N, H, Hk, Dk, Dv, (int)dtype, cu_seqlens != nullptr};
+    fftconv_status_t st = check_shape(s, scale);
+    if (st != FFTCONV_OK) return st;
+    if (n_slots < 0) return fail(FFTCONV_ERR_INVALID_ARGUMENT, "n_slots=%lld must be >= 0", (long long)n_slots);
+    if (B == 0 || H == 0) return ok();
+    auto at = [&](int i) { return strides ? strides + 3 * i : nullptr; };
+    const View vq = heads_view("q", q, s, Hk, Dk, at(0)), vk = heads_view("k", k, s, Hk, Dk, at(1)),
+               vv = heads_view("v", v, s, H, Dv, at(2)), vo = heads_view("out", out, s, H, Dv, at(3));
+    const View vg = gate_view("log_decay", log_decay, s), vb = gate_view("beta", beta, s);
+    for (const View *x : {&vq, &vk, &vv, &vg, &vb})
+        if ((st = check_view(*x, true, false)) != FFTCONV_OK) return st;
+    if ((st = check_view(vo, true, true)) != FFTCONV_OK) return st;
+    for (const View *x : {&vq, &vk, &vv, &vo})
+        if ((st = check_reach(*x)) != FFTCONV_OK) return st;
+    const int64_t states = state_slots ? n_slots : B;
+    const View si = state_view("state_in", state_in, states, s), so = state_view("state_out", state_out, states, s);
+    for (const View *x : {&si, &so})
+        if ((st = check_view(*x, false, false)) != FFTCONV_OK) return st;
+    if ((st = check_ints({state_slots, cu_seqlens})) != FFTCONV_OK) return st;
+    const size_t need = fftconv_delta_fwd_workspace_bytes(B, s.T(), H, Hk, Dk, Dv, dtype);
+    if ((st = check_workspace(workspace, workspace_bytes, need)) != FFTCONV_OK) return st;
+    const View ws = raw_view("workspace", need ? workspace : nullptr, (int64_t)need);
+    const View sl = raw_view("state_slots", state_slots, B * 4), cu = raw_view("cu_seqlens", cu_seqlens, (B + 1) * 4);
+    // state_out may be state_in itself (the pool updated in place), nothing else
+    if (state_out && state_in && state_out != state_in && si.overlaps(so))
+        return fail(FFTCONV_ERR_INVALID_ARGUMENT, "state_out overlaps state_in without being it");
+    const View outs[] = {vo, so, ws}, ins[] = {vq, vk, vv, vg, vb, sl, cu};
+    if ((st = check_apart(outs, 3, ins, 7)) != FFTCONV_OK) return st;
+    const View apart[] = {vo, ws};
+    if ((st = check_apart(apart, 2, &si, 1)) != FFTCONV_OK) return st;
+    if (s.T() == 0 && !state_out) return ok();
+
+    DeltaArgs a = common_args(s, vq, vk, vv, log_decay, beta, scale, cu_seqlens);
+    a.out = out, a.ob = vo.stride[0], a.ot = vo.stride[1], a.oh = vo.stride[2];
+    a.state0 = state_in, a.state1 = state_out, a.slots = state_slots, a.n_slots = n_slots;
+    a.vec = chunk_vec(vq) && chunk_vec(vk) && chunk_vec(vv) && chunk_vec(vo);
+    const DeltaCut c = fwd_cut(s);
+    const DeltaFwdLayout l = fwd_layout(s, c);
+    a.seg_chunks = c.seg_chunks, a.segs = c.segs, a.wide = c.wide;
+    a.rec = static_cast<char *>(workspace);
+    a.seg_state = c.cut ? reinterpret_cast<float *>(a.rec + l.states) : nullptr;
+    a.seg_map = c.cut ? reinterpret_cast<float *>(a.rec + l.maps) : nullptr;
+    hipError_t e = launch_prepare(dtype, a, stream);
+    if (e == hipSuccess) e = launch_fwd(dtype, a, stream);
+    return hip_status("delta rule", e);
+}
+
+fftconv_status_t fftconv_delta_step(const void *q, const void *k, const void *v, const float *log_decay,
+                                    const float *beta, float *state, void *out, const int64_t *strides,
+                                    const int32_t *state_slots, int64_t n_slots, int64_t B, int64_t H, int64_t Hk,
+                                    int64_t Dk, int64_t Dv, float scale, fftconv_dtype_t dtype, hipStream_t stream) {
+    const DeltaShape s{B, 1, H, Hk, Dk, Dv, (int)dtype, false};
+    fftconv_status_t st = check_shape(s, scale);
+    if (st != FFTCONV_OK) return st;
+    if (n_slots < 0) return fail(FFTCONV_ERR_INVALID_ARGUMENT, "n_slots=%lld must be >= 0", (long long)n_slots);
+    if (B == 0 || H == 0) return ok();
+    int64_t full[12];
+    if (strides)
+        for (int i = 0; i < 4; ++i) full[3 * i] = strides[2 * i], full[3 * i + 1] = 0, full[3 * i + 2] = strides[2 * i + 1];
+    auto at = [&](int i) { return strides ? full + 3 * i : nullptr; };
+    const View vq = heads_view("q", q, s, Hk, Dk, at(0)), vk = heads_view("k", k, s, Hk, Dk, at(1)),
+               vv = heads_view("v", v, s, H, Dv, at(2)), vo = heads_view("out", out, s, H, Dv, at(3));
+    const View vg = gate_view("log_decay", log_decay, s), vb = gate_view("beta", beta, s);
+    for (const View *x : {&vq, &vk, &vv, &vg, &vb})
+        if ((st = check_view(*x, true, false)) != FFTCONV_OK) return st;
+    if ((st = check_view(vo, true, true)) != FFTCONV_OK) return st;
+    if (!state && !(state_slots && n_slots == 0)) return fail(FFTCONV_ERR_INVALID_ARGUMENT, "state must be non-null");
+    const View vs = state_view("state", state, state_slots ? n_slots : B, s);
+    if ((st = check_view(vs, false, false)) != FFTCONV_OK) return st;
+    if ((st = check_ints({state_slots})) != FFTCONV_OK) return st;
+    const View outs[] = {vo, vs}, ins[] = {vq, vk, vv, vg, vb, raw_view("state_slots", state_slots, B * 4)};
+    if ((st = check_apart(outs, 2, ins, 6)) != FFTCONV_OK) return st;
+
+    DeltaStep a{};
+    a.q = q, a.k = k, a.v = v, a.out = out;
+    a.qb = vq.stride[0], a.qh = vq.stride[2], a.kb = vk.stride[0], a.kh = vk.stride[2];
+    a.vb = vv.stride[0], a.vh = vv.stride[2], a.ob = vo.stride[0], a.oh = vo.stride[2];
+    a.log_decay = log_decay, a.beta = beta, a.state = state, a.slots = state_slots, a.n_slots = n_slots;
+    a.B = B, a.H = (int)H, a.group = (int)(H / Hk), a.Dk = (int)Dk, a.Dv = (int)Dv, a.scale = scale;
+    const bool vec = Dv % 4 == 0 && aligned(state, 16);
+    const hipError_t e = dtype == FFTCONV_F32   ? launch_delta_step_f32(a, vec, stream)
+                         : dtype == FFTCONV_F16 ? launch_delta_step_f16(a, vec, stream)
+                                                : launch_delta_step_bf16(a, vec, stream);
+    return hip_status("delta step", e);
+}

@@ -1,0 +1,65 @@
+// delta_ops.hpp -- what the host side of the gated delta rule (delta_ops.cpp)
+// passes to its kernels (delta_kernels.hpp), and the launchers per storage type.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "sequence_ops.hpp"
+
+namespace fftconv {
+
+constexpr int kDeltaChunk = 64;      // tokens of a chunk
+
+// What the walks read of one (chunk, head), written by the first kernel, in pieces of 1 KB (16 bytes a lane):
+// the inverse as 6 operands of two fp32 halves, 4 vectors of the tokens, the masked products as 6 operands of
+// `terms` terms; padded to whole rounds of four waves.
+constexpr int kDeltaInverse = 12, kDeltaVectors = 1;
+constexpr int delta_pieces(int terms) { return (kDeltaInverse + kDeltaVectors + 6 * terms + 3) / 4 * 4; }
+// terms of the masked products: bf16 results see them rounded once, like the state; fp16's need two, fp32's three
+constexpr int delta_terms(int elem_bytes, bool narrow) { return elem_bytes == 4 ? 3 : narrow ? 2 : 1; }
+
+struct DeltaArgs {
+    const void *q, *k, *v;           // q and k have H / group heads, v and out H
+    void *out;
+    int64_t qb, qt, qh, kb, kt, kh, vb, vt, vh, ob, ot, oh;   // strides (batch, token, head), elements
+    const float *log_decay, *beta;   // (B, N, H) or (N, H)
+    float scale;
+    const int32_t *cu;               // packed sequences' bounds (B + 1) or null
+    int64_t B, N;                    // N: tokens of each sequence, or of all when packed
+    int H, group, Dk, Dv;
+    const float *state0;             // initial states or null
+    float *state1;                   // final states or null
+    const int32_t *slots;            // state slot of each sequence or null
+    int64_t n_slots;
+    int64_t chunks;                  // places for chunks (an upper bound when packed)
+    int64_t seg_chunks, segs;        // chunks of a segment, places for segments
+    char *rec;                       // (chunks, H) records
+    float *seg_state;                // (segs, H) Dk x Dv: a segment's own sum, then the state before it; null: one segment each
+    float *seg_map;                  // (segs, H) Dk x Dk: what a segment makes of the state before it
+    int vec;                         // rows of q, k, v, out in whole aligned 16-byte pieces
+    int wide;                        // 128 columns of the state a workgroup, else 64
+};
+
+struct DeltaStep {
+    const void *q, *k, *v;
+    void *out;
+    int64_t qb, qh, kb, kh, vb, vh, ob, oh;
+    const float *log_decay, *beta;   // (B, H)
+    float *state;
+    const int32_t *slots;
+    int64_t n_slots, B;
+    int H, group, Dk, Dv;
+    float scale;
+};
+
+#define FFTCONV_DELTA_LAUNCHERS(NAME)                                                       \
+    hipError_t launch_delta_prepare_##NAME(const DeltaArgs &a, hipStream_t stream);         \
+    hipError_t launch_delta_fwd_##NAME(const DeltaArgs &a, hipStream_t stream);             \
+    hipError_t launch_delta_step_##NAME(const DeltaStep &a, bool vec, hipStream_t stream);
+FFTCONV_DELTA_LAUNCHERS(f32)
+FFTCONV_DELTA_LAUNCHERS(f16)
+FFTCONV_DELTA_LAUNCHERS(bf16)
+#undef FFTCONV_DELTA_LAUNCHERS
+
+}  // namespace fftconv

@@ -97,3 +97,49 @@ def linear_bwd(dout, x, W, pre=None, activation="none"):
     """(dx, dW, dbias)."""
     dz = dout if activation == "none" else dout * act_slope(pre, activation)
     return dz @ W, dz.T @ x, dz.sum(0)
+
+
+def delta_fwd(q, k, v, log_decay, beta, scale, state=None):
+    """Gated delta rule over one sequence: q, k (N, Hk, Dk), v (N, H, Dv), log_decay, beta (N, H) -> out, final state.
+
+    u_t = beta_t (v_t - a_t S_{t-1}^T k_t),  S_t = a_t S_{t-1} + k_t u_t^T,  out_t = scale S_t^T q_t,  a = exp(log_decay)
+    """
+    N, H, Dv = v.shape
+    q, k = _heads(q, H), _heads(k, H)
+    S = np.zeros((H, q.shape[2], Dv)) if state is None else np.array(state, dtype=np.float64)
+    out = np.zeros((N, H, Dv))
+    for t in range(N):
+        S = np.exp(log_decay[t])[:, None, None] * S
+        u = beta[t][:, None] * (v[t] - (S * k[t][:, :, None]).sum(1))
+        S = S + k[t][:, :, None] * u[:, None, :]
+        out[t] = scale * (S * q[t][:, :, None]).sum(1)
+    return out, S
+
+
+def delta_bwd(dout, q, k, v, log_decay, beta, scale, state=None, dstate=None):
+    """Gradients of sum(dout * out) + sum(dstate * final state): dq, dk, dv, dlog_decay, dbeta, dstate_in."""
+    N, H, Dv = v.shape
+    Hk, Dk = q.shape[1:]
+    qh, kh = _heads(q, H), _heads(k, H)
+    S = np.zeros((H, Dk, Dv)) if state is None else np.array(state, dtype=np.float64)
+    decayed, wrong, after = [], [], []
+    for t in range(N):
+        D = np.exp(log_decay[t])[:, None, None] * S
+        w = v[t] - (D * kh[t][:, :, None]).sum(1)
+        S = D + kh[t][:, :, None] * (beta[t][:, None] * w)[:, None, :]
+        decayed.append(D), wrong.append(w), after.append(S)
+    dq, dk, dv = np.zeros((N, H, Dk)), np.zeros((N, H, Dk)), np.zeros((N, H, Dv))
+    dg, db = np.zeros((N, H)), np.zeros((N, H))
+    G = np.zeros((H, Dk, Dv)) if dstate is None else np.array(dstate, dtype=np.float64)
+    for t in reversed(range(N)):
+        dq[t] = scale * (after[t] * dout[t][:, None, :]).sum(2)
+        G = G + scale * qh[t][:, :, None] * dout[t][:, None, :]
+        du = (G * kh[t][:, :, None]).sum(1)
+        db[t] = (du * wrong[t]).sum(1)
+        dv[t] = beta[t][:, None] * du
+        dk[t] = (G * (beta[t][:, None] * wrong[t])[:, None, :]).sum(2) - (decayed[t] * dv[t][:, None, :]).sum(2)
+        G = G - kh[t][:, :, None] * dv[t][:, None, :]
+        dg[t] = (G * decayed[t]).sum((1, 2))
+        G = np.exp(log_decay[t])[:, None, None] * G
+    share = H // Hk
+    return dq.reshape(N, Hk, share, Dk).sum(2), dk.reshape(N, Hk, share, Dk).sum(2), dv, dg, db, G
