@@ -428,6 +428,22 @@ fftconv_status_t fftconv_delta_step(const void *q, const void *k, const void *v,
                                     const int32_t *state_slots, int64_t n_slots, int64_t B, int64_t H, int64_t Hk,
                                     int64_t Dk, int64_t Dv, float scale, fftconv_dtype_t dtype, hipStream_t stream);
 
+/* As above, for fftconv_delta_bwd. */
+size_t fftconv_delta_bwd_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t Hk, int64_t Dk, int64_t Dv,
+                                         fftconv_dtype_t dtype);
+
+/* Gradients of sum(dout * out) + sum(dstate_out * state_out) of the prompt form.  dq, dk and dv are in the storage
+ * type, dq and dk summed over the heads that share a q/k head; dlog_decay and dbeta are fp32 (B, N, H), dense.  All of
+ * them and dstate_in may each be NULL (skipped); dstate_out NULL = zero.  States are fp32 (B, H, Dk, Dv).  The call
+ * recomputes what it needs of the forward pass; its workspace holds the state and the state's gradient of every 64
+ * tokens.  strides: int64[21], dout, q, k, v, dq, dk, dv, or NULL.  Results repeat bit by bit. */
+fftconv_status_t fftconv_delta_bwd(const void *dout, const void *q, const void *k, const void *v, const float *log_decay,
+                                   const float *beta, void *dq, void *dk, void *dv, float *dlog_decay, float *dbeta,
+                                   const int64_t *strides, const float *state_in, const float *dstate_out,
+                                   float *dstate_in, const int32_t *cu_seqlens, int64_t B, int64_t N, int64_t H,
+                                   int64_t Hk, int64_t Dk, int64_t Dv, float scale, fftconv_dtype_t dtype,
+                                   void *workspace, size_t workspace_bytes, hipStream_t stream);
+
 /* ---- Linear product ---------------------------------------------------------
  * The dense products around a mixer, with what follows them fused:
  *     pre = x W^T + bias,     out = act(pre) + residual

@@ -117,6 +117,10 @@ def _load():
     lib.fftconv_delta_fwd.restype = ctypes.c_int
     lib.fftconv_delta_step.argtypes = [vp] * 9 + [i64] * 6 + [ctypes.c_float, ctypes.c_int, vp]
     lib.fftconv_delta_step.restype = ctypes.c_int
+    lib.fftconv_delta_bwd_workspace_bytes.argtypes = ints + [ctypes.c_int]
+    lib.fftconv_delta_bwd_workspace_bytes.restype = sz
+    lib.fftconv_delta_bwd.argtypes = [vp] * 16 + ints + [ctypes.c_float, ctypes.c_int, vp, sz, vp]
+    lib.fftconv_delta_bwd.restype = ctypes.c_int
     lib.fftconv_norm_fwd.argtypes = [vp] * 7 + [i64] * 3 + [ctypes.c_float, ctypes.c_int, vp]
     lib.fftconv_norm_fwd.restype = ctypes.c_int
     lib.fftconv_norm_bwd_workspace_bytes.argtypes = [i64, i64]
@@ -779,6 +783,54 @@ def delta_attention(q, k, v, log_decay, beta, scale=None, state_in=None, cu_seql
     fftconv_delta_fwd(q, k, v, log_decay, beta, out, Dk ** -0.5 if scale is None else scale, state_in, state_out,
                       cu_seqlens=cu_seqlens, workspace=ws)
     return out, state_out
+
+
+def fftconv_delta_bwd_workspace_bytes(B: int, T: int, H: int, Hk: int, Dk: int, Dv: int, dtype) -> int:
+    return int(_load().fftconv_delta_bwd_workspace_bytes(B, T, H, Hk, Dk, Dv, _dtype_of(dtype)))
+
+
+def fftconv_delta_bwd(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor,
+                      beta: torch.Tensor, dq: torch.Tensor | None, dk: torch.Tensor | None, dv: torch.Tensor | None,
+                      dlog_decay: torch.Tensor | None, dbeta: torch.Tensor | None, scale: float,
+                      state_in: torch.Tensor | None = None, dstate_out: torch.Tensor | None = None,
+                      dstate_in: torch.Tensor | None = None, cu_seqlens: torch.Tensor | None = None,
+                      workspace: torch.Tensor | None = None, stream=None) -> None:
+    """Gradients of fftconv_delta_fwd into dq, dk, dv, dlog_decay, dbeta, dstate_in (None = skip)."""
+    B, N, H, Hk, Dk, Dv = _delta_shapes(q, k, v, log_decay, beta, cu_seqlens)
+    _rows_tensor(dout, "dout", q, v.shape)
+    for name, t, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
+        if t is not None:
+            _rows_tensor(t, name, q, like.shape)
+    for name, t in (("dlog_decay", dlog_decay), ("dbeta", dbeta)):
+        _plain_tensor(t, name, torch.float32, log_decay.shape, q.device)
+    for name, t in (("state_in", state_in), ("dstate_out", dstate_out), ("dstate_in", dstate_in)):
+        _plain_tensor(t, name, torch.float32, (B, H, Dk, Dv), q.device)
+    _dev_tensor(workspace, "workspace")
+    with _on(q.device):
+        _check((_lib or _load()).fftconv_delta_bwd(
+            dout.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), beta.data_ptr(), _at(dq),
+            _at(dk), _at(dv), _at(dlog_decay), _at(dbeta), _strides((dout, q, k, v, dq, dk, dv), cu_seqlens is not None),
+            _at(state_in), _at(dstate_out), _at(dstate_in), _at(cu_seqlens), B, N, H, Hk, Dk, Dv, scale,
+            _DTYPE_CODE[q.dtype], _at(workspace), _nbytes(workspace), _raw_stream(stream, q.device)))
+
+
+def delta_attention_bwd(q, k, v, log_decay, beta, dout, scale=None, state_in=None, dstate_out=None, cu_seqlens=None,
+                        stream=None):
+    """Gradients of delta_attention; returns (dq, dk, dv, dlog_decay, dbeta, dstate_in), the last None without state_in.
+
+    Rows of packed tokens that belong to no sequence are not set.
+    """
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return delta_attention_bwd(q, k, v, log_decay, beta, dout, scale, state_in, dstate_out, cu_seqlens)
+    B, N, H, Hk, Dk, Dv = _delta_shapes(q, k, v, log_decay, beta, cu_seqlens)
+    T = N if cu_seqlens is not None else B * N
+    grads = [torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k, v, log_decay, beta)]
+    dstate_in = None if state_in is None else torch.empty_like(state_in)
+    ws = _scratch(fftconv_delta_bwd_workspace_bytes(B, T, H, Hk, Dk, Dv, q.dtype), q.device)
+    fftconv_delta_bwd(dout, q, k, v, log_decay, beta, *grads, Dk ** -0.5 if scale is None else scale, state_in,
+                      dstate_out, dstate_in, cu_seqlens, ws)
+    return (*grads, dstate_in)
 
 
 # ---------------------------------------------------------------- root-mean-square norm

@@ -230,7 +230,8 @@ __device__ __forceinline__ void invert_unit_lower(float *M) {
 
 // One wave a (chunk, head): record of the chunk.  grid: chunks * H / 4.  Bound by latency: products, the inverse's
 // 16 serial steps and LDS round trips; eight waves a CU overlap them.
-template <typename T, int DXP, bool VEC> __global__ __launch_bounds__(256) void delta_prepare_kernel(const DeltaArgs a) {
+// BACK: the backward call's record.
+template <typename T, int DXP, bool VEC, bool BACK> __global__ __launch_bounds__(256) void delta_prepare_kernel(const DeltaArgs a) {
     constexpr int KX = DXP / 32, NP = Terms<T>::kP;
     __shared__ __attribute__((aligned(16))) float matrix[4][kC * kLd];
     __shared__ double sums[4][kC];
@@ -265,7 +266,7 @@ template <typename T, int DXP, bool VEC> __global__ __launch_bounds__(256) void 
     const double last = __shfl(sum, 63);
     G[lane] = sum;
     beta[lane] = b;
-    char *rec = a.rec + item * (int64_t)(delta_pieces(NP) * 1024);
+    char *rec = a.rec + item * a.rec_bytes;
     {
         float *vec = reinterpret_cast<float *>(rec + kDeltaInverse * 1024);
         const float first = exp_of(sum);
@@ -299,22 +300,26 @@ template <typename T, int DXP, bool VEC> __global__ __launch_bounds__(256) void 
 #pragma unroll
                 for (int j = 0; j <= i; ++j, ++at) {
                     kk[at] = mma_terms<3>(kf[i], kf[j], kk[at]);
-                    qk[at] = mma_terms<3>(kf[j], qf[i], qk[at]);
+                    // BACK: rows i, columns j
+                    qk[at] = BACK ? mma_terms<3>(qf[i], kf[j], qk[at]) : mma_terms<3>(kf[j], qf[i], qk[at]);
                 }
         }
     }
-    // C diag(beta) into LDS
+    // decayed products of keys into LDS, weighted by beta of their column (I + C diag(beta)) or of their row
+    auto put = [&](bool by_row) __attribute__((always_inline)) {
 #pragma unroll
-    for (int i = 0, at = 0; i < 4; ++i)
+        for (int i = 0, at = 0; i < 4; ++i)
 #pragma unroll
-        for (int j = 0; j <= i; ++j, ++at)
+            for (int j = 0; j <= i; ++j, ++at)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int row = 16 * i + 4 * g + r, col = 16 * j + c;
-                M[row * kLd + col] = col < row ? kk[at][r] * exp_of(G[row] - G[col]) * beta[col] : 0.0f;
-            }
-    wave_sync();
-    invert_unit_lower(M);
+                for (int r = 0; r < 4; ++r) {
+                    const int row = 16 * i + 4 * g + r, col = 16 * j + c;
+                    M[row * kLd + col] = col < row ? kk[at][r] * exp_of(G[row] - G[col]) * beta[by_row ? row : col] : 0.0f;
+                }
+        wave_sync();
+        invert_unit_lower(M);
+    };
+    put(false);
     f32x4 *out = reinterpret_cast<f32x4 *>(rec);
     bf8 *outp = reinterpret_cast<bf8 *>(rec + (kDeltaInverse + kDeltaVectors) * 1024);
 #pragma unroll
@@ -327,18 +332,48 @@ template <typename T, int DXP, bool VEC> __global__ __launch_bounds__(256) void 
                 const int j = 2 * s + half;      // block of columns
                 out[(e * 2 + half) * 64 + lane] =
                     j <= i ? *reinterpret_cast<const f32x4 *>(M + (16 * i + c) * kLd + 16 * j + 4 * g) : f32x4{0, 0, 0, 0};
+                if constexpr (!BACK) {
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int row = 16 * i + c, col = 16 * j + 4 * g + r;
-                    const f32x4 x = qk[j <= i ? i * (i + 1) / 2 + j : 0];
-                    p[half * 4 + r] = ((j <= i) & (col <= row)) ? x[r] * a.scale * exp_of(G[row] - G[col <= row ? col : row]) : 0.0f;
+                    for (int r = 0; r < 4; ++r) {
+                        const int row = 16 * i + c, col = 16 * j + 4 * g + r;
+                        const f32x4 x = qk[j <= i ? i * (i + 1) / 2 + j : 0];
+                        p[half * 4 + r] = ((j <= i) & (col <= row)) ? x[r] * a.scale * exp_of(G[row] - G[col <= row ? col : row]) : 0.0f;
+                    }
                 }
             }
-            bf8 terms[NP];
-            rows_terms<NP>(f32x4{p[0], p[1], p[2], p[3]}, f32x4{p[4], p[5], p[6], p[7]}, terms);
+            if constexpr (!BACK) {
+                bf8 terms[NP];
+                rows_terms<NP>(f32x4{p[0], p[1], p[2], p[3]}, f32x4{p[4], p[5], p[6], p[7]}, terms);
 #pragma unroll
-            for (int u = 0; u < NP; ++u) outp[(e * NP + u) * 64 + lane] = terms[u];
+                for (int u = 0; u < NP; ++u) outp[(e * NP + u) * 64 + lane] = terms[u];
+            }
         }
+    if constexpr (BACK) {
+        // (I + diag(beta) C)^-1 and P by columns: lane (g, c) holds column 16 j + c at the rows of the operand's slots
+        wave_sync();
+        put(true);
+        f32x4 *outt = reinterpret_cast<f32x4 *>(rec + (kDeltaInverse + kDeltaVectors) * 1024);
+#pragma unroll
+        for (int j = 0, e = 0; j < 4; ++j)
+#pragma unroll
+            for (int s = j / 2; s < 2; ++s, ++e)
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const int i = 2 * s + half;
+                    f32x4 m{0, 0, 0, 0}, p{0, 0, 0, 0};
+                    if (i >= j) {
+                        const f32x4 x = qk[i * (i + 1) / 2 + j];
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            const int row = 16 * i + 4 * g + r, col = 16 * j + c;
+                            m[r] = col <= row ? M[row * kLd + col] : 0.0f;
+                            p[r] = col <= row ? x[r] * a.scale * exp_of(G[row] - G[col <= row ? col : row]) : 0.0f;
+                        }
+                    }
+                    outt[(e * 2 + half) * 64 + lane] = m;
+                    outt[kDeltaInverse * 64 + (e * 2 + half) * 64 + lane] = p;
+                }
+    }
 }
 
 // ---- tiles in LDS ------------------------------------------------------------
@@ -457,6 +492,14 @@ template <int KX, int NT> struct State {
             return x;
         });
     }
+    // into a matrix of padded rows, whose padding it fills with what padding gives: zeros
+    template <typename C> __device__ __forceinline__ void keep(float *p, int ld, C &&column) {
+        const auto view = wide_view(p);
+        each([&](int row, int t, float x) __attribute__((always_inline)) {
+            view_store(view, (uint32_t)(row * ld + column(t)) * 4u, x);
+            return x;
+        });
+    }
     __device__ __forceinline__ void terms(int kk, int t, bf8 (&out)[3]) const {
         float f[8];
 #pragma unroll
@@ -464,6 +507,18 @@ template <int KX, int NT> struct State {
         split8<__bf16, 3>(f, out);
     }
 };
+
+// accumulators over tokens (rows 16 r + 4 g + i) into a matrix of 64 padded rows
+template <int NT, typename C> __device__ __forceinline__ void keep_rows(float *p, int ld, const f32x4 (&x)[4][NT], C &&column) {
+    const auto view = wide_view(p);
+    const int g = (threadIdx.x & 63) >> 4;
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) view_store(view, (uint32_t)((16 * r + 4 * g + i) * ld + column(t)) * 4u, x[r][t][i]);
+}
 
 // Work item of workgroup id: ids go to the 8 XCDs in turn, so runs of `run` items are dealt to one XCD, whose L2
 // then holds what they have in common.
@@ -476,8 +531,9 @@ inline __host__ __device__ int delta_run(int tiles, int group) {
     return n < 16 ? n : 16;
 }
 
-// MODE kDeltaSums: a segment's own sum and map, of those that another follows; kDeltaOut: outputs.
-enum DeltaMode : int { kDeltaSums = 0, kDeltaOut = 1 };
+// MODE kDeltaSums: a segment's own sum and map, of those that another follows; kDeltaOut: outputs; kDeltaKeep: for
+// the backward call, the state before each chunk and w.
+enum DeltaMode : int { kDeltaSums = 0, kDeltaOut = 1, kDeltaKeep = 2 };
 
 template <typename T, int DXP, int NT, int MODE, bool VEC> struct WalkShape {
     static constexpr bool OUT = MODE == kDeltaOut;
@@ -492,17 +548,15 @@ template <typename T, int DXP, int NT, int MODE, bool VEC> struct WalkShape {
     static_assert(kBytes <= 160 * 1024, "LDS");
 };
 
+#ifdef __HIP_DEVICE_COMPILE__   // the host pass cannot take the loads' scalar operands and needs the kernels' stubs alone
+// w: the work item, of `tiles` column tiles (the first `ztiles` of values) x heads x places
 template <typename T, int DXP, int NT, int MODE, bool VEC>
-__global__ __launch_bounds__(256, 1) void delta_walk_kernel(const DeltaArgs a, int ztiles, int tiles) {
-#ifdef __HIP_DEVICE_COMPILE__   // the host pass, which cannot take the scalar operands, needs the stub alone
+__device__ __forceinline__ void delta_walk(const DeltaArgs &a, char *lds, uint32_t w, int ztiles, int tiles) {
     using W = WalkShape<T, DXP, NT, MODE, VEC>;
     constexpr bool OUT = W::OUT;
     constexpr int KX = DXP / 32, DZT = W::DZT, NIN = Terms<T>::kIn, NOUT = Terms<T>::kOut, NP = Terms<T>::kP;
     using TX = typename W::TX;
     using TZ = typename W::TZ;
-    __shared__ __attribute__((aligned(1024))) char lds[W::kStages * W::kBytes];
-
-    uint32_t w = dealt(blockIdx.x, delta_run(tiles, a.group));
     const int tile = w % tiles;
     w /= tiles;
     const int h = w % a.H;
@@ -514,14 +568,15 @@ __global__ __launch_bounds__(256, 1) void delta_walk_kernel(const DeltaArgs a, i
     const int64_t chunks = (tk.len + kC - 1) / kC, first = tk.unit * a.seg_chunks;
     const int64_t end = first + a.seg_chunks < chunks ? first + a.seg_chunks : chunks;
     const bool last = end >= chunks;
-    if (!OUT && last) return;
-    const bool map = !OUT && tile >= ztiles;           // this workgroup's columns are the map's
+    if (MODE == kDeltaSums && last) return;
+    const bool map = MODE == kDeltaSums && tile >= ztiles;           // this workgroup's columns are the map's
     const int cols = map ? a.Dk : a.Dv, col0 = (map ? tile - ztiles : tile) * DZT;
     const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), zw = wave * NT * 16;
     // column of accumulator column m of tile t (NT = 2: a lane's two tiles of outputs hold 8 neighbours)
-    auto zcol = [&](int m, int t) { return zw + (NT == 2 ? (m >> 2) * 8 + t * 4 + (m & 3) : m); };
-    auto zgroup = [&](int t) { return zw + (lane & 3) * (NT * 4) + t * 4; };
+    // (kDeltaKeep: neighbouring lanes store neighbours)
+    auto zcol = [&](int m, int t) { return zw + (MODE == kDeltaKeep ? t * 16 + m : NT == 2 ? (m >> 2) * 8 + t * 4 + (m & 3) : m); };
+    auto zgroup = [&](int t) { return zw + (MODE == kDeltaKeep ? t * 16 + (lane & 3) * 4 : (lane & 3) * (NT * 4) + t * 4); };
     auto column = [&](int t) { return col0 + zcol(c, t); };
 
     RowSource<T, DXP, VEC> src_k, src_q;
@@ -530,8 +585,8 @@ __global__ __launch_bounds__(256, 1) void delta_walk_kernel(const DeltaArgs a, i
     src_k.init(a.k, tk.batch * a.kb + tk.row0 * a.kt + hk * a.kh, a.kt, a.Dk, 0);
     if (OUT) src_q.init(a.q, tk.batch * a.qb + tk.row0 * a.qt + hk * a.qh, a.qt, a.Dk, 0);
     src_v.init(a.v, tk.batch * a.vb + tk.row0 * a.vt + h * a.vh, a.vt, map ? 0 : a.Dv, col0);
-    const char *rec0 = a.rec + (first_place(a, tk.seq, kC) * a.H + h) * (int64_t)(delta_pieces(NP) * 1024);
-    const int64_t rec_step = (int64_t)a.H * delta_pieces(NP) * 1024;
+    const char *rec0 = a.rec + (first_place(a, tk.seq, kC) * a.H + h) * a.rec_bytes;
+    const int64_t rec_step = a.H * a.rec_bytes;
     auto bring = [&](int64_t ch, char *stage) __attribute__((always_inline)) {
         const int64_t t = ch * kC;
         const int n = tk.len - t < kC ? (int)(tk.len - t) : kC;
@@ -546,9 +601,9 @@ __global__ __launch_bounds__(256, 1) void delta_walk_kernel(const DeltaArgs a, i
     const int64_t nst = (int64_t)a.Dk * a.Dv;
     {
         const float *p = nullptr;
-        if (OUT && a.seg_state && tk.unit > 0) {
+        if (MODE != kDeltaSums && a.seg_state && tk.unit > 0) {
             p = a.seg_state + (place * a.H + h) * nst;
-        } else if (OUT && a.state0) {
+        } else if (MODE != kDeltaSums && a.state0) {
             const int64_t slot = state_slot(a.slots, a.n_slots, tk.seq);
             if (slot >= 0) p = a.state0 + (slot * a.H + h) * nst;
         }
@@ -565,6 +620,7 @@ __global__ __launch_bounds__(256, 1) void delta_walk_kernel(const DeltaArgs a, i
             // This chunk's loads were issued a chunk ago; four stores followed them (16-bit outputs).  The wait on LDS
             // reads keeps every wave's reads of the other stage before the loads into it.
             if (OUT && sizeof(T) == 2 && ch > first) wait_loads_and_barrier<4>();
+            else if (MODE == kDeltaKeep && ch > first) wait_loads_and_barrier<16>();     // (the states' stores: 16 at least)
             else wait_loads_and_barrier<0>();
             if (ch + 1 < end) bring(ch + 1, lds + ((ch + 1 - first) & 1) * W::kBytes);
         } else {
@@ -578,6 +634,8 @@ __global__ __launch_bounds__(256, 1) void delta_walk_kernel(const DeltaArgs a, i
         const float *vec = reinterpret_cast<const float *>(stage + W::kRec + kDeltaInverse * 1024);
         const bf8 *prod = reinterpret_cast<const bf8 *>((W::kProducts ? stage + W::kRec : rec0 + ch * rec_step) + (kDeltaInverse + kDeltaVectors) * 1024);
 
+        const int64_t kept = (rec0 - a.rec) / a.rec_bytes + ch * a.H;      // (chunk, head)
+        if (MODE == kDeltaKeep) S.keep(a.states + kept * a.dkp * a.dvp, a.dvp, column);
         // k S, and the state's part of the outputs
         f32x4 x[4][NT], o[4][NT];
 #pragma unroll
@@ -648,6 +706,7 @@ __global__ __launch_bounds__(256, 1) void delta_walk_kernel(const DeltaArgs a, i
                 for (int t = 0; t < NT; ++t) u[r][t] = mma_terms<3>(tf, rs[s][t], u[r][t]);
             }
         }
+        if (MODE == kDeltaKeep) keep_rows<NT>(a.wrong + kept * kC * a.dvp, a.dvp, u, column);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
             const f32x4 b = *reinterpret_cast<const f32x4 *>(vec + 128 + 16 * r + 4 * g);
@@ -717,12 +776,561 @@ __global__ __launch_bounds__(256, 1) void delta_walk_kernel(const DeltaArgs a, i
         }
     }
 
-    if (!OUT) {
+    if (MODE == kDeltaSums) {
         float *p = map ? a.seg_map + (place * a.H + h) * (int64_t)a.Dk * a.Dk : a.seg_state + (place * a.H + h) * nst;
         S.store(p, a.Dk, cols, column);
-    } else if (a.state1 && last) {
+    } else if (OUT && a.state1 && last) {
         const int64_t slot = state_slot(a.slots, a.n_slots, tk.seq);
         if (slot >= 0) S.store(a.state1 + (slot * a.H + h) * nst, a.Dk, a.Dv, column);
+    }
+}
+#endif
+
+template <typename T, int DXP, int NT, int MODE, bool VEC>
+__global__ __launch_bounds__(256, 1) void delta_walk_kernel(const DeltaArgs a, int ztiles, int tiles) {
+#ifdef __HIP_DEVICE_COMPILE__
+    using W = WalkShape<T, DXP, NT, MODE, VEC>;
+    __shared__ __attribute__((aligned(1024))) char lds[W::kStages * W::kBytes];
+    delta_walk<T, DXP, NT, MODE, VEC>(a, lds, dealt(blockIdx.x, delta_run(tiles, a.group)), ztiles, tiles);
+#endif
+}
+
+// ---- gradients ------------------------------------------------------------------
+// With G the gradient of the state behind a chunk, dO the outputs' and S the state before it,
+//
+//     x_j = exp(G_last - G_j) G^T k_j + sum_{i >= j} P_ij dO_i,    (I + C^T diag(beta)) y = x  (y: the gradient of u),
+//     dv = beta y,    dbeta_j = y_j . w_j,
+//     G <- exp(G_last) G + sum_i scale exp(G_i) q_i dO_i^T - sum_j exp(G_j) k_j dv_j^T,
+//
+// a walk from the sequence's end that needs no state and is as serial as the forward one: both run side by side in
+// one launch.  What is left is parallel over the chunks (delta_gradients_kernel): with dP_ij = scale exp(G_i - G_j)
+// dO_i . u_j (j <= i) and dC_ij = -exp(G_i - G_j) dv_i . u_j (j < i),
+//
+//     dq_i = scale exp(G_i) S dO_i + sum_j dP_ij k_j,
+//     dk_j = sum_i dP_ij q_i + exp(G_last - G_j) G u_j - exp(G_j) S dv_j + sum_i dC_ij k_i + sum_i dC_ji k_i.
+//
+// Scaling a state by a factor and its values' gradients by the inverse changes nothing, which gives the logarithms'
+// gradient without another product: that of G_i is q_i . dq_i - v_i . dv_i, and of a chunk's last sum <G, S behind> on
+// top, so dlog_decay_t sums those of the chunk's tokens from t on.
+template <typename T, int DXP, int NT, bool VEC> struct BackShape {
+    static constexpr int DZT = NT * 64;
+    using TX = RowTile<T, DXP>;
+    using TZ = RowTile<T, DZT>;
+    static constexpr int kQ = TX::BYTES, kG = 2 * TX::BYTES, kRec = kG + TZ::BYTES;
+    static constexpr bool kProducts = kRec + 28 * 1024 <= 160 * 1024;     // else P stays in memory
+    static constexpr int kPieces = kProducts ? 28 : 16, kBytes = kRec + kPieces * 1024;
+    static constexpr int kStages = VEC && 2 * kBytes <= 156 * 1024 ? 2 : 1;
+    static_assert(kBytes <= 160 * 1024, "LDS");
+};
+
+#ifdef __HIP_DEVICE_COMPILE__
+template <typename T, int DXP, int NT, bool VEC>
+__device__ __forceinline__ void delta_walk_back(const DeltaArgs &a, char *lds, uint32_t w, int tiles) {
+    using W = BackShape<T, DXP, NT, VEC>;
+    constexpr int KX = DXP / 32, DZT = W::DZT, NIN = Terms<T>::kIn;
+    using TX = typename W::TX;
+    using TZ = typename W::TZ;
+    const int tile = w % tiles;
+    w /= tiles;
+    const int h = w % a.H;
+    const int64_t place = w / a.H;
+    if (place >= a.segs) return;
+    Tokens tk;
+    if (!unit_at(a, place, a.seg_chunks * kC, tk)) return;
+    make_scalar(tk);
+    const int64_t chunks = (tk.len + kC - 1) / kC;
+    const int col0 = tile * DZT;
+    const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), zw = wave * NT * 16;
+    auto column = [&](int t) { return col0 + zw + t * 16 + c; };
+
+    RowSource<T, DXP, VEC> src_k, src_q;
+    RowSource<T, DZT, VEC> src_g;
+    const int hk = h / a.group;
+    src_k.init(a.k, tk.batch * a.kb + tk.row0 * a.kt + hk * a.kh, a.kt, a.Dk, 0);
+    src_q.init(a.q, tk.batch * a.qb + tk.row0 * a.qt + hk * a.qh, a.qt, a.Dk, 0);
+    src_g.init(a.dout, tk.batch * a.gb + tk.row0 * a.gt + h * a.gh, a.gt, a.Dv, col0);
+    const int64_t item0 = first_place(a, tk.seq, kC) * a.H + h;
+    // vectors, then the operands
+    const char *rec0 = a.rec + item0 * a.rec_bytes + kDeltaInverse * 1024;
+    const int64_t rec_step = a.H * a.rec_bytes;
+    auto bring = [&](int64_t ch, char *stage) __attribute__((always_inline)) {
+        const int64_t t = ch * kC;
+        const int n = tk.len - t < kC ? (int)(tk.len - t) : kC;
+        src_k.bring(t, n, reinterpret_cast<T *>(stage));
+        src_q.bring(t, n, reinterpret_cast<T *>(stage + W::kQ));
+        src_g.bring(t, n, reinterpret_cast<T *>(stage + W::kG));
+        bring_record<VEC>(rec0 + ch * rec_step, W::kPieces, stage + W::kRec);
+    };
+    if (W::kStages == 2 && chunks > 0) bring(chunks - 1, lds);
+
+    State<KX, NT> G;
+    const int64_t nst = (int64_t)a.Dk * a.Dv;
+    G.load(a.dstate1 ? a.dstate1 + (tk.seq * a.H + h) * nst : nullptr, a.Dk, a.Dv, column);
+
+    for (int64_t back = 0; back < chunks; ++back) {
+        const int64_t ch = chunks - 1 - back;
+        char *stage = lds;
+        if constexpr (W::kStages == 2) {
+            stage += (back & 1) * W::kBytes;
+            if (back > 0) wait_loads_and_barrier<16>();      // (stores followed those loads, 32 at least)
+            else wait_loads_and_barrier<0>();
+            if (ch > 0) bring(ch - 1, lds + ((back + 1) & 1) * W::kBytes);
+        } else {
+            __syncthreads();
+            bring(ch, stage);
+            wait_loads_and_barrier<0>();
+        }
+        const T *tk_ = reinterpret_cast<const T *>(stage), *tq = reinterpret_cast<const T *>(stage + W::kQ),
+                *tg = reinterpret_cast<const T *>(stage + W::kG);
+        const float *vec = reinterpret_cast<const float *>(stage + W::kRec);
+        const f32x4 *inv = reinterpret_cast<const f32x4 *>(stage + W::kRec + kDeltaVectors * 1024);
+        const f32x4 *prod = reinterpret_cast<const f32x4 *>((W::kProducts ? stage + W::kRec : rec0 + ch * rec_step) +
+                                                            (kDeltaVectors + kDeltaInverse) * 1024);
+        const int64_t item = item0 + ch * a.H;
+        G.keep(a.grads + item * a.dkp * a.dvp, a.dvp, column);
+
+        // G^T k
+        f32x4 x[4][NT];
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+            for (int t = 0; t < NT; ++t) x[r][t] = f32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int kk = 0; kk < KX; ++kk) {
+            bf8 st[NT][3];
+#pragma unroll
+            for (int t = 0; t < NT; ++t) G.terms(kk, t, st[t]);
+            bf8 kf[4][NIN];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) in_terms(TX::row8(tk_, 16 * r + c, kk * 32 + g * 8), kf[r]);
+#pragma unroll
+            for (int i = 0; i < NIN; ++i)
+#pragma unroll
+                for (int j = 0; j < 3; ++j)
+                    if (i + j < 3)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+#pragma unroll
+                            for (int t = 0; t < NT; ++t) x[r][t] = Mma<__bf16>::mma(kf[r][i], st[t][j], x[r][t]);
+        }
+        // the outputs' gradients as operands over tokens, as they are and by scale exp(G)
+        bf8 gs[2][NT][3];
+        {
+            bf8 gf[2][NT][NIN];
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                const f32x4 f0 = *reinterpret_cast<const f32x4 *>(vec + 192 + 32 * s + 4 * g),
+                            f1 = *reinterpret_cast<const f32x4 *>(vec + 192 + 32 * s + 16 + 4 * g);
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    const Raw8<T> raw = TZ::col8(tg, s, zw + t * 16 + (lane & 3) * 4, zw + t * 16 + c);
+                    in_terms(raw, gf[s][t]);
+                    f32x4 lo, hi;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) lo[i] = (float)raw.v[i] * f0[i], hi[i] = (float)raw.v[4 + i] * f1[i];
+                    rows_terms<3>(lo, hi, gs[s][t]);
+                }
+            }
+#pragma unroll
+            for (int r = 0, e = 0; r < 4; ++r) {
+                const f32x4 f = *reinterpret_cast<const f32x4 *>(vec + 64 + 16 * r + 4 * g);
+#pragma unroll
+                for (int t = 0; t < NT; ++t) x[r][t] *= f;
+#pragma unroll
+                for (int s = r / 2; s < 2; ++s, ++e) {
+                    bf8 pf[3];
+                    rows_terms<3>(prod[e * 128 + lane], prod[e * 128 + 64 + lane], pf);
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) x[r][t] = mma_terms<3>(pf, gf[s][t], x[r][t]);
+                }
+            }
+        }
+        // y
+        bf8 xs[2][NT][3];
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int t = 0; t < NT; ++t) rows_terms<3>(x[2 * s][t], x[2 * s + 1][t], xs[s][t]);
+        f32x4 y[4][NT];
+#pragma unroll
+        for (int r = 0, e = 0; r < 4; ++r) {
+#pragma unroll
+            for (int t = 0; t < NT; ++t) y[r][t] = f32x4{0, 0, 0, 0};
+#pragma unroll
+            for (int s = r / 2; s < 2; ++s, ++e) {
+                bf8 tf[3];
+                rows_terms<3>(inv[e * 128 + lane], inv[e * 128 + 64 + lane], tf);
+#pragma unroll
+                for (int t = 0; t < NT; ++t) y[r][t] = mma_terms<3>(tf, xs[s][t], y[r][t]);
+            }
+        }
+        keep_rows<NT>(a.dright + item * kC * a.dvp, a.dvp, y, column);
+        // G <- exp(G_last) G + q^T (scale exp(G) dO) - k^T (exp(G) beta y)
+        const float keep = vec[63];
+        bf8 ys[2][NT][3];
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            f32x4 f[2];
+#pragma unroll
+            for (int half = 0; half < 2; ++half)
+                f[half] = -*reinterpret_cast<const f32x4 *>(vec + 32 * s + 16 * half + 4 * g) *
+                          *reinterpret_cast<const f32x4 *>(vec + 128 + 32 * s + 16 * half + 4 * g);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) rows_terms<3>(y[2 * s][t] * f[0], y[2 * s + 1][t] * f[1], ys[s][t]);
+        }
+#pragma unroll
+        for (int kk = 0; kk < KX; ++kk) {
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+#pragma unroll
+                for (int t = 0; t < NT; ++t) G.v[kk][r][t] *= keep;
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                bf8 kf[2][NIN], qf[2][NIN];
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const int group = kk * 32 + (lane & 3) * 8 + r * 4, mine = kk * 32 + (c >> 2) * 8 + r * 4 + (c & 3);
+                    in_terms(TX::col8(tk_, s, group, mine), kf[r]);
+                    in_terms(TX::col8(tq, s, group, mine), qf[r]);
+                }
+#pragma unroll
+                for (int i = 0; i < NIN; ++i)
+#pragma unroll
+                    for (int j = 0; j < 3; ++j)
+                        if (i + j < 3)
+#pragma unroll
+                            for (int r = 0; r < 2; ++r)
+#pragma unroll
+                                for (int t = 0; t < NT; ++t) {
+                                    G.v[kk][r][t] = Mma<__bf16>::mma(kf[r][i], ys[s][t][j], G.v[kk][r][t]);
+                                    G.v[kk][r][t] = Mma<__bf16>::mma(qf[r][i], gs[s][t][j], G.v[kk][r][t]);
+                                }
+            }
+        }
+    }
+    if (a.dstate0) G.store(a.dstate0 + (tk.seq * a.H + h) * nst, a.Dk, a.Dv, column);
+}
+#endif
+
+// Both walks of the backward call: even items forwards, odd ones from the end.
+template <typename T, int DXP, int NT, bool VEC>
+__global__ __launch_bounds__(256, 1) void delta_back_walks_kernel(const DeltaArgs a, int tiles) {
+#ifdef __HIP_DEVICE_COMPILE__
+    using F = WalkShape<T, DXP, NT, kDeltaKeep, VEC>;
+    using R = BackShape<T, DXP, NT, VEC>;
+    constexpr int kF = F::kStages * F::kBytes, kR = R::kStages * R::kBytes;
+    __shared__ __attribute__((aligned(1024))) char lds[kF > kR ? kF : kR];
+    const uint32_t w = dealt(blockIdx.x, delta_run(2 * tiles, a.group));
+    if (w & 1) delta_walk_back<T, DXP, NT, VEC>(a, lds, w / 2, tiles);
+    else delta_walk<T, DXP, NT, kDeltaKeep, VEC>(a, lds, w / 2, tiles, tiles);
+#endif
+}
+
+// One workgroup a (chunk, head); see above.  First each wave takes 16 tokens and forms their rows and columns of dP and
+// dC, left in LDS as operands over tokens; then each takes a quarter of 64 or 128 columns of q and k and all tokens.
+// Tiles of one kind of operand are met by rows of 8 neighbouring values (states, w, y, dO, in memory), k and q by
+// columns (in LDS).  bytes: the states and gradients before it (128 KB at 128 x 128), twice what its tensors hold.
+template <typename T, int DXP, bool VEC>
+__global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void delta_gradients_kernel(const DeltaArgs a) {
+#ifdef __HIP_DEVICE_COMPILE__
+    constexpr int DP = DXP < 128 ? DXP : 128, DA = DP / 64, NIN = Terms<T>::kIn;    // columns at once, tiles of a wave
+    using TX = RowTile<T, DP>;
+    __shared__ __attribute__((aligned(1024))) T tile_k[kC * DP], tile_q[kC * DP];
+    __shared__ __attribute__((aligned(16))) f32x4 by_q[10][64], by_k[10][64], both[16][64];    // dP by queries, by keys; dC + dC^T
+    __shared__ double sums[kC];
+    __shared__ float weights[kC], own[4][kC], rest[4], dots[2][kC];
+    const int64_t item = blockIdx.x;
+    const int64_t place = item / a.H;
+    const int h = (int)(item % a.H), hk = h / a.group;
+    Tokens t;
+    if (!unit_at(a, place, kC, t)) return;
+    make_scalar(t);
+    const int64_t t0 = t.unit * kC;
+    const int n = t.len - t0 < kC ? (int)(t.len - t0) : kC;
+    if (n <= 0) return;
+    const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t gate0 = (t.batch * a.N + t.row0 + t0) * a.H + h;
+    if (wave == 0) {
+        float d = lane < n ? a.log_decay[gate0 + (int64_t)lane * a.H] : 0.0f;
+        d = d < -128.0f ? -128.0f : d;
+        double sum = d;
+#pragma unroll
+        for (int s = 1; s < 64; s <<= 1) {
+            const double up = __shfl_up(sum, s);
+            if (lane >= s) sum += up;
+        }
+        sums[lane] = sum;
+        weights[lane] = lane < n ? a.beta[gate0 + (int64_t)lane * a.H] : 0.0f;
+    }
+    RowSource<T, DP, VEC> src_k, src_q;
+    src_k.init(a.k, t.batch * a.kb + t.row0 * a.kt + hk * a.kh, a.kt, a.Dk, 0);
+    src_q.init(a.q, t.batch * a.qb + t.row0 * a.qt + hk * a.qh, a.qt, a.Dk, 0);
+    src_k.bring(t0, n, tile_k);
+    src_q.bring(t0, n, tile_q);
+    wait_loads_and_barrier<0>();
+
+    const float *S = a.states + item * a.dkp * a.dvp, *G = a.grads + item * a.dkp * a.dvp;
+    const float *W = a.wrong + item * kC * a.dvp, *Y = a.dright + item * kC * a.dvp;
+    const T *go = static_cast<const T *>(a.dout) + t.batch * a.gb + (t.row0 + t0) * a.gt + h * a.gh;
+    const auto gv = wide_view(go);
+    // 8 neighbouring values of row 16 x + c of a padded matrix
+    auto row8 = [&](const float *m, int row, int z, f32x4 &lo, f32x4 &hi) __attribute__((always_inline)) {
+        const f32x4 *p = reinterpret_cast<const f32x4 *>(m + row * a.dvp + z);
+        lo = p[0], hi = p[1];
+    };
+    auto dout8 = [&](int x, int z) __attribute__((always_inline)) {
+        const int row = 16 * x + c, left = row < n ? a.Dv - z : 0;
+        return load_row8<T, VEC>(gv, left > 0 ? (uint32_t)((row * a.gt + z) * (int64_t)sizeof(T)) : kSkip, left);
+    };
+    // u and dv of 16 x + c
+    auto weighted = [&](const float *m, int x, int z, bf8 (&out)[3]) __attribute__((always_inline)) {
+        f32x4 lo, hi;
+        row8(m, 16 * x + c, z, lo, hi);
+        const float b = weights[16 * x + c];
+        rows_terms<3>(lo * b, hi * b, out);
+    };
+    {
+        // columns: the tokens of this wave's tile; rows: those up to them (low: dP by queries, dC by its row) and
+        // from them on (high)
+        f32x4 pq[4], pk[4], cl[4], chh[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) pq[i] = pk[i] = cl[i] = chh[i] = f32x4{0, 0, 0, 0};
+        float dot_v = 0.0f, dot_w = 0.0f;
+        const T *v0 = static_cast<const T *>(a.v) + t.batch * a.vb + (t.row0 + t0) * a.vt + h * a.vh;
+        const auto vv = wide_view(v0);
+        T *dv0 = a.dv ? static_cast<T *>(a.dv) + t.batch * a.dvb + (t.row0 + t0) * a.dvt + h * a.dvh : nullptr;
+        const int mine = 16 * wave + c;
+        const float beta = weights[mine];
+#pragma unroll 1
+        for (int z = g * 8; z < a.dvp; z += 32) {
+            bf8 gx[NIN], ux[3], yx[3];
+            {
+                in_terms(dout8(wave, z), gx);
+                f32x4 wl, wh, yl, yh;
+                row8(W, mine, z, wl, wh);
+                row8(Y, mine, z, yl, yh);
+                const int left = mine < n ? a.Dv - z : 0;
+                const Raw8<T> v = load_row8<T, VEC>(vv, left > 0 ? (uint32_t)((mine * a.vt + z) * (int64_t)sizeof(T)) : kSkip, left);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) dot_w += wl[j] * yl[j] + wh[j] * yh[j];
+                rows_terms<3>(wl * beta, wh * beta, ux);
+                yl *= beta, yh *= beta;
+                rows_terms<3>(yl, yh, yx);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) dot_v += (float)v.v[j] * yl[j] + (float)v.v[4 + j] * yh[j];
+                if (dv0 && left > 0) {
+                    Raw8<T> o;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) o.v[j] = (T)yl[j], o.v[4 + j] = (T)yh[j];
+                    T *p = dv0 + mine * a.dvt + z;
+                    if (VEC && left >= 8) {
+                        __builtin_memcpy(__builtin_assume_aligned(p, 16), &o, sizeof o);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            if (j < left) p[j] = o.v[j];
+                    }
+                }
+            }
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                if (x <= wave) {
+                    bf8 ur[3];
+                    weighted(W, x, z, ur);
+                    pq[x] = mma_terms<3>(ur, gx, pq[x]);
+                    cl[x] = mma_terms<3>(ur, yx, cl[x]);
+                }
+                if (x >= wave) {
+                    bf8 gr[NIN], yr[3];
+                    in_terms(dout8(x, z), gr);
+                    weighted(Y, x, z, yr);
+                    pk[x] = mma_terms<3>(gr, ux, pk[x]);
+                    chh[x] = mma_terms<3>(yr, ux, chh[x]);
+                }
+            }
+        }
+        dot_w += __shfl_xor(dot_w, 16), dot_v += __shfl_xor(dot_v, 16);
+        dot_w += __shfl_xor(dot_w, 32), dot_v += __shfl_xor(dot_v, 32);
+        if (g == 0) {
+            dots[0][mine] = dot_v;
+            if (a.dbeta && mine < n) a.dbeta[gate0 + (int64_t)mine * a.H] = dot_w;
+        }
+        const double gm = sums[mine];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            f32x4 q{0, 0, 0, 0}, k{0, 0, 0, 0}, b{0, 0, 0, 0};
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int row = 16 * x + 4 * g + r;
+                const float f = exp_of(row <= mine ? gm - sums[row] : sums[row] - gm);
+                if (row <= mine) q[r] = pq[x][r] * (f * a.scale);
+                if (row >= mine) k[r] = pk[x][r] * (f * a.scale);
+                b[r] = row < mine ? -cl[x][r] * f : row > mine ? -chh[x][r] * f : 0.0f;
+            }
+            if (x <= wave) by_q[wave * (wave + 1) / 2 + x][lane] = q;
+            if (x >= wave) by_k[wave * (9 - wave) / 2 + x - wave][lane] = k;       // 4 + 3 + .. tiles before
+            both[wave * 4 + x][lane] = b;
+        }
+    }
+    __syncthreads();
+
+    float dot_q = 0.0f, inner = 0.0f;
+    float mine_q[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    const float g_last = exp_of(sums[63]);
+#pragma unroll 1
+    for (int col0 = 0; col0 < DXP; col0 += DP) {
+        if (col0 > 0) {
+            if (col0 >= a.Dk) break;
+            __syncthreads();
+            src_k.col0 = src_q.col0 = col0;
+            src_k.bring(t0, n, tile_k);
+            src_q.bring(t0, n, tile_q);
+            wait_loads_and_barrier<0>();
+        }
+        f32x4 qa[DA][4], ka[DA][4], va[DA][4];      // rows of the states x tokens
+#pragma unroll
+        for (int d = 0; d < DA; ++d)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) qa[d][x] = ka[d][x] = va[d][x] = f32x4{0, 0, 0, 0};
+#pragma unroll 1
+        for (int z = g * 8; z < a.dvp; z += 32) {
+            bf8 sf[DA][3], gf[DA][3];
+#pragma unroll
+            for (int d = 0; d < DA; ++d) {
+                const int row = col0 + (wave * DA + d) * 16 + c;
+                f32x4 sl, sh, gl, gh;
+                row8(S, row, z, sl, sh);
+                row8(G, row, z, gl, gh);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) inner += sl[j] * gl[j] + sh[j] * gh[j];
+                rows_terms<3>(sl, sh, sf[d]);
+                rows_terms<3>(gl, gh, gf[d]);
+            }
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                bf8 gx[NIN], ux[3], vx[3];
+                in_terms(dout8(x, z), gx);
+                weighted(W, x, z, ux);
+                weighted(Y, x, z, vx);
+#pragma unroll
+                for (int d = 0; d < DA; ++d) {
+                    qa[d][x] = mma_terms<3>(sf[d], gx, qa[d][x]);
+                    ka[d][x] = mma_terms<3>(gf[d], ux, ka[d][x]);
+                    va[d][x] = mma_terms<3>(sf[d], vx, va[d][x]);
+                }
+            }
+        }
+        // 4 values of token 16 x + c at this lane's rows of tile d
+        auto row4 = [&](const T *tile, int d, int x, float (&f)[4]) __attribute__((always_inline)) {
+            const int col = (wave * DA + d) * 16 + 4 * g;
+            const T *p = TX::at(tile, 16 * x + c, col / TX::E) + col % TX::E;
+            struct Four { T v[4]; };
+            const Four v = *reinterpret_cast<const Four *>(p);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) f[j] = (float)v.v[j];
+        };
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            const double gx = sums[16 * x + c];
+            const float first = exp_of(gx), last = exp_of(sums[63] - gx);
+#pragma unroll
+            for (int d = 0; d < DA; ++d) {
+                qa[d][x] *= a.scale * first;
+                ka[d][x] *= last;
+                float k[4];
+                row4(tile_k, d, x, k);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) dot_q += k[r] * ka[d][x][r];      // <G, what the chunk adds to the state>
+                ka[d][x] -= va[d][x] * first;
+            }
+        }
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            bf8 kf[DA][NIN], qf[DA][NIN];
+#pragma unroll
+            for (int d = 0; d < DA; ++d) {
+                const int base = (wave * DA + d) * 16;
+                in_terms(TX::col8(tile_k, s, base + (lane & 3) * 4, base + c), kf[d]);
+                in_terms(TX::col8(tile_q, s, base + (lane & 3) * 4, base + c), qf[d]);
+            }
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const f32x4 zero{0, 0, 0, 0};
+                const int lo = 2 * s, hi = 2 * s + 1;
+                bf8 m[3];
+                if (lo <= x) {
+                    rows_terms<3>(by_q[x * (x + 1) / 2 + lo][lane], hi <= x ? by_q[x * (x + 1) / 2 + hi][lane] : zero, m);
+#pragma unroll
+                    for (int d = 0; d < DA; ++d) qa[d][x] = mma_terms<3>(kf[d], m, qa[d][x]);
+                }
+                if (hi >= x) {
+                    rows_terms<3>(lo >= x ? by_k[x * (9 - x) / 2 + lo - x][lane] : zero, by_k[x * (9 - x) / 2 + hi - x][lane], m);
+#pragma unroll
+                    for (int d = 0; d < DA; ++d) ka[d][x] = mma_terms<3>(qf[d], m, ka[d][x]);
+                }
+                rows_terms<3>(both[x * 4 + lo][lane], both[x * 4 + hi][lane], m);
+#pragma unroll
+                for (int d = 0; d < DA; ++d) ka[d][x] = mma_terms<3>(kf[d], m, ka[d][x]);
+            }
+        }
+        // out: lane (g, c) has 4 neighbouring columns of token 16 x + c
+        auto put = [&](void *base, int64_t sb, int64_t st, int64_t sh, const f32x4 &v, int d, int x) __attribute__((always_inline)) {
+            const int row = 16 * x + c, col = col0 + (wave * DA + d) * 16 + 4 * g, left = a.Dk - col;
+            if (!base || row >= n || left <= 0) return;
+            if (a.parts) {
+                float *p = static_cast<float *>(base) + ((t.batch * a.N + t.row0 + t0 + row) * a.H + h) * (int64_t)a.Dk + col;
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    if (r < left) p[r] = v[r];
+                return;
+            }
+            T *p = static_cast<T *>(base) + t.batch * sb + (t.row0 + t0 + row) * st + hk * sh + col;
+            struct Four { T v[4]; } o;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) o.v[r] = (T)v[r];
+            if (VEC && left >= 4) {
+                __builtin_memcpy(__builtin_assume_aligned(p, 4 * sizeof(T)), &o, sizeof o);
+            } else {
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    if (r < left) p[r] = o.v[r];
+            }
+        };
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+#pragma unroll
+            for (int d = 0; d < DA; ++d) {
+                float q[4];
+                row4(tile_q, d, x, q);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) mine_q[x] += q[r] * qa[d][x][r];
+                put(a.dq, a.dqb, a.dqt, a.dqh, qa[d][x], d, x);
+                put(a.dk, a.dkb, a.dkt, a.dkh, ka[d][x], d, x);
+            }
+    }
+    if (!a.dlog_decay) return;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+        mine_q[x] += __shfl_xor(mine_q[x], 16);
+        mine_q[x] += __shfl_xor(mine_q[x], 32);
+        if (g == 0) own[wave][16 * x + c] = mine_q[x];
+    }
+    float behind = dot_q + g_last * inner;
+#pragma unroll
+    for (int s = 1; s < 64; s <<= 1) behind += __shfl_xor(behind, s);
+    if (lane == 0) rest[wave] = behind;
+    __syncthreads();
+    if (wave == 0) {
+        double sum = (double)((own[0][lane] + own[1][lane]) + (own[2][lane] + own[3][lane])) - (double)dots[0][lane];
+#pragma unroll
+        for (int s = 1; s < 64; s <<= 1) {
+            const double down = __shfl_down(sum, s);
+            if (lane + s < 64) sum += down;
+        }
+        sum += (double)((rest[0] + rest[1]) + (rest[2] + rest[3]));
+        if (lane < n) a.dlog_decay[gate0 + (int64_t)lane * a.H] = (float)sum;
     }
 #endif
 }
@@ -852,19 +1460,34 @@ __global__ __launch_bounds__(256) void delta_step_kernel(const DeltaStep a) {
 }
 
 // ---- host side of one storage type ----------------------------------------
-template <typename T> static hipError_t delta_prepare_typed(const DeltaArgs &a, hipStream_t s) {
+template <typename T, bool VEC, bool BACK> static hipError_t delta_prepare_launch(const DeltaArgs &a, hipStream_t s) {
     const unsigned grid = (unsigned)((a.chunks * a.H + 3) / 4);
     if (grid == 0) return hipSuccess;
-    if (a.vec) {
-        if (a.Dk <= 64) delta_prepare_kernel<T, 64, true><<<grid, 256, 0, s>>>(a);
-        else if (a.Dk <= 128) delta_prepare_kernel<T, 128, true><<<grid, 256, 0, s>>>(a);
-        else delta_prepare_kernel<T, 256, true><<<grid, 256, 0, s>>>(a);
-    } else {
-        if (a.Dk <= 64) delta_prepare_kernel<T, 64, false><<<grid, 256, 0, s>>>(a);
-        else if (a.Dk <= 128) delta_prepare_kernel<T, 128, false><<<grid, 256, 0, s>>>(a);
-        else delta_prepare_kernel<T, 256, false><<<grid, 256, 0, s>>>(a);
-    }
+    if (a.Dk <= 64) delta_prepare_kernel<T, 64, VEC, BACK><<<grid, 256, 0, s>>>(a);
+    else if (a.Dk <= 128) delta_prepare_kernel<T, 128, VEC, BACK><<<grid, 256, 0, s>>>(a);
+    else delta_prepare_kernel<T, 256, VEC, BACK><<<grid, 256, 0, s>>>(a);
     return hipGetLastError();
+}
+template <typename T> static hipError_t delta_prepare_typed(const DeltaArgs &a, hipStream_t s) {
+    if (a.states) return a.vec ? delta_prepare_launch<T, true, true>(a, s) : delta_prepare_launch<T, false, true>(a, s);
+    return a.vec ? delta_prepare_launch<T, true, false>(a, s) : delta_prepare_launch<T, false, false>(a, s);
+}
+template <typename T, int DXP, int NT, bool VEC> static hipError_t delta_back_launch(const DeltaArgs &a, hipStream_t s) {
+    const int tiles = a.dvp / (NT * 64);
+    const int64_t items = 2 * a.segs * a.H * tiles, round = 8 * (int64_t)delta_run(2 * tiles, a.group);
+    delta_back_walks_kernel<T, DXP, NT, VEC><<<(unsigned)((items + round - 1) / round * round), 256, 0, s>>>(a, tiles);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || a.chunks == 0) return e;
+    delta_gradients_kernel<T, DXP, VEC><<<(unsigned)(a.chunks * a.H), 256, 0, s>>>(a);
+    return hipGetLastError();
+}
+template <typename T, bool VEC> static hipError_t delta_back(const DeltaArgs &a, hipStream_t s) {
+    if (a.Dk > 128) return delta_back_launch<T, 256, 1, VEC>(a, s);
+    if (a.Dk > 64) return a.wide ? delta_back_launch<T, 128, 2, VEC>(a, s) : delta_back_launch<T, 128, 1, VEC>(a, s);
+    return a.wide ? delta_back_launch<T, 64, 2, VEC>(a, s) : delta_back_launch<T, 64, 1, VEC>(a, s);
+}
+template <typename T> static hipError_t delta_bwd_typed(const DeltaArgs &a, hipStream_t s) {
+    return a.vec ? delta_back<T, true>(a, s) : delta_back<T, false>(a, s);
 }
 template <typename T, int DXP, int NT, int MODE, bool VEC> static hipError_t delta_walk_launch(const DeltaArgs &a, hipStream_t s) {
     const int ztiles = (a.Dv + NT * 64 - 1) / (NT * 64), tiles = ztiles + (MODE == kDeltaSums ? (a.Dk + NT * 64 - 1) / (NT * 64) : 0);
@@ -908,6 +1531,7 @@ template <typename T> static hipError_t delta_step_typed(const DeltaStep &a, boo
 #define FFTCONV_DELTA_TYPE(NAME, T)                                                                                  \
     hipError_t launch_delta_prepare_##NAME(const DeltaArgs &a, hipStream_t s) { return delta_prepare_typed<T>(a, s); } \
     hipError_t launch_delta_fwd_##NAME(const DeltaArgs &a, hipStream_t s) { return delta_fwd_typed<T>(a, s); }         \
+    hipError_t launch_delta_bwd_##NAME(const DeltaArgs &a, hipStream_t s) { return delta_bwd_typed<T>(a, s); }         \
     hipError_t launch_delta_step_##NAME(const DeltaStep &a, bool vec, hipStream_t s) { return delta_step_typed<T>(a, vec, s); }
 
 }  // namespace fftconv

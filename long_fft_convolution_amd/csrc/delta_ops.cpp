@@ -190,6 +190,7 @@ fftconv_status_t fftconv_delta_fwd(const void *q, const void *k, const void *v, 
     const DeltaFwdLayout l = fwd_layout(s, c);
     a.seg_chunks = c.seg_chunks, a.segs = c.segs, a.wide = c.wide;
     a.rec = static_cast<char *>(workspace);
+    a.rec_bytes = (int64_t)record_bytes(s);
     a.seg_state = c.cut ? reinterpret_cast<float *>(a.rec + l.states) : nullptr;
     a.seg_map = c.cut ? reinterpret_cast<float *>(a.rec + l.maps) : nullptr;
     hipError_t e = launch_prepare(dtype, a, stream);
@@ -234,4 +235,119 @@ fftconv_status_t fftconv_delta_step(const void *q, const void *k, const void *v,
                          : dtype == FFTCONV_F16 ? launch_delta_step_f16(a, vec, stream)
                                                 : launch_delta_step_bf16(a, vec, stream);
     return hip_status("delta step", e);
+}
+
+// ---- gradients ----------------------------------------------------------------
+namespace {
+// Workspace of the backward call: the chunks' records, states, their gradients, w and y, and fp32 gradients of the heads
+// that share a query/key head.
+struct DeltaBwdLayout {
+    bool wide;
+    int64_t dkp, dvp;
+    size_t states, grads, wrong, dright, dq, dk, total;
+};
+DeltaBwdLayout bwd_layout(const DeltaShape &s) {
+    DeltaBwdLayout l{};
+    l.wide = fwd_cut(s).wide;
+    l.dkp = s.Dk <= 64 ? 64 : s.Dk <= 128 ? 128 : 256;
+    l.dvp = round_up(s.Dv, l.wide ? 128 : 64);
+    const size_t items = (size_t)s.places(kDeltaChunk) * s.H;
+    l.states = items * kDeltaBackPieces * 1024;
+    l.grads = l.states + items * l.dkp * l.dvp * 4;
+    l.wrong = l.grads + items * l.dkp * l.dvp * 4;
+    l.dright = l.wrong + items * kDeltaChunk * l.dvp * 4;
+    l.dq = l.dright + items * kDeltaChunk * l.dvp * 4;
+    const size_t part = s.H == s.Hk ? 0 : align_up((size_t)s.T() * s.H * s.Dk * 4, 256);
+    l.dk = l.dq + part;
+    l.total = l.dk + part;
+    return l;
+}
+}  // namespace
+
+size_t fftconv_delta_bwd_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t Hk, int64_t Dk, int64_t Dv,
+                                         fftconv_dtype_t dtype) {
+    if (!dtype_ok(dtype) || B < 1 || T < 1 || H < 1 || Hk < 1 || Dk < 1 || Dv < 1 || Dk > kMaxHeadDim || Dv > kMaxHeadDim) return 0;
+    const DeltaShape equal{B, ceil_div(T, B), H, Hk, Dk, Dv, dtype, false}, packed{B, T, H, Hk, Dk, Dv, dtype, true};
+    return std::max(bwd_layout(equal).total, bwd_layout(packed).total);
+}
+
+fftconv_status_t fftconv_delta_bwd(const void *dout, const void *q, const void *k, const void *v, const float *log_decay,
+                                   const float *beta, void *dq, void *dk, void *dv, float *dlog_decay, float *dbeta,
+                                   const int64_t *strides, const float *state_in, const float *dstate_out,
+                                   float *dstate_in, const int32_t *cu_seqlens, int64_t B, int64_t N, int64_t H,
+                                   int64_t Hk, int64_t Dk, int64_t Dv, float scale, fftconv_dtype_t dtype,
+                                   void *workspace, size_t workspace_bytes, hipStream_t stream) {
+    const DeltaShape s{B, N, H, Hk, Dk, Dv, (int)dtype, cu_seqlens != nullptr};
+    fftconv_status_t st = check_shape(s, scale);
+    if (st != FFTCONV_OK) return st;
+    if (B == 0 || H == 0) return ok();
+    auto at = [&](int i) { return strides ? strides + 3 * i : nullptr; };
+    const View vd = heads_view("dout", dout, s, H, Dv, at(0)), vq = heads_view("q", q, s, Hk, Dk, at(1)),
+               vk = heads_view("k", k, s, Hk, Dk, at(2)), vv = heads_view("v", v, s, H, Dv, at(3)),
+               gq = heads_view("dq", dq, s, Hk, Dk, at(4)), gk = heads_view("dk", dk, s, Hk, Dk, at(5)),
+               gv = heads_view("dv", dv, s, H, Dv, at(6));
+    const View vg = gate_view("log_decay", log_decay, s), vb = gate_view("beta", beta, s),
+               gg = gate_view("dlog_decay", dlog_decay, s), gb = gate_view("dbeta", dbeta, s);
+    for (const View *x : {&vd, &vq, &vk, &vv, &vg, &vb})
+        if ((st = check_view(*x, true, false)) != FFTCONV_OK) return st;
+    for (const View *x : {&gq, &gk, &gv, &gg, &gb})
+        if ((st = check_view(*x, false, true)) != FFTCONV_OK) return st;
+    for (const View *x : {&vd, &vq, &vk, &vv, &gq, &gk, &gv})
+        if (x->p && (st = check_reach(*x)) != FFTCONV_OK) return st;
+    const View si = state_view("state_in", state_in, B, s), dso = state_view("dstate_out", dstate_out, B, s),
+               dsi = state_view("dstate_in", dstate_in, B, s);
+    for (const View *x : {&si, &dso, &dsi})
+        if ((st = check_view(*x, false, false)) != FFTCONV_OK) return st;
+    if ((st = check_ints({cu_seqlens})) != FFTCONV_OK) return st;
+    const size_t need = fftconv_delta_bwd_workspace_bytes(B, s.T(), H, Hk, Dk, Dv, dtype);
+    if ((st = check_workspace(workspace, workspace_bytes, need)) != FFTCONV_OK) return st;
+    const View ws = raw_view("workspace", need ? workspace : nullptr, (int64_t)need);
+    const View outs[] = {gq, gk, gv, gg, gb, dsi, ws},
+               ins[] = {vd, vq, vk, vv, vg, vb, si, dso, raw_view("cu_seqlens", cu_seqlens, (B + 1) * 4)};
+    if ((st = check_apart(outs, 7, ins, 9)) != FFTCONV_OK) return st;
+    if (s.T() == 0 && !dstate_in) return ok();
+
+    DeltaArgs a = common_args(s, vq, vk, vv, log_decay, beta, scale, cu_seqlens);
+    const DeltaBwdLayout l = bwd_layout(s);
+    char *base = static_cast<char *>(workspace);
+    const bool shared = H != Hk;
+    a.state0 = state_in, a.dstate1 = dstate_out, a.dstate0 = dstate_in;
+    a.seg_chunks = (int64_t(1) << 31) / kDeltaChunk, a.segs = s.places(a.seg_chunks * kDeltaChunk);
+    a.wide = l.wide, a.dkp = (int)l.dkp, a.dvp = (int)l.dvp;
+    a.rec = base, a.rec_bytes = kDeltaBackPieces * 1024;
+    a.states = reinterpret_cast<float *>(base + l.states), a.grads = reinterpret_cast<float *>(base + l.grads);
+    a.wrong = reinterpret_cast<float *>(base + l.wrong), a.dright = reinterpret_cast<float *>(base + l.dright);
+    a.dout = dout, a.gb = vd.stride[0], a.gt = vd.stride[1], a.gh = vd.stride[2];
+    a.parts = shared;
+    a.dq = shared && dq ? base + l.dq : dq, a.dk = shared && dk ? base + l.dk : dk, a.dv = dv;
+    a.dqb = gq.stride[0], a.dqt = gq.stride[1], a.dqh = gq.stride[2];
+    a.dkb = gk.stride[0], a.dkt = gk.stride[1], a.dkh = gk.stride[2];
+    a.dvb = gv.stride[0], a.dvt = gv.stride[1], a.dvh = gv.stride[2];
+    a.dlog_decay = dlog_decay, a.dbeta = dbeta;
+    a.vec = chunk_vec(vq) && chunk_vec(vk) && chunk_vec(vv) && chunk_vec(vd);
+    for (const View *x : {&gq, &gk, &gv}) a.vec = a.vec && (!x->p || chunk_vec(*x));
+    hipError_t e = launch_prepare(dtype, a, stream);
+    if (e == hipSuccess)
+        e = dtype == FFTCONV_F32   ? launch_delta_bwd_f32(a, stream)
+            : dtype == FFTCONV_F16 ? launch_delta_bwd_f16(a, stream)
+                                   : launch_delta_bwd_bf16(a, stream);
+    if (e == hipSuccess && shared && (dq || dk) && s.T() > 0) {
+        DecayGroupSum g{};
+        const View *grads[] = {&gq, &gk};
+        const size_t parts[] = {l.dq, l.dk};
+        for (int i = 0; i < 2; ++i) {
+            const View &o = *grads[i];
+            g.src[i] = reinterpret_cast<const float *>(base + parts[i]);
+            g.dst[i] = const_cast<void *>(o.p);
+            g.D[i] = (int)o.row;
+            g.db[i] = o.stride[0], g.dt[i] = o.stride[1], g.dh[i] = o.stride[2];
+            g.vec[i] = o.row % 4 == 0 && aligned(o.p, 4 * o.bytes_per) && o.stride[0] % 4 == 0 && o.stride[1] % 4 == 0 &&
+                       o.stride[2] % 4 == 0;
+        }
+        g.B = s.packed ? 1 : B, g.N = N, g.cu = cu_seqlens, g.seqs = B, g.Hk = (int)Hk, g.group = (int)(H / Hk);
+        e = dtype == FFTCONV_F32   ? launch_decay_group_sum_f32(g, stream)
+            : dtype == FFTCONV_F16 ? launch_decay_group_sum_f16(g, stream)
+                                   : launch_decay_group_sum_bf16(g, stream);
+    }
+    return hip_status("delta rule gradients", e);
 }

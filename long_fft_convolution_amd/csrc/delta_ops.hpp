@@ -19,6 +19,10 @@ constexpr int delta_pieces(int terms) { return (kDeltaInverse + kDeltaVectors + 
 // terms of the masked products: bf16 results see them rounded once, like the state; fp16's need two, fp32's three
 constexpr int delta_terms(int elem_bytes, bool narrow) { return elem_bytes == 4 ? 3 : narrow ? 2 : 1; }
 
+// The backward call's record: the inverse of I + C diag(beta), the vectors, then, as operands over tokens from the
+// other side, the inverse of I + C^T diag(beta) and P^T, all in fp32.
+constexpr int kDeltaBackPieces = 3 * kDeltaInverse + 4 * kDeltaVectors;
+
 struct DeltaArgs {
     const void *q, *k, *v;           // q and k have H / group heads, v and out H
     void *out;
@@ -35,10 +39,24 @@ struct DeltaArgs {
     int64_t chunks;                  // places for chunks (an upper bound when packed)
     int64_t seg_chunks, segs;        // chunks of a segment, places for segments
     char *rec;                       // (chunks, H) records
+    int64_t rec_bytes;
     float *seg_state;                // (segs, H) Dk x Dv: a segment's own sum, then the state before it; null: one segment each
     float *seg_map;                  // (segs, H) Dk x Dk: what a segment makes of the state before it
-    int vec;                         // rows of q, k, v, out in whole aligned 16-byte pieces
+    int vec;                         // rows of the tensors in whole aligned 16-byte pieces
     int wide;                        // 128 columns of the state a workgroup, else 64
+
+    // backward
+    const void *dout;
+    int64_t gb, gt, gh;
+    const float *dstate1;            // gradients of the final states or null
+    float *dstate0;                  // gradients of the initial states or null
+    int dkp, dvp;                    // padded widths of what follows
+    float *states, *grads;           // (chunks, H) dkp x dvp: state before a chunk, gradient of the state behind it
+    float *wrong, *dright;           // (chunks, H) 64 x dvp: w, and the gradient of u (its own and what later tokens of the chunk add)
+    void *dq, *dk, *dv;              // null = skip; dq and dk fp32 (tokens, H, Dk) parts where heads share them
+    int64_t dqb, dqt, dqh, dkb, dkt, dkh, dvb, dvt, dvh;
+    int parts;                       // dq and dk are such parts
+    float *dlog_decay, *dbeta;       // null = skip
 };
 
 struct DeltaStep {
@@ -56,6 +74,7 @@ struct DeltaStep {
 #define FFTCONV_DELTA_LAUNCHERS(NAME)                                                       \
     hipError_t launch_delta_prepare_##NAME(const DeltaArgs &a, hipStream_t stream);         \
     hipError_t launch_delta_fwd_##NAME(const DeltaArgs &a, hipStream_t stream);             \
+    hipError_t launch_delta_bwd_##NAME(const DeltaArgs &a, hipStream_t stream);             \
     hipError_t launch_delta_step_##NAME(const DeltaStep &a, bool vec, hipStream_t stream);
 FFTCONV_DELTA_LAUNCHERS(f32)
 FFTCONV_DELTA_LAUNCHERS(f16)

@@ -85,6 +85,32 @@ def test_prompt(B, N, H, Hk, Dk, Dv, dtype):
         _close(S[b], ws, FP32, f"state[{b}]")
 
 
+NAMES = ("dq", "dk", "dv", "dlog_decay", "dbeta")
+
+
+def _grads_close(got, want, dtype, where):
+    for name, x, y in zip(NAMES, got, want):
+        # 16 bits: the result's own rounding, everything before it is fp32
+        _close(x, y, FP32 if x.dtype == torch.float32 else TOL[dtype], f"{name}{where}")
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("B,N,H,Hk,Dk,Dv", PROMPTS)
+def test_gradients(B, N, H, Hk, Dk, Dv, dtype):
+    _say(f"gradients {dtype} B={B} N={N} H={H}/{Hk} Dk={Dk} Dv={Dv}")
+    ins = _inputs((B, N), H, Hk, Dk, Dv, dtype, N + H)
+    dout = _rand((B, N, H, Dv), DT[dtype], 9)
+    S0, dS = (_rand((B, H, Dk, Dv), torch.float32, s) if N % 2 else None for s in (5, 6))
+    got = fc.delta_attention_bwd(*_gpu(*ins, dout), scale=0.25, state_in=None if S0 is None else S0.cuda(),
+                                 dstate_out=None if dS is None else dS.cuda())
+    for b in range(0, B, max(1, B // 3)):
+        want = seq.delta_bwd(_f64(dout[b]), *(_f64(t[b]) for t in ins), 0.25, None if S0 is None else _f64(S0[b]),
+                             None if dS is None else _f64(dS[b]))
+        _grads_close([t[b] for t in got[:5]], want, dtype, f"[{b}]")
+        if S0 is not None:
+            _close(got[5][b], want[5], FP32, f"dstate_in[{b}]")
+
+
 LENGTHS = [(0,), (1,), (0, 1, 63, 64, 65, 0), (5, 700, 0, 300, 1), (0, 0, 0), tuple(range(1, 40)), (300,) + (1,) * 300,
            (2500, 3)]
 
@@ -114,6 +140,33 @@ def test_packed(lens, dtype):
         want, ws_ = seq.delta_fwd(*(_f64(t[x:y]) for t in ins), 0.25, _f64(S0[b]))
         _close(out[x:y], want, TOL[dtype], f"out[{b}]")
         _close(S[b], ws_, FP32, f"state[{b}]")
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("lens", LENGTHS)
+def test_packed_gradients(lens, dtype):
+    _say(f"packed gradients {dtype} lengths {str(lens)[:60]}")
+    H, Hk, Dk, Dv, B, T = 4, 2, 64, 96, len(lens), sum(lens)
+    lead, behind = 3, 2
+    ins = _inputs((lead + T + behind,), H, Hk, Dk, Dv, dtype, T)
+    ends = lead + np.concatenate([[0], np.cumsum(lens)])
+    cu = torch.tensor(ends, dtype=torch.int32).cuda()
+    S0, dS = _rand((B, H, Dk, Dv), torch.float32, 5), _rand((B, H, Dk, Dv), torch.float32, 6)
+    dout = _rand(ins[2].shape, DT[dtype], 9)
+    q, k, v, a, beta, do = _gpu(*ins, dout)
+    grads = [torch.full_like(t, 7.0) for t in (q, k, v, a, beta)]
+    dS0 = torch.empty((B, H, Dk, Dv), device="cuda")
+    ws = torch.empty(max(1, fc.fftconv_delta_bwd_workspace_bytes(B, lead + T + behind, H, Hk, Dk, Dv, q.dtype)), dtype=torch.uint8,
+                     device="cuda")
+    fc.fftconv_delta_bwd(do, q, k, v, a, beta, *grads, 0.25, S0.cuda(), dS.cuda(), dS0, cu, ws)
+    for t in grads:
+        assert (t[:lead] == 7).all() and (t[lead + T:] == 7).all()
+    for b, (x, y) in enumerate(zip(ends, ends[1:])):
+        if b > 12 and b < B - 2:
+            continue
+        want = seq.delta_bwd(_f64(dout[x:y]), *(_f64(t[x:y]) for t in ins), 0.25, _f64(S0[b]), _f64(dS[b]))
+        _grads_close([t[x:y] for t in grads], want, dtype, f"[{b}]")
+        _close(dS0[b], want[5], FP32, f"dstate_in[{b}]")
 
 
 @pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
