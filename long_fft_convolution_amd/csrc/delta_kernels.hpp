@@ -47,7 +47,7 @@
 
 namespace fftconv {
 
-constexpr int kC = kDeltaChunk;
+constexpr int kC = kDeltaChunk, kLdsBytes = 160 * 1024;
 typedef Mma<__bf16>::v8 bf8;
 
 // ---- sequences, chunks, segments -------------------------------------------
@@ -108,6 +108,37 @@ template <> struct Terms<__bf16> { static constexpr int kIn = 1, kOut = 2, kP = 
 template <> struct Terms<_Float16> { static constexpr int kIn = 2, kOut = 2, kP = delta_terms(2, true); };
 template <> struct Terms<float> { static constexpr int kIn = 3, kOut = 3, kP = delta_terms(4, false); };
 
+// Eight fp32 values as N bf16 terms.  bf16 is the upper half of fp32: cutting it off leaves an exact rest, so three
+// terms of 8 bits hold all 24; the last of two is rounded.  A pair's rest costs two dot products of the pair with
+// (-1, 0) and (0, -1), where taking the halves apart first would cost two more instructions.
+template <int N> __device__ __forceinline__ void split_terms(const float (&x)[8], bf8 (&out)[N]) {
+    typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
+    float rest[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) rest[j] = x[j];
+#pragma unroll
+    for (int s = 0; s < N; ++s) {
+        if (s == N - 1 && N < 3) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) out[s][j] = (__bf16)rest[j];
+            continue;
+        }
+        // (as register operands: an inline constant -1.0 would be met as fp32)
+        uint32_t low = 0x0000bf80u, high = 0xbf800000u, u[4];
+        asm("" : "+s"(low), "+s"(high));
+#pragma unroll
+        for (int j = 0; j < 4; ++j)     // upper halves of two values: bytes 2, 3 of each
+            u[j] = __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, rest[2 * j + 1]), __builtin_bit_cast(uint32_t, rest[2 * j]), 0x07060302u);
+        __builtin_memcpy(&out[s], u, 16);
+        if (s + 1 < N) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                rest[2 * j] = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf2, u[j]), __builtin_bit_cast(bf2, low), rest[2 * j], false);
+                rest[2 * j + 1] = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf2, u[j]), __builtin_bit_cast(bf2, high), rest[2 * j + 1], false);
+            }
+        }
+    }
+}
 template <typename T> struct Raw8 { T v[8]; };
 template <typename T> __device__ __forceinline__ void in_terms(const Raw8<T> &x, bf8 (&out)[Terms<T>::kIn]) {
     if constexpr (sizeof(T) == 2 && Terms<T>::kIn == 1) {
@@ -116,18 +147,13 @@ template <typename T> __device__ __forceinline__ void in_terms(const Raw8<T> &x,
         float f[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) f[j] = (float)x.v[j];
-        split8<__bf16, Terms<T>::kIn>(f, out);
+        split_terms(f, out);
     }
 }
 // two accumulators of rows 16 (2 s) and 16 (2 s + 1) as the operand over their 32 rows
 template <int N> __device__ __forceinline__ void rows_terms(const f32x4 &a, const f32x4 &b, bf8 (&out)[N]) {
     float f[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
-    if constexpr (N == 1) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) out[0][j] = (__bf16)f[j];
-    } else {
-        split8<__bf16, N>(f, out);
-    }
+    split_terms(f, out);
 }
 // acc += sum of the products of terms i + j < MOST
 template <int MOST, int NA, int NB> __device__ __forceinline__ f32x4 mma_terms(const bf8 (&a)[NA], const bf8 (&b)[NB], f32x4 acc) {
@@ -320,18 +346,18 @@ template <typename T, int DXP, bool VEC, bool BACK> __global__ __launch_bounds__
         invert_unit_lower(M);
     };
     put(false);
-    f32x4 *out = reinterpret_cast<f32x4 *>(rec);
+    bf8 *out = reinterpret_cast<bf8 *>(rec);
     bf8 *outp = reinterpret_cast<bf8 *>(rec + (kDeltaInverse + kDeltaVectors) * 1024);
 #pragma unroll
     for (int i = 0, e = 0; i < 4; ++i)
 #pragma unroll
         for (int s = 0; s <= i / 2; ++s, ++e) {
             float p[8];
+            f32x4 m[2];
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
                 const int j = 2 * s + half;      // block of columns
-                out[(e * 2 + half) * 64 + lane] =
-                    j <= i ? *reinterpret_cast<const f32x4 *>(M + (16 * i + c) * kLd + 16 * j + 4 * g) : f32x4{0, 0, 0, 0};
+                m[half] = j <= i ? *reinterpret_cast<const f32x4 *>(M + (16 * i + c) * kLd + 16 * j + 4 * g) : f32x4{0, 0, 0, 0};
                 if constexpr (!BACK) {
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
@@ -341,6 +367,10 @@ template <typename T, int DXP, bool VEC, bool BACK> __global__ __launch_bounds__
                     }
                 }
             }
+            bf8 mt[3];
+            rows_terms<3>(m[0], m[1], mt);
+#pragma unroll
+            for (int u = 0; u < 3; ++u) out[(e * 3 + u) * 64 + lane] = mt[u];
             if constexpr (!BACK) {
                 bf8 terms[NP];
                 rows_terms<NP>(f32x4{p[0], p[1], p[2], p[3]}, f32x4{p[4], p[5], p[6], p[7]}, terms);
@@ -352,36 +382,41 @@ template <typename T, int DXP, bool VEC, bool BACK> __global__ __launch_bounds__
         // (I + diag(beta) C)^-1 and P by columns: lane (g, c) holds column 16 j + c at the rows of the operand's slots
         wave_sync();
         put(true);
-        f32x4 *outt = reinterpret_cast<f32x4 *>(rec + (kDeltaInverse + kDeltaVectors) * 1024);
+        f32x4 *outt = reinterpret_cast<f32x4 *>(outp + kDeltaInverse * 64);
 #pragma unroll
         for (int j = 0, e = 0; j < 4; ++j)
 #pragma unroll
-            for (int s = j / 2; s < 2; ++s, ++e)
+            for (int s = j / 2; s < 2; ++s, ++e) {
+                f32x4 m[2], p[2];
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
                     const int i = 2 * s + half;
-                    f32x4 m{0, 0, 0, 0}, p{0, 0, 0, 0};
+                    m[half] = p[half] = f32x4{0, 0, 0, 0};
                     if (i >= j) {
                         const f32x4 x = qk[i * (i + 1) / 2 + j];
 #pragma unroll
                         for (int r = 0; r < 4; ++r) {
                             const int row = 16 * i + 4 * g + r, col = 16 * j + c;
-                            m[r] = col <= row ? M[row * kLd + col] : 0.0f;
-                            p[r] = col <= row ? x[r] * a.scale * exp_of(G[row] - G[col <= row ? col : row]) : 0.0f;
+                            m[half][r] = col <= row ? M[row * kLd + col] : 0.0f;
+                            p[half][r] = col <= row ? x[r] * a.scale * exp_of(G[row] - G[col <= row ? col : row]) : 0.0f;
                         }
                     }
-                    outt[(e * 2 + half) * 64 + lane] = m;
-                    outt[kDeltaInverse * 64 + (e * 2 + half) * 64 + lane] = p;
+                    outt[(e * 2 + half) * 64 + lane] = p[half];
                 }
+                bf8 mt[3];
+                rows_terms<3>(m[0], m[1], mt);
+#pragma unroll
+                for (int u = 0; u < 3; ++u) outp[(e * 3 + u) * 64 + lane] = mt[u];
+            }
     }
 }
 
 // ---- tiles in LDS ------------------------------------------------------------
 // 64 rows of DP values in 16-byte slots, slot s of row r lying at s ^ f(r): eight neighbouring rows of a slot, and
 // four rows of four neighbouring slots, then lie on different banks.
-template <typename T, int DP> struct RowTile {
-    static constexpr int E = 16 / (int)sizeof(T), PR = DP / E, N = kC * PR / 256, BYTES = kC * DP * (int)sizeof(T);
-    static_assert(kC * PR % 256 == 0 && PR % 8 == 0, "whole loads");
+template <typename T, int DP, int WAVES> struct RowTile {
+    static constexpr int E = 16 / (int)sizeof(T), PR = DP / E, N = kC * PR / (WAVES * 64), BYTES = kC * DP * (int)sizeof(T);
+    static_assert(kC * PR % (WAVES * 64) == 0 && PR % 8 == 0, "whole loads");
     static __device__ __forceinline__ int f(int row) { return (row & 1) << 2 | (row & 2) | ((row >> 2) & 1); }
     static __device__ __forceinline__ const T *at(const T *tile, int row, int slot) { return tile + (row * PR + (slot ^ f(row))) * E; }
     // 8 values of a row at column col (a multiple of 8)
@@ -420,8 +455,8 @@ template <typename T, int DP> struct RowTile {
 };
 // Brings a tensor's rows into a tile: VEC by LDS-destination loads (what lies outside the chunk or the columns reads
 // zero by the buffer unit's range check), else value by value.
-template <typename T, int DP, bool VEC> struct RowSource {
-    using Tile = RowTile<T, DP>;
+template <typename T, int DP, int WAVES, bool VEC> struct RowSource {
+    using Tile = RowTile<T, DP, WAVES>;
     const T *p;            // the sequence's first row
     int64_t stride;
     int cols, col0;
@@ -435,11 +470,11 @@ template <typename T, int DP, bool VEC> struct RowSource {
         const T *first = p + t * stride;
 #pragma unroll
         for (int i = 0; i < Tile::N; ++i) {
-            const int idx = i * 256 + threadIdx.x, row = idx / Tile::PR, slot = idx % Tile::PR ^ Tile::f(row);
+            const int idx = i * WAVES * 64 + threadIdx.x, row = idx / Tile::PR, slot = idx % Tile::PR ^ Tile::f(row);
             const int col = col0 + slot * Tile::E;
             const uint32_t at = (uint32_t)((row * stride + col) * (int64_t)sizeof(T));
             if constexpr (VEC) {
-                lds_load16(first, tile + (i * 256 + wave * 64) * Tile::E, ((row < n) & (col < cols)) ? at : kSkip);
+                lds_load16(first, tile + (i * WAVES * 64 + wave * 64) * Tile::E, ((row < n) & (col < cols)) ? at : kSkip);
             } else {
                 const auto view = wide_view(first);
                 T e[Tile::E];
@@ -451,10 +486,10 @@ template <typename T, int DP, bool VEC> struct RowSource {
         }
     }
 };
-// `pieces` KB of a record (a multiple of four) as they are
-template <bool VEC> __device__ __forceinline__ void bring_record(const char *rec, int pieces, char *dst) {
+// `pieces` KB of a record as they are
+template <int WAVES, bool VEC> __device__ __forceinline__ void bring_record(const char *rec, int pieces, char *dst) {
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-    for (int i = wave; i < pieces; i += 4) {
+    for (int i = wave; i < pieces; i += WAVES) {
         if constexpr (VEC) lds_load16(rec, dst + i * 1024, (uint32_t)(i * 1024 + lane * 16));
         else *reinterpret_cast<f32x4 *>(dst + i * 1024 + lane * 16) = *reinterpret_cast<const f32x4 *>(rec + i * 1024 + lane * 16);
     }
@@ -504,7 +539,7 @@ template <int KX, int NT> struct State {
         float f[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) f[j] = v[kk][j >> 2][t][j & 3];
-        split8<__bf16, 3>(f, out);
+        split_terms(f, out);
     }
 };
 
@@ -535,26 +570,29 @@ inline __host__ __device__ int delta_run(int tiles, int group) {
 // the backward call, the state before each chunk and w.
 enum DeltaMode : int { kDeltaSums = 0, kDeltaOut = 1, kDeltaKeep = 2 };
 
-template <typename T, int DXP, int NT, int MODE, bool VEC> struct WalkShape {
+// Eight waves a workgroup, two a SIMD (one splits fp32 values while the other multiplies), for 128 columns; four for 64.
+template <typename T, int DXP, int WAVES, int MODE, bool VEC> struct WalkShape {
     static constexpr bool OUT = MODE == kDeltaOut;
-    static constexpr int DZT = NT * 64;
-    using TX = RowTile<T, DXP>;
-    using TZ = RowTile<T, DZT>;
+    static constexpr int DZT = WAVES * 16;
+    using TX = RowTile<T, DXP, WAVES>;
+    using TZ = RowTile<T, DZT, WAVES>;
     static constexpr int kQ = TX::BYTES, kV = (OUT ? 2 : 1) * TX::BYTES, kRec = kV + TZ::BYTES;
-    // the masked products stay in memory where LDS has no room for them (fp32 rows wider than 128)
-    static constexpr bool kProducts = OUT && kRec + delta_pieces(Terms<T>::kP) * 1024 <= 160 * 1024;
-    static constexpr int kPieces = kProducts ? delta_pieces(Terms<T>::kP) : 16, kBytes = kRec + kPieces * 1024;
-    static constexpr int kStages = VEC && 2 * kBytes <= 156 * 1024 ? 2 : 1;
-    static_assert(kBytes <= 160 * 1024, "LDS");
+    // where LDS has no room (fp32 rows wider than 128) the record, or its masked products, are read from memory
+    static constexpr int kAll = OUT ? delta_pieces(Terms<T>::kP) : 20, kFew = kDeltaInverse + kDeltaVectors + 1;
+    static constexpr int kPieces = kRec + kAll * 1024 <= kLdsBytes ? kAll : kRec + kFew * 1024 <= kLdsBytes ? kFew : 0;
+    static constexpr bool kRecord = kPieces > 0, kProducts = kPieces >= kAll;
+    static constexpr int kBytes = kRec + kPieces * 1024;
+    static constexpr int kStages = VEC && 2 * kBytes <= kLdsBytes ? 2 : 1;
+    static_assert(kBytes <= kLdsBytes, "LDS");
 };
 
 #ifdef __HIP_DEVICE_COMPILE__   // the host pass cannot take the loads' scalar operands and needs the kernels' stubs alone
 // w: the work item, of `tiles` column tiles (the first `ztiles` of values) x heads x places
-template <typename T, int DXP, int NT, int MODE, bool VEC>
+template <typename T, int DXP, int WAVES, int MODE, bool VEC>
 __device__ __forceinline__ void delta_walk(const DeltaArgs &a, char *lds, uint32_t w, int ztiles, int tiles) {
-    using W = WalkShape<T, DXP, NT, MODE, VEC>;
+    using W = WalkShape<T, DXP, WAVES, MODE, VEC>;
     constexpr bool OUT = W::OUT;
-    constexpr int KX = DXP / 32, DZT = W::DZT, NIN = Terms<T>::kIn, NOUT = Terms<T>::kOut, NP = Terms<T>::kP;
+    constexpr int KX = DXP / 32, NT = 1, DZT = W::DZT, NIN = Terms<T>::kIn, NOUT = Terms<T>::kOut, NP = Terms<T>::kP;
     using TX = typename W::TX;
     using TZ = typename W::TZ;
     const int tile = w % tiles;
@@ -572,15 +610,13 @@ __device__ __forceinline__ void delta_walk(const DeltaArgs &a, char *lds, uint32
     const bool map = MODE == kDeltaSums && tile >= ztiles;           // this workgroup's columns are the map's
     const int cols = map ? a.Dk : a.Dv, col0 = (map ? tile - ztiles : tile) * DZT;
     const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), zw = wave * NT * 16;
-    // column of accumulator column m of tile t (NT = 2: a lane's two tiles of outputs hold 8 neighbours)
-    // (kDeltaKeep: neighbouring lanes store neighbours)
-    auto zcol = [&](int m, int t) { return zw + (MODE == kDeltaKeep ? t * 16 + m : NT == 2 ? (m >> 2) * 8 + t * 4 + (m & 3) : m); };
-    auto zgroup = [&](int t) { return zw + (MODE == kDeltaKeep ? t * 16 + (lane & 3) * 4 : (lane & 3) * (NT * 4) + t * 4); };
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), zw = wave * 16;
+    auto zcol = [&](int m, int t) { return zw + t * 16 + m; };
+    auto zgroup = [&](int t) { return zw + t * 16 + (lane & 3) * 4; };
     auto column = [&](int t) { return col0 + zcol(c, t); };
 
-    RowSource<T, DXP, VEC> src_k, src_q;
-    RowSource<T, DZT, VEC> src_v;
+    RowSource<T, DXP, WAVES, VEC> src_k, src_q;
+    RowSource<T, DZT, WAVES, VEC> src_v;
     const int hk = h / a.group;
     src_k.init(a.k, tk.batch * a.kb + tk.row0 * a.kt + hk * a.kh, a.kt, a.Dk, 0);
     if (OUT) src_q.init(a.q, tk.batch * a.qb + tk.row0 * a.qt + hk * a.qh, a.qt, a.Dk, 0);
@@ -593,7 +629,7 @@ __device__ __forceinline__ void delta_walk(const DeltaArgs &a, char *lds, uint32
         src_k.bring(t, n, reinterpret_cast<T *>(stage));
         if (OUT) src_q.bring(t, n, reinterpret_cast<T *>(stage + W::kQ));
         src_v.bring(t, n, reinterpret_cast<T *>(stage + W::kV));
-        bring_record<VEC>(rec0 + ch * rec_step, W::kPieces, stage + W::kRec);
+        if (W::kRecord) bring_record<WAVES, VEC>(rec0 + ch * rec_step, W::kPieces, stage + W::kRec);
     };
     if (W::kStages == 2 && first < end) bring(first, lds);
 
@@ -602,12 +638,12 @@ __device__ __forceinline__ void delta_walk(const DeltaArgs &a, char *lds, uint32
     {
         const float *p = nullptr;
         if (MODE != kDeltaSums && a.seg_state && tk.unit > 0) {
-            p = a.seg_state + (place * a.H + h) * nst;
+            S.load(a.seg_state + (place * a.H + h) * (int64_t)DXP * a.sum_ld, DXP, a.sum_ld, column);
         } else if (MODE != kDeltaSums && a.state0) {
             const int64_t slot = state_slot(a.slots, a.n_slots, tk.seq);
             if (slot >= 0) p = a.state0 + (slot * a.H + h) * nst;
         }
-        S.load(p, a.Dk, cols, column);
+        if (MODE == kDeltaSums || !a.seg_state || tk.unit == 0) S.load(p, a.Dk, cols, column);
         if (map) S.each([&](int row, int t, float) __attribute__((always_inline)) { return row == column(t) ? 1.0f : 0.0f; });
     }
     const int out_cols = a.Dv - (col0 + zw + g * NT * 4);       // of this lane's first column of the output on
@@ -630,9 +666,10 @@ __device__ __forceinline__ void delta_walk(const DeltaArgs &a, char *lds, uint32
         }
         const T *tk_ = reinterpret_cast<const T *>(stage), *tq = reinterpret_cast<const T *>(stage + W::kQ),
                 *tv = reinterpret_cast<const T *>(stage + W::kV);
-        const f32x4 *inv = reinterpret_cast<const f32x4 *>(stage + W::kRec);
-        const float *vec = reinterpret_cast<const float *>(stage + W::kRec + kDeltaInverse * 1024);
-        const bf8 *prod = reinterpret_cast<const bf8 *>((W::kProducts ? stage + W::kRec : rec0 + ch * rec_step) + (kDeltaInverse + kDeltaVectors) * 1024);
+        const char *far = rec0 + ch * rec_step, *rec = W::kRecord ? stage + W::kRec : far;
+        const bf8 *inv = reinterpret_cast<const bf8 *>(rec);
+        const float *vec = reinterpret_cast<const float *>(rec + kDeltaInverse * 1024);
+        const bf8 *prod = reinterpret_cast<const bf8 *>((W::kProducts ? rec : far) + (kDeltaInverse + kDeltaVectors) * 1024);
 
         const int64_t kept = (rec0 - a.rec) / a.rec_bytes + ch * a.H;      // (chunk, head)
         if (MODE == kDeltaKeep) S.keep(a.states + kept * a.dkp * a.dvp, a.dvp, column);
@@ -700,8 +737,7 @@ __device__ __forceinline__ void delta_walk(const DeltaArgs &a, char *lds, uint32
             for (int t = 0; t < NT; ++t) u[r][t] = f32x4{0, 0, 0, 0};
 #pragma unroll
             for (int s = 0; s <= r / 2; ++s, ++e) {
-                bf8 tf[3];
-                rows_terms<3>(inv[e * 128 + lane], inv[e * 128 + 64 + lane], tf);
+                const bf8 tf[3] = {inv[e * 192 + lane], inv[e * 192 + 64 + lane], inv[e * 192 + 128 + lane]};
 #pragma unroll
                 for (int t = 0; t < NT; ++t) u[r][t] = mma_terms<3>(tf, rs[s][t], u[r][t]);
             }
@@ -777,8 +813,8 @@ __device__ __forceinline__ void delta_walk(const DeltaArgs &a, char *lds, uint32
     }
 
     if (MODE == kDeltaSums) {
-        float *p = map ? a.seg_map + (place * a.H + h) * (int64_t)a.Dk * a.Dk : a.seg_state + (place * a.H + h) * nst;
-        S.store(p, a.Dk, cols, column);
+        const int ld = map ? a.map_ld : a.sum_ld;
+        S.keep((map ? a.seg_map : a.seg_sum) + (place * a.H + h) * (int64_t)DXP * ld, ld, column);
     } else if (OUT && a.state1 && last) {
         const int64_t slot = state_slot(a.slots, a.n_slots, tk.seq);
         if (slot >= 0) S.store(a.state1 + (slot * a.H + h) * nst, a.Dk, a.Dv, column);
@@ -786,12 +822,12 @@ __device__ __forceinline__ void delta_walk(const DeltaArgs &a, char *lds, uint32
 }
 #endif
 
-template <typename T, int DXP, int NT, int MODE, bool VEC>
-__global__ __launch_bounds__(256, 1) void delta_walk_kernel(const DeltaArgs a, int ztiles, int tiles) {
+template <typename T, int DXP, int WAVES, int MODE, bool VEC>
+__global__ __launch_bounds__(WAVES * 64, 1) void delta_walk_kernel(const DeltaArgs a, int ztiles, int tiles) {
 #ifdef __HIP_DEVICE_COMPILE__
-    using W = WalkShape<T, DXP, NT, MODE, VEC>;
+    using W = WalkShape<T, DXP, WAVES, MODE, VEC>;
     __shared__ __attribute__((aligned(1024))) char lds[W::kStages * W::kBytes];
-    delta_walk<T, DXP, NT, MODE, VEC>(a, lds, dealt(blockIdx.x, delta_run(tiles, a.group)), ztiles, tiles);
+    delta_walk<T, DXP, WAVES, MODE, VEC>(a, lds, dealt(blockIdx.x, delta_run(tiles, a.group)), ztiles, tiles);
 #endif
 }
 
@@ -812,22 +848,24 @@ __global__ __launch_bounds__(256, 1) void delta_walk_kernel(const DeltaArgs a, i
 // Scaling a state by a factor and its values' gradients by the inverse changes nothing, which gives the logarithms'
 // gradient without another product: that of G_i is q_i . dq_i - v_i . dv_i, and of a chunk's last sum <G, S behind> on
 // top, so dlog_decay_t sums those of the chunk's tokens from t on.
-template <typename T, int DXP, int NT, bool VEC> struct BackShape {
-    static constexpr int DZT = NT * 64;
-    using TX = RowTile<T, DXP>;
-    using TZ = RowTile<T, DZT>;
+template <typename T, int DXP, int WAVES, bool VEC> struct BackShape {
+    static constexpr int DZT = WAVES * 16;
+    using TX = RowTile<T, DXP, WAVES>;
+    using TZ = RowTile<T, DZT, WAVES>;
     static constexpr int kQ = TX::BYTES, kG = 2 * TX::BYTES, kRec = kG + TZ::BYTES;
-    static constexpr bool kProducts = kRec + 28 * 1024 <= 160 * 1024;     // else P stays in memory
-    static constexpr int kPieces = kProducts ? 28 : 16, kBytes = kRec + kPieces * 1024;
-    static constexpr int kStages = VEC && 2 * kBytes <= 156 * 1024 ? 2 : 1;
-    static_assert(kBytes <= 160 * 1024, "LDS");
+    static constexpr int kAll = 32, kFew = kDeltaInverse + kDeltaVectors + 1;
+    static constexpr int kPieces = kRec + kAll * 1024 <= kLdsBytes ? kAll : kRec + kFew * 1024 <= kLdsBytes ? kFew : 0;
+    static constexpr bool kRecord = kPieces > 0, kProducts = kPieces >= kAll;
+    static constexpr int kBytes = kRec + kPieces * 1024;
+    static constexpr int kStages = VEC && 2 * kBytes <= kLdsBytes ? 2 : 1;
+    static_assert(kDeltaInverse + kAll <= kDeltaBackPieces && kBytes <= kLdsBytes, "LDS");
 };
 
 #ifdef __HIP_DEVICE_COMPILE__
-template <typename T, int DXP, int NT, bool VEC>
+template <typename T, int DXP, int WAVES, bool VEC>
 __device__ __forceinline__ void delta_walk_back(const DeltaArgs &a, char *lds, uint32_t w, int tiles) {
-    using W = BackShape<T, DXP, NT, VEC>;
-    constexpr int KX = DXP / 32, DZT = W::DZT, NIN = Terms<T>::kIn;
+    using W = BackShape<T, DXP, WAVES, VEC>;
+    constexpr int KX = DXP / 32, NT = 1, DZT = W::DZT, NIN = Terms<T>::kIn;
     using TX = typename W::TX;
     using TZ = typename W::TZ;
     const int tile = w % tiles;
@@ -841,11 +879,11 @@ __device__ __forceinline__ void delta_walk_back(const DeltaArgs &a, char *lds, u
     const int64_t chunks = (tk.len + kC - 1) / kC;
     const int col0 = tile * DZT;
     const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), zw = wave * NT * 16;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), zw = wave * 16;
     auto column = [&](int t) { return col0 + zw + t * 16 + c; };
 
-    RowSource<T, DXP, VEC> src_k, src_q;
-    RowSource<T, DZT, VEC> src_g;
+    RowSource<T, DXP, WAVES, VEC> src_k, src_q;
+    RowSource<T, DZT, WAVES, VEC> src_g;
     const int hk = h / a.group;
     src_k.init(a.k, tk.batch * a.kb + tk.row0 * a.kt + hk * a.kh, a.kt, a.Dk, 0);
     src_q.init(a.q, tk.batch * a.qb + tk.row0 * a.qt + hk * a.qh, a.qt, a.Dk, 0);
@@ -860,7 +898,7 @@ __device__ __forceinline__ void delta_walk_back(const DeltaArgs &a, char *lds, u
         src_k.bring(t, n, reinterpret_cast<T *>(stage));
         src_q.bring(t, n, reinterpret_cast<T *>(stage + W::kQ));
         src_g.bring(t, n, reinterpret_cast<T *>(stage + W::kG));
-        bring_record<VEC>(rec0 + ch * rec_step, W::kPieces, stage + W::kRec);
+        if (W::kRecord) bring_record<WAVES, VEC>(rec0 + ch * rec_step, W::kPieces, stage + W::kRec);
     };
     if (W::kStages == 2 && chunks > 0) bring(chunks - 1, lds);
 
@@ -883,10 +921,10 @@ __device__ __forceinline__ void delta_walk_back(const DeltaArgs &a, char *lds, u
         }
         const T *tk_ = reinterpret_cast<const T *>(stage), *tq = reinterpret_cast<const T *>(stage + W::kQ),
                 *tg = reinterpret_cast<const T *>(stage + W::kG);
-        const float *vec = reinterpret_cast<const float *>(stage + W::kRec);
-        const f32x4 *inv = reinterpret_cast<const f32x4 *>(stage + W::kRec + kDeltaVectors * 1024);
-        const f32x4 *prod = reinterpret_cast<const f32x4 *>((W::kProducts ? stage + W::kRec : rec0 + ch * rec_step) +
-                                                            (kDeltaVectors + kDeltaInverse) * 1024);
+        const char *far = rec0 + ch * rec_step, *rec = W::kRecord ? stage + W::kRec : far;
+        const float *vec = reinterpret_cast<const float *>(rec);
+        const bf8 *inv = reinterpret_cast<const bf8 *>(rec + kDeltaVectors * 1024);
+        const f32x4 *prod = reinterpret_cast<const f32x4 *>((W::kProducts ? rec : far) + (kDeltaVectors + kDeltaInverse) * 1024);
         const int64_t item = item0 + ch * a.H;
         G.keep(a.grads + item * a.dkp * a.dvp, a.dvp, column);
 
@@ -959,8 +997,7 @@ __device__ __forceinline__ void delta_walk_back(const DeltaArgs &a, char *lds, u
             for (int t = 0; t < NT; ++t) y[r][t] = f32x4{0, 0, 0, 0};
 #pragma unroll
             for (int s = r / 2; s < 2; ++s, ++e) {
-                bf8 tf[3];
-                rows_terms<3>(inv[e * 128 + lane], inv[e * 128 + 64 + lane], tf);
+                const bf8 tf[3] = {inv[e * 192 + lane], inv[e * 192 + 64 + lane], inv[e * 192 + 128 + lane]};
 #pragma unroll
                 for (int t = 0; t < NT; ++t) y[r][t] = mma_terms<3>(tf, xs[s][t], y[r][t]);
             }
@@ -1014,16 +1051,16 @@ __device__ __forceinline__ void delta_walk_back(const DeltaArgs &a, char *lds, u
 #endif
 
 // Both walks of the backward call: even items forwards, odd ones from the end.
-template <typename T, int DXP, int NT, bool VEC>
-__global__ __launch_bounds__(256, 1) void delta_back_walks_kernel(const DeltaArgs a, int tiles) {
+template <typename T, int DXP, int WAVES, bool VEC>
+__global__ __launch_bounds__(WAVES * 64, 1) void delta_back_walks_kernel(const DeltaArgs a, int tiles) {
 #ifdef __HIP_DEVICE_COMPILE__
-    using F = WalkShape<T, DXP, NT, kDeltaKeep, VEC>;
-    using R = BackShape<T, DXP, NT, VEC>;
+    using F = WalkShape<T, DXP, WAVES, kDeltaKeep, VEC>;
+    using R = BackShape<T, DXP, WAVES, VEC>;
     constexpr int kF = F::kStages * F::kBytes, kR = R::kStages * R::kBytes;
     __shared__ __attribute__((aligned(1024))) char lds[kF > kR ? kF : kR];
     const uint32_t w = dealt(blockIdx.x, delta_run(2 * tiles, a.group));
-    if (w & 1) delta_walk_back<T, DXP, NT, VEC>(a, lds, w / 2, tiles);
-    else delta_walk<T, DXP, NT, kDeltaKeep, VEC>(a, lds, w / 2, tiles, tiles);
+    if (w & 1) delta_walk_back<T, DXP, WAVES, VEC>(a, lds, w / 2, tiles);
+    else delta_walk<T, DXP, WAVES, kDeltaKeep, VEC>(a, lds, w / 2, tiles, tiles);
 #endif
 }
 
@@ -1035,7 +1072,7 @@ template <typename T, int DXP, bool VEC>
 __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void delta_gradients_kernel(const DeltaArgs a) {
 #ifdef __HIP_DEVICE_COMPILE__
     constexpr int DP = DXP < 128 ? DXP : 128, DA = DP / 64, NIN = Terms<T>::kIn;    // columns at once, tiles of a wave
-    using TX = RowTile<T, DP>;
+    using TX = RowTile<T, DP, 4>;
     __shared__ __attribute__((aligned(1024))) T tile_k[kC * DP], tile_q[kC * DP];
     __shared__ __attribute__((aligned(16))) f32x4 by_q[10][64], by_k[10][64], both[16][64];    // dP by queries, by keys; dC + dC^T
     __shared__ double sums[kC];
@@ -1064,7 +1101,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void delta_gradients_k
         sums[lane] = sum;
         weights[lane] = lane < n ? a.beta[gate0 + (int64_t)lane * a.H] : 0.0f;
     }
-    RowSource<T, DP, VEC> src_k, src_q;
+    RowSource<T, DP, 4, VEC> src_k, src_q;
     src_k.init(a.k, t.batch * a.kb + t.row0 * a.kt + hk * a.kh, a.kt, a.Dk, 0);
     src_q.init(a.q, t.batch * a.qb + t.row0 * a.qt + hk * a.qh, a.qt, a.Dk, 0);
     src_k.bring(t0, n, tile_k);
@@ -1335,55 +1372,84 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void delta_gradients_k
 #endif
 }
 
-// State before each segment from the segments' own sums and maps, in place of the sums: S <- map S + sum, one
-// workgroup a (sequence, head, 64 columns).  grid (B, H, tiles).
+// State before each segment from the segments' own sums and maps: S <- map S + sum, one workgroup a (sequence, head,
+// 16 columns), grid (B, H, tiles); a wave has a quarter of the rows of the map, of which those of the next segment are on
+// their way while this one's are in use, and the state goes round through LDS.  Bound by latency: the segments are serial.
 template <int DXP> static __global__ __launch_bounds__(256, 1) void delta_chain_kernel(const DeltaArgs a) {
-    constexpr int KX = DXP / 32;
-    const int h = blockIdx.y, col0 = blockIdx.z * 64;
+    constexpr int KX = DXP / 32, R = DXP / 64, LD = DXP + 4;
+    __shared__ __attribute__((aligned(16))) float state[2][16 * LD];
+    const int h = blockIdx.y, col0 = blockIdx.z * 16;
     const int64_t seq = blockIdx.x;
     int64_t start, len;
     sequence_bounds(a, seq, start, len);
     const int64_t length = a.seg_chunks * kC, count = (len + length - 1) / length;
     if (count < 2) return;
-    const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15, wave = threadIdx.x >> 6;
-    auto column = [&](int) { return col0 + wave * 16 + c; };
-    const int64_t nst = (int64_t)a.Dk * a.Dv, nmap = (int64_t)a.Dk * a.Dk, place0 = first_place(a, seq, length);
-    State<KX, 1> S, sum;
+    const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15, wave = threadIdx.x >> 6, row0 = wave * R * 16;
+    const int64_t first = first_place(a, seq, length) * a.H + h, sums = (int64_t)DXP * a.sum_ld, maps = (int64_t)DXP * a.map_ld;
     {
         const float *p = nullptr;
         if (a.state0) {
             const int64_t slot = state_slot(a.slots, a.n_slots, seq);
-            if (slot >= 0) p = a.state0 + (slot * a.H + h) * nst;
+            if (slot >= 0) p = a.state0 + (slot * a.H + h) * (int64_t)a.Dk * a.Dv;
         }
-        S.load(p, a.Dk, a.Dv, column);
+        const auto view = wide_view(p);
+        for (int i = threadIdx.x; i < DXP * 16; i += 256) {
+            const int row = i / 16, col = i % 16;
+            const bool there = (p != nullptr) & (row < a.Dk) & (col0 + col < a.Dv);
+            state[0][col * LD + row] = view_load<float>(view, there ? (uint32_t)(row * a.Dv + col0 + col) * 4u : kSkip);
+        }
     }
+    f32x4 map[R][KX][2], sum[R];
+    auto fetch = [&](int64_t i, f32x4 (&m)[R][KX][2], f32x4 (&s)[R]) __attribute__((always_inline)) {
+        const float *mp = a.seg_map + (first + i * a.H) * maps, *sp = a.seg_sum + (first + i * a.H) * sums;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+#pragma unroll
+            for (int kk = 0; kk < KX; ++kk)
+#pragma unroll
+                for (int half = 0; half < 2; ++half)
+                    m[r][kk][half] = *reinterpret_cast<const f32x4 *>(mp + (row0 + 16 * r + c) * (int64_t)a.map_ld + kk * 32 + g * 8 + half * 4);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s[r][j] = sp[(row0 + 16 * r + 4 * g + j) * (int64_t)a.sum_ld + col0 + c];
+        }
+    };
+    if (DXP <= 128) fetch(0, map, sum);
+    __syncthreads();
     for (int64_t i = 0; i + 1 < count; ++i) {
-        float *own = a.seg_state + ((place0 + i) * a.H + h) * nst;
-        const float *map = a.seg_map + ((place0 + i) * a.H + h) * nmap;
-        sum.load(own, a.Dk, a.Dv, column);
-        const auto view = wide_view(map);
-        bf8 st[KX][3];
+        f32x4 next[R][KX][2], own[R];
+        if (DXP > 128) fetch(i, map, sum);      // (registers hold one)
+        else if (i + 2 < count) fetch(i + 1, next, own);
+        const float *from = state[i & 1];
+        float *to = state[(i & 1) ^ 1];
 #pragma unroll
-        for (int kk = 0; kk < KX; ++kk) S.terms(kk, 0, st[kk]);
+        for (int kk = 0; kk < KX; ++kk) {
+            const f32x4 *p = reinterpret_cast<const f32x4 *>(from + c * LD + kk * 32 + g * 8);
+            bf8 st[3];
+            rows_terms<3>(p[0], p[1], st);
 #pragma unroll
-        for (int kk = 0; kk < KX; ++kk)
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const int row = kk * 32 + (c >> 2) * 8 + r * 4 + (c & 3);
-                f32x4 acc = sum.v[kk][r][0];
-#pragma unroll
-                for (int x = 0; x < KX; ++x) {
-                    const int col = x * 32 + g * 8, left = row < a.Dk ? a.Dk - col : 0;
-                    bf8 mf[3];
-                    in_terms(load_row8<float, false>(view, left > 0 ? (uint32_t)(row * a.Dk + col) * 4u : kSkip, left), mf);
-                    acc = mma_terms<3>(mf, st[x], acc);
-                }
-                sum.v[kk][r][0] = acc;
+            for (int r = 0; r < R; ++r) {
+                bf8 mf[3];
+                rows_terms<3>(map[r][kk][0], map[r][kk][1], mf);
+                sum[r] = mma_terms<3>(mf, st, sum[r]);
             }
-        if (i > 0) S.store(own, a.Dk, a.Dv, column);
-        S = sum;
+        }
+        float *out = a.seg_state + (first + (i + 1) * a.H) * sums;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            *reinterpret_cast<f32x4 *>(to + c * LD + row0 + 16 * r + 4 * g) = sum[r];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) out[(row0 + 16 * r + 4 * g + j) * (int64_t)a.sum_ld + col0 + c] = sum[r][j];
+        }
+        if (DXP <= 128) {
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                sum[r] = own[r];
+#pragma unroll
+                for (int kk = 0; kk < KX; ++kk) map[r][kk][0] = next[r][kk][0], map[r][kk][1] = next[r][kk][1];
+            }
+        }
+        __syncthreads();
     }
-    S.store(a.seg_state + ((place0 + count - 1) * a.H + h) * nst, a.Dk, a.Dv, column);
 }
 
 // The single-token form.  One workgroup a (sequence, head, LANES * VEC columns), LANES lanes along a row of the state,
@@ -1472,40 +1538,41 @@ template <typename T> static hipError_t delta_prepare_typed(const DeltaArgs &a, 
     if (a.states) return a.vec ? delta_prepare_launch<T, true, true>(a, s) : delta_prepare_launch<T, false, true>(a, s);
     return a.vec ? delta_prepare_launch<T, true, false>(a, s) : delta_prepare_launch<T, false, false>(a, s);
 }
-template <typename T, int DXP, int NT, bool VEC> static hipError_t delta_back_launch(const DeltaArgs &a, hipStream_t s) {
-    const int tiles = a.dvp / (NT * 64);
+template <typename T, int DXP, int WAVES, bool VEC> static hipError_t delta_back_launch(const DeltaArgs &a, hipStream_t s) {
+    const int tiles = a.dvp / (WAVES * 16);
     const int64_t items = 2 * a.segs * a.H * tiles, round = 8 * (int64_t)delta_run(2 * tiles, a.group);
-    delta_back_walks_kernel<T, DXP, NT, VEC><<<(unsigned)((items + round - 1) / round * round), 256, 0, s>>>(a, tiles);
+    delta_back_walks_kernel<T, DXP, WAVES, VEC><<<(unsigned)((items + round - 1) / round * round), WAVES * 64, 0, s>>>(a, tiles);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.chunks == 0) return e;
     delta_gradients_kernel<T, DXP, VEC><<<(unsigned)(a.chunks * a.H), 256, 0, s>>>(a);
     return hipGetLastError();
 }
 template <typename T, bool VEC> static hipError_t delta_back(const DeltaArgs &a, hipStream_t s) {
-    if (a.Dk > 128) return delta_back_launch<T, 256, 1, VEC>(a, s);
-    if (a.Dk > 64) return a.wide ? delta_back_launch<T, 128, 2, VEC>(a, s) : delta_back_launch<T, 128, 1, VEC>(a, s);
-    return a.wide ? delta_back_launch<T, 64, 2, VEC>(a, s) : delta_back_launch<T, 64, 1, VEC>(a, s);
+    if (a.Dk > 128) return delta_back_launch<T, 256, 4, VEC>(a, s);
+    if (a.Dk > 64) return a.wide ? delta_back_launch<T, 128, 8, VEC>(a, s) : delta_back_launch<T, 128, 4, VEC>(a, s);
+    return a.wide ? delta_back_launch<T, 64, 8, VEC>(a, s) : delta_back_launch<T, 64, 4, VEC>(a, s);
 }
 template <typename T> static hipError_t delta_bwd_typed(const DeltaArgs &a, hipStream_t s) {
     return a.vec ? delta_back<T, true>(a, s) : delta_back<T, false>(a, s);
 }
-template <typename T, int DXP, int NT, int MODE, bool VEC> static hipError_t delta_walk_launch(const DeltaArgs &a, hipStream_t s) {
-    const int ztiles = (a.Dv + NT * 64 - 1) / (NT * 64), tiles = ztiles + (MODE == kDeltaSums ? (a.Dk + NT * 64 - 1) / (NT * 64) : 0);
+template <typename T, int DXP, int WAVES, int MODE, bool VEC> static hipError_t delta_walk_launch(const DeltaArgs &a, hipStream_t s) {
+    constexpr int DZT = WAVES * 16;
+    const int ztiles = (a.Dv + DZT - 1) / DZT, tiles = ztiles + (MODE == kDeltaSums ? (a.Dk + DZT - 1) / DZT : 0);
     const int64_t items = a.segs * a.H * tiles, round = 8 * (int64_t)delta_run(tiles, a.group);
-    delta_walk_kernel<T, DXP, NT, MODE, VEC><<<(unsigned)((items + round - 1) / round * round), 256, 0, s>>>(a, ztiles, tiles);
+    delta_walk_kernel<T, DXP, WAVES, MODE, VEC><<<(unsigned)((items + round - 1) / round * round), WAVES * 64, 0, s>>>(a, ztiles, tiles);
     return hipGetLastError();
 }
 template <typename T, int MODE, bool VEC> static hipError_t delta_walks(const DeltaArgs &a, hipStream_t s) {
     // (rows wider than 128 leave registers and LDS for 64 columns only)
-    if (a.Dk > 128) return delta_walk_launch<T, 256, 1, MODE, VEC>(a, s);
-    if (a.Dk > 64) return a.wide ? delta_walk_launch<T, 128, 2, MODE, VEC>(a, s) : delta_walk_launch<T, 128, 1, MODE, VEC>(a, s);
-    return a.wide ? delta_walk_launch<T, 64, 2, MODE, VEC>(a, s) : delta_walk_launch<T, 64, 1, MODE, VEC>(a, s);
+    if (a.Dk > 128) return delta_walk_launch<T, 256, 4, MODE, VEC>(a, s);
+    if (a.Dk > 64) return a.wide ? delta_walk_launch<T, 128, 8, MODE, VEC>(a, s) : delta_walk_launch<T, 128, 4, MODE, VEC>(a, s);
+    return a.wide ? delta_walk_launch<T, 64, 8, MODE, VEC>(a, s) : delta_walk_launch<T, 64, 4, MODE, VEC>(a, s);
 }
 template <typename T> static hipError_t delta_fwd_typed(const DeltaArgs &a, hipStream_t s) {
     if (a.seg_state) {
         const hipError_t e = a.vec ? delta_walks<T, kDeltaSums, true>(a, s) : delta_walks<T, kDeltaSums, false>(a, s);
         if (e != hipSuccess) return e;
-        const dim3 grid((unsigned)a.B, (unsigned)a.H, (unsigned)((a.Dv + 63) / 64));
+        const dim3 grid((unsigned)a.B, (unsigned)a.H, (unsigned)((a.Dv + 15) / 16));
         if (a.Dk <= 64) delta_chain_kernel<64><<<grid, 256, 0, s>>>(a);
         else if (a.Dk <= 128) delta_chain_kernel<128><<<grid, 256, 0, s>>>(a);
         else delta_chain_kernel<256><<<grid, 256, 0, s>>>(a);

@@ -49,13 +49,19 @@ DeltaCut fwd_cut(const DeltaShape &s) {
 }
 
 struct DeltaFwdLayout {
-    size_t states, maps, total;
+    int64_t sum_ld, map_ld;
+    size_t sums, maps, states, total;
 };
+int64_t padded_width(int64_t Dk) { return Dk <= 64 ? 64 : Dk <= 128 ? 128 : 256; }
 DeltaFwdLayout fwd_layout(const DeltaShape &s, const DeltaCut &c) {
     DeltaFwdLayout l{};
-    l.states = align_up((size_t)s.places(kDeltaChunk) * s.H * record_bytes(s), 256);
-    l.maps = l.states + (c.cut ? align_up((size_t)c.segs * s.H * s.Dk * s.Dv * 4, 256) : 0);
-    l.total = l.maps + (c.cut ? (size_t)c.segs * s.H * s.Dk * s.Dk * 4 : 0);
+    const int64_t tile = c.wide ? 128 : 64, rows = padded_width(s.Dk);
+    l.sum_ld = round_up(s.Dv, tile), l.map_ld = std::max(rows, round_up(s.Dk, tile));
+    const size_t matrices = c.cut ? (size_t)c.segs * s.H * rows * 4 : 0;
+    l.sums = align_up((size_t)s.places(kDeltaChunk) * s.H * record_bytes(s), 256);
+    l.maps = l.sums + matrices * l.sum_ld;
+    l.states = l.maps + matrices * l.map_ld;
+    l.total = l.states + matrices * l.sum_ld;
     return l;
 }
 
@@ -191,8 +197,12 @@ fftconv_status_t fftconv_delta_fwd(const void *q, const void *k, const void *v, 
     a.seg_chunks = c.seg_chunks, a.segs = c.segs, a.wide = c.wide;
     a.rec = static_cast<char *>(workspace);
     a.rec_bytes = (int64_t)record_bytes(s);
-    a.seg_state = c.cut ? reinterpret_cast<float *>(a.rec + l.states) : nullptr;
-    a.seg_map = c.cut ? reinterpret_cast<float *>(a.rec + l.maps) : nullptr;
+    if (c.cut) {
+        a.seg_sum = reinterpret_cast<float *>(a.rec + l.sums);
+        a.seg_map = reinterpret_cast<float *>(a.rec + l.maps);
+        a.seg_state = reinterpret_cast<float *>(a.rec + l.states);
+        a.sum_ld = (int)l.sum_ld, a.map_ld = (int)l.map_ld;
+    }
     hipError_t e = launch_prepare(dtype, a, stream);
     if (e == hipSuccess) e = launch_fwd(dtype, a, stream);
     return hip_status("delta rule", e);
@@ -249,7 +259,7 @@ struct DeltaBwdLayout {
 DeltaBwdLayout bwd_layout(const DeltaShape &s) {
     DeltaBwdLayout l{};
     l.wide = fwd_cut(s).wide;
-    l.dkp = s.Dk <= 64 ? 64 : s.Dk <= 128 ? 128 : 256;
+    l.dkp = padded_width(s.Dk);
     l.dvp = round_up(s.Dv, l.wide ? 128 : 64);
     const size_t items = (size_t)s.places(kDeltaChunk) * s.H;
     l.states = items * kDeltaBackPieces * 1024;

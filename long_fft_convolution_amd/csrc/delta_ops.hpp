@@ -11,17 +11,17 @@ namespace fftconv {
 
 constexpr int kDeltaChunk = 64;      // tokens of a chunk
 
-// What the walks read of one (chunk, head), written by the first kernel, in pieces of 1 KB (16 bytes a lane):
-// the inverse as 6 operands of two fp32 halves, 4 vectors of the tokens, the masked products as 6 operands of
-// `terms` terms; padded to whole rounds of four waves.
-constexpr int kDeltaInverse = 12, kDeltaVectors = 1;
+// What the walks read of one (chunk, head), written by the first kernel, in pieces of 1 KB (16 bytes a lane): the
+// inverse as 6 operands of three bf16 terms, 4 vectors of the tokens, the masked products as 6 operands of `terms`
+// terms; padded to a multiple of four.
+constexpr int kDeltaInverse = 18, kDeltaVectors = 1;
 constexpr int delta_pieces(int terms) { return (kDeltaInverse + kDeltaVectors + 6 * terms + 3) / 4 * 4; }
 // terms of the masked products: bf16 results see them rounded once, like the state; fp16's need two, fp32's three
 constexpr int delta_terms(int elem_bytes, bool narrow) { return elem_bytes == 4 ? 3 : narrow ? 2 : 1; }
-
 // The backward call's record: the inverse of I + C diag(beta), the vectors, then, as operands over tokens from the
-// other side, the inverse of I + C^T diag(beta) and P^T, all in fp32.
-constexpr int kDeltaBackPieces = 3 * kDeltaInverse + 4 * kDeltaVectors;
+// other side, the inverse of I + C^T diag(beta) in three terms and P^T in fp32 (two halves of an operand).
+constexpr int kDeltaBackProducts = 12;
+constexpr int kDeltaBackPieces = (2 * kDeltaInverse + kDeltaVectors + kDeltaBackProducts + 3) / 4 * 4;
 
 struct DeltaArgs {
     const void *q, *k, *v;           // q and k have H / group heads, v and out H
@@ -40,8 +40,10 @@ struct DeltaArgs {
     int64_t seg_chunks, segs;        // chunks of a segment, places for segments
     char *rec;                       // (chunks, H) records
     int64_t rec_bytes;
-    float *seg_state;                // (segs, H) Dk x Dv: a segment's own sum, then the state before it; null: one segment each
-    float *seg_map;                  // (segs, H) Dk x Dk: what a segment makes of the state before it
+    // (segs, H) matrices of padded rows: a segment's own sum, what it makes of the state before it, and that state;
+    // null: one segment each
+    float *seg_sum, *seg_map, *seg_state;
+    int sum_ld, map_ld;              // row lengths: seg_sum and seg_state, seg_map
     int vec;                         // rows of the tensors in whole aligned 16-byte pieces
     int wide;                        // 128 columns of the state a workgroup, else 64
 
