@@ -109,34 +109,15 @@ template <> struct Terms<_Float16> { static constexpr int kIn = 2, kOut = 2, kP 
 template <> struct Terms<float> { static constexpr int kIn = 3, kOut = 3, kP = delta_terms(4, false); };
 
 // Eight fp32 values as N bf16 terms.  bf16 is the upper half of fp32: cutting it off leaves an exact rest, so three
-// terms of 8 bits hold all 24; the last of two is rounded.  A pair's rest costs two dot products of the pair with
-// (-1, 0) and (0, -1), where taking the halves apart first would cost two more instructions.
+// terms of 8 bits hold all 24; the last of two is rounded.  (The rests as dot products of a pair with (-1, 0) and (0, -1)
+// are fewer instructions, but those wait for the matrix unit and it for them: 33 cycles for a product and two of them,
+// 19 for a product and two ordinary ones.)
 template <int N> __device__ __forceinline__ void split_terms(const float (&x)[8], bf8 (&out)[N]) {
-    typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
-    float rest[8];
+    if constexpr (N == 1) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) rest[j] = x[j];
-#pragma unroll
-    for (int s = 0; s < N; ++s) {
-        if (s == N - 1 && N < 3) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) out[s][j] = (__bf16)rest[j];
-            continue;
-        }
-        // (as register operands: an inline constant -1.0 would be met as fp32)
-        uint32_t low = 0x0000bf80u, high = 0xbf800000u, u[4];
-        asm("" : "+s"(low), "+s"(high));
-#pragma unroll
-        for (int j = 0; j < 4; ++j)     // upper halves of two values: bytes 2, 3 of each
-            u[j] = __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, rest[2 * j + 1]), __builtin_bit_cast(uint32_t, rest[2 * j]), 0x07060302u);
-        __builtin_memcpy(&out[s], u, 16);
-        if (s + 1 < N) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                rest[2 * j] = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf2, u[j]), __builtin_bit_cast(bf2, low), rest[2 * j], false);
-                rest[2 * j + 1] = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf2, u[j]), __builtin_bit_cast(bf2, high), rest[2 * j + 1], false);
-            }
-        }
+        for (int j = 0; j < 8; ++j) out[0][j] = (__bf16)x[j];
+    } else {
+        split8<__bf16, N>(x, out);
     }
 }
 template <typename T> struct Raw8 { T v[8]; };
@@ -495,64 +476,142 @@ template <int WAVES, bool VEC> __device__ __forceinline__ void bring_record(cons
     }
 }
 
+// Where a wave's operands lie in a tile, as byte offsets of this lane: what the swizzle makes of the lane is in a few
+// bases, the rest of an address is a constant of the instruction.
+template <typename T, int DP, int WAVES> struct TileReader {
+    using Tile = RowTile<T, DP, WAVES>;
+    static constexpr int RB = DP * (int)sizeof(T);
+    uint32_t row[2], col[sizeof(T) == 2 ? 2 : 8];
+    __device__ __forceinline__ void init() {
+        const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+            row[p] = c * RB + ((sizeof(T) == 2 ? 4 * p + g : 2 * g + p) ^ Tile::f(c)) * 16;
+            if constexpr (sizeof(T) == 2) {
+                const int r = 4 * g + (c >> 2);
+                col[p] = r * RB + ((4 * p + (c & 3)) ^ Tile::f(r)) * 16;
+            }
+        }
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int r = 0; r < 2; ++r)
+                    col[2 * j + r] = (4 * g + j) * RB + (((c >> 2) * 2 + r) ^ Tile::f(4 * g + j)) * 16 + (c & 3) * 4;
+        }
+    }
+    // columns 32 kk + 8 g .. + 7 of row 16 r + c
+    __device__ __forceinline__ Raw8<T> row8(const char *tile, int r, int kk) const {
+        Raw8<T> v;
+        if constexpr (sizeof(T) == 2) {
+            v = *reinterpret_cast<const Raw8<T> *>(__builtin_assume_aligned(tile + row[kk & 1] + (kk >> 1) * 128 + r * 16 * RB, 16));
+        } else {
+#pragma unroll
+            for (int p = 0; p < 2; ++p)
+                __builtin_memcpy(reinterpret_cast<char *>(&v) + 16 * p, __builtin_assume_aligned(tile + row[p] + kk * 128 + r * 16 * RB, 16), 16);
+        }
+        return v;
+    }
+    // column 32 kk + 8 (c / 4) + 4 r + c % 4 of the rows of an operand over tokens 32 s .. 32 s + 31.  16 bits:
+    // transposing reads, in which 16 lanes read four rows of four 4-column groups and lane c receives column c % 4 of
+    // group c / 4.
+    __device__ __forceinline__ Raw8<T> col8(const char *tile, int s, int kk, int r) const {
+        Raw8<T> v;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const int rows = (32 * s + 16 * half) * RB;
+            if constexpr (sizeof(T) == 2) {
+                const char *p = tile + col[kk & 1] + (kk >> 1) * 128 + r * 8 + rows;
+                const s16x4 x = __builtin_bit_cast(s16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16(FFTCONV_LDS_CAST(s16x4, const_cast<char *>(p))));
+                __builtin_memcpy(v.v + 4 * half, &x, 8);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v.v[4 * half + j] = *reinterpret_cast<const T *>(tile + col[2 * j + r] + kk * 128 + rows);
+            }
+        }
+        return v;
+    }
+};
+// The same of a wave's own 16 columns: rows 16 r + 4 g .. + 3 of column 16 wave + c.
+template <typename T, int DP, int WAVES> struct ColumnReader {
+    using Tile = RowTile<T, DP, WAVES>;
+    static constexpr int RB = DP * (int)sizeof(T);
+    uint32_t col[sizeof(T) == 2 ? 1 : 4];
+    __device__ __forceinline__ void init(int wave) {
+        const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
+        if constexpr (sizeof(T) == 2) {
+            const int r = 4 * g + (c >> 2);
+            col[0] = r * RB + ((2 * wave + ((c & 3) >> 1)) ^ Tile::f(r)) * 16 + (c & 1) * 8;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) col[j] = (4 * g + j) * RB + ((4 * wave + (c >> 2)) ^ Tile::f(4 * g + j)) * 16 + (c & 3) * 4;
+        }
+    }
+    __device__ __forceinline__ void col4(const char *tile, int r, T *out) const {
+        if constexpr (sizeof(T) == 2) {
+            const char *p = tile + col[0] + r * 16 * RB;
+            const s16x4 x = __builtin_bit_cast(s16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16(FFTCONV_LDS_CAST(s16x4, const_cast<char *>(p))));
+            __builtin_memcpy(out, &x, 8);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) out[j] = *reinterpret_cast<const T *>(tile + col[j] + r * 16 * RB);
+        }
+    }
+};
+
 // ---- the state in a wave's accumulators ------------------------------------------
-// S[kk][r][t]: rows kk * 32 + g * 8 + r * 4 + i, column column(c, t) of the wave: as an operand over rows, lane
-// (g, c) holds the slots 8 g + j of its column.
-template <int KX, int NT> struct State {
-    f32x4 v[KX][2][NT];
+// v[kk][r]: rows kk * 32 + g * 8 + r * 4 + i of the column of lane (g, c): as an operand over rows, the lane holds the
+// slots 8 g + j of its column.
+template <int KX> struct State {
+    f32x4 v[KX][2];
     template <typename F> __device__ __forceinline__ void each(F &&f) {
 #pragma unroll
         for (int kk = 0; kk < KX; ++kk)
 #pragma unroll
             for (int r = 0; r < 2; ++r)
 #pragma unroll
-                for (int t = 0; t < NT; ++t)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        v[kk][r][t][i] = f(kk * 32 + (int)((threadIdx.x & 63) >> 4) * 8 + r * 4 + i, t, v[kk][r][t][i]);
+                for (int i = 0; i < 4; ++i) v[kk][r][i] = f(kk * 32 + (int)((threadIdx.x & 63) >> 4) * 8 + r * 4 + i, v[kk][r][i]);
     }
     // of a row-major matrix of rows x cols (null: zeros)
-    template <typename C> __device__ __forceinline__ void load(const float *p, int rows, int cols, C &&column) {
+    __device__ __forceinline__ void load(const float *p, int rows, int cols, int col) {
         const auto view = wide_view(p);
-        each([&](int row, int t, float) __attribute__((always_inline)) {
-            const int col = column(t);
+        each([&](int row, float) __attribute__((always_inline)) {
             return view_load<float>(view, ((p != nullptr) & (row < rows) & (col < cols)) ? (uint32_t)(row * cols + col) * 4u : kSkip);
         });
     }
-    template <typename C> __device__ __forceinline__ void store(float *p, int rows, int cols, C &&column) {
+    // Ends the loads before a loop: waits for them inside it would come with every round, and loads retire in order, so
+    // that each would wait for the next chunk's.
+    __device__ __forceinline__ void settle() {
+        each([&](int, float x) __attribute__((always_inline)) {
+            asm volatile("" : "+v"(x));
+            return x;
+        });
+    }
+    __device__ __forceinline__ void store(float *p, int rows, int cols, int col) {
         const auto view = wide_view(p);
-        each([&](int row, int t, float x) __attribute__((always_inline)) {
-            const int col = column(t);
+        each([&](int row, float x) __attribute__((always_inline)) {
             view_store(view, ((row < rows) & (col < cols)) ? (uint32_t)(row * cols + col) * 4u : kSkip, x);
             return x;
         });
     }
     // into a matrix of padded rows, whose padding it fills with what padding gives: zeros
-    template <typename C> __device__ __forceinline__ void keep(float *p, int ld, C &&column) {
+    __device__ __forceinline__ void keep(float *p, int ld, int col) {
         const auto view = wide_view(p);
-        each([&](int row, int t, float x) __attribute__((always_inline)) {
-            view_store(view, (uint32_t)(row * ld + column(t)) * 4u, x);
+        each([&](int row, float x) __attribute__((always_inline)) {
+            view_store(view, (uint32_t)(row * ld + col) * 4u, x);
             return x;
         });
     }
-    __device__ __forceinline__ void terms(int kk, int t, bf8 (&out)[3]) const {
-        float f[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = v[kk][j >> 2][t][j & 3];
-        split_terms(f, out);
-    }
+    __device__ __forceinline__ void terms(int kk, bf8 (&out)[3]) const { rows_terms<3>(v[kk][0], v[kk][1], out); }
 };
-
 // accumulators over tokens (rows 16 r + 4 g + i) into a matrix of 64 padded rows
-template <int NT, typename C> __device__ __forceinline__ void keep_rows(float *p, int ld, const f32x4 (&x)[4][NT], C &&column) {
+__device__ __forceinline__ void keep_rows(float *p, int ld, const f32x4 (&x)[4], int col) {
     const auto view = wide_view(p);
     const int g = (threadIdx.x & 63) >> 4;
 #pragma unroll
     for (int r = 0; r < 4; ++r)
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) view_store(view, (uint32_t)((16 * r + 4 * g + i) * ld + column(t)) * 4u, x[r][t][i]);
+        for (int i = 0; i < 4; ++i) view_store(view, (uint32_t)((16 * r + 4 * g + i) * ld + col) * 4u, x[r][i]);
 }
 
 // Work item of workgroup id: ids go to the 8 XCDs in turn, so runs of `run` items are dealt to one XCD, whose L2
@@ -586,15 +645,17 @@ template <typename T, int DXP, int WAVES, int MODE, bool VEC> struct WalkShape {
     static_assert(kBytes <= kLdsBytes, "LDS");
 };
 
+// Threads that the walks are compiled for: with 512 the accumulators stay among the 256 registers that all instructions
+// reach; four waves of rows up to 128 fit those, too, and moves to and from the other half would cost a tenth of them.
+constexpr int walk_bound(int dxp, int waves, int bytes) { return dxp <= 128 && bytes == 2 ? 512 : waves * 64; }
+
 #ifdef __HIP_DEVICE_COMPILE__   // the host pass cannot take the loads' scalar operands and needs the kernels' stubs alone
 // w: the work item, of `tiles` column tiles (the first `ztiles` of values) x heads x places
 template <typename T, int DXP, int WAVES, int MODE, bool VEC>
 __device__ __forceinline__ void delta_walk(const DeltaArgs &a, char *lds, uint32_t w, int ztiles, int tiles) {
     using W = WalkShape<T, DXP, WAVES, MODE, VEC>;
     constexpr bool OUT = W::OUT;
-    constexpr int KX = DXP / 32, NT = 1, DZT = W::DZT, NIN = Terms<T>::kIn, NOUT = Terms<T>::kOut, NP = Terms<T>::kP;
-    using TX = typename W::TX;
-    using TZ = typename W::TZ;
+    constexpr int KX = DXP / 32, DZT = W::DZT, NIN = Terms<T>::kIn, NOUT = Terms<T>::kOut, NP = Terms<T>::kP;
     const int tile = w % tiles;
     w /= tiles;
     const int h = w % a.H;
@@ -611,9 +672,7 @@ __device__ __forceinline__ void delta_walk(const DeltaArgs &a, char *lds, uint32
     const int cols = map ? a.Dk : a.Dv, col0 = (map ? tile - ztiles : tile) * DZT;
     const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), zw = wave * 16;
-    auto zcol = [&](int m, int t) { return zw + t * 16 + m; };
-    auto zgroup = [&](int t) { return zw + t * 16 + (lane & 3) * 4; };
-    auto column = [&](int t) { return col0 + zcol(c, t); };
+    const int column = col0 + zw + c;                                   // of this lane's part of the state
 
     RowSource<T, DXP, WAVES, VEC> src_k, src_q;
     RowSource<T, DZT, WAVES, VEC> src_v;
@@ -633,7 +692,11 @@ __device__ __forceinline__ void delta_walk(const DeltaArgs &a, char *lds, uint32
     };
     if (W::kStages == 2 && first < end) bring(first, lds);
 
-    State<KX, NT> S;
+    TileReader<T, DXP, WAVES> in_k;
+    ColumnReader<T, DZT, WAVES> in_v;
+    in_k.init();
+    in_v.init(wave);
+    State<KX> S;
     const int64_t nst = (int64_t)a.Dk * a.Dv;
     {
         const float *p = nullptr;
@@ -644,9 +707,10 @@ __device__ __forceinline__ void delta_walk(const DeltaArgs &a, char *lds, uint32
             if (slot >= 0) p = a.state0 + (slot * a.H + h) * nst;
         }
         if (MODE == kDeltaSums || !a.seg_state || tk.unit == 0) S.load(p, a.Dk, cols, column);
-        if (map) S.each([&](int row, int t, float) __attribute__((always_inline)) { return row == column(t) ? 1.0f : 0.0f; });
+        S.settle();
+        if (map) S.each([&](int row, float) __attribute__((always_inline)) { return row == column ? 1.0f : 0.0f; });
     }
-    const int out_cols = a.Dv - (col0 + zw + g * NT * 4);       // of this lane's first column of the output on
+    const int out_cols = a.Dv - (col0 + zw + g * 4);       // of this lane's first column of the output on
     T *out0 = OUT ? static_cast<T *>(a.out) + tk.batch * a.ob + tk.row0 * a.ot + h * a.oh : nullptr;
 
     for (int64_t ch = first; ch < end; ++ch) {
@@ -664,150 +728,130 @@ __device__ __forceinline__ void delta_walk(const DeltaArgs &a, char *lds, uint32
             bring(ch, stage);
             wait_loads_and_barrier<0>();
         }
-        const T *tk_ = reinterpret_cast<const T *>(stage), *tq = reinterpret_cast<const T *>(stage + W::kQ),
-                *tv = reinterpret_cast<const T *>(stage + W::kV);
         const char *far = rec0 + ch * rec_step, *rec = W::kRecord ? stage + W::kRec : far;
-        const bf8 *inv = reinterpret_cast<const bf8 *>(rec);
+        const bf8 *inv = reinterpret_cast<const bf8 *>(rec) + lane;
         const float *vec = reinterpret_cast<const float *>(rec + kDeltaInverse * 1024);
-        const bf8 *prod = reinterpret_cast<const bf8 *>((W::kProducts ? rec : far) + (kDeltaInverse + kDeltaVectors) * 1024);
-
+        const f32x4 *vec4 = reinterpret_cast<const f32x4 *>(vec) + g;      // the rows 16 r + 4 g ..: [4 r]
+        const bf8 *prod = reinterpret_cast<const bf8 *>((W::kProducts ? rec : far) + (kDeltaInverse + kDeltaVectors) * 1024) + lane;
         const int64_t kept = (rec0 - a.rec) / a.rec_bytes + ch * a.H;      // (chunk, head)
         if (MODE == kDeltaKeep) S.keep(a.states + kept * a.dkp * a.dvp, a.dvp, column);
-        // k S, and the state's part of the outputs
-        f32x4 x[4][NT], o[4][NT];
+        // k S
+        f32x4 x[4], o[4];
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-#pragma unroll
-            for (int t = 0; t < NT; ++t) x[r][t] = o[r][t] = f32x4{0, 0, 0, 0};
+        for (int r = 0; r < 4; ++r) x[r] = o[r] = f32x4{0, 0, 0, 0};
+        bf8 few[OUT ? KX : 1][NOUT];
 #pragma unroll
         for (int kk = 0; kk < KX; ++kk) {
-            bf8 st[NT][3];
+            bf8 st[3];
+            S.terms(kk, st);
+            if (OUT)
 #pragma unroll
-            for (int t = 0; t < NT; ++t) S.terms(kk, t, st[t]);
+                for (int j = 0; j < NOUT; ++j) few[kk][j] = st[j];
             bf8 kf[4][NIN];
 #pragma unroll
-            for (int r = 0; r < 4; ++r) in_terms(TX::row8(tk_, 16 * r + c, kk * 32 + g * 8), kf[r]);
+            for (int r = 0; r < 4; ++r) in_terms(in_k.row8(stage, r, kk), kf[r]);
 #pragma unroll
             for (int i = 0; i < NIN; ++i)
 #pragma unroll
                 for (int j = 0; j < 3; ++j)
                     if (i + j < 3)
 #pragma unroll
-                        for (int r = 0; r < 4; ++r)
+                        for (int r = 0; r < 4; ++r) x[r] = Mma<__bf16>::mma(kf[r][i], st[j], x[r]);
+        }
+        // r = v - exp(G) k S as operands over tokens
+        bf8 rs[2][3];
 #pragma unroll
-                            for (int t = 0; t < NT; ++t) x[r][t] = Mma<__bf16>::mma(kf[r][i], st[t][j], x[r][t]);
-            if (OUT) {
+        for (int s = 0; s < 2; ++s) {
+            f32x4 res[2];
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                T v[4];
+                in_v.col4(stage + W::kV, 2 * s + half, v);
+                const f32x4 f = vec4[8 * s + 4 * half];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) res[half][i] = (float)v[i] - f[i] * x[2 * s + half][i];
+            }
+            rows_terms<3>(res[0], res[1], rs[s]);
+        }
+        // the state's part of the outputs, which needs nothing of the above
+        if (OUT) {
+#pragma unroll
+            for (int kk = 0; kk < KX; ++kk) {
                 bf8 qf[4][NIN];
 #pragma unroll
-                for (int r = 0; r < 4; ++r) in_terms(TX::row8(tq, 16 * r + c, kk * 32 + g * 8), qf[r]);
+                for (int r = 0; r < 4; ++r) in_terms(in_k.row8(stage + W::kQ, r, kk), qf[r]);
 #pragma unroll
                 for (int i = 0; i < NIN; ++i)
 #pragma unroll
                     for (int j = 0; j < NOUT; ++j)
                         if (i + j < NOUT)
 #pragma unroll
-                            for (int r = 0; r < 4; ++r)
-#pragma unroll
-                                for (int t = 0; t < NT; ++t) o[r][t] = Mma<__bf16>::mma(st[t][j], qf[r][i], o[r][t]);
+                            for (int r = 0; r < 4; ++r) o[r] = Mma<__bf16>::mma(few[kk][j], qf[r][i], o[r]);
             }
         }
-        // r = v - exp(G) k S as operands over tokens
-        bf8 rs[2][NT][3];
+        // w = inverse r, u = beta w; terms outermost, so that an accumulator's next product comes four instructions later
+        f32x4 u[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) u[r] = f32x4{0, 0, 0, 0};
 #pragma unroll
         for (int s = 0; s < 2; ++s)
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                f32x4 res[2];
+            for (int i = 0; i < 3; ++i)
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    const int row = 32 * s + 16 * half + 4 * g;
-                    T v[4];
-                    TZ::col4(tv, row, zgroup(t), zcol(c, t), v);
-                    const f32x4 f = *reinterpret_cast<const f32x4 *>(vec + row);
+                for (int j = 0; i + j < 3; ++j)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) res[half][i] = (float)v[i] - f[i] * x[2 * s + half][t][i];
-                }
-                rows_terms<3>(res[0], res[1], rs[s][t]);
-            }
-        // w = inverse r, u = beta w
-        f32x4 u[4][NT];
+                    for (int r = 2 * s; r < 4; ++r) u[r] = Mma<__bf16>::mma(inv[((r + 1) * (r + 1) / 4 + s) * 192 + i * 64], rs[s][j], u[r]);
+        if (MODE == kDeltaKeep) keep_rows(a.wrong + kept * kC * a.dvp, a.dvp, u, col0 + zw + c);
 #pragma unroll
-        for (int r = 0, e = 0; r < 4; ++r) {
-#pragma unroll
-            for (int t = 0; t < NT; ++t) u[r][t] = f32x4{0, 0, 0, 0};
-#pragma unroll
-            for (int s = 0; s <= r / 2; ++s, ++e) {
-                const bf8 tf[3] = {inv[e * 192 + lane], inv[e * 192 + 64 + lane], inv[e * 192 + 128 + lane]};
-#pragma unroll
-                for (int t = 0; t < NT; ++t) u[r][t] = mma_terms<3>(tf, rs[s][t], u[r][t]);
-            }
-        }
-        if (MODE == kDeltaKeep) keep_rows<NT>(a.wrong + kept * kC * a.dvp, a.dvp, u, column);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const f32x4 b = *reinterpret_cast<const f32x4 *>(vec + 128 + 16 * r + 4 * g);
-#pragma unroll
-            for (int t = 0; t < NT; ++t) u[r][t] *= b;
-        }
-        if (OUT) {
-            const int64_t t0 = ch * kC;
-            const int n = tk.len - t0 < kC ? (int)(tk.len - t0) : kC;
-            bf8 us[2][NT][NOUT];
-#pragma unroll
-            for (int s = 0; s < 2; ++s)
-#pragma unroll
-                for (int t = 0; t < NT; ++t) rows_terms<NOUT>(u[2 * s][t], u[2 * s + 1][t], us[s][t]);
-            const auto view = wide_view(out0 + t0 * a.ot);
-#pragma unroll
-            for (int r = 0, e = 0; r < 4; ++r) {
-                const float f = vec[192 + 16 * r + c];
-#pragma unroll
-                for (int t = 0; t < NT; ++t) o[r][t] *= f;
-#pragma unroll
-                for (int s = 0; s <= r / 2; ++s, ++e) {
-                    bf8 pf[NP];
-#pragma unroll
-                    for (int p = 0; p < NP; ++p) pf[p] = prod[(e * NP + p) * 64 + lane];
-#pragma unroll
-                    for (int t = 0; t < NT; ++t) o[r][t] = mma_terms<NOUT>(us[s][t], pf, o[r][t]);
-                }
-                const int row = 16 * r + c;
-                const uint32_t at = ((row < n) & (out_cols > 0)) ? (uint32_t)((row * a.ot + col0 + zw + g * NT * 4) * (int64_t)sizeof(T)) : kSkip;
-                put_row<T, NT, VEC && sizeof(T) == 2>(view, at, o[r], VEC, out_cols);
-            }
-        }
+        for (int r = 0; r < 4; ++r) u[r] *= vec4[32 + 4 * r];
         // S <- exp(G_last) S + k^T (exp(G_last - G) u)
+        bf8 es[2][3];
+#pragma unroll
+        for (int s = 0; s < 2; ++s) rows_terms<3>(u[2 * s] * vec4[16 + 8 * s], u[2 * s + 1] * vec4[16 + 8 * s + 4], es[s]);
         const float keep = vec[63];
-        bf8 es[2][NT][3];
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            const f32x4 f0 = *reinterpret_cast<const f32x4 *>(vec + 64 + 32 * s + 4 * g),
-                        f1 = *reinterpret_cast<const f32x4 *>(vec + 64 + 32 * s + 16 + 4 * g);
-#pragma unroll
-            for (int t = 0; t < NT; ++t) rows_terms<3>(u[2 * s][t] * f0, u[2 * s + 1][t] * f1, es[s][t]);
-        }
 #pragma unroll
         for (int kk = 0; kk < KX; ++kk) {
 #pragma unroll
-            for (int r = 0; r < 2; ++r)
+            for (int r = 0; r < 2; ++r) S.v[kk][r] *= keep;
+            bf8 kf[2][2][NIN];
 #pragma unroll
-                for (int t = 0; t < NT; ++t) S.v[kk][r][t] *= keep;
+            for (int s = 0; s < 2; ++s)
 #pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                // rows of the state permuted like its operand: row m is kk * 32 + 8 (m / 4) + 4 r + m % 4
-                bf8 kf[2][NIN];
+                for (int r = 0; r < 2; ++r) in_terms(in_k.col8(stage, s, kk, r), kf[s][r]);
 #pragma unroll
-                for (int r = 0; r < 2; ++r)
-                    in_terms(TX::col8(tk_, s, kk * 32 + (lane & 3) * 8 + r * 4, kk * 32 + (c >> 2) * 8 + r * 4 + (c & 3)), kf[r]);
+            for (int s = 0; s < 2; ++s)
 #pragma unroll
                 for (int i = 0; i < NIN; ++i)
 #pragma unroll
                     for (int j = 0; j < 3; ++j)
                         if (i + j < 3)
 #pragma unroll
-                            for (int r = 0; r < 2; ++r)
+                            for (int r = 0; r < 2; ++r) S.v[kk][r] = Mma<__bf16>::mma(kf[s][r][i], es[s][j], S.v[kk][r]);
+        }
+        if (OUT) {
+            const int64_t t0 = ch * kC;
+            const int n = tk.len - t0 < kC ? (int)(tk.len - t0) : kC;
+            bf8 us[2][NOUT];
 #pragma unroll
-                                for (int t = 0; t < NT; ++t) S.v[kk][r][t] = Mma<__bf16>::mma(kf[r][i], es[s][t][j], S.v[kk][r][t]);
+            for (int s = 0; s < 2; ++s) rows_terms<NOUT>(u[2 * s], u[2 * s + 1], us[s]);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) o[r] *= vec[192 + 16 * r + c];
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+#pragma unroll
+                for (int i = 0; i < NP; ++i)
+#pragma unroll
+                    for (int j = 0; j < NOUT; ++j)
+                        if (i + j < NOUT)
+#pragma unroll
+                            for (int r = 2 * s; r < 4; ++r)
+                                o[r] = Mma<__bf16>::mma(us[s][j], prod[(((r + 1) * (r + 1) / 4 + s) * NP + i) * 64], o[r]);
+            const auto view = wide_view(out0 + t0 * a.ot);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int row = 16 * r + c;
+                const uint32_t at = ((row < n) & (out_cols > 0)) ? (uint32_t)((row * a.ot + col0 + zw + g * 4) * (int64_t)sizeof(T)) : kSkip;
+                put_row<T, 1, VEC && sizeof(T) == 2>(view, at, &o[r], VEC, out_cols);
             }
         }
     }
@@ -823,7 +867,7 @@ __device__ __forceinline__ void delta_walk(const DeltaArgs &a, char *lds, uint32
 #endif
 
 template <typename T, int DXP, int WAVES, int MODE, bool VEC>
-__global__ __launch_bounds__(WAVES * 64, 1) void delta_walk_kernel(const DeltaArgs a, int ztiles, int tiles) {
+__global__ __launch_bounds__(walk_bound(DXP, WAVES, sizeof(T))) void delta_walk_kernel(const DeltaArgs a, int ztiles, int tiles) {
 #ifdef __HIP_DEVICE_COMPILE__
     using W = WalkShape<T, DXP, WAVES, MODE, VEC>;
     __shared__ __attribute__((aligned(1024))) char lds[W::kStages * W::kBytes];
@@ -865,9 +909,7 @@ template <typename T, int DXP, int WAVES, bool VEC> struct BackShape {
 template <typename T, int DXP, int WAVES, bool VEC>
 __device__ __forceinline__ void delta_walk_back(const DeltaArgs &a, char *lds, uint32_t w, int tiles) {
     using W = BackShape<T, DXP, WAVES, VEC>;
-    constexpr int KX = DXP / 32, NT = 1, DZT = W::DZT, NIN = Terms<T>::kIn;
-    using TX = typename W::TX;
-    using TZ = typename W::TZ;
+    constexpr int KX = DXP / 32, DZT = W::DZT, NIN = Terms<T>::kIn;
     const int tile = w % tiles;
     w /= tiles;
     const int h = w % a.H;
@@ -880,7 +922,7 @@ __device__ __forceinline__ void delta_walk_back(const DeltaArgs &a, char *lds, u
     const int col0 = tile * DZT;
     const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), zw = wave * 16;
-    auto column = [&](int t) { return col0 + zw + t * 16 + c; };
+    const int column = col0 + zw + c;
 
     RowSource<T, DXP, WAVES, VEC> src_k, src_q;
     RowSource<T, DZT, WAVES, VEC> src_g;
@@ -902,9 +944,14 @@ __device__ __forceinline__ void delta_walk_back(const DeltaArgs &a, char *lds, u
     };
     if (W::kStages == 2 && chunks > 0) bring(chunks - 1, lds);
 
-    State<KX, NT> G;
+    TileReader<T, DXP, WAVES> in_k;
+    ColumnReader<T, DZT, WAVES> in_g;
+    in_k.init();
+    in_g.init(wave);
+    State<KX> G;
     const int64_t nst = (int64_t)a.Dk * a.Dv;
     G.load(a.dstate1 ? a.dstate1 + (tk.seq * a.H + h) * nst : nullptr, a.Dk, a.Dv, column);
+    G.settle();
 
     for (int64_t back = 0; back < chunks; ++back) {
         const int64_t ch = chunks - 1 - back;
@@ -919,131 +966,111 @@ __device__ __forceinline__ void delta_walk_back(const DeltaArgs &a, char *lds, u
             bring(ch, stage);
             wait_loads_and_barrier<0>();
         }
-        const T *tk_ = reinterpret_cast<const T *>(stage), *tq = reinterpret_cast<const T *>(stage + W::kQ),
-                *tg = reinterpret_cast<const T *>(stage + W::kG);
         const char *far = rec0 + ch * rec_step, *rec = W::kRecord ? stage + W::kRec : far;
         const float *vec = reinterpret_cast<const float *>(rec);
-        const bf8 *inv = reinterpret_cast<const bf8 *>(rec + kDeltaVectors * 1024);
-        const f32x4 *prod = reinterpret_cast<const f32x4 *>((W::kProducts ? rec : far) + (kDeltaVectors + kDeltaInverse) * 1024);
+        const f32x4 *vec4 = reinterpret_cast<const f32x4 *>(vec) + g;
+        const bf8 *inv = reinterpret_cast<const bf8 *>(rec + kDeltaVectors * 1024) + lane;
+        const f32x4 *prod = reinterpret_cast<const f32x4 *>((W::kProducts ? rec : far) + (kDeltaVectors + kDeltaInverse) * 1024) + lane;
         const int64_t item = item0 + ch * a.H;
         G.keep(a.grads + item * a.dkp * a.dvp, a.dvp, column);
 
-        // G^T k
-        f32x4 x[4][NT];
+        // the outputs' gradients as operands over tokens, as they are and by scale exp(G)
+        bf8 gf[2][NIN], gs[2][3];
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
+        for (int s = 0; s < 2; ++s) {
+            Raw8<T> raw;
+            in_g.col4(stage + W::kG, 2 * s, raw.v);
+            in_g.col4(stage + W::kG, 2 * s + 1, raw.v + 4);
+            in_terms(raw, gf[s]);
+            f32x4 lo = vec4[48 + 8 * s], hi = vec4[48 + 8 * s + 4];
 #pragma unroll
-            for (int t = 0; t < NT; ++t) x[r][t] = f32x4{0, 0, 0, 0};
+            for (int i = 0; i < 4; ++i) lo[i] *= (float)raw.v[i], hi[i] *= (float)raw.v[4 + i];
+            rows_terms<3>(lo, hi, gs[s]);
+        }
+        // G^T k, and sum_i P_ij dO_i
+        f32x4 x[4], p[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) x[r] = p[r] = f32x4{0, 0, 0, 0};
 #pragma unroll
         for (int kk = 0; kk < KX; ++kk) {
-            bf8 st[NT][3];
+            bf8 st[3], kf[4][NIN];
+            G.terms(kk, st);
 #pragma unroll
-            for (int t = 0; t < NT; ++t) G.terms(kk, t, st[t]);
-            bf8 kf[4][NIN];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) in_terms(TX::row8(tk_, 16 * r + c, kk * 32 + g * 8), kf[r]);
+            for (int r = 0; r < 4; ++r) in_terms(in_k.row8(stage, r, kk), kf[r]);
 #pragma unroll
             for (int i = 0; i < NIN; ++i)
 #pragma unroll
                 for (int j = 0; j < 3; ++j)
                     if (i + j < 3)
 #pragma unroll
-                        for (int r = 0; r < 4; ++r)
-#pragma unroll
-                            for (int t = 0; t < NT; ++t) x[r][t] = Mma<__bf16>::mma(kf[r][i], st[t][j], x[r][t]);
+                        for (int r = 0; r < 4; ++r) x[r] = Mma<__bf16>::mma(kf[r][i], st[j], x[r]);
         }
-        // the outputs' gradients as operands over tokens, as they are and by scale exp(G)
-        bf8 gs[2][NT][3];
-        {
-            bf8 gf[2][NT][NIN];
 #pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                const f32x4 f0 = *reinterpret_cast<const f32x4 *>(vec + 192 + 32 * s + 4 * g),
-                            f1 = *reinterpret_cast<const f32x4 *>(vec + 192 + 32 * s + 16 + 4 * g);
-#pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    const Raw8<T> raw = TZ::col8(tg, s, zw + t * 16 + (lane & 3) * 4, zw + t * 16 + c);
-                    in_terms(raw, gf[s][t]);
-                    f32x4 lo, hi;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) lo[i] = (float)raw.v[i] * f0[i], hi[i] = (float)raw.v[4 + i] * f1[i];
-                    rows_terms<3>(lo, hi, gs[s][t]);
-                }
-            }
-#pragma unroll
-            for (int r = 0, e = 0; r < 4; ++r) {
-                const f32x4 f = *reinterpret_cast<const f32x4 *>(vec + 64 + 16 * r + 4 * g);
-#pragma unroll
-                for (int t = 0; t < NT; ++t) x[r][t] *= f;
-#pragma unroll
-                for (int s = r / 2; s < 2; ++s, ++e) {
-                    bf8 pf[3];
-                    rows_terms<3>(prod[e * 128 + lane], prod[e * 128 + 64 + lane], pf);
-#pragma unroll
-                    for (int t = 0; t < NT; ++t) x[r][t] = mma_terms<3>(pf, gf[s][t], x[r][t]);
-                }
-            }
-        }
-        // y
-        bf8 xs[2][NT][3];
-#pragma unroll
-        for (int s = 0; s < 2; ++s)
-#pragma unroll
-            for (int t = 0; t < NT; ++t) rows_terms<3>(x[2 * s][t], x[2 * s + 1][t], xs[s][t]);
-        f32x4 y[4][NT];
-#pragma unroll
-        for (int r = 0, e = 0; r < 4; ++r) {
-#pragma unroll
-            for (int t = 0; t < NT; ++t) y[r][t] = f32x4{0, 0, 0, 0};
+        for (int r = 0, e = 0; r < 4; ++r)
 #pragma unroll
             for (int s = r / 2; s < 2; ++s, ++e) {
-                const bf8 tf[3] = {inv[e * 192 + lane], inv[e * 192 + 64 + lane], inv[e * 192 + 128 + lane]};
-#pragma unroll
-                for (int t = 0; t < NT; ++t) y[r][t] = mma_terms<3>(tf, xs[s][t], y[r][t]);
+                bf8 pf[3];
+                rows_terms<3>(prod[e * 128], prod[e * 128 + 64], pf);
+                p[r] = mma_terms<3>(pf, gf[s], p[r]);
             }
+        // y
+        bf8 xs[2][3];
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            f32x4 sum[2];
+#pragma unroll
+            for (int half = 0; half < 2; ++half) sum[half] = x[2 * s + half] * vec4[16 + 8 * s + 4 * half] + p[2 * s + half];
+            rows_terms<3>(sum[0], sum[1], xs[s]);
         }
-        keep_rows<NT>(a.dright + item * kC * a.dvp, a.dvp, y, column);
+        f32x4 y[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) y[r] = f32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int s = 1; s >= 0; --s)
+#pragma unroll
+            for (int i = 0; i < 3; ++i)
+#pragma unroll
+                for (int j = 0; i + j < 3; ++j)
+#pragma unroll
+                    for (int r = 0; r < 2 * s + 2; ++r) {
+                        const int e = (r < 2 ? 2 * r + s : 3 + r - 1 + s - 1);      // operands (r, s >= r / 2) in order
+                        y[r] = Mma<__bf16>::mma(inv[e * 192 + i * 64], xs[s][j], y[r]);
+                    }
+        keep_rows(a.dright + item * kC * a.dvp, a.dvp, y, column);
         // G <- exp(G_last) G + q^T (scale exp(G) dO) - k^T (exp(G) beta y)
         const float keep = vec[63];
-        bf8 ys[2][NT][3];
+        bf8 ys[2][3];
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
             f32x4 f[2];
 #pragma unroll
-            for (int half = 0; half < 2; ++half)
-                f[half] = -*reinterpret_cast<const f32x4 *>(vec + 32 * s + 16 * half + 4 * g) *
-                          *reinterpret_cast<const f32x4 *>(vec + 128 + 32 * s + 16 * half + 4 * g);
-#pragma unroll
-            for (int t = 0; t < NT; ++t) rows_terms<3>(y[2 * s][t] * f[0], y[2 * s + 1][t] * f[1], ys[s][t]);
+            for (int half = 0; half < 2; ++half) f[half] = -vec4[8 * s + 4 * half] * vec4[32 + 8 * s + 4 * half];
+            rows_terms<3>(y[2 * s] * f[0], y[2 * s + 1] * f[1], ys[s]);
         }
 #pragma unroll
         for (int kk = 0; kk < KX; ++kk) {
 #pragma unroll
-            for (int r = 0; r < 2; ++r)
+            for (int r = 0; r < 2; ++r) G.v[kk][r] *= keep;
+            bf8 kf[2][2][NIN], qf[2][2][NIN];
 #pragma unroll
-                for (int t = 0; t < NT; ++t) G.v[kk][r][t] *= keep;
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                bf8 kf[2][NIN], qf[2][NIN];
+            for (int s = 0; s < 2; ++s)
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                    const int group = kk * 32 + (lane & 3) * 8 + r * 4, mine = kk * 32 + (c >> 2) * 8 + r * 4 + (c & 3);
-                    in_terms(TX::col8(tk_, s, group, mine), kf[r]);
-                    in_terms(TX::col8(tq, s, group, mine), qf[r]);
+                    in_terms(in_k.col8(stage + W::kQ, s, kk, r), qf[s][r]);
+                    in_terms(in_k.col8(stage, s, kk, r), kf[s][r]);
                 }
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
 #pragma unroll
                 for (int i = 0; i < NIN; ++i)
 #pragma unroll
                     for (int j = 0; j < 3; ++j)
                         if (i + j < 3)
 #pragma unroll
-                            for (int r = 0; r < 2; ++r)
-#pragma unroll
-                                for (int t = 0; t < NT; ++t) {
-                                    G.v[kk][r][t] = Mma<__bf16>::mma(kf[r][i], ys[s][t][j], G.v[kk][r][t]);
-                                    G.v[kk][r][t] = Mma<__bf16>::mma(qf[r][i], gs[s][t][j], G.v[kk][r][t]);
-                                }
-            }
+                            for (int r = 0; r < 2; ++r) {
+                                G.v[kk][r] = Mma<__bf16>::mma(qf[s][r][i], gs[s][j], G.v[kk][r]);
+                                G.v[kk][r] = Mma<__bf16>::mma(kf[s][r][i], ys[s][j], G.v[kk][r]);
+                            }
         }
     }
     if (a.dstate0) G.store(a.dstate0 + (tk.seq * a.H + h) * nst, a.Dk, a.Dv, column);
@@ -1052,7 +1079,7 @@ __device__ __forceinline__ void delta_walk_back(const DeltaArgs &a, char *lds, u
 
 // Both walks of the backward call: even items forwards, odd ones from the end.
 template <typename T, int DXP, int WAVES, bool VEC>
-__global__ __launch_bounds__(WAVES * 64, 1) void delta_back_walks_kernel(const DeltaArgs a, int tiles) {
+__global__ __launch_bounds__(walk_bound(DXP, WAVES, sizeof(T))) void delta_back_walks_kernel(const DeltaArgs a, int tiles) {
 #ifdef __HIP_DEVICE_COMPILE__
     using F = WalkShape<T, DXP, WAVES, kDeltaKeep, VEC>;
     using R = BackShape<T, DXP, WAVES, VEC>;
@@ -1064,19 +1091,28 @@ __global__ __launch_bounds__(WAVES * 64, 1) void delta_back_walks_kernel(const D
 #endif
 }
 
-// One workgroup a (chunk, head); see above.  First each wave takes 16 tokens and forms their rows and columns of dP and
-// dC, left in LDS as operands over tokens; then each takes a quarter of 64 or 128 columns of q and k and all tokens.
-// Tiles of one kind of operand are met by rows of 8 neighbouring values (states, w, y, dO, in memory), k and q by
-// columns (in LDS).  bytes: the states and gradients before it (128 KB at 128 x 128), twice what its tensors hold.
+// One workgroup a (chunk, head); see above.  A wave has 16 tokens as columns of all products: it forms their columns of
+// dP and dC, which stay in its registers as operands over tokens, and their rows of dq and dk.  Operands over the
+// values' columns (u, dv, dO, S, G: rows of 32 neighbouring values) are split once, each by one wave, and met by all
+// through LDS, 32 columns at a time; k and q, met by columns, follow in the same place.
+//
+// Bound by the matrix units and the splitting: 4 x 4096 tokens x 20 heads of 128, bf16: DELTA_GRADIENTS_FIGURE.
+template <typename T, int DXP> struct GradientShape {
+    static constexpr int DP = 64, DT = DP / 16;      // columns of q and k at once, their tiles
+    static constexpr int NIN = Terms<T>::kIn;
+    static constexpr int kU = 0, kY = 4 * 3, kG = 8 * 3, kS = kG + 4 * NIN, kD = kS + DT * 3, kPieces = kD + DT * 3;
+    static constexpr int kTiles = 2 * RowTile<T, DP, 4>::BYTES;
+    static constexpr int kBytes = kPieces * 1024 > kTiles ? kPieces * 1024 : kTiles;
+};
 template <typename T, int DXP, bool VEC>
 __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void delta_gradients_kernel(const DeltaArgs a) {
 #ifdef __HIP_DEVICE_COMPILE__
-    constexpr int DP = DXP < 128 ? DXP : 128, DA = DP / 64, NIN = Terms<T>::kIn;    // columns at once, tiles of a wave
+    using Sh = GradientShape<T, DXP>;
+    constexpr int DP = Sh::DP, DT = Sh::DT, NIN = Sh::NIN;
     using TX = RowTile<T, DP, 4>;
-    __shared__ __attribute__((aligned(1024))) T tile_k[kC * DP], tile_q[kC * DP];
-    __shared__ __attribute__((aligned(16))) f32x4 by_q[10][64], by_k[10][64], both[16][64];    // dP by queries, by keys; dC + dC^T
+    __shared__ __attribute__((aligned(1024))) char lds[Sh::kBytes];
     __shared__ double sums[kC];
-    __shared__ float weights[kC], own[4][kC], rest[4], dots[2][kC];
+    __shared__ float weights[kC], own[kC], rest[4];
     const int64_t item = blockIdx.x;
     const int64_t place = item / a.H;
     const int h = (int)(item % a.H), hk = h / a.group;
@@ -1101,266 +1137,276 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void delta_gradients_k
         sums[lane] = sum;
         weights[lane] = lane < n ? a.beta[gate0 + (int64_t)lane * a.H] : 0.0f;
     }
-    RowSource<T, DP, 4, VEC> src_k, src_q;
-    src_k.init(a.k, t.batch * a.kb + t.row0 * a.kt + hk * a.kh, a.kt, a.Dk, 0);
-    src_q.init(a.q, t.batch * a.qb + t.row0 * a.qt + hk * a.qh, a.qt, a.Dk, 0);
-    src_k.bring(t0, n, tile_k);
-    src_q.bring(t0, n, tile_q);
-    wait_loads_and_barrier<0>();
-
-    const float *S = a.states + item * a.dkp * a.dvp, *G = a.grads + item * a.dkp * a.dvp;
-    const float *W = a.wrong + item * kC * a.dvp, *Y = a.dright + item * kC * a.dvp;
-    const T *go = static_cast<const T *>(a.dout) + t.batch * a.gb + (t.row0 + t0) * a.gt + h * a.gh;
-    const auto gv = wide_view(go);
-    // 8 neighbouring values of row 16 x + c of a padded matrix
-    auto row8 = [&](const float *m, int row, int z, f32x4 &lo, f32x4 &hi) __attribute__((always_inline)) {
-        const f32x4 *p = reinterpret_cast<const f32x4 *>(m + row * a.dvp + z);
-        lo = p[0], hi = p[1];
-    };
-    auto dout8 = [&](int x, int z) __attribute__((always_inline)) {
-        const int row = 16 * x + c, left = row < n ? a.Dv - z : 0;
-        return load_row8<T, VEC>(gv, left > 0 ? (uint32_t)((row * a.gt + z) * (int64_t)sizeof(T)) : kSkip, left);
-    };
-    // u and dv of 16 x + c
-    auto weighted = [&](const float *m, int x, int z, bf8 (&out)[3]) __attribute__((always_inline)) {
-        f32x4 lo, hi;
-        row8(m, 16 * x + c, z, lo, hi);
-        const float b = weights[16 * x + c];
-        rows_terms<3>(lo * b, hi * b, out);
-    };
-    {
-        // columns: the tokens of this wave's tile; rows: those up to them (low: dP by queries, dC by its row) and
-        // from them on (high)
-        f32x4 pq[4], pk[4], cl[4], chh[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) pq[i] = pk[i] = cl[i] = chh[i] = f32x4{0, 0, 0, 0};
-        float dot_v = 0.0f, dot_w = 0.0f;
-        const T *v0 = static_cast<const T *>(a.v) + t.batch * a.vb + (t.row0 + t0) * a.vt + h * a.vh;
-        const auto vv = wide_view(v0);
-        T *dv0 = a.dv ? static_cast<T *>(a.dv) + t.batch * a.dvb + (t.row0 + t0) * a.dvt + h * a.dvh : nullptr;
-        const int mine = 16 * wave + c;
-        const float beta = weights[mine];
-#pragma unroll 1
-        for (int z = g * 8; z < a.dvp; z += 32) {
-            bf8 gx[NIN], ux[3], yx[3];
-            {
-                in_terms(dout8(wave, z), gx);
-                f32x4 wl, wh, yl, yh;
-                row8(W, mine, z, wl, wh);
-                row8(Y, mine, z, yl, yh);
-                const int left = mine < n ? a.Dv - z : 0;
-                const Raw8<T> v = load_row8<T, VEC>(vv, left > 0 ? (uint32_t)((mine * a.vt + z) * (int64_t)sizeof(T)) : kSkip, left);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) dot_w += wl[j] * yl[j] + wh[j] * yh[j];
-                rows_terms<3>(wl * beta, wh * beta, ux);
-                yl *= beta, yh *= beta;
-                rows_terms<3>(yl, yh, yx);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) dot_v += (float)v.v[j] * yl[j] + (float)v.v[4 + j] * yh[j];
-                if (dv0 && left > 0) {
-                    Raw8<T> o;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) o.v[j] = (T)yl[j], o.v[4 + j] = (T)yh[j];
-                    T *p = dv0 + mine * a.dvt + z;
-                    if (VEC && left >= 8) {
-                        __builtin_memcpy(__builtin_assume_aligned(p, 16), &o, sizeof o);
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            if (j < left) p[j] = o.v[j];
-                    }
-                }
-            }
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                if (x <= wave) {
-                    bf8 ur[3];
-                    weighted(W, x, z, ur);
-                    pq[x] = mma_terms<3>(ur, gx, pq[x]);
-                    cl[x] = mma_terms<3>(ur, yx, cl[x]);
-                }
-                if (x >= wave) {
-                    bf8 gr[NIN], yr[3];
-                    in_terms(dout8(x, z), gr);
-                    weighted(Y, x, z, yr);
-                    pk[x] = mma_terms<3>(gr, ux, pk[x]);
-                    chh[x] = mma_terms<3>(yr, ux, chh[x]);
-                }
-            }
-        }
-        dot_w += __shfl_xor(dot_w, 16), dot_v += __shfl_xor(dot_v, 16);
-        dot_w += __shfl_xor(dot_w, 32), dot_v += __shfl_xor(dot_v, 32);
-        if (g == 0) {
-            dots[0][mine] = dot_v;
-            if (a.dbeta && mine < n) a.dbeta[gate0 + (int64_t)mine * a.H] = dot_w;
-        }
-        const double gm = sums[mine];
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            f32x4 q{0, 0, 0, 0}, k{0, 0, 0, 0}, b{0, 0, 0, 0};
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int row = 16 * x + 4 * g + r;
-                const float f = exp_of(row <= mine ? gm - sums[row] : sums[row] - gm);
-                if (row <= mine) q[r] = pq[x][r] * (f * a.scale);
-                if (row >= mine) k[r] = pk[x][r] * (f * a.scale);
-                b[r] = row < mine ? -cl[x][r] * f : row > mine ? -chh[x][r] * f : 0.0f;
-            }
-            if (x <= wave) by_q[wave * (wave + 1) / 2 + x][lane] = q;
-            if (x >= wave) by_k[wave * (9 - wave) / 2 + x - wave][lane] = k;       // 4 + 3 + .. tiles before
-            both[wave * 4 + x][lane] = b;
-        }
-    }
     __syncthreads();
 
-    float dot_q = 0.0f, inner = 0.0f;
-    float mine_q[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    const float g_last = exp_of(sums[63]);
+    const float *S = a.states + item * a.dkp * a.dvp, *G = a.grads + item * a.dkp * a.dvp;
+    const int mine = 16 * wave + c;                 // this lane's token, as a column
+    const int width = mine < n ? a.Dv : 0;          // of its rows that exist
+    const float *W = a.wrong + (item * kC + mine) * a.dvp, *Y = a.dright + (item * kC + mine) * a.dvp;
+    const auto gv = wide_view(static_cast<const T *>(a.dout) + t.batch * a.gb + (t.row0 + t0) * a.gt + h * a.gh);
+    const auto vv = wide_view(static_cast<const T *>(a.v) + t.batch * a.vb + (t.row0 + t0) * a.vt + h * a.vh);
+    T *dv0 = a.dv ? static_cast<T *>(a.dv) + t.batch * a.dvb + (t.row0 + t0 + mine) * a.dvt + h * a.dvh : nullptr;
+    const float beta = weights[mine];
+    bf8 *frag = reinterpret_cast<bf8 *>(lds) + lane;
+    auto put = [&](int piece, const auto &terms) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < (int)(sizeof(terms) / sizeof(bf8)); ++i) frag[(piece + i) * 64] = terms[i];
+    };
+    auto get = [&](int piece, auto &terms) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < (int)(sizeof(terms) / sizeof(bf8)); ++i) terms[i] = frag[(piece + i) * 64];
+    };
+
+    // slot i: dP and dC of the wave's tokens with those of tile i up to its own (slots 0 .. wave, rows earlier), then
+    // with those of tile i - 1 from its own on (rows later)
+    f32x4 dp[5], dc[5];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) dp[i] = dc[i] = f32x4{0, 0, 0, 0};
+    float dot_v = 0.0f, dot_w = 0.0f, dot_q = 0.0f, dot_k = 0.0f, inner = 0.0f;
+    const double gm = sums[mine];
+    const float first = exp_of(gm), last = exp_of(sums[63] - gm);
+
 #pragma unroll 1
-    for (int col0 = 0; col0 < DXP; col0 += DP) {
-        if (col0 > 0) {
-            if (col0 >= a.Dk) break;
-            __syncthreads();
-            src_k.col0 = src_q.col0 = col0;
-            src_k.bring(t0, n, tile_k);
-            src_q.bring(t0, n, tile_q);
-            wait_loads_and_barrier<0>();
-        }
-        f32x4 qa[DA][4], ka[DA][4], va[DA][4];      // rows of the states x tokens
+    for (int col0 = 0; col0 < DXP && col0 < a.Dk; col0 += DP) {
+        f32x4 qa[DT], ka[DT], va[DT];      // S dO, G u, S dv: rows of the states x tokens
 #pragma unroll
-        for (int d = 0; d < DA; ++d)
+        for (int d = 0; d < DT; ++d) qa[d] = ka[d] = va[d] = f32x4{0, 0, 0, 0};
+        // a block's values, on their way while the block before is multiplied
+        f32x4 wl, wh, yl, yh, sl[DT / 4], sh[DT / 4], gl[DT / 4], gh[DT / 4];
+        Raw8<T> go, v;
+        auto fetch = [&](int z0) __attribute__((always_inline)) {
+            const int z = z0 + g * 8, left = width - z;
+            const f32x4 *wp = reinterpret_cast<const f32x4 *>(W + z), *yp = reinterpret_cast<const f32x4 *>(Y + z);
+            wl = wp[0], wh = wp[1], yl = yp[0], yh = yp[1];
+            go = load_row8<T, VEC>(gv, left > 0 ? (uint32_t)((mine * a.gt + z) * (int64_t)sizeof(T)) : kSkip, left);
+            if (col0 == 0) v = load_row8<T, VEC>(vv, left > 0 ? (uint32_t)((mine * a.vt + z) * (int64_t)sizeof(T)) : kSkip, left);
 #pragma unroll
-            for (int x = 0; x < 4; ++x) qa[d][x] = ka[d][x] = va[d][x] = f32x4{0, 0, 0, 0};
-#pragma unroll 1
-        for (int z = g * 8; z < a.dvp; z += 32) {
-            bf8 sf[DA][3], gf[DA][3];
-#pragma unroll
-            for (int d = 0; d < DA; ++d) {
-                const int row = col0 + (wave * DA + d) * 16 + c;
-                f32x4 sl, sh, gl, gh;
-                row8(S, row, z, sl, sh);
-                row8(G, row, z, gl, gh);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) inner += sl[j] * gl[j] + sh[j] * gh[j];
-                rows_terms<3>(sl, sh, sf[d]);
-                rows_terms<3>(gl, gh, gf[d]);
+            for (int d = 0; d < DT / 4; ++d) {
+                // (rows of a pair of tiles in the order of the state's own: a lane's results of both are neighbours)
+                const int tile = wave * (DT / 4) + d;
+                const int64_t at = (col0 + (tile >> 1) * 32 + (c >> 2) * 8 + (tile & 1) * 4 + (c & 3)) * (int64_t)a.dvp + z;
+                const f32x4 *sp = reinterpret_cast<const f32x4 *>(S + at), *gp = reinterpret_cast<const f32x4 *>(G + at);
+                sl[d] = sp[0], sh[d] = sp[1], gl[d] = gp[0], gh[d] = gp[1];
             }
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                bf8 gx[NIN], ux[3], vx[3];
-                in_terms(dout8(x, z), gx);
-                weighted(W, x, z, ux);
-                weighted(Y, x, z, vx);
-#pragma unroll
-                for (int d = 0; d < DA; ++d) {
-                    qa[d][x] = mma_terms<3>(sf[d], gx, qa[d][x]);
-                    ka[d][x] = mma_terms<3>(gf[d], ux, ka[d][x]);
-                    va[d][x] = mma_terms<3>(sf[d], vx, va[d][x]);
-                }
-            }
-        }
-        // 4 values of token 16 x + c at this lane's rows of tile d
-        auto row4 = [&](const T *tile, int d, int x, float (&f)[4]) __attribute__((always_inline)) {
-            const int col = (wave * DA + d) * 16 + 4 * g;
-            const T *p = TX::at(tile, 16 * x + c, col / TX::E) + col % TX::E;
-            struct Four { T v[4]; };
-            const Four v = *reinterpret_cast<const Four *>(p);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) f[j] = (float)v.v[j];
         };
+        fetch(0);
+#pragma unroll 1
+        for (int z0 = 0; z0 < a.dvp; z0 += 32) {
+            const int z = z0 + g * 8;
+            bf8 gx[NIN], ux[3], yx[3];
+            {
+                const int left = width - z;
+                if (col0 == 0) {
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            const double gx = sums[16 * x + c];
-            const float first = exp_of(gx), last = exp_of(sums[63] - gx);
+                    for (int j = 0; j < 4; ++j) {
+                        dot_w += wl[j] * yl[j] + wh[j] * yh[j];
+                        dot_v += (float)v.v[j] * (yl[j] * beta) + (float)v.v[4 + j] * (yh[j] * beta);
+                    }
+                    if (dv0 && left > 0) {
+                        Raw8<T> o;
 #pragma unroll
-            for (int d = 0; d < DA; ++d) {
-                qa[d][x] *= a.scale * first;
-                ka[d][x] *= last;
-                float k[4];
-                row4(tile_k, d, x, k);
+                        for (int j = 0; j < 4; ++j) o.v[j] = (T)(yl[j] * beta), o.v[4 + j] = (T)(yh[j] * beta);
+                        if (VEC && left >= 8) {
+                            __builtin_memcpy(__builtin_assume_aligned(dv0 + z, 16), &o, sizeof o);
+                        } else {
 #pragma unroll
-                for (int r = 0; r < 4; ++r) dot_q += k[r] * ka[d][x][r];      // <G, what the chunk adds to the state>
-                ka[d][x] -= va[d][x] * first;
+                            for (int j = 0; j < 8; ++j)
+                                if (j < left) dv0[z + j] = o.v[j];
+                        }
+                    }
+                }
+                in_terms(go, gx);
+                rows_terms<3>(wl * beta, wh * beta, ux);
+                rows_terms<3>(yl * beta, yh * beta, yx);
+                if (z0 > 0 || col0 > 0) __syncthreads();       // the block before has been read
+                put(Sh::kG + wave * NIN, gx);
+                put(Sh::kU + wave * 3, ux);
+                put(Sh::kY + wave * 3, yx);
+#pragma unroll
+                for (int d = 0; d < DT / 4; ++d) {
+                    bf8 x[3];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) inner += sl[d][j] * gl[d][j] + sh[d][j] * gh[d][j];
+                    rows_terms<3>(sl[d], sh[d], x);
+                    put(Sh::kS + (wave * (DT / 4) + d) * 3, x);
+                    rows_terms<3>(gl[d], gh[d], x);
+                    put(Sh::kD + (wave * (DT / 4) + d) * 3, x);
+                }
+            }
+            __syncthreads();
+            if (z0 + 32 < a.dvp) fetch(z0 + 32);
+            if (col0 == 0) {
+#pragma unroll
+                for (int i = 0; i < 5; ++i) {
+                    if (i <= wave && i < 4) {
+                        bf8 u[3];
+                        get(Sh::kU + i * 3, u);
+                        dp[i] = mma_terms<3>(u, gx, dp[i]);
+                        dc[i] = mma_terms<3>(u, yx, dc[i]);
+                    } else if (i > wave) {
+                        bf8 o[NIN], y[3];
+                        get(Sh::kG + (i - 1) * NIN, o);
+                        get(Sh::kY + (i - 1) * 3, y);
+                        dp[i] = mma_terms<3>(o, ux, dp[i]);
+                        dc[i] = mma_terms<3>(y, ux, dc[i]);
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            }
+#pragma unroll
+            for (int d = 0; d < DT; ++d) {
+                bf8 x[3];
+                get(Sh::kS + d * 3, x);
+#pragma unroll
+                for (int i = 0; i < 3; ++i)      // (two accumulators in turn)
+#pragma unroll
+                    for (int j = 0; i + j < 3; ++j) {
+                        if (j < NIN) qa[d] = Mma<__bf16>::mma(x[i], gx[j < NIN ? j : 0], qa[d]);
+                        va[d] = Mma<__bf16>::mma(x[i], yx[j], va[d]);
+                    }
+                get(Sh::kD + d * 3, x);
+                ka[d] = mma_terms<3>(x, ux, ka[d]);
+                __builtin_amdgcn_sched_barrier(0);      // (operands of all tiles at once would not fit the registers)
             }
         }
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            bf8 kf[DA][NIN], qf[DA][NIN];
-#pragma unroll
-            for (int d = 0; d < DA; ++d) {
-                const int base = (wave * DA + d) * 16;
-                in_terms(TX::col8(tile_k, s, base + (lane & 3) * 4, base + c), kf[d]);
-                in_terms(TX::col8(tile_q, s, base + (lane & 3) * 4, base + c), qf[d]);
-            }
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                const f32x4 zero{0, 0, 0, 0};
-                const int lo = 2 * s, hi = 2 * s + 1;
-                bf8 m[3];
-                if (lo <= x) {
-                    rows_terms<3>(by_q[x * (x + 1) / 2 + lo][lane], hi <= x ? by_q[x * (x + 1) / 2 + hi][lane] : zero, m);
-#pragma unroll
-                    for (int d = 0; d < DA; ++d) qa[d][x] = mma_terms<3>(kf[d], m, qa[d][x]);
-                }
-                if (hi >= x) {
-                    rows_terms<3>(lo >= x ? by_k[x * (9 - x) / 2 + lo - x][lane] : zero, by_k[x * (9 - x) / 2 + hi - x][lane], m);
-#pragma unroll
-                    for (int d = 0; d < DA; ++d) ka[d][x] = mma_terms<3>(qf[d], m, ka[d][x]);
-                }
-                rows_terms<3>(both[x * 4 + lo][lane], both[x * 4 + hi][lane], m);
-#pragma unroll
-                for (int d = 0; d < DA; ++d) ka[d][x] = mma_terms<3>(kf[d], m, ka[d][x]);
-            }
+        __syncthreads();
+        // k and q in the place of the operands
+        T *tile_k = reinterpret_cast<T *>(lds), *tile_q = reinterpret_cast<T *>(lds + TX::BYTES);
+        {
+            RowSource<T, DP, 4, VEC> src;
+            src.init(a.k, t.batch * a.kb + t.row0 * a.kt + hk * a.kh, a.kt, a.Dk, col0);
+            src.bring(t0, n, tile_k);
+            src.init(a.q, t.batch * a.qb + t.row0 * a.qt + hk * a.qh, a.qt, a.Dk, col0);
+            src.bring(t0, n, tile_q);
         }
-        // out: lane (g, c) has 4 neighbouring columns of token 16 x + c
-        auto put = [&](void *base, int64_t sb, int64_t st, int64_t sh, const f32x4 &v, int d, int x) __attribute__((always_inline)) {
-            const int row = 16 * x + c, col = col0 + (wave * DA + d) * 16 + 4 * g, left = a.Dk - col;
-            if (!base || row >= n || left <= 0) return;
+        wait_loads_and_barrier<0>();
+        // out: lane (g, c) has 8 neighbouring columns of its token
+        auto out = [&](void *base, int64_t sb, int64_t st, int64_t sh, const f32x4 (&v)[2], int col) __attribute__((always_inline)) {
+            const int left = a.Dk - col;
+            if (!base || mine >= n || left <= 0) return;
             if (a.parts) {
-                float *p = static_cast<float *>(base) + ((t.batch * a.N + t.row0 + t0 + row) * a.H + h) * (int64_t)a.Dk + col;
+                float *p = static_cast<float *>(base) + ((t.batch * a.N + t.row0 + t0 + mine) * a.H + h) * (int64_t)a.Dk + col;
+                if (VEC) {          // (rows of whole 16-byte pieces)
+                    *reinterpret_cast<f32x4 *>(p) = v[0];
+                    if (left > 4) *reinterpret_cast<f32x4 *>(p + 4) = v[1];
+                } else {
 #pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    if (r < left) p[r] = v[r];
+                    for (int r = 0; r < 8; ++r)
+                        if (r < left) p[r] = v[r >> 2][r & 3];
+                }
                 return;
             }
-            T *p = static_cast<T *>(base) + t.batch * sb + (t.row0 + t0 + row) * st + hk * sh + col;
-            struct Four { T v[4]; } o;
+            T *p = static_cast<T *>(base) + t.batch * sb + (t.row0 + t0 + mine) * st + hk * sh + col;
+            Raw8<T> o;
 #pragma unroll
-            for (int r = 0; r < 4; ++r) o.v[r] = (T)v[r];
-            if (VEC && left >= 4) {
-                __builtin_memcpy(__builtin_assume_aligned(p, 4 * sizeof(T)), &o, sizeof o);
+            for (int r = 0; r < 8; ++r) o.v[r] = (T)v[r >> 2][r & 3];
+            if (VEC && (sizeof(T) == 2 || left > 4)) {
+                __builtin_memcpy(__builtin_assume_aligned(p, 16), &o, sizeof o);
             } else {
 #pragma unroll
-                for (int r = 0; r < 4; ++r)
+                for (int r = 0; r < 8; ++r)
                     if (r < left) p[r] = o.v[r];
             }
         };
+        TileReader<T, DP, 4> in;
+        in.init();
+        const char *ck = lds, *cq = lds + TX::BYTES;
+        double from = gm;
+        asm volatile("" : "+v"(from));       // (the factors are formed anew for each 64 columns: kept, they would cost registers)
+        // the masked, decayed products as operands over tokens: dP for dq, then those for dk
+        auto decay = [&](int row) __attribute__((always_inline)) { return exp_of(row <= mine ? from - sums[row] : sums[row] - from); };
+        {
+            bf8 m[2][3];
 #pragma unroll
-        for (int x = 0; x < 4; ++x)
+            for (int s = 0; s < 2; ++s) {
+                f32x4 x[2];
 #pragma unroll
-            for (int d = 0; d < DA; ++d) {
-                float q[4];
-                row4(tile_q, d, x, q);
+                for (int half = 0; half < 2; ++half)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) mine_q[x] += q[r] * qa[d][x][r];
-                put(a.dq, a.dqb, a.dqt, a.dqh, qa[d][x], d, x);
-                put(a.dk, a.dkb, a.dkt, a.dkh, ka[d][x], d, x);
+                    for (int r = 0; r < 4; ++r) {
+                        const int row = 32 * s + 16 * half + 4 * g + r;
+                        x[half][r] = row <= mine ? dp[2 * s + half][r] * (decay(row) * a.scale) : 0.0f;
+                    }
+                rows_terms<3>(x[0], x[1], m[s]);
             }
-    }
-    if (!a.dlog_decay) return;
 #pragma unroll
-    for (int x = 0; x < 4; ++x) {
-        mine_q[x] += __shfl_xor(mine_q[x], 16);
-        mine_q[x] += __shfl_xor(mine_q[x], 32);
-        if (g == 0) own[wave][16 * x + c] = mine_q[x];
+            for (int kk = 0; kk < DP / 32; ++kk) {
+                f32x4 dq[2];
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    dq[r] = qa[2 * kk + r] * (a.scale * first);
+#pragma unroll
+                    for (int s = 0; s < 2; ++s)
+                        if (s == 0 || wave >= 2) {
+                            bf8 x[NIN];
+                            in_terms(in.col8(ck, s, kk, r), x);
+                            dq[r] = mma_terms<3>(x, m[s], dq[r]);
+                        }
+                }
+                const Raw8<T> q = in.row8(cq + wave * 16 * TileReader<T, DP, 4>::RB, 0, kk);
+#pragma unroll
+                for (int r = 0; r < 8; ++r) dot_q += (float)q.v[r] * dq[r >> 2][r & 3];
+                out(a.dq, a.dqb, a.dqt, a.dqh, dq, col0 + kk * 32 + 8 * g);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+        {
+            bf8 m[2][3], b[2][3];
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                f32x4 x[2], y[2];
+#pragma unroll
+                for (int half = 0; half < 2; ++half)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int row = 32 * s + 16 * half + 4 * g + r, tile = 2 * s + half;
+                        const float f = decay(row);
+                        x[half][r] = row >= mine ? dp[tile + 1][r] * (f * a.scale) : 0.0f;
+                        y[half][r] = row < mine ? -dc[tile][r] * f : row > mine ? -dc[tile + 1][r] * f : 0.0f;
+                    }
+                rows_terms<3>(x[0], x[1], m[s]);
+                rows_terms<3>(y[0], y[1], b[s]);
+            }
+#pragma unroll
+            for (int kk = 0; kk < DP / 32; ++kk) {
+                f32x4 dk[2];
+                const Raw8<T> k = in.row8(ck + wave * 16 * TileReader<T, DP, 4>::RB, 0, kk);
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    dk[r] = ka[2 * kk + r] * last;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) dot_k += (float)k.v[4 * r + i] * dk[r][i];      // <G, what the chunk adds to the state>
+                    dk[r] -= va[2 * kk + r] * first;
+#pragma unroll
+                    for (int s = 0; s < 2; ++s) {
+                        bf8 x[NIN];
+                        in_terms(in.col8(ck, s, kk, r), x);
+                        dk[r] = mma_terms<3>(x, b[s], dk[r]);
+                        if (s == 1 || wave < 2) {
+                            in_terms(in.col8(cq, s, kk, r), x);
+                            dk[r] = mma_terms<3>(x, m[s], dk[r]);
+                        }
+                    }
+                }
+                out(a.dk, a.dkb, a.dkt, a.dkh, dk, col0 + kk * 32 + 8 * g);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
     }
-    float behind = dot_q + g_last * inner;
+    // a token's own dot products: four lanes have parts of each
+    float each = dot_q - dot_v;
+    dot_w += __shfl_xor(dot_w, 16), each += __shfl_xor(each, 16);
+    dot_w += __shfl_xor(dot_w, 32), each += __shfl_xor(each, 32);
+    if (a.dbeta && g == 0 && mine < n) a.dbeta[gate0 + (int64_t)mine * a.H] = dot_w;
+    if (!a.dlog_decay) return;
+    if (g == 0) own[mine] = each;
+    float behind = dot_k + exp_of(sums[63]) * inner;      // <G, S behind>
 #pragma unroll
     for (int s = 1; s < 64; s <<= 1) behind += __shfl_xor(behind, s);
     if (lane == 0) rest[wave] = behind;
     __syncthreads();
     if (wave == 0) {
-        double sum = (double)((own[0][lane] + own[1][lane]) + (own[2][lane] + own[3][lane])) - (double)dots[0][lane];
+        double sum = own[lane];
 #pragma unroll
         for (int s = 1; s < 64; s <<= 1) {
             const double down = __shfl_down(sum, s);

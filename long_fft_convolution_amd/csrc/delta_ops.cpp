@@ -258,7 +258,7 @@ struct DeltaBwdLayout {
 };
 DeltaBwdLayout bwd_layout(const DeltaShape &s) {
     DeltaBwdLayout l{};
-    l.wide = fwd_cut(s).wide;
+    l.wide = s.Dk <= 128 && s.Dv > 64 && 2 * s.B * s.H * ceil_div(s.Dv, 64) > kCus;     // (two walks)
     l.dkp = padded_width(s.Dk);
     l.dvp = round_up(s.Dv, l.wide ? 128 : 64);
     const size_t items = (size_t)s.places(kDeltaChunk) * s.H;
