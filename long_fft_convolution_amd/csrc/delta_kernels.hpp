@@ -560,6 +560,10 @@ template <typename T, int DP, int WAVES> struct ColumnReader {
 };
 
 // ---- the state in a wave's accumulators ------------------------------------------
+// Place of an element in a matrix kept for the gradients, which read it 32 columns at a time: blocks of 32 columns of all
+// `rows`.
+__device__ __forceinline__ uint32_t kept_at(int row, int col, int rows) { return (uint32_t)((col >> 5) * rows * 32 + row * 32 + (col & 31)); }
+
 // v[kk][r]: rows kk * 32 + g * 8 + r * 4 + i of the column of lane (g, c): as an operand over rows, the lane holds the
 // slots 8 g + j of its column.
 template <int KX> struct State {
@@ -602,16 +606,24 @@ template <int KX> struct State {
             return x;
         });
     }
+    // into a matrix kept for the gradients
+    __device__ __forceinline__ void keep_blocks(float *p, int col) {
+        const auto view = wide_view(p);
+        each([&](int row, float x) __attribute__((always_inline)) {
+            view_store(view, kept_at(row, col, KX * 32) * 4u, x);
+            return x;
+        });
+    }
     __device__ __forceinline__ void terms(int kk, bf8 (&out)[3]) const { rows_terms<3>(v[kk][0], v[kk][1], out); }
 };
-// accumulators over tokens (rows 16 r + 4 g + i) into a matrix of 64 padded rows
-__device__ __forceinline__ void keep_rows(float *p, int ld, const f32x4 (&x)[4], int col) {
+// accumulators over tokens (rows 16 r + 4 g + i) into a matrix kept for the gradients
+__device__ __forceinline__ void keep_rows(float *p, const f32x4 (&x)[4], int col) {
     const auto view = wide_view(p);
     const int g = (threadIdx.x & 63) >> 4;
 #pragma unroll
     for (int r = 0; r < 4; ++r)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) view_store(view, (uint32_t)((16 * r + 4 * g + i) * ld + col) * 4u, x[r][i]);
+        for (int i = 0; i < 4; ++i) view_store(view, kept_at(16 * r + 4 * g + i, col, kC) * 4u, x[r][i]);
 }
 
 // Work item of workgroup id: ids go to the 8 XCDs in turn, so runs of `run` items are dealt to one XCD, whose L2
@@ -629,6 +641,10 @@ inline __host__ __device__ int delta_run(int tiles, int group) {
 // the backward call, the state before each chunk and w.
 enum DeltaMode : int { kDeltaSums = 0, kDeltaOut = 1, kDeltaKeep = 2 };
 
+// Waves a SIMD that the compiler leaves registers for: the sums' walks, which cut sequences into twice as many pieces as
+// walk at once, share a CU (131072 tokens x 20 heads of 128: 1400 us, 1555 with one of two stages).
+constexpr int walk_waves(int dxp, int waves, int mode, int bytes) { return mode == kDeltaSums && bytes == 2 && dxp <= 128 ? waves / 2 : 1; }
+
 // Eight waves a workgroup, two a SIMD (one splits fp32 values while the other multiplies), for 128 columns; four for 64.
 template <typename T, int DXP, int WAVES, int MODE, bool VEC> struct WalkShape {
     static constexpr bool OUT = MODE == kDeltaOut;
@@ -641,7 +657,9 @@ template <typename T, int DXP, int WAVES, int MODE, bool VEC> struct WalkShape {
     static constexpr int kPieces = kRec + kAll * 1024 <= kLdsBytes ? kAll : kRec + kFew * 1024 <= kLdsBytes ? kFew : 0;
     static constexpr bool kRecord = kPieces > 0, kProducts = kPieces >= kAll;
     static constexpr int kBytes = kRec + kPieces * 1024;
-    static constexpr int kStages = VEC && 2 * kBytes <= kLdsBytes ? 2 : 1;
+    // (sums: two workgroups a CU, one of which loads while the other multiplies)
+    static constexpr bool kShared = walk_waves(DXP, WAVES, MODE, sizeof(T)) > 1;
+    static constexpr int kStages = VEC && 2 * kBytes <= kLdsBytes && !kShared ? 2 : 1;
     static_assert(kBytes <= kLdsBytes, "LDS");
 };
 
@@ -682,15 +700,17 @@ __device__ __forceinline__ void delta_walk(const DeltaArgs &a, char *lds, uint32
     src_v.init(a.v, tk.batch * a.vb + tk.row0 * a.vt + h * a.vh, a.vt, map ? 0 : a.Dv, col0);
     const char *rec0 = a.rec + (first_place(a, tk.seq, kC) * a.H + h) * a.rec_bytes;
     const int64_t rec_step = a.H * a.rec_bytes;
-    auto bring = [&](int64_t ch, char *stage) __attribute__((always_inline)) {
+    // part 0, 1, 2 of a chunk, -1 for all: the next chunk's loads are spread over this one's products, since a wave that
+    // issues many at once waits for the address unit
+    auto bring = [&](int64_t ch, char *stage, int part) __attribute__((always_inline)) {
         const int64_t t = ch * kC;
         const int n = tk.len - t < kC ? (int)(tk.len - t) : kC;
-        src_k.bring(t, n, reinterpret_cast<T *>(stage));
-        if (OUT) src_q.bring(t, n, reinterpret_cast<T *>(stage + W::kQ));
-        src_v.bring(t, n, reinterpret_cast<T *>(stage + W::kV));
-        if (W::kRecord) bring_record<WAVES, VEC>(rec0 + ch * rec_step, W::kPieces, stage + W::kRec);
+        if (part <= 0) src_k.bring(t, n, reinterpret_cast<T *>(stage));
+        if (OUT && (part < 0 || part == 1)) src_q.bring(t, n, reinterpret_cast<T *>(stage + W::kQ));
+        if (part < 0 || part == 1) src_v.bring(t, n, reinterpret_cast<T *>(stage + W::kV));
+        if (W::kRecord && (part < 0 || part == 2)) bring_record<WAVES, VEC>(rec0 + ch * rec_step, W::kPieces, stage + W::kRec);
     };
-    if (W::kStages == 2 && first < end) bring(first, lds);
+    if (W::kStages == 2 && first < end) bring(first, lds, -1);
 
     TileReader<T, DXP, WAVES> in_k;
     ColumnReader<T, DZT, WAVES> in_v;
@@ -717,24 +737,27 @@ __device__ __forceinline__ void delta_walk(const DeltaArgs &a, char *lds, uint32
         char *stage = lds;
         if constexpr (W::kStages == 2) {
             stage += ((ch - first) & 1) * W::kBytes;
-            // This chunk's loads were issued a chunk ago; four stores followed them (16-bit outputs).  The wait on LDS
+            // This chunk's loads were issued in the last one; four stores followed them (16-bit outputs).  The wait on LDS
             // reads keeps every wave's reads of the other stage before the loads into it.
             if (OUT && sizeof(T) == 2 && ch > first) wait_loads_and_barrier<4>();
-            else if (MODE == kDeltaKeep && ch > first) wait_loads_and_barrier<16>();     // (the states' stores: 16 at least)
+            else if (MODE == kDeltaKeep && ch > first) wait_loads_and_barrier<16>();     // (those of w)
             else wait_loads_and_barrier<0>();
-            if (ch + 1 < end) bring(ch + 1, lds + ((ch + 1 - first) & 1) * W::kBytes);
         } else {
             __syncthreads();
-            bring(ch, stage);
+            bring(ch, stage, -1);
             wait_loads_and_barrier<0>();
         }
+        auto ahead = [&](int part) __attribute__((always_inline)) {
+            if (W::kStages == 2 && ch + 1 < end) bring(ch + 1, lds + ((ch + 1 - first) & 1) * W::kBytes, part);
+        };
+        ahead(0);
         const char *far = rec0 + ch * rec_step, *rec = W::kRecord ? stage + W::kRec : far;
         const bf8 *inv = reinterpret_cast<const bf8 *>(rec) + lane;
         const float *vec = reinterpret_cast<const float *>(rec + kDeltaInverse * 1024);
         const f32x4 *vec4 = reinterpret_cast<const f32x4 *>(vec) + g;      // the rows 16 r + 4 g ..: [4 r]
         const bf8 *prod = reinterpret_cast<const bf8 *>((W::kProducts ? rec : far) + (kDeltaInverse + kDeltaVectors) * 1024) + lane;
         const int64_t kept = (rec0 - a.rec) / a.rec_bytes + ch * a.H;      // (chunk, head)
-        if (MODE == kDeltaKeep) S.keep(a.states + kept * a.dkp * a.dvp, a.dvp, column);
+        if (MODE == kDeltaKeep) S.keep_blocks(a.states + kept * a.dkp * a.dvp, column);
         // k S
         f32x4 x[4], o[4];
 #pragma unroll
@@ -758,6 +781,7 @@ __device__ __forceinline__ void delta_walk(const DeltaArgs &a, char *lds, uint32
 #pragma unroll
                         for (int r = 0; r < 4; ++r) x[r] = Mma<__bf16>::mma(kf[r][i], st[j], x[r]);
         }
+        ahead(1);
         // r = v - exp(G) k S as operands over tokens
         bf8 rs[2][3];
 #pragma unroll
@@ -789,6 +813,7 @@ __device__ __forceinline__ void delta_walk(const DeltaArgs &a, char *lds, uint32
                             for (int r = 0; r < 4; ++r) o[r] = Mma<__bf16>::mma(few[kk][j], qf[r][i], o[r]);
             }
         }
+        ahead(2);
         // w = inverse r, u = beta w; terms outermost, so that an accumulator's next product comes four instructions later
         f32x4 u[4];
 #pragma unroll
@@ -801,7 +826,7 @@ __device__ __forceinline__ void delta_walk(const DeltaArgs &a, char *lds, uint32
                 for (int j = 0; i + j < 3; ++j)
 #pragma unroll
                     for (int r = 2 * s; r < 4; ++r) u[r] = Mma<__bf16>::mma(inv[((r + 1) * (r + 1) / 4 + s) * 192 + i * 64], rs[s][j], u[r]);
-        if (MODE == kDeltaKeep) keep_rows(a.wrong + kept * kC * a.dvp, a.dvp, u, col0 + zw + c);
+        if (MODE == kDeltaKeep) keep_rows(a.wrong + kept * kC * a.dvp, u, column);
 #pragma unroll
         for (int r = 0; r < 4; ++r) u[r] *= vec4[32 + 4 * r];
         // S <- exp(G_last) S + k^T (exp(G_last - G) u)
@@ -867,7 +892,7 @@ __device__ __forceinline__ void delta_walk(const DeltaArgs &a, char *lds, uint32
 #endif
 
 template <typename T, int DXP, int WAVES, int MODE, bool VEC>
-__global__ __launch_bounds__(walk_bound(DXP, WAVES, sizeof(T))) void delta_walk_kernel(const DeltaArgs a, int ztiles, int tiles) {
+__global__ __launch_bounds__(walk_bound(DXP, WAVES, sizeof(T)), walk_waves(DXP, WAVES, MODE, sizeof(T))) void delta_walk_kernel(const DeltaArgs a, int ztiles, int tiles) {
 #ifdef __HIP_DEVICE_COMPILE__
     using W = WalkShape<T, DXP, WAVES, MODE, VEC>;
     __shared__ __attribute__((aligned(1024))) char lds[W::kStages * W::kBytes];
@@ -934,15 +959,15 @@ __device__ __forceinline__ void delta_walk_back(const DeltaArgs &a, char *lds, u
     // vectors, then the operands
     const char *rec0 = a.rec + item0 * a.rec_bytes + kDeltaInverse * 1024;
     const int64_t rec_step = a.H * a.rec_bytes;
-    auto bring = [&](int64_t ch, char *stage) __attribute__((always_inline)) {
+    auto bring = [&](int64_t ch, char *stage, int part) __attribute__((always_inline)) {      // (parts as in the forward walk)
         const int64_t t = ch * kC;
         const int n = tk.len - t < kC ? (int)(tk.len - t) : kC;
-        src_k.bring(t, n, reinterpret_cast<T *>(stage));
-        src_q.bring(t, n, reinterpret_cast<T *>(stage + W::kQ));
-        src_g.bring(t, n, reinterpret_cast<T *>(stage + W::kG));
-        if (W::kRecord) bring_record<WAVES, VEC>(rec0 + ch * rec_step, W::kPieces, stage + W::kRec);
+        if (part <= 0) src_k.bring(t, n, reinterpret_cast<T *>(stage));
+        if (part < 0 || part == 1) src_g.bring(t, n, reinterpret_cast<T *>(stage + W::kG));
+        if (part < 0 || part == 1) src_q.bring(t, n, reinterpret_cast<T *>(stage + W::kQ));
+        if (W::kRecord && (part < 0 || part == 2)) bring_record<WAVES, VEC>(rec0 + ch * rec_step, W::kPieces, stage + W::kRec);
     };
-    if (W::kStages == 2 && chunks > 0) bring(chunks - 1, lds);
+    if (W::kStages == 2 && chunks > 0) bring(chunks - 1, lds, -1);
 
     TileReader<T, DXP, WAVES> in_k;
     ColumnReader<T, DZT, WAVES> in_g;
@@ -958,21 +983,24 @@ __device__ __forceinline__ void delta_walk_back(const DeltaArgs &a, char *lds, u
         char *stage = lds;
         if constexpr (W::kStages == 2) {
             stage += (back & 1) * W::kBytes;
-            if (back > 0) wait_loads_and_barrier<16>();      // (stores followed those loads, 32 at least)
+            if (back > 0) wait_loads_and_barrier<16>();      // (sixteen stores of y followed the last of those loads)
             else wait_loads_and_barrier<0>();
-            if (ch > 0) bring(ch - 1, lds + ((back + 1) & 1) * W::kBytes);
         } else {
             __syncthreads();
-            bring(ch, stage);
+            bring(ch, stage, -1);
             wait_loads_and_barrier<0>();
         }
+        auto ahead = [&](int part) __attribute__((always_inline)) {
+            if (W::kStages == 2 && ch > 0) bring(ch - 1, lds + ((back + 1) & 1) * W::kBytes, part);
+        };
         const char *far = rec0 + ch * rec_step, *rec = W::kRecord ? stage + W::kRec : far;
         const float *vec = reinterpret_cast<const float *>(rec);
         const f32x4 *vec4 = reinterpret_cast<const f32x4 *>(vec) + g;
         const bf8 *inv = reinterpret_cast<const bf8 *>(rec + kDeltaVectors * 1024) + lane;
         const f32x4 *prod = reinterpret_cast<const f32x4 *>((W::kProducts ? rec : far) + (kDeltaVectors + kDeltaInverse) * 1024) + lane;
         const int64_t item = item0 + ch * a.H;
-        G.keep(a.grads + item * a.dkp * a.dvp, a.dvp, column);
+        ahead(0);
+        G.keep_blocks(a.grads + item * a.dkp * a.dvp, column);
 
         // the outputs' gradients as operands over tokens, as they are and by scale exp(G)
         bf8 gf[2][NIN], gs[2][3];
@@ -1005,6 +1033,7 @@ __device__ __forceinline__ void delta_walk_back(const DeltaArgs &a, char *lds, u
 #pragma unroll
                         for (int r = 0; r < 4; ++r) x[r] = Mma<__bf16>::mma(kf[r][i], st[j], x[r]);
         }
+        ahead(1);
 #pragma unroll
         for (int r = 0, e = 0; r < 4; ++r)
 #pragma unroll
@@ -1013,6 +1042,7 @@ __device__ __forceinline__ void delta_walk_back(const DeltaArgs &a, char *lds, u
                 rows_terms<3>(prod[e * 128], prod[e * 128 + 64], pf);
                 p[r] = mma_terms<3>(pf, gf[s], p[r]);
             }
+        ahead(2);
         // y
         bf8 xs[2][3];
 #pragma unroll
@@ -1036,7 +1066,7 @@ __device__ __forceinline__ void delta_walk_back(const DeltaArgs &a, char *lds, u
                         const int e = (r < 2 ? 2 * r + s : 3 + r - 1 + s - 1);      // operands (r, s >= r / 2) in order
                         y[r] = Mma<__bf16>::mma(inv[e * 192 + i * 64], xs[s][j], y[r]);
                     }
-        keep_rows(a.dright + item * kC * a.dvp, a.dvp, y, column);
+        keep_rows(a.dright + item * kC * a.dvp, y, column);
         // G <- exp(G_last) G + q^T (scale exp(G) dO) - k^T (exp(G) beta y)
         const float keep = vec[63];
         bf8 ys[2][3];
@@ -1142,7 +1172,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void delta_gradients_k
     const float *S = a.states + item * a.dkp * a.dvp, *G = a.grads + item * a.dkp * a.dvp;
     const int mine = 16 * wave + c;                 // this lane's token, as a column
     const int width = mine < n ? a.Dv : 0;          // of its rows that exist
-    const float *W = a.wrong + (item * kC + mine) * a.dvp, *Y = a.dright + (item * kC + mine) * a.dvp;
+    const float *W = a.wrong + item * kC * a.dvp + mine * 32 + g * 8, *Y = a.dright + item * kC * a.dvp + mine * 32 + g * 8;
     const auto gv = wide_view(static_cast<const T *>(a.dout) + t.batch * a.gb + (t.row0 + t0) * a.gt + h * a.gh);
     const auto vv = wide_view(static_cast<const T *>(a.v) + t.batch * a.vb + (t.row0 + t0) * a.vt + h * a.vh);
     T *dv0 = a.dv ? static_cast<T *>(a.dv) + t.batch * a.dvb + (t.row0 + t0 + mine) * a.dvt + h * a.dvh : nullptr;
@@ -1176,7 +1206,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void delta_gradients_k
         Raw8<T> go, v;
         auto fetch = [&](int z0) __attribute__((always_inline)) {
             const int z = z0 + g * 8, left = width - z;
-            const f32x4 *wp = reinterpret_cast<const f32x4 *>(W + z), *yp = reinterpret_cast<const f32x4 *>(Y + z);
+            const f32x4 *wp = reinterpret_cast<const f32x4 *>(W + z0 * kC), *yp = reinterpret_cast<const f32x4 *>(Y + z0 * kC);
             wl = wp[0], wh = wp[1], yl = yp[0], yh = yp[1];
             go = load_row8<T, VEC>(gv, left > 0 ? (uint32_t)((mine * a.gt + z) * (int64_t)sizeof(T)) : kSkip, left);
             if (col0 == 0) v = load_row8<T, VEC>(vv, left > 0 ? (uint32_t)((mine * a.vt + z) * (int64_t)sizeof(T)) : kSkip, left);
@@ -1184,7 +1214,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void delta_gradients_k
             for (int d = 0; d < DT / 4; ++d) {
                 // (rows of a pair of tiles in the order of the state's own: a lane's results of both are neighbours)
                 const int tile = wave * (DT / 4) + d;
-                const int64_t at = (col0 + (tile >> 1) * 32 + (c >> 2) * 8 + (tile & 1) * 4 + (c & 3)) * (int64_t)a.dvp + z;
+                const int64_t at = z0 * (int64_t)a.dkp + (col0 + (tile >> 1) * 32 + (c >> 2) * 8 + (tile & 1) * 4 + (c & 3)) * 32 + g * 8;
                 const f32x4 *sp = reinterpret_cast<const f32x4 *>(S + at), *gp = reinterpret_cast<const f32x4 *>(G + at);
                 sl[d] = sp[0], sh[d] = sp[1], gl[d] = gp[0], gh[d] = gp[1];
             }
