@@ -1219,10 +1219,10 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void delta_gradients_k
                 sl[d] = sp[0], sh[d] = sp[1], gl[d] = gp[0], gh[d] = gp[1];
             }
         };
-        fetch(0);
 #pragma unroll 1
         for (int z0 = 0; z0 < a.dvp; z0 += 32) {
             const int z = z0 + g * 8;
+            fetch(z0);
             bf8 gx[NIN], ux[3], yx[3];
             {
                 const int left = width - z;
@@ -1249,9 +1249,11 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void delta_gradients_k
                 rows_terms<3>(wl * beta, wh * beta, ux);
                 rows_terms<3>(yl * beta, yh * beta, yx);
                 if (z0 > 0 || col0 > 0) __syncthreads();       // the block before has been read
-                put(Sh::kG + wave * NIN, gx);
-                put(Sh::kU + wave * 3, ux);
-                put(Sh::kY + wave * 3, yx);
+                if (col0 == 0) {
+                    put(Sh::kG + wave * NIN, gx);
+                    put(Sh::kU + wave * 3, ux);
+                    put(Sh::kY + wave * 3, yx);
+                }
 #pragma unroll
                 for (int d = 0; d < DT / 4; ++d) {
                     bf8 x[3];
@@ -1264,7 +1266,6 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void delta_gradients_k
                 }
             }
             __syncthreads();
-            if (z0 + 32 < a.dvp) fetch(z0 + 32);
             if (col0 == 0) {
 #pragma unroll
                 for (int i = 0; i < 5; ++i) {
@@ -1341,23 +1342,26 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void delta_gradients_k
         TileReader<T, DP, 4> in;
         in.init();
         const char *ck = lds, *cq = lds + TX::BYTES;
-        double from = gm;
-        asm volatile("" : "+v"(from));       // (the factors are formed anew for each 64 columns: kept, they would cost registers)
-        // the masked, decayed products as operands over tokens: dP for dq, then those for dk
-        auto decay = [&](int row) __attribute__((always_inline)) { return exp_of(row <= mine ? from - sums[row] : sums[row] - from); };
+        // masked and decayed, once: what is not above (below) the diagonal of earlier (later) rows
+        if (col0 == 0) {
+#pragma unroll
+            for (int i = 0; i < 5; ++i)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const bool low = i <= wave;
+                    const int row = 16 * (low ? i : i - 1) + 4 * g + r;
+                    const float f = exp_of(row <= mine ? gm - sums[row & 63] : sums[row & 63] - gm);
+                    dp[i][r] = (low ? row <= mine : row >= mine) ? dp[i][r] * (f * a.scale) : 0.0f;
+                    dc[i][r] = (low ? row < mine : row > mine) ? -dc[i][r] * f : 0.0f;
+                }
+        }
+        const f32x4 zero{0, 0, 0, 0};
+        // as operands over tokens: dP for dq, then those for dk
         {
             bf8 m[2][3];
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
-                f32x4 x[2];
-#pragma unroll
-                for (int half = 0; half < 2; ++half)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const int row = 32 * s + 16 * half + 4 * g + r;
-                        x[half][r] = row <= mine ? dp[2 * s + half][r] * (decay(row) * a.scale) : 0.0f;
-                    }
-                rows_terms<3>(x[0], x[1], m[s]);
+                rows_terms<3>(2 * s <= wave ? dp[2 * s] : zero, 2 * s + 1 <= wave ? dp[2 * s + 1] : zero, m[s]);
             }
 #pragma unroll
             for (int kk = 0; kk < DP / 32; ++kk) {
@@ -1386,14 +1390,11 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void delta_gradients_k
             for (int s = 0; s < 2; ++s) {
                 f32x4 x[2], y[2];
 #pragma unroll
-                for (int half = 0; half < 2; ++half)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const int row = 32 * s + 16 * half + 4 * g + r, tile = 2 * s + half;
-                        const float f = decay(row);
-                        x[half][r] = row >= mine ? dp[tile + 1][r] * (f * a.scale) : 0.0f;
-                        y[half][r] = row < mine ? -dc[tile][r] * f : row > mine ? -dc[tile + 1][r] * f : 0.0f;
-                    }
+                for (int half = 0; half < 2; ++half) {
+                    const int tile = 2 * s + half;
+                    x[half] = tile >= wave ? dp[tile + 1] : zero;
+                    y[half] = (tile <= wave ? dc[tile] : zero) + (tile >= wave ? dc[tile + 1] : zero);
+                }
                 rows_terms<3>(x[0], x[1], m[s]);
                 rows_terms<3>(y[0], y[1], b[s]);
             }
