@@ -1,4 +1,4 @@
-// delta_bf16.hip -- the delta-attention kernels (delta_kernels.hpp) for bf16 storage.
+// delta_bf16.hip -- the gated delta rule kernels (delta_kernels.hpp) for bf16 storage.
 #include "delta_kernels.hpp"
 
 namespace fftconv {

@@ -1,4 +1,4 @@
-// delta_f16.hip -- the delta-attention kernels (delta_kernels.hpp) for f16 storage.
+// delta_f16.hip -- the gated delta rule kernels (delta_kernels.hpp) for f16 storage.
 #include "delta_kernels.hpp"
 
 namespace fftconv {

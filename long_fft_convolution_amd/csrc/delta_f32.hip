@@ -1,4 +1,4 @@
-// delta_f32.hip -- the delta-attention kernels (delta_kernels.hpp) for f32 storage.
+// delta_f32.hip -- the gated delta rule kernels (delta_kernels.hpp) for f32 storage.
 #include "delta_kernels.hpp"
 
 namespace fftconv {

@@ -18,8 +18,8 @@
 // The inverse of I + C diag(beta) and P need no state: a first kernel computes
 // them for all chunks at once (delta_prepare_kernel).  What is left is serial
 // over the chunks and independent over the state's columns: one workgroup of
-// four waves walks one (sequence or segment, head, 64 or 128 columns), each
-// wave with its columns of S in its accumulators for the whole walk.  r, w and
+// four or eight waves walks one (sequence or segment, head, 64 or 128 columns),
+// each wave with its 16 columns of S in its accumulators for the whole walk.  r, w and
 // u never leave the registers: the accumulators of a product over tokens are
 // the next product's operand when its contraction index is met in the order
 // token(slot 8 g + j) = 32 s + 16 (j / 4) + 4 g + j % 4, which is the order the
@@ -37,7 +37,7 @@
 // are taken, which drops 2^-24 of a product.  bf16 terms have fp32's range, so
 // nothing is scaled, fp16 included, and bf16 products are the fastest there
 // are.  Outputs in 16 bits see the state and u in two terms (2^-16) and P in
-// one (bf16: 2^-9, half an output rounding) or two (fp16).  The sums G are
+// one (bf16: 2^-8, as the output's own rounding) or two (fp16).  The sums G are
 // 64 bits: behind a token that clears the state (a logarithm below -104, exp
 // = 0) the differences of the tokens that follow keep all their bits.
 #pragma once
@@ -1132,7 +1132,8 @@ template <typename T, int DXP> struct GradientShape {
     static constexpr int NIN = Terms<T>::kIn;
     static constexpr int kU = 0, kY = 4 * 3, kG = 8 * 3, kS = kG + 4 * NIN, kD = kS + DT * 3, kPieces = kD + DT * 3;
     static constexpr int kTiles = 2 * RowTile<T, DP, 4>::BYTES;
-    static constexpr int kBytes = kPieces * 1024 > kTiles ? kPieces * 1024 : kTiles;
+    static constexpr int kRaw = kPieces * 1024 > kTiles ? kPieces * 1024 : kTiles;      // S and G as they come
+    static constexpr int kBytes = kRaw + 2 * DP * 128;
 };
 template <typename T, int DXP, bool VEC>
 __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void delta_gradients_kernel(const DeltaArgs a) {
@@ -1201,28 +1202,29 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void delta_gradients_k
         f32x4 qa[DT], ka[DT], va[DT];      // S dO, G u, S dv: rows of the states x tokens
 #pragma unroll
         for (int d = 0; d < DT; ++d) qa[d] = ka[d] = va[d] = f32x4{0, 0, 0, 0};
-        // a block's values, on their way while the block before is multiplied
-        f32x4 wl, wh, yl, yh, sl[DT / 4], sh[DT / 4], gl[DT / 4], gh[DT / 4];
+        // A block's values, on their way while the block before is multiplied: rows of the tokens into registers, those of
+        // the states into LDS, 16-byte slot i of a row at i ^ swizzle (neighbouring lanes' rows on different banks).
+        f32x4 wl, wh, yl, yh;
         Raw8<T> go, v;
+        auto swizzle = [](int row) { return (row & 3) | ((row >> 3) & 1) << 2; };
         auto fetch = [&](int z0) __attribute__((always_inline)) {
             const int z = z0 + g * 8, left = width - z;
+#pragma unroll
+            for (int i = 0; i < 2 * DP * 8 / 256; ++i) {
+                const int at = i * 256 + threadIdx.x, row = at / 8 % DP, slot = at % 8 ^ swizzle(row);
+                lds_load16((i < DP * 8 / 256 ? S : G) + z0 * (int64_t)a.dkp + col0 * 32, lds + Sh::kRaw + (i * 256 + wave * 64) * 16,
+                           (uint32_t)(row * 128 + slot * 16));
+            }
             const f32x4 *wp = reinterpret_cast<const f32x4 *>(W + z0 * kC), *yp = reinterpret_cast<const f32x4 *>(Y + z0 * kC);
             wl = wp[0], wh = wp[1], yl = yp[0], yh = yp[1];
             go = load_row8<T, VEC>(gv, left > 0 ? (uint32_t)((mine * a.gt + z) * (int64_t)sizeof(T)) : kSkip, left);
             if (col0 == 0) v = load_row8<T, VEC>(vv, left > 0 ? (uint32_t)((mine * a.vt + z) * (int64_t)sizeof(T)) : kSkip, left);
-#pragma unroll
-            for (int d = 0; d < DT / 4; ++d) {
-                // (rows of a pair of tiles in the order of the state's own: a lane's results of both are neighbours)
-                const int tile = wave * (DT / 4) + d;
-                const int64_t at = z0 * (int64_t)a.dkp + (col0 + (tile >> 1) * 32 + (c >> 2) * 8 + (tile & 1) * 4 + (c & 3)) * 32 + g * 8;
-                const f32x4 *sp = reinterpret_cast<const f32x4 *>(S + at), *gp = reinterpret_cast<const f32x4 *>(G + at);
-                sl[d] = sp[0], sh[d] = sp[1], gl[d] = gp[0], gh[d] = gp[1];
-            }
         };
+        fetch(0);
 #pragma unroll 1
         for (int z0 = 0; z0 < a.dvp; z0 += 32) {
             const int z = z0 + g * 8;
-            fetch(z0);
+            wait_loads_and_barrier<0>();        // (and the block before has been read)
             bf8 gx[NIN], ux[3], yx[3];
             {
                 const int left = width - z;
@@ -1248,7 +1250,6 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void delta_gradients_k
                 in_terms(go, gx);
                 rows_terms<3>(wl * beta, wh * beta, ux);
                 rows_terms<3>(yl * beta, yh * beta, yx);
-                if (z0 > 0 || col0 > 0) __syncthreads();       // the block before has been read
                 if (col0 == 0) {
                     put(Sh::kG + wave * NIN, gx);
                     put(Sh::kU + wave * 3, ux);
@@ -1256,16 +1257,23 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void delta_gradients_k
                 }
 #pragma unroll
                 for (int d = 0; d < DT / 4; ++d) {
+                    // (rows of a pair of tiles in the order of the state's own: a lane's results of both are neighbours)
+                    const int tile = wave * (DT / 4) + d, row = (tile >> 1) * 32 + (c >> 2) * 8 + (tile & 1) * 4 + (c & 3);
+                    const char *raw = lds + Sh::kRaw + row * 128;
+                    const int lo = (2 * g ^ swizzle(row)) * 16, hi = ((2 * g + 1) ^ swizzle(row)) * 16;
+                    const f32x4 sl = *reinterpret_cast<const f32x4 *>(raw + lo), sh = *reinterpret_cast<const f32x4 *>(raw + hi);
+                    const f32x4 gl = *reinterpret_cast<const f32x4 *>(raw + DP * 128 + lo), gh = *reinterpret_cast<const f32x4 *>(raw + DP * 128 + hi);
                     bf8 x[3];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) inner += sl[d][j] * gl[d][j] + sh[d][j] * gh[d][j];
-                    rows_terms<3>(sl[d], sh[d], x);
+                    for (int j = 0; j < 4; ++j) inner += sl[j] * gl[j] + sh[j] * gh[j];
+                    rows_terms<3>(sl, sh, x);
                     put(Sh::kS + (wave * (DT / 4) + d) * 3, x);
-                    rows_terms<3>(gl[d], gh[d], x);
+                    rows_terms<3>(gl, gh, x);
                     put(Sh::kD + (wave * (DT / 4) + d) * 3, x);
                 }
             }
             __syncthreads();
+            if (z0 + 32 < a.dvp) fetch(z0 + 32);
             if (col0 == 0) {
 #pragma unroll
                 for (int i = 0; i < 5; ++i) {
@@ -1281,7 +1289,6 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void delta_gradients_k
                         dp[i] = mma_terms<3>(o, ux, dp[i]);
                         dc[i] = mma_terms<3>(y, ux, dc[i]);
                     }
-                    __builtin_amdgcn_sched_barrier(0);
                 }
             }
 #pragma unroll
@@ -1297,7 +1304,6 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void delta_gradients_k
                     }
                 get(Sh::kD + d * 3, x);
                 ka[d] = mma_terms<3>(x, ux, ka[d]);
-                __builtin_amdgcn_sched_barrier(0);      // (operands of all tiles at once would not fit the registers)
             }
         }
         __syncthreads();

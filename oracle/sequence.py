@@ -1,5 +1,6 @@
-"""Float64 oracle of the sequence operators next to the convolution: decay attention (its recurrence, token by
-token) and the linear product with activation and residual, each with its gradients.
+"""Float64 oracle of the sequence operators next to the convolution: decay attention and the gated delta rule (their
+recurrences, token by token) and the linear product with activation and residual, each with its gradients, and the
+root-mean-square norm.
 
 Plain definitions in numpy, sharing no code with the HIP path:
 
@@ -143,3 +144,10 @@ def delta_bwd(dout, q, k, v, log_decay, beta, scale, state=None, dstate=None):
         G = np.exp(log_decay[t])[:, None, None] * G
     share = H // Hk
     return dq.reshape(N, Hk, share, Dk).sum(2), dk.reshape(N, Hk, share, Dk).sum(2), dv, dg, db, G
+
+
+def rms_norm(x, weight=None, eps=1e-6, residual=None):
+    """(x + residual) / sqrt(mean of its squares + eps) * weight over the last dimension, and x + residual."""
+    t = x if residual is None else x + residual
+    y = t / np.sqrt((t * t).mean(-1, keepdims=True) + eps)
+    return (y if weight is None else y * weight), t
