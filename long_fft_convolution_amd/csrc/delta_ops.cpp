@@ -23,9 +23,16 @@ struct DeltaShape {
 int terms_of(int dt) { return delta_terms(dt == FFTCONV_F32 ? 4 : 2, dt == FFTCONV_F16); }
 size_t record_bytes(const DeltaShape &s) { return (size_t)delta_pieces(terms_of(s.dt)) * 1024; }
 
-// How sequences are cut.  A walk is serial: 64 tokens take microseconds, whatever else the chip does.  With
-// segments the walks' work is three times that of the walk alone (sums and maps, outputs) and the chain adds to it,
-// so sequences are cut where at least four segments of each walk at once.
+// How sequences are cut.  A walk is serial: 64 tokens take microseconds, whatever else the chip does.  With segments the
+// walks' work is three times that of the walk alone (sums and maps, outputs) and the chain adds to it, so sequences are cut
+// where at least four segments of each walk at once, and more than four where the walks of 128 columns fill the chip.
+// bf16, us uncut / cut:
+//     4096 tokens, heads of 128: 16 heads 227 / 127, 32 heads 240 / 184, 50 heads 264 / 260, 64 heads (four) 272 / 319
+//     heads of 128, 2048 tokens: 8 heads 122 / 106, 20 heads 125 / 111; 1024 tokens, 20 heads (two) 74 / 102
+//     4096 tokens, 64 heads of 64 (four): 196 / 148; 16384 tokens, 16 heads of 256: 1689 / 1068
+// Walks of 128 columns read k, q and the records half as often as those of 64 and take longer a chunk, so an uncut call has
+// them where those of 64 columns would be more than one a CU (1024 tokens, 128 columns, us by 64 / by 128: 120 heads 88 /
+// 109, 129 heads 155 / 121, 400 heads 336 / 298), and a cut one always (16384 tokens, 20 heads: 465 / 426).
 struct DeltaCut {
     int64_t seg_chunks, segs;
     bool cut, wide;
@@ -37,7 +44,7 @@ DeltaCut fwd_cut(const DeltaShape &s) {
     c.wide = s.Dk <= 128 && s.Dv > 64 && narrow > kCus;
     const int64_t most = kCus / std::max<int64_t>(1, s.Dv > 64 && s.Dk <= 128 ? wide : narrow);
     const int64_t segments = std::min<int64_t>(most, chunks / 8);
-    if (segments >= 4) {
+    if (segments >= 4 && (most > 4 || s.Dv <= 64 || s.Dk > 128)) {
         c.seg_chunks = ceil_div(chunks, segments);
         c.cut = true;
         c.wide = s.Dk <= 128 && s.Dv > 64;
@@ -258,7 +265,9 @@ struct DeltaBwdLayout {
 };
 DeltaBwdLayout bwd_layout(const DeltaShape &s) {
     DeltaBwdLayout l{};
-    l.wide = s.Dk <= 128 && s.Dv > 64 && 2 * s.B * s.H * ceil_div(s.Dv, 64) > kCus;     // (two walks)
+    // as for an uncut forward call, with two walks (1024 tokens, 128 columns, us by 64 / by 128: 60 heads 219 / 236, 70
+    // heads 320 / 272, 80 heads 338 / 301)
+    l.wide = s.Dk <= 128 && s.Dv > 64 && 2 * s.B * s.H * ceil_div(s.Dv, 64) > kCus;
     l.dkp = padded_width(s.Dk);
     l.dvp = round_up(s.Dv, l.wide ? 128 : 64);
     const size_t items = (size_t)s.places(kDeltaChunk) * s.H;

@@ -7,8 +7,9 @@
 //
 // All of it is fp32; t is rounded once for `sum` and not at all on its way to
 // y, y once for out.  Bound by memory: a row is read once, held in registers
-// by a wave or part of one, or by a workgroup (16384 rows of 2560, bf16, with
-// residual and sum, 8-bit out: 80 us, 3.7 TB/s).
+// by a wave or part of one, or by a workgroup.  16384 rows of 2560, bf16:
+// with residual and sum 66 us, 5.1 TB/s; with an 8-bit out instead 72 us, 4.1
+// TB/s; gradients with dsum 99 us, 3.4 TB/s.
 #include <hip/hip_bf16.h>
 #include <hip/hip_fp16.h>
 #include <hip/hip_runtime.h>
@@ -27,8 +28,15 @@ template <typename T, int V> __device__ __forceinline__ Piece<T, V> load(const T
     __builtin_memcpy(&r, __builtin_assume_aligned(p, V * sizeof(T)), sizeof r);
     return r;
 }
+// Results pass the caches by where they come in whole pieces of 16 bytes (16384 rows of 2560, bf16, sum and out: 67.5
+// us, 77.8 with ordinary stores; 2048 rows of 4096: 14.3 and 15.2).
 template <typename T, int V> __device__ __forceinline__ void store(T *p, const Piece<T, V> &r) {
-    __builtin_memcpy(__builtin_assume_aligned(p, V * sizeof(T)), &r, sizeof r);
+    if constexpr (V * sizeof(T) == 16) {
+        typedef uint32_t words __attribute__((ext_vector_type(4)));
+        __builtin_nontemporal_store(__builtin_bit_cast(words, r), reinterpret_cast<words *>(p));
+    } else {
+        __builtin_memcpy(__builtin_assume_aligned(p, V * sizeof(T)), &r, sizeof r);
+    }
 }
 
 // Sums (or largest bit patterns) over the LANES threads of a row, in all of them.  A row of 256 threads
@@ -393,28 +401,20 @@ template <typename T> __global__ __launch_bounds__(256) void norm_join_kernel(co
     }
 }
 
-template <typename F> hipError_t with_loads(int loads, F &&f) {
-    switch (loads) {
-        case 1: return f(std::integral_constant<int, 1>{});
-        case 2: return f(std::integral_constant<int, 2>{});
-        case 3: return f(std::integral_constant<int, 3>{});
-        case 4: return f(std::integral_constant<int, 4>{});
-        case 5: return f(std::integral_constant<int, 5>{});
-        case 6: return f(std::integral_constant<int, 6>{});
-        case 7: return f(std::integral_constant<int, 7>{});
-        case 8: return f(std::integral_constant<int, 8>{});
-    }
+template <int MOST, typename F> hipError_t with_loads(int loads, F &&f) {
+    if (loads == MOST) return f(std::integral_constant<int, MOST>{});
+    if constexpr (MOST > 1) return with_loads<MOST - 1>(loads, f);
     return hipErrorInvalidValue;
 }
-// lanes: 8, 16 or 32 with one piece each, else 64 or 256
-template <typename F> hipError_t with_lanes(const NormPlan &p, F &&f) {
+// lanes: 8, 16 or 32 with one piece each, 64 with up to WAVE, 256 with up to eight
+template <int WAVE, typename F> hipError_t with_lanes(const NormPlan &p, F &&f) {
     if (p.lanes == 8 && p.loads == 1) return f(std::integral_constant<int, 8>{}, std::integral_constant<int, 1>{});
     if (p.lanes == 16 && p.loads == 1) return f(std::integral_constant<int, 16>{}, std::integral_constant<int, 1>{});
     if (p.lanes == 32 && p.loads == 1) return f(std::integral_constant<int, 32>{}, std::integral_constant<int, 1>{});
     if (p.lanes == 64)
-        return with_loads(p.loads, [&](auto n) { return f(std::integral_constant<int, 64>{}, n); });
+        return with_loads<WAVE>(p.loads, [&](auto n) { return f(std::integral_constant<int, 64>{}, n); });
     if (p.lanes == 256)
-        return with_loads(p.loads, [&](auto n) { return f(std::integral_constant<int, 256>{}, n); });
+        return with_loads<8>(p.loads, [&](auto n) { return f(std::integral_constant<int, 256>{}, n); });
     return hipErrorInvalidValue;
 }
 
@@ -425,7 +425,7 @@ template <typename T, int V> hipError_t fwd_vec(const NormFwd &a, const NormPlan
         else norm_fwd_kernel<T, V, 256, 0, false><<<grid, 256, 0, s>>>(a);
         return hipGetLastError();
     }
-    return with_lanes(p, [&](auto lanes, auto loads) {
+    return with_lanes<kFwdWave>(p, [&](auto lanes, auto loads) {
         if (a.scales) norm_fwd_kernel<T, V, decltype(lanes)::value, decltype(loads)::value, true><<<grid, 256, 0, s>>>(a);
         else norm_fwd_kernel<T, V, decltype(lanes)::value, decltype(loads)::value, false><<<grid, 256, 0, s>>>(a);
         return hipGetLastError();
@@ -439,7 +439,7 @@ template <typename T, int V> hipError_t bwd_vec(const NormBwd &a, const NormPlan
             norm_bwd_wide_kernel<T, V><<<dim3((unsigned)((a.D / V + 255) / 256), (unsigned)p.slabs), 256, 0, s>>>(a);
             e = hipGetLastError();
         } else {
-            e = with_lanes(p, [&](auto lanes, auto loads) {
+            e = with_lanes<kBwdWave>(p, [&](auto lanes, auto loads) {
                 norm_bwd_kernel<T, V, decltype(lanes)::value, decltype(loads)::value><<<(unsigned)p.groups, 256, 0, s>>>(a);
                 return hipGetLastError();
             });

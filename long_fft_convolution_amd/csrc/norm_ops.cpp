@@ -10,9 +10,12 @@ using namespace fftconv;
 namespace {
 
 constexpr int64_t kMaxWidth = int64_t(1) << 20;
-constexpr int64_t kSlabs = 512;         // partial sums of the weight's gradient: two workgroups a CU
-constexpr int64_t kMostGroups = 16384;  // workgroups of a forward call; more rows are met in turn
-constexpr int64_t kFewRows = 2048;      // rows that would leave the chip part empty at one wave each
+// Partial sums of the weight's gradient.  bf16 with dsum: 512 are two workgroups a CU, as many as hold rows of 2560 at
+// once (16384 rows: 61 us, 85 with 256, 74 with 1024); narrow rows leave room for four (65536 rows of 768: 74 us, 92 with
+// 512 and with 2048).
+int64_t slabs_of(int64_t rows, int64_t D) { return std::min<int64_t>(rows, D <= 1024 ? 1024 : 512); }
+// Workgroups of a forward call; more rows are met in turn (65536 rows of 768: 60 us, 64 with 8192, 81 with 1024).
+constexpr int64_t kMostGroups = 16384;
 
 struct NormShape {
     int64_t M, G, D;
@@ -45,17 +48,21 @@ bool same_place(const View &a, const View &b) {
     return true;
 }
 
-// A part of a wave a row where it fits one piece a lane, a wave with up to eight pieces a lane, a workgroup
-// with up to eight, else the row is read again.  Few rows of more than a wave's single piece are spread over
-// whole workgroups.
-NormPlan plan_of(int64_t rows, int64_t D, int vec) {
+// A part of a wave holds a row where one piece a lane does; else a wave where the rows are many and take at most
+// `wave` pieces a lane; else a workgroup with up to eight pieces a lane; else the row is read again.  bf16, us by waves /
+// by workgroups:
+//     forward, 768 wide: 64 rows 3.4 / 2.8, 2048 rows 7.0 / 6.1, 4096 rows 8.9 / 10.1, 16384 rows 24.8 / 30.4
+//     forward, 16384 rows: 1536 wide 45.4 / 39.7, 2560 wide 77.5 / 69.3, 4096 wide 121 / 101
+//     gradients, 2560 wide: 64 rows 11.9 / 8.2, 512 rows 17.3 / 21.3, 16384 rows 100 / 163
+//     gradients, 4096 wide: 512 rows 25.3 / 23.0, 16384 rows 269 / 183
+NormPlan plan_of(int64_t rows, int64_t D, int vec, int wave, int64_t few) {
     NormPlan p{};
     p.vec = vec;
     const int64_t pieces = ceil_div(D, vec);
     if (pieces <= 32) {
         p.lanes = pieces <= 8 ? 8 : pieces <= 16 ? 16 : 32, p.loads = 1;
     } else {
-        p.lanes = pieces <= 64 || (pieces <= 512 && rows > kFewRows) ? 64 : 256;
+        p.lanes = pieces <= 64 || (pieces <= 64 * wave && rows > few) ? 64 : 256;
         p.loads = pieces <= 2048 ? (int)ceil_div(pieces, p.lanes) : 0;
     }
     p.groups = ceil_div(rows, 256 / p.lanes);
@@ -99,14 +106,14 @@ fftconv_status_t fftconv_norm_fwd(const void *x, const void *residual, const voi
     } else {
         vec = vec && chunk_vec(vo);
     }
-    NormPlan p = plan_of(M * G, D, vec ? v : 1);
+    NormPlan p = plan_of(M * G, D, vec ? v : 1, kFwdWave, 2048);
     p.groups = std::min(p.groups, kMostGroups);
     return hip_status("norm", launch_norm_fwd(s.dt, a, p, stream));
 }
 
 size_t fftconv_norm_bwd_workspace_bytes(int64_t rows, int64_t D) {
     if (rows < 1 || rows >= (int64_t(1) << 31) || D < 1 || D > kMaxWidth) return 0;
-    return align_up((size_t)std::min(rows, kSlabs) * D * 4, 256) + (size_t)rows * 8;
+    return align_up((size_t)slabs_of(rows, D) * D * 4, 256) + (size_t)rows * 8;
 }
 
 fftconv_status_t fftconv_norm_bwd(const void *dout, const void *x, const void *weight, const void *dsum, void *dx,
@@ -138,10 +145,10 @@ fftconv_status_t fftconv_norm_bwd(const void *dout, const void *x, const void *w
         a.gs[i] = vg.stride[i], a.xs[i] = vx.stride[i], a.us[i] = vu.stride[i], a.ds[i] = vd.stride[i];
     a.rows = (uint32_t)rows, a.G = (uint32_t)G, a.D = (int)D, a.eps = eps;
     const bool vec = chunk_vec(vg) && chunk_vec(vx) && (!weight || chunk_vec(vw)) && (!dsum || chunk_vec(vu)) && (!dx || chunk_vec(vd));
-    NormPlan p = plan_of(rows, D, vec ? (int)(16 / e) : 1);
-    p.slabs = p.loads ? std::min(p.groups, kSlabs) : std::min(rows, kSlabs);
+    NormPlan p = plan_of(rows, D, vec ? (int)(16 / e) : 1, kBwdWave, 256);
+    p.slabs = p.loads ? std::min(p.groups, slabs_of(rows, D)) : slabs_of(rows, D);
     p.groups = p.loads ? p.slabs : std::min(rows, kMostGroups);
     a.part = dweight ? static_cast<float *>(workspace) : nullptr;
-    a.stats = need ? reinterpret_cast<float *>(static_cast<char *>(workspace) + align_up((size_t)std::min(rows, kSlabs) * D * 4, 256)) : nullptr;
+    a.stats = need ? reinterpret_cast<float *>(static_cast<char *>(workspace) + align_up((size_t)slabs_of(rows, D) * D * 4, 256)) : nullptr;
     return hip_status("norm backward", launch_norm_bwd(s.dt, a, p, dweight, stream));
 }

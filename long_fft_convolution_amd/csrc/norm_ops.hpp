@@ -31,6 +31,7 @@ struct NormBwd {
 
 // How a call's rows are met: `lanes` of a workgroup's 256 threads hold a row, each `loads` pieces of
 // `vec` values; loads = 0: the row is read again instead of held.
+constexpr int kFwdWave = 2, kBwdWave = 5;      // the most pieces a lane of a wave that holds a row by itself
 struct NormPlan {
     int vec, lanes, loads;
     int64_t groups;      // workgroups
