@@ -399,7 +399,8 @@ fftconv_status_t fftconv_decay_bwd(const void *dout, const void *q, const void *
  * Heads: v, out, log_decay, beta and the states have H heads, q and k Hk, H a multiple of Hk; head h uses q/k
  * head h / (H / Hk).  Widths 1 <= Dk, Dv <= 256.
  * Layouts: q, k (B, N, Hk, Dk), v, out (B, N, H, Dv); `strides` (batch, token, head), alignment, separation of
- * results, packed sequences (cu_seqlens) and state pools (state_slots) as for decay attention.
+ * results, packed sequences (cu_seqlens) and state pools (state_slots) as for decay attention; a call names a slot
+ * at most once (of a slot that two sequences name, the state and those sequences' outputs are undefined).
  * Precision: operands are exact sums of bf16 terms and products are accumulated in fp32; the states, and
  * everything a state depends on, keep fp32 precision.  Outputs in 16 bits see the state to 2^-16 and the products
  * q k^T to one rounding (bf16) or 2^-16 (fp16).

@@ -235,9 +235,10 @@ __device__ __forceinline__ void invert_unit_lower(float *M) {
     }
 }
 
-// One wave a (chunk, head): record of the chunk.  grid: chunks * H / 4.  Bound by latency: products, the inverse's
-// 16 serial steps and LDS round trips; eight waves a CU overlap them.
-// BACK: the backward call's record.
+// One wave a (chunk, head): record of the chunk.  grid: chunks * H / 4.  Bound by latency (products, the inverse's 16
+// serial steps, LDS round trips; eight waves a CU overlap them) and, for long calls, by the records written.  20 heads of
+// 128, bf16: 4 x 4096 tokens 86 us, 131072 tokens 580 us (2.5 GB, 4.3 TB/s).
+// BACK: the backward call's record (4 x 4096 tokens: 130 us).
 template <typename T, int DXP, bool VEC, bool BACK> __global__ __launch_bounds__(256) void delta_prepare_kernel(const DeltaArgs a) {
     constexpr int KX = DXP / 32, NP = Terms<T>::kP;
     __shared__ __attribute__((aligned(16))) float matrix[4][kC * kLd];
@@ -646,6 +647,10 @@ enum DeltaMode : int { kDeltaSums = 0, kDeltaOut = 1, kDeltaKeep = 2 };
 constexpr int walk_waves(int dxp, int waves, int mode, int bytes) { return mode == kDeltaSums && bytes == 2 && dxp <= 128 ? waves / 2 : 1; }
 
 // Eight waves a workgroup, two a SIMD (one splits fp32 values while the other multiplies), for 128 columns; four for 64.
+// Bound by the serial chunk: its products, splits and LDS reads each take two to three microseconds of it, in turns.
+// 20 heads of 128, bf16: 4 x 4096 tokens 230 us (64 columns, 3.6 us a chunk), one sequence of 6001 among shorter ones 432
+// us (128 columns, 4.6 us a chunk), 131072 tokens in 12 segments: sums and maps 1420 us, outputs 1060 us.  fp16, fp32:
+// 433 and 728 us at 4 x 4096.  32 columns a wave took 1032 us for those outputs, and 2213 us for the sums.
 template <typename T, int DXP, int WAVES, int MODE, bool VEC> struct WalkShape {
     static constexpr bool OUT = MODE == kDeltaOut;
     static constexpr int DZT = WAVES * 16;
@@ -1107,7 +1112,8 @@ __device__ __forceinline__ void delta_walk_back(const DeltaArgs &a, char *lds, u
 }
 #endif
 
-// Both walks of the backward call: even items forwards, odd ones from the end.
+// Both walks of the backward call: even items forwards, odd ones from the end.  Bound as the forward walks, the reverse one
+// with twice their products: 4 x 4096 tokens x 20 heads of 128, bf16 560 us (8.7 us a chunk), fp32 1670.
 template <typename T, int DXP, int WAVES, bool VEC>
 __global__ __launch_bounds__(walk_bound(DXP, WAVES, sizeof(T))) void delta_back_walks_kernel(const DeltaArgs a, int tiles) {
 #ifdef __HIP_DEVICE_COMPILE__
@@ -1126,7 +1132,8 @@ __global__ __launch_bounds__(walk_bound(DXP, WAVES, sizeof(T))) void delta_back_
 // values' columns (u, dv, dO, S, G: rows of 32 neighbouring values) are split once, each by one wave, and met by all
 // through LDS, 32 columns at a time; k and q, met by columns, follow in the same place.
 //
-// Bound by the matrix units and the splitting: 4 x 4096 tokens x 20 heads of 128, bf16: DELTA_GRADIENTS_FIGURE.
+// Bound by waits: half of the time at barriers and for LDS, the rest the matrix units and the splitting.  4 x 4096 tokens x
+// 20 heads of 128, bf16: 565 us (612 with S and G loaded into registers), fp32 895.
 template <typename T, int DXP> struct GradientShape {
     static constexpr int DP = 64, DT = DP / 16;      // columns of q and k at once, their tiles
     static constexpr int NIN = Terms<T>::kIn;
@@ -1457,7 +1464,8 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void delta_gradients_k
 
 // State before each segment from the segments' own sums and maps: S <- map S + sum, one workgroup a (sequence, head,
 // 16 columns), grid (B, H, tiles); a wave has a quarter of the rows of the map, of which those of the next segment are on
-// their way while this one's are in use, and the state goes round through LDS.  Bound by latency: the segments are serial.
+// their way while this one's are in use, and the state goes round through LDS.  Bound by latency: the segments are serial (12
+// segments of 20 heads of 128: 47 us).
 template <int DXP> static __global__ __launch_bounds__(256, 1) void delta_chain_kernel(const DeltaArgs a) {
     constexpr int KX = DXP / 32, R = DXP / 64, LD = DXP + 4;
     __shared__ __attribute__((aligned(16))) float state[2][16 * LD];
@@ -1538,7 +1546,8 @@ template <int DXP> static __global__ __launch_bounds__(256, 1) void delta_chain_
 // The single-token form.  One workgroup a (sequence, head, LANES * VEC columns), LANES lanes along a row of the state,
 // 256 / LANES groups of rows; the rows stay in registers between the products with k and q (which are taken of the
 // state before the token: out = scale (a S^T q + (q . k) u)) and the update.  Bound by the state, which is read and
-// written once.
+// written once: 256 sequences x 20 heads of 128 140 us, 4.8 TB/s.  For few sequences, workgroups of a fourth of the
+// columns are no faster (20 heads: 5.0 and 5.1 us; 340 heads: 12.9 and 12.5).
 template <typename T, int VEC, int LANES, int ROWS>
 __global__ __launch_bounds__(256) void delta_step_kernel(const DeltaStep a) {
     constexpr int RG = 256 / LANES, W = LANES * VEC;
@@ -1674,7 +1683,6 @@ template <typename T, int VEC, int LANES> static hipError_t delta_step_rows(cons
 }
 template <typename T> static hipError_t delta_step_typed(const DeltaStep &a, bool vec, hipStream_t s) {
     if (!vec) return delta_step_rows<T, 1, 32>(a, s);
-    if (a.B * a.H * ((a.Dv + 127) / 128) < 352) return delta_step_rows<T, 4, 8>(a, s);
     return delta_step_rows<T, 4, 32>(a, s);
 }
 

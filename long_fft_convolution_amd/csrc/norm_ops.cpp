@@ -11,9 +11,10 @@ namespace {
 
 constexpr int64_t kMaxWidth = int64_t(1) << 20;
 // Partial sums of the weight's gradient.  bf16 with dsum: 512 are two workgroups a CU, as many as hold rows of 2560 at
-// once (16384 rows: 61 us, 85 with 256, 74 with 1024); narrow rows leave room for four (65536 rows of 768: 74 us, 92 with
-// 512 and with 2048).
-int64_t slabs_of(int64_t rows, int64_t D) { return std::min<int64_t>(rows, D <= 1024 ? 1024 : 512); }
+// once (16384 rows: 61 us, 85 with 256, 74 with 1024); narrower ones leave room for four (65536 rows of 768: 74 us, 92
+// with 512 and with 2048).  Of the narrowest, a workgroup holds sixteen rows and more at once, and 512 do (131072 rows of
+// 128: 36 us, 37 with 1024).
+int64_t slabs_of(int64_t rows, int64_t D) { return std::min<int64_t>(rows, D > 128 && D <= 1024 ? 1024 : 512); }
 // Workgroups of a forward call; more rows are met in turn (65536 rows of 768: 60 us, 64 with 8192, 81 with 1024).
 constexpr int64_t kMostGroups = 16384;
 
