@@ -183,8 +183,8 @@ constexpr int kLd = kC + 4;      // row stride of a 64 x 64 matrix in LDS: 16-by
 
 // M (strictly lower, 64 x 64 in LDS) <- (I + M)^-1, lower blocks of 16; the blocks above the diagonal are left.
 // Diagonal blocks by forward substitution, a column a lane; the others, row of blocks by row, as
-// -T_ii sum_k M_ik T_kj on the fp32 matrix cores.
-__device__ __forceinline__ void invert_unit_lower(float *M) {
+// -T_ii sum_k M_ik T_kj on the fp32 matrix cores.  Rows from n on are those of the unit matrix.
+__device__ __forceinline__ void invert_unit_lower(float *M, int n) {
     const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
     {
         const float *block = M + g * 16 * kLd + g * 16;
@@ -209,6 +209,7 @@ __device__ __forceinline__ void invert_unit_lower(float *M) {
     auto row4 = [&](int i, int k) { return *reinterpret_cast<const f32x4 *>(M + (16 * i + c) * kLd + 16 * k + 4 * g); };
 #pragma unroll
     for (int i = 1; i < 4; ++i) {
+        if (16 * i >= n) return;
         f32x4 x[3];
 #pragma unroll
         for (int j = 0; j < i; ++j) {
@@ -237,7 +238,8 @@ __device__ __forceinline__ void invert_unit_lower(float *M) {
 
 // One wave a (chunk, head): record of the chunk.  grid: chunks * H / 4.  Bound by latency (products, the inverse's 16
 // serial steps, LDS round trips; eight waves a CU overlap them) and, for long calls, by the records written.  20 heads of
-// 128, bf16: 4 x 4096 tokens 86 us, 131072 tokens 580 us (2.5 GB, 4.3 TB/s).
+// 128, bf16: 4 x 4096 tokens 87 us, 131072 tokens 580 us (2.5 GB, 4.3 TB/s).  A chunk that ends early has fewer blocks to
+// invert (17 tokens: 14.8 us, 16.6 with all of them).
 // BACK: the backward call's record (4 x 4096 tokens: 130 us).
 template <typename T, int DXP, bool VEC, bool BACK> __global__ __launch_bounds__(256) void delta_prepare_kernel(const DeltaArgs a) {
     constexpr int KX = DXP / 32, NP = Terms<T>::kP;
@@ -325,7 +327,7 @@ template <typename T, int DXP, bool VEC, bool BACK> __global__ __launch_bounds__
                     M[row * kLd + col] = col < row ? kk[at][r] * exp_of(G[row] - G[col]) * beta[by_row ? row : col] : 0.0f;
                 }
         wave_sync();
-        invert_unit_lower(M);
+        invert_unit_lower(M, n);
     };
     put(false);
     bf8 *out = reinterpret_cast<bf8 *>(rec);
