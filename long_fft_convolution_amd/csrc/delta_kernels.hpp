@@ -1651,7 +1651,8 @@ template <typename T> static hipError_t delta_bwd_typed(const DeltaArgs &a, hipS
 }
 template <typename T, int DXP, int WAVES, int MODE, bool VEC> static hipError_t delta_walk_launch(const DeltaArgs &a, hipStream_t s) {
     constexpr int DZT = WAVES * 16;
-    const int ztiles = (a.Dv + DZT - 1) / DZT, tiles = ztiles + (MODE == kDeltaSums ? (a.Dk + DZT - 1) / DZT : 0);
+    // (the chain reads all DXP columns of a map, zeros behind Dk among them)
+    const int ztiles = (a.Dv + DZT - 1) / DZT, tiles = ztiles + (MODE == kDeltaSums ? (DXP + DZT - 1) / DZT : 0);
     const int64_t items = a.segs * a.H * tiles, round = 8 * (int64_t)delta_run(tiles, a.group);
     delta_walk_kernel<T, DXP, WAVES, MODE, VEC><<<(unsigned)((items + round - 1) / round * round), WAVES * 64, 0, s>>>(a, ztiles, tiles);
     return hipGetLastError();
