@@ -727,13 +727,16 @@ __device__ __forceinline__ void delta_walk(const DeltaArgs &a, char *lds, uint32
     const int64_t nst = (int64_t)a.Dk * a.Dv;
     {
         const float *p = nullptr;
-        if (MODE != kDeltaSums && a.seg_state && tk.unit > 0) {
+        // Of a sequence of several segments the chain has written the first one's state, too: state1 may be state0's own
+        // memory, and nothing orders the last segment's workgroup behind the first one's.
+        const bool joined = MODE != kDeltaSums && a.seg_state && chunks > a.seg_chunks;
+        if (joined) {
             S.load(a.seg_state + (place * a.H + h) * (int64_t)DXP * a.sum_ld, DXP, a.sum_ld, column);
         } else if (MODE != kDeltaSums && a.state0) {
             const int64_t slot = state_slot(a.slots, a.n_slots, tk.seq);
             if (slot >= 0) p = a.state0 + (slot * a.H + h) * nst;
         }
-        if (MODE == kDeltaSums || !a.seg_state || tk.unit == 0) S.load(p, a.Dk, cols, column);
+        if (!joined) S.load(p, a.Dk, cols, column);
         S.settle();
         if (map) S.each([&](int row, float) __attribute__((always_inline)) { return row == column ? 1.0f : 0.0f; });
     }
@@ -1464,10 +1467,10 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void delta_gradients_k
 #endif
 }
 
-// State before each segment from the segments' own sums and maps: S <- map S + sum, one workgroup a (sequence, head,
-// 16 columns), grid (B, H, tiles); a wave has a quarter of the rows of the map, of which those of the next segment are on
-// their way while this one's are in use, and the state goes round through LDS.  Bound by latency: the segments are serial (12
-// segments of 20 heads of 128: 47 us).
+// State before each segment from the segments' own sums and maps: S <- map S + sum, the first one's as the caller gave it.
+// One workgroup a (sequence, head, 16 columns), grid (B, H, tiles); a wave has a quarter of the rows of the map, of which
+// those of the next segment are on their way while this one's are in use, and the state goes round through LDS.  Bound by
+// latency: the segments are serial (12 segments of 20 heads of 128: 47 us).
 template <int DXP> static __global__ __launch_bounds__(256, 1) void delta_chain_kernel(const DeltaArgs a) {
     constexpr int KX = DXP / 32, R = DXP / 64, LD = DXP + 4;
     __shared__ __attribute__((aligned(16))) float state[2][16 * LD];
@@ -1486,10 +1489,13 @@ template <int DXP> static __global__ __launch_bounds__(256, 1) void delta_chain_
             if (slot >= 0) p = a.state0 + (slot * a.H + h) * (int64_t)a.Dk * a.Dv;
         }
         const auto view = wide_view(p);
+        float *out = a.seg_state + first * sums;
         for (int i = threadIdx.x; i < DXP * 16; i += 256) {
             const int row = i / 16, col = i % 16;
             const bool there = (p != nullptr) & (row < a.Dk) & (col0 + col < a.Dv);
-            state[0][col * LD + row] = view_load<float>(view, there ? (uint32_t)(row * a.Dv + col0 + col) * 4u : kSkip);
+            const float x = view_load<float>(view, there ? (uint32_t)(row * a.Dv + col0 + col) * 4u : kSkip);
+            state[0][col * LD + row] = x;
+            out[row * (int64_t)a.sum_ld + col0 + col] = x;
         }
     }
     f32x4 map[R][KX][2], sum[R];

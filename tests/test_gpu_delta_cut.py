@@ -1,9 +1,9 @@
 """Prompts of the gated delta rule that are cut into segments: key widths that leave columns of a segment's map without a
-key, whatever the workspace holds.
+key, whatever the workspace holds, and states of a pool that is updated in place.
 
 Tolerances, relative L2 against the float64 oracle on the rounded inputs: 16-bit results 1.5 half units of their type (2^-11,
 2^-8: the result's rounding and, below it, those of its operands), fp32 results 5e-6 (products of exact terms accumulated in
-fp32 over at most 40 chunks of 64 tokens)."""
+fp32 over at most 80 chunks of 64 tokens, whose errors the decay forgets)."""
 import numpy as np
 import pytest
 import torch
@@ -59,3 +59,34 @@ def test_widths_between_the_padded_ones(Dk, Dv, dtype):
     want, wS = seq.delta_fwd(*(_f64(t[0]) for t in ins), 0.25, _f64(S0[0]))
     _close(out[0], want, TOL[dtype], "out")
     _close(S[0], wS, FP32, "state")
+
+
+@pytest.mark.parametrize("lens", [(2624,) * 9, (2600, 900, 5000, 64, 1, 3333, 2624, 4095, 5002), (0, 9000, 513, 2049, 3000, 2600, 2600, 2600, 1)])
+@pytest.mark.parametrize("H,D", [(4, 128), (7, 64)])
+def test_a_pool_in_place_as_one_beside(lens, H, D):
+    """More segments than CUs, other work on the chip: where the last segment of a sequence ends before the first one starts,
+    the first one still starts from the state that the caller gave."""
+    print(f"[case] in place {lens} H={H} D={D}", flush=True)
+    B, T = len(lens), sum(lens)
+    cu = torch.tensor([0, *np.cumsum(lens)], dtype=torch.int32).cuda()
+    ins = _inputs((T,), H, H, D, D, "bf16", T)
+    pool = torch.randn((B + 2, H, D, D), generator=torch.Generator().manual_seed(3)).cuda()
+    slots = torch.randperm(B + 2, generator=torch.Generator().manual_seed(4))[:B].to(torch.int32)
+    slots[6] = -1
+    where, ws = slots.cuda(), _garbage(fc.fftconv_delta_fwd_workspace_bytes(B, T, H, H, D, D, torch.bfloat16))
+    want, after = torch.empty_like(ins[2]), pool.clone()
+    fc.fftconv_delta_fwd(*ins, want, 0.25, pool, after, where, cu, ws)
+    out, inplace = torch.empty_like(want), [pool.clone() for _ in range(4)]
+    work, other = torch.randn((2048, 2048), device="cuda"), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(other):
+        for _ in range(8):
+            work = torch.nn.functional.normalize(work @ work)
+    for p in inplace:
+        fc.fftconv_delta_fwd(*ins, out, 0.25, p, p, where, cu, ws)
+        assert torch.equal(out, want) and torch.equal(p, after)
+    for b in (0, 2):      # (cut in several)
+        x, y = int(cu[b]), int(cu[b + 1])
+        ref, wS = seq.delta_fwd(*(_f64(t[x:y]) for t in ins), 0.25, _f64(pool[int(slots[b])]))
+        _close(want[x:y], ref, TOL["bf16"], f"out[{b}]")
+        _close(after[int(slots[b])], wS, FP32, f"state[{b}]")
