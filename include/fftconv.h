@@ -402,8 +402,8 @@ fftconv_status_t fftconv_decay_bwd(const void *dout, const void *q, const void *
  * results, packed sequences (cu_seqlens) and state pools (state_slots) as for decay attention; a call names a slot
  * at most once (of a slot that two sequences name, the state and those sequences' outputs are undefined).
  * Precision: operands are exact sums of bf16 terms and products are accumulated in fp32; the states, and
- * everything a state depends on, keep fp32 precision.  Outputs in 16 bits see the state to 2^-16 and the products
- * q k^T to one rounding (bf16) or 2^-16 (fp16).
+ * everything a state depends on, keep fp32 precision.  Outputs in 16 bits see the state, u and the products q k^T in
+ * two bf16 terms each (2^-15 of a value).
  * A NaN or infinity in a token may reach every output of its sequence and head from its block of 64 tokens on,
  * never another sequence.
  * Refused with FFTCONV_ERR_UNSUPPORTED: token strides of 16 MiB or more, and calls whose (64 tokens, head) pairs

@@ -36,8 +36,8 @@
 // value: three, fp16: two, bf16: itself) and the products of terms i + j < 3
 // are taken, which drops 2^-24 of a product.  bf16 terms have fp32's range, so
 // nothing is scaled, fp16 included, and bf16 products are the fastest there
-// are.  Outputs in 16 bits see the state and u in two terms (2^-16) and P in
-// one (bf16: 2^-8, as the output's own rounding) or two (fp16).  The sums G are
+// are.  Outputs in 16 bits see the state, u and P in two terms each (2^-15 of a
+// value, beside the result's own rounding of 2^-8 or 2^-11).  The sums G are
 // 64 bits: behind a token that clears the state (a logarithm below -104, exp
 // = 0) the differences of the tokens that follow keep all their bits.
 #pragma once
@@ -102,11 +102,11 @@ __device__ __forceinline__ void make_scalar(Tokens &t) {
 }
 
 // ---- operands ---------------------------------------------------------------
-// exact bf16 terms of a storage value, and of the masked products
+// bf16 terms of a storage value (exact), and of what the outputs see: the state, u and the masked products
 template <typename T> struct Terms;
-template <> struct Terms<__bf16> { static constexpr int kIn = 1, kOut = 2, kP = delta_terms(2, false); };
-template <> struct Terms<_Float16> { static constexpr int kIn = 2, kOut = 2, kP = delta_terms(2, true); };
-template <> struct Terms<float> { static constexpr int kIn = 3, kOut = 3, kP = delta_terms(4, false); };
+template <> struct Terms<__bf16> { static constexpr int kIn = 1, kOut = delta_terms(2); };
+template <> struct Terms<_Float16> { static constexpr int kIn = 2, kOut = delta_terms(2); };
+template <> struct Terms<float> { static constexpr int kIn = 3, kOut = delta_terms(4); };
 
 // Eight fp32 values as N bf16 terms.  bf16 is the upper half of fp32: cutting it off leaves an exact rest, so three
 // terms of 8 bits hold all 24; the last of two is rounded.  (The rests as dot products of a pair with (-1, 0) and (0, -1)
@@ -242,7 +242,7 @@ __device__ __forceinline__ void invert_unit_lower(float *M, int n) {
 // invert (17 tokens: 14.8 us, 16.6 with all of them).
 // BACK: the backward call's record (4 x 4096 tokens: 130 us).
 template <typename T, int DXP, bool VEC, bool BACK> __global__ __launch_bounds__(256) void delta_prepare_kernel(const DeltaArgs a) {
-    constexpr int KX = DXP / 32, NP = Terms<T>::kP;
+    constexpr int KX = DXP / 32, NP = Terms<T>::kOut;
     __shared__ __attribute__((aligned(16))) float matrix[4][kC * kLd];
     __shared__ double sums[4][kC];
     __shared__ float betas[4][kC];
@@ -660,7 +660,7 @@ template <typename T, int DXP, int WAVES, int MODE, bool VEC> struct WalkShape {
     using TZ = RowTile<T, DZT, WAVES>;
     static constexpr int kQ = TX::BYTES, kV = (OUT ? 2 : 1) * TX::BYTES, kRec = kV + TZ::BYTES;
     // where LDS has no room (fp32 rows wider than 128) the record, or its masked products, are read from memory
-    static constexpr int kAll = OUT ? delta_pieces(Terms<T>::kP) : 20, kFew = kDeltaInverse + kDeltaVectors + 1;
+    static constexpr int kAll = OUT ? delta_pieces(Terms<T>::kOut) : 20, kFew = kDeltaInverse + kDeltaVectors + 1;
     static constexpr int kPieces = kRec + kAll * 1024 <= kLdsBytes ? kAll : kRec + kFew * 1024 <= kLdsBytes ? kFew : 0;
     static constexpr bool kRecord = kPieces > 0, kProducts = kPieces >= kAll;
     static constexpr int kBytes = kRec + kPieces * 1024;
@@ -680,7 +680,7 @@ template <typename T, int DXP, int WAVES, int MODE, bool VEC>
 __device__ __forceinline__ void delta_walk(const DeltaArgs &a, char *lds, uint32_t w, int ztiles, int tiles) {
     using W = WalkShape<T, DXP, WAVES, MODE, VEC>;
     constexpr bool OUT = W::OUT;
-    constexpr int KX = DXP / 32, DZT = W::DZT, NIN = Terms<T>::kIn, NOUT = Terms<T>::kOut, NP = Terms<T>::kP;
+    constexpr int KX = DXP / 32, DZT = W::DZT, NIN = Terms<T>::kIn, NOUT = Terms<T>::kOut;
     const int tile = w % tiles;
     w /= tiles;
     const int h = w % a.H;
@@ -874,13 +874,12 @@ __device__ __forceinline__ void delta_walk(const DeltaArgs &a, char *lds, uint32
 #pragma unroll
             for (int s = 0; s < 2; ++s)
 #pragma unroll
-                for (int i = 0; i < NP; ++i)
+                for (int i = 0; i < NOUT; ++i)
 #pragma unroll
-                    for (int j = 0; j < NOUT; ++j)
-                        if (i + j < NOUT)
+                    for (int j = 0; i + j < NOUT; ++j)
 #pragma unroll
-                            for (int r = 2 * s; r < 4; ++r)
-                                o[r] = Mma<__bf16>::mma(us[s][j], prod[(((r + 1) * (r + 1) / 4 + s) * NP + i) * 64], o[r]);
+                        for (int r = 2 * s; r < 4; ++r)
+                            o[r] = Mma<__bf16>::mma(us[s][j], prod[(((r + 1) * (r + 1) / 4 + s) * NOUT + i) * 64], o[r]);
             const auto view = wide_view(out0 + t0 * a.ot);
 #pragma unroll
             for (int r = 0; r < 4; ++r) {

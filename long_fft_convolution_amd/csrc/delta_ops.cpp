@@ -20,8 +20,7 @@ struct DeltaShape {
     int64_t places(int64_t length) const { return packed ? N / length + B : B * std::max<int64_t>(1, ceil_div(N, length)); }
 };
 
-int terms_of(int dt) { return delta_terms(dt == FFTCONV_F32 ? 4 : 2, dt == FFTCONV_F16); }
-size_t record_bytes(const DeltaShape &s) { return (size_t)delta_pieces(terms_of(s.dt)) * 1024; }
+size_t record_bytes(const DeltaShape &s) { return (size_t)delta_pieces(delta_terms((int)elem_bytes(s.dt))) * 1024; }
 
 // How sequences are cut.  A walk is serial: 64 tokens take microseconds, whatever else the chip does.  With segments the
 // walks' work is three times that of the walk alone (sums and maps, outputs) and the chain adds to it, so sequences are cut

@@ -16,8 +16,9 @@ constexpr int kDeltaChunk = 64;      // tokens of a chunk
 // terms; padded to a multiple of four.
 constexpr int kDeltaInverse = 18, kDeltaVectors = 1;
 constexpr int delta_pieces(int terms) { return (kDeltaInverse + kDeltaVectors + 6 * terms + 3) / 4 * 4; }
-// terms of the masked products: bf16 results see them rounded once, like the state; fp16's need two, fp32's three
-constexpr int delta_terms(int elem_bytes, bool narrow) { return elem_bytes == 4 ? 3 : narrow ? 2 : 1; }
+// terms of the masked products, as of all else that outputs see: two for 16 bits (one would be a rounding as large as a
+// bf16 result's own), three for fp32
+constexpr int delta_terms(int elem_bytes) { return elem_bytes == 4 ? 3 : 2; }
 // The backward call's record: the inverse of I + C diag(beta), the vectors, then, as operands over tokens from the
 // other side, the inverse of I + C^T diag(beta) in three terms and P^T in fp32 (two halves of an operand).
 constexpr int kDeltaBackProducts = 12;
