@@ -393,8 +393,8 @@ fftconv_status_t fftconv_decay_bwd(const void *dout, const void *q, const void *
  *
  *     u_t = beta_t (v_t - a_t S_{t-1}^T k_t),    S_t = a_t S_{t-1} + k_t u_t^T,    out_t = scale * S_t^T q_t
  *
- * log_decay and beta are fp32 (B, N, H), dense: logarithms <= 0 (-inf: the state is cleared before the token),
- * and any weight.  The rule is stable while beta |k|^2 <= 2: keys are meant to be normed (fftconv_norm_fwd over
+ * log_decay and beta are fp32 (B, N, H), dense: logarithms <= 0 (below -104, -inf among them: the state is cleared
+ * before the token), and any weight.  The rule is stable while beta |k|^2 <= 2: keys are meant to be normed (fftconv_norm_fwd over
  * the heads' rows, weight 1 / sqrt(Dk)).
  * Heads: v, out, log_decay, beta and the states have H heads, q and k Hk, H a multiple of Hk; head h uses q/k
  * head h / (H / Hk).  Widths 1 <= Dk, Dv <= 256.
@@ -405,7 +405,7 @@ fftconv_status_t fftconv_decay_bwd(const void *dout, const void *q, const void *
  * everything a state depends on, keep fp32 precision.  Outputs in 16 bits see the state, u and the products q k^T in
  * two bf16 terms each (2^-15 of a value).
  * A NaN or infinity in a token may reach every output of its sequence and head from its block of 64 tokens on,
- * never another sequence.
+ * never another sequence; one in a state that is passed in may reach all of them, unless the first token clears it.
  * Refused with FFTCONV_ERR_UNSUPPORTED: token strides of 16 MiB or more, and calls whose (64 tokens, head) pairs
  * pass 2^24 or whose (sequence, head) pairs pass 2^20. */
 

@@ -172,6 +172,17 @@ template <typename T, bool VEC> __device__ __forceinline__ Raw8<T> load_row8(__a
     return r;
 }
 
+// A token whose logarithm is below this clears the state before it: its decay is 0 in fp32.
+constexpr float kClears = -104.0f;
+// The caller's state of a sequence and head or null, and whether the sequence's first token (its row in log_decay) clears
+// it: products with 0 would keep a NaN or infinity of it.
+__device__ __forceinline__ const float *first_state(const DeltaArgs &a, int64_t seq, int64_t token, int64_t len, int h, bool &cleared) {
+    cleared = a.state0 && len > 0 && a.log_decay[token * a.H + h] < kClears;
+    if (!a.state0) return nullptr;
+    const int64_t slot = state_slot(a.slots, a.n_slots, seq);
+    return slot >= 0 ? a.state0 + (slot * a.H + h) * (int64_t)a.Dk * a.Dv : nullptr;
+}
+
 // Ends a wave's LDS writes before its reads of them by other lanes.
 __device__ __forceinline__ void wave_sync() {
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
@@ -726,18 +737,14 @@ __device__ __forceinline__ void delta_walk(const DeltaArgs &a, char *lds, uint32
     State<KX> S;
     const int64_t nst = (int64_t)a.Dk * a.Dv;
     {
-        const float *p = nullptr;
         // Of a sequence of several segments the chain has written the first one's state, too: state1 may be state0's own
         // memory, and nothing orders the last segment's workgroup behind the first one's.
         const bool joined = MODE != kDeltaSums && a.seg_state && chunks > a.seg_chunks;
-        if (joined) {
-            S.load(a.seg_state + (place * a.H + h) * (int64_t)DXP * a.sum_ld, DXP, a.sum_ld, column);
-        } else if (MODE != kDeltaSums && a.state0) {
-            const int64_t slot = state_slot(a.slots, a.n_slots, tk.seq);
-            if (slot >= 0) p = a.state0 + (slot * a.H + h) * nst;
-        }
-        if (!joined) S.load(p, a.Dk, cols, column);
+        bool cleared = false;
+        if (joined) S.load(a.seg_state + (place * a.H + h) * (int64_t)DXP * a.sum_ld, DXP, a.sum_ld, column);
+        else S.load(MODE == kDeltaSums ? nullptr : first_state(a, tk.seq, tk.batch * a.N + tk.row0, tk.len, h, cleared), a.Dk, cols, column);
         S.settle();
+        if (cleared) S.each([](int, float) { return 0.0f; });
         if (map) S.each([&](int row, float) __attribute__((always_inline)) { return row == column ? 1.0f : 0.0f; });
     }
     const int out_cols = a.Dv - (col0 + zw + g * 4);       // of this lane's first column of the output on
@@ -1482,17 +1489,15 @@ template <int DXP> static __global__ __launch_bounds__(256, 1) void delta_chain_
     const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15, wave = threadIdx.x >> 6, row0 = wave * R * 16;
     const int64_t first = first_place(a, seq, length) * a.H + h, sums = (int64_t)DXP * a.sum_ld, maps = (int64_t)DXP * a.map_ld;
     {
-        const float *p = nullptr;
-        if (a.state0) {
-            const int64_t slot = state_slot(a.slots, a.n_slots, seq);
-            if (slot >= 0) p = a.state0 + (slot * a.H + h) * (int64_t)a.Dk * a.Dv;
-        }
+        bool cleared;
+        const float *p = first_state(a, seq, a.cu ? start : seq * a.N, len, h, cleared);
         const auto view = wide_view(p);
         float *out = a.seg_state + first * sums;
         for (int i = threadIdx.x; i < DXP * 16; i += 256) {
             const int row = i / 16, col = i % 16;
             const bool there = (p != nullptr) & (row < a.Dk) & (col0 + col < a.Dv);
-            const float x = view_load<float>(view, there ? (uint32_t)(row * a.Dv + col0 + col) * 4u : kSkip);
+            float x = view_load<float>(view, there ? (uint32_t)(row * a.Dv + col0 + col) * 4u : kSkip);
+            if (cleared) x = 0.0f;
             state[0][col * LD + row] = x;
             out[row * (int64_t)a.sum_ld + col0 + col] = x;
         }
@@ -1581,7 +1586,10 @@ __global__ __launch_bounds__(256) void delta_step_kernel(const DeltaStep a) {
         e[i] = (vec)0.0f;
         if (live && r < a.Dk) e[i] = *reinterpret_cast<const vec *>(s + (int64_t)r * a.Dv);
     }
-    const float d = expf(a.log_decay[b * a.H + h]), beta = a.beta[b * a.H + h];
+    const float log = a.log_decay[b * a.H + h], d = expf(log), beta = a.beta[b * a.H + h];
+    if (log < kClears)      // (0 times what is no number would keep it)
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i) e[i] = (vec)0.0f;
     {
         const float qi = tid < a.Dk ? (float)q[tid] : 0.0f, ki = tid < a.Dk ? (float)k[tid] : 0.0f;
         sq[tid] = qi;
