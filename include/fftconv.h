@@ -437,7 +437,10 @@ size_t fftconv_delta_bwd_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_
  * type, dq and dk summed over the heads that share a q/k head; dlog_decay and dbeta are fp32 (B, N, H), dense.  All of
  * them and dstate_in may each be NULL (skipped); dstate_out NULL = zero.  States are fp32 (B, H, Dk, Dv).  The call
  * recomputes what it needs of the forward pass; its workspace holds the state and the state's gradient of every 64
- * tokens.  strides: int64[21], dout, q, k, v, dq, dk, dv, or NULL.  Results repeat bit by bit. */
+ * tokens.  strides: int64[21], dout, q, k, v, dq, dk, dv, or NULL.  Results repeat bit by bit.
+ * dlog_decay_t is the sum of q_i . dq_i - v_i . dv_i over the tokens i >= t of t's block of 64 and of <G, S> behind the
+ * block (the state and its gradient), in fp32: its error is some 2^-20 of those terms, which do not shrink with the
+ * decay, so that little is left of a gradient that a small a_t makes small.  It is 0 where the token clears the state. */
 fftconv_status_t fftconv_delta_bwd(const void *dout, const void *q, const void *k, const void *v, const float *log_decay,
                                    const float *beta, void *dq, void *dk, void *dv, float *dlog_decay, float *dbeta,
                                    const int64_t *strides, const float *state_in, const float *dstate_out,

@@ -1468,7 +1468,9 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void delta_gradients_k
             if (lane + s < 64) sum += down;
         }
         sum += (double)((rest[0] + rest[1]) + (rest[2] + rest[3]));
-        if (lane < n) a.dlog_decay[gate0 + (int64_t)lane * a.H] = (float)sum;
+        // (the terms cancel to roundings where a token clears the state: there it is 0)
+        const int64_t gate = gate0 + (int64_t)lane * a.H;
+        if (lane < n) a.dlog_decay[gate] = a.log_decay[gate] < kClears ? 0.0f : (float)sum;
     }
 #endif
 }

@@ -109,3 +109,36 @@ def test_packed_sequences_keep_or_clear_each_their_own_state(lens):
         want, wS = seq.delta_fwd(*(_f64(t[x:y]) for t in ins), 0.25, None if b % 2 else _f64(S0[b]))
         _close(out[x:y], want, TOL["bf16"], f"out[{b}]")
         _close(S[b], wS, FP32, f"state[{b}]")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+def test_gradients_of_decays_of_any_size(dtype):
+    """Each head, from one that forgets nothing to one that forgets all, by itself.
+
+    dlog_decay_t is formed as the sum over the tokens i >= t of t's block of 64 of q_i dq_i - v_i dv_i and of <G, S> behind the
+    block.  Its terms are fp32 values from products of exact terms, each off by at most 5e-6 of the sum of its products'
+    magnitudes (the tolerance of fp32 results), and so is the whole of the sum of all those.  A token that clears the state has
+    the gradient 0."""
+    N, H, D, scale = 200, 7, 64, 0.3
+    ins = _inputs((1, N), H, H, D, D, dtype, 21)
+    a = ins[3]
+    for h, x in enumerate([0.0, -1e-3, -2.0, -12.0, -40.0, -100.0]):
+        a[..., h] = x
+    a[..., 6] = -0.1
+    a[0, ::9, 6], a[0, 4::9, 6], a[0, 7::9, 6] = CLEAR
+    dout = torch.randn((1, N, H, D), generator=torch.Generator().manual_seed(3)).cuda().to(DT[dtype])
+    S0, dS = (torch.randn((1, H, D, D), generator=torch.Generator().manual_seed(s)).cuda() for s in (4, 5))
+    got = _f64(fc.delta_attention_bwd(*ins, dout, scale=scale, state_in=S0, dstate_out=dS)[3][0])
+    q, k, v, g, b, do = (_f64(t[0]) for t in (*ins, dout))
+    want = seq.delta_bwd(do, q, k, v, g, b, scale, _f64(S0[0]), _f64(dS[0]))
+    each = np.abs(q * want[0]).sum(-1) + np.abs(v * want[2]).sum(-1)
+    S = _f64(S0[0])
+    for t0 in range(0, N, 64):
+        t1 = min(N, t0 + 64)
+        S = seq.delta_fwd(*(t[t0:t1] for t in (q, k, v, g, b)), scale, S)[1]
+        G = seq.delta_bwd(*(t[t1:] for t in (do, q, k, v, g, b)), scale, S, _f64(dS[0]))[5] if t1 < N else _f64(dS[0])
+        terms = each[t0:t1][::-1].cumsum(0)[::-1] + np.abs(G * S).sum((1, 2))
+        off = np.abs(got[t0:t1] - want[3][t0:t1]) / terms
+        assert off.max() <= FP32, f"{off.max():.2e} at token, head {np.unravel_index(off.argmax(), off.shape)} of {t0}"
+    cleared = _f64(a[0]) < -104
+    assert cleared[:, 6].sum() > 60 and not cleared[:, :6].any() and (got[cleared] == 0).all()
