@@ -71,19 +71,28 @@ __device__ __forceinline__ int64_t row_at(uint32_t row, uint32_t G, const int64_
 }
 __device__ __forceinline__ float inverse_rms(float squares, int D, float eps) { return 1.0f / sqrtf(squares / (float)D + eps); }
 
-// V values as e4m3 (round to nearest even), y / scale of at most 448
-template <int V> __device__ __forceinline__ void store8(uint8_t *p, const float (&y)[V], float inv) {
+// V values as e4m3 (round to nearest even), y / scale of at most 448.  A product with the scale's rounded reciprocal lies
+// beside some quotients that end in a tie of e4m3; what it leaves of y, times the reciprocal again, makes it the quotient
+// rounded once.
+template <int V> __device__ __forceinline__ void store8(uint8_t *p, const float (&from)[V], float scale, float inv) {
+    const float whole = scale < __builtin_inff() ? scale : 0.0f;      // (an infinite scale leaves zeros and NaNs)
+    float y[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        const float q = from[j] * inv;
+        y[j] = __builtin_fmaf(__builtin_fmaf(-q, whole, from[j]), inv, q);
+    }
     if constexpr (V % 4 == 0) {
         Piece<uint32_t, V / 4> r;
 #pragma unroll
         for (int j = 0; j < V / 4; ++j) {
-            int u = __builtin_amdgcn_cvt_pk_fp8_f32(y[4 * j] * inv, y[4 * j + 1] * inv, 0, false);
-            r.v[j] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(y[4 * j + 2] * inv, y[4 * j + 3] * inv, u, true);
+            int u = __builtin_amdgcn_cvt_pk_fp8_f32(y[4 * j], y[4 * j + 1], 0, false);
+            r.v[j] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(y[4 * j + 2], y[4 * j + 3], u, true);
         }
         store<uint32_t, V / 4>(reinterpret_cast<uint32_t *>(p), r);
     } else {
 #pragma unroll
-        for (int j = 0; j < V; ++j) p[j] = (uint8_t)__builtin_amdgcn_cvt_pk_fp8_f32(y[j] * inv, 0.0f, 0, false);
+        for (int j = 0; j < V; ++j) p[j] = (uint8_t)__builtin_amdgcn_cvt_pk_fp8_f32(y[j], 0.0f, 0, false);
     }
 }
 
@@ -189,7 +198,7 @@ __global__ __launch_bounds__(256) void norm_fwd_kernel(const NormFwd a) {
             each([&](int i, float (&from)[V]) __attribute__((always_inline)) {
                 float y[V];
                 normed(i, from, y);
-                store8<V>(o + i * V, y, inv);
+                store8<V>(o + i * V, y, scale, inv);
                 keep(i, from);
             });
         } else {
