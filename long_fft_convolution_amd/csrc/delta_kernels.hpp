@@ -413,40 +413,6 @@ template <typename T, int DP, int WAVES> struct RowTile {
     static constexpr int E = 16 / (int)sizeof(T), PR = DP / E, N = kC * PR / (WAVES * 64), BYTES = kC * DP * (int)sizeof(T);
     static_assert(kC * PR % (WAVES * 64) == 0 && PR % 8 == 0, "whole loads");
     static __device__ __forceinline__ int f(int row) { return (row & 1) << 2 | (row & 2) | ((row >> 2) & 1); }
-    static __device__ __forceinline__ const T *at(const T *tile, int row, int slot) { return tile + (row * PR + (slot ^ f(row))) * E; }
-    // 8 values of a row at column col (a multiple of 8)
-    static __device__ __forceinline__ Raw8<T> row8(const T *tile, int row, int col) {
-        Raw8<T> r;
-        if constexpr (sizeof(T) == 2) {
-            r = *reinterpret_cast<const Raw8<T> *>(__builtin_assume_aligned(at(tile, row, col / 8), 16));
-        } else {
-            const f32x4 a = *reinterpret_cast<const f32x4 *>(at(tile, row, col / 4)), b = *reinterpret_cast<const f32x4 *>(at(tile, row, col / 4 + 1));
-            __builtin_memcpy(&r, &a, 16);
-            __builtin_memcpy(reinterpret_cast<char *>(&r) + 16, &b, 16);
-        }
-        return r;
-    }
-    // Rows row0 .. row0 + 3 of this lane's own column, mine; row0 may differ between the wave's four groups of 16
-    // lanes.  16 bits: a transposing read, in which 16 lanes read four rows of four 4-column groups and lane c
-    // receives column c % 4 of group c / 4; group is the first column of the one that lanes of this c % 4 read.
-    static __device__ __forceinline__ void col4(const T *tile, int row0, int group, int mine, T *out) {
-        if constexpr (sizeof(T) == 2) {
-            const T *p = at(tile, row0 + ((threadIdx.x & 15) >> 2), group / 8) + group % 8;
-            const s16x4 v = __builtin_bit_cast(s16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16(FFTCONV_LDS_CAST(s16x4, p)));
-            __builtin_memcpy(out, &v, 8);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) out[j] = at(tile, row0 + j, mine / 4)[mine % 4];
-        }
-    }
-    // rows of the operand over tokens 32 s .. 32 s + 31
-    static __device__ __forceinline__ Raw8<T> col8(const T *tile, int s, int group, int mine) {
-        const int g = (threadIdx.x & 63) >> 4;
-        Raw8<T> r;
-        col4(tile, 32 * s + 4 * g, group, mine, r.v);
-        col4(tile, 32 * s + 16 + 4 * g, group, mine, r.v + 4);
-        return r;
-    }
 };
 // Brings a tensor's rows into a tile: VEC by LDS-destination loads (what lies outside the chunk or the columns reads
 // zero by the buffer unit's range check), else value by value.

@@ -474,7 +474,7 @@ GemmPlan plan_gemm(int64_t M, int64_t N, int64_t K, int dt, bool vec) {
     };
     static const Kind kinds[] = {{256, 1.45, 1.45, 0.0, 0.0}, {128, 0.60, 0.47, 2.2, 2.05}, {64, 0.28, 0.22, 0.60, 0.52}};
     constexpr double kStart = 4.0, kJoin = 2.0, kBytesPerUs = 6.0e6;
-        const int64_t bk = 128 / elem_bytes(dt), stages = std::max<int64_t>(1, ceil_div(K, bk));
+    const int64_t bk = 128 / elem_bytes(dt), stages = std::max<int64_t>(1, ceil_div(K, bk));
     GemmPlan best{};
     double least = 1e300;
     for (const Kind &k : kinds) {
