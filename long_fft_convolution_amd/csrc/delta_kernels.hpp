@@ -249,9 +249,9 @@ __device__ __forceinline__ void invert_unit_lower(float *M, int n) {
 
 // One wave a (chunk, head): record of the chunk.  grid: chunks * H / 4.  Bound by latency (products, the inverse's 16
 // serial steps, LDS round trips; eight waves a CU overlap them) and, for long calls, by the records written.  20 heads of
-// 128, bf16: 4 x 4096 tokens 87 us, 131072 tokens 580 us (2.5 GB, 4.3 TB/s).  A chunk that ends early has fewer blocks to
-// invert (17 tokens: 14.8 us, 16.6 with all of them).
-// BACK: the backward call's record (4 x 4096 tokens: 130 us).
+// 128, bf16: 4 x 4096 tokens 91 us, 131072 tokens 605 us (2.7 GB, 4.4 TB/s).  A chunk that ends early has fewer blocks to
+// invert (17 tokens: 14.3 us, 16.6 with all of them).
+// BACK: the backward call's record (4 x 4096 tokens: 145 to 155 us).
 template <typename T, int DXP, bool VEC, bool BACK> __global__ __launch_bounds__(256) void delta_prepare_kernel(const DeltaArgs a) {
     constexpr int KX = DXP / 32, NP = Terms<T>::kOut;
     __shared__ __attribute__((aligned(16))) float matrix[4][kC * kLd];
@@ -622,14 +622,14 @@ inline __host__ __device__ int delta_run(int tiles, int group) {
 enum DeltaMode : int { kDeltaSums = 0, kDeltaOut = 1, kDeltaKeep = 2 };
 
 // Waves a SIMD that the compiler leaves registers for: the sums' walks, which cut sequences into twice as many pieces as
-// walk at once, share a CU (131072 tokens x 20 heads of 128: 1400 us, 1555 with one of two stages).
+// walk at once, share a CU (131072 tokens x 20 heads of 128: 1380 us, 1555 with one of two stages).
 constexpr int walk_waves(int dxp, int waves, int mode, int bytes) { return mode == kDeltaSums && bytes == 2 && dxp <= 128 ? waves / 2 : 1; }
 
 // Eight waves a workgroup, two a SIMD (one splits fp32 values while the other multiplies), for 128 columns; four for 64.
 // Bound by the serial chunk: its products, splits and LDS reads each take two to three microseconds of it, in turns.
-// 20 heads of 128, bf16: 4 x 4096 tokens 230 us (64 columns, 3.6 us a chunk), one sequence of 6001 among shorter ones 432
-// us (128 columns, 4.6 us a chunk), 131072 tokens in 12 segments: sums and maps 1420 us, outputs 1060 us.  fp16, fp32:
-// 433 and 728 us at 4 x 4096.  32 columns a wave took 1032 us for those outputs, and 2213 us for the sums.
+// 20 heads of 128, bf16: 4 x 4096 tokens 245 us (64 columns, 3.8 us a chunk), one sequence of 6001 among shorter ones 443
+// us (128 columns, 4.7 us a chunk), 131072 tokens in 12 segments: sums and maps 1380 us, outputs 990 us.  fp16, fp32:
+// 452 and 718 us at 4 x 4096.  32 columns a wave took 1032 us for those outputs, and 2213 us for the sums.
 template <typename T, int DXP, int WAVES, int MODE, bool VEC> struct WalkShape {
     static constexpr bool OUT = MODE == kDeltaOut;
     static constexpr int DZT = WAVES * 16;
@@ -1090,7 +1090,7 @@ __device__ __forceinline__ void delta_walk_back(const DeltaArgs &a, char *lds, u
 #endif
 
 // Both walks of the backward call: even items forwards, odd ones from the end.  Bound as the forward walks, the reverse one
-// with twice their products: 4 x 4096 tokens x 20 heads of 128, bf16 560 us (8.7 us a chunk), fp32 1670.
+// with twice their products: 4 x 4096 tokens x 20 heads of 128, bf16 540 us (8.5 us a chunk), fp32 1640.
 template <typename T, int DXP, int WAVES, bool VEC>
 __global__ __launch_bounds__(walk_bound(DXP, WAVES, sizeof(T))) void delta_back_walks_kernel(const DeltaArgs a, int tiles) {
 #ifdef __HIP_DEVICE_COMPILE__
@@ -1110,7 +1110,7 @@ __global__ __launch_bounds__(walk_bound(DXP, WAVES, sizeof(T))) void delta_back_
 // through LDS, 32 columns at a time; k and q, met by columns, follow in the same place.
 //
 // Bound by waits: half of the time at barriers and for LDS, the rest the matrix units and the splitting.  4 x 4096 tokens x
-// 20 heads of 128, bf16: 565 us (612 with S and G loaded into registers), fp32 895.
+// 20 heads of 128, bf16: 550 us (612 with S and G loaded into registers), fp32 875.
 template <typename T, int DXP> struct GradientShape {
     static constexpr int DP = 64, DT = DP / 16;      // columns of q and k at once, their tiles
     static constexpr int NIN = Terms<T>::kIn;
@@ -1444,7 +1444,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void delta_gradients_k
 // State before each segment from the segments' own sums and maps: S <- map S + sum, the first one's as the caller gave it.
 // One workgroup a (sequence, head, 16 columns), grid (B, H, tiles); a wave has a quarter of the rows of the map, of which
 // those of the next segment are on their way while this one's are in use, and the state goes round through LDS.  Bound by
-// latency: the segments are serial (12 segments of 20 heads of 128: 47 us).
+// latency: the segments are serial (12 segments of 20 heads of 128: 42 us).
 template <int DXP> static __global__ __launch_bounds__(256, 1) void delta_chain_kernel(const DeltaArgs a) {
     constexpr int KX = DXP / 32, R = DXP / 64, LD = DXP + 4;
     __shared__ __attribute__((aligned(16))) float state[2][16 * LD];

@@ -25,13 +25,15 @@ size_t record_bytes(const DeltaShape &s) { return (size_t)delta_pieces(delta_ter
 // How sequences are cut.  A walk is serial: 64 tokens take microseconds, whatever else the chip does.  With segments the
 // walks' work is three times that of the walk alone (sums and maps, outputs) and the chain adds to it, so sequences are cut
 // where at least four segments of each walk at once, and more than four where the walks of 128 columns fill the chip.
-// bf16, us uncut / cut:
-//     4096 tokens, heads of 128: 16 heads 227 / 127, 32 heads 240 / 184, 50 heads 264 / 260, 64 heads (four) 272 / 319
-//     heads of 128, 2048 tokens: 8 heads 122 / 106, 20 heads 125 / 111; 1024 tokens, 20 heads (two) 74 / 102
-//     4096 tokens, 64 heads of 64 (four): 196 / 148; 16384 tokens, 16 heads of 256: 1689 / 1068
+// bf16, us a call uncut / cut:
+//     4096 tokens, heads of 128: 16 heads 241 / 133, 32 heads 249 / 187, 50 heads 272 / 274, 64 heads (four) 283 / 324
+//     heads of 128, 2048 tokens: 8 heads 126 / 108, 20 heads 128 / 111; 1024 tokens, 20 heads (two) 76 / 103
+//     4096 tokens, 64 heads of 64 (four): 206 / 156; 16384 tokens, 16 heads of 256: 1738 / 1085
+// Packed sequences' lengths live on the device, so their mean stands for them: one of 100000 tokens beside 60 of 64 walks
+// uncut (20 heads of 128: 7.4 ms, by itself 2.2).
 // Walks of 128 columns read k, q and the records half as often as those of 64 and take longer a chunk, so an uncut call has
-// them where those of 64 columns would be more than one a CU (1024 tokens, 128 columns, us by 64 / by 128: 120 heads 88 /
-// 109, 129 heads 155 / 121, 400 heads 336 / 298), and a cut one always (16384 tokens, 20 heads: 465 / 426).
+// them where those of 64 columns would be more than one a CU (1024 tokens, 128 columns, us by 64 / by 128: 120 heads 90 /
+// 110, 129 heads 156 / 123, 400 heads 352 / 312), and a cut one always (16384 tokens, 20 heads: 479 / 442).
 struct DeltaCut {
     int64_t seg_chunks, segs;
     bool cut, wide;
@@ -264,8 +266,8 @@ struct DeltaBwdLayout {
 };
 DeltaBwdLayout bwd_layout(const DeltaShape &s) {
     DeltaBwdLayout l{};
-    // as for an uncut forward call, with two walks (1024 tokens, 128 columns, us by 64 / by 128: 60 heads 219 / 236, 70
-    // heads 320 / 272, 80 heads 338 / 301)
+    // as for an uncut forward call, with two walks (1024 tokens, 128 columns, us by 64 / by 128: 60 heads 217 / 237, 65
+    // heads 333 / 280, 80 heads 349 / 311)
     l.wide = s.Dk <= 128 && s.Dv > 64 && 2 * s.B * s.H * ceil_div(s.Dv, 64) > kCus;
     l.dkp = padded_width(s.Dk);
     l.dvp = round_up(s.Dv, l.wide ? 128 : 64);

@@ -7,9 +7,10 @@
 //
 // All of it is fp32; t is rounded once for `sum` and not at all on its way to
 // y, y once for out.  Bound by memory: a row is read once, held in registers
-// by a wave or part of one, or by a workgroup.  16384 rows of 2560, bf16:
-// with residual and sum 66 us, 5.1 TB/s; with an 8-bit out instead 72 us, 4.1
-// TB/s; gradients with dsum 99 us, 3.4 TB/s.
+// by a wave or part of one, or by a workgroup.  16384 rows of 2560, bf16,
+// a call on inputs that no cache holds: with residual and sum 66 us, 5.1 TB/s;
+// with an 8-bit out instead 69 to 74 us, 4.0 to 4.3 TB/s; gradients with dsum 98
+// to 103 us, 3.3 to 3.4 TB/s.
 #include <hip/hip_bf16.h>
 #include <hip/hip_fp16.h>
 #include <hip/hip_runtime.h>
@@ -28,8 +29,8 @@ template <typename T, int V> __device__ __forceinline__ Piece<T, V> load(const T
     __builtin_memcpy(&r, __builtin_assume_aligned(p, V * sizeof(T)), sizeof r);
     return r;
 }
-// Results pass the caches by where they come in whole pieces of 16 bytes (16384 rows of 2560, bf16, sum and out: 67.5
-// us, 77.8 with ordinary stores; 2048 rows of 4096: 14.3 and 15.2).
+// Results pass the caches by where they come in whole pieces of 16 bytes (16384 rows of 2560, bf16, sum and out: 65.5
+// us, 71.3 with ordinary stores; 2048 rows of 4096: 13.2 and 13.6).
 template <typename T, int V> __device__ __forceinline__ void store(T *p, const Piece<T, V> &r) {
     if constexpr (V * sizeof(T) == 16) {
         typedef uint32_t words __attribute__((ext_vector_type(4)));

@@ -10,12 +10,12 @@ using namespace fftconv;
 namespace {
 
 constexpr int64_t kMaxWidth = int64_t(1) << 20;
-// Partial sums of the weight's gradient.  bf16 with dsum: 512 are two workgroups a CU, as many as hold rows of 2560 at
-// once (16384 rows: 61 us, 85 with 256, 74 with 1024); narrower ones leave room for four (65536 rows of 768: 74 us, 92
-// with 512 and with 2048).  Of the narrowest, a workgroup holds sixteen rows and more at once, and 512 do (131072 rows of
-// 128: 36 us, 37 with 1024).
+// Partial sums of the weight's gradient.  bf16 with dsum, a call (both launches) on inputs that no cache holds: 512 are two
+// workgroups a CU, as many as hold rows of 2560 at once (16384 rows: 103 us, 158 with 256, 116 with 1024); narrower ones
+// leave room for four (65536 rows of 768: 116 us, 154 with 512, 139 with 2048).  Of the narrowest, a workgroup holds sixteen
+// rows and more at once, and 512 do (131072 rows of 128: 50 us, 48 with 1024; on inputs in the caches 38 and 42).
 int64_t slabs_of(int64_t rows, int64_t D) { return std::min<int64_t>(rows, D > 128 && D <= 1024 ? 1024 : 512); }
-// Workgroups of a forward call; more rows are met in turn (65536 rows of 768: 60 us, 64 with 8192, 81 with 1024).
+// Workgroups of a forward call; more rows are met in turn (65536 rows of 768: 79 us, 80 with 8192, 90 with 1024).
 constexpr int64_t kMostGroups = 16384;
 
 struct NormShape {
@@ -51,11 +51,11 @@ bool same_place(const View &a, const View &b) {
 
 // A part of a wave holds a row where one piece a lane does; else a wave where the rows are many and take at most
 // `wave` pieces a lane; else a workgroup with up to eight pieces a lane; else the row is read again.  bf16, us by waves /
-// by workgroups:
-//     forward, 768 wide: 64 rows 3.4 / 2.8, 2048 rows 7.0 / 6.1, 4096 rows 8.9 / 10.1, 16384 rows 24.8 / 30.4
-//     forward, 16384 rows: 1536 wide 45.4 / 39.7, 2560 wide 77.5 / 69.3, 4096 wide 121 / 101
-//     gradients, 2560 wide: 64 rows 11.9 / 8.2, 512 rows 17.3 / 21.3, 16384 rows 100 / 163
-//     gradients, 4096 wide: 512 rows 25.3 / 23.0, 16384 rows 269 / 183
+// by workgroups, a call in a captured graph on inputs that no cache holds:
+//     forward, 768 wide: 64 rows 3.3 / 2.7, 2048 rows 6.0 / 5.0, 4096 rows 7.2 / 9.5, 16384 rows 22.4 / 28.8
+//     forward, 16384 rows: 1536 wide 40.7 / 39.5, 2560 wide 72.7 / 64.9, 4096 wide 122 / 97
+//     gradients, 2560 wide: 64 rows 12.5 / 8.3, 512 rows 17.2 / 21.2, 16384 rows 101 / 161
+//     gradients, 4096 wide: 512 rows 25.6 / 22.9, 16384 rows 258 / 179
 NormPlan plan_of(int64_t rows, int64_t D, int vec, int wave, int64_t few) {
     NormPlan p{};
     p.vec = vec;
